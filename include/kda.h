@@ -23,8 +23,8 @@
  *     prefill entry points kda_chunk_prefill and kda_chunk_prefill_ex take
  *     their hand-off rings stream-ordered from a memory pool the library owns
  *     (see kda_chunk_prefill); kda_chunk_prefill_noalloc uses a fixed device
- *     array instead and allocates nothing; every other entry point needs no
- *     scratch.
+ *     array instead and allocates nothing; kda_latent_decode takes its partial
+ *     results from the same pool; every other entry point needs no scratch.
  *   - Tensors are dense, row-major, with the last dimension contiguous.
  *     bf16 tensors are passed as uint16_t bit patterns (IEEE bfloat16).
  *     Every device pointer must be 16-byte aligned.
@@ -394,6 +394,146 @@ int kda_prepare_inputs(const uint16_t* xq, const uint16_t* xk, const uint16_t* x
 int kda_output_norm(const void* o, int o_dtype, const float* gamma, float eps,
                     uint16_t* y, int total_tokens, int H, int Dv, void* stream);
 
+/*
+ * Latent attention -- the full-attention layers that a KDA hybrid interleaves with the
+ * recurrence (the Kimi K3 primer, wiki summary, section 3: 3:1 KDA to MLA, keys and values
+ * from one shared latent vector a token).  A token's cache row holds its latent c
+ * (KDA_LATENT_DIM values) and one position key r (KDA_LATENT_ROPE values) shared by all heads.
+ *
+ * The cache is paged: [num_pages, page_size, row bytes], row bytes per kda_latent_row_bytes,
+ * page_size a multiple of 16 (at most KDA_LATENT_MAX_PAGE), dense.  Token t of sequence n lies
+ * in row t % page_size of page block_table[n * max_pages + t / page_size]; a cache row's number
+ * (a "slot") is page * page_size + row and stays below 2^31.
+ *   KDA_CACHE_BF16   1152 bytes: c (512 bf16), r (64 bf16)
+ *   KDA_CACHE_E4M3    656 bytes: 512 e4m3 codes, r (64 bf16), fp32 scale s, 12 bytes of zero.
+ *       c = code * s with s = 2^e, e the smallest integer with max |c| <= 448 * 2^e, clamped to
+ *       [-117, 119] so that every code * s is a bf16 value (an all-zero row: s = 1); codes are
+ *       c / s rounded to nearest even, magnitudes above 448 s (only where e was clamped) stored
+ *       as 448.  A NaN or infinity is stored as NaN and does not enter the scale.
+ * Device-side indices (slots, pages, lengths) that are out of range are skipped as each entry
+ * point says, and the next kda_device_status returns KDA_ERR_INVALID_ARG.
+ */
+typedef enum { KDA_CACHE_BF16 = 0, KDA_CACHE_E4M3 = 1 } kda_cache_dtype;
+#define KDA_LATENT_DIM 512
+#define KDA_LATENT_ROPE 64
+#define KDA_LATENT_MAX_PAGE 1024
+
+/* Bytes of one cache row (1152 or 656), or KDA_ERR_INVALID_ARG for another cache_dtype. */
+int kda_latent_row_bytes(int cache_dtype);
+
+/*
+ * kda_latent_append -- write new tokens into the cache, quantising on the way.
+ *
+ *   c           (device) bf16 [total_tokens, KDA_LATENT_DIM], rows ldc elements apart
+ *   k_rope      (device) bf16 [total_tokens, KDA_LATENT_ROPE], rows ldr elements apart
+ *               (ldc, ldr multiples of 8: both may be slices of one projection's rows)
+ *   cache       (device) as above
+ *   slots       (device) int32 [total_tokens]: the cache row of each token; a negative slot
+ *               skips its token (padding); one >= num_pages * page_size is skipped and reported.
+ *               Two tokens with the same slot: unspecified which one stays.
+ */
+int kda_latent_append(const uint16_t* c, int64_t ldc, const uint16_t* k_rope, int64_t ldr,
+                      void* cache, int cache_dtype, int num_pages, int page_size,
+                      const int32_t* slots, int total_tokens, void* stream);
+
+/*
+ * kda_latent_gather -- read cached tokens back as dense bf16 rows (to expand a cached prefix
+ * into per-head keys and values, or to move it).
+ *
+ *   block_table (device) int32 [num_seqs, max_pages]
+ *   start_pos   (device) int32 [num_seqs] or NULL (= 0): first token read of each sequence
+ *   cu_seqlens  (device) / cu_seqlens_host: int32 [num_seqs + 1]; sequence n's tokens start_pos[n]
+ *               .. start_pos[n] + len_n - 1 go to rows cu_seqlens[n] ..
+ *   c, k_rope   (device) bf16 [total_tokens, 512] / [total_tokens, 64], rows ldc / ldr elements
+ *               apart (multiples of 8).  The values are exactly those the cache stands for.
+ * A token whose position or page is out of range is reported and its row is left as it was.
+ */
+int kda_latent_gather(const void* cache, int cache_dtype, int num_pages, int page_size,
+                      const int32_t* block_table, int max_pages, const int32_t* start_pos,
+                      const int32_t* cu_seqlens, const int32_t* cu_seqlens_host,
+                      int num_seqs, int total_tokens,
+                      uint16_t* c, int64_t ldc, uint16_t* k_rope, int64_t ldr, void* stream);
+
+/*
+ * kda_latent_decode -- absorbed latent attention of the last K tokens of N sequences over the
+ * paged cache (K = 1: a decode step; K > 1: the verify pass of a speculative step).
+ *
+ *   q           (device) bf16 [N, K, H, 576]: per head the absorbed query (W_uk^T q_nope, 512)
+ *               then its position part (64)
+ *   seq_lens    (device) int32 [N]: tokens in the cache, the K new ones included
+ *   out         (device) bf16 [N, K, H, 512]: the attention-weighted latent (W_uv is applied by
+ *               the caller)
+ *   lse         (device) fp32 [N, K, H] or NULL: natural log of the softmax denominator,
+ *               log sum_t exp(x_t)
+ * Query j of sequence n sees tokens t < seq_lens[n] - (K - 1 - j):
+ *     x_t = sm_scale * (q[:512] . c_t + q[512:] . r_t),  out = sum_t softmax(x)_t c_t
+ * A query that sees nothing gives zeros and lse = -inf.  Cache rows past the end of a sequence
+ * (the rest of its last page) are never part of a result, whatever they hold.  Softmax
+ * statistics and sums are fp32; the probabilities enter the second product as bf16.
+ * 1 <= K * H <= KDA_LATENT_MAX_ROWS, else KDA_ERR_UNSUPPORTED.  seq_lens[n] outside
+ * [0, max_pages * page_size] counts as 0 and is reported; a page outside [0, num_pages) is
+ * reported and leaves the sequence's outputs unspecified.  Scratch: partial results of at most
+ * two work items per SM, stream-ordered from the library's pool as for kda_chunk_prefill.
+ * Deterministic.
+ */
+#define KDA_LATENT_MAX_ROWS 512
+int kda_latent_decode(const uint16_t* q, const void* cache, int cache_dtype, int num_pages, int page_size,
+                      const int32_t* block_table, int max_pages, const int32_t* seq_lens,
+                      int N, int K, int H, float sm_scale, uint16_t* out, float* lse, void* stream);
+
+/*
+ * kda_latent_prefill -- expanded latent attention over packed prompts: per-head keys and values
+ * (already projected up from the latents), the position key shared by all heads.
+ *
+ *   q           (device) bf16 [total_q, H, 192]: per head 128 values, then the position part (64)
+ *   k, v        (device) bf16 [total_k, H, 128], token / head strides ldk, hdk and ldv, hdv in
+ *               elements (multiples of 8, at least 128: slices of one projection's output or a
+ *               head-major layout)
+ *   k_rope      (device) bf16 [total_k, 64], rows ldr elements apart (a multiple of 8)
+ *   cu_q, cu_k  (device) int32 [num_seqs + 1] and their host copies: the queries and the keys of
+ *               each sequence (a chunk of a prompt has more keys than queries)
+ *   causal      1: query i of a sequence of Lq queries and Lk keys sees keys t <= i + Lk - Lq;
+ *               0: all its keys
+ *   out         (device) bf16 [total_q, H, 128];  lse (device) fp32 [total_q, H] or NULL
+ *     x_t = sm_scale * (q[:128] . k_t + q[128:] . r_t),  out = sum_t softmax(x)_t v_t
+ * A query that sees nothing gives zeros and lse = -inf.  Keys and values that a query does not
+ * see never reach its result, whatever they hold.  Softmax statistics and sums are fp32; the
+ * probabilities enter the second product as bf16.  Deterministic.
+ */
+int kda_latent_prefill(const uint16_t* q, const uint16_t* k, int64_t ldk, int64_t hdk,
+                       const uint16_t* v, int64_t ldv, int64_t hdv, const uint16_t* k_rope, int64_t ldr,
+                       const int32_t* cu_q, const int32_t* cu_q_host, const int32_t* cu_k, const int32_t* cu_k_host,
+                       int num_seqs, int total_q, int total_k, int H, int causal, float sm_scale,
+                       uint16_t* out, float* lse, void* stream);
+
+/*
+ * kda_verify_draft -- accept or reject drafted tokens by the target's probabilities (speculative
+ * sampling: the accepted tokens and the one drawn after them follow the target's distribution).
+ *
+ *   target_probs (device) fp32 [N, K + 1, V], rows ldp elements apart: the target's distribution
+ *               at each drafted position and after the last
+ *   draft_probs (device) fp32 [N, K, V], rows ldq elements apart, or NULL for a draft that
+ *               proposes with certainty (probability 1 at the drafted token, 0 elsewhere)
+ *   draft_tokens (device) int32 [N, K]
+ *   num_draft   (device) int32 [N] in [0, K] or NULL (= K): drafted tokens of each sequence
+ *   u_accept    (device) fp32 [N, K] and u_sample (device) fp32 [N]: uniform numbers in [0, 1)
+ *   tokens      (device) int32 [N, K + 1]: the accepted drafts, then one drawn token, then -1
+ *   num_tokens  (device) int32 [N]: accepted drafts + 1: the tokens the sequence advances by, and
+ *               the num_tokens of the kda_decode_multi that commits them
+ * Draft j is accepted while u_accept_j * q_j(x_j) < p_j(x_j) (compared exactly).  At the first
+ * rejected position i the drawn token follows max(0, p_i - q_i) (p_i where that is all zero),
+ * after a whole accepted draft it follows p at the position after it: the smallest t whose
+ * cumulative weight exceeds u_sample times the total weight, sums carried to about 45 bits.
+ * Negative, NaN and infinite weights count as 0; no weight at all draws token -1.  A drafted
+ * token outside [0, V) or a count outside [0, K] skips the sequence (num_tokens 0, tokens -1)
+ * and is reported.  Deterministic.  K <= KDA_VERIFY_MAX_DRAFT.
+ */
+#define KDA_VERIFY_MAX_DRAFT 64
+int kda_verify_draft(const float* target_probs, int64_t ldp, const float* draft_probs, int64_t ldq,
+                     const int32_t* draft_tokens, const int32_t* num_draft, const float* u_accept,
+                     const float* u_sample, int N, int K, int V, int32_t* tokens, int32_t* num_tokens,
+                     void* stream);
+
 /* Number of checkpoint slots kda_chunk_prefill writes: sum over sequences of
  * ceil(len / ckpt_stride) (0 when ckpt_stride == 0).  cu_seqlens_host is a host
  * array of num_seqs + 1 offsets.  Returns -1 on invalid arguments. */
@@ -411,7 +551,7 @@ int64_t kda_ckpt_count_ex(const int32_t* cu_seqlens_host, const int32_t* start_p
  * kernel returned early; its outputs are undefined), KDA_ERR_RANGE (a prefill
  * met decays or magnitudes outside its numeric domain, see the conventions at
  * the top; its outputs are undefined), KDA_ERR_INVALID_ARG (a device-side index
- * of kda_decode_multi was out of range), or KDA_ERR_CUDA if the
+ * of kda_decode_multi, kda_latent_* or kda_verify_draft was out of range), or KDA_ERR_CUDA if the
  * synchronisation itself failed.  The first failure recorded since the last
  * call is the one returned. */
 int kda_device_status(void* stream);

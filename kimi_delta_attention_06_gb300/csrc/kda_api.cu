@@ -44,6 +44,21 @@ int launch_decode_multi(const uint16_t* q, const uint16_t* k, const uint16_t* v,
                         const uint16_t* beta, float* pool, int num_slots, const int32_t* slots,
                         const int32_t* ntok, int commit, void* out, int out_f32,
                         int N, int K, int H, int D, int decay, int* status, cudaStream_t stream);
+int launch_latent_append(const uint16_t* c, long long ldc, const uint16_t* r, long long ldr, void* cache, int e4m3,
+                         long long num_rows, const int32_t* slots, int T, int* status, cudaStream_t stream);
+int launch_latent_gather(const void* cache, int e4m3, int num_pages, int page_size, const int32_t* table, int max_pages,
+                         const int32_t* start, const int32_t* cu, int num_seqs, int T, uint16_t* c, long long ldc,
+                         uint16_t* r, long long ldr, int* status, cudaStream_t stream);
+int launch_latent_decode(const uint16_t* q, const void* cache, int e4m3, int num_pages, int page_size,
+                         const int32_t* table, int max_pages, const int32_t* seq_lens, int N, int K, int H,
+                         float sm_scale, uint16_t* out, float* lse, int* status, cudaStream_t stream);
+int launch_latent_prefill(const uint16_t* q, const uint16_t* k, long long ldk, long long hdk, const uint16_t* v,
+                          long long ldv, long long hdv, const uint16_t* r, long long ldr, const int32_t* cu_q,
+                          const int32_t* cu_k, int num_seqs, int total_q, int total_k, int max_q, int H, int causal,
+                          float sm_scale, uint16_t* out, float* lse, int* status, cudaStream_t stream);
+int launch_verify(const float* tp, long long ldp, const float* dp, long long ldq, const int32_t* toks,
+                  const int32_t* num_draft, const float* ua, const float* us, int N, int K, int V, int32_t* out,
+                  int32_t* num_out, int* status, cudaStream_t stream);
 }  // namespace kda
 
 namespace {
@@ -169,6 +184,28 @@ int check_prefill_args(const uint16_t* q, const uint16_t* k, const uint16_t* v, 
     if (static_cast<int64_t>(total_tokens) * H * (Dk > Dv ? Dk : Dv) >= (int64_t(1) << 40)) return KDA_ERR_INVALID_ARG;
     return KDA_OK;
 }
+
+// Packed sequences: offsets from 0 to `total`, non-decreasing.
+bool cu_ok(const int32_t* dev, const int32_t* host, int num_seqs, int total) {
+    if (num_seqs == 0) return total == 0;
+    if (!dev || !host || (reinterpret_cast<uintptr_t>(dev) & 3u)) return false;
+    if (host[0] != 0 || host[num_seqs] != total) return false;
+    for (int n = 0; n < num_seqs; ++n)
+        if (host[n + 1] < host[n]) return false;
+    return true;
+}
+
+// The latent cache's description, shared by its entry points.
+int check_latent_cache(const void* cache, int cache_dtype, int num_pages, int page_size) {
+    if (cache_dtype != KDA_CACHE_BF16 && cache_dtype != KDA_CACHE_E4M3) return KDA_ERR_INVALID_ARG;
+    if (num_pages < 0 || page_size <= 0) return KDA_ERR_INVALID_ARG;
+    if (page_size % 16 != 0 || page_size > KDA_LATENT_MAX_PAGE) return KDA_ERR_UNSUPPORTED;
+    if (static_cast<int64_t>(num_pages) * page_size > INT32_MAX) return KDA_ERR_INVALID_ARG;
+    if ((num_pages > 0 && !cache) || !aligned16(cache)) return KDA_ERR_INVALID_ARG;
+    return KDA_OK;
+}
+bool stride_ok(int64_t ld, int64_t least) { return ld >= least && ld % 8 == 0 && ld < (int64_t(1) << 40); }
+bool scale_ok(float x) { return x > -3.0e38f && x < 3.0e38f; }
 
 // One thread waits, with a bound, on an mbarrier phase that nothing completes.
 __global__ void expire_wait_kernel(unsigned long long limit_ns, int* status) {
@@ -739,6 +776,125 @@ int kda_output_norm(const void* o, int o_dtype, const float* gamma, float eps,
     if (rc != KDA_OK) return rc;
     rc = kda::launch_output_norm(o, o_dtype == KDA_OUT_F32, gamma, eps, y, total_tokens, H, Dv,
                                  static_cast<cudaStream_t>(stream));
+    return rc == 0 ? KDA_OK : KDA_ERR_CUDA;
+}
+
+int kda_latent_row_bytes(int cache_dtype) {
+    if (cache_dtype == KDA_CACHE_BF16) return 1152;
+    return cache_dtype == KDA_CACHE_E4M3 ? 656 : KDA_ERR_INVALID_ARG;
+}
+
+int kda_latent_append(const uint16_t* c, int64_t ldc, const uint16_t* k_rope, int64_t ldr,
+                      void* cache, int cache_dtype, int num_pages, int page_size,
+                      const int32_t* slots, int total_tokens, void* stream) {
+    int rc = check_latent_cache(cache, cache_dtype, num_pages, page_size);
+    if (rc != KDA_OK) return rc;
+    if (total_tokens < 0) return KDA_ERR_INVALID_ARG;
+    if (total_tokens == 0) return KDA_OK;
+    if (!stride_ok(ldc, KDA_LATENT_DIM) || !stride_ok(ldr, KDA_LATENT_ROPE)) return KDA_ERR_INVALID_ARG;
+    if (!c || !k_rope || !slots || !aligned16(c) || !aligned16(k_rope)) return KDA_ERR_INVALID_ARG;
+    if (reinterpret_cast<uintptr_t>(slots) & 3u) return KDA_ERR_INVALID_ARG;
+    int* status = nullptr;
+    rc = device_setup(&status);
+    if (rc != KDA_OK) return rc;
+    rc = kda::launch_latent_append(c, ldc, k_rope, ldr, cache, cache_dtype == KDA_CACHE_E4M3,
+                                   static_cast<int64_t>(num_pages) * page_size, slots, total_tokens, status,
+                                   static_cast<cudaStream_t>(stream));
+    return rc == 0 ? KDA_OK : KDA_ERR_CUDA;
+}
+
+int kda_latent_gather(const void* cache, int cache_dtype, int num_pages, int page_size,
+                      const int32_t* block_table, int max_pages, const int32_t* start_pos,
+                      const int32_t* cu_seqlens, const int32_t* cu_seqlens_host,
+                      int num_seqs, int total_tokens,
+                      uint16_t* c, int64_t ldc, uint16_t* k_rope, int64_t ldr, void* stream) {
+    int rc = check_latent_cache(cache, cache_dtype, num_pages, page_size);
+    if (rc != KDA_OK) return rc;
+    if (num_seqs < 0 || total_tokens < 0 || max_pages < 0) return KDA_ERR_INVALID_ARG;
+    if (!cu_ok(cu_seqlens, cu_seqlens_host, num_seqs, total_tokens)) return KDA_ERR_INVALID_ARG;
+    if (total_tokens == 0) return KDA_OK;
+    if (!stride_ok(ldc, KDA_LATENT_DIM) || !stride_ok(ldr, KDA_LATENT_ROPE)) return KDA_ERR_INVALID_ARG;
+    if (!c || !k_rope || !block_table || !aligned16(c) || !aligned16(k_rope)) return KDA_ERR_INVALID_ARG;
+    if ((reinterpret_cast<uintptr_t>(block_table) & 3u) || (reinterpret_cast<uintptr_t>(start_pos) & 3u))
+        return KDA_ERR_INVALID_ARG;
+    int* status = nullptr;
+    rc = device_setup(&status);
+    if (rc != KDA_OK) return rc;
+    rc = kda::launch_latent_gather(cache, cache_dtype == KDA_CACHE_E4M3, num_pages, page_size, block_table, max_pages,
+                                   start_pos, cu_seqlens, num_seqs, total_tokens, c, ldc, k_rope, ldr, status,
+                                   static_cast<cudaStream_t>(stream));
+    return rc == 0 ? KDA_OK : KDA_ERR_CUDA;
+}
+
+int kda_latent_decode(const uint16_t* q, const void* cache, int cache_dtype, int num_pages, int page_size,
+                      const int32_t* block_table, int max_pages, const int32_t* seq_lens,
+                      int N, int K, int H, float sm_scale, uint16_t* out, float* lse, void* stream) {
+    int rc = check_latent_cache(cache, cache_dtype, num_pages, page_size);
+    if (rc != KDA_OK) return rc;
+    if (N < 0 || K < 0 || H <= 0 || max_pages < 0 || !scale_ok(sm_scale)) return KDA_ERR_INVALID_ARG;
+    if (static_cast<int64_t>(K) * H > KDA_LATENT_MAX_ROWS) return KDA_ERR_UNSUPPORTED;
+    if (static_cast<int64_t>(max_pages) * page_size > INT32_MAX) return KDA_ERR_INVALID_ARG;
+    if (static_cast<int64_t>(N) * K * H >= (int64_t(1) << 31)) return KDA_ERR_INVALID_ARG;
+    if (N == 0 || K == 0) return KDA_OK;
+    if (!q || !seq_lens || !out || (max_pages > 0 && !block_table)) return KDA_ERR_INVALID_ARG;
+    if (!aligned16(q) || !aligned16(out)) return KDA_ERR_INVALID_ARG;
+    const void* p4[] = {block_table, seq_lens, lse};
+    for (const void* p : p4)
+        if (reinterpret_cast<uintptr_t>(p) & 3u) return KDA_ERR_INVALID_ARG;
+    int* status = nullptr;
+    rc = device_setup(&status);
+    if (rc != KDA_OK) return rc;
+    rc = kda::launch_latent_decode(q, cache, cache_dtype == KDA_CACHE_E4M3, num_pages, page_size, block_table, max_pages,
+                                   seq_lens, N, K, H, sm_scale, out, lse, status, static_cast<cudaStream_t>(stream));
+    return rc == 0 ? KDA_OK : KDA_ERR_CUDA;
+}
+
+int kda_latent_prefill(const uint16_t* q, const uint16_t* k, int64_t ldk, int64_t hdk,
+                       const uint16_t* v, int64_t ldv, int64_t hdv, const uint16_t* k_rope, int64_t ldr,
+                       const int32_t* cu_q, const int32_t* cu_q_host, const int32_t* cu_k, const int32_t* cu_k_host,
+                       int num_seqs, int total_q, int total_k, int H, int causal, float sm_scale,
+                       uint16_t* out, float* lse, void* stream) {
+    if (num_seqs < 0 || total_q < 0 || total_k < 0 || H <= 0 || !scale_ok(sm_scale)) return KDA_ERR_INVALID_ARG;
+    if (causal != 0 && causal != 1) return KDA_ERR_INVALID_ARG;
+    if (!cu_ok(cu_q, cu_q_host, num_seqs, total_q) || !cu_ok(cu_k, cu_k_host, num_seqs, total_k)) return KDA_ERR_INVALID_ARG;
+    if (total_q == 0) return KDA_OK;
+    if (!q || !out || !aligned16(q) || !aligned16(out)) return KDA_ERR_INVALID_ARG;
+    if (reinterpret_cast<uintptr_t>(lse) & 3u) return KDA_ERR_INVALID_ARG;
+    if (total_k > 0) {
+        if (!k || !v || !k_rope || !aligned16(k) || !aligned16(v) || !aligned16(k_rope)) return KDA_ERR_INVALID_ARG;
+        if (!stride_ok(hdk, 128) || !stride_ok(hdv, 128) || !stride_ok(ldr, KDA_LATENT_ROPE)) return KDA_ERR_INVALID_ARG;
+        if (!stride_ok(ldk, 128) || !stride_ok(ldv, 128)) return KDA_ERR_INVALID_ARG;
+    }
+    if (static_cast<int64_t>(total_q) * H >= (int64_t(1) << 31)) return KDA_ERR_INVALID_ARG;
+    int max_q = 0;
+    for (int n = 0; n < num_seqs; ++n) max_q = cu_q_host[n + 1] - cu_q_host[n] > max_q ? cu_q_host[n + 1] - cu_q_host[n] : max_q;
+    int* status = nullptr;
+    int rc = device_setup(&status);
+    if (rc != KDA_OK) return rc;
+    rc = kda::launch_latent_prefill(q, k, ldk, hdk, v, ldv, hdv, k_rope, ldr, cu_q, cu_k, num_seqs, total_q, total_k, max_q,
+                                    H, causal, sm_scale, out, lse, status, static_cast<cudaStream_t>(stream));
+    return rc == 0 ? KDA_OK : KDA_ERR_CUDA;
+}
+
+int kda_verify_draft(const float* target_probs, int64_t ldp, const float* draft_probs, int64_t ldq,
+                     const int32_t* draft_tokens, const int32_t* num_draft, const float* u_accept,
+                     const float* u_sample, int N, int K, int V, int32_t* tokens, int32_t* num_tokens,
+                     void* stream) {
+    if (N < 0 || K < 0 || V <= 0) return KDA_ERR_INVALID_ARG;
+    if (K > KDA_VERIFY_MAX_DRAFT || V > (1 << 30)) return KDA_ERR_UNSUPPORTED;
+    if (N == 0) return KDA_OK;
+    if (ldp < V || (draft_probs && ldq < V)) return KDA_ERR_INVALID_ARG;
+    if (static_cast<int64_t>(N) * 8 >= (int64_t(1) << 31)) return KDA_ERR_INVALID_ARG;
+    if (!target_probs || !u_sample || !tokens || !num_tokens) return KDA_ERR_INVALID_ARG;
+    if (K > 0 && (!draft_tokens || !u_accept)) return KDA_ERR_INVALID_ARG;
+    const void* p4[] = {target_probs, draft_probs, draft_tokens, num_draft, u_accept, u_sample, tokens, num_tokens};
+    for (const void* p : p4)
+        if (reinterpret_cast<uintptr_t>(p) & 3u) return KDA_ERR_INVALID_ARG;
+    int* status = nullptr;
+    int rc = device_setup(&status);
+    if (rc != KDA_OK) return rc;
+    rc = kda::launch_verify(target_probs, ldp, draft_probs, ldq, draft_tokens, num_draft, u_accept, u_sample, N, K, V,
+                            tokens, num_tokens, status, static_cast<cudaStream_t>(stream));
     return rc == 0 ? KDA_OK : KDA_ERR_CUDA;
 }
 

@@ -1,0 +1,38 @@
+// latent.cuh -- the latent cache's row formats and small device helpers of the latent
+// attention kernels.
+#pragma once
+#include <cstdint>
+#include <cuda_fp16.h>
+#include <cuda_fp8.h>
+#include "common.cuh"
+
+namespace kda {
+
+constexpr int kLatDim = 512;                     // latent values a token
+constexpr int kLatRope = 64;                     // shared position key values a token
+constexpr int kLatQ = kLatDim + kLatRope;        // absorbed query length
+constexpr int kLatRowBf16 = kLatQ * 2;           // 1152 bytes: latent, position key
+// 656 bytes: 512 codes, the position key (64 bf16), the fp32 scale, 12 bytes of zero
+constexpr int kLatRowE4m3 = kLatDim + 2 * kLatRope + 16;
+constexpr int kLatScaleAt = kLatDim + 2 * kLatRope;
+constexpr int kStatusIndex = -1;                 // KDA_ERR_INVALID_ARG, recorded on the device
+
+__host__ __device__ constexpr int lat_row_bytes(bool e4m3) { return e4m3 ? kLatRowE4m3 : kLatRowBf16; }
+
+__device__ __forceinline__ float lat_ex2(float x) {
+    float y;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
+
+// Two e4m3 codes (low byte first) -> two floats.
+__device__ __forceinline__ float2 e4m3x2_to_f32(uint32_t w) {
+    const __half2_raw h = __nv_cvt_fp8x2_to_halfraw2(static_cast<__nv_fp8x2_storage_t>(w & 0xFFFFu), __NV_E4M3);
+    return __half22float2(__half2(h));
+}
+// Two floats -> two e4m3 codes (low byte first), nearest even, magnitudes above 448 -> 448, NaN stays NaN.
+__device__ __forceinline__ uint32_t f32x2_to_e4m3x2(float lo, float hi) {
+    return __nv_cvt_float2_to_fp8x2(make_float2(lo, hi), __NV_SATFINITE, __NV_E4M3);
+}
+
+}  // namespace kda

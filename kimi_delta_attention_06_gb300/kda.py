@@ -3,11 +3,13 @@
 The functions named like the C entry points (``kda_chunk_prefill``,
 ``kda_chunk_prefill_ex``, ``kda_chunk_prefill_noalloc``, ``kda_decode_step``,
 ``kda_prepare_inputs``, ``kda_output_norm``, ``kda_decode_multi``, ``kda_ckpt_count``,
+``kda_latent_append``, ``kda_latent_gather``, ``kda_latent_decode``, ``kda_latent_prefill``, ``kda_verify_draft``,
 ``kda_device_status``, ``kda_status_string``, ``kda_chunk_size``) only marshal
 arguments: torch
 tensors become raw device pointers, the current torch stream becomes the
-``stream`` argument, and a negative status raises ``KdaError``.  ``prefill``
-and ``decode_step`` additionally allocate the output tensors with torch.
+``stream`` argument, and a negative status raises ``KdaError``.  ``prefill``,
+``decode_step``, ``latent_gather``, ``latent_decode``, ``latent_prefill`` and ``verify_draft``
+additionally allocate the output tensors with torch.
 
 There is no fallback: if ``libkda.so`` is missing or cannot be loaded the
 first call raises.
@@ -39,9 +41,18 @@ KDA_MAX_SEGMENTS = 64
 KDA_DECAY_CHANNEL = 0
 KDA_DECAY_HEAD = 1
 KDA_DECAY_NONE = 2
+KDA_CACHE_BF16 = 0
+KDA_CACHE_E4M3 = 1
+KDA_LATENT_DIM = 512
+KDA_LATENT_ROPE = 64
+KDA_LATENT_MAX_PAGE = 1024
+KDA_LATENT_MAX_ROWS = 512
+KDA_VERIFY_MAX_DRAFT = 64
 
 _vp = ctypes.c_void_p
 _i = ctypes.c_int
+_i64 = ctypes.c_int64
+_f = ctypes.c_float
 
 
 class KdaError(RuntimeError):
@@ -90,6 +101,20 @@ def load():
                                                _vp, _vp, _vp, _vp, _vp, _vp]
             lib.kda_output_norm.restype = _i
             lib.kda_output_norm.argtypes = [_vp, _i, _vp, ctypes.c_float, _vp, _i, _i, _i, _vp]
+            lib.kda_latent_row_bytes.restype = _i
+            lib.kda_latent_row_bytes.argtypes = [_i]
+            lib.kda_latent_append.restype = _i
+            lib.kda_latent_append.argtypes = [_vp, _i64, _vp, _i64, _vp, _i, _i, _i, _vp, _i, _vp]
+            lib.kda_latent_gather.restype = _i
+            lib.kda_latent_gather.argtypes = [_vp, _i, _i, _i, _vp, _i, _vp, _vp, _vp, _i, _i, _vp, _i64, _vp, _i64,
+                                              _vp]
+            lib.kda_latent_decode.restype = _i
+            lib.kda_latent_decode.argtypes = [_vp, _vp, _i, _i, _i, _vp, _i, _vp, _i, _i, _i, _f, _vp, _vp, _vp]
+            lib.kda_latent_prefill.restype = _i
+            lib.kda_latent_prefill.argtypes = [_vp, _vp, _i64, _i64, _vp, _i64, _i64, _vp, _i64, _vp, _vp, _vp, _vp,
+                                               _i, _i, _i, _i, _i, _f, _vp, _vp, _vp]
+            lib.kda_verify_draft.restype = _i
+            lib.kda_verify_draft.argtypes = [_vp, _i64, _vp, _i64, _vp, _vp, _vp, _vp, _i, _i, _i, _vp, _vp, _vp]
             lib.kda_ckpt_count.restype = ctypes.c_int64
             lib.kda_ckpt_count.argtypes = [_vp, _i, _i]
             lib.kda_ckpt_count_ex.restype = ctypes.c_int64
@@ -307,6 +332,105 @@ def kda_output_norm(o, o_dtype: int, gamma, eps: float, y, total_tokens: int, H:
     _check(rc, "kda_output_norm")
 
 
+def _strided(t: torch.Tensor):
+    """Device pointer of a tensor whose last dimension is contiguous (its other strides are passed on)."""
+    if t.numel() and t.stride(-1) != 1:
+        raise ValueError("the last dimension of a KDA tensor must be contiguous")
+    return ctypes.c_void_p(t.data_ptr())
+
+
+def _step(t: torch.Tensor, dim: int, least: int) -> int:
+    """Stride of a dimension, in elements (any where it has one entry: a value the checks pass)."""
+    return t.stride(dim) if t.shape[dim] > 1 else least
+
+
+def _i32(t: Optional[torch.Tensor]) -> Optional[torch.Tensor]:
+    if t is not None and t.dtype != torch.int32:
+        raise TypeError(f"expected an int32 tensor, got {t.dtype}")
+    return t
+
+
+def _f32(t: Optional[torch.Tensor]) -> Optional[torch.Tensor]:
+    if t is not None and t.dtype != torch.float32:
+        raise TypeError(f"expected a float32 tensor, got {t.dtype}")
+    return t
+
+
+def _host32(t):
+    return torch.as_tensor(t).to(device="cpu", dtype=torch.int32).contiguous()
+
+
+def kda_latent_row_bytes(cache_dtype: int) -> int:
+    n = load().kda_latent_row_bytes(int(cache_dtype))
+    _check(min(n, 0), "kda_latent_row_bytes")
+    return int(n)
+
+
+def _pages(cache: torch.Tensor, cache_dtype: int):
+    """(pointer, num_pages, page_size) of a cache [num_pages, page_size, row bytes] uint8."""
+    if cache.dtype != torch.uint8 or cache.dim() != 3 or cache.shape[2] != kda_latent_row_bytes(cache_dtype):
+        raise ValueError("a latent cache is a uint8 tensor [num_pages, page_size, row bytes of its cache_dtype]")
+    return _ptr(cache), int(cache.shape[0]), int(cache.shape[1])
+
+
+def kda_latent_append(c, k_rope, cache, cache_dtype: int, slots, total_tokens: int, stream=None):
+    p, num_pages, page_size = _pages(cache, cache_dtype)
+    rc = load().kda_latent_append(_strided(_bits16(c)), _step(c, 0, KDA_LATENT_DIM),
+                                  _strided(_bits16(k_rope)), _step(k_rope, 0, KDA_LATENT_ROPE), p,
+                                  int(cache_dtype), num_pages, page_size, _ptr(_i32(slots)), int(total_tokens),
+                                  _stream(stream))
+    _check(rc, "kda_latent_append")
+
+
+def kda_latent_gather(cache, cache_dtype: int, block_table, start_pos, cu_seqlens, cu_seqlens_host, num_seqs: int,
+                      total_tokens: int, c, k_rope, stream=None):
+    p, num_pages, page_size = _pages(cache, cache_dtype)
+    cu_host = _host32(cu_seqlens_host)
+    rc = load().kda_latent_gather(p, int(cache_dtype), num_pages, page_size, _ptr(_i32(block_table)),
+                                  int(block_table.shape[1]), _ptr(_i32(start_pos)), _ptr(_i32(cu_seqlens)),
+                                  ctypes.c_void_p(cu_host.data_ptr()), int(num_seqs), int(total_tokens),
+                                  _strided(_bits16(c)), _step(c, 0, KDA_LATENT_DIM), _strided(_bits16(k_rope)),
+                                  _step(k_rope, 0, KDA_LATENT_ROPE), _stream(stream))
+    _check(rc, "kda_latent_gather")
+
+
+def kda_latent_decode(q, cache, cache_dtype: int, block_table, seq_lens, N: int, K: int, H: int, sm_scale: float, out,
+                      lse, stream=None):
+    p, num_pages, page_size = _pages(cache, cache_dtype)
+    rc = load().kda_latent_decode(_ptr(_bits16(q)), p, int(cache_dtype), num_pages, page_size, _ptr(_i32(block_table)),
+                                  int(block_table.shape[1]), _ptr(_i32(seq_lens)), int(N), int(K), int(H),
+                                  float(sm_scale), _ptr(_bits16(out)), _ptr(_f32(lse)), _stream(stream))
+    _check(rc, "kda_latent_decode")
+
+
+def kda_latent_prefill(q, k, v, k_rope, cu_q, cu_q_host, cu_k, cu_k_host, num_seqs: int, total_q: int, total_k: int,
+                       H: int, causal: int, sm_scale: float, out, lse, stream=None):
+    cq, ck = _host32(cu_q_host), _host32(cu_k_host)
+    rc = load().kda_latent_prefill(_ptr(_bits16(q)), _strided(_bits16(k)), _step(k, 0, 128), _step(k, 1, 128),
+                                   _strided(_bits16(v)), _step(v, 0, 128), _step(v, 1, 128), _strided(_bits16(k_rope)),
+                                   _step(k_rope, 0, KDA_LATENT_ROPE), _ptr(_i32(cu_q)), ctypes.c_void_p(cq.data_ptr()), _ptr(_i32(cu_k)),
+                                   ctypes.c_void_p(ck.data_ptr()), int(num_seqs), int(total_q), int(total_k), int(H),
+                                   int(causal), float(sm_scale), _ptr(_bits16(out)), _ptr(_f32(lse)), _stream(stream))
+    _check(rc, "kda_latent_prefill")
+
+
+def kda_verify_draft(target_probs, draft_probs, draft_tokens, num_draft, u_accept, u_sample, N: int, K: int, V: int,
+                     tokens, num_tokens, stream=None):
+    def rows(t, per):           # rows of V values, one constant stride apart
+        if t is None:
+            return None, 0
+        if t.shape[0] > 1 and t.stride(0) != per * t.stride(1):
+            raise ValueError("the probability rows of consecutive sequences must be evenly spaced")
+        return _strided(_f32(t)), t.stride(1) if t.shape[0] * per > 1 else V
+
+    tp, ldp = rows(target_probs, K + 1)
+    dp, ldq = rows(draft_probs, K)
+    rc = load().kda_verify_draft(tp, ldp, dp, ldq, _ptr(_i32(draft_tokens)), _ptr(_i32(num_draft)), _ptr(_f32(u_accept)),
+                                 _ptr(_f32(u_sample)), int(N), int(K), int(V), _ptr(_i32(tokens)),
+                                 _ptr(_i32(num_tokens)), _stream(stream))
+    _check(rc, "kda_verify_draft")
+
+
 def kda_debug_expire_wait(limit_ns: int, stream=None):
     _check(load().kda_debug_expire_wait(int(limit_ns), _stream(stream)), "kda_debug_expire_wait")
 
@@ -365,3 +489,63 @@ def decode_step(q, k, v, log_alpha, beta, state, out_dtype=torch.bfloat16, strea
     kda_decode_step(q, k, v, log_alpha, beta, state, out,
                     KDA_OUT_F32 if out_dtype == torch.float32 else KDA_OUT_BF16, N, H, Dk, Dv, stream)
     return out
+
+
+def latent_cache(num_pages: int, page_size: int, cache_dtype: int = KDA_CACHE_BF16, device="cuda") -> torch.Tensor:
+    """A zeroed latent cache [num_pages, page_size, row bytes]."""
+    return torch.zeros(num_pages, page_size, kda_latent_row_bytes(cache_dtype), dtype=torch.uint8, device=device)
+
+
+def latent_append(c, k_rope, cache, cache_dtype: int, slots, stream=None):
+    """Write tokens c [T, 512] and k_rope [T, 64] into the cache rows ``slots`` [T] (in place)."""
+    kda_latent_append(c, k_rope, cache, cache_dtype, slots, c.shape[0], stream)
+
+
+def latent_gather(cache, cache_dtype: int, block_table, cu_seqlens_host, cu_seqlens=None, start_pos=None, stream=None):
+    """Read sequences back as dense rows; returns (c [T, 512], k_rope [T, 64]), bf16."""
+    cu_host = _host32(cu_seqlens_host)
+    N, T = cu_host.numel() - 1, int(cu_host[-1])
+    if cu_seqlens is None:
+        cu_seqlens = cu_host.to(cache.device)
+    c = torch.empty(T, KDA_LATENT_DIM, device=cache.device, dtype=torch.bfloat16)
+    r = torch.empty(T, KDA_LATENT_ROPE, device=cache.device, dtype=torch.bfloat16)
+    kda_latent_gather(cache, cache_dtype, block_table, start_pos, cu_seqlens, cu_host, N, T, c, r, stream)
+    return c, r
+
+
+def latent_decode(q, cache, cache_dtype: int, block_table, seq_lens, sm_scale: float, want_lse: bool = False, stream=None):
+    """Absorbed latent attention of q [N, K, H, 576] over the cache; returns (out [N, K, H, 512] bf16,
+    lse [N, K, H] fp32 or None)."""
+    N, K, H, _ = q.shape
+    out = torch.empty(N, K, H, KDA_LATENT_DIM, device=q.device, dtype=torch.bfloat16)
+    lse = torch.empty(N, K, H, device=q.device, dtype=torch.float32) if want_lse else None
+    kda_latent_decode(q, cache, cache_dtype, block_table, seq_lens, N, K, H, sm_scale, out, lse, stream)
+    return out, lse
+
+
+def latent_prefill(q, k, v, k_rope, cu_q_host, cu_k_host, sm_scale: float, causal: bool = True, cu_q=None, cu_k=None,
+                   want_lse: bool = False, stream=None):
+    """Expanded latent attention of q [Tq, H, 192] over k, v [Tk, H, 128] and k_rope [Tk, 64]; returns
+    (out [Tq, H, 128] bf16, lse [Tq, H] fp32 or None)."""
+    cq, ck = _host32(cu_q_host), _host32(cu_k_host)
+    if cu_q is None:
+        cu_q = cq.to(q.device)
+    if cu_k is None:
+        cu_k = ck.to(q.device)
+    Tq, H, _ = q.shape
+    out = torch.empty(Tq, H, 128, device=q.device, dtype=torch.bfloat16)
+    lse = torch.empty(Tq, H, device=q.device, dtype=torch.float32) if want_lse else None
+    kda_latent_prefill(q, k, v, k_rope, cu_q, cq, cu_k, ck, cq.numel() - 1, Tq, k.shape[0], H, int(bool(causal)),
+                       sm_scale, out, lse, stream)
+    return out, lse
+
+
+def verify_draft(target_probs, draft_probs, draft_tokens, u_accept, u_sample, num_draft=None, stream=None):
+    """Accept or reject draft_tokens [N, K] against target_probs [N, K + 1, V] (draft_probs [N, K, V] or None);
+    returns (tokens [N, K + 1] int32, num_tokens [N] int32)."""
+    N, K1, V = target_probs.shape
+    tokens = torch.empty(N, K1, device=target_probs.device, dtype=torch.int32)
+    num = torch.empty(N, device=target_probs.device, dtype=torch.int32)
+    kda_verify_draft(target_probs, draft_probs, draft_tokens, num_draft, u_accept, u_sample, N, K1 - 1, V, tokens, num,
+                     stream)
+    return tokens, num
