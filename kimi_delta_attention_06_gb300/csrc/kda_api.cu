@@ -51,7 +51,8 @@ int launch_latent_gather(const void* cache, int e4m3, int num_pages, int page_si
                          uint16_t* r, long long ldr, int* status, cudaStream_t stream);
 int launch_latent_decode(const uint16_t* q, const void* cache, int e4m3, int num_pages, int page_size,
                          const int32_t* table, int max_pages, const int32_t* seq_lens, int N, int K, int H,
-                         float sm_scale, uint16_t* out, float* lse, int* status, cudaStream_t stream);
+                         float sm_scale, uint16_t* out, float* lse, void* scratch, int* status, cudaStream_t stream);
+size_t latent_decode_scratch(int rows);
 int launch_latent_prefill(const uint16_t* q, const uint16_t* k, long long ldk, long long hdk, const uint16_t* v,
                           long long ldv, long long hdv, const uint16_t* r, long long ldr, const int32_t* cu_q,
                           const int32_t* cu_k, int num_seqs, int total_q, int total_k, int max_q, int H, int causal,
@@ -844,9 +845,16 @@ int kda_latent_decode(const uint16_t* q, const void* cache, int cache_dtype, int
     int* status = nullptr;
     rc = device_setup(&status);
     if (rc != KDA_OK) return rc;
+    cudaMemPool_t pool = nullptr;
+    rc = workspace_pool(&pool);
+    if (rc != KDA_OK) return rc;
+    const cudaStream_t st = static_cast<cudaStream_t>(stream);
+    void* ws = nullptr;
+    if (cudaMallocFromPoolAsync(&ws, kda::latent_decode_scratch(K * H), pool, st) != cudaSuccess) return KDA_ERR_CUDA;
     rc = kda::launch_latent_decode(q, cache, cache_dtype == KDA_CACHE_E4M3, num_pages, page_size, block_table, max_pages,
-                                   seq_lens, N, K, H, sm_scale, out, lse, status, static_cast<cudaStream_t>(stream));
-    return rc == 0 ? KDA_OK : KDA_ERR_CUDA;
+                                   seq_lens, N, K, H, sm_scale, out, lse, ws, status, st);
+    const bool freed = cudaFreeAsync(ws, st) == cudaSuccess;
+    return (rc == 0 && freed) ? KDA_OK : KDA_ERR_CUDA;
 }
 
 int kda_latent_prefill(const uint16_t* q, const uint16_t* k, int64_t ldk, int64_t hdk,

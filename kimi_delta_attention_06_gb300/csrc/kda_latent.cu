@@ -3,7 +3,16 @@
 // Row (n, j, h) of the output: x_t = scale * (q[:512] . c_t + q[512:] . r_t) over the tokens the
 // query sees, out = sum_t softmax(x)_t c_t, with one pass over the tokens: the running maximum m,
 // the sum l of exp(x - m) and the weighted sum of c are rescaled when m grows.
+//
+// All K * H rows of a sequence read the same cached vectors, so both products run on the tensor
+// cores with the cached tokens on the M side: per tile of 64 tokens
+//     S^T [64 tokens x R rows]      = C [64 x 576] Q^T                 (M = 64, N = R)
+//     O^T [512 channels x R rows]  += C[:, :512]^T P^T [64 x R]        (4 blocks of M = 128, N = R)
+// with R = 16, 32 or 64 rows a CTA, so few rows do not leave the tensor cores' M side empty.  One
+// shared-memory tile of C (128-byte swizzle) serves both: K-major for S, MN-major for O.
+#include <cuda.h>
 #include "latent.cuh"
+#include "tc.cuh"
 
 namespace kda {
 
@@ -97,35 +106,764 @@ __device__ void latent_row(const uint16_t* __restrict__ q, const LatentCache& ch
     if (lse && lane == 0) *lse = (m + log2f(l)) * 0.69314718055994531f;     // l = 0: -inf
 }
 
-template <bool E4M3>
-__global__ void __launch_bounds__(128)
-kda_latent_rows_kernel(const uint16_t* __restrict__ q, LatentCache ch, const int32_t* __restrict__ seq_lens, int K, int H,
-                       long long rows, float scale_log2, uint16_t* __restrict__ out, float* __restrict__ lse, int* status)
-{
-    const long long row = static_cast<long long>(blockIdx.x) * 4 + (threadIdx.x >> 5);
-    if (row >= rows) return;
-    const int n = static_cast<int>(row / (static_cast<long long>(K) * H));
-    const int j = static_cast<int>(row / H % K);
-    int len = seq_lens[n];
-    if (len < 0 || len > static_cast<long long>(ch.max_pages) * ch.page_size) {
-        if ((threadIdx.x & 31) == 0) set_status(status, kStatusIndex);
-        len = 0;
+
+// ---- work split ------------------------------------------------------------------------------
+// The sequences' 64-token tiles, one after another, are cut into G equal runs, one per CTA
+// (x the row tiles, which run side by side over the same tokens so that the second reader finds
+// them in L2).  A CTA's run covers parts of one or several sequences (segments).  A segment that
+// is a whole sequence is finished by its CTA; the others leave partial (m, l, O) in scratch, at
+// most two per CTA (its first and its last), which the combine kernel joins.
+constexpr int kTile = 64;                       // tokens per tile
+constexpr int kMinTiles = 2;                    // shortest run of tiles worth a CTA of its own
+
+struct LatWork {
+    const int32_t* seq_lens;
+    int N, G;                                   // G: most runs
+    long long max_len;
+};
+
+__device__ __forceinline__ int lat_len(const LatWork& w, int n) {
+    const int len = w.seq_lens[n];
+    return len < 0 || len > w.max_len ? 0 : len;
+}
+__device__ __forceinline__ int lat_tiles(int len) { return (len + kTile - 1) / kTile; }
+// Runs in use for T tiles, and the bounds of run c.
+__device__ __forceinline__ long long lat_runs(long long T, int G) {
+    const long long r = (T + kMinTiles - 1) / kMinTiles;
+    return r < G ? r : G;
+}
+__device__ __forceinline__ long long run_begin(long long T, long long runs, long long c) { return c * T / runs; }
+// The run that holds tile t: the largest c with c T / runs (rounded down) <= t.
+__device__ __forceinline__ long long run_of(long long T, long long runs, long long t) { return ((t + 1) * runs - 1) / T; }
+
+// Walks the segments of one run; every warp keeps its own copy (init is warp-collective).
+struct SegWalk {
+    long long pos, end, base;                   // next tile, end of the run, first tile of sequence n
+    int n, len, tiles;
+    int t0, t1;                                 // current segment: tiles [t0, t1) of sequence n
+    bool first;
+
+    __device__ void init(const LatWork& w, int c) {
+        const int lane = threadIdx.x & 31;
+        long long T = 0;
+        for (int i = lane; i < w.N; i += 32) T += lat_tiles(lat_len(w, i));
+#pragma unroll
+        for (int off = 16; off > 0; off >>= 1) T += __shfl_xor_sync(0xffffffffu, T, off);
+        pos = end = base = 0;
+        n = len = tiles = t0 = t1 = 0;
+        first = true;
+        if (T == 0) return;
+        const long long runs = lat_runs(T, w.G);
+        if (c >= runs) return;
+        pos = run_begin(T, runs, c);
+        end = run_begin(T, runs, c + 1);
+        for (int i0 = 0; i0 < w.N; i0 += 32) {
+            const int mine = i0 + lane < w.N ? lat_tiles(lat_len(w, i0 + lane)) : 0;
+            int incl = mine;
+#pragma unroll
+            for (int off = 1; off < 32; off <<= 1) {
+                const int o = __shfl_up_sync(0xffffffffu, incl, off);
+                if (lane >= off) incl += o;
+            }
+            const unsigned hit = __ballot_sync(0xffffffffu, base + incl > pos);
+            if (hit) {
+                const int at = __ffs(hit) - 1;
+                n = i0 + at;
+                base += __shfl_sync(0xffffffffu, incl - mine, at);
+                break;
+            }
+            base += __shfl_sync(0xffffffffu, incl, 31);
+        }
+        len = lat_len(w, n);
+        tiles = lat_tiles(len);
     }
-    latent_row<E4M3>(q + row * kLatQ, ch, n, len - (K - 1 - j), scale_log2, out + row * kLatDim, lse ? lse + row : nullptr,
-                     status);
+    // The next segment; false when the run is done.
+    __device__ bool next(const LatWork& w) {
+        if (pos >= end) return false;
+        while (pos >= base + tiles) {
+            base += tiles;
+            ++n;
+            len = lat_len(w, n);
+            tiles = lat_tiles(len);
+        }
+        t0 = static_cast<int>(pos - base);
+        t1 = static_cast<int>(end - base < tiles ? end - base : tiles);
+        pos = base + t1;
+        return true;
+    }
+    __device__ bool whole() const { return t0 == 0 && t1 == tiles; }
+};
+
+// ---- the tensor-core kernel --------------------------------------------------------------------
+struct LatMaps { CUtensorMap q, c; };            // q [rows, 576], bf16 cache [slots, 576]; 64-column boxes
+
+struct LatArgs {
+    LatWork w;
+    LatentCache ch;
+    const uint16_t* q;
+    int K, H, rows, RT;                          // rows = K * H, RT row tiles
+    int box;                                     // cache rows per TMA box (divides the page and the tile)
+    float scale_log2;
+    uint16_t* out;
+    float* lse;
+    float *part_o, *part_ml;                     // partials: [run][row tile][2][R][512], [..][R][2]
+    int* status;
+};
+
+template <int R, bool E4M3>
+struct LatShape {
+    static constexpr int kSoft = 128;            // warps 0..3: softmax, rescale, epilogue
+    static constexpr int kMmaWarp = 4;
+    static constexpr int kProdWarps = E4M3 ? 8 : 1;
+    static constexpr int kThreads = kSoft + 32 + 32 * kProdWarps;
+    static constexpr uint32_t kSlabQ = R * 128u, kSlabC = kTile * 128u;
+    static constexpr uint32_t kStage = 9u * kSlabC;
+    static constexpr uint32_t oQ = 0, oC = 9u * kSlabQ, oP = oC + 2u * kStage, oBar = oP + kTile * 128u;
+    static constexpr uint32_t kBytes = oBar + 64u + 4u + 5u * R * 4u + 64u;
+    static constexpr uint32_t kTmemCols = R == 16 ? 128u : R == 32 ? 256u : 512u;     // 4 R (O) + 2 R (S)
+};
+// shared memory: 9 slabs of Q | 2 stages of 9 slabs of C | P | barriers, exchange
+static_assert(LatShape<64, false>::kBytes <= 232448, "227 KB of shared memory");
+
+constexpr float kLatTau = 8.f;                   // scores may exceed the running maximum by 2^8 before a rescale
+constexpr uint32_t kBarSoft = 1;                 // named barrier of the softmax warps
+
+// Columns of S^T in the 16 x 256-bit shape: thread T holds tokens T / 4 and T / 4 + 8 of its warp's
+// 16, rows 8 b + 2 (T % 4) + {0, 1}: registers 4 b + {0, 1} (token T / 4) and 4 b + {2, 3}.
+template <int R>
+__device__ __forceinline__ void tmem_ld_s(uint32_t ta, float (&r)[R / 2]) {
+    uint32_t* u = reinterpret_cast<uint32_t*>(r);
+    if constexpr (R == 16) {
+        asm volatile("tcgen05.ld.sync.aligned.16x256b.x2.b32 {%0,%1,%2,%3,%4,%5,%6,%7}, [%8];"
+                     : "=r"(u[0]), "=r"(u[1]), "=r"(u[2]), "=r"(u[3]), "=r"(u[4]), "=r"(u[5]), "=r"(u[6]), "=r"(u[7])
+                     : "r"(ta));
+    } else {
+#pragma unroll
+        for (int i = 0; i < R / 32; ++i)
+            asm volatile("tcgen05.ld.sync.aligned.16x256b.x4.b32 "
+                         "{%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];"
+                         : "=r"(u[16 * i + 0]), "=r"(u[16 * i + 1]), "=r"(u[16 * i + 2]), "=r"(u[16 * i + 3]),
+                           "=r"(u[16 * i + 4]), "=r"(u[16 * i + 5]), "=r"(u[16 * i + 6]), "=r"(u[16 * i + 7]),
+                           "=r"(u[16 * i + 8]), "=r"(u[16 * i + 9]), "=r"(u[16 * i + 10]), "=r"(u[16 * i + 11]),
+                           "=r"(u[16 * i + 12]), "=r"(u[16 * i + 13]), "=r"(u[16 * i + 14]), "=r"(u[16 * i + 15])
+                         : "r"(ta + 32u * i));
+    }
+    tc::tmem_wait_ld();
+}
+
+// Row (n, j, h) again, in fp32 over exactly the tokens it sees: for results that a NaN or infinity
+// in a token that other rows of the tile see has spoilt (0 * NaN in the product with P).
+template <bool E4M3>
+__device__ __noinline__ void latent_row_again(const LatArgs& a, int n, int row, int see) {
+    const long long at = static_cast<long long>(n) * a.rows + row;
+    latent_row<E4M3>(a.q + at * kLatQ, a.ch, n, see, a.scale_log2, a.out + at * kLatDim, a.lse ? a.lse + at : nullptr,
+                     a.status);
+}
+
+template <int R, bool E4M3>
+__global__ void __launch_bounds__(LatShape<R, E4M3>::kThreads, 1)
+kda_latent_decode_kernel(const __grid_constant__ LatMaps maps, const LatArgs a)
+{
+    using Sh = LatShape<R, E4M3>;
+    extern __shared__ __align__(1024) uint8_t smem[];
+    uint8_t* sQ = smem + Sh::oQ;
+    uint8_t* sC = smem + Sh::oC;
+    uint8_t* sP = smem + Sh::oP;
+    uint64_t* bars = reinterpret_cast<uint64_t*>(smem + Sh::oBar);
+    uint64_t *full = bars, *empty = bars + 2, *s_full = bars + 4, *p_full = bars + 6, *q_full = bars + 7;
+    uint32_t* s_tmem = reinterpret_cast<uint32_t*>(bars + 8);
+    float* s_red = reinterpret_cast<float*>(bars + 8) + 4;      // [4][R]
+    float* s_f = s_red + 4 * R;                                 // [R]
+
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    const int rt = blockIdx.x % a.RT, run = blockIdx.x / a.RT;
+    const int row0 = rt * R, nrows = min(R, a.rows - row0);
+
+    if (tid == 0) {
+        for (int i = 0; i < 2; ++i) {
+            tc::mbar_init(&full[i], Sh::kProdWarps);
+            tc::mbar_init(&empty[i], 1);
+            tc::mbar_init(&s_full[i], 1);
+        }
+        tc::mbar_init(p_full, Sh::kSoft);
+        tc::mbar_init(q_full, 1);
+        tc::mbar_fence_init();
+    }
+    if (warp == Sh::kMmaWarp) tc::tmem_alloc(s_tmem, Sh::kTmemCols);
+    tc::fence_before_sync();
+    __syncthreads();
+    tc::fence_after_sync();
+    const uint32_t tm = *s_tmem, tmO = tm, tmS = tm + 4 * R;
+    SegWalk sw;
+    sw.init(a.w, run);
+    bool ok = true;
+
+    if (warp < 4) {
+        // ---- softmax ----
+        const int tq = lane >> 2, rq = 2 * (lane & 3);
+        const uint32_t lane_tm = static_cast<uint32_t>(warp * 32) << 16;
+        float m[R / 4], l[R / 4];
+        int g = 0;                                              // tiles done by this CTA
+        while (ok && sw.next(a.w)) {
+#pragma unroll
+            for (int i = 0; i < R / 4; ++i) { m[i] = -INFINITY; l[i] = 0.f; }
+            const int clear = sw.len - (a.K - 1);               // tokens that every row sees
+            for (int t = sw.t0; t < sw.t1; ++t, ++g) {
+                ok = __all_sync(0xffffffffu, tc::mbar_wait_bounded(&s_full[g & 1], (g >> 1) & 1, kWaitLimitNs));
+                float x[R / 2];
+                if (ok) {
+                    tc::fence_after_sync();
+                    tmem_ld_s<R>(tmS + (g & 1) * R + lane_tm, x);
+                }
+                const int tok = t * kTile + 16 * warp + tq;     // and tok + 8
+                const bool edge = (t + 1) * kTile > clear;
+                if (edge) {
+#pragma unroll
+                    for (int i = 0; i < R / 2; ++i) {
+                        const int row = row0 + 8 * (i >> 2) + rq + (i & 1);
+                        const int see = clear + min(row / a.H, a.K - 1);
+                        x[i] = tok + 4 * (i & 2) < see ? x[i] * a.scale_log2 : -INFINITY;
+                    }
+                    // rows past the end of the sequence hold anything: they enter the second product as zeros
+                    const int valid = sw.len - t * kTile;
+                    if (!E4M3 && valid < kTile) {
+                        uint8_t* c = sC + (g & 1) * Sh::kStage;
+                        for (int i = tid; i < 8 * (kTile - max(valid, 0)) * 8; i += Sh::kSoft) {
+                            const int slab = i & 7, ch = (i >> 3) & 7, r = valid + (i >> 6);
+                            *reinterpret_cast<uint4*>(c + slab * Sh::kSlabC + r * 128 + ch * 16) = make_uint4(0, 0, 0, 0);
+                        }
+                    }
+                } else {
+#pragma unroll
+                    for (int i = 0; i < R / 2; ++i) x[i] *= a.scale_log2;
+                }
+                // the previous tile's product has read P and is in O
+                if (ok && g > 0) ok = tc::mbar_wait_bounded(&empty[(g - 1) & 1], ((g - 1) >> 1) & 1, kWaitLimitNs);
+                bool grow = !ok;
+#pragma unroll
+                for (int i = 0; i < R / 2; ++i) grow |= x[i] > m[2 * (i >> 2) + (i & 1)] + kLatTau;
+                if (!tc::named_sync_and(kBarSoft, Sh::kSoft, !grow)) {
+                    ok = tc::named_sync_and(kBarSoft, Sh::kSoft, ok);
+                    if (!ok) break;
+                    tc::fence_after_sync();
+#pragma unroll
+                    for (int i = 0; i < R / 4; ++i) {           // maxima of the tile, per row
+                        float v = fmaxf(x[4 * (i >> 1) + (i & 1)], x[4 * (i >> 1) + 2 + (i & 1)]);
+                        v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, 4));
+                        v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, 8));
+                        v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, 16));
+                        if (lane < 4) s_red[warp * R + 8 * (i >> 1) + rq + (i & 1)] = v;
+                    }
+                    tc::named_sync(kBarSoft, Sh::kSoft);
+#pragma unroll
+                    for (int i = 0; i < R / 4; ++i) {
+                        const int r = 8 * (i >> 1) + rq + (i & 1);
+                        const float mx = fmaxf(fmaxf(s_red[r], s_red[R + r]), fmaxf(s_red[2 * R + r], s_red[3 * R + r]));
+                        const float mn = fmaxf(m[i], mx);
+                        const float f = mn == m[i] ? 1.f : lat_ex2(m[i] - mn);
+                        m[i] = mn;
+                        l[i] *= f;
+                        if (tid < 4) s_f[r] = f;
+                    }
+                    tc::named_sync(kBarSoft, Sh::kSoft);
+                    if (t > sw.t0) {                            // O *= f, 16 columns (rows) at a time
+#pragma unroll 1
+                        for (int c0 = 0; c0 < R; c0 += 16) {
+                            bool one = true;
+#pragma unroll
+                            for (int i = 0; i < 16; ++i) one = one && s_f[c0 + i] == 1.f;
+                            if (one) continue;
+#pragma unroll 1
+                            for (int b = 0; b < 4; ++b) {
+                                float o[16];
+                                tc::tmem_ld16(tmO + b * R + c0 + lane_tm, o);
+                                tc::tmem_wait_ld();
+#pragma unroll
+                                for (int i = 0; i < 16; ++i) o[i] *= s_f[c0 + i];
+                                tc::tmem_st16(tmO + b * R + c0 + lane_tm, o);
+                            }
+                        }
+                        tc::tmem_wait_st();
+                    }
+                }
+                // P = exp2(x - m), rounded to bf16 for the product; the sums keep fp32
+                const int tr = 16 * warp + tq;
+#pragma unroll
+                for (int b = 0; b < R / 8; ++b) {
+                    const float m0 = m[2 * b] == -INFINITY ? 0.f : m[2 * b], m1 = m[2 * b + 1] == -INFINITY ? 0.f : m[2 * b + 1];
+                    const float p0 = lat_ex2(x[4 * b] - m0), p1 = lat_ex2(x[4 * b + 1] - m1);
+                    const float p2 = lat_ex2(x[4 * b + 2] - m0), p3 = lat_ex2(x[4 * b + 3] - m1);
+                    l[2 * b] += p0 + p2;
+                    l[2 * b + 1] += p1 + p3;
+                    const uint32_t off = tc::sw128_off16(tr, 8 * b + rq, kTile);
+                    *reinterpret_cast<uint32_t*>(sP + off) = f32x2_to_bf16x2_bits(p0, p1);
+                    *reinterpret_cast<uint32_t*>(sP + off + 8 * 128) = f32x2_to_bf16x2_bits(p2, p3);   // token + 8: same swizzle
+                }
+                tc::fence_smem_to_async();
+                tc::fence_before_sync();
+                tc::mbar_arrive(p_full);
+            }
+            if (!ok) break;
+            // ---- epilogue of the segment: O^T is complete once the last product is ----
+            ok = tc::mbar_wait_bounded(&empty[(g - 1) & 1], ((g - 1) >> 1) & 1, kWaitLimitNs);
+            ok = tc::named_sync_and(kBarSoft, Sh::kSoft, ok);
+            if (!ok) break;
+            tc::fence_after_sync();
+#pragma unroll
+            for (int i = 0; i < R / 4; ++i) {
+                float v = l[i];
+                v += __shfl_xor_sync(0xffffffffu, v, 4);
+                v += __shfl_xor_sync(0xffffffffu, v, 8);
+                v += __shfl_xor_sync(0xffffffffu, v, 16);
+                if (lane < 4) s_red[warp * R + 8 * (i >> 1) + rq + (i & 1)] = v;
+            }
+            tc::named_sync(kBarSoft, Sh::kSoft);
+            const bool whole = sw.whole();
+            const long long row_at = static_cast<long long>(sw.n) * a.rows + row0;
+            const size_t part = (static_cast<size_t>(run) * a.RT + rt) * 2 + (sw.first ? 0 : 1);
+#pragma unroll
+            for (int i = 0; i < R / 4; ++i) {
+                const int r = 8 * (i >> 1) + rq + (i & 1);
+                const float sum = (s_red[r] + s_red[R + r]) + (s_red[2 * R + r] + s_red[3 * R + r]);
+                if (tid < 4) {
+                    s_f[r] = sum == 0.f ? 0.f : 1.f / sum;
+                    if (!whole) {
+                        *reinterpret_cast<float2*>(a.part_ml + (part * R + r) * 2) = make_float2(m[i], sum);
+                    } else if (a.lse && r < nrows) {
+                        a.lse[row_at + r] = (m[i] + log2f(sum)) * 0.69314718055994531f;
+                    }
+                }
+            }
+            tc::named_sync(kBarSoft, Sh::kSoft);
+            uint32_t bad[2] = {0u, 0u};                          // rows with a result that is no number
+#pragma unroll 1
+            for (int c0 = 0; c0 < R; c0 += 16) {
+#pragma unroll 1
+                for (int b = 0; b < 4; ++b) {
+                    float o[16];
+                    tc::tmem_ld16(tmO + b * R + c0 + lane_tm, o);
+                    tc::tmem_wait_ld();
+                    const int ch = 128 * b + 32 * warp + lane;
+                    if (whole) {
+#pragma unroll
+                        for (int i = 0; i < 16; ++i)
+                            if (c0 + i < nrows) {
+                                const float v = s_f[c0 + i] == 0.f ? 0.f : o[i] * s_f[c0 + i];
+                                if (!(fabsf(v) < INFINITY)) bad[c0 >> 5] |= 1u << ((c0 + i) & 31);
+                                a.out[(row_at + c0 + i) * kLatDim + ch] = f32_to_bf16_bits(v);
+                            }
+                    } else {
+                        float* d = a.part_o + (part * R + c0) * kLatDim + ch;
+#pragma unroll
+                        for (int i = 0; i < 16; ++i)
+                            if (c0 + i < nrows) d[static_cast<size_t>(i) * kLatDim] = o[i];
+                    }
+                }
+            }
+            tc::fence_before_sync();                             // the next segment's product overwrites O
+            if (whole && a.K > 1) {
+#pragma unroll
+                for (int h = 0; h < 2; ++h) {
+                    bad[h] = __reduce_or_sync(0xffffffffu, bad[h]);
+                    if (lane == 0) reinterpret_cast<uint32_t*>(s_red)[warp * 2 + h] = bad[h];
+                }
+                tc::named_sync(kBarSoft, Sh::kSoft);
+                for (int r = warp; r < nrows; r += 4) {
+                    const uint32_t* f = reinterpret_cast<const uint32_t*>(s_red) + (r >> 5);
+                    const int j = (row0 + r) / a.H;
+                    if (((f[0] | f[2] | f[4] | f[6]) >> (r & 31) & 1u) && j < a.K - 1)
+                        latent_row_again<E4M3>(a, sw.n, row0 + r, sw.len - (a.K - 1 - j));
+                }
+                tc::named_sync(kBarSoft, Sh::kSoft);
+            }
+            sw.first = false;
+        }
+    } else if (warp == Sh::kMmaWarp) {
+        // ---- both products; whichever has its inputs goes first ----
+        if (lane == 0) {
+            const uint32_t id_s = tc::idesc(64, R, tc::kFmtBF16, false, false);
+            const uint32_t id_o = tc::idesc(128, R, tc::kFmtBF16, true, true);
+            const uint32_t uQ = tc::smem_u32(sQ), uC = tc::smem_u32(sC), uP = tc::smem_u32(sP);
+            SegWalk sv = sw;                                    // the O product's walk follows the S product's
+            bool more_s = sw.next(a.w), more_o = sv.next(a.w);
+            int gs = 0, go = 0, qs = 0;                         // S and O tiles issued, segments whose Q is in
+            int ts = sw.t0, to = sv.t0;
+            uint64_t since = 0;
+            uint32_t idle = 0;
+            while (more_o) {
+                bool moved = false;
+                // S of a tile: at most one ahead of O (its S buffer is read before P is written)
+                if (more_s && gs <= go + 1 && (ts > sw.t0 || tc::mbar_test_wait(q_full, qs & 1)) &&
+                    tc::mbar_test_wait(&full[gs & 1], (gs >> 1) & 1)) {
+                    tc::fence_after_sync();
+                    const uint32_t c = uC + (gs & 1) * Sh::kStage;
+#pragma unroll 4
+                    for (uint32_t k = 0; k < 36; ++k) {
+                        const uint32_t sl = k >> 2, in = (k & 3) * 32u;
+                        tc::mma_f16(tmS + (gs & 1) * R, tc::sdesc(c + sl * Sh::kSlabC + in, 16, 1024, tc::kSwizzle128B),
+                                    tc::sdesc(uQ + sl * Sh::kSlabQ + in, 16, 1024, tc::kSwizzle128B), id_s, k > 0);
+                    }
+                    tc::mma_commit(&s_full[gs & 1]);
+                    ++gs;
+                    if (++ts == sw.t1) {
+                        ++qs;
+                        more_s = sw.next(a.w);
+                        ts = sw.t0;
+                    }
+                    moved = true;
+                }
+                if (go < gs && tc::mbar_test_wait(p_full, go & 1)) {
+                    tc::fence_after_sync();
+                    const uint32_t c = uC + (go & 1) * Sh::kStage;
+#pragma unroll 1
+                    for (uint32_t b = 0; b < 4; ++b)
+#pragma unroll
+                        for (uint32_t k = 0; k < 4; ++k)
+                            tc::mma_f16(tmO + b * R, tc::sdesc(c + b * 2u * Sh::kSlabC + k * 2048u, Sh::kSlabC, 1024, tc::kSwizzle128B),
+                                        tc::sdesc(uP + k * 2048u, kTile * 128u, 1024, tc::kSwizzle128B), id_o,
+                                        to > sv.t0 || k > 0);
+                    tc::mma_commit(&empty[go & 1]);
+                    ++go;
+                    if (++to == sv.t1) {
+                        more_o = sv.next(a.w);
+                        to = sv.t0;
+                    }
+                    moved = true;
+                }
+                if (moved) {
+                    idle = 0;
+                } else if ((++idle & 255u) == 0) {              // the clock is read every 256 idle rounds
+                    const uint64_t now = tc::globaltimer_ns();
+                    if (idle == 256u) since = now;
+                    else if (now - since > kWaitLimitNs) { ok = false; break; }
+                }
+            }
+            // nothing of this CTA's is left running when it returns its TMEM
+            if (gs > 0 && !tc::mbar_wait_bounded(&s_full[(gs - 1) & 1], ((gs - 1) >> 1) & 1, kWaitLimitNs)) ok = false;
+            if (go > 0 && !tc::mbar_wait_bounded(&empty[(go - 1) & 1], ((go - 1) >> 1) & 1, kWaitLimitNs)) ok = false;
+        }
+        __syncwarp();
+    } else if constexpr (!E4M3) {
+        // ---- TMA: Q of each segment, C tiles in boxes of `box` rows (one page or a part of one) ----
+        const int nbox = kTile / a.box;
+        int g = 0, seg = 0;
+        while (ok && sw.next(a.w)) {
+            auto pages = [&](int t) {                           // lane i: first cache row of box i of tile t, -1 = past the end
+                const int tok = t * kTile + lane * a.box;
+                if (t >= sw.t1 || lane >= nbox || tok >= sw.len) return -1;
+                int page = a.ch.table[static_cast<size_t>(sw.n) * a.ch.max_pages + tok / a.ch.page_size];
+                if (page < 0 || page >= a.ch.num_pages) { set_status(a.status, kStatusIndex); page = 0; }
+                return page * a.ch.page_size + tok % a.ch.page_size;
+            };
+            int at = pages(sw.t0);
+            // Q is free once the last S product of the segment before has run
+            if (g > 0) ok = tc::mbar_wait_bounded(&s_full[(g - 1) & 1], ((g - 1) >> 1) & 1, kWaitLimitNs);
+            ok = __all_sync(0xffffffffu, ok);
+            if (!ok) break;
+            if (lane == 0) {
+                tc::mbar_arrive_expect_tx(q_full, 9u * Sh::kSlabQ);
+                const int qrow = static_cast<int>(static_cast<long long>(sw.n) * a.rows + row0);
+                for (int s = 0; s < 9; ++s)
+                    tc::tma_load_2d(tc::smem_u32(sQ) + s * Sh::kSlabQ, &maps.q, 64 * s, qrow, q_full);
+            }
+            ++seg;
+            for (int t = sw.t0; t < sw.t1; ++t, ++g) {
+                const int next = pages(t + 1);
+                if (g >= 2) ok = tc::mbar_wait_bounded(&empty[g & 1], ((g - 2) >> 1) & 1, kWaitLimitNs);
+                ok = __all_sync(0xffffffffu, ok);
+                if (!ok) break;
+                const int boxes = __popc(__ballot_sync(0xffffffffu, at >= 0));
+                const uint32_t dst = tc::smem_u32(sC) + (g & 1) * Sh::kStage;
+                // rows that softmax threads zeroed are overwritten by the copy: order the two
+                tc::fence_smem_to_async();
+                if (lane == 0) tc::mbar_arrive_expect_tx(&full[g & 1], static_cast<uint32_t>(boxes * a.box) * 9u * 128u);
+                __syncwarp();
+                for (int b = 0; b < boxes; ++b) {
+                    const int row = __shfl_sync(0xffffffffu, at, b);
+                    if (lane < 9)
+                        tc::tma_load_2d(dst + lane * Sh::kSlabC + b * a.box * 128, &maps.c, 64 * lane, row, &full[g & 1]);
+                }
+                at = next;
+            }
+        }
+        // copies in flight land before the CTA's shared memory is given back
+        if (!ok) {
+            if (seg > 0) tc::mbar_wait_bounded(q_full, (seg - 1) & 1, kWaitLimitNs);
+            for (int i = max(0, g - 2); i < g; ++i) tc::mbar_wait_bounded(&full[i & 1], (i >> 1) & 1, kWaitLimitNs);
+        }
+    } else {
+        // ---- e4m3: 8 warps load 8 tokens each, expand to bf16 (exact) and store the swizzled tile ----
+        const int pw = warp - 5;
+        const int sl = lane >> 2, half = sl & 1;
+        int g = 0, seg = 0;
+        while (ok && sw.next(a.w)) {
+            if (g > 0) ok = tc::mbar_wait_bounded(&s_full[(g - 1) & 1], ((g - 1) >> 1) & 1, kWaitLimitNs);
+            ok = __all_sync(0xffffffffu, ok);
+            if (!ok) break;
+            if (pw == 0 && lane == 0) {
+                tc::mbar_arrive_expect_tx(q_full, 9u * Sh::kSlabQ);
+                const int qrow = static_cast<int>(static_cast<long long>(sw.n) * a.rows + row0);
+                for (int s = 0; s < 9; ++s)
+                    tc::tma_load_2d(tc::smem_u32(sQ) + s * Sh::kSlabQ, &maps.q, 64 * s, qrow, q_full);
+            }
+            auto locate = [&](int t) {                          // lane i < 8: cache row of token 8 pw + i of tile t
+                const int tok = t * kTile + 8 * pw + lane;
+                if (t >= sw.t1 || lane >= 8 || tok >= sw.len) return -1;
+                const int page = a.ch.table[static_cast<size_t>(sw.n) * a.ch.max_pages + tok / a.ch.page_size];
+                if (page < 0 || page >= a.ch.num_pages) { set_status(a.status, kStatusIndex); return -1; }
+                return page * a.ch.page_size + tok % a.ch.page_size;
+            };
+            uint4 code[8], rope[2];
+            float scale = 0.f;
+            auto fetch = [&](int at) {
+                scale = at >= 0 ? *reinterpret_cast<const float*>(a.ch.rows + static_cast<size_t>(at) * kLatRowE4m3 + kLatScaleAt) : 0.f;
+#pragma unroll
+                for (int i = 0; i < 8; ++i) {
+                    const int r = __shfl_sync(0xffffffffu, at, i);
+                    code[i] = r >= 0 ? __ldg(reinterpret_cast<const uint4*>(a.ch.rows + static_cast<size_t>(r) * kLatRowE4m3) + lane)
+                                     : make_uint4(0, 0, 0, 0);
+                }
+#pragma unroll
+                for (int i = 0; i < 2; ++i) {                   // 4 tokens x 8 chunks of 16 bytes
+                    const int r = __shfl_sync(0xffffffffu, at, 4 * i + (lane >> 3));
+                    rope[i] = r >= 0 ? __ldg(reinterpret_cast<const uint4*>(a.ch.rows + static_cast<size_t>(r) * kLatRowE4m3 + kLatDim) + (lane & 7))
+                                     : make_uint4(0, 0, 0, 0);
+                }
+            };
+            int at = locate(sw.t0);
+            fetch(at);
+            at = locate(sw.t0 + 1);
+            for (int t = sw.t0; t < sw.t1; ++t, ++g) {
+                if (g >= 2) ok = tc::mbar_wait_bounded(&empty[g & 1], ((g - 2) >> 1) & 1, kWaitLimitNs);
+                ok = __all_sync(0xffffffffu, ok);
+                if (!ok) break;
+                uint8_t* c = sC + (g & 1) * Sh::kStage;
+#pragma unroll
+                for (int i = 0; i < 8; ++i) {
+                    const float s = __shfl_sync(0xffffffffu, scale, i);
+                    const uint32_t w[4] = {code[i].x, code[i].y, code[i].z, code[i].w};
+                    uint32_t v[8];
+#pragma unroll
+                    for (int k = 0; k < 4; ++k) {
+                        const float2 f = e4m3x2_to_f32(w[k]), h = e4m3x2_to_f32(w[k] >> 16);
+                        v[2 * k] = f32x2_to_bf16x2_bits(f.x * s, f.y * s);
+                        v[2 * k + 1] = f32x2_to_bf16x2_bits(h.x * s, h.y * s);
+                    }
+                    const uint4 lo = make_uint4(v[0], v[1], v[2], v[3]), hi = make_uint4(v[4], v[5], v[6], v[7]);
+                    // lane: chunks 2 (lane % 4) and + 1 of slab lane / 4; odd slabs store theirs in the
+                    // other order so that 8 lanes cover all banks
+                    const uint32_t row = 8 * pw + i, cb = 2 * (lane & 3);
+                    uint8_t* d = c + sl * Sh::kSlabC + row * 128;
+                    *reinterpret_cast<uint4*>(d + (((cb + half) ^ i) << 4)) = half ? hi : lo;
+                    *reinterpret_cast<uint4*>(d + (((cb + 1 - half) ^ i) << 4)) = half ? lo : hi;
+                }
+#pragma unroll
+                for (int i = 0; i < 2; ++i) {
+                    const uint32_t r = 4 * i + (lane >> 3);
+                    *reinterpret_cast<uint4*>(c + 8 * Sh::kSlabC + (8 * pw + r) * 128 + (((lane & 7) ^ r) << 4)) = rope[i];
+                }
+                tc::fence_smem_to_async();
+                __syncwarp();
+                if (lane == 0) tc::mbar_arrive(&full[g & 1]);
+                if (t + 1 < sw.t1) {
+                    fetch(at);
+                    at = locate(t + 2);
+                }
+            }
+            ++seg;
+        }
+        if (!ok && pw == 0 && seg > 0) tc::mbar_wait_bounded(q_full, (seg - 1) & 1, kWaitLimitNs);
+    }
+    if (!ok) set_status(a.status, kStatusTimeout);
+    __syncwarp();
+    tc::fence_before_sync();
+    __syncthreads();
+    tc::fence_after_sync();
+    if (warp == Sh::kMmaWarp) tc::tmem_dealloc(tm, Sh::kTmemCols);
+}
+
+// Joins the partials of sequences that several CTAs worked on, and writes empty sequences.  One
+// block per (sequence, row): 4 groups of 128 threads take every fourth partial, 4 channels a
+// thread.
+template <int R, bool E4M3>
+__global__ void __launch_bounds__(512)
+kda_latent_combine_kernel(const LatArgs a)
+{
+    __shared__ long long s_sum[2][16];
+    __shared__ float4 s_acc[3][128];
+    __shared__ int s_bad;
+    const int n = blockIdx.x / a.rows, row = blockIdx.x % a.rows;
+    const int tid = threadIdx.x, grp = tid >> 7, ch = (tid & 127) * 4;
+    long long before = 0, T = 0;
+    for (int i = tid; i < a.w.N; i += 512) {
+        const int raw = a.w.seq_lens[i];
+        const int tiles = lat_tiles(lat_len(a.w, i));
+        if (i == n && row == 0 && (raw < 0 || raw > a.w.max_len)) set_status(a.status, kStatusIndex);
+        T += tiles;
+        if (i < n) before += tiles;
+    }
+#pragma unroll
+    for (int off = 16; off > 0; off >>= 1) {
+        T += __shfl_xor_sync(0xffffffffu, T, off);
+        before += __shfl_xor_sync(0xffffffffu, before, off);
+    }
+    if ((tid & 31) == 0) { s_sum[0][tid >> 5] = T; s_sum[1][tid >> 5] = before; }
+    if (tid == 0) s_bad = 0;
+    __syncthreads();
+    T = before = 0;
+    for (int i = 0; i < 16; ++i) { T += s_sum[0][i]; before += s_sum[1][i]; }
+    const int len = lat_len(a.w, n), tiles = lat_tiles(len);
+    const long long at = static_cast<long long>(n) * a.rows + row;
+    asm volatile("griddepcontrol.wait;" ::: "memory");          // every block: this grid ends after the one before it
+    if (tiles == 0) {
+        if (grp == 0) *reinterpret_cast<uint2*>(a.out + at * kLatDim + ch) = make_uint2(0u, 0u);
+        if (tid == 0 && a.lse) a.lse[at] = -INFINITY;
+        return;
+    }
+    const long long runs = lat_runs(T, a.w.G);
+    const long long c0 = run_of(T, runs, before), c1 = run_of(T, runs, before + tiles - 1);
+    if (c0 == c1) return;                                        // its CTA finished it
+    const int rt = row / R, r = row % R;
+    // run c's partial: its first segment, unless it began with an earlier sequence's tiles
+    auto slot = [&](long long c) {
+        const int second = c == c0 && run_begin(T, runs, c) < before ? 1 : 0;
+        return ((static_cast<size_t>(c) * a.RT + rt) * 2 + second) * R + r;
+    };
+    float M = -INFINITY;
+    for (long long c = c0; c <= c1; ++c) M = fmaxf(M, a.part_ml[slot(c) * 2]);
+    float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+    float L = 0.f;
+    for (long long c = c0; c <= c1; ++c) {
+        const float2 ml = *reinterpret_cast<const float2*>(a.part_ml + slot(c) * 2);
+        if (ml.x == -INFINITY && ml.y == 0.f) continue;          // saw nothing there
+        const float f = ml.x == M ? 1.f : lat_ex2(ml.x - M);
+        L += f * ml.y;
+        if (((c - c0) & 3) == grp) {
+            const float4 o = *reinterpret_cast<const float4*>(a.part_o + slot(c) * kLatDim + ch);
+            acc.x += f * o.x; acc.y += f * o.y; acc.z += f * o.z; acc.w += f * o.w;
+        }
+    }
+    if (grp > 0) s_acc[grp - 1][tid & 127] = acc;
+    __syncthreads();
+    if (grp == 0) {
+#pragma unroll
+        for (int i = 0; i < 3; ++i) {
+            const float4 o = s_acc[i][tid];
+            acc.x += o.x; acc.y += o.y; acc.z += o.z; acc.w += o.w;
+        }
+        const float inv = L == 0.f ? 0.f : 1.f / L;
+        const float v[4] = {acc.x * inv, acc.y * inv, acc.z * inv, acc.w * inv};
+        if (!(fabsf(v[0]) < INFINITY && fabsf(v[1]) < INFINITY && fabsf(v[2]) < INFINITY && fabsf(v[3]) < INFINITY)) s_bad = 1;
+        *reinterpret_cast<uint2*>(a.out + at * kLatDim + ch) = make_uint2(f32x2_to_bf16x2_bits(v[0], v[1]),
+                                                                          f32x2_to_bf16x2_bits(v[2], v[3]));
+        if (tid == 0 && a.lse) a.lse[at] = (M + log2f(L)) * 0.69314718055994531f;
+    }
+    __syncthreads();
+    const int j = row / a.H;
+    if (s_bad && j < a.K - 1 && tid < 32) latent_row_again<E4M3>(a, n, row, len - (a.K - 1 - j));
+}
+
+namespace {
+using EncodeTiledFn = CUresult (*)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*, const cuuint64_t*,
+                                   const cuuint64_t*, const cuuint32_t*, const cuuint32_t*, CUtensorMapInterleave,
+                                   CUtensorMapSwizzle, CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
+EncodeTiledFn encode_fn() {
+    static EncodeTiledFn fn = nullptr;
+    if (!fn) {
+        void* ptr = nullptr;
+        cudaDriverEntryPointQueryResult qr;
+        if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &ptr, 12000, cudaEnableDefault, &qr) == cudaSuccess &&
+            qr == cudaDriverEntryPointSuccess)
+            fn = reinterpret_cast<EncodeTiledFn>(ptr);
+    }
+    return fn;
+}
+// [rows, 576] bf16, boxes of 64 columns x box_rows rows, 128-byte swizzle, zeros past the end
+bool map_576(CUtensorMap* m, const void* base, long long rows, int box_rows) {
+    EncodeTiledFn fn = encode_fn();
+    if (!fn) return false;
+    const cuuint64_t dims[2] = {static_cast<cuuint64_t>(kLatQ), static_cast<cuuint64_t>(rows)};
+    const cuuint64_t strides[1] = {static_cast<cuuint64_t>(kLatQ) * 2};
+    const cuuint32_t box[2] = {64u, static_cast<cuuint32_t>(box_rows)};
+    const cuuint32_t estr[2] = {1u, 1u};
+    return fn(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, const_cast<void*>(base), dims, strides, box, estr,
+              CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+              CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+int sm_count() {
+    static int count[kMaxDevicesAttr] = {};
+    int dev = 0;
+    if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= kMaxDevicesAttr) return 0;
+    if (!count[dev] && cudaDeviceGetAttribute(&count[dev], cudaDevAttrMultiProcessorCount, dev) != cudaSuccess) return 0;
+    return count[dev];
+}
+
+template <int R, bool E4M3>
+int launch_decode_shape(const LatMaps& maps, const LatArgs& a, cudaStream_t stream) {
+    using Sh = LatShape<R, E4M3>;
+    static bool attr_done[kMaxDevicesAttr] = {};
+    if (!raise_smem_limit(reinterpret_cast<const void*>(kda_latent_decode_kernel<R, E4M3>), static_cast<int>(Sh::kBytes), attr_done))
+        return -3;
+    kda_latent_decode_kernel<R, E4M3><<<static_cast<unsigned>(a.w.G) * a.RT, Sh::kThreads, Sh::kBytes, stream>>>(maps, a);
+    if (cudaGetLastError() != cudaSuccess) return -3;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(static_cast<unsigned>(a.w.N) * a.rows);
+    cfg.blockDim = dim3(512);
+    cfg.stream = stream;
+    cudaLaunchAttribute at[1];
+    at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    at[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = at;
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(&cfg, kda_latent_combine_kernel<R, E4M3>, a) == cudaSuccess ? 0 : -3;
+}
+
+// Rows a CTA takes: 16, 32 or 64.
+int rows_per_cta(int rows) { return rows <= 16 ? 16 : rows <= 32 ? 32 : 64; }
+}  // namespace
+
+// Runs of tiles (times row tiles: one CTA per SM) and the scratch bytes of their partials.
+int latent_decode_runs(int rows) {
+    const int R = rows_per_cta(rows), RT = (rows + R - 1) / R, sms = sm_count();
+    return sms / RT > 0 ? sms / RT : (sms > 0 ? 1 : 0);
+}
+size_t latent_decode_scratch(int rows) {
+    const size_t R = rows_per_cta(rows), RT = (rows + R - 1) / R;
+    return static_cast<size_t>(latent_decode_runs(rows)) * RT * 2 * R * (kLatDim + 2) * sizeof(float);
 }
 
 int launch_latent_decode(const uint16_t* q, const void* cache, int e4m3, int num_pages, int page_size,
                          const int32_t* table, int max_pages, const int32_t* seq_lens, int N, int K, int H,
-                         float sm_scale, uint16_t* out, float* lse, int* status, cudaStream_t stream)
+                         float sm_scale, uint16_t* out, float* lse, void* scratch, int* status, cudaStream_t stream)
 {
-    const long long rows = static_cast<long long>(N) * K * H;
-    const LatentCache ch{static_cast<const uint8_t*>(cache), table, num_pages, page_size, max_pages};
-    const float sl2 = sm_scale * 1.4426950408889634f;
-    const unsigned blocks = static_cast<unsigned>((rows + 3) / 4);
-    if (e4m3) kda_latent_rows_kernel<true><<<blocks, 128, 0, stream>>>(q, ch, seq_lens, K, H, rows, sl2, out, lse, status);
-    else kda_latent_rows_kernel<false><<<blocks, 128, 0, stream>>>(q, ch, seq_lens, K, H, rows, sl2, out, lse, status);
-    return cudaGetLastError() == cudaSuccess ? 0 : -3;
+    LatArgs a = {};
+    const int rows = K * H, R = rows_per_cta(rows);
+    a.w = LatWork{seq_lens, N, latent_decode_runs(rows), static_cast<long long>(max_pages) * page_size};
+    if (a.w.G <= 0) return -3;
+    a.ch = LatentCache{static_cast<const uint8_t*>(cache), table, num_pages, page_size, max_pages};
+    a.q = q;
+    a.K = K;
+    a.H = H;
+    a.rows = rows;
+    a.RT = (rows + R - 1) / R;
+    a.box = page_size % 64 == 0 ? 64 : page_size % 32 == 0 ? 32 : 16;
+    a.scale_log2 = sm_scale * 1.4426950408889634f;
+    a.out = out;
+    a.lse = lse;
+    a.part_o = static_cast<float*>(scratch);
+    a.part_ml = a.part_o + static_cast<size_t>(a.w.G) * a.RT * 2 * R * kLatDim;
+    a.status = status;
+    LatMaps maps;
+    if (!map_576(&maps.q, q, static_cast<long long>(N) * rows, R)) return -3;
+    // (an empty cache holds no token to read; the map then only has to be valid)
+    if (num_pages == 0) a.w.max_len = 0;
+    if (e4m3 || num_pages == 0) maps.c = maps.q;
+    else if (!map_576(&maps.c, cache, static_cast<long long>(num_pages) * page_size, a.box)) return -3;
+    if (e4m3) return R == 16 ? launch_decode_shape<16, true>(maps, a, stream)
+                   : R == 32 ? launch_decode_shape<32, true>(maps, a, stream) : launch_decode_shape<64, true>(maps, a, stream);
+    return R == 16 ? launch_decode_shape<16, false>(maps, a, stream)
+         : R == 32 ? launch_decode_shape<32, false>(maps, a, stream) : launch_decode_shape<64, false>(maps, a, stream);
 }
 
 }  // namespace kda
