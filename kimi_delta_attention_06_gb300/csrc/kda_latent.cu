@@ -132,9 +132,12 @@ __device__ __forceinline__ long long lat_runs(long long T, int G) {
     const long long r = (T + kMinTiles - 1) / kMinTiles;
     return r < G ? r : G;
 }
-__device__ __forceinline__ long long run_begin(long long T, long long runs, long long c) { return c * T / runs; }
+__device__ __forceinline__ long long run_div(long long x, long long y) {      // x / y of non-negative numbers
+    return x >> 32 ? x / y : static_cast<long long>(static_cast<uint32_t>(x) / static_cast<uint32_t>(y));
+}
+__device__ __forceinline__ long long run_begin(long long T, long long runs, long long c) { return run_div(c * T, runs); }
 // The run that holds tile t: the largest c with c T / runs (rounded down) <= t.
-__device__ __forceinline__ long long run_of(long long T, long long runs, long long t) { return ((t + 1) * runs - 1) / T; }
+__device__ __forceinline__ long long run_of(long long T, long long runs, long long t) { return run_div((t + 1) * runs - 1, T); }
 
 // Walks the segments of one run; every warp keeps its own copy (init is warp-collective).
 struct SegWalk {
@@ -219,7 +222,7 @@ struct LatShape {
     static constexpr uint32_t kSlabQ = R * 128u, kSlabC = kTile * 128u;
     static constexpr uint32_t kStage = 9u * kSlabC;
     static constexpr uint32_t oQ = 0, oC = 9u * kSlabQ, oP = oC + 2u * kStage, oBar = oP + kTile * 128u;
-    static constexpr uint32_t kBytes = oBar + 64u + 4u + 5u * R * 4u + 64u;
+    static constexpr uint32_t kBytes = oBar + 80u + 6u * R * 4u;
     static constexpr uint32_t kTmemCols = R == 16 ? 128u : R == 32 ? 256u : 512u;     // 4 R (O) + 2 R (S)
 };
 // shared memory: 9 slabs of Q | 2 stages of 9 slabs of C | P | barriers, exchange
@@ -274,6 +277,7 @@ kda_latent_decode_kernel(const __grid_constant__ LatMaps maps, const LatArgs a)
     uint32_t* s_tmem = reinterpret_cast<uint32_t*>(bars + 8);
     float* s_red = reinterpret_cast<float*>(bars + 8) + 4;      // [4][R]
     float* s_f = s_red + 4 * R;                                 // [R]
+    int* s_j = reinterpret_cast<int*>(s_f + R);                 // [R]: query token of each row
 
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const int rt = blockIdx.x % a.RT, run = blockIdx.x / a.RT;
@@ -289,10 +293,12 @@ kda_latent_decode_kernel(const __grid_constant__ LatMaps maps, const LatArgs a)
         tc::mbar_init(q_full, 1);
         tc::mbar_fence_init();
     }
+    if (tid < R) s_j[tid] = min((row0 + tid) / a.H, a.K - 1);
     if (warp == Sh::kMmaWarp) tc::tmem_alloc(s_tmem, Sh::kTmemCols);
     tc::fence_before_sync();
     __syncthreads();
     tc::fence_after_sync();
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");   // the combine kernel waits for this grid's end
     const uint32_t tm = *s_tmem, tmO = tm, tmS = tm + 4 * R;
     SegWalk sw;
     sw.init(a.w, run);
@@ -320,8 +326,7 @@ kda_latent_decode_kernel(const __grid_constant__ LatMaps maps, const LatArgs a)
                 if (edge) {
 #pragma unroll
                     for (int i = 0; i < R / 2; ++i) {
-                        const int row = row0 + 8 * (i >> 2) + rq + (i & 1);
-                        const int see = clear + min(row / a.H, a.K - 1);
+                        const int see = clear + s_j[8 * (i >> 2) + rq + (i & 1)];
                         x[i] = tok + 4 * (i & 2) < see ? x[i] * a.scale_log2 : -INFINITY;
                     }
                     // rows past the end of the sequence hold anything: they enter the second product as zeros
@@ -436,27 +441,43 @@ kda_latent_decode_kernel(const __grid_constant__ LatMaps maps, const LatArgs a)
             }
             tc::named_sync(kBarSoft, Sh::kSoft);
             uint32_t bad[2] = {0u, 0u};                          // rows with a result that is no number
+            const int ch = 32 * warp + lane;
+            // two rows a store: the even lane of a pair takes both channels of the first, the odd of the second
+            const int odd = lane & 1;
+            uint16_t* d16 = a.out + (row_at + odd) * kLatDim + (ch - odd);
+            float* d32 = a.part_o + part * R * kLatDim + ch;
 #pragma unroll 1
             for (int c0 = 0; c0 < R; c0 += 16) {
+                if (c0 >= nrows) break;
 #pragma unroll 1
-                for (int b = 0; b < 4; ++b) {
-                    float o[16];
-                    tc::tmem_ld16(tmO + b * R + c0 + lane_tm, o);
+                for (int b2 = 0; b2 < 4; b2 += 2) {
+                    float o[2][16];
+                    tc::tmem_ld16(tmO + b2 * R + c0 + lane_tm, o[0]);
+                    tc::tmem_ld16(tmO + (b2 + 1) * R + c0 + lane_tm, o[1]);
                     tc::tmem_wait_ld();
-                    const int ch = 128 * b + 32 * warp + lane;
                     if (whole) {
 #pragma unroll
-                        for (int i = 0; i < 16; ++i)
-                            if (c0 + i < nrows) {
-                                const float v = s_f[c0 + i] == 0.f ? 0.f : o[i] * s_f[c0 + i];
-                                if (!(fabsf(v) < INFINITY)) bad[c0 >> 5] |= 1u << ((c0 + i) & 31);
-                                a.out[(row_at + c0 + i) * kLatDim + ch] = f32_to_bf16_bits(v);
-                            }
-                    } else {
-                        float* d = a.part_o + (part * R + c0) * kLatDim + ch;
+                        for (int i = 0; i < 16; i += 2) {
+                            const float f0 = s_f[c0 + i], f1 = s_f[c0 + i + 1];
 #pragma unroll
-                        for (int i = 0; i < 16; ++i)
-                            if (c0 + i < nrows) d[static_cast<size_t>(i) * kLatDim] = o[i];
+                            for (int b = 0; b < 2; ++b) {
+                                const float v0 = f0 == 0.f ? 0.f : o[b][i] * f0, v1 = f1 == 0.f ? 0.f : o[b][i + 1] * f1;
+                                if (!(fabsf(v0) < INFINITY)) bad[c0 >> 5] |= 1u << ((c0 + i) & 31);
+                                if (!(fabsf(v1) < INFINITY)) bad[c0 >> 5] |= 1u << ((c0 + i + 1) & 31);
+                                const float got = __shfl_xor_sync(0xffffffffu, odd ? v0 : v1, 1);
+                                const uint32_t w = odd ? f32x2_to_bf16x2_bits(got, v1) : f32x2_to_bf16x2_bits(v0, got);
+                                if (c0 + i + odd < nrows)
+                                    *reinterpret_cast<uint32_t*>(d16 + (c0 + i) * kLatDim + (b2 + b) * 128) = w;
+                            }
+                        }
+                    } else {
+#pragma unroll
+                        for (int i = 0; i < 16; ++i) {
+                            if (c0 + i < nrows) {
+                                d32[(c0 + i) * kLatDim + b2 * 128] = o[0][i];
+                                d32[(c0 + i) * kLatDim + b2 * 128 + 128] = o[1][i];
+                            }
+                        }
                     }
                 }
             }
@@ -480,68 +501,78 @@ kda_latent_decode_kernel(const __grid_constant__ LatMaps maps, const LatArgs a)
         }
     } else if (warp == Sh::kMmaWarp) {
         // ---- both products; whichever has its inputs goes first ----
-        if (lane == 0) {
-            const uint32_t id_s = tc::idesc(64, R, tc::kFmtBF16, false, false);
-            const uint32_t id_o = tc::idesc(128, R, tc::kFmtBF16, true, true);
-            const uint32_t uQ = tc::smem_u32(sQ), uC = tc::smem_u32(sC), uP = tc::smem_u32(sP);
-            SegWalk sv = sw;                                    // the O product's walk follows the S product's
-            bool more_s = sw.next(a.w), more_o = sv.next(a.w);
-            int gs = 0, go = 0, qs = 0;                         // S and O tiles issued, segments whose Q is in
-            int ts = sw.t0, to = sv.t0;
-            uint64_t since = 0;
-            uint32_t idle = 0;
-            while (more_o) {
-                bool moved = false;
-                // S of a tile: at most one ahead of O (its S buffer is read before P is written)
-                if (more_s && gs <= go + 1 && (ts > sw.t0 || tc::mbar_test_wait(q_full, qs & 1)) &&
-                    tc::mbar_test_wait(&full[gs & 1], (gs >> 1) & 1)) {
-                    tc::fence_after_sync();
-                    const uint32_t c = uC + (gs & 1) * Sh::kStage;
-#pragma unroll 4
-                    for (uint32_t k = 0; k < 36; ++k) {
-                        const uint32_t sl = k >> 2, in = (k & 3) * 32u;
-                        tc::mma_f16(tmS + (gs & 1) * R, tc::sdesc(c + sl * Sh::kSlabC + in, 16, 1024, tc::kSwizzle128B),
-                                    tc::sdesc(uQ + sl * Sh::kSlabQ + in, 16, 1024, tc::kSwizzle128B), id_s, k > 0);
-                    }
-                    tc::mma_commit(&s_full[gs & 1]);
-                    ++gs;
-                    if (++ts == sw.t1) {
-                        ++qs;
-                        more_s = sw.next(a.w);
-                        ts = sw.t0;
-                    }
-                    moved = true;
-                }
-                if (go < gs && tc::mbar_test_wait(p_full, go & 1)) {
-                    tc::fence_after_sync();
-                    const uint32_t c = uC + (go & 1) * Sh::kStage;
-#pragma unroll 1
+        // (the warp runs as one, so that addresses stay in uniform registers; one elected lane issues)
+        constexpr uint32_t id_s = tc::idesc(64, R, tc::kFmtBF16, false, false);
+        constexpr uint32_t id_o = tc::idesc(128, R, tc::kFmtBF16, true, true);
+        // descriptors: constant high words, low words = address / 16 and the leading offset
+        const uint64_t d0 = tc::sdesc(0, 16, 1024, tc::kSwizzle128B), dC = tc::sdesc(0, Sh::kSlabC, 1024, tc::kSwizzle128B);
+        const uint32_t hi = static_cast<uint32_t>(d0 >> 32);
+        const uint32_t q_lo = static_cast<uint32_t>(d0) | (tc::smem_u32(sQ) >> 4);
+        const uint32_t c_lo = static_cast<uint32_t>(d0) | (tc::smem_u32(sC) >> 4);
+        const uint32_t ct_lo = static_cast<uint32_t>(dC) | (tc::smem_u32(sC) >> 4);
+        const uint32_t p_lo = static_cast<uint32_t>(dC) | (tc::smem_u32(sP) >> 4);
+        SegWalk sv = sw;                                        // the O product's walk follows the S product's
+        bool more_s = sw.next(a.w), more_o = sv.next(a.w);
+        int gs = 0, go = 0, qs = 0;                             // S and O tiles issued, segments whose Q is in
+        int ts = sw.t0, to = sv.t0;
+        uint64_t since = 0;
+        uint32_t idle = 0;
+        while (more_o) {
+            bool moved = false;
+            // O of a tile before S of the next but one; S at most one tile ahead of O (its S buffer is
+            // read before P is written)
+            if (go < gs && __all_sync(0xffffffffu, tc::mbar_test_wait(p_full, go & 1))) {
+                tc::fence_after_sync();
+                const uint32_t c = ct_lo + (go & 1) * (Sh::kStage >> 4);
+                const uint32_t acc = to > sv.t0 ? 1u : 0u;
+                if (tc::elect_one()) {
+#pragma unroll
                     for (uint32_t b = 0; b < 4; ++b)
 #pragma unroll
                         for (uint32_t k = 0; k < 4; ++k)
-                            tc::mma_f16(tmO + b * R, tc::sdesc(c + b * 2u * Sh::kSlabC + k * 2048u, Sh::kSlabC, 1024, tc::kSwizzle128B),
-                                        tc::sdesc(uP + k * 2048u, kTile * 128u, 1024, tc::kSwizzle128B), id_o,
-                                        to > sv.t0 || k > 0);
+                            tc::mma_f16_lo(tmO + b * R, c + ((b * 2u * Sh::kSlabC + k * 2048u) >> 4), hi,
+                                           p_lo + (k * 2048u >> 4), hi, id_o, k > 0 ? 1u : acc);
                     tc::mma_commit(&empty[go & 1]);
-                    ++go;
-                    if (++to == sv.t1) {
-                        more_o = sv.next(a.w);
-                        to = sv.t0;
-                    }
-                    moved = true;
                 }
-                if (moved) {
-                    idle = 0;
-                } else if ((++idle & 255u) == 0) {              // the clock is read every 256 idle rounds
-                    const uint64_t now = tc::globaltimer_ns();
-                    if (idle == 256u) since = now;
-                    else if (now - since > kWaitLimitNs) { ok = false; break; }
+                __syncwarp();
+                ++go;
+                if (++to == sv.t1) {
+                    more_o = sv.next(a.w);
+                    to = sv.t0;
                 }
+                moved = true;
             }
-            // nothing of this CTA's is left running when it returns its TMEM
-            if (gs > 0 && !tc::mbar_wait_bounded(&s_full[(gs - 1) & 1], ((gs - 1) >> 1) & 1, kWaitLimitNs)) ok = false;
-            if (go > 0 && !tc::mbar_wait_bounded(&empty[(go - 1) & 1], ((go - 1) >> 1) & 1, kWaitLimitNs)) ok = false;
+            if (more_s && gs <= go + 1 && (ts > sw.t0 || __all_sync(0xffffffffu, tc::mbar_test_wait(q_full, qs & 1))) &&
+                __all_sync(0xffffffffu, tc::mbar_test_wait(&full[gs & 1], (gs >> 1) & 1))) {
+                tc::fence_after_sync();
+                const uint32_t c = c_lo + (gs & 1) * (Sh::kStage >> 4), d = tmS + (gs & 1) * R;
+                if (tc::elect_one()) {
+#pragma unroll
+                    for (uint32_t k = 0; k < 36; ++k)
+                        tc::mma_f16_lo(d, c + (((k >> 2) * Sh::kSlabC + (k & 3) * 32u) >> 4), hi,
+                                       q_lo + (((k >> 2) * Sh::kSlabQ + (k & 3) * 32u) >> 4), hi, id_s, k > 0 ? 1u : 0u);
+                    tc::mma_commit(&s_full[gs & 1]);
+                }
+                __syncwarp();
+                ++gs;
+                if (++ts == sw.t1) {
+                    ++qs;
+                    more_s = sw.next(a.w);
+                    ts = sw.t0;
+                }
+                moved = true;
+            }
+            if (moved) {
+                idle = 0;
+            } else if ((++idle & 255u) == 0) {                  // the clock is read every 256 idle rounds
+                const uint64_t now = tc::globaltimer_ns();
+                if (idle == 256u) since = now;
+                else if (__any_sync(0xffffffffu, now - since > kWaitLimitNs)) { ok = false; break; }
+            }
         }
+        // nothing of this CTA's is left running when it returns its TMEM
+        if (gs > 0 && !tc::mbar_wait_bounded(&s_full[(gs - 1) & 1], ((gs - 1) >> 1) & 1, kWaitLimitNs)) ok = false;
+        if (go > 0 && !tc::mbar_wait_bounded(&empty[(go - 1) & 1], ((go - 1) >> 1) & 1, kWaitLimitNs)) ok = false;
         __syncwarp();
     } else if constexpr (!E4M3) {
         // ---- TMA: Q of each segment, C tiles in boxes of `box` rows (one page or a part of one) ----
@@ -682,20 +713,25 @@ kda_latent_decode_kernel(const __grid_constant__ LatMaps maps, const LatArgs a)
     if (warp == Sh::kMmaWarp) tc::tmem_dealloc(tm, Sh::kTmemCols);
 }
 
-// Joins the partials of sequences that several CTAs worked on, and writes empty sequences.  One
-// block per (sequence, row): 4 groups of 128 threads take every fourth partial, 4 channels a
-// thread.
+// Joins the partials of sequences that several CTAs worked on, and writes empty sequences.  A block
+// takes one row (x 1 / Q of its channels when there are few rows): NG groups of 128 / Q threads, 4
+// channels a thread, group i every NG-th partial.
+constexpr int kMaxRuns = 1024;                  // partials of a row (at most one a run)
+
 template <int R, bool E4M3>
 __global__ void __launch_bounds__(512)
-kda_latent_combine_kernel(const LatArgs a)
+kda_latent_combine_kernel(const LatArgs a, int Q, int NG)
 {
     __shared__ long long s_sum[2][16];
-    __shared__ float4 s_acc[3][128];
-    __shared__ int s_bad;
-    const int n = blockIdx.x / a.rows, row = blockIdx.x % a.rows;
-    const int tid = threadIdx.x, grp = tid >> 7, ch = (tid & 127) * 4;
+    __shared__ float s_w[kMaxRuns];              // weight of each partial
+    __shared__ float4 s_acc[512];
+    __shared__ float s_ml[2][16];
+    const int lanes = 128 / Q, threads = lanes * NG;
+    const int unit = blockIdx.x / Q, n = unit / a.rows, row = unit % a.rows;
+    const int tid = threadIdx.x, grp = tid / lanes, ch = (blockIdx.x % Q * lanes + tid % lanes) * 4;
+    const int warps = threads >> 5;
     long long before = 0, T = 0;
-    for (int i = tid; i < a.w.N; i += 512) {
+    for (int i = tid; i < a.w.N; i += threads) {
         const int raw = a.w.seq_lens[i];
         const int tiles = lat_tiles(lat_len(a.w, i));
         if (i == n && row == 0 && (raw < 0 || raw > a.w.max_len)) set_status(a.status, kStatusIndex);
@@ -708,59 +744,84 @@ kda_latent_combine_kernel(const LatArgs a)
         before += __shfl_xor_sync(0xffffffffu, before, off);
     }
     if ((tid & 31) == 0) { s_sum[0][tid >> 5] = T; s_sum[1][tid >> 5] = before; }
-    if (tid == 0) s_bad = 0;
     __syncthreads();
     T = before = 0;
-    for (int i = 0; i < 16; ++i) { T += s_sum[0][i]; before += s_sum[1][i]; }
+    for (int i = 0; i < warps; ++i) { T += s_sum[0][i]; before += s_sum[1][i]; }
     const int len = lat_len(a.w, n), tiles = lat_tiles(len);
     const long long at = static_cast<long long>(n) * a.rows + row;
+    int c0 = 0, parts = 1, late = 0;
+    if (tiles > 0) {
+        const long long runs = lat_runs(T, a.w.G);
+        c0 = static_cast<int>(run_of(T, runs, before));
+        parts = static_cast<int>(run_of(T, runs, before + tiles - 1)) - c0 + 1;
+        // a run's partial is its first segment's, unless it began with an earlier sequence's tiles
+        late = run_begin(T, runs, c0) < before ? 1 : 0;
+    }
     asm volatile("griddepcontrol.wait;" ::: "memory");          // every block: this grid ends after the one before it
     if (tiles == 0) {
         if (grp == 0) *reinterpret_cast<uint2*>(a.out + at * kLatDim + ch) = make_uint2(0u, 0u);
-        if (tid == 0 && a.lse) a.lse[at] = -INFINITY;
+        if (tid == 0 && ch == 0 && a.lse) a.lse[at] = -INFINITY;
         return;
     }
-    const long long runs = lat_runs(T, a.w.G);
-    const long long c0 = run_of(T, runs, before), c1 = run_of(T, runs, before + tiles - 1);
-    if (c0 == c1) return;                                        // its CTA finished it
-    const int rt = row / R, r = row % R;
-    // run c's partial: its first segment, unless it began with an earlier sequence's tiles
-    auto slot = [&](long long c) {
-        const int second = c == c0 && run_begin(T, runs, c) < before ? 1 : 0;
-        return ((static_cast<size_t>(c) * a.RT + rt) * 2 + second) * R + r;
-    };
+    if (parts == 1) return;                                      // its CTA finished it
+    const int r = row % R;
+    const size_t stride = static_cast<size_t>(a.RT) * 2 * R;     // rows of partials between runs
+    const size_t base = (static_cast<size_t>(c0) * a.RT + row / R) * 2 * R + r;
+    auto slot = [&](int i) { return base + i * stride + (i == 0 && late ? R : 0); };
+    // M = the largest maximum; weights exp2(m_i - M); L = sum of weight_i l_i
     float M = -INFINITY;
-    for (long long c = c0; c <= c1; ++c) M = fmaxf(M, a.part_ml[slot(c) * 2]);
-    float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
-    float L = 0.f;
-    for (long long c = c0; c <= c1; ++c) {
-        const float2 ml = *reinterpret_cast<const float2*>(a.part_ml + slot(c) * 2);
-        if (ml.x == -INFINITY && ml.y == 0.f) continue;          // saw nothing there
-        const float f = ml.x == M ? 1.f : lat_ex2(ml.x - M);
-        L += f * ml.y;
-        if (((c - c0) & 3) == grp) {
-            const float4 o = *reinterpret_cast<const float4*>(a.part_o + slot(c) * kLatDim + ch);
-            acc.x += f * o.x; acc.y += f * o.y; acc.z += f * o.z; acc.w += f * o.w;
-        }
+    for (int i = tid; i < parts; i += threads) {
+        const float m = a.part_ml[slot(i) * 2];
+        s_w[i] = m;
+        M = fmaxf(M, m);
     }
-    if (grp > 0) s_acc[grp - 1][tid & 127] = acc;
-    __syncthreads();
-    if (grp == 0) {
 #pragma unroll
-        for (int i = 0; i < 3; ++i) {
-            const float4 o = s_acc[i][tid];
+    for (int off = 16; off > 0; off >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, off));
+    if ((tid & 31) == 0) s_ml[0][tid >> 5] = M;
+    __syncthreads();
+    for (int i = 0; i < warps; ++i) M = fmaxf(M, s_ml[0][i]);
+    float L = 0.f;
+    for (int i = tid; i < parts; i += threads) {
+        const float m = s_w[i], l = a.part_ml[slot(i) * 2 + 1];
+        const float w = m == -INFINITY && l == 0.f ? 0.f : m == M ? 1.f : lat_ex2(m - M);     // 0: saw nothing there
+        s_w[i] = m == -INFINITY && l == 0.f ? -1.f : w;
+        L += w * l;
+    }
+#pragma unroll
+    for (int off = 16; off > 0; off >>= 1) L += __shfl_xor_sync(0xffffffffu, L, off);
+    if ((tid & 31) == 0) s_ml[1][tid >> 5] = L;
+    __syncthreads();
+    L = 0.f;
+    for (int i = 0; i < warps; ++i) L += s_ml[1][i];
+    float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 4
+    for (int i = grp; i < parts; i += NG) {
+        const float4 o = *reinterpret_cast<const float4*>(a.part_o + slot(i) * kLatDim + ch);
+        const float w = s_w[i];
+        if (w >= 0.f) { acc.x += w * o.x; acc.y += w * o.y; acc.z += w * o.z; acc.w += w * o.w; }
+    }
+    int bad = 0;
+    if (NG > 1) {
+        s_acc[tid] = acc;
+        __syncthreads();
+    }
+    if (grp == 0) {
+        for (int i = 1; i < NG; ++i) {
+            const float4 o = s_acc[tid + i * lanes];
             acc.x += o.x; acc.y += o.y; acc.z += o.z; acc.w += o.w;
         }
         const float inv = L == 0.f ? 0.f : 1.f / L;
         const float v[4] = {acc.x * inv, acc.y * inv, acc.z * inv, acc.w * inv};
-        if (!(fabsf(v[0]) < INFINITY && fabsf(v[1]) < INFINITY && fabsf(v[2]) < INFINITY && fabsf(v[3]) < INFINITY)) s_bad = 1;
+        bad = !(fabsf(v[0]) < INFINITY && fabsf(v[1]) < INFINITY && fabsf(v[2]) < INFINITY && fabsf(v[3]) < INFINITY);
         *reinterpret_cast<uint2*>(a.out + at * kLatDim + ch) = make_uint2(f32x2_to_bf16x2_bits(v[0], v[1]),
                                                                           f32x2_to_bf16x2_bits(v[2], v[3]));
-        if (tid == 0 && a.lse) a.lse[at] = (M + log2f(L)) * 0.69314718055994531f;
+        if (ch == 0 && a.lse) a.lse[at] = (M + log2f(L)) * 0.69314718055994531f;
     }
-    __syncthreads();
     const int j = row / a.H;
-    if (s_bad && j < a.K - 1 && tid < 32) latent_row_again<E4M3>(a, n, row, len - (a.K - 1 - j));
+    if (j < a.K - 1) {                                           // (Q = 1 where K > 1: the block owns the row)
+        bad = __syncthreads_or(bad);
+        if (bad && tid < 32) latent_row_again<E4M3>(a, n, row, len - (a.K - 1 - j));
+    }
 }
 
 namespace {
@@ -808,15 +869,20 @@ int launch_decode_shape(const LatMaps& maps, const LatArgs& a, cudaStream_t stre
     kda_latent_decode_kernel<R, E4M3><<<static_cast<unsigned>(a.w.G) * a.RT, Sh::kThreads, Sh::kBytes, stream>>>(maps, a);
     if (cudaGetLastError() != cudaSuccess) return -3;
     cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3(static_cast<unsigned>(a.w.N) * a.rows);
-    cfg.blockDim = dim3(512);
+    // a row's partials number about G / N + 1: one group of threads for every 8 of them; a
+    // row's channels over 4 blocks where rows are too few to fill the device
+    const int Q = a.K == 1 && static_cast<long long>(a.w.N) * a.rows < 256 ? 4 : 1;
+    int NG = Q;
+    while (NG < 4 * Q && NG * 8 < Q * (a.w.G / a.w.N + 1)) NG *= 2;
+    cfg.gridDim = dim3(static_cast<unsigned>(a.w.N) * a.rows * Q);
+    cfg.blockDim = dim3(128 / Q * NG);
     cfg.stream = stream;
     cudaLaunchAttribute at[1];
     at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
     at[0].val.programmaticStreamSerializationAllowed = 1;
     cfg.attrs = at;
     cfg.numAttrs = 1;
-    return cudaLaunchKernelEx(&cfg, kda_latent_combine_kernel<R, E4M3>, a) == cudaSuccess ? 0 : -3;
+    return cudaLaunchKernelEx(&cfg, kda_latent_combine_kernel<R, E4M3>, a, Q, NG) == cudaSuccess ? 0 : -3;
 }
 
 // Rows a CTA takes: 16, 32 or 64.
@@ -826,7 +892,8 @@ int rows_per_cta(int rows) { return rows <= 16 ? 16 : rows <= 32 ? 32 : 64; }
 // Runs of tiles (times row tiles: one CTA per SM) and the scratch bytes of their partials.
 int latent_decode_runs(int rows) {
     const int R = rows_per_cta(rows), RT = (rows + R - 1) / R, sms = sm_count();
-    return sms / RT > 0 ? sms / RT : (sms > 0 ? 1 : 0);
+    const int G = sms / RT > 0 ? sms / RT : (sms > 0 ? 1 : 0);
+    return G < kMaxRuns ? G : kMaxRuns;
 }
 size_t latent_decode_scratch(int rows) {
     const size_t R = rows_per_cta(rows), RT = (rows + R - 1) / R;
