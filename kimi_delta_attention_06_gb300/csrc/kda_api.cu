@@ -55,7 +55,7 @@ int launch_latent_decode(const uint16_t* q, const void* cache, int e4m3, int num
 size_t latent_decode_scratch(int rows);
 int launch_latent_prefill(const uint16_t* q, const uint16_t* k, long long ldk, long long hdk, const uint16_t* v,
                           long long ldv, long long hdv, const uint16_t* r, long long ldr, const int32_t* cu_q,
-                          const int32_t* cu_k, int num_seqs, int total_q, int total_k, int max_q, int H, int causal,
+                          const int32_t* cu_k, int num_seqs, int total_q, int total_k, int units, int H, int causal,
                           float sm_scale, uint16_t* out, float* lse, int* status, cudaStream_t stream);
 int launch_verify(const float* tp, long long ldp, const float* dp, long long ldq, const int32_t* toks,
                   const int32_t* num_draft, const float* ua, const float* us, int N, int K, int V, int32_t* out,
@@ -874,12 +874,13 @@ int kda_latent_prefill(const uint16_t* q, const uint16_t* k, int64_t ldk, int64_
         if (!stride_ok(ldk, 128) || !stride_ok(ldv, 128)) return KDA_ERR_INVALID_ARG;
     }
     if (static_cast<int64_t>(total_q) * H >= (int64_t(1) << 31)) return KDA_ERR_INVALID_ARG;
-    int max_q = 0;
-    for (int n = 0; n < num_seqs; ++n) max_q = cu_q_host[n + 1] - cu_q_host[n] > max_q ? cu_q_host[n + 1] - cu_q_host[n] : max_q;
+    int units = 0;                                            // CTAs a head: 256 queries of one sequence each
+    for (int n = 0; n < num_seqs; ++n) units += (cu_q_host[n + 1] - cu_q_host[n] + 255) / 256;
+    if (H > 65535) return KDA_ERR_UNSUPPORTED;
     int* status = nullptr;
     int rc = device_setup(&status);
     if (rc != KDA_OK) return rc;
-    rc = kda::launch_latent_prefill(q, k, ldk, hdk, v, ldv, hdv, k_rope, ldr, cu_q, cu_k, num_seqs, total_q, total_k, max_q,
+    rc = kda::launch_latent_prefill(q, k, ldk, hdk, v, ldv, hdv, k_rope, ldr, cu_q, cu_k, num_seqs, total_q, total_k, units,
                                     H, causal, sm_scale, out, lse, status, static_cast<cudaStream_t>(stream));
     return rc == 0 ? KDA_OK : KDA_ERR_CUDA;
 }
