@@ -9,20 +9,19 @@
 // pass over them.  One cluster of C CTAs serves a sequence, each CTA a contiguous slice of the
 // vocabulary and each warp a contiguous part of it; the slice sums are exchanged through
 // distributed shared memory, the CTA whose slice crosses the threshold narrows it to a warp's
-// part, then to 1/16 of that, then walks it.
+// part, then to one warp's share of that, then walks it.
 //
 // Which token is drawn depends on sums of up to V terms compared with a threshold, so they carry
 // about 45 bits: a lane's sum is an unevaluated pair of floats (Knuth's two-sum, 1969; the
-// difference p - q by Dekker's fast form, 1971, exact for p > q >= 0), and lanes are joined in
-// fp64.  fp64 throughout would be bound by the fp64 rate (2 operations a clock and SM): 3 of them
-// an element.
+// difference p - q by Dekker's fast form, 1971, exact for p > q >= 0), and so are the lanes joined;
+// fp64 only joins the warps' sums.  fp64 throughout would be bound by its rate (2 operations a
+// clock and SM): joining a CTA's 512 lanes in fp64 alone took longer than reading its slice.
 #include "common.cuh"
 #include "tc.cuh"
 
 namespace kda {
 
-constexpr int kVerWarps = 16, kVerThreads = kVerWarps * 32;
-constexpr int kVerMaxCluster = 8;
+constexpr int kVerMaxWarps = 16;
 
 struct VerRows {
     const float* p;
@@ -31,15 +30,15 @@ struct VerRows {
 };
 
 __device__ __forceinline__ float ver_clean(float x) {      // negative, NaN, infinite -> 0
-    return x > 0.f && x < __int_as_float(0x7f800000) ? x : 0.f;
+    return x < __int_as_float(0x7f800000) ? fmaxf(x, 0.f) : 0.f;
 }
 // Weight of a token as a pair hi + lo (exact).
 __device__ __forceinline__ float ver_weight(float p, float q, float& lo) {
     p = ver_clean(p);
     q = ver_clean(q);
-    const float d = p - q;
-    lo = p > q ? (p - d) - q : 0.f;
-    return p > q ? d : 0.f;
+    const float d = fmaxf(p - q, 0.f);
+    lo = d > 0.f ? (p - d) - q : 0.f;
+    return d;
 }
 __device__ __forceinline__ double ver_one(const VerRows& w, int t) {
     float lo;
@@ -50,7 +49,7 @@ __device__ __forceinline__ double ver_one(const VerRows& w, int t) {
 // Sum of the weights of tokens [a, b), over the lanes of a warp.
 template <bool Q>
 __device__ __forceinline__ double ver_sum(const VerRows& w, int a, int b, int lane) {
-    constexpr int U = 8;                       // loads in flight per row and lane
+    constexpr int U = 16;                      // loads in flight per row and lane
     float hi = 0.f, lo = 0.f;
     for (int t0 = a + lane; t0 < b; t0 += 32 * U) {
         float p[U], q[U];
@@ -69,27 +68,40 @@ __device__ __forceinline__ double ver_sum(const VerRows& w, int a, int b, int la
             hi = s;
         }
     }
-    double s = static_cast<double>(hi) + static_cast<double>(lo);
 #pragma unroll
-    for (int off = 16; off > 0; off >>= 1) s += __shfl_xor_sync(0xffffffffu, s, off);
-    return s;
+    for (int off = 16; off > 0; off >>= 1) {              // (still pairs of floats: fp64 adds of a whole warp are slow)
+        const float h = __shfl_xor_sync(0xffffffffu, hi, off), e = __shfl_xor_sync(0xffffffffu, lo, off);
+        const float s = hi + h, z = s - hi;
+        lo = (lo + e) + ((hi - (s - z)) + (h - z));
+        hi = s;
+    }
+    return static_cast<double>(hi) + static_cast<double>(lo);
 }
 __device__ __forceinline__ double ver_sum(const VerRows& w, int a, int b, int lane) {
     return w.q ? ver_sum<true>(w, a, b, lane) : ver_sum<false>(w, a, b, lane);
 }
 
-// First part whose running sum exceeds x, else the last part with weight; `base` becomes the sum
-// of the parts before it.
-__device__ __forceinline__ int ver_find(const double* part, int n, double x, double& base) {
-    double c = base, before = base;
-    int last = 0;
-    for (int i = 0; i < n; ++i) {
-        if (part[i] > 0.) { last = i; before = c; }
-        c += part[i];
-        if (part[i] > 0. && c > x) break;
+// Lane i of a warp holds the sum of part i.  The first part with weight whose running sum exceeds x
+// (else the last with weight: rounding left x at the total); `base` grows by the parts before it.
+__device__ __forceinline__ int ver_find(double part, double x, double& base) {
+    const int lane = threadIdx.x & 31;
+    double c = part;
+#pragma unroll
+    for (int off = 1; off < 32; off <<= 1) {
+        const double o = __shfl_up_sync(0xffffffffu, c, off);
+        if (lane >= off) c += o;
     }
-    base = before;
-    return last;
+    const unsigned has = __ballot_sync(0xffffffffu, part > 0.);
+    const unsigned over = __ballot_sync(0xffffffffu, part > 0. && base + c > x);
+    const int at = over ? __ffs(over) - 1 : has ? 31 - __clz(has) : 0;
+    const double before = __shfl_sync(0xffffffffu, c, at > 0 ? at - 1 : 0);
+    if (at > 0) base += before;
+    return at;
+}
+__device__ __forceinline__ double warp_total(double v) {
+#pragma unroll
+    for (int off = 16; off > 0; off >>= 1) v += __shfl_xor_sync(0xffffffffu, v, off);
+    return v;
 }
 
 __device__ __forceinline__ double ld_cluster_f64(uint32_t addr) {
@@ -98,19 +110,20 @@ __device__ __forceinline__ double ld_cluster_f64(uint32_t addr) {
     return v;
 }
 
-__global__ void __launch_bounds__(kVerThreads)
+__global__ void __launch_bounds__(kVerMaxWarps * 32, 2)
 kda_verify_kernel(const float* __restrict__ tp, long long ldp, const float* __restrict__ dp, long long ldq,
                   const int32_t* __restrict__ toks, const int32_t* __restrict__ num_draft,
                   const float* __restrict__ ua, const float* __restrict__ us, int K, int V, int C,
                   int32_t* __restrict__ out, int32_t* __restrict__ num_out, int* status)
 {
-    __shared__ double s_part[kVerWarps];
-    __shared__ double s_total;
-    __shared__ int s_first, s_bad;
+    __shared__ double s_part[kVerMaxWarps];
+    __shared__ double s_total, s_want, s_base;
+    __shared__ int s_first, s_bad, s_owner;
 
     const int rank = C > 1 ? static_cast<int>(tc::cluster_ctarank()) : 0;
     const long long n = blockIdx.x / static_cast<unsigned>(C);
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    const int threads = blockDim.x, warps = threads >> 5;
 
     // 1. the accepted count (every CTA of the cluster on its own)
     const int nd = num_draft ? num_draft[n] : K;
@@ -132,7 +145,7 @@ kda_verify_kernel(const float* __restrict__ tp, long long ldp, const float* __re
     __syncthreads();
     if (s_bad) {                                            // the same in every CTA of the cluster
         if (rank == 0) {
-            for (int i = tid; i <= K; i += kVerThreads) out[n * (K + 1) + i] = -1;
+            for (int i = tid; i <= K; i += threads) out[n * (K + 1) + i] = -1;
             if (tid == 0) { num_out[n] = 0; set_status(status, -1); }
         }
         return;
@@ -140,7 +153,7 @@ kda_verify_kernel(const float* __restrict__ tp, long long ldp, const float* __re
     const int a = s_first;
     if (rank == 0) {
         if (tid < a) out[n * (K + 1) + tid] = x;
-        for (int i = a + 1 + tid; i <= K; i += kVerThreads) out[n * (K + 1) + i] = -1;
+        for (int i = a + 1 + tid; i <= K; i += threads) out[n * (K + 1) + i] = -1;
         if (tid == 0) num_out[n] = a + 1;
     }
 
@@ -151,56 +164,56 @@ kda_verify_kernel(const float* __restrict__ tp, long long ldp, const float* __re
     w.hot = a < nd && !dp ? toks[n * K + a] : -1;
     const int S = (V + C - 1) / C;
     const int c0 = min(V, rank * S), c1 = min(V, c0 + S);
-    const int sub = (c1 - c0 + kVerWarps - 1) / kVerWarps;
-    double total, base;
-    int owner;
+    const int sub = (c1 - c0 + warps - 1) / warps;
     while (true) {
         const int a0 = min(c1, c0 + warp * sub), a1 = min(c1, a0 + sub);
         const double s = ver_sum(w, a0, a1, lane);
         if (lane == 0) s_part[warp] = s;
         __syncthreads();
-        if (tid == 0) {
-            double t = 0.;
-            for (int i = 0; i < kVerWarps; ++i) t += s_part[i];
-            s_total = t;
+        if (warp == 0) {
+            const double t = warp_total(lane < warps ? s_part[lane] : 0.);
+            if (lane == 0) s_total = t;
         }
-        double part[kVerMaxCluster];
-        if (C > 1) {
-            tc::cluster_sync();
-            const uint32_t mine = tc::smem_u32(&s_total);
-            for (int i = 0; i < kVerMaxCluster; ++i) part[i] = i < C ? ld_cluster_f64(tc::mapa(mine, i)) : 0.;
-            tc::cluster_sync();                             // s_total may change or go away after this
-        } else {
-            __syncthreads();
-            for (int i = 0; i < kVerMaxCluster; ++i) part[i] = i == 0 ? s_total : 0.;
+        if (C > 1) tc::cluster_sync();
+        if (warp == 0) {
+            __syncwarp();
+            double part = 0.;
+            if (C > 1) { if (lane < C) part = ld_cluster_f64(tc::mapa(tc::smem_u32(&s_total), lane)); }
+            else if (lane == 0) part = s_total;
+            const double total = warp_total(part), want = static_cast<double>(us[n]) * total;
+            double base = 0.;
+            const int owner = ver_find(part, want, base);
+            if (lane == 0) { s_owner = total > 0. ? owner : -1; s_want = want; s_base = base; }
         }
-        total = 0.;
-        for (int i = 0; i < kVerMaxCluster; ++i) total += part[i];
-        if (total > 0. || (!w.q && w.hot < 0)) {
-            base = 0.;
-            owner = ver_find(part, kVerMaxCluster, static_cast<double>(us[n]) * total, base);
-            break;
-        }
+        __syncthreads();
+        if (C > 1) tc::cluster_sync();                      // s_total may change or go away after this
+        if (s_owner >= 0 || (!w.q && w.hot < 0)) break;
         w.q = nullptr;
         w.hot = -1;
+        __syncthreads();                                    // everyone has read s_owner
     }
-    if (rank != owner) return;
-    if (!(total > 0.)) {
-        if (tid == 0) out[n * (K + 1) + a] = -1;
+    if (s_owner < 0) {
+        if (rank == 0 && tid == 0) out[n * (K + 1) + a] = -1;
         return;
     }
+    if (rank != s_owner) return;
 
-    // 3. narrow: this CTA's warp part, then 1/16 of it, then walk
-    const double want = static_cast<double>(us[n]) * total;
-    const int f = ver_find(s_part, kVerWarps, want, base);
-    const int b0 = min(c1, c0 + f * sub), b1 = min(c1, b0 + sub);
-    const int sub2 = (b1 - b0 + kVerWarps - 1) / kVerWarps;
+    // 3. narrow: this CTA's warp part, then one warp's share of that, then walk
+    const double want = s_want;
+    if (warp == 0) {
+        double base = s_base;
+        const int f = ver_find(lane < warps ? s_part[lane] : 0., want, base);
+        if (lane == 0) { s_first = f; s_base = base; }
+    }
+    __syncthreads();
+    const int b0 = min(c1, c0 + s_first * sub), b1 = min(c1, b0 + sub);
+    const int sub2 = (b1 - b0 + warps - 1) / warps;
     const double s2 = ver_sum(w, min(b1, b0 + warp * sub2), min(b1, b0 + (warp + 1) * sub2), lane);
-    __syncthreads();                                        // everyone is done with s_part
     if (lane == 0) s_part[warp] = s2;
     __syncthreads();
     if (warp != 0) return;
-    const int g = ver_find(s_part, kVerWarps, want, base);
+    double base = s_base;
+    const int g = ver_find(lane < warps ? s_part[lane] : 0., want, base);
     const int d0 = min(b1, b0 + g * sub2), d1 = min(b1, d0 + sub2);
     int pick = -1;
     for (int t0 = d0; t0 < d1; t0 += 32) {
@@ -225,12 +238,24 @@ int launch_verify(const float* tp, long long ldp, const float* dp, long long ldq
                   const int32_t* num_draft, const float* ua, const float* us, int N, int K, int V, int32_t* out,
                   int32_t* num_out, int* status, cudaStream_t stream)
 {
-    // enough CTAs to fill the device twice, slices of 4096 tokens at least
+    // Few sequences: 16 CTAs of 16 warps each (16 is past the portable cluster size), so that a row
+    // of 131072 is one round of loads.  Many: up to 8 CTAs of 8 warps, in slices of 2048 tokens
+    // at least, several per SM so that one's reads cover another's acceptance and narrowing.
+    const bool few = static_cast<long long>(N) * 16 <= 152 && V > 8 * 4096;
+    const int most = few ? 16 : 8, warps = few ? 16 : 8;
     int C = 1;
-    while (C < kVerMaxCluster && static_cast<long long>(N) * C < 2 * 152 && V / (2 * C) >= 4096) C *= 2;
+    while (C < most && static_cast<long long>(N) * C < 8 * 152 && V / (2 * C) >= 2048) C *= 2;
+    static bool wide_done[kMaxDevicesAttr] = {};
+    int dev = 0;
+    if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= kMaxDevicesAttr) return -3;
+    if (C > 8 && !wide_done[dev]) {
+        if (cudaFuncSetAttribute(kda_verify_kernel, cudaFuncAttributeNonPortableClusterSizeAllowed, 1) != cudaSuccess)
+            return -3;
+        wide_done[dev] = true;
+    }
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(static_cast<unsigned>(N) * C);
-    cfg.blockDim = dim3(kVerThreads);
+    cfg.blockDim = dim3(static_cast<unsigned>(warps) * 32);
     cfg.stream = stream;
     cudaLaunchAttribute at[1];
     at[0].id = cudaLaunchAttributeClusterDimension;

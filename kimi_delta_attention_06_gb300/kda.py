@@ -68,6 +68,8 @@ def library_path() -> str:
 def load():
     """Load libkda.so (raises if it was not built)."""
     global _lib
+    if _lib is not None:
+        return _lib
     with _lock:
         if _lib is None:
             if not os.path.exists(_LIB_PATH):
@@ -132,17 +134,25 @@ def load():
 
 
 def _ptr(t: Optional[torch.Tensor]):
+    """Device address of a contiguous tensor (the argument types make a pointer of it)."""
     if t is None:
         return None
     if not t.is_contiguous():
         raise ValueError("KDA tensors must be contiguous")
-    return ctypes.c_void_p(t.data_ptr())
+    return t.data_ptr()
 
 
-def _stream(stream) -> ctypes.c_void_p:
+# The current stream's handle without building a Stream object: a few microseconds a call, which
+# is as long as a small kernel runs.
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+
+
+def _stream(stream) -> int:
     if stream is None:
+        if _raw_stream is not None:
+            return _raw_stream(torch.cuda.current_device())
         stream = torch.cuda.current_stream()
-    return ctypes.c_void_p(stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream))
+    return stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)
 
 
 def _check(rc: int, what: str):
@@ -336,7 +346,7 @@ def _strided(t: torch.Tensor):
     """Device pointer of a tensor whose last dimension is contiguous (its other strides are passed on)."""
     if t.numel() and t.stride(-1) != 1:
         raise ValueError("the last dimension of a KDA tensor must be contiguous")
-    return ctypes.c_void_p(t.data_ptr())
+    return t.data_ptr()
 
 
 def _step(t: torch.Tensor, dim: int, least: int) -> int:
@@ -357,7 +367,18 @@ def _f32(t: Optional[torch.Tensor]) -> Optional[torch.Tensor]:
 
 
 def _host32(t):
+    if isinstance(t, torch.Tensor) and t.dtype == torch.int32 and not t.is_cuda and t.is_contiguous():
+        return t
     return torch.as_tensor(t).to(device="cpu", dtype=torch.int32).contiguous()
+
+
+def _last32(t: torch.Tensor) -> int:
+    """Last entry of a contiguous host int32 tensor (0 of an empty one), without an indexing call."""
+    n = t.numel()
+    return ctypes.c_int32.from_address(t.data_ptr() + 4 * (n - 1)).value if n else 0
+
+
+_ROW_BYTES = {KDA_CACHE_BF16: 2 * (KDA_LATENT_DIM + KDA_LATENT_ROPE), KDA_CACHE_E4M3: KDA_LATENT_DIM + 2 * KDA_LATENT_ROPE + 16}
 
 
 def kda_latent_row_bytes(cache_dtype: int) -> int:
@@ -368,9 +389,10 @@ def kda_latent_row_bytes(cache_dtype: int) -> int:
 
 def _pages(cache: torch.Tensor, cache_dtype: int):
     """(pointer, num_pages, page_size) of a cache [num_pages, page_size, row bytes] uint8."""
-    if cache.dtype != torch.uint8 or cache.dim() != 3 or cache.shape[2] != kda_latent_row_bytes(cache_dtype):
+    shape = cache.shape
+    if cache.dtype != torch.uint8 or len(shape) != 3 or shape[2] != _ROW_BYTES.get(cache_dtype):
         raise ValueError("a latent cache is a uint8 tensor [num_pages, page_size, row bytes of its cache_dtype]")
-    return _ptr(cache), int(cache.shape[0]), int(cache.shape[1])
+    return _ptr(cache), shape[0], shape[1]
 
 
 def kda_latent_append(c, k_rope, cache, cache_dtype: int, slots, total_tokens: int, stream=None):
@@ -388,7 +410,7 @@ def kda_latent_gather(cache, cache_dtype: int, block_table, start_pos, cu_seqlen
     cu_host = _host32(cu_seqlens_host)
     rc = load().kda_latent_gather(p, int(cache_dtype), num_pages, page_size, _ptr(_i32(block_table)),
                                   int(block_table.shape[1]), _ptr(_i32(start_pos)), _ptr(_i32(cu_seqlens)),
-                                  ctypes.c_void_p(cu_host.data_ptr()), int(num_seqs), int(total_tokens),
+                                  cu_host.data_ptr(), int(num_seqs), int(total_tokens),
                                   _strided(_bits16(c)), _step(c, 0, KDA_LATENT_DIM), _strided(_bits16(k_rope)),
                                   _step(k_rope, 0, KDA_LATENT_ROPE), _stream(stream))
     _check(rc, "kda_latent_gather")
@@ -408,9 +430,9 @@ def kda_latent_prefill(q, k, v, k_rope, cu_q, cu_q_host, cu_k, cu_k_host, num_se
     cq, ck = _host32(cu_q_host), _host32(cu_k_host)
     rc = load().kda_latent_prefill(_ptr(_bits16(q)), _strided(_bits16(k)), _step(k, 0, 128), _step(k, 1, 128),
                                    _strided(_bits16(v)), _step(v, 0, 128), _step(v, 1, 128), _strided(_bits16(k_rope)),
-                                   _step(k_rope, 0, KDA_LATENT_ROPE), _ptr(_i32(cu_q)), ctypes.c_void_p(cq.data_ptr()), _ptr(_i32(cu_k)),
-                                   ctypes.c_void_p(ck.data_ptr()), int(num_seqs), int(total_q), int(total_k), int(H),
-                                   int(causal), float(sm_scale), _ptr(_bits16(out)), _ptr(_f32(lse)), _stream(stream))
+                                   _step(k_rope, 0, KDA_LATENT_ROPE), _ptr(_i32(cu_q)), cq.data_ptr(), _ptr(_i32(cu_k)),
+                                   ck.data_ptr(), int(num_seqs), int(total_q), int(total_k), int(H), int(causal),
+                                   float(sm_scale), _ptr(_bits16(out)), _ptr(_f32(lse)), _stream(stream))
     _check(rc, "kda_latent_prefill")
 
 
@@ -504,7 +526,7 @@ def latent_append(c, k_rope, cache, cache_dtype: int, slots, stream=None):
 def latent_gather(cache, cache_dtype: int, block_table, cu_seqlens_host, cu_seqlens=None, start_pos=None, stream=None):
     """Read sequences back as dense rows; returns (c [T, 512], k_rope [T, 64]), bf16."""
     cu_host = _host32(cu_seqlens_host)
-    N, T = cu_host.numel() - 1, int(cu_host[-1])
+    N, T = cu_host.numel() - 1, _last32(cu_host)
     if cu_seqlens is None:
         cu_seqlens = cu_host.to(cache.device)
     c = torch.empty(T, KDA_LATENT_DIM, device=cache.device, dtype=torch.bfloat16)
