@@ -52,10 +52,7 @@ kda_latent_append_kernel(const uint16_t* __restrict__ c, long long ldc, const ui
             x[i] = fin ? x[i] : __int_as_float(0x7fffffff);
         }
         amax = __uint_as_float(__reduce_max_sync(0xffffffffu, __float_as_uint(amax)));   // non-negative: bits order
-        // smallest e with amax <= 448 * 2^e = 1.75 * 2^(8 + e)
-        const uint32_t bits = __float_as_uint(amax);
-        int e = static_cast<int>(bits >> 23) - 127 - 8 + ((bits & 0x7fffffu) > 0x600000u ? 1 : 0);
-        e = bits == 0 ? 0 : max(-117, min(119, e));
+        const int e = lat_scale_exponent(__float_as_uint(amax));
         const float inv = __uint_as_float(static_cast<uint32_t>(127 - e) << 23);          // 2^-e: products are exact
         uint32_t o[4];
 #pragma unroll

@@ -10,6 +10,18 @@
 //     O^T [512 channels x R rows]  += C[:, :512]^T P^T [64 x R]        (4 blocks of M = 128, N = R)
 // with R = 16, 32 or 64 rows a CTA, so few rows do not leave the tensor cores' M side empty.  One
 // shared-memory tile of C (128-byte swizzle) serves both: K-major for S, MN-major for O.
+//
+// An e4m3 cache enters both products as it is, without being expanded:
+//   - q / 2^k (2^k a row: the largest magnitude in (224, 448]) is the sum of two e4m3 values, exactly
+//     where |q| is above 1/1800 of the row's largest (8 bits of bf16 in 4 + 4), within 2^-19 of it
+//     below.  The position part is bf16 and has its own accumulator, as the scale s of a token
+//     belongs to its latent only: x = scale * (2^k s S_c + S_r).
+//   - s moves from the latents to the weights: O = sum (p s) codes.  p s is the sum of three e5m2
+//     values (3 bits each: a relative 2^-9, less than a rounding to bf16), scaled so that the
+//     largest lies near 2^12, which leaves 28 binades below it.
+// Expanding the tile to bf16 instead (exact too) took 4800 clocks a tile of 64 rows: loads into
+// registers hold too little in flight beside 227 KB of shared memory, and the tile is written and
+// read once more.
 #include <cuda.h>
 #include "latent.cuh"
 #include "tc.cuh"
@@ -146,12 +158,17 @@ struct SegWalk {
     int t0, t1;                                 // current segment: tiles [t0, t1) of sequence n
     bool first;
 
-    __device__ void init(const LatWork& w, int c) {
+    __device__ __forceinline__ void init(const LatWork& w, int c) {
         const int lane = threadIdx.x & 31;
-        long long T = 0;
-        for (int i = lane; i < w.N; i += 32) T += lat_tiles(lat_len(w, i));
+        const int len0 = lane < w.N ? lat_len(w, lane) : 0;     // the first 32 stay in registers
+        long long T = lat_tiles(len0);
+        for (int i = lane + 32; i < w.N; i += 32) T += lat_tiles(lat_len(w, i));
+        if (w.N <= 32 && __reduce_max_sync(0xffffffffu, static_cast<unsigned>(T)) < (1u << 26)) {
+            T = __reduce_add_sync(0xffffffffu, static_cast<unsigned>(T));
+        } else {
 #pragma unroll
-        for (int off = 16; off > 0; off >>= 1) T += __shfl_xor_sync(0xffffffffu, T, off);
+            for (int off = 16; off > 0; off >>= 1) T += __shfl_xor_sync(0xffffffffu, T, off);
+        }
         pos = end = base = 0;
         n = len = tiles = t0 = t1 = 0;
         first = true;
@@ -161,7 +178,8 @@ struct SegWalk {
         pos = run_begin(T, runs, c);
         end = run_begin(T, runs, c + 1);
         for (int i0 = 0; i0 < w.N; i0 += 32) {
-            const int mine = i0 + lane < w.N ? lat_tiles(lat_len(w, i0 + lane)) : 0;
+            const int lane_len = i0 == 0 ? len0 : i0 + lane < w.N ? lat_len(w, i0 + lane) : 0;
+            const int mine = lat_tiles(lane_len);
             int incl = mine;
 #pragma unroll
             for (int off = 1; off < 32; off <<= 1) {
@@ -173,12 +191,12 @@ struct SegWalk {
                 const int at = __ffs(hit) - 1;
                 n = i0 + at;
                 base += __shfl_sync(0xffffffffu, incl - mine, at);
-                break;
+                len = __shfl_sync(0xffffffffu, lane_len, at);
+                tiles = lat_tiles(len);
+                return;
             }
             base += __shfl_sync(0xffffffffu, incl, 31);
         }
-        len = lat_len(w, n);
-        tiles = lat_tiles(len);
     }
     // The next segment; false when the run is done.
     __device__ bool next(const LatWork& w) {
@@ -198,7 +216,9 @@ struct SegWalk {
 };
 
 // ---- the tensor-core kernel --------------------------------------------------------------------
-struct LatMaps { CUtensorMap q, c; };            // q [rows, 576], bf16 cache [slots, 576]; 64-column boxes
+// q [rows, 576] and a bf16 cache [slots, 576] in boxes of 64 columns; an e4m3 cache [slots, 656 bytes] in
+// boxes of 128 bytes (128 codes, or the position key), and its scales in boxes of 16 bytes
+struct LatMaps { CUtensorMap q, c, s; };
 
 struct LatArgs {
     LatWork w;
@@ -216,19 +236,26 @@ struct LatArgs {
 template <int R, bool E4M3>
 struct LatShape {
     static constexpr int kSoft = 128;            // warps 0..3: softmax, rescale, epilogue
-    static constexpr int kMmaWarp = 4;
-    static constexpr int kProdWarps = E4M3 ? 8 : 1;
-    static constexpr int kThreads = kSoft + 32 + 32 * kProdWarps;
+    static constexpr int kMmaWarp = 4, kTmaWarp = 5;
+    static constexpr int kThreads = 192;
+    static constexpr int kStages = E4M3 ? 3 : 2;
     static constexpr uint32_t kSlabQ = R * 128u, kSlabC = kTile * 128u;
-    static constexpr uint32_t kStage = 9u * kSlabC;
-    static constexpr uint32_t oQ = 0, oC = 9u * kSlabQ, oP = oC + 2u * kStage, oBar = oP + kTile * 128u;
-    static constexpr uint32_t kBytes = oBar + 80u + 6u * R * 4u;
-    static constexpr uint32_t kTmemCols = R == 16 ? 128u : R == 32 ? 256u : 512u;     // 4 R (O) + 2 R (S)
+    // bf16: 9 slabs of 64 values; e4m3: 4 slabs of 128 codes, the position key's, 64 scales of 16 bytes
+    static constexpr uint32_t kSlabs = E4M3 ? 5u : 9u, kStage = kSlabs * kSlabC + (E4M3 ? 1024u : 0u);
+    // Q: 9 slabs of 64 bf16; e4m3: 2 terms x 4 slabs of 128 codes, then the position part's
+    static constexpr uint32_t kP = E4M3 ? 3u : 1u;                                    // tiles of P
+    static constexpr uint32_t oQ = 0, oC = 9u * kSlabQ, oP = oC + kStages * kStage, oBar = oP + kP * kTile * 128u;
+    static constexpr uint32_t kBytes = oBar + 96u + 7u * R * 4u;
+    static constexpr uint32_t kS = E4M3 ? 2u * R : R;                                 // TMEM columns of one S buffer
+    static constexpr uint32_t kTmemCols = R == 16 ? 128u : R == 32 ? 256u : 512u;     // 4 R (O) + 2 kS
 };
-// shared memory: 9 slabs of Q | 2 stages of 9 slabs of C | P | barriers, exchange
-static_assert(LatShape<64, false>::kBytes <= 232448, "227 KB of shared memory");
+static_assert(LatShape<64, false>::kBytes <= 232448 && LatShape<64, true>::kBytes <= 232448, "227 KB of shared memory");
 
-constexpr float kLatTau = 8.f;                   // scores may exceed the running maximum by 2^8 before a rescale
+// A row's weights are exp2(x - m).  m follows the row's maximum M lazily: bf16, m <= M <= m + 8 (the
+// sums have the range for it); e4m3, m + 12 <= M <= m + 15, so that the weights times s fill e5m2's
+// range and stay below its 57344.
+template <bool E4M3> constexpr float kAbove = E4M3 ? 12.f : 0.f;
+template <bool E4M3> constexpr float kMost = E4M3 ? 15.f : 8.f;
 constexpr uint32_t kBarSoft = 1;                 // named barrier of the softmax warps
 
 // Columns of S^T in the 16 x 256-bit shape: thread T holds tokens T / 4 and T / 4 + 8 of its warp's
@@ -273,25 +300,33 @@ kda_latent_decode_kernel(const __grid_constant__ LatMaps maps, const LatArgs a)
     uint8_t* sC = smem + Sh::oC;
     uint8_t* sP = smem + Sh::oP;
     uint64_t* bars = reinterpret_cast<uint64_t*>(smem + Sh::oBar);
-    uint64_t *full = bars, *empty = bars + 2, *s_full = bars + 4, *p_full = bars + 6, *q_full = bars + 7;
-    uint32_t* s_tmem = reinterpret_cast<uint32_t*>(bars + 8);
-    float* s_red = reinterpret_cast<float*>(bars + 8) + 4;      // [4][R]
+    uint64_t *full = bars, *empty = bars + 3, *s_full = bars + 6, *p_full = bars + 8, *q_full = bars + 9;
+    uint32_t* s_tmem = reinterpret_cast<uint32_t*>(bars + 10);
+    float* s_red = reinterpret_cast<float*>(bars + 12);         // [4][R]
     float* s_f = s_red + 4 * R;                                 // [R]
     int* s_j = reinterpret_cast<int*>(s_f + R);                 // [R]: query token of each row
+    float* s_a = s_f + 2 * R;                                   // [R]: e4m3: 2^k * scale of each row
+    constexpr int NS = Sh::kStages;
 
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const int rt = blockIdx.x % a.RT, run = blockIdx.x / a.RT;
     const int row0 = rt * R, nrows = min(R, a.rows - row0);
 
     if (tid == 0) {
-        for (int i = 0; i < 2; ++i) {
-            tc::mbar_init(&full[i], Sh::kProdWarps);
+        for (int i = 0; i < NS; ++i) {
+            tc::mbar_init(&full[i], 1);
             tc::mbar_init(&empty[i], 1);
-            tc::mbar_init(&s_full[i], 1);
         }
+        tc::mbar_init(&s_full[0], 1);
+        tc::mbar_init(&s_full[1], 1);
         tc::mbar_init(p_full, Sh::kSoft);
-        tc::mbar_init(q_full, 1);
+        tc::mbar_init(q_full, E4M3 ? Sh::kSoft : 1);
         tc::mbar_fence_init();
+    }
+    if (tid == 0) {
+        tc::tma_prefetch_map(&maps.c);
+        if (E4M3) tc::tma_prefetch_map(&maps.s);
+        else tc::tma_prefetch_map(&maps.q);
     }
     if (tid < R) s_j[tid] = min((row0 + tid) / a.H, a.K - 1);
     if (warp == Sh::kMmaWarp) tc::tmem_alloc(s_tmem, Sh::kTmemCols);
@@ -314,12 +349,88 @@ kda_latent_decode_kernel(const __grid_constant__ LatMaps maps, const LatArgs a)
 #pragma unroll
             for (int i = 0; i < R / 4; ++i) { m[i] = -INFINITY; l[i] = 0.f; }
             const int clear = sw.len - (a.K - 1);               // tokens that every row sees
+            if constexpr (E4M3) {
+                // Q of the segment (the last S product of the segment before has run): a warp a row, the
+                // loads of 4 rows in flight
+#pragma unroll 1
+                for (int rb = warp; rb < R; rb += 16) {
+                    uint4 w0[4], w1[4];
+                    uint32_t rope[4];
+#pragma unroll
+                    for (int k = 0; k < 4; ++k) {
+                        const uint16_t* src = a.q + (static_cast<long long>(sw.n) * a.rows + row0 + min(rb + 4 * k, nrows - 1)) * kLatQ;
+                        w0[k] = reinterpret_cast<const uint4*>(src)[2 * lane];
+                        w1[k] = reinterpret_cast<const uint4*>(src)[2 * lane + 1];
+                        rope[k] = reinterpret_cast<const uint32_t*>(src + kLatDim)[lane];
+                    }
+#pragma unroll
+                    for (int k = 0; k < 4; ++k) {
+                        const int r = rb + 4 * k;
+                        const uint32_t wv[8] = {w0[k].x, w0[k].y, w0[k].z, w0[k].w, w1[k].x, w1[k].y, w1[k].z, w1[k].w};
+                        float v[16], top = 0.f;
+#pragma unroll
+                        for (int i = 0; i < 8; ++i) {
+                            const float2 f = bf16x2_bits_to_f32(wv[i]);
+                            v[2 * i] = f.x; v[2 * i + 1] = f.y;
+                        }
+#pragma unroll
+                        for (int i = 0; i < 16; ++i) {          // an infinity has no code: NaN, as its scores would be
+                            const bool fin = fabsf(v[i]) < INFINITY;
+                            top = fmaxf(top, fin ? fabsf(v[i]) : 0.f);
+                            v[i] = fin ? v[i] : __int_as_float(0x7fffffff);
+                        }
+                        top = __uint_as_float(__reduce_max_sync(0xffffffffu, __float_as_uint(top)));
+                        const int e = lat_scale_exponent(__float_as_uint(top));
+                        const float inv = __uint_as_float(static_cast<uint32_t>(127 - e) << 23);
+                        uint32_t t1[4], t2[4];
+#pragma unroll
+                        for (int i = 0; i < 4; ++i) {
+                            t1[i] = t2[i] = 0u;
+#pragma unroll
+                            for (int h = 0; h < 2; ++h) {
+                                const float x0 = v[4 * i + 2 * h] * inv, x1 = v[4 * i + 2 * h + 1] * inv;
+                                const uint32_t c = f32x2_to_e4m3x2(x0, x1);
+                                const float2 b = e4m3x2_to_f32(c);
+                                t1[i] |= c << (16 * h);
+                                t2[i] |= f32x2_to_e4m3x2(x0 - b.x, x1 - b.y) << (16 * h);
+                            }
+                        }
+                        uint8_t* d = sQ + (lane >> 3) * Sh::kSlabQ + r * 128 + (((lane & 7) ^ (r & 7)) << 4);
+                        *reinterpret_cast<uint4*>(d) = make_uint4(t1[0], t1[1], t1[2], t1[3]);
+                        *reinterpret_cast<uint4*>(d + 4 * Sh::kSlabQ) = make_uint4(t2[0], t2[1], t2[2], t2[3]);
+                        *reinterpret_cast<uint32_t*>(sQ + 8 * Sh::kSlabQ + tc::sw128_off16(r, 2 * lane, R)) = rope[k];
+                        if (lane == 0) s_a[r] = __uint_as_float(static_cast<uint32_t>(127 + e) << 23) * a.scale_log2;
+                    }
+                }
+                tc::fence_smem_to_async();
+                tc::mbar_arrive(q_full);
+                tc::named_sync(kBarSoft, Sh::kSoft);             // s_a is read by all
+            }
             for (int t = sw.t0; t < sw.t1; ++t, ++g) {
                 ok = __all_sync(0xffffffffu, tc::mbar_wait_bounded(&s_full[g & 1], (g >> 1) & 1, kWaitLimitNs));
                 float x[R / 2];
+                float s0 = 1.f, s1 = 1.f, e0 = 0.f, e1 = 0.f;   // e4m3: scales of the thread's two tokens, their exponents
                 if (ok) {
                     tc::fence_after_sync();
-                    tmem_ld_s<R>(tmS + (g & 1) * R + lane_tm, x);
+                    tmem_ld_s<R>(tmS + (g & 1) * Sh::kS + lane_tm, x);
+                    if constexpr (E4M3) {
+                        const float* sc = reinterpret_cast<const float*>(sC + g % NS * Sh::kStage + Sh::kSlabs * Sh::kSlabC);
+                        s0 = sc[(16 * warp + tq) * 4];
+                        s1 = sc[(16 * warp + tq + 8) * 4];
+                        e0 = static_cast<float>(static_cast<int>(__float_as_uint(s0) >> 23) - 127);
+                        e1 = static_cast<float>(static_cast<int>(__float_as_uint(s1) >> 23) - 127);
+                        float xr[R / 2];
+                        tmem_ld_s<R>(tmS + (g & 1) * Sh::kS + R + lane_tm, xr);
+                        // x: scores in powers of two, plus the scale's exponent (the weights carry s)
+#pragma unroll
+                        for (int i = 0; i < R / 2; ++i) {
+                            const float sa = s_a[8 * (i >> 2) + rq + (i & 1)] * (i & 2 ? s1 : s0);
+                            x[i] = fmaf(x[i], sa, fmaf(xr[i], a.scale_log2, i & 2 ? e1 : e0));
+                        }
+                    } else {
+#pragma unroll
+                        for (int i = 0; i < R / 2; ++i) x[i] *= a.scale_log2;
+                    }
                 }
                 const int tok = t * kTile + 16 * warp + tq;     // and tok + 8
                 const bool edge = (t + 1) * kTile > clear;
@@ -327,26 +438,28 @@ kda_latent_decode_kernel(const __grid_constant__ LatMaps maps, const LatArgs a)
 #pragma unroll
                     for (int i = 0; i < R / 2; ++i) {
                         const int see = clear + s_j[8 * (i >> 2) + rq + (i & 1)];
-                        x[i] = tok + 4 * (i & 2) < see ? x[i] * a.scale_log2 : -INFINITY;
+                        x[i] = tok + 4 * (i & 2) < see ? x[i] : -INFINITY;
                     }
                     // rows past the end of the sequence hold anything: they enter the second product as zeros
                     const int valid = sw.len - t * kTile;
-                    if (!E4M3 && valid < kTile) {
-                        uint8_t* c = sC + (g & 1) * Sh::kStage;
-                        for (int i = tid; i < 8 * (kTile - max(valid, 0)) * 8; i += Sh::kSoft) {
-                            const int slab = i & 7, ch = (i >> 3) & 7, r = valid + (i >> 6);
+                    if (valid < kTile) {
+                        uint8_t* c = sC + g % NS * Sh::kStage;
+                        constexpr int W = E4M3 ? 4 : 8;         // slabs of latents
+                        for (int i = tid; i < W * (kTile - valid) * 8; i += Sh::kSoft) {
+                            const int ch = i & 7, slab = i / 8 % W, r = valid + i / (8 * W);
                             *reinterpret_cast<uint4*>(c + slab * Sh::kSlabC + r * 128 + ch * 16) = make_uint4(0, 0, 0, 0);
                         }
+                        if (E4M3) {                             // and their scales are not to be used
+                            if (16 * warp + tq >= valid) s0 = 1.f;
+                            if (16 * warp + tq + 8 >= valid) s1 = 1.f;
+                        }
                     }
-                } else {
-#pragma unroll
-                    for (int i = 0; i < R / 2; ++i) x[i] *= a.scale_log2;
                 }
                 // the previous tile's product has read P and is in O
-                if (ok && g > 0) ok = tc::mbar_wait_bounded(&empty[(g - 1) & 1], ((g - 1) >> 1) & 1, kWaitLimitNs);
+                if (ok && g > 0) ok = tc::mbar_wait_bounded(&empty[(g - 1) % NS], (g - 1) / NS & 1, kWaitLimitNs);
                 bool grow = !ok;
 #pragma unroll
-                for (int i = 0; i < R / 2; ++i) grow |= x[i] > m[2 * (i >> 2) + (i & 1)] + kLatTau;
+                for (int i = 0; i < R / 2; ++i) grow |= x[i] > m[2 * (i >> 2) + (i & 1)] + kMost<E4M3>;
                 if (!tc::named_sync_and(kBarSoft, Sh::kSoft, !grow)) {
                     ok = tc::named_sync_and(kBarSoft, Sh::kSoft, ok);
                     if (!ok) break;
@@ -364,7 +477,7 @@ kda_latent_decode_kernel(const __grid_constant__ LatMaps maps, const LatArgs a)
                     for (int i = 0; i < R / 4; ++i) {
                         const int r = 8 * (i >> 1) + rq + (i & 1);
                         const float mx = fmaxf(fmaxf(s_red[r], s_red[R + r]), fmaxf(s_red[2 * R + r], s_red[3 * R + r]));
-                        const float mn = fmaxf(m[i], mx);
+                        const float mn = fmaxf(m[i], mx - kAbove<E4M3>);
                         const float f = mn == m[i] ? 1.f : lat_ex2(m[i] - mn);
                         m[i] = mn;
                         l[i] *= f;
@@ -391,18 +504,37 @@ kda_latent_decode_kernel(const __grid_constant__ LatMaps maps, const LatArgs a)
                         tc::tmem_wait_st();
                     }
                 }
-                // P = exp2(x - m), rounded to bf16 for the product; the sums keep fp32
+                // P = exp2(x - m), rounded for the product (see above); the sums keep fp32
                 const int tr = 16 * warp + tq;
+                const float r0 = 1.f / s0, r1 = 1.f / s1;       // (powers of two)
 #pragma unroll
                 for (int b = 0; b < R / 8; ++b) {
                     const float m0 = m[2 * b] == -INFINITY ? 0.f : m[2 * b], m1 = m[2 * b + 1] == -INFINITY ? 0.f : m[2 * b + 1];
                     const float p0 = lat_ex2(x[4 * b] - m0), p1 = lat_ex2(x[4 * b + 1] - m1);
                     const float p2 = lat_ex2(x[4 * b + 2] - m0), p3 = lat_ex2(x[4 * b + 3] - m1);
-                    l[2 * b] += p0 + p2;
-                    l[2 * b + 1] += p1 + p3;
-                    const uint32_t off = tc::sw128_off16(tr, 8 * b + rq, kTile);
-                    *reinterpret_cast<uint32_t*>(sP + off) = f32x2_to_bf16x2_bits(p0, p1);
-                    *reinterpret_cast<uint32_t*>(sP + off + 8 * 128) = f32x2_to_bf16x2_bits(p2, p3);   // token + 8: same swizzle
+                    if constexpr (!E4M3) {
+                        l[2 * b] += p0 + p2;
+                        l[2 * b + 1] += p1 + p3;
+                        const uint32_t off = tc::sw128_off16(tr, 8 * b + rq, kTile);
+                        *reinterpret_cast<uint32_t*>(sP + off) = f32x2_to_bf16x2_bits(p0, p1);
+                        *reinterpret_cast<uint32_t*>(sP + off + 8 * 128) = f32x2_to_bf16x2_bits(p2, p3);   // token + 8: same swizzle
+                    } else {
+                        l[2 * b] += fmaf(p0, r0, p2 * r1);
+                        l[2 * b + 1] += fmaf(p1, r0, p3 * r1);
+                        const uint32_t n = 8 * b + rq, off = tr * 128 + (((n >> 4) ^ (tr & 7)) << 4) + (n & 15);
+                        float q0 = p0, q1 = p1, q2 = p2, q3 = p3;
+#pragma unroll
+                        for (int k = 0; k < 3; ++k) {           // three terms, each the rounding of what is left
+                            const uint32_t u = f32x2_to_e5m2x2(q0, q1), v = f32x2_to_e5m2x2(q2, q3);
+                            uint8_t* d = sP + k * kTile * 128 + off;
+                            *reinterpret_cast<uint16_t*>(d) = static_cast<uint16_t>(u);
+                            *reinterpret_cast<uint16_t*>(d + 8 * 128) = static_cast<uint16_t>(v);
+                            if (k < 2) {
+                                const float2 fu = e5m2x2_to_f32(u), fv = e5m2x2_to_f32(v);
+                                q0 -= fu.x; q1 -= fu.y; q2 -= fv.x; q3 -= fv.y;
+                            }
+                        }
+                    }
                 }
                 tc::fence_smem_to_async();
                 tc::fence_before_sync();
@@ -410,7 +542,7 @@ kda_latent_decode_kernel(const __grid_constant__ LatMaps maps, const LatArgs a)
             }
             if (!ok) break;
             // ---- epilogue of the segment: O^T is complete once the last product is ----
-            ok = tc::mbar_wait_bounded(&empty[(g - 1) & 1], ((g - 1) >> 1) & 1, kWaitLimitNs);
+            ok = tc::mbar_wait_bounded(&empty[(g - 1) % NS], (g - 1) / NS & 1, kWaitLimitNs);
             ok = tc::named_sync_and(kBarSoft, Sh::kSoft, ok);
             if (!ok) break;
             tc::fence_after_sync();
@@ -420,64 +552,66 @@ kda_latent_decode_kernel(const __grid_constant__ LatMaps maps, const LatArgs a)
                 v += __shfl_xor_sync(0xffffffffu, v, 4);
                 v += __shfl_xor_sync(0xffffffffu, v, 8);
                 v += __shfl_xor_sync(0xffffffffu, v, 16);
-                if (lane < 4) s_red[warp * R + 8 * (i >> 1) + rq + (i & 1)] = v;
+                const int r = 8 * (i >> 1) + rq + (i & 1);
+                if (lane < 4) s_red[warp * R + r] = v;
+                if (tid < 4) s_f[r] = m[i];
             }
             tc::named_sync(kBarSoft, Sh::kSoft);
             const bool whole = sw.whole();
             const long long row_at = static_cast<long long>(sw.n) * a.rows + row0;
             const size_t part = (static_cast<size_t>(run) * a.RT + rt) * 2 + (sw.first ? 0 : 1);
-#pragma unroll
-            for (int i = 0; i < R / 4; ++i) {
-                const int r = 8 * (i >> 1) + rq + (i & 1);
-                const float sum = (s_red[r] + s_red[R + r]) + (s_red[2 * R + r] + s_red[3 * R + r]);
-                if (tid < 4) {
-                    s_f[r] = sum == 0.f ? 0.f : 1.f / sum;
-                    if (!whole) {
-                        *reinterpret_cast<float2*>(a.part_ml + (part * R + r) * 2) = make_float2(m[i], sum);
-                    } else if (a.lse && r < nrows) {
-                        a.lse[row_at + r] = (m[i] + log2f(sum)) * 0.69314718055994531f;
-                    }
-                }
+            if (tid < R) {                                       // a thread a row
+                const float mr = s_f[tid], sum = (s_red[tid] + s_red[R + tid]) + (s_red[2 * R + tid] + s_red[3 * R + tid]);
+                if (!whole) *reinterpret_cast<float2*>(a.part_ml + (part * R + tid) * 2) = make_float2(mr, sum);
+                else if (a.lse && tid < nrows) a.lse[row_at + tid] = (mr + log2f(sum)) * 0.69314718055994531f;
+                s_f[tid] = sum == 0.f ? 0.f : 1.f / sum;
             }
             tc::named_sync(kBarSoft, Sh::kSoft);
             uint32_t bad[2] = {0u, 0u};                          // rows with a result that is no number
             const int ch = 32 * warp + lane;
-            // two rows a store: the even lane of a pair takes both channels of the first, the odd of the second
-            const int odd = lane & 1;
-            uint16_t* d16 = a.out + (row_at + odd) * kLatDim + (ch - odd);
-            float* d32 = a.part_o + part * R * kLatDim + ch;
+            if (!whole) {
+                float* d32 = a.part_o + part * R * kLatDim + ch;
 #pragma unroll 1
-            for (int c0 = 0; c0 < R; c0 += 16) {
-                if (c0 >= nrows) break;
-#pragma unroll 1
-                for (int b2 = 0; b2 < 4; b2 += 2) {
-                    float o[2][16];
-                    tc::tmem_ld16(tmO + b2 * R + c0 + lane_tm, o[0]);
-                    tc::tmem_ld16(tmO + (b2 + 1) * R + c0 + lane_tm, o[1]);
+                for (int c = 0; c < R / 4; ++c) {                // 16 rows x 128 channels a step
+                    float o[16];
+                    tc::tmem_ld16(tmO + (c & 3) * R + (c >> 2) * 16 + lane_tm, o);
                     tc::tmem_wait_ld();
-                    if (whole) {
+                    float* d = d32 + (c >> 2) * 16 * kLatDim + (c & 3) * 128;
 #pragma unroll
-                        for (int i = 0; i < 16; i += 2) {
-                            const float f0 = s_f[c0 + i], f1 = s_f[c0 + i + 1];
+                    for (int i = 0; i < 16; ++i) d[i * kLatDim] = o[i];
+                }
+            } else {
+                // two rows a store: packed as (row i, row i + 1) of one channel, then the even lane of a pair
+                // takes both channels of row i, the odd lane those of row i + 1
+                const int odd = lane & 1;
+                const uint32_t sel = odd ? 0x3276u : 0x5410u;
+                uint16_t* d16 = a.out + (row_at + odd) * kLatDim + (ch - odd);
+#pragma unroll 1
+                for (int c = 0; c < R / 4; ++c) {
+                    const int c0 = (c >> 2) * 16;
+                    if (c0 >= nrows) break;
+                    float o[16];
+                    tc::tmem_ld16(tmO + (c & 3) * R + c0 + lane_tm, o);
+                    tc::tmem_wait_ld();
+                    uint16_t* d = d16 + c0 * kLatDim + (c & 3) * 128;
+                    float check = 0.f;
 #pragma unroll
-                            for (int b = 0; b < 2; ++b) {
-                                const float v0 = f0 == 0.f ? 0.f : o[b][i] * f0, v1 = f1 == 0.f ? 0.f : o[b][i + 1] * f1;
-                                if (!(fabsf(v0) < INFINITY)) bad[c0 >> 5] |= 1u << ((c0 + i) & 31);
-                                if (!(fabsf(v1) < INFINITY)) bad[c0 >> 5] |= 1u << ((c0 + i + 1) & 31);
-                                const float got = __shfl_xor_sync(0xffffffffu, odd ? v0 : v1, 1);
-                                const uint32_t w = odd ? f32x2_to_bf16x2_bits(got, v1) : f32x2_to_bf16x2_bits(v0, got);
-                                if (c0 + i + odd < nrows)
-                                    *reinterpret_cast<uint32_t*>(d16 + (c0 + i) * kLatDim + (b2 + b) * 128) = w;
-                            }
+                    for (int i = 0; i < 16; i += 2) {
+                        const float2 f = *reinterpret_cast<const float2*>(s_f + c0 + i);
+                        const float v0 = o[i] * f.x, v1 = o[i + 1] * f.y;
+                        if (a.K > 1) {
+                            check = fmaf(v0, 0.f, check);        // NaN once a value is none or infinite
+                            check = fmaf(v1, 0.f, check);
                         }
-                    } else {
+                        const uint32_t w = f32x2_to_bf16x2_bits(v0, v1);
+                        const uint32_t got = __shfl_xor_sync(0xffffffffu, w, 1);
+                        if (c0 + i + odd < nrows) *reinterpret_cast<uint32_t*>(d + i * kLatDim) = __byte_perm(w, got, sel);
+                    }
+                    if (!(check == 0.f)) {                       // some row of these: which
+                        uint32_t rows = 0u;
 #pragma unroll
-                        for (int i = 0; i < 16; ++i) {
-                            if (c0 + i < nrows) {
-                                d32[(c0 + i) * kLatDim + b2 * 128] = o[0][i];
-                                d32[(c0 + i) * kLatDim + b2 * 128 + 128] = o[1][i];
-                            }
-                        }
+                        for (int i = 0; i < 16; ++i) rows |= fabsf(o[i] * s_f[c0 + i]) < INFINITY ? 0u : 1u << i;
+                        bad[c0 >> 5] |= rows << (c0 & 31);
                     }
                 }
             }
@@ -503,7 +637,9 @@ kda_latent_decode_kernel(const __grid_constant__ LatMaps maps, const LatArgs a)
         // ---- both products; whichever has its inputs goes first ----
         // (the warp runs as one, so that addresses stay in uniform registers; one elected lane issues)
         constexpr uint32_t id_s = tc::idesc(64, R, tc::kFmtBF16, false, false);
-        constexpr uint32_t id_o = tc::idesc(128, R, tc::kFmtBF16, true, true);
+        constexpr uint32_t id_o = E4M3 ? tc::idesc8(128, R, tc::kFmtE4M3, tc::kFmtE5M2, true, true)
+                                       : tc::idesc(128, R, tc::kFmtBF16, true, true);
+        constexpr uint32_t id_c = tc::idesc8(64, R, tc::kFmtE4M3, tc::kFmtE4M3, false, false);
         // descriptors: constant high words, low words = address / 16 and the leading offset
         const uint64_t d0 = tc::sdesc(0, 16, 1024, tc::kSwizzle128B), dC = tc::sdesc(0, Sh::kSlabC, 1024, tc::kSwizzle128B);
         const uint32_t hi = static_cast<uint32_t>(d0 >> 32);
@@ -523,16 +659,24 @@ kda_latent_decode_kernel(const __grid_constant__ LatMaps maps, const LatArgs a)
             // read before P is written)
             if (go < gs && __all_sync(0xffffffffu, tc::mbar_test_wait(p_full, go & 1))) {
                 tc::fence_after_sync();
-                const uint32_t c = ct_lo + (go & 1) * (Sh::kStage >> 4);
+                const uint32_t c = ct_lo + go % NS * (Sh::kStage >> 4);
                 const uint32_t acc = to > sv.t0 ? 1u : 0u;
                 if (tc::elect_one()) {
 #pragma unroll
-                    for (uint32_t b = 0; b < 4; ++b)
+                    for (uint32_t b = 0; b < 4; ++b) {
+                        if constexpr (!E4M3) {
 #pragma unroll
-                        for (uint32_t k = 0; k < 4; ++k)
-                            tc::mma_f16_lo(tmO + b * R, c + ((b * 2u * Sh::kSlabC + k * 2048u) >> 4), hi,
-                                           p_lo + (k * 2048u >> 4), hi, id_o, k > 0 ? 1u : acc);
-                    tc::mma_commit(&empty[go & 1]);
+                            for (uint32_t k = 0; k < 4; ++k)
+                                tc::mma_f16_lo(tmO + b * R, c + ((b * 2u * Sh::kSlabC + k * 2048u) >> 4), hi,
+                                               p_lo + (k * 2048u >> 4), hi, id_o, k > 0 ? 1u : acc);
+                        } else {
+#pragma unroll
+                            for (uint32_t k = 0; k < 6; ++k)     // 2 steps of 32 tokens x 3 terms
+                                tc::mma_f8_lo(tmO + b * R, c + ((b * Sh::kSlabC + k / 3u * 4096u) >> 4), hi,
+                                              p_lo + ((k % 3u * kTile * 128u + k / 3u * 4096u) >> 4), hi, id_o, k > 0 ? 1u : acc);
+                        }
+                    }
+                    tc::mma_commit(&empty[go % NS]);
                 }
                 __syncwarp();
                 ++go;
@@ -543,14 +687,26 @@ kda_latent_decode_kernel(const __grid_constant__ LatMaps maps, const LatArgs a)
                 moved = true;
             }
             if (more_s && gs <= go + 1 && (ts > sw.t0 || __all_sync(0xffffffffu, tc::mbar_test_wait(q_full, qs & 1))) &&
-                __all_sync(0xffffffffu, tc::mbar_test_wait(&full[gs & 1], (gs >> 1) & 1))) {
+                __all_sync(0xffffffffu, tc::mbar_test_wait(&full[gs % NS], gs / NS & 1))) {
                 tc::fence_after_sync();
-                const uint32_t c = c_lo + (gs & 1) * (Sh::kStage >> 4), d = tmS + (gs & 1) * R;
+                const uint32_t c = c_lo + gs % NS * (Sh::kStage >> 4), d = tmS + (gs & 1) * Sh::kS;
                 if (tc::elect_one()) {
+                    if constexpr (!E4M3) {
 #pragma unroll
-                    for (uint32_t k = 0; k < 36; ++k)
-                        tc::mma_f16_lo(d, c + (((k >> 2) * Sh::kSlabC + (k & 3) * 32u) >> 4), hi,
-                                       q_lo + (((k >> 2) * Sh::kSlabQ + (k & 3) * 32u) >> 4), hi, id_s, k > 0 ? 1u : 0u);
+                        for (uint32_t k = 0; k < 36; ++k)
+                            tc::mma_f16_lo(d, c + (((k >> 2) * Sh::kSlabC + (k & 3) * 32u) >> 4), hi,
+                                           q_lo + (((k >> 2) * Sh::kSlabQ + (k & 3) * 32u) >> 4), hi, id_s, k > 0 ? 1u : 0u);
+                    } else {
+#pragma unroll
+                        for (uint32_t k = 0; k < 32; ++k)        // 16 steps of 32 codes x 2 terms of q
+                            tc::mma_f8_lo(d, c + (((k >> 3) * Sh::kSlabC + (k >> 1 & 3) * 32u) >> 4), hi,
+                                          q_lo + (((k & 1) * 4u * Sh::kSlabQ + (k >> 3) * Sh::kSlabQ + (k >> 1 & 3) * 32u) >> 4), hi,
+                                          id_c, k > 0 ? 1u : 0u);
+#pragma unroll
+                        for (uint32_t k = 0; k < 4; ++k)         // the position part, bf16
+                            tc::mma_f16_lo(d + R, c + ((4u * Sh::kSlabC + k * 32u) >> 4), hi,
+                                           q_lo + ((8u * Sh::kSlabQ + k * 32u) >> 4), hi, id_s, k > 0 ? 1u : 0u);
+                    }
                     tc::mma_commit(&s_full[gs & 1]);
                 }
                 __syncwarp();
@@ -572,10 +728,10 @@ kda_latent_decode_kernel(const __grid_constant__ LatMaps maps, const LatArgs a)
         }
         // nothing of this CTA's is left running when it returns its TMEM
         if (gs > 0 && !tc::mbar_wait_bounded(&s_full[(gs - 1) & 1], ((gs - 1) >> 1) & 1, kWaitLimitNs)) ok = false;
-        if (go > 0 && !tc::mbar_wait_bounded(&empty[(go - 1) & 1], ((go - 1) >> 1) & 1, kWaitLimitNs)) ok = false;
+        if (go > 0 && !tc::mbar_wait_bounded(&empty[(go - 1) % NS], (go - 1) / NS & 1, kWaitLimitNs)) ok = false;
         __syncwarp();
-    } else if constexpr (!E4M3) {
-        // ---- TMA: Q of each segment, C tiles in boxes of `box` rows (one page or a part of one) ----
+    } else {
+        // ---- TMA: C tiles in boxes of `box` rows (one page or a part of one); bf16: Q of each segment ----
         const int nbox = kTile / a.box;
         int g = 0, seg = 0;
         while (ok && sw.next(a.w)) {
@@ -587,32 +743,36 @@ kda_latent_decode_kernel(const __grid_constant__ LatMaps maps, const LatArgs a)
                 return page * a.ch.page_size + tok % a.ch.page_size;
             };
             int at = pages(sw.t0);
-            // Q is free once the last S product of the segment before has run
-            if (g > 0) ok = tc::mbar_wait_bounded(&s_full[(g - 1) & 1], ((g - 1) >> 1) & 1, kWaitLimitNs);
-            ok = __all_sync(0xffffffffu, ok);
-            if (!ok) break;
-            if (lane == 0) {
-                tc::mbar_arrive_expect_tx(q_full, 9u * Sh::kSlabQ);
-                const int qrow = static_cast<int>(static_cast<long long>(sw.n) * a.rows + row0);
-                for (int s = 0; s < 9; ++s)
-                    tc::tma_load_2d(tc::smem_u32(sQ) + s * Sh::kSlabQ, &maps.q, 64 * s, qrow, q_full);
+            if constexpr (!E4M3) {
+                // Q is free once the last S product of the segment before has run
+                if (g > 0) ok = tc::mbar_wait_bounded(&s_full[(g - 1) & 1], ((g - 1) >> 1) & 1, kWaitLimitNs);
+                ok = __all_sync(0xffffffffu, ok);
+                if (!ok) break;
+                if (lane == 0) tc::mbar_arrive_expect_tx(q_full, 9u * Sh::kSlabQ);
+                __syncwarp();
+                if (lane < 9)
+                    tc::tma_load_2d(tc::smem_u32(sQ) + lane * Sh::kSlabQ, &maps.q, 64 * lane,
+                                    static_cast<int>(static_cast<long long>(sw.n) * a.rows + row0), q_full);
+                ++seg;
             }
-            ++seg;
             for (int t = sw.t0; t < sw.t1; ++t, ++g) {
                 const int next = pages(t + 1);
-                if (g >= 2) ok = tc::mbar_wait_bounded(&empty[g & 1], ((g - 2) >> 1) & 1, kWaitLimitNs);
+                if (g >= NS) ok = tc::mbar_wait_bounded(&empty[g % NS], (g / NS - 1) & 1, kWaitLimitNs);
                 ok = __all_sync(0xffffffffu, ok);
                 if (!ok) break;
                 const int boxes = __popc(__ballot_sync(0xffffffffu, at >= 0));
-                const uint32_t dst = tc::smem_u32(sC) + (g & 1) * Sh::kStage;
+                const uint32_t dst = tc::smem_u32(sC) + g % NS * Sh::kStage;
                 // rows that softmax threads zeroed are overwritten by the copy: order the two
                 tc::fence_smem_to_async();
-                if (lane == 0) tc::mbar_arrive_expect_tx(&full[g & 1], static_cast<uint32_t>(boxes * a.box) * 9u * 128u);
+                if (lane == 0)
+                    tc::mbar_arrive_expect_tx(&full[g % NS], static_cast<uint32_t>(boxes * a.box) * (Sh::kSlabs * 128u + (E4M3 ? 16u : 0u)));
                 __syncwarp();
                 for (int b = 0; b < boxes; ++b) {
                     const int row = __shfl_sync(0xffffffffu, at, b);
-                    if (lane < 9)
-                        tc::tma_load_2d(dst + lane * Sh::kSlabC + b * a.box * 128, &maps.c, 64 * lane, row, &full[g & 1]);
+                    if (lane < Sh::kSlabs)
+                        tc::tma_load_2d(dst + lane * Sh::kSlabC + b * a.box * 128, &maps.c, (E4M3 ? 128 : 64) * lane, row, &full[g % NS]);
+                    if (E4M3 && lane == Sh::kSlabs)
+                        tc::tma_load_2d(dst + Sh::kSlabs * Sh::kSlabC + b * a.box * 16, &maps.s, kLatScaleAt, row, &full[g % NS]);
                 }
                 at = next;
             }
@@ -620,90 +780,8 @@ kda_latent_decode_kernel(const __grid_constant__ LatMaps maps, const LatArgs a)
         // copies in flight land before the CTA's shared memory is given back
         if (!ok) {
             if (seg > 0) tc::mbar_wait_bounded(q_full, (seg - 1) & 1, kWaitLimitNs);
-            for (int i = max(0, g - 2); i < g; ++i) tc::mbar_wait_bounded(&full[i & 1], (i >> 1) & 1, kWaitLimitNs);
+            for (int i = max(0, g - NS); i < g; ++i) tc::mbar_wait_bounded(&full[i % NS], i / NS & 1, kWaitLimitNs);
         }
-    } else {
-        // ---- e4m3: 8 warps load 8 tokens each, expand to bf16 (exact) and store the swizzled tile ----
-        const int pw = warp - 5;
-        const int sl = lane >> 2, half = sl & 1;
-        int g = 0, seg = 0;
-        while (ok && sw.next(a.w)) {
-            if (g > 0) ok = tc::mbar_wait_bounded(&s_full[(g - 1) & 1], ((g - 1) >> 1) & 1, kWaitLimitNs);
-            ok = __all_sync(0xffffffffu, ok);
-            if (!ok) break;
-            if (pw == 0 && lane == 0) {
-                tc::mbar_arrive_expect_tx(q_full, 9u * Sh::kSlabQ);
-                const int qrow = static_cast<int>(static_cast<long long>(sw.n) * a.rows + row0);
-                for (int s = 0; s < 9; ++s)
-                    tc::tma_load_2d(tc::smem_u32(sQ) + s * Sh::kSlabQ, &maps.q, 64 * s, qrow, q_full);
-            }
-            auto locate = [&](int t) {                          // lane i < 8: cache row of token 8 pw + i of tile t
-                const int tok = t * kTile + 8 * pw + lane;
-                if (t >= sw.t1 || lane >= 8 || tok >= sw.len) return -1;
-                const int page = a.ch.table[static_cast<size_t>(sw.n) * a.ch.max_pages + tok / a.ch.page_size];
-                if (page < 0 || page >= a.ch.num_pages) { set_status(a.status, kStatusIndex); return -1; }
-                return page * a.ch.page_size + tok % a.ch.page_size;
-            };
-            uint4 code[8], rope[2];
-            float scale = 0.f;
-            auto fetch = [&](int at) {
-                scale = at >= 0 ? *reinterpret_cast<const float*>(a.ch.rows + static_cast<size_t>(at) * kLatRowE4m3 + kLatScaleAt) : 0.f;
-#pragma unroll
-                for (int i = 0; i < 8; ++i) {
-                    const int r = __shfl_sync(0xffffffffu, at, i);
-                    code[i] = r >= 0 ? __ldg(reinterpret_cast<const uint4*>(a.ch.rows + static_cast<size_t>(r) * kLatRowE4m3) + lane)
-                                     : make_uint4(0, 0, 0, 0);
-                }
-#pragma unroll
-                for (int i = 0; i < 2; ++i) {                   // 4 tokens x 8 chunks of 16 bytes
-                    const int r = __shfl_sync(0xffffffffu, at, 4 * i + (lane >> 3));
-                    rope[i] = r >= 0 ? __ldg(reinterpret_cast<const uint4*>(a.ch.rows + static_cast<size_t>(r) * kLatRowE4m3 + kLatDim) + (lane & 7))
-                                     : make_uint4(0, 0, 0, 0);
-                }
-            };
-            int at = locate(sw.t0);
-            fetch(at);
-            at = locate(sw.t0 + 1);
-            for (int t = sw.t0; t < sw.t1; ++t, ++g) {
-                if (g >= 2) ok = tc::mbar_wait_bounded(&empty[g & 1], ((g - 2) >> 1) & 1, kWaitLimitNs);
-                ok = __all_sync(0xffffffffu, ok);
-                if (!ok) break;
-                uint8_t* c = sC + (g & 1) * Sh::kStage;
-#pragma unroll
-                for (int i = 0; i < 8; ++i) {
-                    const float s = __shfl_sync(0xffffffffu, scale, i);
-                    const uint32_t w[4] = {code[i].x, code[i].y, code[i].z, code[i].w};
-                    uint32_t v[8];
-#pragma unroll
-                    for (int k = 0; k < 4; ++k) {
-                        const float2 f = e4m3x2_to_f32(w[k]), h = e4m3x2_to_f32(w[k] >> 16);
-                        v[2 * k] = f32x2_to_bf16x2_bits(f.x * s, f.y * s);
-                        v[2 * k + 1] = f32x2_to_bf16x2_bits(h.x * s, h.y * s);
-                    }
-                    const uint4 lo = make_uint4(v[0], v[1], v[2], v[3]), hi = make_uint4(v[4], v[5], v[6], v[7]);
-                    // lane: chunks 2 (lane % 4) and + 1 of slab lane / 4; odd slabs store theirs in the
-                    // other order so that 8 lanes cover all banks
-                    const uint32_t row = 8 * pw + i, cb = 2 * (lane & 3);
-                    uint8_t* d = c + sl * Sh::kSlabC + row * 128;
-                    *reinterpret_cast<uint4*>(d + (((cb + half) ^ i) << 4)) = half ? hi : lo;
-                    *reinterpret_cast<uint4*>(d + (((cb + 1 - half) ^ i) << 4)) = half ? lo : hi;
-                }
-#pragma unroll
-                for (int i = 0; i < 2; ++i) {
-                    const uint32_t r = 4 * i + (lane >> 3);
-                    *reinterpret_cast<uint4*>(c + 8 * Sh::kSlabC + (8 * pw + r) * 128 + (((lane & 7) ^ r) << 4)) = rope[i];
-                }
-                tc::fence_smem_to_async();
-                __syncwarp();
-                if (lane == 0) tc::mbar_arrive(&full[g & 1]);
-                if (t + 1 < sw.t1) {
-                    fetch(at);
-                    at = locate(t + 2);
-                }
-            }
-            ++seg;
-        }
-        if (!ok && pw == 0 && seg > 0) tc::mbar_wait_bounded(q_full, (seg - 1) & 1, kWaitLimitNs);
     }
     if (!ok) set_status(a.status, kStatusTimeout);
     __syncwarp();
@@ -839,17 +917,17 @@ EncodeTiledFn encode_fn() {
     }
     return fn;
 }
-// [rows, 576] bf16, boxes of 64 columns x box_rows rows, 128-byte swizzle, zeros past the end
-bool map_576(CUtensorMap* m, const void* base, long long rows, int box_rows) {
+// [rows, cols], rows `pitch` bytes apart, boxes of box_cols x box_rows, zeros past the end
+bool map_2d(CUtensorMap* m, CUtensorMapDataType dt, const void* base, long long rows, int cols, int pitch, int box_cols,
+            int box_rows, CUtensorMapSwizzle swz) {
     EncodeTiledFn fn = encode_fn();
     if (!fn) return false;
-    const cuuint64_t dims[2] = {static_cast<cuuint64_t>(kLatQ), static_cast<cuuint64_t>(rows)};
-    const cuuint64_t strides[1] = {static_cast<cuuint64_t>(kLatQ) * 2};
-    const cuuint32_t box[2] = {64u, static_cast<cuuint32_t>(box_rows)};
+    const cuuint64_t dims[2] = {static_cast<cuuint64_t>(cols), static_cast<cuuint64_t>(rows)};
+    const cuuint64_t strides[1] = {static_cast<cuuint64_t>(pitch)};
+    const cuuint32_t box[2] = {static_cast<cuuint32_t>(box_cols), static_cast<cuuint32_t>(box_rows)};
     const cuuint32_t estr[2] = {1u, 1u};
-    return fn(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, const_cast<void*>(base), dims, strides, box, estr,
-              CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
-              CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+    return fn(m, dt, 2, const_cast<void*>(base), dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE, swz,
+              CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
 int sm_count() {
@@ -922,11 +1000,21 @@ int launch_latent_decode(const uint16_t* q, const void* cache, int e4m3, int num
     a.part_ml = a.part_o + static_cast<size_t>(a.w.G) * a.RT * 2 * R * kLatDim;
     a.status = status;
     LatMaps maps;
-    if (!map_576(&maps.q, q, static_cast<long long>(N) * rows, R)) return -3;
+    const CUtensorMapSwizzle swz = CU_TENSOR_MAP_SWIZZLE_128B;
+    const long long slots = static_cast<long long>(num_pages) * page_size;
+    if (!map_2d(&maps.q, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, q, static_cast<long long>(N) * rows, kLatQ, kLatQ * 2, 64, R, swz))
+        return -3;
     // (an empty cache holds no token to read; the map then only has to be valid)
     if (num_pages == 0) a.w.max_len = 0;
-    if (e4m3 || num_pages == 0) maps.c = maps.q;
-    else if (!map_576(&maps.c, cache, static_cast<long long>(num_pages) * page_size, a.box)) return -3;
+    maps.c = maps.s = maps.q;
+    if (num_pages > 0 && !e4m3 &&
+        !map_2d(&maps.c, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, cache, slots, kLatQ, kLatRowBf16, 64, a.box, swz))
+        return -3;
+    if (num_pages > 0 && e4m3 &&
+        (!map_2d(&maps.c, CU_TENSOR_MAP_DATA_TYPE_UINT8, cache, slots, kLatRowE4m3, kLatRowE4m3, 128, a.box, swz) ||
+         !map_2d(&maps.s, CU_TENSOR_MAP_DATA_TYPE_UINT8, cache, slots, kLatRowE4m3, kLatRowE4m3, 16, a.box,
+                 CU_TENSOR_MAP_SWIZZLE_NONE)))
+        return -3;
     if (e4m3) return R == 16 ? launch_decode_shape<16, true>(maps, a, stream)
                    : R == 32 ? launch_decode_shape<32, true>(maps, a, stream) : launch_decode_shape<64, true>(maps, a, stream);
     return R == 16 ? launch_decode_shape<16, false>(maps, a, stream)

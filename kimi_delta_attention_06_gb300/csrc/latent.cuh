@@ -25,6 +25,12 @@ __device__ __forceinline__ float lat_ex2(float x) {
     return y;
 }
 
+// Smallest e with x <= 448 * 2^e = 1.75 * 2^(8 + e), in [-117, 119]; 0 for x = 0 (x >= 0 by its bits).
+__device__ __forceinline__ int lat_scale_exponent(uint32_t bits) {
+    const int e = static_cast<int>(bits >> 23) - 127 - 8 + ((bits & 0x7fffffu) > 0x600000u ? 1 : 0);
+    return bits == 0 ? 0 : max(-117, min(119, e));
+}
+
 // Two e4m3 codes (low byte first) -> two floats.
 __device__ __forceinline__ float2 e4m3x2_to_f32(uint32_t w) {
     const __half2_raw h = __nv_cvt_fp8x2_to_halfraw2(static_cast<__nv_fp8x2_storage_t>(w & 0xFFFFu), __NV_E4M3);
@@ -33,6 +39,15 @@ __device__ __forceinline__ float2 e4m3x2_to_f32(uint32_t w) {
 // Two floats -> two e4m3 codes (low byte first), nearest even, magnitudes above 448 -> 448, NaN stays NaN.
 __device__ __forceinline__ uint32_t f32x2_to_e4m3x2(float lo, float hi) {
     return __nv_cvt_float2_to_fp8x2(make_float2(lo, hi), __NV_SATFINITE, __NV_E4M3);
+}
+
+// The same for e5m2 (an e5m2 value is the upper byte of an fp16 value).
+__device__ __forceinline__ float2 e5m2x2_to_f32(uint32_t w) {
+    const uint32_t h = ((w & 0xFFu) << 8) | ((w & 0xFF00u) << 16);
+    return __half22float2(*reinterpret_cast<const __half2*>(&h));
+}
+__device__ __forceinline__ uint32_t f32x2_to_e5m2x2(float lo, float hi) {
+    return __nv_cvt_float2_to_fp8x2(make_float2(lo, hi), __NV_SATFINITE, __NV_E5M2);
 }
 
 }  // namespace kda
