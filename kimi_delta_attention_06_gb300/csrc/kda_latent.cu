@@ -367,32 +367,28 @@ kda_latent_decode_kernel(const __grid_constant__ LatMaps maps, const LatArgs a)
                     for (int k = 0; k < 4; ++k) {
                         const int r = rb + 4 * k;
                         const uint32_t wv[8] = {w0[k].x, w0[k].y, w0[k].z, w0[k].w, w1[k].x, w1[k].y, w1[k].z, w1[k].w};
-                        float v[16], top = 0.f;
+                        uint32_t top2 = 0u;                     // largest magnitudes by their bits, two at a time
 #pragma unroll
-                        for (int i = 0; i < 8; ++i) {
-                            const float2 f = bf16x2_bits_to_f32(wv[i]);
-                            v[2 * i] = f.x; v[2 * i + 1] = f.y;
-                        }
-#pragma unroll
-                        for (int i = 0; i < 16; ++i) {          // an infinity has no code: NaN, as its scores would be
-                            const bool fin = fabsf(v[i]) < INFINITY;
-                            top = fmaxf(top, fin ? fabsf(v[i]) : 0.f);
-                            v[i] = fin ? v[i] : __int_as_float(0x7fffffff);
-                        }
-                        top = __uint_as_float(__reduce_max_sync(0xffffffffu, __float_as_uint(top)));
-                        const int e = lat_scale_exponent(__float_as_uint(top));
+                        for (int i = 0; i < 8; ++i) top2 = __vmaxu2(top2, wv[i] & 0x7fff7fffu);
+                        uint32_t top = __reduce_max_sync(0xffffffffu, max(top2 & 0xffffu, top2 >> 16));
+                        uint32_t none = 0u;                     // a row with a NaN or an infinity: its scores are NaN
+                        if (top >= 0x7f80u) { none = 0x7f7f7f7fu; top = 0u; }
+                        const int e = lat_scale_exponent(top << 16);
                         const float inv = __uint_as_float(static_cast<uint32_t>(127 - e) << 23);
                         uint32_t t1[4], t2[4];
 #pragma unroll
                         for (int i = 0; i < 4; ++i) {
-                            t1[i] = t2[i] = 0u;
+                            t1[i] = none;
+                            t2[i] = 0u;
 #pragma unroll
-                            for (int h = 0; h < 2; ++h) {
-                                const float x0 = v[4 * i + 2 * h] * inv, x1 = v[4 * i + 2 * h + 1] * inv;
-                                const uint32_t c = f32x2_to_e4m3x2(x0, x1);
-                                const float2 b = e4m3x2_to_f32(c);
-                                t1[i] |= c << (16 * h);
-                                t2[i] |= f32x2_to_e4m3x2(x0 - b.x, x1 - b.y) << (16 * h);
+                            for (int h = 0; h < 2; ++h) {       // (fp16 holds q / 2^k: 8 bits, at most 448)
+                                const float2 f = bf16x2_bits_to_f32(wv[2 * i + h]);
+                                const uint32_t x = f32x2_to_f16x2(f.x * inv, f.y * inv);
+                                const uint32_t c = f16x2_to_e4m3x2(x);
+                                if (!none) {
+                                    t1[i] |= c << (16 * h);
+                                    t2[i] |= f16x2_to_e4m3x2(f16x2_sub(x, e4m3x2_to_f16x2(c))) << (16 * h);
+                                }
                             }
                         }
                         uint8_t* d = sQ + (lane >> 3) * Sh::kSlabQ + r * 128 + (((lane & 7) ^ (r & 7)) << 4);
@@ -407,7 +403,7 @@ kda_latent_decode_kernel(const __grid_constant__ LatMaps maps, const LatArgs a)
                 tc::named_sync(kBarSoft, Sh::kSoft);             // s_a is read by all
             }
             for (int t = sw.t0; t < sw.t1; ++t, ++g) {
-                ok = __all_sync(0xffffffffu, tc::mbar_wait_bounded(&s_full[g & 1], (g >> 1) & 1, kWaitLimitNs));
+                ok = __all_sync(0xffffffffu, ok && tc::mbar_wait_bounded(&s_full[g & 1], (g >> 1) & 1, kWaitLimitNs));
                 float x[R / 2];
                 float s0 = 1.f, s1 = 1.f, e0 = 0.f, e1 = 0.f;   // e4m3: scales of the thread's two tokens, their exponents
                 if (ok) {
@@ -442,7 +438,7 @@ kda_latent_decode_kernel(const __grid_constant__ LatMaps maps, const LatArgs a)
                     }
                     // rows past the end of the sequence hold anything: they enter the second product as zeros
                     const int valid = sw.len - t * kTile;
-                    if (valid < kTile) {
+                    if (ok && valid < kTile) {
                         uint8_t* c = sC + g % NS * Sh::kStage;
                         constexpr int W = E4M3 ? 4 : 8;         // slabs of latents
                         for (int i = tid; i < W * (kTile - valid) * 8; i += Sh::kSoft) {
@@ -455,12 +451,13 @@ kda_latent_decode_kernel(const __grid_constant__ LatMaps maps, const LatArgs a)
                         }
                     }
                 }
-                // the previous tile's product has read P and is in O
-                if (ok && g > 0) ok = tc::mbar_wait_bounded(&empty[(g - 1) % NS], (g - 1) / NS & 1, kWaitLimitNs);
                 bool grow = !ok;
 #pragma unroll
                 for (int i = 0; i < R / 2; ++i) grow |= x[i] > m[2 * (i >> 2) + (i & 1)] + kMost<E4M3>;
+                bool waited = g == 0;                           // for the previous tile's product: it has read P and is in O
                 if (!tc::named_sync_and(kBarSoft, Sh::kSoft, !grow)) {
+                    if (ok && !waited) ok = tc::mbar_wait_bounded(&empty[(g - 1) % NS], (g - 1) / NS & 1, kWaitLimitNs);
+                    waited = true;
                     ok = tc::named_sync_and(kBarSoft, Sh::kSoft, ok);
                     if (!ok) break;
                     tc::fence_after_sync();
@@ -504,9 +501,11 @@ kda_latent_decode_kernel(const __grid_constant__ LatMaps maps, const LatArgs a)
                         tc::tmem_wait_st();
                     }
                 }
-                // P = exp2(x - m), rounded for the product (see above); the sums keep fp32
+                // P = exp2(x - m), rounded for the product (see above); the sums keep fp32.  It is made in
+                // registers while the previous tile's product still reads P
                 const int tr = 16 * warp + tq;
                 const float r0 = 1.f / s0, r1 = 1.f / s1;       // (powers of two)
+                uint32_t pk[E4M3 ? 3 * (R / 8) : R / 4];
 #pragma unroll
                 for (int b = 0; b < R / 8; ++b) {
                     const float m0 = m[2 * b] == -INFINITY ? 0.f : m[2 * b], m1 = m[2 * b + 1] == -INFINITY ? 0.f : m[2 * b + 1];
@@ -515,24 +514,40 @@ kda_latent_decode_kernel(const __grid_constant__ LatMaps maps, const LatArgs a)
                     if constexpr (!E4M3) {
                         l[2 * b] += p0 + p2;
                         l[2 * b + 1] += p1 + p3;
-                        const uint32_t off = tc::sw128_off16(tr, 8 * b + rq, kTile);
-                        *reinterpret_cast<uint32_t*>(sP + off) = f32x2_to_bf16x2_bits(p0, p1);
-                        *reinterpret_cast<uint32_t*>(sP + off + 8 * 128) = f32x2_to_bf16x2_bits(p2, p3);   // token + 8: same swizzle
+                        pk[2 * b] = f32x2_to_bf16x2_bits(p0, p1);
+                        pk[2 * b + 1] = f32x2_to_bf16x2_bits(p2, p3);
                     } else {
                         l[2 * b] += fmaf(p0, r0, p2 * r1);
                         l[2 * b + 1] += fmaf(p1, r0, p3 * r1);
-                        const uint32_t n = 8 * b + rq, off = tr * 128 + (((n >> 4) ^ (tr & 7)) << 4) + (n & 15);
-                        float q0 = p0, q1 = p1, q2 = p2, q3 = p3;
+                        uint32_t u = f32x2_to_f16x2(p0, p1), v = f32x2_to_f16x2(p2, p3);
 #pragma unroll
                         for (int k = 0; k < 3; ++k) {           // three terms, each the rounding of what is left
-                            const uint32_t u = f32x2_to_e5m2x2(q0, q1), v = f32x2_to_e5m2x2(q2, q3);
-                            uint8_t* d = sP + k * kTile * 128 + off;
-                            *reinterpret_cast<uint16_t*>(d) = static_cast<uint16_t>(u);
-                            *reinterpret_cast<uint16_t*>(d + 8 * 128) = static_cast<uint16_t>(v);
+                            const uint32_t cu = f16x2_to_e5m2x2(u), cv = f16x2_to_e5m2x2(v);
+                            pk[3 * b + k] = cu | (cv << 16);
                             if (k < 2) {
-                                const float2 fu = e5m2x2_to_f32(u), fv = e5m2x2_to_f32(v);
-                                q0 -= fu.x; q1 -= fu.y; q2 -= fv.x; q3 -= fv.y;
+                                u = f16x2_sub(u, e5m2x2_to_f16x2(cu));
+                                v = f16x2_sub(v, e5m2x2_to_f16x2(cv));
                             }
+                        }
+                    }
+                }
+                // (a wait that ran out is agreed on at the next vote, so that no warp leaves the others there)
+                if (ok && !waited) ok = tc::mbar_wait_bounded(&empty[(g - 1) % NS], (g - 1) / NS & 1, kWaitLimitNs);
+                ok = __all_sync(0xffffffffu, ok);
+                if (!ok) continue;
+#pragma unroll
+                for (int b = 0; b < R / 8; ++b) {
+                    if constexpr (!E4M3) {
+                        const uint32_t off = tc::sw128_off16(tr, 8 * b + rq, kTile);
+                        *reinterpret_cast<uint32_t*>(sP + off) = pk[2 * b];
+                        *reinterpret_cast<uint32_t*>(sP + off + 8 * 128) = pk[2 * b + 1];    // token + 8: same swizzle
+                    } else {
+                        const uint32_t n = 8 * b + rq, off = tr * 128 + (((n >> 4) ^ (tr & 7)) << 4) + (n & 15);
+#pragma unroll
+                        for (int k = 0; k < 3; ++k) {
+                            uint8_t* d = sP + k * kTile * 128 + off;
+                            *reinterpret_cast<uint16_t*>(d) = static_cast<uint16_t>(pk[3 * b + k]);
+                            *reinterpret_cast<uint16_t*>(d + 8 * 128) = static_cast<uint16_t>(pk[3 * b + k] >> 16);
                         }
                     }
                 }
@@ -540,9 +555,8 @@ kda_latent_decode_kernel(const __grid_constant__ LatMaps maps, const LatArgs a)
                 tc::fence_before_sync();
                 tc::mbar_arrive(p_full);
             }
-            if (!ok) break;
             // ---- epilogue of the segment: O^T is complete once the last product is ----
-            ok = tc::mbar_wait_bounded(&empty[(g - 1) % NS], (g - 1) / NS & 1, kWaitLimitNs);
+            ok = ok && tc::mbar_wait_bounded(&empty[(g - 1) % NS], (g - 1) / NS & 1, kWaitLimitNs);
             ok = tc::named_sync_and(kBarSoft, Sh::kSoft, ok);
             if (!ok) break;
             tc::fence_after_sync();

@@ -41,13 +41,33 @@ __device__ __forceinline__ uint32_t f32x2_to_e4m3x2(float lo, float hi) {
     return __nv_cvt_float2_to_fp8x2(make_float2(lo, hi), __NV_SATFINITE, __NV_E4M3);
 }
 
-// The same for e5m2 (an e5m2 value is the upper byte of an fp16 value).
-__device__ __forceinline__ float2 e5m2x2_to_f32(uint32_t w) {
-    const uint32_t h = ((w & 0xFFu) << 8) | ((w & 0xFF00u) << 16);
-    return __half22float2(*reinterpret_cast<const __half2*>(&h));
+// fp16 pairs (packed bits) <-> pairs of 8-bit codes, low byte first; nearest even, saturating, NaN stays
+// NaN.  An e5m2 value is the upper byte of an fp16 value.
+__device__ __forceinline__ uint32_t f16x2_to_e4m3x2(uint32_t h) {
+    __half2_raw r;
+    r.x = static_cast<unsigned short>(h & 0xFFFFu);
+    r.y = static_cast<unsigned short>(h >> 16);
+    return __nv_cvt_halfraw2_to_fp8x2(r, __NV_SATFINITE, __NV_E4M3);
 }
-__device__ __forceinline__ uint32_t f32x2_to_e5m2x2(float lo, float hi) {
-    return __nv_cvt_float2_to_fp8x2(make_float2(lo, hi), __NV_SATFINITE, __NV_E5M2);
+__device__ __forceinline__ uint32_t f16x2_to_e5m2x2(uint32_t h) {
+    __half2_raw r;
+    r.x = static_cast<unsigned short>(h & 0xFFFFu);
+    r.y = static_cast<unsigned short>(h >> 16);
+    return __nv_cvt_halfraw2_to_fp8x2(r, __NV_SATFINITE, __NV_E5M2);
+}
+__device__ __forceinline__ uint32_t e4m3x2_to_f16x2(uint32_t c) {
+    const __half2_raw r = __nv_cvt_fp8x2_to_halfraw2(static_cast<__nv_fp8x2_storage_t>(c & 0xFFFFu), __NV_E4M3);
+    return static_cast<uint32_t>(r.x) | (static_cast<uint32_t>(r.y) << 16);
+}
+__device__ __forceinline__ uint32_t e5m2x2_to_f16x2(uint32_t c) { return __byte_perm(c, 0u, 0x1404); }
+__device__ __forceinline__ uint32_t f16x2_sub(uint32_t a, uint32_t b) {
+    uint32_t d;
+    asm("sub.rn.f16x2 %0, %1, %2;" : "=r"(d) : "r"(a), "r"(b));
+    return d;
+}
+__device__ __forceinline__ uint32_t f32x2_to_f16x2(float lo, float hi) {
+    const __half2 h = __floats2half2_rn(lo, hi);
+    return *reinterpret_cast<const uint32_t*>(&h);
 }
 
 }  // namespace kda
