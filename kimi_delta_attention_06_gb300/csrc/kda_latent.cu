@@ -18,7 +18,7 @@
 //     belongs to its latent only: x = scale * (2^k s S_c + S_r).
 //   - s moves from the latents to the weights: O = sum (p s) codes.  p s is the sum of three e5m2
 //     values (3 bits each: a relative 2^-9, less than a rounding to bf16), scaled so that the
-//     largest lies near 2^12, which leaves 28 binades below it.
+//     largest lies in 2^10 .. 2^15, which leaves 26 binades or more below it.
 // Expanding the tile to bf16 instead (exact too) took 4800 clocks a tile of 64 rows: loads into
 // registers hold too little in flight beside 227 KB of shared memory, and the tile is written and
 // read once more.
@@ -252,9 +252,9 @@ struct LatShape {
 static_assert(LatShape<64, false>::kBytes <= 232448 && LatShape<64, true>::kBytes <= 232448, "227 KB of shared memory");
 
 // A row's weights are exp2(x - m).  m follows the row's maximum M lazily: bf16, m <= M <= m + 8 (the
-// sums have the range for it); e4m3, m + 12 <= M <= m + 15, so that the weights times s fill e5m2's
+// sums have the range for it); e4m3, m + 10 <= M <= m + 15, so that the weights times s fill e5m2's
 // range and stay below its 57344.
-template <bool E4M3> constexpr float kAbove = E4M3 ? 12.f : 0.f;
+template <bool E4M3> constexpr float kAbove = E4M3 ? 10.f : 0.f;
 template <bool E4M3> constexpr float kMost = E4M3 ? 15.f : 8.f;
 constexpr uint32_t kBarSoft = 1;                 // named barrier of the softmax warps
 
@@ -371,25 +371,23 @@ kda_latent_decode_kernel(const __grid_constant__ LatMaps maps, const LatArgs a)
 #pragma unroll
                         for (int i = 0; i < 8; ++i) top2 = __vmaxu2(top2, wv[i] & 0x7fff7fffu);
                         uint32_t top = __reduce_max_sync(0xffffffffu, max(top2 & 0xffffu, top2 >> 16));
-                        uint32_t none = 0u;                     // a row with a NaN or an infinity: its scores are NaN
-                        if (top >= 0x7f80u) { none = 0x7f7f7f7fu; top = 0u; }
-                        const int e = lat_scale_exponent(top << 16);
-                        const float inv = __uint_as_float(static_cast<uint32_t>(127 - e) << 23);
+                        // (a row with a NaN or an infinity gets codes of NaN, as its scores are none)
+                        const bool none = top >= 0x7f80u;
+                        const int e = none ? 0 : lat_scale_exponent(top << 16);
+                        const float inv = __uint_as_float(static_cast<uint32_t>(127 - 8 - e) << 23);
                         uint32_t t1[4], t2[4];
 #pragma unroll
                         for (int i = 0; i < 4; ++i) {
-                            t1[i] = none;
-                            t2[i] = 0u;
+                            uint32_t c1[2], c2[2];
 #pragma unroll
-                            for (int h = 0; h < 2; ++h) {       // (fp16 holds q / 2^k: 8 bits, at most 448)
+                            for (int h = 0; h < 2; ++h) {       // x = q / 2^k: 8 bits, at most 448; fp16 holds x / 2^8
                                 const float2 f = bf16x2_bits_to_f32(wv[2 * i + h]);
-                                const uint32_t x = f32x2_to_f16x2(f.x * inv, f.y * inv);
-                                const uint32_t c = f16x2_to_e4m3x2(x);
-                                if (!none) {
-                                    t1[i] |= c << (16 * h);
-                                    t2[i] |= f16x2_to_e4m3x2(f16x2_sub(x, e4m3x2_to_f16x2(c))) << (16 * h);
-                                }
+                                const uint32_t x = f32x2_to_f16x2(f.x * inv, f.y * inv), y = f16x2_round_e4m3(x);
+                                c1[h] = e4m3_codes(y);
+                                c2[h] = e4m3_codes(f16x2_round_e4m3(f16x2_sub(x, y)));
                             }
+                            t1[i] = none ? 0x7f7f7f7fu : __byte_perm(c1[0], c1[1], 0x6420);
+                            t2[i] = none ? 0u : __byte_perm(c2[0], c2[1], 0x6420);
                         }
                         uint8_t* d = sQ + (lane >> 3) * Sh::kSlabQ + r * 128 + (((lane & 7) ^ (r & 7)) << 4);
                         *reinterpret_cast<uint4*>(d) = make_uint4(t1[0], t1[1], t1[2], t1[3]);
@@ -522,12 +520,10 @@ kda_latent_decode_kernel(const __grid_constant__ LatMaps maps, const LatArgs a)
                         uint32_t u = f32x2_to_f16x2(p0, p1), v = f32x2_to_f16x2(p2, p3);
 #pragma unroll
                         for (int k = 0; k < 3; ++k) {           // three terms, each the rounding of what is left
-                            const uint32_t cu = f16x2_to_e5m2x2(u), cv = f16x2_to_e5m2x2(v);
-                            pk[3 * b + k] = cu | (cv << 16);
-                            if (k < 2) {
-                                u = f16x2_sub(u, e5m2x2_to_f16x2(cu));
-                                v = f16x2_sub(v, e5m2x2_to_f16x2(cv));
-                            }
+                            const uint32_t ru = f16x2_round_e5m2(u), rv = f16x2_round_e5m2(v);
+                            pk[3 * b + k] = __byte_perm(ru, rv, 0x7531);
+                            u = f16x2_sub(u, ru);
+                            v = f16x2_sub(v, rv);
                         }
                     }
                 }
@@ -916,6 +912,98 @@ kda_latent_combine_kernel(const LatArgs a, int Q, int NG)
     }
 }
 
+// The same for many rows of few partials: a warp a row, 16 channels a lane, no block-wide step.
+template <int R, bool E4M3>
+__global__ void __launch_bounds__(128)
+kda_latent_combine_rows_kernel(const LatArgs a)
+{
+    const int lane = threadIdx.x & 31;
+    const long long at = static_cast<long long>(blockIdx.x) * 4 + (threadIdx.x >> 5);     // row n * rows + row
+    const int n = static_cast<int>(min(at, static_cast<long long>(a.w.N) * a.rows - 1) / a.rows);
+    const int row = static_cast<int>(at - static_cast<long long>(n) * a.rows);
+    long long T = 0, before = 0;
+    int len = 0;
+    for (int i0 = 0; i0 < a.w.N; i0 += 32) {
+        const int i = i0 + lane, v = i < a.w.N ? lat_len(a.w, i) : 0;
+        if (i == n && row == 0 && a.w.seq_lens[i] != v) set_status(a.status, kStatusIndex);   // out of range: counted as 0
+        T += lat_tiles(v);
+        if (i < n) before += lat_tiles(v);
+        if (n >= i0 && n < i0 + 32) len = __shfl_sync(0xffffffffu, v, n - i0);
+    }
+#pragma unroll
+    for (int off = 16; off > 0; off >>= 1) {
+        T += __shfl_xor_sync(0xffffffffu, T, off);
+        before += __shfl_xor_sync(0xffffffffu, before, off);
+    }
+    const int tiles = lat_tiles(len);
+    int c0 = 0, parts = 1, late = 0;
+    if (tiles > 0) {
+        const long long runs = lat_runs(T, a.w.G);
+        c0 = static_cast<int>(run_of(T, runs, before));
+        parts = static_cast<int>(run_of(T, runs, before + tiles - 1)) - c0 + 1;
+        late = run_begin(T, runs, c0) < before ? 1 : 0;
+    }
+    asm volatile("griddepcontrol.wait;" ::: "memory");          // every block: this grid ends after the one before it
+    if (row >= a.rows) return;                                   // (past the last row)
+    uint2* out = reinterpret_cast<uint2*>(a.out + at * kLatDim) + lane;
+    if (tiles == 0) {
+#pragma unroll
+        for (int k = 0; k < 4; ++k) out[32 * k] = make_uint2(0u, 0u);
+        if (lane == 0 && a.lse) a.lse[at] = -INFINITY;
+        return;
+    }
+    if (parts == 1) return;                                      // its CTA finished it
+    const size_t stride = static_cast<size_t>(a.RT) * 2 * R;
+    const size_t base = (static_cast<size_t>(c0) * a.RT + row / R) * 2 * R + row % R;
+    float M = -INFINITY, L = 0.f;
+    float4 acc[4];
+#pragma unroll
+    for (int k = 0; k < 4; ++k) acc[k] = make_float4(0.f, 0.f, 0.f, 0.f);
+    for (int i0 = 0; i0 < parts; i0 += 32) {                     // 32 partials at a time, one pass
+        const size_t mine = base + (i0 + lane) * stride + (i0 + lane == 0 && late ? R : 0);
+        const float2 ml = i0 + lane < parts ? *reinterpret_cast<const float2*>(a.part_ml + mine * 2) : make_float2(-INFINITY, 0.f);
+        float mx = ml.x;
+#pragma unroll
+        for (int off = 16; off > 0; off >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, off));
+        const float Mn = fmaxf(M, mx), f = Mn == M ? 1.f : lat_ex2(M - Mn);
+        M = Mn;
+        const bool none = ml.x == -INFINITY && ml.y == 0.f;      // saw nothing there
+        const float w = none ? -1.f : ml.x == M ? 1.f : lat_ex2(ml.x - M);
+        float sum = none ? 0.f : w * ml.y;
+#pragma unroll
+        for (int off = 16; off > 0; off >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, off);
+        L = L * f + sum;
+#pragma unroll
+        for (int k = 0; k < 4; ++k) { acc[k].x *= f; acc[k].y *= f; acc[k].z *= f; acc[k].w *= f; }
+        const int some = min(32, parts - i0);
+#pragma unroll 2
+        for (int i = 0; i < some; ++i) {
+            const float wi = __shfl_sync(0xffffffffu, w, i);
+            const size_t sl = base + (i0 + i) * stride + (i0 + i == 0 && late ? R : 0);
+            const float4* o = reinterpret_cast<const float4*>(a.part_o + sl * kLatDim) + lane;
+            float4 v[4];
+#pragma unroll
+            for (int k = 0; k < 4; ++k) v[k] = o[32 * k];
+            if (wi >= 0.f)
+#pragma unroll
+                for (int k = 0; k < 4; ++k) {
+                    acc[k].x += wi * v[k].x; acc[k].y += wi * v[k].y; acc[k].z += wi * v[k].z; acc[k].w += wi * v[k].w;
+                }
+        }
+    }
+    const float inv = L == 0.f ? 0.f : 1.f / L;
+    bool bad = false;
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+        const float v0 = acc[k].x * inv, v1 = acc[k].y * inv, v2 = acc[k].z * inv, v3 = acc[k].w * inv;
+        bad = bad || !(fabsf(v0) < INFINITY && fabsf(v1) < INFINITY && fabsf(v2) < INFINITY && fabsf(v3) < INFINITY);
+        out[32 * k] = make_uint2(f32x2_to_bf16x2_bits(v0, v1), f32x2_to_bf16x2_bits(v2, v3));
+    }
+    if (lane == 0 && a.lse) a.lse[at] = (M + log2f(L)) * 0.69314718055994531f;
+    const int j = row / a.H;
+    if (j < a.K - 1 && __any_sync(0xffffffffu, bad)) latent_row_again<E4M3>(a, n, row, len - (a.K - 1 - j));
+}
+
 namespace {
 using EncodeTiledFn = CUresult (*)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*, const cuuint64_t*,
                                    const cuuint64_t*, const cuuint32_t*, const cuuint32_t*, CUtensorMapInterleave,
@@ -961,19 +1049,23 @@ int launch_decode_shape(const LatMaps& maps, const LatArgs& a, cudaStream_t stre
     kda_latent_decode_kernel<R, E4M3><<<static_cast<unsigned>(a.w.G) * a.RT, Sh::kThreads, Sh::kBytes, stream>>>(maps, a);
     if (cudaGetLastError() != cudaSuccess) return -3;
     cudaLaunchConfig_t cfg = {};
-    // a row's partials number about G / N + 1: one group of threads for every 8 of them; a
-    // row's channels over 4 blocks where rows are too few to fill the device
+    // a row's partials number about G / N + 1: few of them (many sequences), a warp a row; else
+    // groups of threads with 8 of them each, a row's channels over 4 blocks where rows are too few
+    // to fill the device
+    const int about = a.w.G / a.w.N + 1;
+    const bool by_warp = about <= 16;
     const int Q = a.K == 1 && static_cast<long long>(a.w.N) * a.rows < 256 ? 4 : 1;
     int NG = Q;
-    while (NG < 4 * Q && NG * 8 < Q * (a.w.G / a.w.N + 1)) NG *= 2;
-    cfg.gridDim = dim3(static_cast<unsigned>(a.w.N) * a.rows * Q);
-    cfg.blockDim = dim3(128 / Q * NG);
+    while (NG < 4 * Q && NG * 8 < Q * about) NG *= 2;
+    cfg.gridDim = dim3(by_warp ? (static_cast<unsigned>(a.w.N) * a.rows + 3) / 4 : static_cast<unsigned>(a.w.N) * a.rows * Q);
+    cfg.blockDim = dim3(by_warp ? 128 : 128 / Q * NG);
     cfg.stream = stream;
     cudaLaunchAttribute at[1];
     at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
     at[0].val.programmaticStreamSerializationAllowed = 1;
     cfg.attrs = at;
     cfg.numAttrs = 1;
+    if (by_warp) return cudaLaunchKernelEx(&cfg, kda_latent_combine_rows_kernel<R, E4M3>, a) == cudaSuccess ? 0 : -3;
     return cudaLaunchKernelEx(&cfg, kda_latent_combine_kernel<R, E4M3>, a, Q, NG) == cudaSuccess ? 0 : -3;
 }
 
