@@ -71,6 +71,14 @@ __device__ __forceinline__ float2 fmul2(float2 a, float2 b) {
     return *reinterpret_cast<const float2*>(&d);
 }
 
+__device__ __forceinline__ float2 fadd2(float2 a, float2 b) {
+    uint64_t d;
+    asm("add.rn.f32x2 %0, %1, %2;"
+        : "=l"(d)
+        : "l"(*reinterpret_cast<const uint64_t*>(&a)), "l"(*reinterpret_cast<const uint64_t*>(&b)));
+    return *reinterpret_cast<const float2*>(&d);
+}
+
 // Raise a kernel's dynamic shared-memory limit on the current device, once per device
 // (the attribute belongs to the device's copy of the kernel).  `done` holds one flag per
 // device ordinal; setting the attribute twice is harmless, so no lock is needed.

@@ -100,8 +100,8 @@ kda_expanded_kernel(const __grid_constant__ ExpMaps maps, const ExpArgs a)
 {
     extern __shared__ __align__(1024) uint8_t smem[];
     uint64_t* bars = reinterpret_cast<uint64_t*>(smem + oExpBar);
-    uint64_t *full = bars, *kfree = bars + 8, *vfree = bars + 10, *s_full = bars + 12, *p_full = bars + 14, *q_full = bars + 16;
-    uint32_t* s_tmem = reinterpret_cast<uint32_t*>(bars + 18);
+    uint64_t *full = bars, *kfree = bars + 8, *vfree = bars + 10, *s_full = bars + 12, *p_full = bars + 14, *q_full = bars + 18;
+    uint32_t* s_tmem = reinterpret_cast<uint32_t*>(bars + 20);
 
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const int h = blockIdx.y;
@@ -150,7 +150,8 @@ kda_expanded_kernel(const __grid_constant__ ExpMaps maps, const ExpArgs a)
             tc::mbar_init(&kfree[i], 1);
             tc::mbar_init(&vfree[i], 1);
             tc::mbar_init(&s_full[i], 1);
-            tc::mbar_init(&p_full[i], kExpTile);
+            tc::mbar_init(&p_full[2 * i], kExpTile);
+            tc::mbar_init(&p_full[2 * i + 1], kExpTile);
             tc::mbar_init(&q_full[i], 1);
         }
         tc::mbar_fence_init();
@@ -178,7 +179,8 @@ kda_expanded_kernel(const __grid_constant__ ExpMaps maps, const ExpArgs a)
             for (int c = 0; c < 4; ++c) tc::tmem_ld32x(tS + 32u * c, u[c]);
             tc::tmem_wait_ld();
             const int vis = see - j * kExpTile;                  // columns of this tile that the row sees
-            float mx = -INFINITY;
+            // mx = the largest score; p = exp2(u * by - ref) below
+            float mx = -INFINITY, by = a.scale_log2;
             if (__any_sync(0xffffffffu, vis < kExpTile)) {
 #pragma unroll
                 for (int c = 0; c < 4; ++c)
@@ -188,15 +190,20 @@ kda_expanded_kernel(const __grid_constant__ ExpMaps maps, const ExpArgs a)
                         u[c][i] = __float_as_uint(x);
                         mx = fmaxf(mx, x);
                     }
-            } else {
+                by = 1.f;
+            } else if (a.scale_log2 >= 0.f) {
 #pragma unroll
                 for (int c = 0; c < 4; ++c)
 #pragma unroll
-                    for (int i = 0; i < 32; ++i) {
-                        const float x = __uint_as_float(u[c][i]) * a.scale_log2;
-                        u[c][i] = __float_as_uint(x);
-                        mx = fmaxf(mx, x);
-                    }
+                    for (int i = 0; i < 32; i += 2) mx = fmaxf(mx, fmaxf(__uint_as_float(u[c][i]), __uint_as_float(u[c][i + 1])));
+                mx *= by;
+            } else {
+                mx = INFINITY;
+#pragma unroll
+                for (int c = 0; c < 4; ++c)
+#pragma unroll
+                    for (int i = 0; i < 32; i += 2) mx = fminf(mx, fminf(__uint_as_float(u[c][i]), __uint_as_float(u[c][i + 1])));
+                mx *= by;
             }
             if (__any_sync(0xffffffffu, mx > m + kExpTau)) {     // (the product before this tile's scores is in O)
                 const float mn = fmaxf(m, mx);
@@ -215,24 +222,26 @@ kda_expanded_kernel(const __grid_constant__ ExpMaps maps, const ExpArgs a)
                     }
                 }
             }
-            const float ref = m == -INFINITY ? 0.f : m;
-            float s0 = 0.f, s1 = 0.f;
+            const float2 neg = make_float2(m == -INFINITY ? 0.f : -m, m == -INFINITY ? 0.f : -m), by2 = make_float2(by, by);
+            float2 sum = make_float2(0.f, 0.f);
             uint32_t pk[32];
 #pragma unroll
             for (int c = 0; c < 4; ++c) {
 #pragma unroll
                 for (int i = 0; i < 16; ++i) {
-                    const float p0 = lat_ex2(__uint_as_float(u[c][2 * i]) - ref), p1 = lat_ex2(__uint_as_float(u[c][2 * i + 1]) - ref);
-                    s0 += p0;
-                    s1 += p1;
-                    pk[(c & 1) * 16 + i] = f32x2_to_bf16x2_bits(p0, p1);   // the sums keep fp32; the product takes bf16
+                    const float2 x = ffma2(make_float2(__uint_as_float(u[c][2 * i]), __uint_as_float(u[c][2 * i + 1])), by2, neg);
+                    const float2 p = make_float2(lat_ex2(x.x), lat_ex2(x.y));
+                    sum = fadd2(sum, p);
+                    pk[(c & 1) * 16 + i] = f32x2_to_bf16x2_bits(p.x, p.y);   // the sums keep fp32; the product takes bf16
                 }
-                if (c & 1) tc::tmem_st32x(tS + 16u * (c - 1), pk);
+                if (c & 1) {                                     // 64 keys: the product takes each half as it comes
+                    tc::tmem_st32x(tS + 16u * (c - 1), pk);
+                    tc::tmem_wait_st();
+                    tc::fence_before_sync();
+                    tc::mbar_arrive(&p_full[2 * w + (c >> 1)]);
+                }
             }
-            l += s0 + s1;
-            tc::tmem_wait_st();
-            tc::fence_before_sync();
-            tc::mbar_arrive(&p_full[w]);
+            l += sum.x + sum.y;
         }
         // ---- the tile's result: the last product is complete once s_full's next phase is ----
         if (ok && nt[w] > 0) {
@@ -295,35 +304,51 @@ kda_expanded_kernel(const __grid_constant__ ExpMaps maps, const ExpArgs a)
             ok = ok && __all_sync(0xffffffffu, tc::mbar_wait_bounded(bar, parity, kWaitLimitNs));
             return ok;
         };
-        auto qk = [&](int w, int j) {                            // S_w = Q_w K_j^T, slab by slab
+        // a look at several barriers costs the latency of one (about 100 clocks, as each wait does), which
+        // the tensor cores' queue of about four products covers
+        auto ready = [&](uint32_t a, uint32_t b, uint32_t c) { return __all_sync(0xffffffffu, (a & b & c) != 0u) != 0; };
+        // one elected block a product half, so that nothing but address adds stands between its MMAs
+        auto qk = [&](int w, int j) {                            // S_w = Q_w K_j^T
             if (j == 0 && !wait(&q_full[w], 0)) return;
-            for (int s = 0; s < 3; ++s) {
-                const uint32_t i = 5u * j + s, slot = i & (kRing - 1);
-                if (!wait(&full[slot], (i / kRing) & 1)) return;
-                tc::fence_after_sync();
-                const uint32_t b = k_lo + slot * (kSlab >> 4), q = q_lo + (w * 3u + s) * (kSlab >> 4);
-                if (tc::elect_one()) {
+            const uint32_t i = 5u * j;
+            const uint32_t s0 = i & (kRing - 1), s1 = (i + 1u) & (kRing - 1), s2 = (i + 2u) & (kRing - 1);
+            const uint32_t b[3] = {k_lo + s0 * (kSlab >> 4), k_lo + s1 * (kSlab >> 4), k_lo + s2 * (kSlab >> 4)};
+            if (w == 0 || j >= nt[0]) {                          // (tile 1 uses what tile 0 has waited for)
+                const uint32_t h0 = (i / kRing) & 1, h1 = ((i + 1u) / kRing) & 1, h2 = ((i + 2u) / kRing) & 1;
+                if (!ready(tc::mbar_test_wait(&full[s0], h0), tc::mbar_test_wait(&full[s1], h1), tc::mbar_test_wait(&full[s2], h2)) &&
+                    (!wait(&full[s0], h0) || !wait(&full[s1], h1) || !wait(&full[s2], h2)))
+                    return;
+            }
+            tc::fence_after_sync();
+            const uint32_t q = q_lo + w * (3u * kSlab >> 4), d = tm + w * 128u;
+            if (tc::elect_one()) {
+#pragma unroll
+                for (uint32_t s = 0; s < 3; ++s)
 #pragma unroll
                     for (uint32_t k = 0; k < 4; ++k)
-                        tc::mma_f16_lo(tm + w * 128u, q + k * 2u, hi, b + k * 2u, hi, id_s, s > 0 || k > 0 ? 1u : 0u);
-                }
-                __syncwarp();
+                        tc::mma_f16_lo(d, q + (s * kSlab >> 4) + k * 2u, hi, b[s] + k * 2u, hi, id_s, s > 0 || k > 0 ? 1u : 0u);
+                tc::mma_commit(&s_full[w]);
             }
-            if (tc::elect_one()) tc::mma_commit(&s_full[w]);
             __syncwarp();
         };
-        auto pv = [&](int w, int j) {                            // O_w += P_w V_j, half the channels a slab
-            if (!wait(&p_full[w], j & 1)) return;
-            for (int s = 0; s < 2; ++s) {
-                const uint32_t i = 5u * j + 3u + s, slot = i & (kRing - 1);
-                if (!wait(&full[slot], (i / kRing) & 1)) return;
+        auto pv = [&](int w, int j) {                            // O_w += P_w V_j, half the keys, then half the channels a slab
+            const uint32_t i = 5u * j + 3u, s0 = i & (kRing - 1), s1 = (i + 1u) & (kRing - 1);
+            const uint32_t h0 = (i / kRing) & 1, h1 = ((i + 1u) / kRing) & 1;
+            if (!ready(tc::mbar_test_wait(&full[s0], h0), tc::mbar_test_wait(&full[s1], h1), tc::mbar_test_wait(&p_full[2 * w], j & 1)) &&
+                (!wait(&full[s0], h0) || !wait(&full[s1], h1) || !wait(&p_full[2 * w], j & 1)))
+                return;
+            const uint32_t b0 = v_lo + s0 * (kSlab >> 4), b1 = v_lo + s1 * (kSlab >> 4);
+            const uint32_t d = tm + 256u + w * 128u, p = tm + w * 128u, acc = j > 0 ? 1u : 0u;
+#pragma unroll
+            for (uint32_t half = 0; half < 2; ++half) {
+                if (half == 1 && !wait(&p_full[2 * w + 1], j & 1)) return;
                 tc::fence_after_sync();
-                const uint32_t b = v_lo + slot * (kSlab >> 4);
                 if (tc::elect_one()) {
 #pragma unroll
-                    for (uint32_t k = 0; k < 8; ++k)
-                        tc::mma_f16_ta(tm + 256u + w * 128u + s * 64u, tm + w * 128u + k * 8u, b + k * 128u, hi, id_o,
-                                       j > 0 || k > 0 ? 1u : 0u);
+                    for (uint32_t k = 4 * half; k < 4 * half + 4; ++k) {
+                        tc::mma_f16_ta(d, p + k * 8u, b0 + k * 128u, hi, id_o, k > 0 ? 1u : acc);
+                        tc::mma_f16_ta(d + 64u, p + k * 8u, b1 + k * 128u, hi, id_o, k > 0 ? 1u : acc);
+                    }
                 }
                 __syncwarp();
             }
@@ -353,6 +378,10 @@ kda_expanded_kernel(const __grid_constant__ ExpMaps maps, const ExpArgs a)
     } else {
         // ---- copies ----
         if (lane == 0) {
+            tc::tma_prefetch_map(&maps.q);
+            tc::tma_prefetch_map(&maps.k);
+            tc::tma_prefetch_map(&maps.r);
+            tc::tma_prefetch_map(&maps.v);
             const uint32_t ring = tc::smem_u32(smem + oExpRing), sq = tc::smem_u32(smem + oExpQ);
             for (int w = 0; w < 2; ++w)
                 if (nt[w] > 0) {
@@ -360,21 +389,22 @@ kda_expanded_kernel(const __grid_constant__ ExpMaps maps, const ExpArgs a)
                     for (int s = 0; s < 3; ++s)
                         tc::tma_load_3d(sq + (w * 3u + s) * kSlab, &maps.q, 64 * s, h, cq + q0 + w * kExpTile, &q_full[w]);
                 }
-            uint32_t i = 0;
+            uint32_t i = 0;                                      // slabs issued: 5 j + s goes to slot (5 j + s) % 8
             for (int j = 0; j < nmax && ok; ++j) {
                 const int key = ck + j * kExpTile;
-                for (int s = 0; s < 5; ++s, ++i) {
-                    if (i >= kRing) {                            // slab i - 8: K or V of an earlier tile, freed as a whole
-                        const uint32_t jj = (i - kRing) / 5u, ss = (i - kRing) % 5u;
-                        if (ss == 0) ok = tc::mbar_wait_bounded(&kfree[jj & 1], (jj >> 1) & 1, kWaitLimitNs);
-                        if (ss == 3) ok = tc::mbar_wait_bounded(&vfree[jj & 1], (jj >> 1) & 1, kWaitLimitNs);
-                        if (!ok) break;
-                    }
+#pragma unroll
+                for (int s = 0; s < 5; ++s) {
+                    // slab i - 8 leaves its slot first: V of tile j - 2 from s = 1 on, K and r of tile j - 1 from
+                    // s = 3 on (s = 0 takes the last slab of K j - 2, waited for with the first)
+                    if (s == 1 && j >= 2) ok = tc::mbar_wait_bounded(&vfree[j & 1], ((j - 2) >> 1) & 1, kWaitLimitNs);
+                    if (s == 3 && j >= 1) ok = tc::mbar_wait_bounded(&kfree[(j - 1) & 1], ((j - 1) >> 1) & 1, kWaitLimitNs);
+                    if (!ok) break;
                     const uint32_t slot = i & (kRing - 1), dst = ring + slot * kSlab;
                     tc::mbar_arrive_expect_tx(&full[slot], kSlab);
                     if (s < 2) tc::tma_load_3d(dst, &maps.k, 64 * s, h, key, &full[slot]);
                     else if (s == 2) tc::tma_load_2d(dst, &maps.r, 0, key, &full[slot]);
                     else tc::tma_load_3d(dst, &maps.v, 64 * (s - 3), h, key, &full[slot]);
+                    ++i;
                 }
             }
             if (!ok) {                                           // copies in flight land before the CTA ends
