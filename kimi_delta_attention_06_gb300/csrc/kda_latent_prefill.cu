@@ -300,81 +300,64 @@ kda_expanded_kernel(const __grid_constant__ ExpMaps maps, const ExpArgs a)
         const uint32_t q_lo = static_cast<uint32_t>(d0) | (tc::smem_u32(smem + oExpQ) >> 4);
         const uint32_t k_lo = static_cast<uint32_t>(d0) | (tc::smem_u32(smem + oExpRing) >> 4);
         const uint32_t v_lo = static_cast<uint32_t>(dV) | (tc::smem_u32(smem + oExpRing) >> 4);
+        // One thread runs it all: what stands between two products is then a barrier look or two (the
+        // tensor cores queue only about two products, so every clock more is lost)
         auto wait = [&](uint64_t* bar, uint32_t parity) {
-            ok = ok && __all_sync(0xffffffffu, tc::mbar_wait_bounded(bar, parity, kWaitLimitNs));
+            if (!tc::mbar_test_wait(bar, parity)) ok = tc::mbar_wait_bounded(bar, parity, kWaitLimitNs);
             return ok;
         };
-        // a look at several barriers costs the latency of one (about 100 clocks, as each wait does), which
-        // the tensor cores' queue of about four products covers
-        auto ready = [&](uint32_t a, uint32_t b, uint32_t c) { return __all_sync(0xffffffffu, (a & b & c) != 0u) != 0; };
-        // one elected block a product half, so that nothing but address adds stands between its MMAs
         auto qk = [&](int w, int j) {                            // S_w = Q_w K_j^T
-            if (j == 0 && !wait(&q_full[w], 0)) return;
-            const uint32_t i = 5u * j;
-            const uint32_t s0 = i & (kRing - 1), s1 = (i + 1u) & (kRing - 1), s2 = (i + 2u) & (kRing - 1);
-            const uint32_t b[3] = {k_lo + s0 * (kSlab >> 4), k_lo + s1 * (kSlab >> 4), k_lo + s2 * (kSlab >> 4)};
-            if (w == 0 || j >= nt[0]) {                          // (tile 1 uses what tile 0 has waited for)
-                const uint32_t h0 = (i / kRing) & 1, h1 = ((i + 1u) / kRing) & 1, h2 = ((i + 2u) / kRing) & 1;
-                if (!ready(tc::mbar_test_wait(&full[s0], h0), tc::mbar_test_wait(&full[s1], h1), tc::mbar_test_wait(&full[s2], h2)) &&
-                    (!wait(&full[s0], h0) || !wait(&full[s1], h1) || !wait(&full[s2], h2)))
-                    return;
-            }
-            tc::fence_after_sync();
             const uint32_t q = q_lo + w * (3u * kSlab >> 4), d = tm + w * 128u;
-            if (tc::elect_one()) {
 #pragma unroll
-                for (uint32_t s = 0; s < 3; ++s)
+            for (uint32_t s = 0; s < 3; ++s) {
+                const uint32_t i = 5u * j + s, slot = i & (kRing - 1);
+                if (!wait(&full[slot], (i / kRing) & 1)) return;
+                const uint32_t b = k_lo + slot * (kSlab >> 4);
 #pragma unroll
-                    for (uint32_t k = 0; k < 4; ++k)
-                        tc::mma_f16_lo(d, q + (s * kSlab >> 4) + k * 2u, hi, b[s] + k * 2u, hi, id_s, s > 0 || k > 0 ? 1u : 0u);
-                tc::mma_commit(&s_full[w]);
+                for (uint32_t k = 0; k < 4; ++k)
+                    tc::mma_f16_lo(d, q + (s * kSlab >> 4) + k * 2u, hi, b + k * 2u, hi, id_s, s > 0 || k > 0 ? 1u : 0u);
             }
-            __syncwarp();
+            tc::mma_commit(&s_full[w]);
         };
         auto pv = [&](int w, int j) {                            // O_w += P_w V_j, half the keys, then half the channels a slab
             const uint32_t i = 5u * j + 3u, s0 = i & (kRing - 1), s1 = (i + 1u) & (kRing - 1);
-            const uint32_t h0 = (i / kRing) & 1, h1 = ((i + 1u) / kRing) & 1;
-            if (!ready(tc::mbar_test_wait(&full[s0], h0), tc::mbar_test_wait(&full[s1], h1), tc::mbar_test_wait(&p_full[2 * w], j & 1)) &&
-                (!wait(&full[s0], h0) || !wait(&full[s1], h1) || !wait(&p_full[2 * w], j & 1)))
-                return;
             const uint32_t b0 = v_lo + s0 * (kSlab >> 4), b1 = v_lo + s1 * (kSlab >> 4);
             const uint32_t d = tm + 256u + w * 128u, p = tm + w * 128u, acc = j > 0 ? 1u : 0u;
+            if (!wait(&full[s0], (i / kRing) & 1) || !wait(&full[s1], ((i + 1u) / kRing) & 1)) return;
 #pragma unroll
             for (uint32_t half = 0; half < 2; ++half) {
-                if (half == 1 && !wait(&p_full[2 * w + 1], j & 1)) return;
+                if (!wait(&p_full[2 * w + half], j & 1)) return;
                 tc::fence_after_sync();
-                if (tc::elect_one()) {
 #pragma unroll
-                    for (uint32_t k = 4 * half; k < 4 * half + 4; ++k) {
-                        tc::mma_f16_ta(d, p + k * 8u, b0 + k * 128u, hi, id_o, k > 0 ? 1u : acc);
-                        tc::mma_f16_ta(d + 64u, p + k * 8u, b1 + k * 128u, hi, id_o, k > 0 ? 1u : acc);
-                    }
+                for (uint32_t k = 4 * half; k < 4 * half + 4; ++k) {
+                    tc::mma_f16_ta(d, p + k * 8u, b0 + k * 128u, hi, id_o, k > 0 ? 1u : acc);
+                    tc::mma_f16_ta(d + 64u, p + k * 8u, b1 + k * 128u, hi, id_o, k > 0 ? 1u : acc);
                 }
-                __syncwarp();
             }
         };
-        for (int j = -1; j < nmax && ok; ++j) {
+        if (tc::elect_one()) {
+            for (int w = 0; w < 2; ++w)
+                if (nt[w] > 0 && wait(&q_full[w], 0)) {
+                    tc::fence_after_sync();
+                    qk(w, 0);
+                }
+            if (ok && nmax > 0) tc::mma_commit(&kfree[0]);
+            for (int j = 0; j < nmax && ok; ++j) {
 #pragma unroll
-            for (int w = 0; w < 2; ++w) {
-                if (j >= 0 && j < nt[w]) {
-                    pv(w, j);
-                    if (!ok) break;
-                    if (j + 1 == nt[w] && tc::elect_one()) tc::mma_commit(&s_full[w]);   // the tile's result
-                    __syncwarp();
+                for (int w = 0; w < 2; ++w) {
+                    if (j < nt[w] && ok) {
+                        pv(w, j);
+                        if (ok && j + 1 == nt[w]) tc::mma_commit(&s_full[w]);        // the tile's result
+                    }
+                    if (w == 1 && ok) tc::mma_commit(&vfree[j & 1]);
+                    if (j + 1 < nt[w] && ok) qk(w, j + 1);
                 }
-                if (j + 1 < nt[w]) {
-                    qk(w, j + 1);
-                    if (!ok) break;
-                }
+                if (ok && j + 1 < nmax) tc::mma_commit(&kfree[(j + 1) & 1]);
             }
-            if (ok && tc::elect_one()) {
-                if (j >= 0) tc::mma_commit(&vfree[j & 1]);
-                if (j + 1 < nmax) tc::mma_commit(&kfree[(j + 1) & 1]);
-            }
-            __syncwarp();
+            // nothing is left running when the TMEM goes back
+            if (ok && nmax > 0) wait(&vfree[(nmax - 1) & 1], ((nmax - 1) >> 1) & 1);
         }
-        // nothing is left running when the TMEM goes back
-        if (ok && nmax > 0) wait(&vfree[(nmax - 1) & 1], ((nmax - 1) >> 1) & 1);
+        __syncwarp();
     } else {
         // ---- copies ----
         if (lane == 0) {
