@@ -645,7 +645,8 @@ kda_latent_decode_kernel(const __grid_constant__ LatMaps maps, const LatArgs a)
         }
     } else if (warp == Sh::kMmaWarp) {
         // ---- both products; whichever has its inputs goes first ----
-        // (the warp runs as one, so that addresses stay in uniform registers; one elected lane issues)
+        // One thread runs it all: the tensor cores queue only about two products, so what stands between
+        // two groups of them (a vote, an election) is lost
         constexpr uint32_t id_s = tc::idesc(64, R, tc::kFmtBF16, false, false);
         constexpr uint32_t id_o = E4M3 ? tc::idesc8(128, R, tc::kFmtE4M3, tc::kFmtE5M2, true, true)
                                        : tc::idesc(128, R, tc::kFmtBF16, true, true);
@@ -663,32 +664,30 @@ kda_latent_decode_kernel(const __grid_constant__ LatMaps maps, const LatArgs a)
         int ts = sw.t0, to = sv.t0;
         uint64_t since = 0;
         uint32_t idle = 0;
-        while (more_o) {
+        const bool leader = tc::elect_one();
+        while (more_o && leader) {
             bool moved = false;
             // O of a tile before S of the next but one; S at most one tile ahead of O (its S buffer is
             // read before P is written)
-            if (go < gs && __all_sync(0xffffffffu, tc::mbar_test_wait(p_full, go & 1))) {
+            if (go < gs && tc::mbar_test_wait(p_full, go & 1)) {
                 tc::fence_after_sync();
                 const uint32_t c = ct_lo + go % NS * (Sh::kStage >> 4);
                 const uint32_t acc = to > sv.t0 ? 1u : 0u;
-                if (tc::elect_one()) {
 #pragma unroll
-                    for (uint32_t b = 0; b < 4; ++b) {
-                        if constexpr (!E4M3) {
+                for (uint32_t b = 0; b < 4; ++b) {
+                    if constexpr (!E4M3) {
 #pragma unroll
-                            for (uint32_t k = 0; k < 4; ++k)
-                                tc::mma_f16_lo(tmO + b * R, c + ((b * 2u * Sh::kSlabC + k * 2048u) >> 4), hi,
-                                               p_lo + (k * 2048u >> 4), hi, id_o, k > 0 ? 1u : acc);
-                        } else {
+                        for (uint32_t k = 0; k < 4; ++k)
+                            tc::mma_f16_lo(tmO + b * R, c + ((b * 2u * Sh::kSlabC + k * 2048u) >> 4), hi,
+                                           p_lo + (k * 2048u >> 4), hi, id_o, k > 0 ? 1u : acc);
+                    } else {
 #pragma unroll
-                            for (uint32_t k = 0; k < 6; ++k)     // 2 steps of 32 tokens x 3 terms
-                                tc::mma_f8_lo(tmO + b * R, c + ((b * Sh::kSlabC + k / 3u * 4096u) >> 4), hi,
-                                              p_lo + ((k % 3u * kTile * 128u + k / 3u * 4096u) >> 4), hi, id_o, k > 0 ? 1u : acc);
-                        }
+                        for (uint32_t k = 0; k < 6; ++k)     // 2 steps of 32 tokens x 3 terms
+                            tc::mma_f8_lo(tmO + b * R, c + ((b * Sh::kSlabC + k / 3u * 4096u) >> 4), hi,
+                                          p_lo + ((k % 3u * kTile * 128u + k / 3u * 4096u) >> 4), hi, id_o, k > 0 ? 1u : acc);
                     }
-                    tc::mma_commit(&empty[go % NS]);
                 }
-                __syncwarp();
+                tc::mma_commit(&empty[go % NS]);
                 ++go;
                 if (++to == sv.t1) {
                     more_o = sv.next(a.w);
@@ -696,30 +695,27 @@ kda_latent_decode_kernel(const __grid_constant__ LatMaps maps, const LatArgs a)
                 }
                 moved = true;
             }
-            if (more_s && gs <= go + 1 && (ts > sw.t0 || __all_sync(0xffffffffu, tc::mbar_test_wait(q_full, qs & 1))) &&
-                __all_sync(0xffffffffu, tc::mbar_test_wait(&full[gs % NS], gs / NS & 1))) {
+            if (more_s && gs <= go + 1 && (ts > sw.t0 || tc::mbar_test_wait(q_full, qs & 1)) &&
+                tc::mbar_test_wait(&full[gs % NS], gs / NS & 1)) {
                 tc::fence_after_sync();
                 const uint32_t c = c_lo + gs % NS * (Sh::kStage >> 4), d = tmS + (gs & 1) * Sh::kS;
-                if (tc::elect_one()) {
-                    if constexpr (!E4M3) {
+                if constexpr (!E4M3) {
 #pragma unroll
-                        for (uint32_t k = 0; k < 36; ++k)
-                            tc::mma_f16_lo(d, c + (((k >> 2) * Sh::kSlabC + (k & 3) * 32u) >> 4), hi,
-                                           q_lo + (((k >> 2) * Sh::kSlabQ + (k & 3) * 32u) >> 4), hi, id_s, k > 0 ? 1u : 0u);
-                    } else {
+                    for (uint32_t k = 0; k < 36; ++k)
+                        tc::mma_f16_lo(d, c + (((k >> 2) * Sh::kSlabC + (k & 3) * 32u) >> 4), hi,
+                                       q_lo + (((k >> 2) * Sh::kSlabQ + (k & 3) * 32u) >> 4), hi, id_s, k > 0 ? 1u : 0u);
+                } else {
 #pragma unroll
-                        for (uint32_t k = 0; k < 32; ++k)        // 16 steps of 32 codes x 2 terms of q
-                            tc::mma_f8_lo(d, c + (((k >> 3) * Sh::kSlabC + (k >> 1 & 3) * 32u) >> 4), hi,
-                                          q_lo + (((k & 1) * 4u * Sh::kSlabQ + (k >> 3) * Sh::kSlabQ + (k >> 1 & 3) * 32u) >> 4), hi,
-                                          id_c, k > 0 ? 1u : 0u);
+                    for (uint32_t k = 0; k < 32; ++k)        // 16 steps of 32 codes x 2 terms of q
+                        tc::mma_f8_lo(d, c + (((k >> 3) * Sh::kSlabC + (k >> 1 & 3) * 32u) >> 4), hi,
+                                      q_lo + (((k & 1) * 4u * Sh::kSlabQ + (k >> 3) * Sh::kSlabQ + (k >> 1 & 3) * 32u) >> 4), hi,
+                                      id_c, k > 0 ? 1u : 0u);
 #pragma unroll
-                        for (uint32_t k = 0; k < 4; ++k)         // the position part, bf16
-                            tc::mma_f16_lo(d + R, c + ((4u * Sh::kSlabC + k * 32u) >> 4), hi,
-                                           q_lo + ((8u * Sh::kSlabQ + k * 32u) >> 4), hi, id_s, k > 0 ? 1u : 0u);
-                    }
-                    tc::mma_commit(&s_full[gs & 1]);
+                    for (uint32_t k = 0; k < 4; ++k)         // the position part, bf16
+                        tc::mma_f16_lo(d + R, c + ((4u * Sh::kSlabC + k * 32u) >> 4), hi,
+                                       q_lo + ((8u * Sh::kSlabQ + k * 32u) >> 4), hi, id_s, k > 0 ? 1u : 0u);
                 }
-                __syncwarp();
+                tc::mma_commit(&s_full[gs & 1]);
                 ++gs;
                 if (++ts == sw.t1) {
                     ++qs;
@@ -733,12 +729,12 @@ kda_latent_decode_kernel(const __grid_constant__ LatMaps maps, const LatArgs a)
             } else if ((++idle & 255u) == 0) {                  // the clock is read every 256 idle rounds
                 const uint64_t now = tc::globaltimer_ns();
                 if (idle == 256u) since = now;
-                else if (__any_sync(0xffffffffu, now - since > kWaitLimitNs)) { ok = false; break; }
+                else if (now - since > kWaitLimitNs) { ok = false; break; }
             }
         }
         // nothing of this CTA's is left running when it returns its TMEM
-        if (gs > 0 && !tc::mbar_wait_bounded(&s_full[(gs - 1) & 1], ((gs - 1) >> 1) & 1, kWaitLimitNs)) ok = false;
-        if (go > 0 && !tc::mbar_wait_bounded(&empty[(go - 1) % NS], (go - 1) / NS & 1, kWaitLimitNs)) ok = false;
+        if (leader && gs > 0 && !tc::mbar_wait_bounded(&s_full[(gs - 1) & 1], ((gs - 1) >> 1) & 1, kWaitLimitNs)) ok = false;
+        if (leader && go > 0 && !tc::mbar_wait_bounded(&empty[(go - 1) % NS], (go - 1) / NS & 1, kWaitLimitNs)) ok = false;
         __syncwarp();
     } else {
         // ---- TMA: C tiles in boxes of `box` rows (one page or a part of one); bf16: Q of each segment ----
