@@ -342,28 +342,30 @@ def kda_output_norm(o, o_dtype: int, gamma, eps: float, y, total_tokens: int, H:
     _check(rc, "kda_output_norm")
 
 
-def _strided(t: torch.Tensor):
-    """Device pointer of a tensor whose last dimension is contiguous (its other strides are passed on)."""
-    if t.numel() and t.stride(-1) != 1:
-        raise ValueError("the last dimension of a KDA tensor must be contiguous")
+# The calls below are as short as a small kernel, so each tensor is looked at once: its address (and
+# its strides) come out of the function that checks its type and layout.
+_BF16, _I32, _F32 = torch.bfloat16, torch.int32, torch.float32
+
+
+def _dense(t: Optional[torch.Tensor], dtype):
+    if t is None:
+        return None
+    if t.dtype != dtype:
+        raise TypeError(f"expected a {dtype} tensor, got {t.dtype}")
+    if not t.is_contiguous():
+        raise ValueError("KDA tensors must be contiguous")
     return t.data_ptr()
 
 
-def _step(t: torch.Tensor, dim: int, least: int) -> int:
-    """Stride of a dimension, in elements (any where it has one entry: a value the checks pass)."""
-    return t.stride(dim) if t.shape[dim] > 1 else least
-
-
-def _i32(t: Optional[torch.Tensor]) -> Optional[torch.Tensor]:
-    if t is not None and t.dtype != torch.int32:
-        raise TypeError(f"expected an int32 tensor, got {t.dtype}")
-    return t
-
-
-def _f32(t: Optional[torch.Tensor]) -> Optional[torch.Tensor]:
-    if t is not None and t.dtype != torch.float32:
-        raise TypeError(f"expected a float32 tensor, got {t.dtype}")
-    return t
+def _rows(t: torch.Tensor, dtype, *least: int):
+    """(address, strides of the leading dimensions in elements) of a tensor whose last dimension is
+    contiguous; a dimension of one entry has any stride: `least`, which the checks pass."""
+    if t.dtype != dtype:
+        raise TypeError(f"expected a {dtype} tensor, got {t.dtype}")
+    st, shape = t.stride(), t.shape
+    if st[-1] != 1 and t.numel():
+        raise ValueError("the last dimension of a KDA tensor must be contiguous")
+    return (t.data_ptr(), *(st[i] if shape[i] > 1 else x for i, x in enumerate(least)))
 
 
 def _host32(t):
@@ -396,44 +398,49 @@ def _pages(cache: torch.Tensor, cache_dtype: int):
 
 
 def kda_latent_append(c, k_rope, cache, cache_dtype: int, slots, total_tokens: int, stream=None):
+    cp, ldc = _rows(c, _BF16, KDA_LATENT_DIM)
+    rp, ldr = _rows(k_rope, _BF16, KDA_LATENT_ROPE)
     p, num_pages, page_size = _pages(cache, cache_dtype)
-    rc = load().kda_latent_append(_strided(_bits16(c)), _step(c, 0, KDA_LATENT_DIM),
-                                  _strided(_bits16(k_rope)), _step(k_rope, 0, KDA_LATENT_ROPE), p,
-                                  int(cache_dtype), num_pages, page_size, _ptr(_i32(slots)), int(total_tokens),
-                                  _stream(stream))
-    _check(rc, "kda_latent_append")
+    rc = load().kda_latent_append(cp, ldc, rp, ldr, p, cache_dtype, num_pages, page_size, _dense(slots, _I32),
+                                  total_tokens, _stream(stream))
+    if rc:
+        _check(rc, "kda_latent_append")
 
 
 def kda_latent_gather(cache, cache_dtype: int, block_table, start_pos, cu_seqlens, cu_seqlens_host, num_seqs: int,
                       total_tokens: int, c, k_rope, stream=None):
     p, num_pages, page_size = _pages(cache, cache_dtype)
     cu_host = _host32(cu_seqlens_host)
-    rc = load().kda_latent_gather(p, int(cache_dtype), num_pages, page_size, _ptr(_i32(block_table)),
-                                  int(block_table.shape[1]), _ptr(_i32(start_pos)), _ptr(_i32(cu_seqlens)),
-                                  cu_host.data_ptr(), int(num_seqs), int(total_tokens),
-                                  _strided(_bits16(c)), _step(c, 0, KDA_LATENT_DIM), _strided(_bits16(k_rope)),
-                                  _step(k_rope, 0, KDA_LATENT_ROPE), _stream(stream))
-    _check(rc, "kda_latent_gather")
+    cp, ldc = _rows(c, _BF16, KDA_LATENT_DIM)
+    rp, ldr = _rows(k_rope, _BF16, KDA_LATENT_ROPE)
+    rc = load().kda_latent_gather(p, cache_dtype, num_pages, page_size, _dense(block_table, _I32), block_table.shape[1],
+                                  _dense(start_pos, _I32), _dense(cu_seqlens, _I32), cu_host.data_ptr(), num_seqs,
+                                  total_tokens, cp, ldc, rp, ldr, _stream(stream))
+    if rc:
+        _check(rc, "kda_latent_gather")
 
 
 def kda_latent_decode(q, cache, cache_dtype: int, block_table, seq_lens, N: int, K: int, H: int, sm_scale: float, out,
                       lse, stream=None):
     p, num_pages, page_size = _pages(cache, cache_dtype)
-    rc = load().kda_latent_decode(_ptr(_bits16(q)), p, int(cache_dtype), num_pages, page_size, _ptr(_i32(block_table)),
-                                  int(block_table.shape[1]), _ptr(_i32(seq_lens)), int(N), int(K), int(H),
-                                  float(sm_scale), _ptr(_bits16(out)), _ptr(_f32(lse)), _stream(stream))
-    _check(rc, "kda_latent_decode")
+    rc = load().kda_latent_decode(_dense(q, _BF16), p, cache_dtype, num_pages, page_size, _dense(block_table, _I32),
+                                  block_table.shape[1], _dense(seq_lens, _I32), N, K, H, sm_scale, _dense(out, _BF16),
+                                  _dense(lse, _F32), _stream(stream))
+    if rc:
+        _check(rc, "kda_latent_decode")
 
 
 def kda_latent_prefill(q, k, v, k_rope, cu_q, cu_q_host, cu_k, cu_k_host, num_seqs: int, total_q: int, total_k: int,
                        H: int, causal: int, sm_scale: float, out, lse, stream=None):
     cq, ck = _host32(cu_q_host), _host32(cu_k_host)
-    rc = load().kda_latent_prefill(_ptr(_bits16(q)), _strided(_bits16(k)), _step(k, 0, 128), _step(k, 1, 128),
-                                   _strided(_bits16(v)), _step(v, 0, 128), _step(v, 1, 128), _strided(_bits16(k_rope)),
-                                   _step(k_rope, 0, KDA_LATENT_ROPE), _ptr(_i32(cu_q)), cq.data_ptr(), _ptr(_i32(cu_k)),
-                                   ck.data_ptr(), int(num_seqs), int(total_q), int(total_k), int(H), int(causal),
-                                   float(sm_scale), _ptr(_bits16(out)), _ptr(_f32(lse)), _stream(stream))
-    _check(rc, "kda_latent_prefill")
+    kp, ldk, hdk = _rows(k, _BF16, 128, 128)
+    vp, ldv, hdv = _rows(v, _BF16, 128, 128)
+    rp, ldr = _rows(k_rope, _BF16, KDA_LATENT_ROPE)
+    rc = load().kda_latent_prefill(_dense(q, _BF16), kp, ldk, hdk, vp, ldv, hdv, rp, ldr, _dense(cu_q, _I32), cq.data_ptr(),
+                                   _dense(cu_k, _I32), ck.data_ptr(), num_seqs, total_q, total_k, H, causal, sm_scale,
+                                   _dense(out, _BF16), _dense(lse, _F32), _stream(stream))
+    if rc:
+        _check(rc, "kda_latent_prefill")
 
 
 def kda_verify_draft(target_probs, draft_probs, draft_tokens, num_draft, u_accept, u_sample, N: int, K: int, V: int,
@@ -441,16 +448,18 @@ def kda_verify_draft(target_probs, draft_probs, draft_tokens, num_draft, u_accep
     def rows(t, per):           # rows of V values, one constant stride apart
         if t is None:
             return None, 0
-        if t.shape[0] > 1 and t.stride(0) != per * t.stride(1):
+        p, seq, ld = _rows(t, _F32, per * V, V)
+        if t.shape[0] > 1 and per > 1 and seq != per * ld:
             raise ValueError("the probability rows of consecutive sequences must be evenly spaced")
-        return _strided(_f32(t)), t.stride(1) if t.shape[0] * per > 1 else V
+        return p, seq if per == 1 else ld
 
     tp, ldp = rows(target_probs, K + 1)
     dp, ldq = rows(draft_probs, K)
-    rc = load().kda_verify_draft(tp, ldp, dp, ldq, _ptr(_i32(draft_tokens)), _ptr(_i32(num_draft)), _ptr(_f32(u_accept)),
-                                 _ptr(_f32(u_sample)), int(N), int(K), int(V), _ptr(_i32(tokens)),
-                                 _ptr(_i32(num_tokens)), _stream(stream))
-    _check(rc, "kda_verify_draft")
+    rc = load().kda_verify_draft(tp, ldp, dp, ldq, _dense(draft_tokens, _I32), _dense(num_draft, _I32),
+                                 _dense(u_accept, _F32), _dense(u_sample, _F32), N, K, V, _dense(tokens, _I32),
+                                 _dense(num_tokens, _I32), _stream(stream))
+    if rc:
+        _check(rc, "kda_verify_draft")
 
 
 def kda_debug_expire_wait(limit_ns: int, stream=None):
@@ -527,10 +536,11 @@ def latent_gather(cache, cache_dtype: int, block_table, cu_seqlens_host, cu_seql
     """Read sequences back as dense rows; returns (c [T, 512], k_rope [T, 64]), bf16."""
     cu_host = _host32(cu_seqlens_host)
     N, T = cu_host.numel() - 1, _last32(cu_host)
+    dev = cache.device
     if cu_seqlens is None:
-        cu_seqlens = cu_host.to(cache.device)
-    c = torch.empty(T, KDA_LATENT_DIM, device=cache.device, dtype=torch.bfloat16)
-    r = torch.empty(T, KDA_LATENT_ROPE, device=cache.device, dtype=torch.bfloat16)
+        cu_seqlens = cu_host.to(dev)
+    c = torch.empty((T, KDA_LATENT_DIM), device=dev, dtype=_BF16)
+    r = torch.empty((T, KDA_LATENT_ROPE), device=dev, dtype=_BF16)
     kda_latent_gather(cache, cache_dtype, block_table, start_pos, cu_seqlens, cu_host, N, T, c, r, stream)
     return c, r
 
@@ -539,8 +549,9 @@ def latent_decode(q, cache, cache_dtype: int, block_table, seq_lens, sm_scale: f
     """Absorbed latent attention of q [N, K, H, 576] over the cache; returns (out [N, K, H, 512] bf16,
     lse [N, K, H] fp32 or None)."""
     N, K, H, _ = q.shape
-    out = torch.empty(N, K, H, KDA_LATENT_DIM, device=q.device, dtype=torch.bfloat16)
-    lse = torch.empty(N, K, H, device=q.device, dtype=torch.float32) if want_lse else None
+    dev = q.device
+    out = torch.empty((N, K, H, KDA_LATENT_DIM), device=dev, dtype=_BF16)
+    lse = torch.empty((N, K, H), device=dev, dtype=_F32) if want_lse else None
     kda_latent_decode(q, cache, cache_dtype, block_table, seq_lens, N, K, H, sm_scale, out, lse, stream)
     return out, lse
 
@@ -550,15 +561,16 @@ def latent_prefill(q, k, v, k_rope, cu_q_host, cu_k_host, sm_scale: float, causa
     """Expanded latent attention of q [Tq, H, 192] over k, v [Tk, H, 128] and k_rope [Tk, 64]; returns
     (out [Tq, H, 128] bf16, lse [Tq, H] fp32 or None)."""
     cq, ck = _host32(cu_q_host), _host32(cu_k_host)
+    dev = q.device
     if cu_q is None:
-        cu_q = cq.to(q.device)
+        cu_q = cq.to(dev)
     if cu_k is None:
-        cu_k = ck.to(q.device)
+        cu_k = ck.to(dev)
     Tq, H, _ = q.shape
-    out = torch.empty(Tq, H, 128, device=q.device, dtype=torch.bfloat16)
-    lse = torch.empty(Tq, H, device=q.device, dtype=torch.float32) if want_lse else None
-    kda_latent_prefill(q, k, v, k_rope, cu_q, cq, cu_k, ck, cq.numel() - 1, Tq, k.shape[0], H, int(bool(causal)),
-                       sm_scale, out, lse, stream)
+    out = torch.empty((Tq, H, 128), device=dev, dtype=_BF16)
+    lse = torch.empty((Tq, H), device=dev, dtype=_F32) if want_lse else None
+    kda_latent_prefill(q, k, v, k_rope, cu_q, cq, cu_k, ck, cq.numel() - 1, Tq, k.shape[0], H, int(causal), sm_scale, out,
+                       lse, stream)
     return out, lse
 
 
@@ -566,8 +578,9 @@ def verify_draft(target_probs, draft_probs, draft_tokens, u_accept, u_sample, nu
     """Accept or reject draft_tokens [N, K] against target_probs [N, K + 1, V] (draft_probs [N, K, V] or None);
     returns (tokens [N, K + 1] int32, num_tokens [N] int32)."""
     N, K1, V = target_probs.shape
-    tokens = torch.empty(N, K1, device=target_probs.device, dtype=torch.int32)
-    num = torch.empty(N, device=target_probs.device, dtype=torch.int32)
+    dev = target_probs.device
+    tokens = torch.empty((N, K1), device=dev, dtype=_I32)
+    num = torch.empty((N,), device=dev, dtype=_I32)
     kda_verify_draft(target_probs, draft_probs, draft_tokens, num_draft, u_accept, u_sample, N, K1 - 1, V, tokens, num,
                      stream)
     return tokens, num
