@@ -814,7 +814,7 @@ __global__ void __launch_bounds__(512)
 kda_latent_combine_kernel(const LatArgs a, int Q, int NG)
 {
     __shared__ long long s_sum[2][16];
-    __shared__ float s_w[kMaxRuns];              // weight of each partial
+    __shared__ float s_w[kMaxRuns], s_l[kMaxRuns];             // weight (first m) and l of each partial
     __shared__ float4 s_acc[512];
     __shared__ float s_ml[2][16];
     const int lanes = 128 / Q, threads = lanes * NG;
@@ -863,9 +863,10 @@ kda_latent_combine_kernel(const LatArgs a, int Q, int NG)
     // M = the largest maximum; weights exp2(m_i - M); L = sum of weight_i l_i
     float M = -INFINITY;
     for (int i = tid; i < parts; i += threads) {
-        const float m = a.part_ml[slot(i) * 2];
-        s_w[i] = m;
-        M = fmaxf(M, m);
+        const float2 ml = *reinterpret_cast<const float2*>(a.part_ml + slot(i) * 2);
+        s_w[i] = ml.x;
+        s_l[i] = ml.y;
+        M = fmaxf(M, ml.x);
     }
 #pragma unroll
     for (int off = 16; off > 0; off >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, off));
@@ -874,7 +875,7 @@ kda_latent_combine_kernel(const LatArgs a, int Q, int NG)
     for (int i = 0; i < warps; ++i) M = fmaxf(M, s_ml[0][i]);
     float L = 0.f;
     for (int i = tid; i < parts; i += threads) {
-        const float m = s_w[i], l = a.part_ml[slot(i) * 2 + 1];
+        const float m = s_w[i], l = s_l[i];
         const float w = m == -INFINITY && l == 0.f ? 0.f : m == M ? 1.f : lat_ex2(m - M);     // 0: saw nothing there
         s_w[i] = m == -INFINITY && l == 0.f ? -1.f : w;
         L += w * l;
@@ -886,7 +887,7 @@ kda_latent_combine_kernel(const LatArgs a, int Q, int NG)
     L = 0.f;
     for (int i = 0; i < warps; ++i) L += s_ml[1][i];
     float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll 4
+#pragma unroll 8
     for (int i = grp; i < parts; i += NG) {
         const float4 o = *reinterpret_cast<const float4*>(a.part_o + slot(i) * kLatDim + ch);
         const float w = s_w[i];
@@ -1094,8 +1095,8 @@ int launch_latent_decode(const uint16_t* q, const void* cache, int e4m3, int num
 {
     LatArgs a = {};
     const int rows = K * H, R = rows_per_cta(rows);
-    // (a segment's start and end in tiles, as measured: 9000 of 3300 clocks; e4m3 splits Q too)
-    a.w = LatWork{seq_lens, N, latent_decode_runs(rows), N == 1 ? 0 : e4m3 && R == 64 ? 6 : 3, static_cast<long long>(max_pages) * page_size};
+    // (a segment's start and end in tiles: the best of 1, 2, 3, 4, 6 and of 4, 6, 8, 10, where Q is split too)
+    a.w = LatWork{seq_lens, N, latent_decode_runs(rows), N == 1 ? 0 : e4m3 && R == 64 ? 8 : 2, static_cast<long long>(max_pages) * page_size};
     if (a.w.G <= 0) return -3;
     a.ch = LatentCache{static_cast<const uint8_t*>(cache), table, num_pages, page_size, max_pages};
     a.q = q;
