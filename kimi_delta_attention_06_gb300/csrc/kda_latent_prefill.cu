@@ -90,6 +90,7 @@ constexpr int kExpTile = 128;                    // rows of a query tile, keys o
 constexpr int kExpRows = 2 * kExpTile;           // query rows a CTA
 constexpr uint32_t kSlab = kExpTile * 128u;      // 64 channels x 128 rows of bf16
 constexpr uint32_t kRing = 8;
+constexpr int kExpCopyWarp = 9;
 constexpr int kExpThreads = 320;                 // warps 0-3, 4-7: softmax of tile 0, 1; 8: products; 9: copies
 constexpr uint32_t oExpQ = 0, oExpRing = 6 * kSlab, oExpBar = oExpRing + kRing * kSlab;
 constexpr uint32_t kExpSmem = oExpBar + 32 * 8 + 16;
@@ -143,8 +144,23 @@ kda_expanded_kernel(const __grid_constant__ ExpMaps maps, const ExpArgs a)
         nt[w] = see > 0 ? (see + kExpTile - 1) / kExpTile : 0;
     }
     const int nmax = max(nt[0], nt[1]);
+    const uint32_t ring = tc::smem_u32(smem + oExpRing), sq = tc::smem_u32(smem + oExpQ);
+    auto copy_q = [&](int w) {
+        if (nt[w] == 0) return;
+        tc::mbar_arrive_expect_tx(&q_full[w], 3u * kSlab);
+        for (int s = 0; s < 3; ++s)
+            tc::tma_load_3d(sq + (w * 3u + s) * kSlab, &maps.q, 64 * s, h, cq + q0 + w * kExpTile, &q_full[w]);
+    };
+    auto copy_kv = [&](uint32_t i, int j, int s) {               // slab s of key tile j, the i-th of all, to slot i % 8
+        const uint32_t slot = i & (kRing - 1), dst = ring + slot * kSlab;
+        const int key = ck + j * kExpTile;
+        tc::mbar_arrive_expect_tx(&full[slot], kSlab);
+        if (s < 2) tc::tma_load_3d(dst, &maps.k, 64 * s, h, key, &full[slot]);
+        else if (s == 2) tc::tma_load_2d(dst, &maps.r, 0, key, &full[slot]);
+        else tc::tma_load_3d(dst, &maps.v, 64 * (s - 3), h, key, &full[slot]);
+    };
 
-    if (tid == 0) {
+    if (tid == 32 * kExpCopyWarp) {
         for (uint32_t i = 0; i < kRing; ++i) tc::mbar_init(&full[i], 1);
         for (int i = 0; i < 2; ++i) {
             tc::mbar_init(&kfree[i], 1);
@@ -155,7 +171,15 @@ kda_expanded_kernel(const __grid_constant__ ExpMaps maps, const ExpArgs a)
             tc::mbar_init(&q_full[i], 1);
         }
         tc::mbar_fence_init();
+        // the first copies go out before the CTA meets, in the order in which they are used
+        if (nmax > 0) {
+            copy_q(0);
+            for (int s = 0; s < 3; ++s) copy_kv(s, 0, s);
+            copy_q(1);
+            for (int s = 3; s < 5; ++s) copy_kv(s, 0, s);
+        }
     }
+    __syncwarp();
     if (warp == 8) tc::tmem_alloc(s_tmem, 512);
     tc::fence_before_sync();
     __syncthreads();
@@ -251,35 +275,29 @@ kda_expanded_kernel(const __grid_constant__ ExpMaps maps, const ExpArgs a)
         if (ok && q0 + w * kExpTile < Lq) {
             const bool mine = row < Lq;
             const long long at = (static_cast<long long>(cq) + row) * a.H + h;
-            const float inv = l == 0.f ? 0.f : 1.f / l;
-            bool bad = false;
+            const bool some = nt[w] > 0 && l != 0.f;            // (else the row sees nothing: zeros)
+            const float inv = 1.f / l;
+            float check = 0.f;                                   // NaN once a value is none or infinite
 #pragma unroll 1
             for (int c = 0; c < 4; ++c) {
                 uint32_t o[32];
-                if (nt[w] > 0) {
-                    tc::tmem_ld32x(tO + 32u * c, o);
-                    tc::tmem_wait_ld();
-                }
-                uint4 v[4];
+                tc::tmem_ld32x(tO + 32u * c, o);
+                tc::tmem_wait_ld();
+                uint32_t pk[16];
 #pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    uint32_t pk[4];
-#pragma unroll
-                    for (int e = 0; e < 4; ++e) {
-                        const float x0 = nt[w] > 0 && inv != 0.f ? __uint_as_float(o[8 * i + 2 * e]) * inv : 0.f;
-                        const float x1 = nt[w] > 0 && inv != 0.f ? __uint_as_float(o[8 * i + 2 * e + 1]) * inv : 0.f;
-                        bad = bad || !(fabsf(x0) < INFINITY) || !(fabsf(x1) < INFINITY);
-                        pk[e] = f32x2_to_bf16x2_bits(x0, x1);
-                    }
-                    v[i] = make_uint4(pk[0], pk[1], pk[2], pk[3]);
+                for (int i = 0; i < 16; ++i) {
+                    const float x0 = __uint_as_float(o[2 * i]) * inv, x1 = __uint_as_float(o[2 * i + 1]) * inv;
+                    check = fmaf(x1, 0.f, fmaf(x0, 0.f, check));
+                    pk[i] = some ? f32x2_to_bf16x2_bits(x0, x1) : 0u;
                 }
                 if (mine) {
                     uint4* d = reinterpret_cast<uint4*>(a.out + at * kExpV + 32 * c);
 #pragma unroll
-                    for (int i = 0; i < 4; ++i) d[i] = v[i];
+                    for (int i = 0; i < 4; ++i) d[i] = make_uint4(pk[4 * i], pk[4 * i + 1], pk[4 * i + 2], pk[4 * i + 3]);
                 }
             }
-            if (mine && a.lse) a.lse[at] = (m + log2f(l)) * 0.69314718055994531f;
+            const bool bad = some && !(check == 0.f);
+            if (mine && a.lse) a.lse[at] = (m + log2f(l)) * 0.69314718055994531f;     // nothing seen: -inf
             // a NaN or infinity in a key or value that other rows of the tile see spoils this row's sum
             // (0 * NaN): such a row is computed again over exactly its own keys
             unsigned again = __ballot_sync(0xffffffffu, mine && bad);
@@ -361,33 +379,16 @@ kda_expanded_kernel(const __grid_constant__ ExpMaps maps, const ExpArgs a)
     } else {
         // ---- copies ----
         if (lane == 0) {
-            tc::tma_prefetch_map(&maps.q);
-            tc::tma_prefetch_map(&maps.k);
-            tc::tma_prefetch_map(&maps.r);
-            tc::tma_prefetch_map(&maps.v);
-            const uint32_t ring = tc::smem_u32(smem + oExpRing), sq = tc::smem_u32(smem + oExpQ);
-            for (int w = 0; w < 2; ++w)
-                if (nt[w] > 0) {
-                    tc::mbar_arrive_expect_tx(&q_full[w], 3u * kSlab);
-                    for (int s = 0; s < 3; ++s)
-                        tc::tma_load_3d(sq + (w * 3u + s) * kSlab, &maps.q, 64 * s, h, cq + q0 + w * kExpTile, &q_full[w]);
-                }
-            uint32_t i = 0;                                      // slabs issued: 5 j + s goes to slot (5 j + s) % 8
-            for (int j = 0; j < nmax && ok; ++j) {
-                const int key = ck + j * kExpTile;
+            uint32_t i = nmax > 0 ? 5u : 0u;                     // slabs issued: 5 j + s goes to slot (5 j + s) % 8
+            for (int j = 1; j < nmax && ok; ++j) {
 #pragma unroll
                 for (int s = 0; s < 5; ++s) {
                     // slab i - 8 leaves its slot first: V of tile j - 2 from s = 1 on, K and r of tile j - 1 from
                     // s = 3 on (s = 0 takes the last slab of K j - 2, waited for with the first)
                     if (s == 1 && j >= 2) ok = tc::mbar_wait_bounded(&vfree[j & 1], ((j - 2) >> 1) & 1, kWaitLimitNs);
-                    if (s == 3 && j >= 1) ok = tc::mbar_wait_bounded(&kfree[(j - 1) & 1], ((j - 1) >> 1) & 1, kWaitLimitNs);
+                    if (s == 3) ok = tc::mbar_wait_bounded(&kfree[(j - 1) & 1], ((j - 1) >> 1) & 1, kWaitLimitNs);
                     if (!ok) break;
-                    const uint32_t slot = i & (kRing - 1), dst = ring + slot * kSlab;
-                    tc::mbar_arrive_expect_tx(&full[slot], kSlab);
-                    if (s < 2) tc::tma_load_3d(dst, &maps.k, 64 * s, h, key, &full[slot]);
-                    else if (s == 2) tc::tma_load_2d(dst, &maps.r, 0, key, &full[slot]);
-                    else tc::tma_load_3d(dst, &maps.v, 64 * (s - 3), h, key, &full[slot]);
-                    ++i;
+                    copy_kv(i++, j, s);
                 }
             }
             if (!ok) {                                           // copies in flight land before the CTA ends
