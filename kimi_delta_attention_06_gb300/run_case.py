@@ -8,6 +8,12 @@
   python -m kimi_delta_attention_06_gb300.run_case --what decode_multi --N 512 --K 4 [--commit 1] [--reps 2]
   python -m kimi_delta_attention_06_gb300.run_case --what prep --T 145408 [--reps 2]     (input preparation)
   python -m kimi_delta_attention_06_gb300.run_case --what outnorm --T 145408 [--reps 2]  (output norm)
+  python -m kimi_delta_attention_06_gb300.run_case --what latent_append --T 145408 [--cache e4m3] [--reps 2]
+  python -m kimi_delta_attention_06_gb300.run_case --what latent_gather --T 145408 [--cache e4m3] [--reps 2]
+  python -m kimi_delta_attention_06_gb300.run_case --what latent_decode --N 64 --T 16384 [--K 1] [--H 32] [--cache bf16]
+      (absorbed latent attention of K tokens of N sequences of T cached tokens each, pages of 64)
+  python -m kimi_delta_attention_06_gb300.run_case --what latent_prefill --T 8192 [--H 32]
+  python -m kimi_delta_attention_06_gb300.run_case --what verify --N 256 --K 4 [--vocab 131072]
 
 Inputs are the seeded synthetic tensors of workloads.py, generated on the GPU
 (varlen: 16 packed sequences of log-uniform length, about 280k tokens).
@@ -23,11 +29,52 @@ import torch
 from . import build, kda, workloads
 
 
+def latent_case(a, dev, stream):
+    """The run, its description and its count of units for the latent and verification cases."""
+    g = torch.Generator(device=dev).manual_seed(7)
+    rn = lambda *s: torch.randn(*s, generator=g, device=dev).to(torch.bfloat16)
+    if a.what == "verify":
+        p = torch.softmax(torch.randn(a.N, a.K + 1, a.vocab, generator=g, device=dev) * 2, -1)
+        q = torch.softmax(p[:, :a.K].log() + 0.5 * torch.randn(a.N, a.K, a.vocab, generator=g, device=dev), -1)
+        x = torch.multinomial(q.view(-1, a.vocab), 1, generator=g).view(a.N, a.K).to(torch.int32)
+        u, us = torch.rand(a.N, a.K, generator=g, device=dev), torch.rand(a.N, generator=g, device=dev)
+        return (lambda: kda.verify_draft(p, q, x, u, us, stream=stream)), f"{a.N} sequences x {a.K} drafts of {a.vocab}", a.N
+    if a.what == "latent_prefill":
+        q, kv, r = rn(a.T, a.H, 192), rn(a.T, a.H, 256), rn(a.T, 64)
+        cu = torch.tensor([0, a.T], dtype=torch.int32)
+        cud = cu.to(dev)
+        return (lambda: kda.latent_prefill(q, kv[..., :128], kv[..., 128:], r, cu, cu, 192 ** -0.5, cu_q=cud, cu_k=cud,
+                                           stream=stream)), f"{a.T} tokens x {a.H} heads, causal", a.T
+    dt = kda.KDA_CACHE_E4M3 if a.cache == "e4m3" else kda.KDA_CACHE_BF16
+    n = a.N if a.what == "latent_decode" else 1
+    per = -(-a.T // 64)
+    table = torch.randperm(n * per, generator=g, device=dev).to(torch.int32).view(n, per)
+    cache = kda.latent_cache(n * per, 64, dt, device=dev)
+    t = torch.arange(a.T, device=dev)
+    slots = (table.long()[:, t // 64] * 64 + t % 64).to(torch.int32)
+    c, r = rn(a.T, 512), rn(a.T, 64)
+    for i in range(n):
+        kda.latent_append(c, r, cache, dt, slots[i], stream=stream)
+    if a.what == "latent_append":
+        return (lambda: kda.latent_append(c, r, cache, dt, slots[0], stream=stream)), f"{a.T} tokens, {a.cache}", a.T
+    if a.what == "latent_gather":
+        cu = torch.tensor([0, a.T], dtype=torch.int32)
+        cud = cu.to(dev)
+        return (lambda: kda.latent_gather(cache, dt, table, cu, cu_seqlens=cud, stream=stream)), f"{a.T} tokens, {a.cache}", a.T
+    q = rn(n, a.K, a.H, 576)
+    lens = torch.full((n,), a.T, dtype=torch.int32, device=dev)
+    return (lambda: kda.latent_decode(q, cache, dt, table, lens, 192 ** -0.5, stream=stream)), \
+        f"{n} sequences of {a.T} cached tokens ({n * a.T * cache.shape[2] / 1e9:.3f} GB), {a.K} x {a.H} rows, {a.cache}", n * a.K
+
+
 def main(argv=None):
     ap = argparse.ArgumentParser()
-    ap.add_argument("--what", choices=["prefill", "varlen", "decode", "decode_multi", "prep", "outnorm"],
+    ap.add_argument("--what", choices=["prefill", "varlen", "decode", "decode_multi", "prep", "outnorm", "latent_append",
+                                       "latent_gather", "latent_decode", "latent_prefill", "verify"],
                     default="prefill")
-    ap.add_argument("--K", type=int, default=4, help="tokens per sequence (decode_multi)")
+    ap.add_argument("--cache", choices=["bf16", "e4m3"], default="e4m3", help="latent cache rows")
+    ap.add_argument("--vocab", type=int, default=131072, help="verify: vocabulary size")
+    ap.add_argument("--K", type=int, default=4, help="tokens per sequence (decode_multi, latent_decode), drafts (verify)")
     ap.add_argument("--commit", type=int, default=0, help="decode_multi: 1 writes the states back")
     ap.add_argument("--decay", choices=["channel", "head", "none"], default="channel",
                     help="prefill decay layout (per channel = KDA, per head = Gated DeltaNet, none = DeltaNet)")
@@ -98,6 +145,8 @@ def main(argv=None):
                 kda.kda_output_norm(o, kda.KDA_OUT_BF16, gam, 1e-6, y, T, H, D, stream)
             nbytes = T * H * D * 2 * 2
         units, count = f"{T} tokens x {H} heads ({nbytes / 1e9:.3f} GB moved)", T
+    elif a.what.startswith("latent") or a.what == "verify":
+        run, units, count = latent_case(a, dev, stream)
     elif a.what == "decode_multi":
         d = workloads.decode_case(N=a.N, H=a.H, D=a.D, steps=a.K, seed=4, device=dev)
         tok = {key: torch.stack([s[key] for s in d.steps], dim=1).contiguous()
