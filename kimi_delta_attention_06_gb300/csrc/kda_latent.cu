@@ -250,11 +250,18 @@ struct LatShape {
     // bf16: 9 slabs of 64 values; e4m3: 4 slabs of 128 codes, the position key's, 64 scales of 16 bytes
     static constexpr uint32_t kSlabs = E4M3 ? 5u : 9u, kStage = kSlabs * kSlabC + (E4M3 ? 1024u : 0u);
     // Q: 9 slabs of 64 bf16; e4m3: 2 terms x 4 slabs of 128 codes, then the position part's
-    static constexpr uint32_t kP = E4M3 ? 3u : 1u;                                    // tiles of P
+    // e4m3: the three terms of P lie side by side along N where TMEM holds three accumulators for them
+    // (R <= 32: the codes are then read once for all three; 2590 -> 2050 clocks a tile at R = 32), else
+    // in tiles of their own that share one accumulator
+    static constexpr bool kSide = E4M3 && R <= 32;
+    static constexpr uint32_t kO = kSide ? 3u * R : R;                                // TMEM columns of a block of O
+    static constexpr uint32_t kP = E4M3 && !kSide ? 3u : 1u;                          // tiles of P
     static constexpr uint32_t oQ = 0, oC = 9u * kSlabQ, oP = oC + kStages * kStage, oBar = oP + kP * kTile * 128u;
     static constexpr uint32_t kBytes = oBar + 96u + 7u * R * 4u;
     static constexpr uint32_t kS = E4M3 ? 2u * R : R;                                 // TMEM columns of one S buffer
-    static constexpr uint32_t kTmemCols = R == 16 ? 128u : R == 32 ? 256u : 512u;     // 4 R (O) + 2 kS
+    static constexpr uint32_t kUsed = 4u * kO + 2u * kS;
+    static constexpr uint32_t kTmemCols = kUsed <= 128u ? 128u : kUsed <= 256u ? 256u : 512u;
+    static_assert(kUsed <= 512u, "TMEM");
 };
 static_assert(LatShape<64, false>::kBytes <= 232448 && LatShape<64, true>::kBytes <= 232448, "227 KB of shared memory");
 
@@ -286,6 +293,22 @@ __device__ __forceinline__ void tmem_ld_s(uint32_t ta, float (&r)[R / 2]) {
                          : "r"(ta + 32u * i));
     }
     tc::tmem_wait_ld();
+}
+
+// 16 rows of a block of O (the sum of its three accumulators where P's terms lie side by side).
+template <int R, bool SIDE>
+__device__ __forceinline__ void load_o(uint32_t ta, float (&o)[16]) {
+    tc::tmem_ld16(ta, o);
+    if constexpr (SIDE) {
+        float p[16], q[16];
+        tc::tmem_ld16(ta + R, p);
+        tc::tmem_ld16(ta + 2 * R, q);
+        tc::tmem_wait_ld();
+#pragma unroll
+        for (int i = 0; i < 16; ++i) o[i] += p[i] + q[i];
+    } else {
+        tc::tmem_wait_ld();
+    }
 }
 
 // Row (n, j, h) again, in fp32 over exactly the tokens it sees: for results that a NaN or infinity
@@ -341,7 +364,7 @@ kda_latent_decode_kernel(const __grid_constant__ LatMaps maps, const LatArgs a)
     __syncthreads();
     tc::fence_after_sync();
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");   // the combine kernel waits for this grid's end
-    const uint32_t tm = *s_tmem, tmO = tm, tmS = tm + 4 * R;
+    const uint32_t tm = *s_tmem, tmO = tm, tmS = tm + 4 * Sh::kO;
     SegWalk sw;
     sw.init(a.w, run);
     bool ok = true;
@@ -488,19 +511,20 @@ kda_latent_decode_kernel(const __grid_constant__ LatMaps maps, const LatArgs a)
                     tc::named_sync(kBarSoft, Sh::kSoft);
                     if (t > sw.t0) {                            // O *= f, 16 columns (rows) at a time
 #pragma unroll 1
-                        for (int c0 = 0; c0 < R; c0 += 16) {
+                        for (int c0 = 0; c0 < static_cast<int>(Sh::kO); c0 += 16) {
+                            const float* f = s_f + c0 % R;
                             bool one = true;
 #pragma unroll
-                            for (int i = 0; i < 16; ++i) one = one && s_f[c0 + i] == 1.f;
+                            for (int i = 0; i < 16; ++i) one = one && f[i] == 1.f;
                             if (one) continue;
 #pragma unroll 1
                             for (int b = 0; b < 4; ++b) {
                                 float o[16];
-                                tc::tmem_ld16(tmO + b * R + c0 + lane_tm, o);
+                                tc::tmem_ld16(tmO + b * Sh::kO + c0 + lane_tm, o);
                                 tc::tmem_wait_ld();
 #pragma unroll
-                                for (int i = 0; i < 16; ++i) o[i] *= s_f[c0 + i];
-                                tc::tmem_st16(tmO + b * R + c0 + lane_tm, o);
+                                for (int i = 0; i < 16; ++i) o[i] *= f[i];
+                                tc::tmem_st16(tmO + b * Sh::kO + c0 + lane_tm, o);
                             }
                         }
                         tc::tmem_wait_st();
@@ -545,10 +569,10 @@ kda_latent_decode_kernel(const __grid_constant__ LatMaps maps, const LatArgs a)
                         *reinterpret_cast<uint32_t*>(sP + off) = pk[2 * b];
                         *reinterpret_cast<uint32_t*>(sP + off + 8 * 128) = pk[2 * b + 1];    // token + 8: same swizzle
                     } else {
-                        const uint32_t n = 8 * b + rq, off = tr * 128 + (((n >> 4) ^ (tr & 7)) << 4) + (n & 15);
 #pragma unroll
                         for (int k = 0; k < 3; ++k) {
-                            uint8_t* d = sP + k * kTile * 128 + off;
+                            const uint32_t n = 8 * b + rq + (Sh::kSide ? k * R : 0);
+                            uint8_t* d = sP + (Sh::kSide ? 0 : k * kTile * 128) + tr * 128 + (((n >> 4) ^ (tr & 7)) << 4) + (n & 15);
                             *reinterpret_cast<uint16_t*>(d) = static_cast<uint16_t>(pk[3 * b + k]);
                             *reinterpret_cast<uint16_t*>(d + 8 * 128) = static_cast<uint16_t>(pk[3 * b + k] >> 16);
                         }
@@ -591,8 +615,7 @@ kda_latent_decode_kernel(const __grid_constant__ LatMaps maps, const LatArgs a)
 #pragma unroll 1
                 for (int c = 0; c < R / 4; ++c) {                // 16 rows x 128 channels a step
                     float o[16];
-                    tc::tmem_ld16(tmO + (c & 3) * R + (c >> 2) * 16 + lane_tm, o);
-                    tc::tmem_wait_ld();
+                    load_o<R, Sh::kSide>(tmO + (c & 3) * Sh::kO + (c >> 2) * 16 + lane_tm, o);
                     float* d = d32 + (c >> 2) * 16 * kLatDim + (c & 3) * 128;
 #pragma unroll
                     for (int i = 0; i < 16; ++i) d[i * kLatDim] = o[i];
@@ -608,8 +631,7 @@ kda_latent_decode_kernel(const __grid_constant__ LatMaps maps, const LatArgs a)
                     const int c0 = (c >> 2) * 16;
                     if (c0 >= nrows) break;
                     float o[16];
-                    tc::tmem_ld16(tmO + (c & 3) * R + c0 + lane_tm, o);
-                    tc::tmem_wait_ld();
+                    load_o<R, Sh::kSide>(tmO + (c & 3) * Sh::kO + c0 + lane_tm, o);
                     uint16_t* d = d16 + c0 * kLatDim + (c & 3) * 128;
                     float check = 0.f;
 #pragma unroll
@@ -655,7 +677,7 @@ kda_latent_decode_kernel(const __grid_constant__ LatMaps maps, const LatArgs a)
         // One thread runs it all: the tensor cores queue only about two products, so what stands between
         // two groups of them (a vote, an election) is lost
         constexpr uint32_t id_s = tc::idesc(64, R, tc::kFmtBF16, false, false);
-        constexpr uint32_t id_o = E4M3 ? tc::idesc8(128, R, tc::kFmtE4M3, tc::kFmtE5M2, true, true)
+        constexpr uint32_t id_o = E4M3 ? tc::idesc8(128, Sh::kO, tc::kFmtE4M3, tc::kFmtE5M2, true, true)
                                        : tc::idesc(128, R, tc::kFmtBF16, true, true);
         constexpr uint32_t id_c = tc::idesc8(64, R, tc::kFmtE4M3, tc::kFmtE4M3, false, false);
         // descriptors: constant high words, low words = address / 16 and the leading offset
@@ -687,6 +709,11 @@ kda_latent_decode_kernel(const __grid_constant__ LatMaps maps, const LatArgs a)
                         for (uint32_t k = 0; k < 4; ++k)
                             tc::mma_f16_lo(tmO + b * R, c + ((b * 2u * Sh::kSlabC + k * 2048u) >> 4), hi,
                                            p_lo + (k * 2048u >> 4), hi, id_o, k > 0 ? 1u : acc);
+                    } else if constexpr (Sh::kSide) {
+#pragma unroll
+                        for (uint32_t k = 0; k < 2; ++k)     // 2 steps of 32 tokens, all terms at once
+                            tc::mma_f8_lo(tmO + b * Sh::kO, c + ((b * Sh::kSlabC + k * 4096u) >> 4), hi,
+                                          p_lo + (k * 4096u >> 4), hi, id_o, k > 0 ? 1u : acc);
                     } else {
 #pragma unroll
                         for (uint32_t k = 0; k < 6; ++k)     // 2 steps of 32 tokens x 3 terms
