@@ -46,13 +46,12 @@ __device__ __forceinline__ uint32_t f32x2_to_e4m3x2(float lo, float hi) {
 // e5m2 is fp16 with 2 of its 10 fraction bits, so rounding the magnitude's low byte away rounds to
 // e5m2; the code is the upper byte.  (Halves round up; a NaN is not kept.)
 __device__ __forceinline__ uint32_t f16x2_round_e5m2(uint32_t h) { return (h + 0x00800080u) & 0xff00ff00u; }
-// e4m3 codes of x are the bits 13..7 of fp16 values x / 2^8 (both formats' subnormals line up: 2^-6 / 2^8
-// = 2^-14), for |x| <= 448.  Here h holds x / 2^8 and the result is the rounded x / 2^8.
-__device__ __forceinline__ uint32_t f16x2_round_e4m3(uint32_t h) {
-    return (((h & 0x7fff7fffu) + 0x00400040u) & 0x7f807f80u) | (h & 0x80008000u);
-}
-// The two e4m3 codes of such a rounded pair, in bytes 0 and 2.
-__device__ __forceinline__ uint32_t e4m3_codes(uint32_t r) { return ((r & 0x7f807f80u) >> 7) | ((r & 0x80008000u) >> 8); }
+// e4m3 codes of x are the bits 13..7 of fp16 values x / 2^8 and the sign (both formats' subnormals line
+// up: 2^-6 / 2^8 = 2^-14), for |x| <= 448.  Here h holds x / 2^8 (at most 1.75: no carry leaves its
+// half) and the result is the rounded x / 2^8.
+__device__ __forceinline__ uint32_t f16x2_round_e4m3(uint32_t h) { return (h + 0x00400040u) & 0xff80ff80u; }
+// The two e4m3 codes of such a rounded pair, in bytes 0 and 2 (bytes 1 and 3: anything).
+__device__ __forceinline__ uint32_t e4m3_codes(uint32_t r) { return ((r >> 7) & 0x007f007fu) | ((r >> 8) & ~0x007f007fu); }
 __device__ __forceinline__ uint32_t f16x2_sub(uint32_t a, uint32_t b) {
     uint32_t d;
     asm("sub.rn.f16x2 %0, %1, %2;" : "=r"(d) : "r"(a), "r"(b));
