@@ -312,7 +312,7 @@ kda_expanded_kernel(const __grid_constant__ ExpMaps maps, const ExpArgs a)
     } else if (warp == 8) {
         // ---- products, in the order PV 0, QK 0, PV 1, QK 1 of consecutive key tiles ----
         constexpr uint32_t id_s = tc::idesc(128, 128, tc::kFmtBF16, false, false);
-        constexpr uint32_t id_o = tc::idesc(128, 64, tc::kFmtBF16, false, true);
+        constexpr uint32_t id_o = tc::idesc(128, 64, tc::kFmtBF16, false, true), id_o2 = tc::idesc(128, 128, tc::kFmtBF16, false, true);
         const uint64_t d0 = tc::sdesc(0, 16, 1024, tc::kSwizzle128B), dV = tc::sdesc(0, kSlab, 1024, tc::kSwizzle128B);
         const uint32_t hi = static_cast<uint32_t>(d0 >> 32);
         const uint32_t q_lo = static_cast<uint32_t>(d0) | (tc::smem_u32(smem + oExpQ) >> 4);
@@ -337,7 +337,7 @@ kda_expanded_kernel(const __grid_constant__ ExpMaps maps, const ExpArgs a)
             }
             tc::mma_commit(&s_full[w]);
         };
-        auto pv = [&](int w, int j) {                            // O_w += P_w V_j, half the keys, then half the channels a slab
+        auto pv = [&](int w, int j) {                            // O_w += P_w V_j, half the keys at a time
             const uint32_t i = 5u * j + 3u, s0 = i & (kRing - 1), s1 = (i + 1u) & (kRing - 1);
             const uint32_t b0 = v_lo + s0 * (kSlab >> 4), b1 = v_lo + s1 * (kSlab >> 4);
             const uint32_t d = tm + 256u + w * 128u, p = tm + w * 128u, acc = j > 0 ? 1u : 0u;
@@ -346,10 +346,16 @@ kda_expanded_kernel(const __grid_constant__ ExpMaps maps, const ExpArgs a)
             for (uint32_t half = 0; half < 2; ++half) {
                 if (!wait(&p_full[2 * w + half], j & 1)) return;
                 tc::fence_after_sync();
+                if (s0 + 1u == s1) {                             // V's two slabs adjacent: all channels at once
 #pragma unroll
-                for (uint32_t k = 4 * half; k < 4 * half + 4; ++k) {
-                    tc::mma_f16_ta(d, p + k * 8u, b0 + k * 128u, hi, id_o, k > 0 ? 1u : acc);
-                    tc::mma_f16_ta(d + 64u, p + k * 8u, b1 + k * 128u, hi, id_o, k > 0 ? 1u : acc);
+                    for (uint32_t k = 4 * half; k < 4 * half + 4; ++k)
+                        tc::mma_f16_ta(d, p + k * 8u, b0 + k * 128u, hi, id_o2, k > 0 ? 1u : acc);
+                } else {                                         // (every eighth tile: the ring wraps between them)
+#pragma unroll
+                    for (uint32_t k = 4 * half; k < 4 * half + 4; ++k) {
+                        tc::mma_f16_ta(d, p + k * 8u, b0 + k * 128u, hi, id_o, k > 0 ? 1u : acc);
+                        tc::mma_f16_ta(d + 64u, p + k * 8u, b1 + k * 128u, hi, id_o, k > 0 ? 1u : acc);
+                    }
                 }
             }
         };
