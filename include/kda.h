@@ -469,7 +469,10 @@ int kda_latent_gather(const void* cache, int cache_dtype, int num_pages, int pag
  *     x_t = sm_scale * (q[:512] . c_t + q[512:] . r_t),  out = sum_t softmax(x)_t c_t
  * A query that sees nothing gives zeros and lse = -inf.  Cache rows past the end of a sequence
  * (the rest of its last page) are never part of a result, whatever they hold.  Softmax
- * statistics and sums are fp32; the probabilities enter the second product as bf16.
+ * statistics and sums are fp32.  The probabilities enter the second product as bf16; over an
+ * e4m3 cache, times the token's scale, as a sum of three e5m2 values (9 bits; weighted latents
+ * below 2^-26 of the largest are rounded to that step, and results below 2^-80 may vanish), and the
+ * query as a sum of two e4m3 values (8 bits).
  * 1 <= K * H <= KDA_LATENT_MAX_ROWS, else KDA_ERR_UNSUPPORTED.  seq_lens[n] outside
  * [0, max_pages * page_size] counts as 0 and is reported; a page outside [0, num_pages) is
  * reported and leaves the sequence's outputs unspecified.  Scratch: partial results of at most

@@ -441,8 +441,9 @@ kda_latent_decode_kernel(const __grid_constant__ LatMaps maps, const LatArgs a)
                         const float* sc = reinterpret_cast<const float*>(sC + g % NS * Sh::kStage + Sh::kSlabs * Sh::kSlabC);
                         s0 = sc[(16 * warp + tq) * 4];
                         s1 = sc[(16 * warp + tq + 8) * 4];
-                        e0 = static_cast<float>(static_cast<int>(__float_as_uint(s0) >> 23) - 127);
-                        e1 = static_cast<float>(static_cast<int>(__float_as_uint(s1) >> 23) - 127);
+                        // (held above -90, so that the sums of 2^(x - m) stay within fp32; see f0, f1)
+                        e0 = static_cast<float>(max(static_cast<int>(__float_as_uint(s0) >> 23) - 127, -90));
+                        e1 = static_cast<float>(max(static_cast<int>(__float_as_uint(s1) >> 23) - 127, -90));
                         float xr[R / 2];
                         tmem_ld_s<R>(tmS + (g & 1) * Sh::kS + R + lane_tm, xr);
                         // x: scores in powers of two, plus the scale's exponent (the weights carry s)
@@ -474,8 +475,8 @@ kda_latent_decode_kernel(const __grid_constant__ LatMaps maps, const LatArgs a)
                             *reinterpret_cast<uint4*>(c + slab * Sh::kSlabC + r * 128 + ch * 16) = make_uint4(0, 0, 0, 0);
                         }
                         if (E4M3) {                             // and their scales are not to be used
-                            if (16 * warp + tq >= valid) s0 = 1.f;
-                            if (16 * warp + tq + 8 >= valid) s1 = 1.f;
+                            if (16 * warp + tq >= valid) { s0 = 1.f; e0 = 0.f; }
+                            if (16 * warp + tq + 8 >= valid) { s1 = 1.f; e1 = 0.f; }
                         }
                     }
                 }
@@ -533,7 +534,9 @@ kda_latent_decode_kernel(const __grid_constant__ LatMaps maps, const LatArgs a)
                 // P = exp2(x - m), rounded for the product (see above); the sums keep fp32.  It is made in
                 // registers while the previous tile's product still reads P
                 const int tr = 16 * warp + tq;
-                const float r0 = 1.f / s0, r1 = 1.f / s1;       // (powers of two)
+                // e4m3: exp2(x - m) carries 2^e; the sums take it out (r0, r1), and a scale below 2^-90 puts the
+                // rest of it in (f0, f1, else 1).  A NaN score leaves no NaN in P, but one in the sums
+                const float r0 = lat_ex2(-e0), r1 = lat_ex2(-e1), f0 = s0 * r0, f1 = s1 * r1;
                 uint32_t pk[E4M3 ? 3 * (R / 8) : R / 4];
 #pragma unroll
                 for (int b = 0; b < R / 8; ++b) {
@@ -548,7 +551,7 @@ kda_latent_decode_kernel(const __grid_constant__ LatMaps maps, const LatArgs a)
                     } else {
                         l[2 * b] += fmaf(p0, r0, p2 * r1);
                         l[2 * b + 1] += fmaf(p1, r0, p3 * r1);
-                        uint32_t u = f32x2_to_f16x2(p0, p1), v = f32x2_to_f16x2(p2, p3);
+                        uint32_t u = f32x2_to_f16x2(p0 * f0, p1 * f0), v = f32x2_to_f16x2(p2 * f1, p3 * f1);
 #pragma unroll
                         for (int k = 0; k < 3; ++k) {           // three terms, each the rounding of what is left
                             const uint32_t ru = f16x2_round_e5m2(u), rv = f16x2_round_e5m2(v);
