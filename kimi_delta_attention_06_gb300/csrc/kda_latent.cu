@@ -353,6 +353,11 @@ kda_latent_decode_kernel(const __grid_constant__ LatMaps maps, const LatArgs a)
         tc::mbar_init(q_full, E4M3 ? Sh::kSoft : 1);
         tc::mbar_fence_init();
     }
+    {   // the page table goes to L2 while the lengths that say where to read it are on their way: a line a thread
+        const size_t lines = (static_cast<size_t>(a.w.N) * a.ch.max_pages * 4 + 127) / 128;
+        const size_t mine = static_cast<size_t>(blockIdx.x) * Sh::kThreads + tid;
+        if (mine < lines) asm volatile("prefetch.global.L2 [%0];" :: "l"(reinterpret_cast<const uint8_t*>(a.ch.table) + mine * 128));
+    }
     if (tid == 0) {
         tc::tma_prefetch_map(&maps.c);
         if (E4M3) tc::tma_prefetch_map(&maps.s);
