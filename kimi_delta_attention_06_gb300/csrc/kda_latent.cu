@@ -245,7 +245,8 @@ struct LatShape {
     static constexpr int kSoft = 128;            // warps 0..3: softmax, rescale, epilogue
     static constexpr int kMmaWarp = 4, kTmaWarp = 5;
     static constexpr int kThreads = 192;
-    static constexpr int kStages = E4M3 ? 3 : 2;
+    // as many as fit: a stage is taken for a copy's latency (about 3000 clocks) and both products
+    static constexpr int kStages = E4M3 ? (R <= 32 ? 4 : 3) : 2;
     static constexpr uint32_t kSlabQ = R * 128u, kSlabC = kTile * 128u;
     // bf16: 9 slabs of 64 values; e4m3: 4 slabs of 128 codes, the position key's, 64 scales of 16 bytes
     static constexpr uint32_t kSlabs = E4M3 ? 5u : 9u, kStage = kSlabs * kSlabC + (E4M3 ? 1024u : 0u);
@@ -257,7 +258,7 @@ struct LatShape {
     static constexpr uint32_t kO = kSide ? 3u * R : R;                                // TMEM columns of a block of O
     static constexpr uint32_t kP = E4M3 && !kSide ? 3u : 1u;                          // tiles of P
     static constexpr uint32_t oQ = 0, oC = 9u * kSlabQ, oP = oC + kStages * kStage, oBar = oP + kP * kTile * 128u;
-    static constexpr uint32_t kBytes = oBar + 96u + 7u * R * 4u;
+    static constexpr uint32_t kBytes = oBar + 112u + 7u * R * 4u;
     static constexpr uint32_t kS = E4M3 ? 2u * R : R;                                 // TMEM columns of one S buffer
     static constexpr uint32_t kUsed = 4u * kO + 2u * kS;
     static constexpr uint32_t kTmemCols = kUsed <= 128u ? 128u : kUsed <= 256u ? 256u : 512u;
@@ -330,9 +331,9 @@ kda_latent_decode_kernel(const __grid_constant__ LatMaps maps, const LatArgs a)
     uint8_t* sC = smem + Sh::oC;
     uint8_t* sP = smem + Sh::oP;
     uint64_t* bars = reinterpret_cast<uint64_t*>(smem + Sh::oBar);
-    uint64_t *full = bars, *empty = bars + 3, *s_full = bars + 6, *p_full = bars + 8, *q_full = bars + 9;
-    uint32_t* s_tmem = reinterpret_cast<uint32_t*>(bars + 10);
-    float* s_red = reinterpret_cast<float*>(bars + 12);         // [4][R]
+    uint64_t *full = bars, *empty = bars + 4, *s_full = bars + 8, *p_full = bars + 10, *q_full = bars + 11;
+    uint32_t* s_tmem = reinterpret_cast<uint32_t*>(bars + 12);
+    float* s_red = reinterpret_cast<float*>(bars + 14);         // [4][R]
     float* s_f = s_red + 4 * R;                                 // [R]
     int* s_j = reinterpret_cast<int*>(s_f + R);                 // [R]: query token of each row
     float* s_a = s_f + 2 * R;                                   // [R]: e4m3: 2^k * scale of each row
