@@ -277,14 +277,14 @@ int launch_verify(const float* tp, long long ldp, const float* dp, long long ldq
                   const int32_t* num_draft, const float* ua, const float* us, int N, int K, int V, int32_t* out,
                   int32_t* num_out, int* status, cudaStream_t stream)
 {
-    // Few sequences: 16 CTAs of 16 warps each (16 is past the portable cluster size), so that a row
-    // of 131072 is one round of loads.  Many: the fewest CTAs of 8 warps that fill the device (three
-    // an SM), as each one's acceptance, exchange and narrowing are latency that more of them only
-    // repeat (256 rows of 100003 at 8 CTAs a row: 59 us, at 2: 54 us); slices of 2048 tokens at least.
-    const bool few = static_cast<long long>(N) * 16 <= 152 && V > 8 * 4096;
-    const int most = few ? 16 : 8, warps = few ? 16 : 8;
+    // CTAs of 16 warps; the fewest a row that give every SM one, as each one's acceptance, exchange
+    // and narrowing are latency that more of them only repeat (256 rows of 100003: 48.6 us at one CTA
+    // a row, 55 at two; of 8 warps 54 at two, 52 at four, 59 at eight).  Few sequences take up to 16 (past
+    // the portable cluster size), so that a row of 131072 is one round of loads; slices of 2048 tokens
+    // at least.
+    const int most = static_cast<long long>(N) * 16 <= 152 && V > 8 * 4096 ? 16 : 8, warps = 16;
     int C = 1;
-    while (C < most && static_cast<long long>(N) * C < 3 * 152 && V / (2 * C) >= 2048) C *= 2;
+    while (C < most && static_cast<long long>(N) * C < 152 && V / (2 * C) >= 2048) C *= 2;
     static bool wide_done[kMaxDevicesAttr] = {};
     int dev = 0;
     if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= kMaxDevicesAttr) return -3;
