@@ -357,15 +357,25 @@ def _dense(t: Optional[torch.Tensor], dtype):
     return t.data_ptr()
 
 
-def _rows(t: torch.Tensor, dtype, *least: int):
-    """(address, strides of the leading dimensions in elements) of a tensor whose last dimension is
-    contiguous; a dimension of one entry has any stride: `least`, which the checks pass."""
+def _rows2(t: torch.Tensor, dtype, least: int):
+    """(address, row stride in elements) of a 2-D tensor whose rows are contiguous; one row has any
+    stride: `least`, which the checks pass."""
+    if t.dtype != dtype:
+        raise TypeError(f"expected a {dtype} tensor, got {t.dtype}")
+    st = t.stride()
+    if st[1] != 1 and t.numel():
+        raise ValueError("the last dimension of a KDA tensor must be contiguous")
+    return t.data_ptr(), st[0] if t.shape[0] > 1 else least
+
+
+def _rows3(t: torch.Tensor, dtype, least0: int, least1: int):
+    """The same of a 3-D tensor: (address, strides of its first two dimensions)."""
     if t.dtype != dtype:
         raise TypeError(f"expected a {dtype} tensor, got {t.dtype}")
     st, shape = t.stride(), t.shape
-    if st[-1] != 1 and t.numel():
+    if st[2] != 1 and t.numel():
         raise ValueError("the last dimension of a KDA tensor must be contiguous")
-    return (t.data_ptr(), *(st[i] if shape[i] > 1 else x for i, x in enumerate(least)))
+    return t.data_ptr(), st[0] if shape[0] > 1 else least0, st[1] if shape[1] > 1 else least1
 
 
 def _host32(t):
@@ -398,8 +408,8 @@ def _pages(cache: torch.Tensor, cache_dtype: int):
 
 
 def kda_latent_append(c, k_rope, cache, cache_dtype: int, slots, total_tokens: int, stream=None):
-    cp, ldc = _rows(c, _BF16, KDA_LATENT_DIM)
-    rp, ldr = _rows(k_rope, _BF16, KDA_LATENT_ROPE)
+    cp, ldc = _rows2(c, _BF16, KDA_LATENT_DIM)
+    rp, ldr = _rows2(k_rope, _BF16, KDA_LATENT_ROPE)
     p, num_pages, page_size = _pages(cache, cache_dtype)
     rc = load().kda_latent_append(cp, ldc, rp, ldr, p, cache_dtype, num_pages, page_size, _dense(slots, _I32),
                                   total_tokens, _stream(stream))
@@ -407,12 +417,12 @@ def kda_latent_append(c, k_rope, cache, cache_dtype: int, slots, total_tokens: i
         _check(rc, "kda_latent_append")
 
 
-def kda_latent_gather(cache, cache_dtype: int, block_table, start_pos, cu_seqlens, cu_seqlens_host, num_seqs: int,
-                      total_tokens: int, c, k_rope, stream=None):
+# (the calls themselves, with the outputs as addresses: the functions that allocate outputs have nothing
+# to check about them)
+
+def _latent_gather(cache, cache_dtype, block_table, start_pos, cu_seqlens, cu_host, num_seqs, total_tokens, cp, ldc, rp,
+                   ldr, stream):
     p, num_pages, page_size = _pages(cache, cache_dtype)
-    cu_host = _host32(cu_seqlens_host)
-    cp, ldc = _rows(c, _BF16, KDA_LATENT_DIM)
-    rp, ldr = _rows(k_rope, _BF16, KDA_LATENT_ROPE)
     rc = load().kda_latent_gather(p, cache_dtype, num_pages, page_size, _dense(block_table, _I32), block_table.shape[1],
                                   _dense(start_pos, _I32), _dense(cu_seqlens, _I32), cu_host.data_ptr(), num_seqs,
                                   total_tokens, cp, ldc, rp, ldr, _stream(stream))
@@ -420,46 +430,71 @@ def kda_latent_gather(cache, cache_dtype: int, block_table, start_pos, cu_seqlen
         _check(rc, "kda_latent_gather")
 
 
-def kda_latent_decode(q, cache, cache_dtype: int, block_table, seq_lens, N: int, K: int, H: int, sm_scale: float, out,
-                      lse, stream=None):
+def _latent_decode(q, cache, cache_dtype, block_table, seq_lens, N, K, H, sm_scale, out, lse, stream):
     p, num_pages, page_size = _pages(cache, cache_dtype)
     rc = load().kda_latent_decode(_dense(q, _BF16), p, cache_dtype, num_pages, page_size, _dense(block_table, _I32),
-                                  block_table.shape[1], _dense(seq_lens, _I32), N, K, H, sm_scale, _dense(out, _BF16),
-                                  _dense(lse, _F32), _stream(stream))
+                                  block_table.shape[1], _dense(seq_lens, _I32), N, K, H, sm_scale, out, lse,
+                                  _stream(stream))
     if rc:
         _check(rc, "kda_latent_decode")
 
 
-def kda_latent_prefill(q, k, v, k_rope, cu_q, cu_q_host, cu_k, cu_k_host, num_seqs: int, total_q: int, total_k: int,
-                       H: int, causal: int, sm_scale: float, out, lse, stream=None):
-    cq, ck = _host32(cu_q_host), _host32(cu_k_host)
-    kp, ldk, hdk = _rows(k, _BF16, 128, 128)
-    vp, ldv, hdv = _rows(v, _BF16, 128, 128)
-    rp, ldr = _rows(k_rope, _BF16, KDA_LATENT_ROPE)
+def _latent_prefill(q, k, v, k_rope, cu_q, cq, cu_k, ck, num_seqs, total_q, total_k, H, causal, sm_scale, out, lse, stream):
+    kp, ldk, hdk = _rows3(k, _BF16, 128, 128)
+    vp, ldv, hdv = _rows3(v, _BF16, 128, 128)
+    rp, ldr = _rows2(k_rope, _BF16, KDA_LATENT_ROPE)
     rc = load().kda_latent_prefill(_dense(q, _BF16), kp, ldk, hdk, vp, ldv, hdv, rp, ldr, _dense(cu_q, _I32), cq.data_ptr(),
                                    _dense(cu_k, _I32), ck.data_ptr(), num_seqs, total_q, total_k, H, causal, sm_scale,
-                                   _dense(out, _BF16), _dense(lse, _F32), _stream(stream))
+                                   out, lse, _stream(stream))
     if rc:
         _check(rc, "kda_latent_prefill")
 
 
-def kda_verify_draft(target_probs, draft_probs, draft_tokens, num_draft, u_accept, u_sample, N: int, K: int, V: int,
-                     tokens, num_tokens, stream=None):
-    def rows(t, per):           # rows of V values, one constant stride apart
-        if t is None:
-            return None, 0
-        p, seq, ld = _rows(t, _F32, per * V, V)
-        if t.shape[0] > 1 and per > 1 and seq != per * ld:
-            raise ValueError("the probability rows of consecutive sequences must be evenly spaced")
-        return p, seq if per == 1 else ld
+def _prob_rows(t, per: int, V: int):
+    """(address, stride) of probabilities [N, per, V] whose N * per rows are one constant stride apart."""
+    p, seq, ld = _rows3(t, _F32, -1, V)
+    if per <= 1:
+        return p, V if seq < 0 else seq
+    if seq >= 0 and seq != per * ld:
+        raise ValueError("the probability rows of consecutive sequences must be evenly spaced")
+    return p, ld
 
-    tp, ldp = rows(target_probs, K + 1)
-    dp, ldq = rows(draft_probs, K)
+
+def _verify_draft(target_probs, draft_probs, draft_tokens, num_draft, u_accept, u_sample, N, K, V, tokens, num_tokens,
+                  stream):
+    tp, ldp = _prob_rows(target_probs, K + 1, V)
+    dp, ldq = (None, 0) if draft_probs is None else _prob_rows(draft_probs, K, V)
     rc = load().kda_verify_draft(tp, ldp, dp, ldq, _dense(draft_tokens, _I32), _dense(num_draft, _I32),
-                                 _dense(u_accept, _F32), _dense(u_sample, _F32), N, K, V, _dense(tokens, _I32),
-                                 _dense(num_tokens, _I32), _stream(stream))
+                                 _dense(u_accept, _F32), _dense(u_sample, _F32), N, K, V, tokens, num_tokens,
+                                 _stream(stream))
     if rc:
         _check(rc, "kda_verify_draft")
+
+
+def kda_latent_gather(cache, cache_dtype: int, block_table, start_pos, cu_seqlens, cu_seqlens_host, num_seqs: int,
+                      total_tokens: int, c, k_rope, stream=None):
+    cp, ldc = _rows2(c, _BF16, KDA_LATENT_DIM)
+    rp, ldr = _rows2(k_rope, _BF16, KDA_LATENT_ROPE)
+    _latent_gather(cache, cache_dtype, block_table, start_pos, cu_seqlens, _host32(cu_seqlens_host), num_seqs, total_tokens,
+                   cp, ldc, rp, ldr, stream)
+
+
+def kda_latent_decode(q, cache, cache_dtype: int, block_table, seq_lens, N: int, K: int, H: int, sm_scale: float, out,
+                      lse, stream=None):
+    _latent_decode(q, cache, cache_dtype, block_table, seq_lens, N, K, H, sm_scale, _dense(out, _BF16), _dense(lse, _F32),
+                   stream)
+
+
+def kda_latent_prefill(q, k, v, k_rope, cu_q, cu_q_host, cu_k, cu_k_host, num_seqs: int, total_q: int, total_k: int,
+                       H: int, causal: int, sm_scale: float, out, lse, stream=None):
+    _latent_prefill(q, k, v, k_rope, cu_q, _host32(cu_q_host), cu_k, _host32(cu_k_host), num_seqs, total_q, total_k, H,
+                    causal, sm_scale, _dense(out, _BF16), _dense(lse, _F32), stream)
+
+
+def kda_verify_draft(target_probs, draft_probs, draft_tokens, num_draft, u_accept, u_sample, N: int, K: int, V: int,
+                     tokens, num_tokens, stream=None):
+    _verify_draft(target_probs, draft_probs, draft_tokens, num_draft, u_accept, u_sample, N, K, V, _dense(tokens, _I32),
+                  _dense(num_tokens, _I32), stream)
 
 
 def kda_debug_expire_wait(limit_ns: int, stream=None):
@@ -541,7 +576,8 @@ def latent_gather(cache, cache_dtype: int, block_table, cu_seqlens_host, cu_seql
         cu_seqlens = cu_host.to(dev)
     c = torch.empty((T, KDA_LATENT_DIM), device=dev, dtype=_BF16)
     r = torch.empty((T, KDA_LATENT_ROPE), device=dev, dtype=_BF16)
-    kda_latent_gather(cache, cache_dtype, block_table, start_pos, cu_seqlens, cu_host, N, T, c, r, stream)
+    _latent_gather(cache, cache_dtype, block_table, start_pos, cu_seqlens, cu_host, N, T, c.data_ptr(), KDA_LATENT_DIM,
+                   r.data_ptr(), KDA_LATENT_ROPE, stream)
     return c, r
 
 
@@ -552,7 +588,8 @@ def latent_decode(q, cache, cache_dtype: int, block_table, seq_lens, sm_scale: f
     dev = q.device
     out = torch.empty((N, K, H, KDA_LATENT_DIM), device=dev, dtype=_BF16)
     lse = torch.empty((N, K, H), device=dev, dtype=_F32) if want_lse else None
-    kda_latent_decode(q, cache, cache_dtype, block_table, seq_lens, N, K, H, sm_scale, out, lse, stream)
+    _latent_decode(q, cache, cache_dtype, block_table, seq_lens, N, K, H, sm_scale, out.data_ptr(),
+                   lse.data_ptr() if want_lse else None, stream)
     return out, lse
 
 
@@ -569,8 +606,8 @@ def latent_prefill(q, k, v, k_rope, cu_q_host, cu_k_host, sm_scale: float, causa
     Tq, H, _ = q.shape
     out = torch.empty((Tq, H, 128), device=dev, dtype=_BF16)
     lse = torch.empty((Tq, H), device=dev, dtype=_F32) if want_lse else None
-    kda_latent_prefill(q, k, v, k_rope, cu_q, cq, cu_k, ck, cq.numel() - 1, Tq, k.shape[0], H, int(causal), sm_scale, out,
-                       lse, stream)
+    _latent_prefill(q, k, v, k_rope, cu_q, cq, cu_k, ck, cq.numel() - 1, Tq, k.shape[0], H, int(causal), sm_scale,
+                    out.data_ptr(), lse.data_ptr() if want_lse else None, stream)
     return out, lse
 
 
@@ -581,6 +618,6 @@ def verify_draft(target_probs, draft_probs, draft_tokens, u_accept, u_sample, nu
     dev = target_probs.device
     tokens = torch.empty((N, K1), device=dev, dtype=_I32)
     num = torch.empty((N,), device=dev, dtype=_I32)
-    kda_verify_draft(target_probs, draft_probs, draft_tokens, num_draft, u_accept, u_sample, N, K1 - 1, V, tokens, num,
-                     stream)
+    _verify_draft(target_probs, draft_probs, draft_tokens, num_draft, u_accept, u_sample, N, K1 - 1, V, tokens.data_ptr(),
+                  num.data_ptr(), stream)
     return tokens, num

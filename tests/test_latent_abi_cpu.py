@@ -123,3 +123,8 @@ def test_python_binding_checks_types_and_layouts(lib):
     p = torch.zeros(4, 3, 8)[::2]                              # rows of consecutive sequences unevenly spaced
     with pytest.raises(ValueError):
         kda.kda_verify_draft(p, None, slots, None, p, p, 2, 2, 8, slots, slots, stream=0)
+    p = torch.zeros(1, 3, 8).expand(2, 3, 8)                    # one sequence's rows for all
+    with pytest.raises(ValueError):
+        kda.kda_verify_draft(p, None, slots, None, p, p, 2, 2, 8, slots, slots, stream=0)
+    with pytest.raises(TypeError):
+        kda.kda_verify_draft(p.double(), None, slots, None, p, p, 2, 2, 8, slots, slots, stream=0)
