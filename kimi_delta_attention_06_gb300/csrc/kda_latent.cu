@@ -19,6 +19,9 @@
 //   - s moves from the latents to the weights: O = sum (p s) codes.  p s is the sum of three e5m2
 //     values (3 bits each: a relative 2^-9, less than a rounding to bf16), scaled so that the
 //     largest lies in 2^10 .. 2^15, which leaves 26 binades or more below it.
+// Measured, 32 heads: 64 sequences (970k tokens), bf16, K = 1, 190 us, 5.9 TB/s (HBM); e4m3 135 us
+// (4.7 TB/s; 16 heads 113 us); 16 sequences, K = 4, e4m3, 99 us (64 rows a CTA: shared memory, which
+// feeds the products 128 bytes a clock); one sequence of 145408, bf16, 43 us, 7 of them the join.
 // Expanding the tile to bf16 instead (exact too) took 4800 clocks a tile of 64 rows: loads into
 // registers hold too little in flight beside 227 KB of shared memory, and the tile is written and
 // read once more.
@@ -252,7 +255,7 @@ struct LatShape {
     static constexpr uint32_t kSlabs = E4M3 ? 5u : 9u, kStage = kSlabs * kSlabC + (E4M3 ? 1024u : 0u);
     // Q: 9 slabs of 64 bf16; e4m3: 2 terms x 4 slabs of 128 codes, then the position part's
     // e4m3: the three terms of P lie side by side along N where TMEM holds three accumulators for them
-    // (R <= 32: the codes are then read once for all three; 2590 -> 2050 clocks a tile at R = 32), else
+    // (R <= 32: the codes are then read once for all three; 64 sequences, R = 32: 170 -> 149 us), else
     // in tiles of their own that share one accumulator
     static constexpr bool kSide = E4M3 && R <= 32;
     static constexpr uint32_t kO = kSide ? 3u * R : R;                                // TMEM columns of a block of O

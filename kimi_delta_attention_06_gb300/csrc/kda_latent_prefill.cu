@@ -11,6 +11,11 @@
 // S, P and O stay in TMEM (2 x 128 + 2 x 128 columns: all of it); a softmax thread owns one row.
 // Keys and values pass through a ring of eight 16 KB slabs (64 channels x 128 keys), K's two, r's
 // one and V's two a tile, in the order in which the products use and free them.
+//
+// Bound by the power limit of the card: 32 heads, causal, 8192 tokens take 443 us (1550 TFLOP/s at
+// 1370 W), 2048 tokens after 32768 cached ones 840 us (1690 TFLOP/s); a seconds-long plain matrix
+// product holds 1727.  One thread issues all products: with one warp a query tile the two tiles'
+// products interleaved instead of taking turns (518 -> 586 us, against 451 with one thread).
 #include <cuda.h>
 #include "latent.cuh"
 #include "tc.cuh"
