@@ -23,8 +23,9 @@
  *     prefill entry points kda_chunk_prefill and kda_chunk_prefill_ex take
  *     their hand-off rings stream-ordered from a memory pool the library owns
  *     (see kda_chunk_prefill); kda_chunk_prefill_noalloc uses a fixed device
- *     array instead and allocates nothing; kda_latent_decode takes its partial
- *     results from the same pool; every other entry point needs no scratch.
+ *     array instead and allocates nothing; kda_latent_decode and, for few
+ *     queries over many keys, kda_latent_prefill take their partial results
+ *     from the same pool; every other entry point needs no scratch.
  *   - Tensors are dense, row-major, with the last dimension contiguous.
  *     bf16 tensors are passed as uint16_t bit patterns (IEEE bfloat16).
  *     Every device pointer must be 16-byte aligned.
@@ -501,7 +502,9 @@ int kda_latent_decode(const uint16_t* q, const void* cache, int cache_dtype, int
  *     x_t = sm_scale * (q[:128] . k_t + q[128:] . r_t),  out = sum_t softmax(x)_t v_t
  * A query that sees nothing gives zeros and lse = -inf.  Keys and values that a query does not
  * see never reach its result, whatever they hold.  Softmax statistics and sums are fp32; the
- * probabilities enter the second product as bf16.  Deterministic.
+ * probabilities enter the second product as bf16.  Few queries over many keys split the keys
+ * over CTAs; the partial results (at most 256 MB, chosen from the host copies) are scratch,
+ * stream-ordered from the library's pool as for kda_chunk_prefill.  Deterministic.
  */
 int kda_latent_prefill(const uint16_t* q, const uint16_t* k, int64_t ldk, int64_t hdk,
                        const uint16_t* v, int64_t ldv, int64_t hdv, const uint16_t* k_rope, int64_t ldr,

@@ -56,7 +56,11 @@ size_t latent_decode_scratch(int rows);
 int launch_latent_prefill(const uint16_t* q, const uint16_t* k, long long ldk, long long hdk, const uint16_t* v,
                           long long ldv, long long hdv, const uint16_t* r, long long ldr, const int32_t* cu_q,
                           const int32_t* cu_k, int num_seqs, int total_q, int total_k, int units, int H, int causal,
-                          float sm_scale, uint16_t* out, float* lse, int* status, cudaStream_t stream);
+                          float sm_scale, uint16_t* out, float* lse, int span, int parts, void* scratch, int* status,
+                          cudaStream_t stream);
+int expanded_span(const int32_t* cu_q, const int32_t* cu_k, int num_seqs, int H, int causal, int total_q, int units,
+                  int* parts);
+size_t expanded_scratch(long long parts, int H, int total_q);
 int launch_verify(const float* tp, long long ldp, const float* dp, long long ldq, const int32_t* toks,
                   const int32_t* num_draft, const float* ua, const float* us, int N, int K, int V, int32_t* out,
                   int32_t* num_out, int* status, cudaStream_t stream);
@@ -880,9 +884,20 @@ int kda_latent_prefill(const uint16_t* q, const uint16_t* k, int64_t ldk, int64_
     int* status = nullptr;
     int rc = device_setup(&status);
     if (rc != KDA_OK) return rc;
+    const cudaStream_t st = static_cast<cudaStream_t>(stream);
+    int parts = 1;
+    const int span = kda::expanded_span(cu_q_host, cu_k_host, num_seqs, H, causal, total_q, units, &parts);
+    void* ws = nullptr;
+    if (span > 0) {
+        cudaMemPool_t pool = nullptr;
+        rc = workspace_pool(&pool);
+        if (rc != KDA_OK) return rc;
+        if (cudaMallocFromPoolAsync(&ws, kda::expanded_scratch(parts, H, total_q), pool, st) != cudaSuccess) return KDA_ERR_CUDA;
+    }
     rc = kda::launch_latent_prefill(q, k, ldk, hdk, v, ldv, hdv, k_rope, ldr, cu_q, cu_k, num_seqs, total_q, total_k, units,
-                                    H, causal, sm_scale, out, lse, status, static_cast<cudaStream_t>(stream));
-    return rc == 0 ? KDA_OK : KDA_ERR_CUDA;
+                                    H, causal, sm_scale, out, lse, span, parts, ws, status, st);
+    const bool freed = !ws || cudaFreeAsync(ws, st) == cudaSuccess;
+    return (rc == 0 && freed) ? KDA_OK : KDA_ERR_CUDA;
 }
 
 int kda_verify_draft(const float* target_probs, int64_t ldp, const float* draft_probs, int64_t ldq,
