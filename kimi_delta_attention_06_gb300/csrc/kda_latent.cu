@@ -21,7 +21,7 @@
 //     largest lies in 2^10 .. 2^15, which leaves 26 binades or more below it.
 // Measured, 32 heads: 64 sequences (970k tokens), bf16, K = 1, 190 us, 5.9 TB/s (HBM); e4m3 135 us
 // (4.7 TB/s; 16 heads 113 us); 16 sequences, K = 4, e4m3, 99 us (64 rows a CTA: shared memory, which
-// feeds the products 128 bytes a clock); one sequence of 145408, bf16, 43 us, 7 of them the join.
+// feeds the products 128 bytes a clock); one sequence of 145408, bf16, 43 us, 6 of them the join.
 // Expanding the tile to bf16 instead (exact too) took 4800 clocks a tile of 64 rows: loads into
 // registers hold too little in flight beside 227 KB of shared memory, and the tile is written and
 // read once more.
@@ -41,7 +41,7 @@ struct LatentCache {
 // 16 i .. 16 i + 15 and position values 2 i, 2 i + 1.
 template <bool E4M3>
 __device__ void latent_row(const uint16_t* __restrict__ q, const LatentCache& ch, int n, int see, float scale_log2,
-                           uint16_t* __restrict__ out, float* __restrict__ lse, int* status)
+                           uint16_t* __restrict__ out, float* __restrict__ lse, int* status, int quarter)
 {
     const int lane = threadIdx.x & 31;
     float qc[16], acc[16];
@@ -116,8 +116,10 @@ __device__ void latent_row(const uint16_t* __restrict__ q, const LatentCache& ch
 #pragma unroll
     for (int i = 0; i < 8; ++i) o[i] = f32x2_to_bf16x2_bits(acc[2 * i] * inv, acc[2 * i + 1] * inv);
     uint4* d = reinterpret_cast<uint4*>(out) + 2 * lane;
-    d[0] = make_uint4(o[0], o[1], o[2], o[3]);
-    d[1] = make_uint4(o[4], o[5], o[6], o[7]);
+    if (quarter < 0 || lane >> 3 == quarter) {       // all channels, or 128 of them
+        d[0] = make_uint4(o[0], o[1], o[2], o[3]);
+        d[1] = make_uint4(o[4], o[5], o[6], o[7]);
+    }
     if (lse && lane == 0) *lse = (m + log2f(l)) * 0.69314718055994531f;     // l = 0: -inf
 }
 
@@ -318,10 +320,10 @@ __device__ __forceinline__ void load_o(uint32_t ta, float (&o)[16]) {
 // Row (n, j, h) again, in fp32 over exactly the tokens it sees: for results that a NaN or infinity
 // in a token that other rows of the tile see has spoilt (0 * NaN in the product with P).
 template <bool E4M3>
-__device__ __noinline__ void latent_row_again(const LatArgs& a, int n, int row, int see) {
+__device__ __noinline__ void latent_row_again(const LatArgs& a, int n, int row, int see, int quarter = -1) {
     const long long at = static_cast<long long>(n) * a.rows + row;
-    latent_row<E4M3>(a.q + at * kLatQ, a.ch, n, see, a.scale_log2, a.out + at * kLatDim, a.lse ? a.lse + at : nullptr,
-                     a.status);
+    latent_row<E4M3>(a.q + at * kLatQ, a.ch, n, see, a.scale_log2, a.out + at * kLatDim,
+                     a.lse && quarter <= 0 ? a.lse + at : nullptr, a.status, quarter);
 }
 
 template <int R, bool E4M3>
@@ -858,7 +860,8 @@ kda_latent_decode_kernel(const __grid_constant__ LatMaps maps, const LatArgs a)
 
 // Joins the partials of sequences that several CTAs worked on, and writes empty sequences.  A block
 // takes one row (x 1 / Q of its channels when there are few rows): NG groups of 128 / Q threads, 4
-// channels a thread, group i every NG-th partial.
+// channels a thread, group i every NG-th partial, in one pass with the running maximum and 8 partials'
+// loads in flight; then the groups are joined.
 constexpr int kMaxRuns = 1024;                  // partials of a row (at most one a run)
 
 template <int R, bool E4M3>
@@ -866,9 +869,8 @@ __global__ void __launch_bounds__(512)
 kda_latent_combine_kernel(const LatArgs a, int Q, int NG)
 {
     __shared__ long long s_sum[2][16];
-    __shared__ float s_w[kMaxRuns], s_l[kMaxRuns];             // weight (first m) and l of each partial
     __shared__ float4 s_acc[512];
-    __shared__ float s_ml[2][16];
+    __shared__ float2 s_ml[16];                                 // (m, l) of each group
     const int lanes = 128 / Q, threads = lanes * NG;
     const int unit = blockIdx.x / Q, n = unit / a.rows, row = unit % a.rows;
     const int tid = threadIdx.x, grp = tid / lanes, ch = (blockIdx.x % Q * lanes + tid % lanes) * 4;
@@ -912,48 +914,48 @@ kda_latent_combine_kernel(const LatArgs a, int Q, int NG)
     const size_t stride = static_cast<size_t>(a.RT) * 2 * R;     // rows of partials between runs
     const size_t base = (static_cast<size_t>(c0) * a.RT + row / R) * 2 * R + r;
     auto slot = [&](int i) { return base + i * stride + (i == 0 && late ? R : 0); };
-    // M = the largest maximum; weights exp2(m_i - M); L = sum of weight_i l_i
-    float M = -INFINITY;
-    for (int i = tid; i < parts; i += threads) {
-        const float2 ml = *reinterpret_cast<const float2*>(a.part_ml + slot(i) * 2);
-        s_w[i] = ml.x;
-        s_l[i] = ml.y;
-        M = fmaxf(M, ml.x);
-    }
-#pragma unroll
-    for (int off = 16; off > 0; off >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, off));
-    if ((tid & 31) == 0) s_ml[0][tid >> 5] = M;
-    __syncthreads();
-    for (int i = 0; i < warps; ++i) M = fmaxf(M, s_ml[0][i]);
-    float L = 0.f;
-    for (int i = tid; i < parts; i += threads) {
-        const float m = s_w[i], l = s_l[i];
-        const float w = m == -INFINITY && l == 0.f ? 0.f : m == M ? 1.f : lat_ex2(m - M);     // 0: saw nothing there
-        s_w[i] = m == -INFINITY && l == 0.f ? -1.f : w;
-        L += w * l;
-    }
-#pragma unroll
-    for (int off = 16; off > 0; off >>= 1) L += __shfl_xor_sync(0xffffffffu, L, off);
-    if ((tid & 31) == 0) s_ml[1][tid >> 5] = L;
-    __syncthreads();
-    L = 0.f;
-    for (int i = 0; i < warps; ++i) L += s_ml[1][i];
+    float M = -INFINITY, L = 0.f;
     float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll 8
-    for (int i = grp; i < parts; i += NG) {
-        const float4 o = *reinterpret_cast<const float4*>(a.part_o + slot(i) * kLatDim + ch);
-        const float w = s_w[i];
-        if (w >= 0.f) { acc.x += w * o.x; acc.y += w * o.y; acc.z += w * o.z; acc.w += w * o.w; }
+    // joins B partials (m, l, O) with it; one that saw nothing (m = -inf, l = 0) has no part in it
+    auto join = [&](const auto& v, const auto& x) {
+        constexpr int B = sizeof(v) / sizeof(float2);
+        float mx = M;
+#pragma unroll
+        for (int i = 0; i < B; ++i) mx = fmaxf(mx, v[i].x);
+        const float f = mx == M ? 1.f : lat_ex2(M - mx);
+        M = mx;
+        L *= f;
+        acc.x *= f; acc.y *= f; acc.z *= f; acc.w *= f;
+#pragma unroll
+        for (int i = 0; i < B; ++i) {
+            if (v[i].x == -INFINITY && v[i].y == 0.f) continue;
+            const float w = v[i].x == M ? 1.f : lat_ex2(v[i].x - M);
+            L += w * v[i].y;
+            acc.x += w * x[i].x; acc.y += w * x[i].y; acc.z += w * x[i].z; acc.w += w * x[i].w;
+        }
+    };
+    for (int i0 = grp; i0 < parts; i0 += 8 * NG) {
+        float2 v[8];
+        float4 x[8];
+#pragma unroll
+        for (int k = 0; k < 8; ++k) {
+            const int i = i0 + k * NG;
+            v[k] = i < parts ? *reinterpret_cast<const float2*>(a.part_ml + slot(i) * 2) : make_float2(-INFINITY, 0.f);
+            x[k] = i < parts ? *reinterpret_cast<const float4*>(a.part_o + slot(i) * kLatDim + ch) : make_float4(0.f, 0.f, 0.f, 0.f);
+        }
+        join(v, x);
     }
     int bad = 0;
     if (NG > 1) {
         s_acc[tid] = acc;
+        if (tid % lanes == 0) s_ml[grp] = make_float2(M, L);
         __syncthreads();
     }
     if (grp == 0) {
         for (int i = 1; i < NG; ++i) {
-            const float4 o = s_acc[tid + i * lanes];
-            acc.x += o.x; acc.y += o.y; acc.z += o.z; acc.w += o.w;
+            const float2 v[1] = {s_ml[i]};
+            const float4 x[1] = {s_acc[tid + i * lanes]};
+            join(v, x);
         }
         const float inv = L == 0.f ? 0.f : 1.f / L;
         const float v[4] = {acc.x * inv, acc.y * inv, acc.z * inv, acc.w * inv};
@@ -963,9 +965,9 @@ kda_latent_combine_kernel(const LatArgs a, int Q, int NG)
         if (ch == 0 && a.lse) a.lse[at] = (M + log2f(L)) * 0.69314718055994531f;
     }
     const int j = row / a.H;
-    if (j < a.K - 1) {                                           // (Q = 1 where K > 1: the block owns the row)
+    if (j < a.K - 1) {
         bad = __syncthreads_or(bad);
-        if (bad && tid < 32) latent_row_again<E4M3>(a, n, row, len - (a.K - 1 - j));
+        if (bad && tid < 32) latent_row_again<E4M3>(a, n, row, len - (a.K - 1 - j), Q == 1 ? -1 : static_cast<int>(blockIdx.x % Q));
     }
 }
 
@@ -1107,13 +1109,14 @@ int launch_decode_shape(const LatMaps& maps, const LatArgs& a, cudaStream_t stre
     if (cudaGetLastError() != cudaSuccess) return -3;
     cudaLaunchConfig_t cfg = {};
     // a row's partials number about G / N + 1: few of them (many sequences), a warp a row; else
-    // groups of threads with 8 of them each, a row's channels over 4 blocks where rows are too few
-    // to fill the device
+    // groups of threads with 8 of them each (4: 1 to 10 us more), a row's channels over 4 blocks where
+    // rows are too few for a block on each SM (20 tokens of 48 rows each, 192 rows: 16.5 us with 4, 15.3
+    // with 1; 24 rows over 33851 tokens: 19.8 with 4, 27.4 with 1 and a pass each for maxima, sums and O)
     const int about = a.w.G / a.w.N + 1;
     const bool by_warp = about <= 16;
-    const int Q = a.K == 1 && static_cast<long long>(a.w.N) * a.rows < 256 ? 4 : 1;
-    int NG = Q;
-    while (NG < 4 * Q && NG * 8 < Q * about) NG *= 2;
+    const int Q = static_cast<long long>(a.w.N) * a.rows < sm_count() ? 4 : 1;
+    int NG = 1;
+    while (NG < 4 * Q && NG * 8 < about) NG *= 2;
     cfg.gridDim = dim3(by_warp ? (static_cast<unsigned>(a.w.N) * a.rows + 3) / 4 : static_cast<unsigned>(a.w.N) * a.rows * Q);
     cfg.blockDim = dim3(by_warp ? 128 : 128 / Q * NG);
     cfg.stream = stream;
