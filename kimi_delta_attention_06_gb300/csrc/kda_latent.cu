@@ -228,8 +228,10 @@ struct SegWalk {
 };
 
 // ---- the tensor-core kernel --------------------------------------------------------------------
-// q [rows, 576] and a bf16 cache [slots, 576] in boxes of 64 columns; an e4m3 cache [slots, 656 bytes] in
-// boxes of 128 bytes (128 codes, or the position key), and its scales in boxes of 16 bytes
+// q [rows, 576] in boxes of 64 columns; the cache in boxes of whole rows, as slabs of 128 bytes (64 bf16
+// values; 128 codes, or the position key); the scales of an e4m3 cache in boxes of 16 bytes.  (A box a
+// slab instead is 36 copies a tile with pages of 16 tokens: 64 sequences 191 -> 208 us, e4m3 134 -> 185,
+// K = 4 94 -> 145.)
 struct LatMaps { CUtensorMap q, c, s; };
 
 struct LatArgs {
@@ -252,9 +254,12 @@ struct LatShape {
     static constexpr int kThreads = 192;
     // as many as fit: a stage is taken for a copy's latency (about 3000 clocks) and both products
     static constexpr int kStages = E4M3 ? (R <= 32 ? 4 : 3) : 2;
-    static constexpr uint32_t kSlabQ = R * 128u, kSlabC = kTile * 128u;
+    static constexpr uint32_t kSlabQ = R * 128u;
     // bf16: 9 slabs of 64 values; e4m3: 4 slabs of 128 codes, the position key's, 64 scales of 16 bytes
-    static constexpr uint32_t kSlabs = E4M3 ? 5u : 9u, kStage = kSlabs * kSlabC + (E4M3 ? 1024u : 0u);
+    // (a slab: 128 bytes of a row; a tile: 8 groups of 8 rows, each of kSlabs slabs of 8 x 128 bytes, which is
+    // what one copy of whole rows lays down)
+    static constexpr uint32_t kSlabs = E4M3 ? 5u : 9u, kSlabC = 1024u, kGroup = kSlabs * kSlabC, kRows = 8u * kGroup;
+    static constexpr uint32_t kStage = kRows + (E4M3 ? 1024u : 0u);
     // Q: 9 slabs of 64 bf16; e4m3: 2 terms x 4 slabs of 128 codes, then the position part's
     // e4m3: the three terms of P lie side by side along N where TMEM holds three accumulators for them
     // (R <= 32: the codes are then read once for all three; 64 sequences, R = 32: 170 -> 149 us), else
@@ -449,7 +454,7 @@ kda_latent_decode_kernel(const __grid_constant__ LatMaps maps, const LatArgs a)
                     tc::fence_after_sync();
                     tmem_ld_s<R>(tmS + (g & 1) * Sh::kS + lane_tm, x);
                     if constexpr (E4M3) {
-                        const float* sc = reinterpret_cast<const float*>(sC + g % NS * Sh::kStage + Sh::kSlabs * Sh::kSlabC);
+                        const float* sc = reinterpret_cast<const float*>(sC + g % NS * Sh::kStage + Sh::kRows);
                         s0 = sc[(16 * warp + tq) * 4];
                         s1 = sc[(16 * warp + tq + 8) * 4];
                         // (held above -90, so that the sums of 2^(x - m) stay within fp32; see f0, f1)
@@ -483,7 +488,7 @@ kda_latent_decode_kernel(const __grid_constant__ LatMaps maps, const LatArgs a)
                         constexpr int W = E4M3 ? 4 : 8;         // slabs of latents
                         for (int i = tid; i < W * (kTile - valid) * 8; i += Sh::kSoft) {
                             const int ch = i & 7, slab = i / 8 % W, r = valid + i / (8 * W);
-                            *reinterpret_cast<uint4*>(c + slab * Sh::kSlabC + r * 128 + ch * 16) = make_uint4(0, 0, 0, 0);
+                            *reinterpret_cast<uint4*>(c + (r >> 3) * Sh::kGroup + slab * Sh::kSlabC + (r & 7) * 128 + ch * 16) = make_uint4(0, 0, 0, 0);
                         }
                         if (E4M3) {                             // and their scales are not to be used
                             if (16 * warp + tq >= valid) { s0 = 1.f; e0 = 0.f; }
@@ -695,12 +700,12 @@ kda_latent_decode_kernel(const __grid_constant__ LatMaps maps, const LatArgs a)
                                        : tc::idesc(128, R, tc::kFmtBF16, true, true);
         constexpr uint32_t id_c = tc::idesc8(64, R, tc::kFmtE4M3, tc::kFmtE4M3, false, false);
         // descriptors: constant high words, low words = address / 16 and the leading offset
-        const uint64_t d0 = tc::sdesc(0, 16, 1024, tc::kSwizzle128B), dC = tc::sdesc(0, Sh::kSlabC, 1024, tc::kSwizzle128B);
+        const uint64_t d0 = tc::sdesc(0, 16, 1024, tc::kSwizzle128B), dC = tc::sdesc(0, Sh::kSlabC, Sh::kGroup, tc::kSwizzle128B);
         const uint32_t hi = static_cast<uint32_t>(d0 >> 32);
         const uint32_t q_lo = static_cast<uint32_t>(d0) | (tc::smem_u32(sQ) >> 4);
-        const uint32_t c_lo = static_cast<uint32_t>(d0) | (tc::smem_u32(sC) >> 4);
-        const uint32_t ct_lo = static_cast<uint32_t>(dC) | (tc::smem_u32(sC) >> 4);
-        const uint32_t p_lo = static_cast<uint32_t>(dC) | (tc::smem_u32(sP) >> 4);
+        const uint32_t hi_c = static_cast<uint32_t>(dC >> 32);
+        const uint32_t c_lo = static_cast<uint32_t>(dC) | (tc::smem_u32(sC) >> 4);
+        const uint32_t p_lo = static_cast<uint32_t>(d0) | (tc::smem_u32(sP) >> 4);
         SegWalk sv = sw;                                        // the O product's walk follows the S product's
         bool more_s = sw.next(a.w), more_o = sv.next(a.w);
         int gs = 0, go = 0, qs = 0;                             // S and O tiles issued, segments whose Q is in
@@ -714,24 +719,24 @@ kda_latent_decode_kernel(const __grid_constant__ LatMaps maps, const LatArgs a)
             // read before P is written)
             if (go < gs && tc::mbar_test_wait(p_full, go & 1)) {
                 tc::fence_after_sync();
-                const uint32_t c = ct_lo + go % NS * (Sh::kStage >> 4);
+                const uint32_t c = c_lo + go % NS * (Sh::kStage >> 4);
                 const uint32_t acc = to > sv.t0 ? 1u : 0u;
 #pragma unroll
                 for (uint32_t b = 0; b < 4; ++b) {
                     if constexpr (!E4M3) {
 #pragma unroll
                         for (uint32_t k = 0; k < 4; ++k)
-                            tc::mma_f16_lo(tmO + b * R, c + ((b * 2u * Sh::kSlabC + k * 2048u) >> 4), hi,
+                            tc::mma_f16_lo(tmO + b * R, c + ((b * 2u * Sh::kSlabC + k * 2u * Sh::kGroup) >> 4), hi_c,
                                            p_lo + (k * 2048u >> 4), hi, id_o, k > 0 ? 1u : acc);
                     } else if constexpr (Sh::kSide) {
 #pragma unroll
                         for (uint32_t k = 0; k < 2; ++k)     // 2 steps of 32 tokens, all terms at once
-                            tc::mma_f8_lo(tmO + b * Sh::kO, c + ((b * Sh::kSlabC + k * 4096u) >> 4), hi,
+                            tc::mma_f8_lo(tmO + b * Sh::kO, c + ((b * Sh::kSlabC + k * 4u * Sh::kGroup) >> 4), hi_c,
                                           p_lo + (k * 4096u >> 4), hi, id_o, k > 0 ? 1u : acc);
                     } else {
 #pragma unroll
                         for (uint32_t k = 0; k < 6; ++k)     // 2 steps of 32 tokens x 3 terms
-                            tc::mma_f8_lo(tmO + b * R, c + ((b * Sh::kSlabC + k / 3u * 4096u) >> 4), hi,
+                            tc::mma_f8_lo(tmO + b * R, c + ((b * Sh::kSlabC + k / 3u * 4u * Sh::kGroup) >> 4), hi_c,
                                           p_lo + ((k % 3u * kTile * 128u + k / 3u * 4096u) >> 4), hi, id_o, k > 0 ? 1u : acc);
                     }
                 }
@@ -750,17 +755,17 @@ kda_latent_decode_kernel(const __grid_constant__ LatMaps maps, const LatArgs a)
                 if constexpr (!E4M3) {
 #pragma unroll
                     for (uint32_t k = 0; k < 36; ++k)
-                        tc::mma_f16_lo(d, c + (((k >> 2) * Sh::kSlabC + (k & 3) * 32u) >> 4), hi,
+                        tc::mma_f16_lo(d, c + (((k >> 2) * Sh::kSlabC + (k & 3) * 32u) >> 4), hi_c,
                                        q_lo + (((k >> 2) * Sh::kSlabQ + (k & 3) * 32u) >> 4), hi, id_s, k > 0 ? 1u : 0u);
                 } else {
 #pragma unroll
                     for (uint32_t k = 0; k < 32; ++k)        // 16 steps of 32 codes x 2 terms of q
-                        tc::mma_f8_lo(d, c + (((k >> 3) * Sh::kSlabC + (k >> 1 & 3) * 32u) >> 4), hi,
+                        tc::mma_f8_lo(d, c + (((k >> 3) * Sh::kSlabC + (k >> 1 & 3) * 32u) >> 4), hi_c,
                                       q_lo + (((k & 1) * 4u * Sh::kSlabQ + (k >> 3) * Sh::kSlabQ + (k >> 1 & 3) * 32u) >> 4), hi,
                                       id_c, k > 0 ? 1u : 0u);
 #pragma unroll
                     for (uint32_t k = 0; k < 4; ++k)         // the position part, bf16
-                        tc::mma_f16_lo(d + R, c + ((4u * Sh::kSlabC + k * 32u) >> 4), hi,
+                        tc::mma_f16_lo(d + R, c + ((4u * Sh::kSlabC + k * 32u) >> 4), hi_c,
                                        q_lo + ((8u * Sh::kSlabQ + k * 32u) >> 4), hi, id_s, k > 0 ? 1u : 0u);
                 }
                 tc::mma_commit(&s_full[gs & 1]);
@@ -785,7 +790,7 @@ kda_latent_decode_kernel(const __grid_constant__ LatMaps maps, const LatArgs a)
         if (leader && go > 0 && !tc::mbar_wait_bounded(&empty[(go - 1) % NS], (go - 1) / NS & 1, kWaitLimitNs)) ok = false;
         __syncwarp();
     } else {
-        // ---- TMA: C tiles in boxes of `box` rows (one page or a part of one); bf16: Q of each segment ----
+        // ---- TMA: C tiles in boxes of `box` whole rows (one page or a part of one); bf16: Q of each segment ----
         const int nbox = kTile / a.box;
         int g = 0, seg = 0;
         while (ok && sw.next(a.w)) {
@@ -821,25 +826,16 @@ kda_latent_decode_kernel(const __grid_constant__ LatMaps maps, const LatArgs a)
                 if (lane == 0)
                     tc::mbar_arrive_expect_tx(&full[g % NS], static_cast<uint32_t>(boxes * a.box) * (Sh::kSlabs * 128u + (E4M3 ? 16u : 0u)));
                 __syncwarp();
-                for (int b = 0; b < boxes; ++b) {
-                    const int row = __shfl_sync(0xffffffffu, at, b);
-                    if (lane < Sh::kSlabs)
-                        tc::tma_load_2d(dst + lane * Sh::kSlabC + b * a.box * 128, &maps.c, (E4M3 ? 128 : 64) * lane, row, &full[g % NS]);
-                    if (E4M3 && lane == Sh::kSlabs)
-                        tc::tma_load_2d(dst + Sh::kSlabs * Sh::kSlabC + b * a.box * 16, &maps.s, kLatScaleAt, row, &full[g % NS]);
+                if (at >= 0) {                                   // a box a lane: all of its rows in one copy
+                    tc::tma_load_4d(dst + lane * (a.box >> 3) * Sh::kGroup, &maps.c, 0, 0, 0, at >> 3, &full[g % NS]);
+                    if (E4M3) tc::tma_load_2d(dst + Sh::kRows + lane * a.box * 16, &maps.s, kLatScaleAt, at, &full[g % NS]);
                 }
                 if constexpr (R == 64 && !E4M3) {
                     // the next tile is fetched into L2 meanwhile, as two stages do not cover a copy from HBM: 64
                     // sequences x 64 heads 209 -> 194 us, 16 x K = 4 x 32 heads 105 -> 97, one of 145408 x 64
                     // heads 55.6 -> 53.3.  (With 32 rows HBM is the bound: 189 -> 205.  Three stages of an e4m3
                     // cache cover it: no change.  Two tiles ahead: 196, 99, 53.7.)
-                    if (rt == 0) {
-                        const int ahead = __popc(__ballot_sync(0xffffffffu, next >= 0));
-                        for (int b = 0; b < ahead; ++b) {
-                            const int row = __shfl_sync(0xffffffffu, next, b);
-                            if (lane < Sh::kSlabs) tc::tma_prefetch_2d(&maps.c, 64 * lane, row);
-                        }
-                    }
+                    if (rt == 0 && next >= 0) tc::tma_prefetch_4d(&maps.c, 0, 0, 0, next >> 3);
                 }
                 at = next;
             }
@@ -1091,6 +1087,18 @@ bool map_2d(CUtensorMap* m, CUtensorMapDataType dt, const void* base, long long 
               CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
+// A cache [slots, pitch bytes] as [slots / 8][slabs][8 rows][128 bytes]: boxes of `rows` rows, all slabs
+bool map_rows(CUtensorMap* m, CUtensorMapDataType dt, const void* base, long long slots, int pitch, int slab, int slabs, int rows) {
+    EncodeTiledFn fn = encode_fn();
+    if (!fn) return false;
+    const cuuint64_t dims[4] = {static_cast<cuuint64_t>(slab), 8u, static_cast<cuuint64_t>(slabs), static_cast<cuuint64_t>(slots / 8)};
+    const cuuint64_t strides[3] = {static_cast<cuuint64_t>(pitch), 128u, static_cast<cuuint64_t>(pitch) * 8};
+    const cuuint32_t box[4] = {static_cast<cuuint32_t>(slab), 8u, static_cast<cuuint32_t>(slabs), static_cast<cuuint32_t>(rows / 8)};
+    const cuuint32_t estr[4] = {1u, 1u, 1u, 1u};
+    return fn(m, dt, 4, const_cast<void*>(base), dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
+              CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
 int sm_count() {
     static int count[kMaxDevicesAttr] = {};
     int dev = 0;
@@ -1175,10 +1183,10 @@ int launch_latent_decode(const uint16_t* q, const void* cache, int e4m3, int num
     if (num_pages == 0) a.w.max_len = 0;
     maps.c = maps.s = maps.q;
     if (num_pages > 0 && !e4m3 &&
-        !map_2d(&maps.c, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, cache, slots, kLatQ, kLatRowBf16, 64, a.box, swz))
+        !map_rows(&maps.c, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, cache, slots, kLatRowBf16, 64, 9, a.box))
         return -3;
     if (num_pages > 0 && e4m3 &&
-        (!map_2d(&maps.c, CU_TENSOR_MAP_DATA_TYPE_UINT8, cache, slots, kLatRowE4m3, kLatRowE4m3, 128, a.box, swz) ||
+        (!map_rows(&maps.c, CU_TENSOR_MAP_DATA_TYPE_UINT8, cache, slots, kLatRowE4m3, 128, 5, a.box) ||
          !map_2d(&maps.s, CU_TENSOR_MAP_DATA_TYPE_UINT8, cache, slots, kLatRowE4m3, kLatRowE4m3, 16, a.box,
                  CU_TENSOR_MAP_SWIZZLE_NONE)))
         return -3;
