@@ -280,14 +280,16 @@ int launch_verify(const float* tp, long long ldp, const float* dp, long long ldq
                   const int32_t* num_draft, const float* ua, const float* us, int N, int K, int V, int32_t* out,
                   int32_t* num_out, int* status, cudaStream_t stream)
 {
-    // CTAs of 16 warps; the fewest a row that give every SM one, as each one's acceptance, exchange
+    // CTAs of 16 warps; as many a row as leave each an SM of its own, as each one's acceptance, exchange
     // and narrowing are latency that more of them only repeat (256 rows of 100003: 48.6 us at one CTA
-    // a row, 55 at two; of 8 warps 54 at two, 52 at four, 59 at eight).  Few sequences take up to 16 (past
-    // the portable cluster size), so that a row of 131072 is one round of loads; slices of 2048 tokens
-    // at least.
+    // a row, 55 at two; of 8 warps 54 at two, 52 at four, 59 at eight; with two on some SMs 24 rows of
+    // 90511 took 15.1 instead of 12.1, 100 of 50000 20.3 instead of 16.5, 78 of 37080 14.8 instead of
+    // 11.7).  17 clusters of 8 find room at once (19 rows: 15.0 with 8, 13.4 with 4).  Few sequences take
+    // up to 16 (past the portable cluster size), so that a row of 131072 is one round of loads; slices of
+    // 2048 tokens at least.
     const int most = static_cast<long long>(N) * 16 <= 152 && V > 8 * 4096 ? 16 : 8, warps = 16;
     int C = 1;
-    while (C < most && static_cast<long long>(N) * C < 152 && V / (2 * C) >= 2048) C *= 2;
+    while (C < most && static_cast<long long>(N) * 2 * C <= (C == 4 ? 17 * 8 : 152) && V / (2 * C) >= 2048) C *= 2;
     static bool wide_done[kMaxDevicesAttr] = {};
     int dev = 0;
     if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= kMaxDevicesAttr) return -3;
