@@ -12,9 +12,9 @@
 // Keys and values pass through a ring of eight 16 KB slabs (64 channels x 128 keys), K's two, r's
 // one and V's two a tile, in the order in which the products use and free them.
 //
-// Bound by the power limit of the card: 32 heads, causal, 8192 tokens take 443 us (1550 TFLOP/s at
-// 1370 W), 2048 tokens after 32768 cached ones 840 us (1690 TFLOP/s); a seconds-long plain matrix
-// product holds 1727.  One thread issues all products: with one warp a query tile the two tiles'
+// Bound by the tensor cores and, in long runs, by the power limit of the card: 32 heads, causal, 8192
+// tokens take 393 us (1750 TFLOP/s; a plain matrix product reaches 1900 for moments and holds 1730 for
+// seconds), 2048 tokens after 32768 cached ones 843 us (1680 TFLOP/s: 256 CTAs on 152 SMs).  One thread issues all products: with one warp a query tile the two tiles'
 // products interleaved instead of taking turns (518 -> 586 us, against 451 with one thread).
 //
 // Few queries over many keys: the keys are split over CTAs, whose partial (m, l, O) a second kernel joins
@@ -87,7 +87,7 @@ struct ExpArgs {
     const uint16_t* q;
     ExpKv kv;
     const int32_t *cu_q, *cu_k;
-    int num_seqs, H, causal;
+    int num_seqs, H, causal, hg;                 // hg: heads that go side by side
     float scale_log2;
     uint16_t* out;
     float* lse;
@@ -125,12 +125,13 @@ kda_expanded_kernel(const __grid_constant__ ExpMaps maps, const ExpArgs a)
     uint32_t* s_tmem = reinterpret_cast<uint32_t*>(bars + 20);
 
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-    const int h = blockIdx.y;
+    const int h = blockIdx.y * a.hg + blockIdx.x % a.hg;
+    if (h >= a.H) return;                                        // (the last group's)
     // the unit (sequence n, 256 rows from q0): the last rows of a sequence, the longest, come first
     int n = 0, q0 = 0, cq = 0, Lq = 0;
     {
         int base = 0;
-        const int want = static_cast<int>(blockIdx.x);
+        const int want = static_cast<int>(blockIdx.x / a.hg);
         for (int i0 = 0; i0 < a.num_seqs; i0 += 32) {
             const int i = i0 + lane;
             const int c = i < a.num_seqs ? a.cu_q[i] : 0, len = i < a.num_seqs ? a.cu_q[i + 1] - c : 0;
@@ -646,7 +647,15 @@ int launch_latent_prefill(const uint16_t* q, const uint16_t* k, long long ldk, l
     a.out = out;
     a.lse = lse;
     a.status = status;
-    const dim3 grid(static_cast<unsigned>(units), static_cast<unsigned>(H), static_cast<unsigned>(parts));
+    // A prompt's last queries have the most keys and come first, of some heads side by side, so that short
+    // units fill the end: 8192 tokens x 32 heads 441 -> 393 us with 8 heads (401 with 16), 2000 x 32 54.7 ->
+    // 41.2 with 16 (49.9 with 8), 16384 x 32 1550 -> 1479 with 4 or 8 (1516 with 16).  The heads' keys and
+    // values are to stay in L2: less than 64 MB.  Behind long prefixes the units are much alike, and a head's
+    // go together (2048 queries over 18432 keys, 8 heads: 128 us so, 148 side by side).
+    a.hg = 1;
+    if (causal && total_k < 2LL * total_q)
+        while (a.hg < 16 && 2 * a.hg <= H && total_k * 2LL * a.hg * (kExpK + kExpV) * 2 < (64 << 20)) a.hg *= 2;
+    const dim3 grid(static_cast<unsigned>(units) * a.hg, static_cast<unsigned>((H + a.hg - 1) / a.hg), static_cast<unsigned>(parts));
     if (span == 0) {
         static bool attr_done[kMaxDevicesAttr] = {};
         if (!raise_smem_limit(reinterpret_cast<const void*>(kda_expanded_kernel<false>), static_cast<int>(kExpSmem), attr_done)) return -3;
