@@ -19,9 +19,10 @@
 //   - s moves from the latents to the weights: O = sum (p s) codes.  p s is the sum of three e5m2
 //     values (3 bits each: a relative 2^-9, less than a rounding to bf16), scaled so that the
 //     largest lies in 2^10 .. 2^15, which leaves 26 binades or more below it.
-// Measured, 32 heads: 64 sequences (970k tokens), bf16, K = 1, 190 us, 5.9 TB/s (HBM); e4m3 135 us
-// (4.7 TB/s; 16 heads 113 us); 16 sequences, K = 4, e4m3, 99 us (64 rows a CTA: shared memory, which
-// feeds the products 128 bytes a clock); one sequence of 145408, bf16, 43 us, 6 of them the join.
+// Measured, 32 heads: 64 sequences (970k tokens), bf16, K = 1, 188 us, 5.9 TB/s (HBM); e4m3 134 us
+// (4.8 TB/s; 16 heads 114 us); 16 sequences (220k tokens), K = 4, e4m3 99 us, bf16 95 us (64 rows a CTA:
+// the products' operands, which shared memory feeds at 128 bytes a clock); one sequence of 145408, bf16,
+// 42 us, 6 of them the join.
 // Expanding the tile to bf16 instead (exact too) took 4800 clocks a tile of 64 rows: loads into
 // registers hold too little in flight beside 227 KB of shared memory, and the tile is written and
 // read once more.

@@ -18,8 +18,8 @@
 // its rounding error from one fma.  fp64 runs at 2 operations a clock and SM here: joining a CTA's
 // 512 lanes in it took longer than reading its slice, and the few joins after the reads 5 us.
 //
-// Measured: one sequence of 3 drafts, V = 131072, 8.4 us (latency: drafts, their odds, rows, exchange,
-// the crossing part); 256 sequences of 4 drafts, V = 100003, 48.6 us (205 MB: 4.2 TB/s).
+// Measured: one sequence of 3 drafts, V = 131072, 8.6 us (latency: drafts, their odds, rows, exchange,
+// the crossing part); 256 sequences of 4 drafts, V = 100003, 48.4 us (205 MB: 4.2 TB/s).
 #include "common.cuh"
 #include "tc.cuh"
 
