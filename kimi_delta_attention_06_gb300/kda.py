@@ -343,39 +343,68 @@ def kda_output_norm(o, o_dtype: int, gamma, eps: float, y, total_tokens: int, H:
 
 
 # The calls below are as short as a small kernel, so each tensor is looked at once: its address (and
-# its strides) come out of the function that checks its type and layout.
+# its strides) come out of the function that checks its type, shape and layout.  The library sees
+# addresses only, so a tensor that is smaller than the sizes of the call is refused here.
 _BF16, _I32, _F32 = torch.bfloat16, torch.int32, torch.float32
 
 
-def _dense(t: Optional[torch.Tensor], dtype):
+def _dense(t: Optional[torch.Tensor], dtype, need: int, what: str):
+    """Address of a contiguous tensor of at least `need` elements (None stays None)."""
     if t is None:
         return None
-    if t.dtype != dtype:
-        raise TypeError(f"expected a {dtype} tensor, got {t.dtype}")
+    if t.dtype is not dtype:
+        raise TypeError(f"{what}: expected a {dtype} tensor, got {t.dtype}")
     if not t.is_contiguous():
-        raise ValueError("KDA tensors must be contiguous")
+        raise ValueError(f"{what}: KDA tensors must be contiguous")
+    if t.numel() < need:
+        raise ValueError(f"{what}: {need} elements are needed, {tuple(t.shape)} has {t.numel()}")
     return t.data_ptr()
 
 
-def _rows2(t: torch.Tensor, dtype, least: int):
-    """(address, row stride in elements) of a 2-D tensor whose rows are contiguous; one row has any
-    stride: `least`, which the checks pass."""
-    if t.dtype != dtype:
-        raise TypeError(f"expected a {dtype} tensor, got {t.dtype}")
+def _rows2(t: torch.Tensor, dtype, rows: int, width: int, what: str):
+    """(address, row stride in elements) of a 2-D tensor [rows or more, width] whose rows are contiguous; one
+    row has any stride: `width`, which the checks pass."""
+    if t.dtype is not dtype:
+        raise TypeError(f"{what}: expected a {dtype} tensor, got {t.dtype}")
+    shape = t.shape
+    if len(shape) != 2 or shape[0] < rows or shape[1] != width:
+        raise ValueError(f"{what}: expected a tensor [{rows}, {width}], got {tuple(shape)}")
     st = t.stride()
     if st[1] != 1 and t.numel():
-        raise ValueError("the last dimension of a KDA tensor must be contiguous")
-    return t.data_ptr(), st[0] if t.shape[0] > 1 else least
+        raise ValueError(f"{what}: the last dimension of a KDA tensor must be contiguous")
+    return t.data_ptr(), st[0] if shape[0] > 1 else width
 
 
-def _rows3(t: torch.Tensor, dtype, least0: int, least1: int):
-    """The same of a 3-D tensor: (address, strides of its first two dimensions)."""
-    if t.dtype != dtype:
-        raise TypeError(f"expected a {dtype} tensor, got {t.dtype}")
-    st, shape = t.stride(), t.shape
+def _rows3(t: torch.Tensor, dtype, n0: int, n1: int, width: int, least0: int, what: str):
+    """The same of a 3-D tensor [n0 or more, n1, width]: (address, strides of its first two dimensions; of a
+    single entry: least0 and width)."""
+    if t.dtype is not dtype:
+        raise TypeError(f"{what}: expected a {dtype} tensor, got {t.dtype}")
+    shape = t.shape
+    if len(shape) != 3 or shape[0] < n0 or shape[1] != n1 or shape[2] != width:
+        raise ValueError(f"{what}: expected a tensor [{n0}, {n1}, {width}], got {tuple(shape)}")
+    st = t.stride()
     if st[2] != 1 and t.numel():
-        raise ValueError("the last dimension of a KDA tensor must be contiguous")
-    return t.data_ptr(), st[0] if shape[0] > 1 else least0, st[1] if shape[1] > 1 else least1
+        raise ValueError(f"{what}: the last dimension of a KDA tensor must be contiguous")
+    return t.data_ptr(), st[0] if shape[0] > 1 else least0, st[1] if n1 > 1 else width
+
+
+def _short(what: str, t: torch.Tensor, need: str):
+    raise ValueError(f"{what}: expected a tensor {need}, got {tuple(t.shape)}")
+
+
+def _on_gpu(*tensors):
+    """After the other checks: the kernels follow these addresses."""
+    for t in tensors:
+        if t is not None and not t.is_cuda:
+            raise ValueError("KDA tensors must be on the GPU")
+
+
+def _out(t, dtype, need: int, what: str):
+    """Address of an output that the caller brings."""
+    p = _dense(t, dtype, need, what)
+    _on_gpu(t)
+    return p
 
 
 def _host32(t):
@@ -388,6 +417,13 @@ def _last32(t: torch.Tensor) -> int:
     """Last entry of a contiguous host int32 tensor (0 of an empty one), without an indexing call."""
     n = t.numel()
     return ctypes.c_int32.from_address(t.data_ptr() + 4 * (n - 1)).value if n else 0
+
+
+def _host_offsets(t, seqs: int, what: str) -> torch.Tensor:
+    t = _host32(t)
+    if t.numel() < seqs + 1:
+        raise ValueError(f"{what}: {seqs + 1} offsets are needed, got {t.numel()}")
+    return t
 
 
 _ROW_BYTES = {KDA_CACHE_BF16: 2 * (KDA_LATENT_DIM + KDA_LATENT_ROPE), KDA_CACHE_E4M3: KDA_LATENT_DIM + 2 * KDA_LATENT_ROPE + 16}
@@ -408,93 +444,116 @@ def _pages(cache: torch.Tensor, cache_dtype: int):
 
 
 def kda_latent_append(c, k_rope, cache, cache_dtype: int, slots, total_tokens: int, stream=None):
-    cp, ldc = _rows2(c, _BF16, KDA_LATENT_DIM)
-    rp, ldr = _rows2(k_rope, _BF16, KDA_LATENT_ROPE)
+    cp, ldc = _rows2(c, _BF16, total_tokens, KDA_LATENT_DIM, "c")
+    rp, ldr = _rows2(k_rope, _BF16, total_tokens, KDA_LATENT_ROPE, "k_rope")
     p, num_pages, page_size = _pages(cache, cache_dtype)
-    rc = load().kda_latent_append(cp, ldc, rp, ldr, p, cache_dtype, num_pages, page_size, _dense(slots, _I32),
-                                  total_tokens, _stream(stream))
+    sp = _dense(slots, _I32, total_tokens, "slots")
+    _on_gpu(c, k_rope, cache, slots)
+    rc = load().kda_latent_append(cp, ldc, rp, ldr, p, cache_dtype, num_pages, page_size, sp, total_tokens, _stream(stream))
     if rc:
         _check(rc, "kda_latent_append")
 
 
-# (the calls themselves, with the outputs as addresses: the functions that allocate outputs have nothing
-# to check about them)
+# (the calls with outputs as tensors or, from the functions that allocate them, as addresses)
 
-def _latent_gather(cache, cache_dtype, block_table, start_pos, cu_seqlens, cu_host, num_seqs, total_tokens, cp, ldc, rp,
+def _latent_gather(cache, cache_dtype, block_table, start_pos, cu_seqlens, cu_host, num_seqs, total_tokens, c, cp, ldc, r, rp,
                    ldr, stream):
     p, num_pages, page_size = _pages(cache, cache_dtype)
-    rc = load().kda_latent_gather(p, cache_dtype, num_pages, page_size, _dense(block_table, _I32), block_table.shape[1],
-                                  _dense(start_pos, _I32), _dense(cu_seqlens, _I32), cu_host.data_ptr(), num_seqs,
+    tp, table = _dense(block_table, _I32, 0, "block_table"), block_table.shape
+    if len(table) != 2 or table[0] < num_seqs:
+        _short("block_table", block_table, f"[{num_seqs}, max_pages]")
+    sp, cu = _dense(start_pos, _I32, num_seqs, "start_pos"), _dense(cu_seqlens, _I32, num_seqs + 1, "cu_seqlens")
+    _on_gpu(cache, block_table, start_pos, cu_seqlens, c, r)
+    rc = load().kda_latent_gather(p, cache_dtype, num_pages, page_size, tp, table[1], sp, cu, cu_host.data_ptr(), num_seqs,
                                   total_tokens, cp, ldc, rp, ldr, _stream(stream))
     if rc:
         _check(rc, "kda_latent_gather")
 
 
 def _latent_decode(q, cache, cache_dtype, block_table, seq_lens, N, K, H, sm_scale, out, lse, stream):
+    qp = _dense(q, _BF16, N * K * H * 576, "q")
+    if q.size(-1) != 576:
+        _short("q", q, "[N, K, H, 576] (the absorbed query, then its position part)")
     p, num_pages, page_size = _pages(cache, cache_dtype)
-    rc = load().kda_latent_decode(_dense(q, _BF16), p, cache_dtype, num_pages, page_size, _dense(block_table, _I32),
-                                  block_table.shape[1], _dense(seq_lens, _I32), N, K, H, sm_scale, out, lse,
+    tp, table = _dense(block_table, _I32, 0, "block_table"), block_table.shape
+    if len(table) != 2 or table[0] < N:
+        _short("block_table", block_table, f"[{N}, max_pages]")
+    lp = _dense(seq_lens, _I32, N, "seq_lens")
+    _on_gpu(q, cache, block_table, seq_lens)
+    if type(out) is not int:
+        out, lse = _out(out, _BF16, N * K * H * KDA_LATENT_DIM, "out"), _out(lse, _F32, N * K * H, "lse")
+    rc = load().kda_latent_decode(qp, p, cache_dtype, num_pages, page_size, tp, table[1], lp, N, K, H, sm_scale, out, lse,
                                   _stream(stream))
     if rc:
         _check(rc, "kda_latent_decode")
 
 
 def _latent_prefill(q, k, v, k_rope, cu_q, cq, cu_k, ck, num_seqs, total_q, total_k, H, causal, sm_scale, out, lse, stream):
-    kp, ldk, hdk = _rows3(k, _BF16, 128, 128)
-    vp, ldv, hdv = _rows3(v, _BF16, 128, 128)
-    rp, ldr = _rows2(k_rope, _BF16, KDA_LATENT_ROPE)
-    rc = load().kda_latent_prefill(_dense(q, _BF16), kp, ldk, hdk, vp, ldv, hdv, rp, ldr, _dense(cu_q, _I32), cq.data_ptr(),
-                                   _dense(cu_k, _I32), ck.data_ptr(), num_seqs, total_q, total_k, H, causal, sm_scale,
-                                   out, lse, _stream(stream))
+    qp = _dense(q, _BF16, total_q * H * 192, "q")
+    if q.size(-1) != 192:
+        _short("q", q, "[Tq, H, 192]")
+    kp, ldk, hdk = _rows3(k, _BF16, total_k, H, 128, 128, "k")
+    vp, ldv, hdv = _rows3(v, _BF16, total_k, H, 128, 128, "v")
+    rp, ldr = _rows2(k_rope, _BF16, total_k, KDA_LATENT_ROPE, "k_rope")
+    cqd, ckd = _dense(cu_q, _I32, num_seqs + 1, "cu_q"), _dense(cu_k, _I32, num_seqs + 1, "cu_k")
+    _on_gpu(q, k, v, k_rope, cu_q, cu_k)
+    if type(out) is not int:
+        out, lse = _out(out, _BF16, total_q * H * 128, "out"), _out(lse, _F32, total_q * H, "lse")
+    rc = load().kda_latent_prefill(qp, kp, ldk, hdk, vp, ldv, hdv, rp, ldr, cqd, cq.data_ptr(), ckd, ck.data_ptr(), num_seqs,
+                                   total_q, total_k, H, causal, sm_scale, out, lse, _stream(stream))
     if rc:
         _check(rc, "kda_latent_prefill")
 
 
-def _prob_rows(t, per: int, V: int):
+def _prob_rows(t, N: int, per: int, V: int, what: str):
     """(address, stride) of probabilities [N, per, V] whose N * per rows are one constant stride apart."""
-    p, seq, ld = _rows3(t, _F32, -1, V)
+    p, seq, ld = _rows3(t, _F32, N, per, V, -1, what)
     if per <= 1:
         return p, V if seq < 0 else seq
     if seq >= 0 and seq != per * ld:
-        raise ValueError("the probability rows of consecutive sequences must be evenly spaced")
+        raise ValueError(f"{what}: the probability rows of consecutive sequences must be evenly spaced")
     return p, ld
 
 
 def _verify_draft(target_probs, draft_probs, draft_tokens, num_draft, u_accept, u_sample, N, K, V, tokens, num_tokens,
                   stream):
-    tp, ldp = _prob_rows(target_probs, K + 1, V)
-    dp, ldq = (None, 0) if draft_probs is None else _prob_rows(draft_probs, K, V)
-    rc = load().kda_verify_draft(tp, ldp, dp, ldq, _dense(draft_tokens, _I32), _dense(num_draft, _I32),
-                                 _dense(u_accept, _F32), _dense(u_sample, _F32), N, K, V, tokens, num_tokens,
-                                 _stream(stream))
+    tp, ldp = _prob_rows(target_probs, N, K + 1, V, "target_probs")
+    dp, ldq = (None, 0) if draft_probs is None else _prob_rows(draft_probs, N, K, V, "draft_probs")
+    xp, up = _dense(draft_tokens, _I32, N * K, "draft_tokens"), _dense(u_accept, _F32, N * K, "u_accept")
+    np_, sp = _dense(num_draft, _I32, N, "num_draft"), _dense(u_sample, _F32, N, "u_sample")
+    _on_gpu(target_probs, draft_probs, draft_tokens, num_draft, u_accept, u_sample)
+    if type(tokens) is not int:
+        tokens, num_tokens = _out(tokens, _I32, N * (K + 1), "tokens"), _out(num_tokens, _I32, N, "num_tokens")
+    rc = load().kda_verify_draft(tp, ldp, dp, ldq, xp, np_, up, sp, N, K, V, tokens, num_tokens, _stream(stream))
     if rc:
         _check(rc, "kda_verify_draft")
 
 
 def kda_latent_gather(cache, cache_dtype: int, block_table, start_pos, cu_seqlens, cu_seqlens_host, num_seqs: int,
                       total_tokens: int, c, k_rope, stream=None):
-    cp, ldc = _rows2(c, _BF16, KDA_LATENT_DIM)
-    rp, ldr = _rows2(k_rope, _BF16, KDA_LATENT_ROPE)
-    _latent_gather(cache, cache_dtype, block_table, start_pos, cu_seqlens, _host32(cu_seqlens_host), num_seqs, total_tokens,
-                   cp, ldc, rp, ldr, stream)
+    cp, ldc = _rows2(c, _BF16, total_tokens, KDA_LATENT_DIM, "c")
+    rp, ldr = _rows2(k_rope, _BF16, total_tokens, KDA_LATENT_ROPE, "k_rope")
+    cu_host = _host_offsets(cu_seqlens_host, num_seqs, "cu_seqlens_host")
+    _latent_gather(cache, cache_dtype, block_table, start_pos, cu_seqlens, cu_host, num_seqs, total_tokens, c, cp, ldc, k_rope,
+                   rp, ldr, stream)
 
 
 def kda_latent_decode(q, cache, cache_dtype: int, block_table, seq_lens, N: int, K: int, H: int, sm_scale: float, out,
                       lse, stream=None):
-    _latent_decode(q, cache, cache_dtype, block_table, seq_lens, N, K, H, sm_scale, _dense(out, _BF16), _dense(lse, _F32),
-                   stream)
+    _latent_decode(q, cache, cache_dtype, block_table, seq_lens, N, K, H, sm_scale, out, lse, stream)
 
 
 def kda_latent_prefill(q, k, v, k_rope, cu_q, cu_q_host, cu_k, cu_k_host, num_seqs: int, total_q: int, total_k: int,
                        H: int, causal: int, sm_scale: float, out, lse, stream=None):
-    _latent_prefill(q, k, v, k_rope, cu_q, _host32(cu_q_host), cu_k, _host32(cu_k_host), num_seqs, total_q, total_k, H,
-                    causal, sm_scale, _dense(out, _BF16), _dense(lse, _F32), stream)
+    _latent_prefill(q, k, v, k_rope, cu_q, _host_offsets(cu_q_host, num_seqs, "cu_q_host"), cu_k,
+                    _host_offsets(cu_k_host, num_seqs, "cu_k_host"), num_seqs, total_q, total_k, H, causal, sm_scale, out, lse,
+                    stream)
 
 
 def kda_verify_draft(target_probs, draft_probs, draft_tokens, num_draft, u_accept, u_sample, N: int, K: int, V: int,
                      tokens, num_tokens, stream=None):
-    _verify_draft(target_probs, draft_probs, draft_tokens, num_draft, u_accept, u_sample, N, K, V, _dense(tokens, _I32),
-                  _dense(num_tokens, _I32), stream)
+    _verify_draft(target_probs, draft_probs, draft_tokens, num_draft, u_accept, u_sample, N, K, V, tokens, num_tokens,
+                  stream)
 
 
 def kda_debug_expire_wait(limit_ns: int, stream=None):
@@ -576,8 +635,8 @@ def latent_gather(cache, cache_dtype: int, block_table, cu_seqlens_host, cu_seql
         cu_seqlens = cu_host.to(dev)
     c = torch.empty((T, KDA_LATENT_DIM), device=dev, dtype=_BF16)
     r = torch.empty((T, KDA_LATENT_ROPE), device=dev, dtype=_BF16)
-    _latent_gather(cache, cache_dtype, block_table, start_pos, cu_seqlens, cu_host, N, T, c.data_ptr(), KDA_LATENT_DIM,
-                   r.data_ptr(), KDA_LATENT_ROPE, stream)
+    _latent_gather(cache, cache_dtype, block_table, start_pos, cu_seqlens, cu_host, N, T, None, c.data_ptr(), KDA_LATENT_DIM,
+                   None, r.data_ptr(), KDA_LATENT_ROPE, stream)
     return c, r
 
 
@@ -598,12 +657,14 @@ def latent_prefill(q, k, v, k_rope, cu_q_host, cu_k_host, sm_scale: float, causa
     """Expanded latent attention of q [Tq, H, 192] over k, v [Tk, H, 128] and k_rope [Tk, 64]; returns
     (out [Tq, H, 128] bf16, lse [Tq, H] fp32 or None)."""
     cq, ck = _host32(cu_q_host), _host32(cu_k_host)
+    Tq, H, _ = q.shape
+    if ck.numel() != cq.numel():
+        raise ValueError("cu_q_host and cu_k_host: offsets of one number of sequences")
     dev = q.device
     if cu_q is None:
         cu_q = cq.to(dev)
     if cu_k is None:
         cu_k = ck.to(dev)
-    Tq, H, _ = q.shape
     out = torch.empty((Tq, H, 128), device=dev, dtype=_BF16)
     lse = torch.empty((Tq, H), device=dev, dtype=_F32) if want_lse else None
     _latent_prefill(q, k, v, k_rope, cu_q, cq, cu_k, ck, cq.numel() - 1, Tq, k.shape[0], H, int(causal), sm_scale,
@@ -615,6 +676,8 @@ def verify_draft(target_probs, draft_probs, draft_tokens, u_accept, u_sample, nu
     """Accept or reject draft_tokens [N, K] against target_probs [N, K + 1, V] (draft_probs [N, K, V] or None);
     returns (tokens [N, K + 1] int32, num_tokens [N] int32)."""
     N, K1, V = target_probs.shape
+    if draft_tokens.size(-1) != K1 - 1 or u_accept.size(-1) != K1 - 1:
+        _short("draft_tokens, u_accept", draft_tokens, f"[{N}, {K1 - 1}]")
     dev = target_probs.device
     tokens = torch.empty((N, K1), device=dev, dtype=_I32)
     num = torch.empty((N,), device=dev, dtype=_I32)
