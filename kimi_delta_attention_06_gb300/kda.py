@@ -9,7 +9,7 @@ arguments: torch
 tensors become raw device pointers, the current torch stream becomes the
 ``stream`` argument, and a negative status raises ``KdaError``.  ``prefill``,
 ``decode_step``, ``latent_gather``, ``latent_decode``, ``latent_prefill`` and ``verify_draft``
-additionally allocate the output tensors with torch.
+additionally allocate the output tensors with torch (a call with ``stream=`` from that stream's memory).
 
 There is no fallback: if ``libkda.so`` is missing or cannot be loaded the
 first call raises.
@@ -153,6 +153,41 @@ def _stream(stream) -> int:
             return _raw_stream(torch.cuda.current_device())
         stream = torch.cuda.current_stream()
     return stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)
+
+
+def _side(stream):
+    """The torch stream of a ``stream`` argument, None where it is the current one."""
+    if stream is None:
+        return None
+    handle = _stream(stream)
+    if handle == _stream(None):
+        return None
+    if isinstance(stream, torch.cuda.Stream):
+        return stream
+    return torch.cuda.ExternalStream(handle) if handle else torch.cuda.default_stream()
+
+
+def _empty(shape, dev, dtype, side=None):
+    """An output for a call on the current stream or on ``side``.  Memory that the current stream's allocator
+    hands out again may still be in use by work pending there, which nothing orders before a call on another
+    stream: such a call's outputs come from its own stream's memory, and are marked as used here too."""
+    if side is None:
+        return torch.empty(shape, device=dev, dtype=dtype)
+    here = torch.cuda.current_stream(dev)
+    with torch.cuda.stream(side):
+        t = torch.empty(shape, device=dev, dtype=dtype)
+    t.record_stream(here)
+    return t
+
+
+def _to_device(host: torch.Tensor, dev, side=None):
+    """A device copy of a host array that lives as long as this call's launches need it, on ``side`` too: the
+    copy is complete on return (pageable memory), and its memory is not handed out again before ``side`` gets
+    past the work it holds by then."""
+    t = host.to(dev)
+    if side is not None:
+        t.record_stream(side)
+    return t
 
 
 def _check(rc: int, what: str):
@@ -454,23 +489,35 @@ def kda_latent_append(c, k_rope, cache, cache_dtype: int, slots, total_tokens: i
         _check(rc, "kda_latent_append")
 
 
-# (the calls with outputs as tensors or, from the functions that allocate them, as addresses)
+# (the calls with the caller's outputs or, where `make` is set, with outputs of their own)
 
-def _latent_gather(cache, cache_dtype, block_table, start_pos, cu_seqlens, cu_host, num_seqs, total_tokens, c, cp, ldc, r, rp,
-                   ldr, stream):
+def _latent_gather(cache, cache_dtype, block_table, start_pos, cu_seqlens, cu_host, num_seqs, total_tokens, c, k_rope, stream,
+                   make=False):
+    if not make:
+        cp, ldc = _rows2(c, _BF16, total_tokens, KDA_LATENT_DIM, "c")
+        rp, ldr = _rows2(k_rope, _BF16, total_tokens, KDA_LATENT_ROPE, "k_rope")
     p, num_pages, page_size = _pages(cache, cache_dtype)
     tp, table = _dense(block_table, _I32, 0, "block_table"), block_table.shape
     if len(table) != 2 or table[0] < num_seqs:
         _short("block_table", block_table, f"[{num_seqs}, max_pages]")
     sp, cu = _dense(start_pos, _I32, num_seqs, "start_pos"), _dense(cu_seqlens, _I32, num_seqs + 1, "cu_seqlens")
-    _on_gpu(cache, block_table, start_pos, cu_seqlens, c, r)
+    _on_gpu(cache, block_table, start_pos, cu_seqlens, c, k_rope)
+    if make:
+        dev, side = cache.device, _side(stream)
+        if cu is None:
+            cu_seqlens = _to_device(cu_host, dev, side)
+            cu = cu_seqlens.data_ptr()
+        c = _empty((total_tokens, KDA_LATENT_DIM), dev, _BF16, side)
+        k_rope = _empty((total_tokens, KDA_LATENT_ROPE), dev, _BF16, side)
+        cp, ldc, rp, ldr = c.data_ptr(), KDA_LATENT_DIM, k_rope.data_ptr(), KDA_LATENT_ROPE
     rc = load().kda_latent_gather(p, cache_dtype, num_pages, page_size, tp, table[1], sp, cu, cu_host.data_ptr(), num_seqs,
                                   total_tokens, cp, ldc, rp, ldr, _stream(stream))
     if rc:
         _check(rc, "kda_latent_gather")
+    return c, k_rope
 
 
-def _latent_decode(q, cache, cache_dtype, block_table, seq_lens, N, K, H, sm_scale, out, lse, stream):
+def _latent_decode(q, cache, cache_dtype, block_table, seq_lens, N, K, H, sm_scale, out, lse, stream, make=False, want_lse=False):
     qp = _dense(q, _BF16, N * K * H * 576, "q")
     if q.size(-1) != 576:
         _short("q", q, "[N, K, H, 576] (the absorbed query, then its position part)")
@@ -478,17 +525,24 @@ def _latent_decode(q, cache, cache_dtype, block_table, seq_lens, N, K, H, sm_sca
     tp, table = _dense(block_table, _I32, 0, "block_table"), block_table.shape
     if len(table) != 2 or table[0] < N:
         _short("block_table", block_table, f"[{N}, max_pages]")
-    lp = _dense(seq_lens, _I32, N, "seq_lens")
+    sp = _dense(seq_lens, _I32, N, "seq_lens")
     _on_gpu(q, cache, block_table, seq_lens)
-    if type(out) is not int:
-        out, lse = _out(out, _BF16, N * K * H * KDA_LATENT_DIM, "out"), _out(lse, _F32, N * K * H, "lse")
-    rc = load().kda_latent_decode(qp, p, cache_dtype, num_pages, page_size, tp, table[1], lp, N, K, H, sm_scale, out, lse,
+    if make:
+        dev, side = q.device, _side(stream)
+        out = _empty((N, K, H, KDA_LATENT_DIM), dev, _BF16, side)
+        lse = _empty((N, K, H), dev, _F32, side) if want_lse else None
+        op, lp = out.data_ptr(), lse.data_ptr() if want_lse else None
+    else:
+        op, lp = _out(out, _BF16, N * K * H * KDA_LATENT_DIM, "out"), _out(lse, _F32, N * K * H, "lse")
+    rc = load().kda_latent_decode(qp, p, cache_dtype, num_pages, page_size, tp, table[1], sp, N, K, H, sm_scale, op, lp,
                                   _stream(stream))
     if rc:
         _check(rc, "kda_latent_decode")
+    return out, lse
 
 
-def _latent_prefill(q, k, v, k_rope, cu_q, cq, cu_k, ck, num_seqs, total_q, total_k, H, causal, sm_scale, out, lse, stream):
+def _latent_prefill(q, k, v, k_rope, cu_q, cq, cu_k, ck, num_seqs, total_q, total_k, H, causal, sm_scale, out, lse, stream,
+                    make=False, want_lse=False):
     qp = _dense(q, _BF16, total_q * H * 192, "q")
     if q.size(-1) != 192:
         _short("q", q, "[Tq, H, 192]")
@@ -497,12 +551,24 @@ def _latent_prefill(q, k, v, k_rope, cu_q, cq, cu_k, ck, num_seqs, total_q, tota
     rp, ldr = _rows2(k_rope, _BF16, total_k, KDA_LATENT_ROPE, "k_rope")
     cqd, ckd = _dense(cu_q, _I32, num_seqs + 1, "cu_q"), _dense(cu_k, _I32, num_seqs + 1, "cu_k")
     _on_gpu(q, k, v, k_rope, cu_q, cu_k)
-    if type(out) is not int:
-        out, lse = _out(out, _BF16, total_q * H * 128, "out"), _out(lse, _F32, total_q * H, "lse")
+    if make:
+        dev, side = q.device, _side(stream)
+        if cqd is None:
+            cu_q = _to_device(cq, dev, side)
+            cqd = cu_q.data_ptr()
+        if ckd is None:
+            cu_k = _to_device(ck, dev, side)
+            ckd = cu_k.data_ptr()
+        out = _empty((total_q, H, 128), dev, _BF16, side)
+        lse = _empty((total_q, H), dev, _F32, side) if want_lse else None
+        op, lp = out.data_ptr(), lse.data_ptr() if want_lse else None
+    else:
+        op, lp = _out(out, _BF16, total_q * H * 128, "out"), _out(lse, _F32, total_q * H, "lse")
     rc = load().kda_latent_prefill(qp, kp, ldk, hdk, vp, ldv, hdv, rp, ldr, cqd, cq.data_ptr(), ckd, ck.data_ptr(), num_seqs,
-                                   total_q, total_k, H, causal, sm_scale, out, lse, _stream(stream))
+                                   total_q, total_k, H, causal, sm_scale, op, lp, _stream(stream))
     if rc:
         _check(rc, "kda_latent_prefill")
+    return out, lse
 
 
 def _prob_rows(t, N: int, per: int, V: int, what: str):
@@ -516,26 +582,28 @@ def _prob_rows(t, N: int, per: int, V: int, what: str):
 
 
 def _verify_draft(target_probs, draft_probs, draft_tokens, num_draft, u_accept, u_sample, N, K, V, tokens, num_tokens,
-                  stream):
+                  stream, make=False):
     tp, ldp = _prob_rows(target_probs, N, K + 1, V, "target_probs")
     dp, ldq = (None, 0) if draft_probs is None else _prob_rows(draft_probs, N, K, V, "draft_probs")
     xp, up = _dense(draft_tokens, _I32, N * K, "draft_tokens"), _dense(u_accept, _F32, N * K, "u_accept")
     np_, sp = _dense(num_draft, _I32, N, "num_draft"), _dense(u_sample, _F32, N, "u_sample")
     _on_gpu(target_probs, draft_probs, draft_tokens, num_draft, u_accept, u_sample)
-    if type(tokens) is not int:
-        tokens, num_tokens = _out(tokens, _I32, N * (K + 1), "tokens"), _out(num_tokens, _I32, N, "num_tokens")
-    rc = load().kda_verify_draft(tp, ldp, dp, ldq, xp, np_, up, sp, N, K, V, tokens, num_tokens, _stream(stream))
+    if make:
+        dev, side = target_probs.device, _side(stream)
+        tokens, num_tokens = _empty((N, K + 1), dev, _I32, side), _empty((N,), dev, _I32, side)
+        op, mp = tokens.data_ptr(), num_tokens.data_ptr()
+    else:
+        op, mp = _out(tokens, _I32, N * (K + 1), "tokens"), _out(num_tokens, _I32, N, "num_tokens")
+    rc = load().kda_verify_draft(tp, ldp, dp, ldq, xp, np_, up, sp, N, K, V, op, mp, _stream(stream))
     if rc:
         _check(rc, "kda_verify_draft")
+    return tokens, num_tokens
 
 
 def kda_latent_gather(cache, cache_dtype: int, block_table, start_pos, cu_seqlens, cu_seqlens_host, num_seqs: int,
                       total_tokens: int, c, k_rope, stream=None):
-    cp, ldc = _rows2(c, _BF16, total_tokens, KDA_LATENT_DIM, "c")
-    rp, ldr = _rows2(k_rope, _BF16, total_tokens, KDA_LATENT_ROPE, "k_rope")
-    cu_host = _host_offsets(cu_seqlens_host, num_seqs, "cu_seqlens_host")
-    _latent_gather(cache, cache_dtype, block_table, start_pos, cu_seqlens, cu_host, num_seqs, total_tokens, c, cp, ldc, k_rope,
-                   rp, ldr, stream)
+    _latent_gather(cache, cache_dtype, block_table, start_pos, cu_seqlens,
+                   _host_offsets(cu_seqlens_host, num_seqs, "cu_seqlens_host"), num_seqs, total_tokens, c, k_rope, stream)
 
 
 def kda_latent_decode(q, cache, cache_dtype: int, block_table, seq_lens, N: int, K: int, H: int, sm_scale: float, out,
@@ -578,13 +646,13 @@ def prefill(q, k, v, log_alpha, beta, cu_seqlens_host, init_state=None, ckpt_str
     Dv = v.shape[2]
     cu_host = cu_seqlens_host.to(device="cpu", dtype=torch.int32).contiguous()
     N = cu_host.numel() - 1
-    dev = q.device
+    dev, side = q.device, _side(stream)
     if cu_seqlens is None:
-        cu_seqlens = cu_host.to(dev, non_blocking=False)
-    out = torch.empty(T, H, Dv, device=dev, dtype=out_dtype)
-    fin = torch.empty(N, H, Dk, Dv, device=dev, dtype=torch.float32) if want_final else None
+        cu_seqlens = _to_device(cu_host, dev, side)
+    out = _empty((T, H, Dv), dev, out_dtype, side)
+    fin = _empty((N, H, Dk, Dv), dev, torch.float32, side) if want_final else None
     nck = kda_ckpt_count_ex(cu_host, start_pos_host, ckpt_stride) if ckpt_stride > 0 else 0
-    ck = torch.empty(nck, H, Dk, Dv, device=dev, dtype=torch.float32) if ckpt_stride > 0 else None
+    ck = _empty((nck, H, Dk, Dv), dev, torch.float32, side) if ckpt_stride > 0 else None
     odt = KDA_OUT_F32 if out_dtype == torch.float32 else KDA_OUT_BF16
     if segments > 0 and N == 1:
         sp0 = 0 if start_pos_host is None else int(torch.as_tensor(start_pos_host).reshape(-1)[0])
@@ -602,7 +670,7 @@ def prefill(q, k, v, log_alpha, beta, cu_seqlens_host, init_state=None, ckpt_str
         sp = None if start_pos_host is None else start_pos_host.to(device="cpu", dtype=torch.int32).contiguous()
         kda_chunk_prefill_ex(q, k, v, log_alpha, beta, init_state, cu_seqlens, cu_host, N, T, H, Dk, Dv,
                              out, odt, fin, ck if nck > 0 else None, ckpt_stride, decay,
-                             None if sp is None else sp.to(dev), sp, norm_gamma, norm_eps, stream)
+                             None if sp is None else _to_device(sp, dev, side), sp, norm_gamma, norm_eps, stream)
     return out, fin, ck
 
 
@@ -610,7 +678,7 @@ def decode_step(q, k, v, log_alpha, beta, state, out_dtype=torch.bfloat16, strea
     """Run kda_decode_step in place on ``state``; returns the output tensor."""
     N, H, Dk = q.shape
     Dv = v.shape[2]
-    out = torch.empty(N, H, Dv, device=q.device, dtype=out_dtype)
+    out = _empty((N, H, Dv), q.device, out_dtype, _side(stream))
     kda_decode_step(q, k, v, log_alpha, beta, state, out,
                     KDA_OUT_F32 if out_dtype == torch.float32 else KDA_OUT_BF16, N, H, Dk, Dv, stream)
     return out
@@ -629,27 +697,15 @@ def latent_append(c, k_rope, cache, cache_dtype: int, slots, stream=None):
 def latent_gather(cache, cache_dtype: int, block_table, cu_seqlens_host, cu_seqlens=None, start_pos=None, stream=None):
     """Read sequences back as dense rows; returns (c [T, 512], k_rope [T, 64]), bf16."""
     cu_host = _host32(cu_seqlens_host)
-    N, T = cu_host.numel() - 1, _last32(cu_host)
-    dev = cache.device
-    if cu_seqlens is None:
-        cu_seqlens = cu_host.to(dev)
-    c = torch.empty((T, KDA_LATENT_DIM), device=dev, dtype=_BF16)
-    r = torch.empty((T, KDA_LATENT_ROPE), device=dev, dtype=_BF16)
-    _latent_gather(cache, cache_dtype, block_table, start_pos, cu_seqlens, cu_host, N, T, None, c.data_ptr(), KDA_LATENT_DIM,
-                   None, r.data_ptr(), KDA_LATENT_ROPE, stream)
-    return c, r
+    return _latent_gather(cache, cache_dtype, block_table, start_pos, cu_seqlens, cu_host, cu_host.numel() - 1,
+                          _last32(cu_host), None, None, stream, make=True)
 
 
 def latent_decode(q, cache, cache_dtype: int, block_table, seq_lens, sm_scale: float, want_lse: bool = False, stream=None):
     """Absorbed latent attention of q [N, K, H, 576] over the cache; returns (out [N, K, H, 512] bf16,
     lse [N, K, H] fp32 or None)."""
     N, K, H, _ = q.shape
-    dev = q.device
-    out = torch.empty((N, K, H, KDA_LATENT_DIM), device=dev, dtype=_BF16)
-    lse = torch.empty((N, K, H), device=dev, dtype=_F32) if want_lse else None
-    _latent_decode(q, cache, cache_dtype, block_table, seq_lens, N, K, H, sm_scale, out.data_ptr(),
-                   lse.data_ptr() if want_lse else None, stream)
-    return out, lse
+    return _latent_decode(q, cache, cache_dtype, block_table, seq_lens, N, K, H, sm_scale, None, None, stream, True, want_lse)
 
 
 def latent_prefill(q, k, v, k_rope, cu_q_host, cu_k_host, sm_scale: float, causal: bool = True, cu_q=None, cu_k=None,
@@ -657,19 +713,11 @@ def latent_prefill(q, k, v, k_rope, cu_q_host, cu_k_host, sm_scale: float, causa
     """Expanded latent attention of q [Tq, H, 192] over k, v [Tk, H, 128] and k_rope [Tk, 64]; returns
     (out [Tq, H, 128] bf16, lse [Tq, H] fp32 or None)."""
     cq, ck = _host32(cu_q_host), _host32(cu_k_host)
-    Tq, H, _ = q.shape
     if ck.numel() != cq.numel():
         raise ValueError("cu_q_host and cu_k_host: offsets of one number of sequences")
-    dev = q.device
-    if cu_q is None:
-        cu_q = cq.to(dev)
-    if cu_k is None:
-        cu_k = ck.to(dev)
-    out = torch.empty((Tq, H, 128), device=dev, dtype=_BF16)
-    lse = torch.empty((Tq, H), device=dev, dtype=_F32) if want_lse else None
-    _latent_prefill(q, k, v, k_rope, cu_q, cq, cu_k, ck, cq.numel() - 1, Tq, k.shape[0], H, int(causal), sm_scale,
-                    out.data_ptr(), lse.data_ptr() if want_lse else None, stream)
-    return out, lse
+    Tq, H, _ = q.shape
+    return _latent_prefill(q, k, v, k_rope, cu_q, cq, cu_k, ck, cq.numel() - 1, Tq, k.shape[0], H, int(causal), sm_scale, None,
+                           None, stream, True, want_lse)
 
 
 def verify_draft(target_probs, draft_probs, draft_tokens, u_accept, u_sample, num_draft=None, stream=None):
@@ -678,9 +726,5 @@ def verify_draft(target_probs, draft_probs, draft_tokens, u_accept, u_sample, nu
     N, K1, V = target_probs.shape
     if draft_tokens.size(-1) != K1 - 1 or u_accept.size(-1) != K1 - 1:
         _short("draft_tokens, u_accept", draft_tokens, f"[{N}, {K1 - 1}]")
-    dev = target_probs.device
-    tokens = torch.empty((N, K1), device=dev, dtype=_I32)
-    num = torch.empty((N,), device=dev, dtype=_I32)
-    _verify_draft(target_probs, draft_probs, draft_tokens, num_draft, u_accept, u_sample, N, K1 - 1, V, tokens.data_ptr(),
-                  num.data_ptr(), stream)
-    return tokens, num
+    return _verify_draft(target_probs, draft_probs, draft_tokens, num_draft, u_accept, u_sample, N, K1 - 1, V, None, None, stream,
+                         make=True)
