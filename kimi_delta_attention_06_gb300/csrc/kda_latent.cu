@@ -461,13 +461,18 @@ kda_latent_decode_kernel(const __grid_constant__ LatMaps maps, const LatArgs a)
                         // (held above -90, so that the sums of 2^(x - m) stay within fp32; see f0, f1)
                         e0 = static_cast<float>(max(static_cast<int>(__float_as_uint(s0) >> 23) - 127, -90));
                         e1 = static_cast<float>(max(static_cast<int>(__float_as_uint(s1) >> 23) - 127, -90));
+                        // a scale that is NaN or infinite: the token's scores are NaN, for the rows that see it, and
+                        // it enters P as if it were 1, where the others have zeros
+                        float a0 = e0, a1 = e1;
+                        if (!(fabsf(s0) < INFINITY)) { a0 = __int_as_float(0x7fffffff); s0 = 1.f; e0 = 0.f; }
+                        if (!(fabsf(s1) < INFINITY)) { a1 = __int_as_float(0x7fffffff); s1 = 1.f; e1 = 0.f; }
                         float xr[R / 2];
                         tmem_ld_s<R>(tmS + (g & 1) * Sh::kS + R + lane_tm, xr);
                         // x: scores in powers of two, plus the scale's exponent (the weights carry s)
 #pragma unroll
                         for (int i = 0; i < R / 2; ++i) {
                             const float sa = s_a[8 * (i >> 2) + rq + (i & 1)] * (i & 2 ? s1 : s0);
-                            x[i] = fmaf(x[i], sa, fmaf(xr[i], a.scale_log2, i & 2 ? e1 : e0));
+                            x[i] = fmaf(x[i], sa, fmaf(xr[i], a.scale_log2, i & 2 ? a1 : a0));
                         }
                     } else {
 #pragma unroll
