@@ -38,93 +38,6 @@ struct LatentCache {
     int num_pages, page_size, max_pages;
 };
 
-// One warp computes one row in fp32, straight from the formula.  Lane i owns latents
-// 16 i .. 16 i + 15 and position values 2 i, 2 i + 1.
-template <bool E4M3>
-__device__ void latent_row(const uint16_t* __restrict__ q, const LatentCache& ch, int n, int see, float scale_log2,
-                           uint16_t* __restrict__ out, float* __restrict__ lse, int* status, int quarter)
-{
-    const int lane = threadIdx.x & 31;
-    float qc[16], acc[16];
-    {
-        const uint4* p = reinterpret_cast<const uint4*>(q) + 2 * lane;
-        const uint4 a = p[0], b = p[1];
-        const uint32_t w[8] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
-#pragma unroll
-        for (int i = 0; i < 8; ++i) {
-            const float2 f = bf16x2_bits_to_f32(w[i]);
-            qc[2 * i] = f.x; qc[2 * i + 1] = f.y;
-        }
-    }
-    const float2 qr = bf16x2_bits_to_f32(reinterpret_cast<const uint32_t*>(q + kLatDim)[lane]);
-#pragma unroll
-    for (int i = 0; i < 16; ++i) acc[i] = 0.f;
-    float m = -INFINITY, l = 0.f;
-    int page = 0;
-    for (int t = 0; t < see; ++t) {
-        const int in = t % ch.page_size;
-        if (in == 0 || t == 0) {
-            page = ch.table[static_cast<size_t>(n) * ch.max_pages + t / ch.page_size];
-            if (page < 0 || page >= ch.num_pages) {
-                if (lane == 0) set_status(status, kStatusIndex);
-                page = 0;
-            }
-        }
-        const uint8_t* row = ch.rows + (static_cast<size_t>(page) * ch.page_size + in) * lat_row_bytes(E4M3);
-        float c[16];
-        float2 r;
-        if constexpr (E4M3) {
-            const uint4 a = reinterpret_cast<const uint4*>(row)[lane];
-            const uint32_t w[4] = {a.x, a.y, a.z, a.w};
-            const float s = *reinterpret_cast<const float*>(row + kLatScaleAt);
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                const float2 f = e4m3x2_to_f32(w[i]), g = e4m3x2_to_f32(w[i] >> 16);
-                c[4 * i] = f.x * s; c[4 * i + 1] = f.y * s; c[4 * i + 2] = g.x * s; c[4 * i + 3] = g.y * s;
-            }
-            r = bf16x2_bits_to_f32(reinterpret_cast<const uint32_t*>(row + kLatDim)[lane]);
-        } else {
-            const uint4* p = reinterpret_cast<const uint4*>(row) + 2 * lane;
-            const uint4 a = p[0], b = p[1];
-            const uint32_t w[8] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
-#pragma unroll
-            for (int i = 0; i < 8; ++i) {
-                const float2 f = bf16x2_bits_to_f32(w[i]);
-                c[2 * i] = f.x; c[2 * i + 1] = f.y;
-            }
-            r = bf16x2_bits_to_f32(reinterpret_cast<const uint32_t*>(row + 2 * kLatDim)[lane]);
-        }
-        float x = qr.x * r.x + qr.y * r.y;
-#pragma unroll
-        for (int i = 0; i < 16; ++i) x += qc[i] * c[i];
-#pragma unroll
-        for (int off = 16; off > 0; off >>= 1) x += __shfl_xor_sync(0xffffffffu, x, off);
-        x *= scale_log2;
-        if (x > m) {
-            const float f = lat_ex2(m - x);
-            m = x;
-            l *= f;
-#pragma unroll
-            for (int i = 0; i < 16; ++i) acc[i] *= f;
-        }
-        const float p = x == -INFINITY ? 0.f : lat_ex2(x - m);
-        l += p;
-#pragma unroll
-        for (int i = 0; i < 16; ++i) acc[i] += p * c[i];
-    }
-    const float inv = l == 0.f ? 0.f : 1.f / l;      // (a NaN sum stays NaN)
-    uint32_t o[8];
-#pragma unroll
-    for (int i = 0; i < 8; ++i) o[i] = f32x2_to_bf16x2_bits(acc[2 * i] * inv, acc[2 * i + 1] * inv);
-    uint4* d = reinterpret_cast<uint4*>(out) + 2 * lane;
-    if (quarter < 0 || lane >> 3 == quarter) {       // all channels, or 128 of them
-        d[0] = make_uint4(o[0], o[1], o[2], o[3]);
-        d[1] = make_uint4(o[4], o[5], o[6], o[7]);
-    }
-    if (lse && lane == 0) *lse = (m + log2f(l)) * 0.69314718055994531f;     // l = 0: -inf
-}
-
-
 // ---- work split ------------------------------------------------------------------------------
 // The sequences' 64-token tiles, one after another, are cut into G equal runs, one per CTA
 // (x the row tiles, which run side by side over the same tokens so that the second reader finds
@@ -323,13 +236,57 @@ __device__ __forceinline__ void load_o(uint32_t ta, float (&o)[16]) {
     }
 }
 
-// Row (n, j, h) again, in fp32 over exactly the tokens it sees: for results that a NaN or infinity
-// in a token that other rows of the tile see has spoilt (0 * NaN in the product with P).
-template <bool E4M3>
-__device__ __noinline__ void latent_row_again(const LatArgs& a, int n, int row, int see, int quarter = -1) {
-    const long long at = static_cast<long long>(n) * a.rows + row;
-    latent_row<E4M3>(a.q + at * kLatQ, a.ch, n, see, a.scale_log2, a.out + at * kLatDim,
-                     a.lse && quarter <= 0 ? a.lse + at : nullptr, a.status, quarter);
+// The last K - 1 tokens of a sequence are seen by some of its queries and not by others.  In P the others
+// have zeros there, but 0 * NaN is none in the product: latents that are NaN or infinite leave rows
+// [lo, hi) of the tile before it.  For the queries that see such a token, an e4m3 one's score is NaN, and
+// so is their sum; a bf16 one may score -inf and leave the sum alone, so mark_nonfinite puts it back.
+template <int R, bool E4M3>
+__device__ __forceinline__ bool drop_nonfinite(uint8_t* c, int lo, int hi, int tid) {
+    using Sh = LatShape<R, E4M3>;
+    constexpr int W = E4M3 ? 4 : 8;                              // slabs of latents
+    auto kept = [](uint32_t w) {                                 // NaN codes, or an exponent of ones: zeroed
+        return w & ~(E4M3 ? __vcmpeq4(w & 0x7f7f7f7fu, 0x7f7f7f7fu) : __vcmpeq2(w & 0x7f807f80u, 0x7f807f80u));
+    };
+    bool found = false;
+    for (int i = tid; i < W * (hi - lo) * 8; i += Sh::kSoft) {
+        const int ch = i & 7, slab = i / 8 % W, r = lo + i / (8 * W);
+        uint4* p = reinterpret_cast<uint4*>(c + (r >> 3) * Sh::kGroup + slab * Sh::kSlabC + (r & 7) * 128 + ch * 16);
+        const uint4 v = *p, k = make_uint4(kept(v.x), kept(v.y), kept(v.z), kept(v.w));
+        if (k.x != v.x || k.y != v.y || k.z != v.z || k.w != v.w) {
+            *p = k;
+            found = true;
+        }
+    }
+    return found;
+}
+
+// In O, the results of rows that see a NaN or infinite bf16 latent among the segment's tokens from `clear` on: NaN in
+// that channel (weight 0: 0 * inf; any other weight has made the sum NaN already).
+template <int R>
+__device__ __noinline__ void mark_nonfinite(const LatentCache& ch, int n, int clear, int from, int to, const int* s_j,
+                                            uint32_t ta, int channel) {
+#pragma unroll 1
+    for (int b = 0; b < 4; ++b) {
+        int first = 0x7fffffff;                                  // the first such token: rows that see past it
+        for (int t = max(from, max(clear, 0)); t < to && first == 0x7fffffff; ++t) {
+            int page = ch.table[static_cast<size_t>(n) * ch.max_pages + t / ch.page_size];
+            if (page < 0 || page >= ch.num_pages) page = 0;     // (as it was copied)
+            const uint8_t* row = ch.rows + (static_cast<size_t>(page) * ch.page_size + t % ch.page_size) * kLatRowBf16;
+            if ((reinterpret_cast<const uint16_t*>(row)[128 * b + channel] & 0x7f80u) == 0x7f80u) first = t;
+        }
+        if (!__any_sync(0xffffffffu, first != 0x7fffffff)) continue;
+#pragma unroll 1
+        for (int c0 = 0; c0 < R; c0 += 16) {
+            float o[16];
+            tc::tmem_ld16(ta + b * R + c0, o);
+            tc::tmem_wait_ld();
+#pragma unroll
+            for (int i = 0; i < 16; ++i)
+                if (clear + s_j[c0 + i] > first) o[i] = __int_as_float(0x7fffffff);
+            tc::tmem_st16(ta + b * R + c0, o);
+        }
+        tc::tmem_wait_st();
+    }
 }
 
 template <int R, bool E4M3>
@@ -396,6 +353,7 @@ kda_latent_decode_kernel(const __grid_constant__ LatMaps maps, const LatArgs a)
 #pragma unroll
             for (int i = 0; i < R / 4; ++i) { m[i] = -INFINITY; l[i] = 0.f; }
             const int clear = sw.len - (a.K - 1);               // tokens that every row sees
+            bool spoilt = false;                                // a later one held a NaN or infinity
             if constexpr (E4M3) {
                 // Q of the segment (the last S product of the segment before has run): a warp a row, the
                 // loads of 4 rows in flight
@@ -501,6 +459,8 @@ kda_latent_decode_kernel(const __grid_constant__ LatMaps maps, const LatArgs a)
                             if (16 * warp + tq + 8 >= valid) { s1 = 1.f; e1 = 0.f; }
                         }
                     }
+                    if (ok && a.K > 1)
+                        spoilt |= drop_nonfinite<R, E4M3>(sC + g % NS * Sh::kStage, max(0, clear - t * kTile), min(kTile, valid), tid);
                 }
                 bool grow = !ok;
 #pragma unroll
@@ -622,7 +582,8 @@ kda_latent_decode_kernel(const __grid_constant__ LatMaps maps, const LatArgs a)
                 if (lane < 4) s_red[warp * R + r] = v;
                 if (tid < 4) s_f[r] = m[i];
             }
-            tc::named_sync(kBarSoft, Sh::kSoft);
+            if (!tc::named_sync_and(kBarSoft, Sh::kSoft, !spoilt) && !E4M3)
+                mark_nonfinite<R>(a.ch, sw.n, clear, sw.t0 * kTile, min(sw.len, sw.t1 * kTile), s_j, tmO + lane_tm, 32 * warp + lane);
             const bool whole = sw.whole();
             const long long row_at = static_cast<long long>(sw.n) * a.rows + row0;
             const size_t part = (static_cast<size_t>(run) * a.RT + rt) * 2 + (sw.first ? 0 : 1);
@@ -633,7 +594,6 @@ kda_latent_decode_kernel(const __grid_constant__ LatMaps maps, const LatArgs a)
                 s_f[tid] = sum == 0.f ? 0.f : 1.f / sum;
             }
             tc::named_sync(kBarSoft, Sh::kSoft);
-            uint32_t bad[2] = {0u, 0u};                          // rows with a result that is no number
             const int ch = 32 * warp + lane;
             if (!whole) {
                 float* d32 = a.part_o + part * R * kLatDim + ch;
@@ -658,43 +618,16 @@ kda_latent_decode_kernel(const __grid_constant__ LatMaps maps, const LatArgs a)
                     float o[16];
                     load_o<R, Sh::kSide>(tmO + (c & 3) * Sh::kO + c0 + lane_tm, o);
                     uint16_t* d = d16 + c0 * kLatDim + (c & 3) * 128;
-                    float check = 0.f;
 #pragma unroll
                     for (int i = 0; i < 16; i += 2) {
                         const float2 f = *reinterpret_cast<const float2*>(s_f + c0 + i);
-                        const float v0 = o[i] * f.x, v1 = o[i + 1] * f.y;
-                        if (a.K > 1) {
-                            check = fmaf(v0, 0.f, check);        // NaN once a value is none or infinite
-                            check = fmaf(v1, 0.f, check);
-                        }
-                        const uint32_t w = f32x2_to_bf16x2_bits(v0, v1);
+                        const uint32_t w = f32x2_to_bf16x2_bits(o[i] * f.x, o[i + 1] * f.y);
                         const uint32_t got = __shfl_xor_sync(0xffffffffu, w, 1);
                         if (c0 + i + odd < nrows) *reinterpret_cast<uint32_t*>(d + i * kLatDim) = __byte_perm(w, got, sel);
-                    }
-                    if (!(check == 0.f)) {                       // some row of these: which
-                        uint32_t rows = 0u;
-#pragma unroll
-                        for (int i = 0; i < 16; ++i) rows |= fabsf(o[i] * s_f[c0 + i]) < INFINITY ? 0u : 1u << i;
-                        bad[c0 >> 5] |= rows << (c0 & 31);
                     }
                 }
             }
             tc::fence_before_sync();                             // the next segment's product overwrites O
-            if (whole && a.K > 1) {
-#pragma unroll
-                for (int h = 0; h < 2; ++h) {
-                    bad[h] = __reduce_or_sync(0xffffffffu, bad[h]);
-                    if (lane == 0) reinterpret_cast<uint32_t*>(s_red)[warp * 2 + h] = bad[h];
-                }
-                tc::named_sync(kBarSoft, Sh::kSoft);
-                for (int r = warp; r < nrows; r += 4) {
-                    const uint32_t* f = reinterpret_cast<const uint32_t*>(s_red) + (r >> 5);
-                    const int j = (row0 + r) / a.H;
-                    if (((f[0] | f[2] | f[4] | f[6]) >> (r & 31) & 1u) && j < a.K - 1)
-                        latent_row_again<E4M3>(a, sw.n, row0 + r, sw.len - (a.K - 1 - j));
-                }
-                tc::named_sync(kBarSoft, Sh::kSoft);
-            }
             sw.first = false;
         }
     } else if (warp == Sh::kMmaWarp) {
@@ -866,7 +799,7 @@ kda_latent_decode_kernel(const __grid_constant__ LatMaps maps, const LatArgs a)
 // loads in flight; then the groups are joined.
 constexpr int kMaxRuns = 1024;                  // partials of a row (at most one a run)
 
-template <int R, bool E4M3>
+template <int R>
 __global__ void __launch_bounds__(512)
 kda_latent_combine_kernel(const LatArgs a, int Q, int NG)
 {
@@ -947,7 +880,6 @@ kda_latent_combine_kernel(const LatArgs a, int Q, int NG)
         }
         join(v, x);
     }
-    int bad = 0;
     if (NG > 1) {
         s_acc[tid] = acc;
         if (tid % lanes == 0) s_ml[grp] = make_float2(M, L);
@@ -960,22 +892,16 @@ kda_latent_combine_kernel(const LatArgs a, int Q, int NG)
             join(v, x);
         }
         const float inv = L == 0.f ? 0.f : 1.f / L;
-        const float v[4] = {acc.x * inv, acc.y * inv, acc.z * inv, acc.w * inv};
-        bad = !(fabsf(v[0]) < INFINITY && fabsf(v[1]) < INFINITY && fabsf(v[2]) < INFINITY && fabsf(v[3]) < INFINITY);
-        *reinterpret_cast<uint2*>(a.out + at * kLatDim + ch) = make_uint2(f32x2_to_bf16x2_bits(v[0], v[1]),
-                                                                          f32x2_to_bf16x2_bits(v[2], v[3]));
+        *reinterpret_cast<uint2*>(a.out + at * kLatDim + ch) = make_uint2(f32x2_to_bf16x2_bits(acc.x * inv, acc.y * inv),
+                                                                          f32x2_to_bf16x2_bits(acc.z * inv, acc.w * inv));
         if (ch == 0 && a.lse) a.lse[at] = (M + log2f(L)) * 0.69314718055994531f;
-    }
-    const int j = row / a.H;
-    if (j < a.K - 1) {
-        bad = __syncthreads_or(bad);
-        if (bad && tid < 32) latent_row_again<E4M3>(a, n, row, len - (a.K - 1 - j), Q == 1 ? -1 : static_cast<int>(blockIdx.x % Q));
     }
 }
 
 // The same for many rows of few partials: a warp a row, 16 channels a lane, no block-wide step.
-template <int R, bool E4M3>
-__global__ void __launch_bounds__(128)
+// (Four blocks an SM are enough: for more, the compiler spills into 48 registers.)
+template <int R>
+__global__ void __launch_bounds__(128, 4)
 kda_latent_combine_rows_kernel(const LatArgs a)
 {
     const int lane = threadIdx.x & 31;
@@ -1053,16 +979,11 @@ kda_latent_combine_rows_kernel(const LatArgs a)
         }
     }
     const float inv = L == 0.f ? 0.f : 1.f / L;
-    bool bad = false;
 #pragma unroll
-    for (int k = 0; k < 4; ++k) {
-        const float v0 = acc[k].x * inv, v1 = acc[k].y * inv, v2 = acc[k].z * inv, v3 = acc[k].w * inv;
-        bad = bad || !(fabsf(v0) < INFINITY && fabsf(v1) < INFINITY && fabsf(v2) < INFINITY && fabsf(v3) < INFINITY);
-        out[32 * k] = make_uint2(f32x2_to_bf16x2_bits(v0, v1), f32x2_to_bf16x2_bits(v2, v3));
-    }
+    for (int k = 0; k < 4; ++k)
+        out[32 * k] = make_uint2(f32x2_to_bf16x2_bits(acc[k].x * inv, acc[k].y * inv),
+                                 f32x2_to_bf16x2_bits(acc[k].z * inv, acc[k].w * inv));
     if (lane == 0 && a.lse) a.lse[at] = (M + log2f(L)) * 0.69314718055994531f;
-    const int j = row / a.H;
-    if (j < a.K - 1 && __any_sync(0xffffffffu, bad)) latent_row_again<E4M3>(a, n, row, len - (a.K - 1 - j));
 }
 
 namespace {
@@ -1139,8 +1060,8 @@ int launch_decode_shape(const LatMaps& maps, const LatArgs& a, cudaStream_t stre
     at[0].val.programmaticStreamSerializationAllowed = 1;
     cfg.attrs = at;
     cfg.numAttrs = 1;
-    if (by_warp) return cudaLaunchKernelEx(&cfg, kda_latent_combine_rows_kernel<R, E4M3>, a) == cudaSuccess ? 0 : -3;
-    return cudaLaunchKernelEx(&cfg, kda_latent_combine_kernel<R, E4M3>, a, Q, NG) == cudaSuccess ? 0 : -3;
+    if (by_warp) return cudaLaunchKernelEx(&cfg, kda_latent_combine_rows_kernel<R>, a) == cudaSuccess ? 0 : -3;
+    return cudaLaunchKernelEx(&cfg, kda_latent_combine_kernel<R>, a, Q, NG) == cudaSuccess ? 0 : -3;
 }
 
 // Rows a CTA takes: 16, 32 or 64.
