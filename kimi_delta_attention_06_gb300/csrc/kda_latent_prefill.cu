@@ -27,50 +27,6 @@ namespace kda {
 
 constexpr int kExpK = 128, kExpV = 128, kExpQ = kExpK + kLatRope;
 
-struct ExpKv {
-    const uint16_t *k, *v, *r;
-    long long ldk, hdk, ldv, hdv, ldr;
-};
-
-// One warp computes one row in fp32, straight from the formula, over keys [k0, k0 + see).  Lane i
-// owns key and value channels 4 i .. 4 i + 3 and position values 2 i, 2 i + 1.
-__device__ __noinline__ void expanded_row(const uint16_t* __restrict__ q, const ExpKv& kv, int h, long long k0, int see,
-                             float scale_log2, uint16_t* __restrict__ out, float* __restrict__ lse)
-{
-    const int lane = threadIdx.x & 31;
-    const uint2 qw = reinterpret_cast<const uint2*>(q)[lane];
-    const float2 q0 = bf16x2_bits_to_f32(qw.x), q1 = bf16x2_bits_to_f32(qw.y);
-    const float2 qr = bf16x2_bits_to_f32(reinterpret_cast<const uint32_t*>(q + kExpK)[lane]);
-    float acc[4] = {0.f, 0.f, 0.f, 0.f}, m = -INFINITY, l = 0.f;
-    for (int t = 0; t < see; ++t) {
-        const long long at = k0 + t;
-        const uint2 kw = reinterpret_cast<const uint2*>(kv.k + at * kv.ldk + h * kv.hdk)[lane];
-        const float2 a = bf16x2_bits_to_f32(kw.x), b = bf16x2_bits_to_f32(kw.y);
-        const float2 r = bf16x2_bits_to_f32(reinterpret_cast<const uint32_t*>(kv.r + at * kv.ldr)[lane]);
-        float x = q0.x * a.x + q0.y * a.y + q1.x * b.x + q1.y * b.y + qr.x * r.x + qr.y * r.y;
-#pragma unroll
-        for (int off = 16; off > 0; off >>= 1) x += __shfl_xor_sync(0xffffffffu, x, off);
-        x *= scale_log2;
-        if (x > m) {
-            const float f = lat_ex2(m - x);
-            m = x;
-            l *= f;
-#pragma unroll
-            for (int i = 0; i < 4; ++i) acc[i] *= f;
-        }
-        const float p = x == -INFINITY ? 0.f : lat_ex2(x - m);
-        l += p;
-        const uint2 vw = reinterpret_cast<const uint2*>(kv.v + at * kv.ldv + h * kv.hdv)[lane];
-        const float2 c = bf16x2_bits_to_f32(vw.x), d = bf16x2_bits_to_f32(vw.y);
-        acc[0] += p * c.x; acc[1] += p * c.y; acc[2] += p * d.x; acc[3] += p * d.y;
-    }
-    const float inv = l == 0.f ? 0.f : 1.f / l;      // (a NaN sum stays NaN)
-    reinterpret_cast<uint2*>(out)[lane] = make_uint2(f32x2_to_bf16x2_bits(acc[0] * inv, acc[1] * inv),
-                                                     f32x2_to_bf16x2_bits(acc[2] * inv, acc[3] * inv));
-    if (lse && lane == 0) *lse = (m + log2f(l)) * 0.69314718055994531f;     // l = 0: -inf
-}
-
-
 // Rows that see nothing (no keys at all): zeros and -inf.
 __global__ void __launch_bounds__(256)
 kda_expanded_empty_kernel(long long rows, uint16_t* __restrict__ out, float* __restrict__ lse)
@@ -84,8 +40,9 @@ kda_expanded_empty_kernel(long long rows, uint16_t* __restrict__ out, float* __r
 struct ExpMaps { CUtensorMap q, k, v, r; };      // 64-channel x 128-row boxes, 128-byte swizzle
 
 struct ExpArgs {
-    const uint16_t* q;
-    ExpKv kv;
+    const uint16_t* v;                           // values, as for the maps
+    long long ldv, hdv;
+    int total_k;
     const int32_t *cu_q, *cu_k;
     int num_seqs, H, causal, hg;                 // hg: heads that go side by side
     float scale_log2;
@@ -105,8 +62,10 @@ constexpr uint32_t kSlab = kExpTile * 128u;      // 64 channels x 128 rows of bf
 constexpr uint32_t kRing = 8;
 constexpr int kExpCopyWarp = 9;
 constexpr int kExpThreads = 320;                 // warps 0-3, 4-7: softmax of tile 0, 1; 8: products; 9: copies
-constexpr uint32_t oExpQ = 0, oExpRing = 6 * kSlab, oExpBar = oExpRing + kRing * kSlab;
-constexpr uint32_t kExpSmem = oExpBar + 32 * 8 + 16;
+constexpr uint32_t kExpBars = 20;                // barriers of a pass
+constexpr uint32_t oExpQ = 0, oExpRing = 6 * kSlab, oExpBar = oExpRing + kRing * kSlab, oExpFirst = oExpBar + 2 * kExpBars * 8 + 16;
+constexpr uint32_t kExpSmem = oExpFirst + 3 * kExpV * 4 + 16;
+static_assert(kExpSmem <= 232448, "227 KB of shared memory");
 // Key tiles that query rows [r0, r0 + 128) of a sequence see.
 __device__ __forceinline__ int exp_tiles(int r0, int Lq, int Lk, int causal) {
     const int r1 = min(r0 + kExpTile, Lq) - 1;
@@ -115,105 +74,136 @@ __device__ __forceinline__ int exp_tiles(int r0, int Lq, int Lk, int causal) {
 }
 constexpr float kExpTau = 8.f;                   // scores may exceed the running maximum by 2^8 before a rescale
 
-template <bool SPLIT>
-__global__ void __launch_bounds__(kExpThreads, 1)
-kda_expanded_kernel(const __grid_constant__ ExpMaps maps, const ExpArgs a)
-{
-    extern __shared__ __align__(1024) uint8_t smem[];
-    uint64_t* bars = reinterpret_cast<uint64_t*>(smem + oExpBar);
-    uint64_t *full = bars, *kfree = bars + 8, *vfree = bars + 10, *s_full = bars + 12, *p_full = bars + 14, *q_full = bars + 18;
-    uint32_t* s_tmem = reinterpret_cast<uint32_t*>(bars + 20);
+// A row has zeros in P for the keys that it does not see, but 0 * NaN is none: in a tile of keys that some rows see and
+// others do not (the diagonal, and a sequence's last tile, which the next one's keys share), a value that is NaN or
+// infinite spoils the rows that do not see it.  So such values leave these tiles before the product; for each channel the
+// first key with a NaN, an infinity and a negative infinity is kept, and the rows that see past it get it into their
+// results (CAREFUL below).  Looking the tiles over costs the kernel with split keys nothing (2048 queries x 8 heads over 18432
+// keys 127 us, as without); the one with whole keys, whose softmax loop is out of registers, 4 to 10 % (8192 tokens x 32
+// heads 389 -> 412 us, behind a call; by two warps more, as the values come too late for them, 430).  That one looks where a
+// row's results are no numbers beside a sum of weights that is one, and where there are such values in those tiles, the CTA
+// takes its rows a second time.  (A row computed again by a warp over its keys, as was done at first, took 0.3 us a key.)
+__device__ __noinline__ void drop_nonfinite(uint4* p, uint4 v, int key, int* first, volatile int* any) {
+    uint32_t w[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+        const uint32_t at = 16 * (i & 1), bits = w[i >> 1] >> at & 0xffffu;
+        if ((bits & 0x7f80u) != 0x7f80u) continue;
+        atomicMin(first + (bits & 0x7fu ? 0 : bits >> 15 ? 2 * kExpV : kExpV) + i, key);
+        w[i >> 1] &= ~(0xffffu << at);
+    }
+    *any = 1;
+    __threadfence_block();                       // the other query tile's threads see the marks once they see the zeros
+    *p = make_uint4(w[0], w[1], w[2], w[3]);
+}
+__device__ __forceinline__ bool any_nonfinite(uint4 v) {         // of eight bf16 values
+    const uint32_t top = __vmaxu2(__vmaxu2(v.x & 0x7fff7fffu, v.y & 0x7fff7fffu),
+                                  __vmaxu2(v.z & 0x7fff7fffu, v.w & 0x7fff7fffu));
+    return top >= 0x7f800000u || (top & 0xffffu) >= 0x7f80u;
+}
+// Keys [from, 128) of a tile of values in slabs lo (channels 0 .. 63) and hi, by the 128 threads of a query tile.
+__device__ __noinline__ void clean_tile(uint8_t* lo, uint8_t* hi, int from, int key0, int* first) {
+    volatile int* any = first + 3 * kExpV;
+    bool found = false;
+    for (int x = threadIdx.x & 127; x < (kExpTile - from) * 16; x += kExpTile) {
+        const int r = from + (x >> 4), c = x & 7;                // 16 bytes: 8 channels of a key
+        uint4* p = reinterpret_cast<uint4*>((x & 8 ? hi : lo) + r * 128 + c * 16);
+        const uint4 v = *p;
+        if (any_nonfinite(v)) {
+            drop_nonfinite(p, v, key0 + r, first + (x & 8) * 8 + ((c ^ (r & 7)) << 3), any);
+            found = true;
+        }
+    }
+    if (found || *any) tc::fence_smem_to_async();
+}
+// What the keys that a thread's row sees put into its results (O in TMEM): NaN, infinities or nothing.
+__device__ __noinline__ void put_back(uint32_t tO, const int* first, int see) {
+#pragma unroll 1
+    for (int c = 0; c < kExpV; c += 16) {
+        float o[16];
+        tc::tmem_ld16(tO + c, o);
+        tc::tmem_wait_ld();
+#pragma unroll
+        for (int i = 0; i < 16; ++i) {
+            const int* f = first + c + i;
+            const bool none = see > f[0], pos = see > f[kExpV], neg = see > f[2 * kExpV];
+            o[i] += none || (pos && neg) ? __int_as_float(0x7fffffff) : pos ? INFINITY : neg ? -INFINITY : 0.f;
+        }
+        tc::tmem_st16(tO + c, o);
+    }
+    tc::tmem_wait_st();
+}
 
-    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-    const int h = blockIdx.y * a.hg + blockIdx.x % a.hg;
-    if (h >= a.H) return;                                        // (the last group's)
-    // the unit (sequence n, 256 rows from q0): the last rows of a sequence, the longest, come first
-    int n = 0, q0 = 0, cq = 0, Lq = 0;
-    {
-        int base = 0;
-        const int want = static_cast<int>(blockIdx.x / a.hg);
-        for (int i0 = 0; i0 < a.num_seqs; i0 += 32) {
-            const int i = i0 + lane;
-            const int c = i < a.num_seqs ? a.cu_q[i] : 0, len = i < a.num_seqs ? a.cu_q[i + 1] - c : 0;
-            const int units = (len + kExpRows - 1) / kExpRows;
-            int incl = units;
-#pragma unroll
-            for (int off = 1; off < 32; off <<= 1) {
-                const int o = __shfl_up_sync(0xffffffffu, incl, off);
-                if (lane >= off) incl += o;
-            }
-            const unsigned hit = __ballot_sync(0xffffffffu, base + incl > want);
-            if (hit) {
-                const int at = __ffs(hit) - 1;
-                n = i0 + at;
-                cq = __shfl_sync(0xffffffffu, c, at);
-                Lq = __shfl_sync(0xffffffffu, len, at);
-                q0 = (base + __shfl_sync(0xffffffffu, incl, at) - 1 - want) * kExpRows;
-                break;
-            }
-            base += __shfl_sync(0xffffffffu, incl, 31);
-        }
-    }
-    const int ck = a.cu_k[n], Lk = a.cu_k[n + 1] - ck;
-    // keys that row i sees: i + more (causal), else all; key tiles of query tile w: nt[w]
-    const int more = a.causal ? 1 + Lk - Lq : Lk;
+__device__ __forceinline__ void clear_marks(uint8_t* smem) {     // [3][channels] and a flag, by the whole CTA
+    int* first = reinterpret_cast<int*>(smem + oExpFirst);
+    for (int i = threadIdx.x; i < 3 * kExpV + 1; i += kExpThreads) first[i] = i < 3 * kExpV ? 0x7fffffff : 0;
+}
+
+// What a CTA works on: rows [q0, q0 + 256) of head h of a sequence (its queries from cq on, its keys from ck on) over the
+// key tiles from j0 on, nt[w] for query tile w; cut[w]: tile w has more parts than this one.
+struct ExpUnit {
+    int h, cq, q0, Lq, Lk, ck, more, part, j0, nmax;
     int nt[2];
-#pragma unroll
-    for (int w = 0; w < 2; ++w) nt[w] = exp_tiles(q0 + w * kExpTile, Lq, Lk, a.causal);
-    const int part = SPLIT ? static_cast<int>(blockIdx.z) : 0, j0 = SPLIT ? part * a.span : 0;
-    bool cut[2] = {false, false};                                // tile w has more parts than one
-    if constexpr (SPLIT) {
-        asm volatile("griddepcontrol.launch_dependents;" ::: "memory");   // the joining kernel waits for this grid's end
-#pragma unroll
-        for (int w = 0; w < 2; ++w) {
-            cut[w] = nt[w] > a.span;
-            nt[w] = max(0, min(nt[w] - j0, a.span));
-        }
-    }
-    const int nmax = max(nt[0], nt[1]);
-    if (SPLIT && part > 0 && nmax == 0) return;                  // no such part
-    const uint32_t ring = tc::smem_u32(smem + oExpRing), sq = tc::smem_u32(smem + oExpQ);
-    auto copy_q = [&](int w) {
-        if (nt[w] == 0) return;
+    bool cut[2];
+};
+
+// The barriers of a pass and its copies (by one thread).
+struct ExpCopies {
+    const ExpMaps& maps;
+    const ExpUnit& u;
+    uint64_t *full, *q_full;
+    uint32_t ring, sq;
+    __device__ __forceinline__ ExpCopies(const ExpMaps& m, const ExpUnit& unit, uint8_t* smem, uint64_t* bars)
+        : maps(m), u(unit), full(bars), q_full(bars + 18), ring(tc::smem_u32(smem + oExpRing)), sq(tc::smem_u32(smem + oExpQ)) {}
+    __device__ __forceinline__ void q(int w) const {
+        if (u.nt[w] == 0) return;
         tc::mbar_arrive_expect_tx(&q_full[w], 3u * kSlab);
         for (int s = 0; s < 3; ++s)
-            tc::tma_load_3d(sq + (w * 3u + s) * kSlab, &maps.q, 64 * s, h, cq + q0 + w * kExpTile, &q_full[w]);
-    };
-    auto copy_kv = [&](uint32_t i, int j, int s) {               // slab s of key tile j, the i-th of all, to slot i % 8
+            tc::tma_load_3d(sq + (w * 3u + s) * kSlab, &maps.q, 64 * s, u.h, u.cq + u.q0 + w * kExpTile, &q_full[w]);
+    }
+    __device__ __forceinline__ void kv(uint32_t i, int j, int s) const {   // slab s of key tile j, the i-th of all, to slot i % 8
         const uint32_t slot = i & (kRing - 1), dst = ring + slot * kSlab;
-        const int key = ck + (j0 + j) * kExpTile;
+        const int key = u.ck + (u.j0 + j) * kExpTile;
         tc::mbar_arrive_expect_tx(&full[slot], kSlab);
-        if (s < 2) tc::tma_load_3d(dst, &maps.k, 64 * s, h, key, &full[slot]);
+        if (s < 2) tc::tma_load_3d(dst, &maps.k, 64 * s, u.h, key, &full[slot]);
         else if (s == 2) tc::tma_load_2d(dst, &maps.r, 0, key, &full[slot]);
-        else tc::tma_load_3d(dst, &maps.v, 64 * (s - 3), h, key, &full[slot]);
-    };
-
-    if (tid == 32 * kExpCopyWarp) {
+        else tc::tma_load_3d(dst, &maps.v, 64 * (s - 3), u.h, key, &full[slot]);
+    }
+    __device__ __forceinline__ void start() const {
+        uint64_t* bars = full;
         for (uint32_t i = 0; i < kRing; ++i) tc::mbar_init(&full[i], 1);
         for (int i = 0; i < 2; ++i) {
-            tc::mbar_init(&kfree[i], 1);
-            tc::mbar_init(&vfree[i], 1);
-            tc::mbar_init(&s_full[i], 1);
-            tc::mbar_init(&p_full[2 * i], kExpTile);
-            tc::mbar_init(&p_full[2 * i + 1], kExpTile);
+            tc::mbar_init(&bars[8 + i], 1);                      // kfree, vfree, s_full
+            tc::mbar_init(&bars[10 + i], 1);
+            tc::mbar_init(&bars[12 + i], 1);
+            tc::mbar_init(&bars[14 + 2 * i], kExpTile);          // p_full
+            tc::mbar_init(&bars[15 + 2 * i], kExpTile);
             tc::mbar_init(&q_full[i], 1);
         }
         tc::mbar_fence_init();
         // the first copies go out before the CTA meets, in the order in which they are used
-        if (nmax > 0) {
-            copy_q(0);
-            for (int s = 0; s < 3; ++s) copy_kv(s, 0, s);
-            copy_q(1);
-            for (int s = 3; s < 5; ++s) copy_kv(s, 0, s);
+        if (u.nmax > 0) {
+            q(0);
+            for (int s = 0; s < 3; ++s) kv(s, 0, s);
+            q(1);
+            for (int s = 3; s < 5; ++s) kv(s, 0, s);
         }
     }
-    __syncwarp();
-    if (warp == 8) tc::tmem_alloc(s_tmem, 512);
-    tc::fence_before_sync();
-    __syncthreads();
-    tc::fence_after_sync();
-    const uint32_t tm = *s_tmem;
-    bool ok = true;
+};
+
+// One pass over the unit by all warps.  `bad`: a row of this thread has results that are no numbers beside a sum that is one.
+// CAREFUL: see drop_nonfinite.
+template <bool SPLIT, bool CAREFUL>
+__device__ __forceinline__ void run_unit(const ExpMaps& maps, const ExpArgs& a, const ExpUnit& u, uint8_t* smem, uint64_t* bars,
+                                         uint32_t tm, bool& ok, bool& bad)
+{
+    uint64_t *full = bars, *kfree = bars + 8, *vfree = bars + 10, *s_full = bars + 12, *p_full = bars + 14, *q_full = bars + 18;
+    int* s_first = reinterpret_cast<int*>(smem + oExpFirst);     // [3][channels], then a flag
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    const int h = u.h, cq = u.cq, q0 = u.q0, Lq = u.Lq, Lk = u.Lk, more = u.more, part = u.part, j0 = u.j0, nmax = u.nmax;
+    const int nt[2] = {u.nt[0], u.nt[1]};
+    const bool cut[2] = {u.cut[0], u.cut[1]};
+    const ExpCopies copies(maps, u, smem, bars);
 
     if (warp < 8) {
         // ---- softmax: one row a thread ----
@@ -221,8 +211,17 @@ kda_expanded_kernel(const __grid_constant__ ExpMaps maps, const ExpArgs a)
         const uint32_t lane_tm = static_cast<uint32_t>((warp & 3) * 32) << 16;
         const uint32_t tS = tm + w * 128u + lane_tm, tO = tm + 256u + w * 128u + lane_tm;
         const int see = (a.causal ? row + more : Lk) - j0 * kExpTile;
+        const int all = (a.causal ? q0 + w * kExpTile + more : Lk) - j0 * kExpTile;   // keys that every row sees
         float m = -INFINITY, l = 0.f;
         for (int j = 0; j < nt[w]; ++j) {
+            if (CAREFUL && all < (j + 1) * kExpTile) {
+                const uint32_t i = 5u * j + 3u, s0 = i & (kRing - 1), s1 = (i + 1u) & (kRing - 1);
+                ok = __all_sync(0xffffffffu, tc::mbar_wait_bounded(&full[s0], (i / kRing) & 1, kWaitLimitNs) &&
+                                                 tc::mbar_wait_bounded(&full[s1], ((i + 1u) / kRing) & 1, kWaitLimitNs));
+                if (!ok) break;
+                clean_tile(smem + oExpRing + s0 * kSlab, smem + oExpRing + s1 * kSlab, max(all - j * kExpTile, 0),
+                           (j0 + j) * kExpTile, s_first);
+            }
             ok = __all_sync(0xffffffffu, tc::mbar_wait_bounded(&s_full[w], j & 1, kWaitLimitNs));
             if (!ok) break;
             tc::fence_after_sync();
@@ -300,6 +299,8 @@ kda_expanded_kernel(const __grid_constant__ ExpMaps maps, const ExpArgs a)
             ok = __all_sync(0xffffffffu, tc::mbar_wait_bounded(&s_full[w], nt[w] & 1, kWaitLimitNs));
             tc::fence_after_sync();
         }
+        if (CAREFUL && ok && nt[w] > 0 && *const_cast<volatile int*>(s_first + 3 * kExpV)) put_back(tO, s_first, see + j0 * kExpTile);
+        float check = 0.f;                                       // NaN once a result is none or infinite
         if (SPLIT && cut[w]) {                                   // a part of the keys: to the joining kernel
             if (ok && nt[w] > 0) {
                 const size_t ph = static_cast<size_t>(part) * a.H + h;
@@ -323,7 +324,6 @@ kda_expanded_kernel(const __grid_constant__ ExpMaps maps, const ExpArgs a)
             const long long at = (static_cast<long long>(cq) + row) * a.H + h;
             const bool some = nt[w] > 0 && l != 0.f;            // (else the row sees nothing: zeros)
             const float inv = 1.f / l;
-            float check = 0.f;                                   // NaN once a value is none or infinite
 #pragma unroll 1
             for (int c = 0; c < 4; ++c) {
                 uint32_t o[32];
@@ -342,19 +342,10 @@ kda_expanded_kernel(const __grid_constant__ ExpMaps maps, const ExpArgs a)
                     for (int i = 0; i < 4; ++i) d[i] = make_uint4(pk[4 * i], pk[4 * i + 1], pk[4 * i + 2], pk[4 * i + 3]);
                 }
             }
-            const bool bad = some && !(check == 0.f);
             if (mine && a.lse) a.lse[at] = (m + log2f(l)) * 0.69314718055994531f;     // nothing seen: -inf
-            // a NaN or infinity in a key or value that other rows of the tile see spoils this row's sum
-            // (0 * NaN): such a row is computed again over exactly its own keys
-            unsigned again = __ballot_sync(0xffffffffu, mine && bad);
-            while (again) {
-                const int r = row - lane + __ffs(again) - 1;
-                again &= again - 1;
-                const long long ra = (static_cast<long long>(cq) + r) * a.H + h;
-                expanded_row(a.q + ra * kExpQ, a.kv, h, ck, a.causal ? r + more : Lk, a.scale_log2, a.out + ra * kExpV,
-                             a.lse ? a.lse + ra : nullptr);
-            }
         }
+        // (where the sum is none the row saw a NaN itself, in a key or in q)
+        bad = !CAREFUL && row < Lq && l > 0.f && !(check == 0.f);
     } else if (warp == 8) {
         // ---- products, in the order PV 0, QK 0, PV 1, QK 1 of consecutive key tiles ----
         constexpr uint32_t id_s = tc::idesc(128, 128, tc::kFmtBF16, false, false);
@@ -440,7 +431,7 @@ kda_expanded_kernel(const __grid_constant__ ExpMaps maps, const ExpArgs a)
                     if (s == 1 && j >= 2) ok = tc::mbar_wait_bounded(&vfree[j & 1], ((j - 2) >> 1) & 1, kWaitLimitNs);
                     if (s == 3) ok = tc::mbar_wait_bounded(&kfree[(j - 1) & 1], ((j - 1) >> 1) & 1, kWaitLimitNs);
                     if (!ok) break;
-                    copy_kv(i++, j, s);
+                    copies.kv(i++, j, s);
                 }
             }
             if (!ok) {                                           // copies in flight land before the CTA ends
@@ -452,11 +443,106 @@ kda_expanded_kernel(const __grid_constant__ ExpMaps maps, const ExpArgs a)
         }
         __syncwarp();
     }
+}
+
+// A second pass of a CTA that had its rows' keys whole: its own barriers.
+__device__ __noinline__ void run_unit_again(const ExpMaps& maps, const ExpArgs& a, const ExpUnit& u, uint8_t* smem, uint32_t tm) {
+    uint64_t* bars = reinterpret_cast<uint64_t*>(smem + oExpBar) + kExpBars;
+    // values that are NaN or infinite among the keys from the first that some row does not see to the end of the last tile
+    // (what lies past all keys is copied as zeros)
+    const int all = max(a.causal ? u.q0 + u.more : u.Lk, 0), end = min(u.nmax * kExpTile, a.total_k - u.ck);
+    const uint16_t* v = a.v + static_cast<long long>(u.ck) * a.ldv + u.h * a.hdv;
+    bool found = false;
+    for (long long x = all * 16LL + threadIdx.x; x < end * 16LL; x += kExpThreads)
+        found = found || any_nonfinite(*reinterpret_cast<const uint4*>(v + (x >> 4) * a.ldv + (x & 15) * 8));
+    if (!__syncthreads_or(found)) return;
+    clear_marks(smem);
+    if (threadIdx.x == 32 * kExpCopyWarp) ExpCopies(maps, u, smem, bars).start();
+    __syncthreads();
+    tc::fence_after_sync();
+    bool ok = true, bad;
+    run_unit<false, true>(maps, a, u, smem, bars, tm, ok, bad);
     if (!ok) set_status(a.status, kStatusTimeout);
     __syncwarp();
     tc::fence_before_sync();
     __syncthreads();
     tc::fence_after_sync();
+}
+
+template <bool SPLIT>
+__global__ void __launch_bounds__(kExpThreads, 1)
+kda_expanded_kernel(const __grid_constant__ ExpMaps maps, const __grid_constant__ ExpArgs a)
+{
+    extern __shared__ __align__(1024) uint8_t smem[];
+    uint64_t* bars = reinterpret_cast<uint64_t*>(smem + oExpBar);
+    uint32_t* s_tmem = reinterpret_cast<uint32_t*>(bars + 2 * kExpBars);
+
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    const int h = blockIdx.y * a.hg + blockIdx.x % a.hg;
+    if (h >= a.H) return;                                        // (the last group's)
+    // the unit (sequence n, 256 rows from q0): the last rows of a sequence, the longest, come first
+    int n = 0, q0 = 0, cq = 0, Lq = 0;
+    {
+        int base = 0;
+        const int want = static_cast<int>(blockIdx.x / a.hg);
+        for (int i0 = 0; i0 < a.num_seqs; i0 += 32) {
+            const int i = i0 + lane;
+            const int c = i < a.num_seqs ? a.cu_q[i] : 0, len = i < a.num_seqs ? a.cu_q[i + 1] - c : 0;
+            const int units = (len + kExpRows - 1) / kExpRows;
+            int incl = units;
+#pragma unroll
+            for (int off = 1; off < 32; off <<= 1) {
+                const int o = __shfl_up_sync(0xffffffffu, incl, off);
+                if (lane >= off) incl += o;
+            }
+            const unsigned hit = __ballot_sync(0xffffffffu, base + incl > want);
+            if (hit) {
+                const int at = __ffs(hit) - 1;
+                n = i0 + at;
+                cq = __shfl_sync(0xffffffffu, c, at);
+                Lq = __shfl_sync(0xffffffffu, len, at);
+                q0 = (base + __shfl_sync(0xffffffffu, incl, at) - 1 - want) * kExpRows;
+                break;
+            }
+            base += __shfl_sync(0xffffffffu, incl, 31);
+        }
+    }
+    const int ck = a.cu_k[n], Lk = a.cu_k[n + 1] - ck;
+    // keys that row i sees: i + more (causal), else all; key tiles of query tile w: nt[w]
+    const int more = a.causal ? 1 + Lk - Lq : Lk;
+    int nt[2];
+#pragma unroll
+    for (int w = 0; w < 2; ++w) nt[w] = exp_tiles(q0 + w * kExpTile, Lq, Lk, a.causal);
+    const int part = SPLIT ? static_cast<int>(blockIdx.z) : 0, j0 = SPLIT ? part * a.span : 0;
+    bool cut[2] = {false, false};                                // tile w has more parts than one
+    if constexpr (SPLIT) {
+        asm volatile("griddepcontrol.launch_dependents;" ::: "memory");   // the joining kernel waits for this grid's end
+#pragma unroll
+        for (int w = 0; w < 2; ++w) {
+            cut[w] = nt[w] > a.span;
+            nt[w] = max(0, min(nt[w] - j0, a.span));
+        }
+    }
+    const int nmax = max(nt[0], nt[1]);
+    if (SPLIT && part > 0 && nmax == 0) return;                  // no such part
+    const ExpUnit u{h, cq, q0, Lq, Lk, ck, more, part, j0, nmax, {nt[0], nt[1]}, {cut[0], cut[1]}};
+    if (tid == 32 * kExpCopyWarp) ExpCopies(maps, u, smem, bars).start();
+    if (SPLIT) clear_marks(smem);
+    __syncwarp();
+    if (warp == 8) tc::tmem_alloc(s_tmem, 512);
+    tc::fence_before_sync();
+    __syncthreads();
+    tc::fence_after_sync();
+    const uint32_t tm = *s_tmem;
+    bool ok = true, bad = false;
+
+    run_unit<SPLIT, SPLIT>(maps, a, u, smem, bars, tm, ok, bad);
+    if (!ok) set_status(a.status, kStatusTimeout);
+    __syncwarp();
+    tc::fence_before_sync();
+    const bool again = __syncthreads_or(bad);
+    tc::fence_after_sync();
+    if (!SPLIT && again && __syncthreads_and(ok)) run_unit_again(maps, a, u, smem, tm);
     if (warp == 8) tc::tmem_dealloc(tm, 512);
 }
 
@@ -466,10 +552,9 @@ template <int B>
 __global__ void __launch_bounds__(256)
 kda_expanded_join_kernel(const ExpArgs a)
 {
-    __shared__ unsigned s_bad;
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, h = blockIdx.y;
     const int row = blockIdx.x * 8 + (lane & 7), c4 = warp * 4 + (lane >> 3);     // query of all sequences, channels 4 c4 ..
-    int parts = 0, see = 0, ck = 0;
+    int parts = 0;
     if (row < a.total_q) {
         int lo = 0, hi = a.num_seqs;                             // cu_q[lo] <= row < cu_q[lo + 1]
         while (hi - lo > 1) {
@@ -477,13 +562,9 @@ kda_expanded_join_kernel(const ExpArgs a)
             if (a.cu_q[mid] <= row) lo = mid; else hi = mid;
         }
         const int cq = a.cu_q[lo], Lq = a.cu_q[lo + 1] - cq, Lk = a.cu_k[lo + 1] - a.cu_k[lo], in = row - cq;
-        ck = a.cu_k[lo];
-        see = a.causal ? in + 1 + Lk - Lq : Lk;
         const int nt = exp_tiles(in / kExpTile * kExpTile, Lq, Lk, a.causal);
         parts = nt > a.span ? min((nt + a.span - 1) / a.span, a.parts) : 0;
     }
-    if (threadIdx.x == 0) s_bad = 0u;
-    __syncthreads();
     asm volatile("griddepcontrol.wait;" ::: "memory");          // every block: this grid ends after the one before it
     const size_t step = static_cast<size_t>(a.H) * a.total_q;
     const float2* ml = a.part_ml + static_cast<size_t>(h) * a.total_q + row;
@@ -517,18 +598,9 @@ kda_expanded_join_kernel(const ExpArgs a)
     if (parts > 0) {
         const size_t at = static_cast<size_t>(row) * a.H + h;
         const float inv = L == 0.f ? 0.f : 1.f / L;
-        const float x0 = acc.x * inv, x1 = acc.y * inv, x2 = acc.z * inv, x3 = acc.w * inv;
-        *reinterpret_cast<uint2*>(a.out + at * kExpV + 4 * c4) = make_uint2(f32x2_to_bf16x2_bits(x0, x1), f32x2_to_bf16x2_bits(x2, x3));
+        *reinterpret_cast<uint2*>(a.out + at * kExpV + 4 * c4) = make_uint2(f32x2_to_bf16x2_bits(acc.x * inv, acc.y * inv),
+                                                                            f32x2_to_bf16x2_bits(acc.z * inv, acc.w * inv));
         if (c4 == 0 && a.lse) a.lse[at] = (M + log2f(L)) * 0.69314718055994531f;
-        if (!(fmaf(x3, 0.f, fmaf(x2, 0.f, fmaf(x1, 0.f, x0 * 0.f))) == 0.f)) atomicOr(&s_bad, 1u << (lane & 7));
-    }
-    __syncthreads();
-    // (a row that a key or value it does not see has spoilt: see above)
-    for (unsigned bad = s_bad; bad; bad &= bad - 1) {
-        const int r = __ffs(bad) - 1, see_r = __shfl_sync(0xffffffffu, see, r), ck_r = __shfl_sync(0xffffffffu, ck, r);
-        const size_t ra = static_cast<size_t>(blockIdx.x * 8 + r) * a.H + h;
-        if (r == warp)
-            expanded_row(a.q + ra * kExpQ, a.kv, h, ck_r, see_r, a.scale_log2, a.out + ra * kExpV, a.lse ? a.lse + ra : nullptr);
     }
 }
 
@@ -636,8 +708,10 @@ int launch_latent_prefill(const uint16_t* q, const uint16_t* k, long long ldk, l
         !map_tokens(&maps.r, r, total_k, 0, kLatRope, ldr, 0))
         return -3;
     ExpArgs a = {};
-    a.q = q;
-    a.kv = ExpKv{k, v, r, ldk, hdk, ldv, hdv, ldr};
+    a.v = v;
+    a.ldv = ldv;
+    a.hdv = hdv;
+    a.total_k = total_k;
     a.cu_q = cu_q;
     a.cu_k = cu_k;
     a.num_seqs = num_seqs;
