@@ -473,7 +473,8 @@ int kda_latent_gather(const void* cache, int cache_dtype, int num_pages, int pag
  * statistics and sums are fp32.  The probabilities enter the second product as bf16; over an
  * e4m3 cache, times the token's scale, as a sum of three e5m2 values (9 bits; weighted latents
  * below 2^-26 of the largest are rounded to that step, and results below 2^-80 may vanish), and the
- * query as a sum of two e4m3 values (8 bits).
+ * query as a sum of two e4m3 values (exact above 1/900 of its row's largest magnitude, to within
+ * 2^-17 of that magnitude below).
  * An e4m3 row whose scale is NaN or infinite makes the queries that see it NaN.
  * 1 <= K * H <= KDA_LATENT_MAX_ROWS, else KDA_ERR_UNSUPPORTED.  seq_lens[n] outside
  * [0, max_pages * page_size] counts as 0 and is reported; a page outside [0, num_pages) is

@@ -13,7 +13,7 @@
 //
 // An e4m3 cache enters both products as it is, without being expanded:
 //   - q / 2^k (2^k a row: the largest magnitude in (224, 448]) is the sum of two e4m3 values, exactly
-//     where |q| is above 1/1800 of the row's largest (8 bits of bf16 in 4 + 4), within 2^-19 of it
+//     where |q| is above 1/900 of the row's largest (8 bits of bf16 in 4 + 4), within 2^-17 of it
 //     below.  The position part is bf16 and has its own accumulator, as the scale s of a token
 //     belongs to its latent only: x = scale * (2^k s S_c + S_r).
 //   - s moves from the latents to the weights: O = sum (p s) codes.  p s is the sum of three e5m2
@@ -378,8 +378,9 @@ kda_latent_decode_kernel(const __grid_constant__ LatMaps maps, const LatArgs a)
                         uint32_t top = __reduce_max_sync(0xffffffffu, max(top2 & 0xffffu, top2 >> 16));
                         // (a row with a NaN or an infinity gets codes of NaN, as its scores are none)
                         const bool none = top >= 0x7f80u;
-                        const int e = none ? 0 : lat_scale_exponent(top << 16);
-                        const float inv = __uint_as_float(static_cast<uint32_t>(127 - 8 - e) << 23);
+                        const int e = none ? 0 : lat_scale_exponent(top << 16, 120);
+                        // 2^-(8 + e): a denormal from e = 119 on (products with it are exact, as with the others)
+                        const float inv = __uint_as_float(e < 119 ? static_cast<uint32_t>(119 - e) << 23 : 0x400000u >> (e - 119));
                         uint32_t t1[4], t2[4];
 #pragma unroll
                         for (int i = 0; i < 4; ++i) {

@@ -25,10 +25,11 @@ __device__ __forceinline__ float lat_ex2(float x) {
     return y;
 }
 
-// Smallest e with x <= 448 * 2^e = 1.75 * 2^(8 + e), in [-117, 119]; 0 for x = 0 (x >= 0 by its bits).
-__device__ __forceinline__ int lat_scale_exponent(uint32_t bits) {
+// Smallest e with x <= 448 * 2^e = 1.75 * 2^(8 + e), in [-117, most]; 0 for x = 0 (x >= 0 by its bits).  A cache
+// row's scale ends at 2^119; the largest finite x needs 120.
+__device__ __forceinline__ int lat_scale_exponent(uint32_t bits, int most = 119) {
     const int e = static_cast<int>(bits >> 23) - 127 - 8 + ((bits & 0x7fffffu) > 0x600000u ? 1 : 0);
-    return bits == 0 ? 0 : max(-117, min(119, e));
+    return bits == 0 ? 0 : max(-117, min(most, e));
 }
 
 // Two e4m3 codes (low byte first) -> two floats.
