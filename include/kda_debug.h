@@ -1,5 +1,5 @@
 /*
- * kda_debug.h -- test hook for the library's failure detection.
+ * kda_debug.h -- test hooks: the library's failure detection, and a launch rule.
  *
  * Every device-side wait in the KDA kernels is bounded: when a wait expires the
  * kernel records KDA_ERR_TIMEOUT in the device status word and returns early,
@@ -24,6 +24,12 @@ extern "C" {
  * failure.  The paper describes no counterpart; this exists for testing.
  */
 int kda_debug_expire_wait(unsigned long long limit_ns, void* stream);
+
+/*
+ * kda_debug_verify_cluster -- the CTAs that kda_verify_draft gives each of N sequences over a vocabulary of V, on a
+ * device of `sms` SMs that holds `clusters16` clusters of 16 such CTAs at once (0: it refuses them).  Touches no GPU.
+ */
+int kda_debug_verify_cluster(int N, int V, int sms, int clusters16);
 
 #ifdef __cplusplus
 }

@@ -64,6 +64,7 @@ size_t expanded_scratch(long long parts, int H, int total_q);
 int launch_verify(const float* tp, long long ldp, const float* dp, long long ldq, const int32_t* toks,
                   const int32_t* num_draft, const float* ua, const float* us, int N, int K, int V, int32_t* out,
                   int32_t* num_out, int* status, cudaStream_t stream);
+int verify_cluster(int N, int V, int sms, int clusters16);
 }  // namespace kda
 
 namespace {
@@ -921,6 +922,8 @@ int kda_verify_draft(const float* target_probs, int64_t ldp, const float* draft_
                             tokens, num_tokens, status, static_cast<cudaStream_t>(stream));
     return rc == 0 ? KDA_OK : KDA_ERR_CUDA;
 }
+
+int kda_debug_verify_cluster(int N, int V, int sms, int clusters16) { return kda::verify_cluster(N, V, sms, clusters16); }
 
 int kda_debug_expire_wait(unsigned long long limit_ns, void* stream) {
     int* status = nullptr;

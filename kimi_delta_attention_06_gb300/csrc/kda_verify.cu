@@ -276,39 +276,59 @@ kda_verify_kernel(const float* __restrict__ tp, long long ldp, const float* __re
     out[n * (K + 1) + a] = pick;
 }
 
-int launch_verify(const float* tp, long long ldp, const float* dp, long long ldq, const int32_t* toks,
-                  const int32_t* num_draft, const float* ua, const float* us, int N, int K, int V, int32_t* out,
-                  int32_t* num_out, int* status, cudaStream_t stream)
-{
-    // CTAs of 16 warps; as many a row as leave each an SM of its own, as each one's acceptance, exchange
-    // and narrowing are latency that more of them only repeat (256 rows of 100003: 48.6 us at one CTA
-    // a row, 55 at two; of 8 warps 54 at two, 52 at four, 59 at eight; with two on some SMs 24 rows of
-    // 90511 took 15.1 instead of 12.1, 100 of 50000 20.3 instead of 16.5, 78 of 37080 14.8 instead of
-    // 11.7).  17 clusters of 8 find room at once (19 rows: 15.0 with 8, 13.4 with 4).  Few sequences take
-    // up to 16 (past the portable cluster size), so that a row of 131072 is one round of loads; slices of
-    // 2048 tokens at least.
-    const int most = static_cast<long long>(N) * 16 <= 152 && V > 8 * 4096 ? 16 : 8, warps = 16;
+// CTAs of 16 warps a row: as many as leave each an SM of its own, as each one's acceptance, exchange and narrowing are
+// latency that more of them only repeat (152 SMs: 256 rows of 100003 48.6 us at one CTA a row, 55 at two; of 8 warps 54 at
+// two, 52 at four, 59 at eight; with two on some SMs 24 rows of 90511 took 15.1 instead of 12.1, 100 of 50000 20.3 instead of
+// 16.5, 78 of 37080 14.8 instead of 11.7).  Clusters of 8 do not find room on all SMs (19 rows: 15.0 with 8, 13.4 with 4), on
+// nine tenths of them they do.  Few sequences take up to 16, past the portable cluster size, where the device holds that
+// many such clusters, so that a row of 131072 is one round of loads; slices of 2048 tokens at least.
+int verify_cluster(int N, int V, int sms, int clusters16) {
+    const int most = static_cast<long long>(N) * 16 <= sms && N <= clusters16 && V > 8 * 4096 ? 16 : 8;
     int C = 1;
-    while (C < most && static_cast<long long>(N) * 2 * C <= (C == 4 ? 17 * 8 : 152) && V / (2 * C) >= 2048) C *= 2;
-    static bool wide_done[kMaxDevicesAttr] = {};
-    int dev = 0;
-    if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= kMaxDevicesAttr) return -3;
-    if (C > 8 && !wide_done[dev]) {
-        if (cudaFuncSetAttribute(kda_verify_kernel, cudaFuncAttributeNonPortableClusterSizeAllowed, 1) != cudaSuccess)
-            return -3;
-        wide_done[dev] = true;
-    }
+    while (C < most && static_cast<long long>(N) * 2 * C <= (C == 4 ? sms * 9 / 10 : sms) && V / (2 * C) >= 2048) C *= 2;
+    return C;
+}
+
+namespace {
+cudaLaunchConfig_t verify_config(unsigned rows, int C, cudaLaunchAttribute (&at)[1]) {
     cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3(static_cast<unsigned>(N) * C);
-    cfg.blockDim = dim3(static_cast<unsigned>(warps) * 32);
-    cfg.stream = stream;
-    cudaLaunchAttribute at[1];
+    cfg.gridDim = dim3(rows * C);
+    cfg.blockDim = dim3(kVerMaxWarps * 32);
     at[0].id = cudaLaunchAttributeClusterDimension;
     at[0].val.clusterDim.x = C;
     at[0].val.clusterDim.y = 1;
     at[0].val.clusterDim.z = 1;
     cfg.attrs = at;
     cfg.numAttrs = 1;
+    return cfg;
+}
+// Clusters of 16 that the device holds at once: 0 where it refuses them.
+int clusters_of_16() {
+    cudaLaunchAttribute at[1];
+    const cudaLaunchConfig_t cfg = verify_config(1, 16, at);
+    int n = 0;
+    if (cudaFuncSetAttribute(kda_verify_kernel, cudaFuncAttributeNonPortableClusterSizeAllowed, 1) != cudaSuccess ||
+        cudaOccupancyMaxActiveClusters(&n, kda_verify_kernel, &cfg) != cudaSuccess) {
+        cudaGetLastError();                                 // (the smaller clusters do without)
+        return 0;
+    }
+    return n;
+}
+}  // namespace
+
+int launch_verify(const float* tp, long long ldp, const float* dp, long long ldq, const int32_t* toks,
+                  const int32_t* num_draft, const float* ua, const float* us, int N, int K, int V, int32_t* out,
+                  int32_t* num_out, int* status, cudaStream_t stream)
+{
+    static int sms[kMaxDevicesAttr] = {}, held[kMaxDevicesAttr] = {};       // of each device; held: clusters of 16, + 1
+    int dev = 0;
+    if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= kMaxDevicesAttr) return -3;
+    if (!sms[dev] && cudaDeviceGetAttribute(&sms[dev], cudaDevAttrMultiProcessorCount, dev) != cudaSuccess) return -3;
+    if (!held[dev]) held[dev] = clusters_of_16() + 1;
+    const int C = verify_cluster(N, V, sms[dev], held[dev] - 1);
+    cudaLaunchAttribute at[1];
+    cudaLaunchConfig_t cfg = verify_config(static_cast<unsigned>(N), C, at);
+    cfg.stream = stream;
     return cudaLaunchKernelEx(&cfg, kda_verify_kernel, tp, ldp, dp, ldq, toks, num_draft, ua, us, K, V, C, out, num_out,
                               status) == cudaSuccess ? 0 : -3;
 }

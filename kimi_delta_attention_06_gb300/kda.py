@@ -129,6 +129,8 @@ def load():
             lib.kda_chunk_size.argtypes = []
             lib.kda_debug_expire_wait.restype = _i
             lib.kda_debug_expire_wait.argtypes = [ctypes.c_ulonglong, _vp]
+            lib.kda_debug_verify_cluster.restype = _i
+            lib.kda_debug_verify_cluster.argtypes = [_i, _i, _i, _i]
             _lib = lib
     return _lib
 
@@ -626,6 +628,10 @@ def kda_verify_draft(target_probs, draft_probs, draft_tokens, num_draft, u_accep
 
 def kda_debug_expire_wait(limit_ns: int, stream=None):
     _check(load().kda_debug_expire_wait(int(limit_ns), _stream(stream)), "kda_debug_expire_wait")
+
+
+def kda_debug_verify_cluster(N: int, V: int, sms: int, clusters16: int) -> int:
+    return int(load().kda_debug_verify_cluster(int(N), int(V), int(sms), int(clusters16)))
 
 
 def kda_device_status(stream=None) -> int:
