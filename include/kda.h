@@ -476,13 +476,15 @@ int kda_latent_gather(const void* cache, int cache_dtype, int num_pages, int pag
  * query as a sum of two e4m3 values (exact above 1/900 of its row's largest magnitude, to within
  * 2^-17 of that magnitude below).
  * An e4m3 row whose scale is NaN or infinite makes the queries that see it NaN.
- * 1 <= K * H <= KDA_LATENT_MAX_ROWS, else KDA_ERR_UNSUPPORTED.  seq_lens[n] outside
+ * 1 <= K * H <= KDA_LATENT_MAX_ROWS, else KDA_ERR_UNSUPPORTED; max_pages * page_size <=
+ * KDA_LATENT_MAX_TOKENS, else KDA_ERR_INVALID_ARG.  seq_lens[n] outside
  * [0, max_pages * page_size] counts as 0 and is reported; a page outside [0, num_pages) is
  * reported and leaves the sequence's outputs unspecified.  Scratch: partial results of at most
  * two work items per SM, stream-ordered from the library's pool as for kda_chunk_prefill.
  * Deterministic.
  */
 #define KDA_LATENT_MAX_ROWS 512
+#define KDA_LATENT_MAX_TOKENS 2147479552     /* 2^31 - 4096: max_pages * page_size of kda_latent_decode */
 int kda_latent_decode(const uint16_t* q, const void* cache, int cache_dtype, int num_pages, int page_size,
                       const int32_t* block_table, int max_pages, const int32_t* seq_lens,
                       int N, int K, int H, float sm_scale, uint16_t* out, float* lse, void* stream);

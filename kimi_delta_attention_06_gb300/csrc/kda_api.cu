@@ -839,7 +839,8 @@ int kda_latent_decode(const uint16_t* q, const void* cache, int cache_dtype, int
     if (rc != KDA_OK) return rc;
     if (N < 0 || K < 0 || H <= 0 || max_pages < 0 || !scale_ok(sm_scale)) return KDA_ERR_INVALID_ARG;
     if (static_cast<int64_t>(K) * H > KDA_LATENT_MAX_ROWS) return KDA_ERR_UNSUPPORTED;
-    if (static_cast<int64_t>(max_pages) * page_size > INT32_MAX) return KDA_ERR_INVALID_ARG;
+    // (a tile or a copy's boxes past the longest sequence still count in 32 bits)
+    if (static_cast<int64_t>(max_pages) * page_size > KDA_LATENT_MAX_TOKENS) return KDA_ERR_INVALID_ARG;
     if (static_cast<int64_t>(N) * K * H >= (int64_t(1) << 31)) return KDA_ERR_INVALID_ARG;
     if (N == 0 || K == 0) return KDA_OK;
     if (!q || !seq_lens || !out || (max_pages > 0 && !block_table)) return KDA_ERR_INVALID_ARG;

@@ -47,6 +47,7 @@ KDA_LATENT_DIM = 512
 KDA_LATENT_ROPE = 64
 KDA_LATENT_MAX_PAGE = 1024
 KDA_LATENT_MAX_ROWS = 512
+KDA_LATENT_MAX_TOKENS = 2**31 - 4096
 KDA_VERIFY_MAX_DRAFT = 64
 
 _vp = ctypes.c_void_p
