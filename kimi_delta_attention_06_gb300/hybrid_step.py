@@ -92,6 +92,17 @@ class HybridServer:
         self.table = torch.randperm(seqs * pages, generator=g).to(torch.int32).view(seqs, pages).to(m.device)
         self.state = torch.zeros(seqs, m.H, 128, 128, device=m.device)
         self.lens = torch.zeros(seqs, dtype=torch.int32, device=m.device)
+        self.room = pages * page                               # tokens that a sequence's pages hold
+        self.most = 0                                          # upper bound of the lengths, kept on the host
+
+    def _take(self, tokens: int):
+        """Refuse a step of `tokens` a sequence that the pages do not hold (an index past the table would be a fault on
+        the GPU).  The bound counts every entered token as accepted; the lengths are read back only where it is reached."""
+        if self.most + tokens > self.room:
+            self.most = int(self.lens.max()) if self.N else 0
+            if self.most + tokens > self.room:
+                raise ValueError(f"{tokens} more tokens do not fit: a sequence holds {self.most} of {self.room}")
+        self.most += tokens
 
     def _slots(self, seq, pos):
         """Cache rows of tokens at positions pos of sequences seq."""
@@ -102,9 +113,14 @@ class HybridServer:
         returns the target's distribution [N, V] after each."""
         m, dev = self.m, self.m.device
         lens = torch.tensor([t.numel() for t in tokens], dtype=torch.int32)
+        if len(tokens) != self.N:
+            raise ValueError(f"{self.N} sequences, got the tokens of {len(tokens)}")
         cu_host = F.pad(lens.cumsum(0), (1, 0)).to(torch.int32)
         before = self.lens.cpu()
         total = before + lens
+        if self.N and int(total.max()) > self.room:
+            raise ValueError(f"the prompt does not fit: a sequence would hold {int(total.max())} of {self.room} tokens")
+        self.most = int(total.max()) if self.N else 0
         cu_k_host = F.pad(total.cumsum(0), (1, 0)).to(torch.int32)
         seq = torch.repeat_interleave(torch.arange(self.N), lens.long()).to(dev)
         pos = (torch.cat([torch.arange(int(n)) for n in lens]).to(dev) + self.lens[seq]).long()
@@ -129,6 +145,9 @@ class HybridServer:
         m = self.m
         N, K = drafts.shape
         K1 = K + 1
+        if N != self.N:
+            raise ValueError(f"{self.N} sequences, got the drafts of {N}")
+        self._take(K1)
         ids = torch.cat([last[:, None], drafts], dim=1)
         x = m.embed[ids.long()].view(N * K1, m.M)
         kin = [t.view(N, K1, *t.shape[1:]) for t in m.kda_inputs(x)]
