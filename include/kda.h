@@ -471,10 +471,12 @@ int kda_latent_gather(const void* cache, int cache_dtype, int num_pages, int pag
  * A query that sees nothing gives zeros and lse = -inf.  Cache rows past the end of a sequence
  * (the rest of its last page) are never part of a result, whatever they hold.  Softmax
  * statistics and sums are fp32.  The probabilities enter the second product as bf16; over an
- * e4m3 cache, times the token's scale, as a sum of three e5m2 values (9 bits; weighted latents
- * below 2^-26 of the largest are rounded to that step, and results below 2^-80 may vanish), and the
- * query as a sum of two e4m3 values (exact above 1/900 of its row's largest magnitude, to within
- * 2^-17 of that magnitude below).
+ * e4m3 cache, times the token's scale, as a sum of three e5m2 values, and the query as a sum of two
+ * e4m3 values (exact above 1/900 of its row's largest magnitude, to within 2^-17 of that magnitude
+ * below).  The three values keep 9 bits of a product of probability and scale, or a step of 2^-26 of
+ * the largest such product of the sequence where that is coarser (an all-zero row counts with its
+ * scale of 1, and a token whose product is below 2^-130 of the largest may be left out of the
+ * denominator too: scales of latents that far apart); results below 2^-80 may vanish.
  * An e4m3 row whose scale is NaN or infinite makes the queries that see it NaN.
  * 1 <= K * H <= KDA_LATENT_MAX_ROWS, else KDA_ERR_UNSUPPORTED; max_pages * page_size <=
  * KDA_LATENT_MAX_TOKENS, else KDA_ERR_INVALID_ARG.  seq_lens[n] outside

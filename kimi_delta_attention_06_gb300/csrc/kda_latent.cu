@@ -19,10 +19,11 @@
 //   - s moves from the latents to the weights: O = sum (p s) codes.  p s is the sum of three e5m2
 //     values (3 bits each: a relative 2^-9, less than a rounding to bf16), scaled so that the
 //     largest lies in 2^10 .. 2^15, which leaves 26 binades or more below it.
-// Measured, 32 heads: 64 sequences (970k tokens), bf16, K = 1, 188 us, 5.9 TB/s (HBM); e4m3 134 us
-// (4.8 TB/s; 16 heads 114 us); 16 sequences (220k tokens), K = 4, e4m3 99 us, bf16 95 us (64 rows a CTA:
-// the products' operands, which shared memory feeds at 128 bytes a clock); one sequence of 145408, bf16,
-// 42 us, 6 of them the join.
+// Measured, 32 heads: 64 sequences (970k tokens), bf16, K = 1, 185 us, 6.0 TB/s (HBM); e4m3 133 us
+// (4.8 TB/s; 16 heads 112 us; the softmax warps' chain through each tile); 16 sequences (214k tokens), K = 4,
+// e4m3 100 us, bf16 93 us (64 rows a CTA: over e4m3 58 us are tiles, of 2750 clocks each, 2364 of them products
+// whose operands shared memory feeds at 128 bytes a clock, 28 us segments' starts and ends, 13 us the join); one
+// sequence of 145408, bf16, 42 us, 6 of them the join.
 // Expanding the tile to bf16 instead (exact too) took 4800 clocks a tile of 64 rows: loads into
 // registers hold too little in flight beside 227 KB of shared memory, and the tile is written and
 // read once more.

@@ -13,9 +13,10 @@
 // one and V's two a tile, in the order in which the products use and free them.
 //
 // Bound by the tensor cores and, in long runs, by the power limit of the card: 32 heads, causal, 8192
-// tokens take 393 us (1750 TFLOP/s; a plain matrix product reaches 1900 for moments and holds 1730 for
-// seconds), 2048 tokens after 32768 cached ones 843 us (1680 TFLOP/s: 256 CTAs on 152 SMs).  One thread issues all products: with one warp a query tile the two tiles'
-// products interleaved instead of taking turns (518 -> 586 us, against 451 with one thread).
+// tokens take 393 us in a graph (1750 TFLOP/s; a plain matrix product reaches 1900 for moments and holds
+// 1730 for seconds), 2048 tokens after 32768 cached ones 852 us (1660 TFLOP/s: 256 CTAs on 152 SMs).  One
+// thread issues all products: with one warp a query tile the two tiles' products interleaved instead of
+// taking turns (518 -> 586 us, against 451 with one thread).
 //
 // Few queries over many keys: the keys are split over CTAs, whose partial (m, l, O) a second kernel joins
 // (see expanded_span).
