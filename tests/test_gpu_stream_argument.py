@@ -8,7 +8,7 @@ from tests import _latent as L
 
 pytestmark = pytest.mark.gpu
 DEV = "cuda"
-LONG = 100_000_000                                              # clocks: about 50 ms
+LONG = 300_000_000                                              # clocks: about 150 ms
 
 
 @pytest.fixture(scope="module", autouse=True)
