@@ -400,12 +400,12 @@ def _dense(t: Optional[torch.Tensor], dtype, need: int, what: str):
 
 
 def _rows2(t: torch.Tensor, dtype, rows: int, width: int, what: str):
-    """(address, row stride in elements) of a 2-D tensor [rows or more, width] whose rows are contiguous; one
-    row has any stride: `width`, which the checks pass."""
+    """(address, row stride in elements) of a 2-D tensor [rows or more, width or more] whose rows are contiguous;
+    one row has any stride: `width`, which the checks pass."""
     if t.dtype is not dtype:
         raise TypeError(f"{what}: expected a {dtype} tensor, got {t.dtype}")
     shape = t.shape
-    if len(shape) != 2 or shape[0] < rows or shape[1] != width:
+    if len(shape) != 2 or shape[0] < rows or shape[1] < width:
         raise ValueError(f"{what}: expected a tensor [{rows}, {width}], got {tuple(shape)}")
     st = t.stride()
     if st[1] != 1 and t.numel():
@@ -414,17 +414,17 @@ def _rows2(t: torch.Tensor, dtype, rows: int, width: int, what: str):
 
 
 def _rows3(t: torch.Tensor, dtype, n0: int, n1: int, width: int, least0: int, what: str):
-    """The same of a 3-D tensor [n0 or more, n1, width]: (address, strides of its first two dimensions; of a
+    """The same of a 3-D tensor [n0, n1, width] or more: (address, strides of its first two dimensions; of a
     single entry: least0 and width)."""
     if t.dtype is not dtype:
         raise TypeError(f"{what}: expected a {dtype} tensor, got {t.dtype}")
     shape = t.shape
-    if len(shape) != 3 or shape[0] < n0 or shape[1] != n1 or shape[2] != width:
+    if len(shape) != 3 or shape[0] < n0 or shape[1] < n1 or shape[2] < width:
         raise ValueError(f"{what}: expected a tensor [{n0}, {n1}, {width}], got {tuple(shape)}")
     st = t.stride()
     if st[2] != 1 and t.numel():
         raise ValueError(f"{what}: the last dimension of a KDA tensor must be contiguous")
-    return t.data_ptr(), st[0] if shape[0] > 1 else least0, st[1] if n1 > 1 else width
+    return t.data_ptr(), st[0] if shape[0] > 1 else least0, st[1] if shape[1] > 1 else width
 
 
 def _short(what: str, t: torch.Tensor, need: str):

@@ -40,7 +40,7 @@ def _cache(dt=kda.KDA_CACHE_E4M3, pages=4, page=16):
 def test_append():
     good = dict(c=bf(5, 512), k_rope=bf(5, 64), cache=_cache(), cache_dtype=1, slots=i32(5), stream=0)
     _refused(kda.latent_append, good, [
-        dict(k_rope=bf(4, 64)), dict(slots=i32(4)), dict(c=bf(5, 448)), dict(c=bf(5, 576)),
+        dict(k_rope=bf(4, 64)), dict(slots=i32(4)), dict(c=bf(5, 448)), dict(c=bf(2, 3, 512)),
         dict(k_rope=bf(5, 32)), dict(c=bf(1, 100), k_rope=bf(1, 64), slots=i32(1)),
         dict(c=bf(1, 512), k_rope=bf(1, 8), slots=i32(1)), dict(c=bf(5 * 512)), dict(cache=_cache(0))])
     low = dict(good, total_tokens=5)
@@ -55,7 +55,7 @@ def test_gather(dt):
            dict(cache=_cache(1 - dt))]
     low = dict(good, num_seqs=2, total_tokens=9, c=bf(9, 512), k_rope=bf(9, 64))
     _refused(kda.kda_latent_gather, low, bad + [dict(c=bf(8, 512)), dict(k_rope=bf(8, 64)), dict(c=bf(9, 500)),
-                                                dict(k_rope=bf(9, 72)), dict(cu_seqlens_host=i32(2))])
+                                                dict(k_rope=bf(9, 56)), dict(cu_seqlens_host=i32(2))])
     _refused(kda.latent_gather, good, bad)
 
 
@@ -75,7 +75,7 @@ def test_prefill():
     good = dict(q=bf(9, 4, 192), k=bf(9, 4, 128), v=bf(9, 4, 128), k_rope=bf(9, 64), cu_q_host=cu, cu_k_host=cu, sm_scale=0.07,
                 cu_q=i32(3), cu_k=i32(3), stream=0)
     bad = [dict(q=bf(9, 4, 128)), dict(q=bf(9, 4, 576)), dict(v=bf(8, 4, 128)), dict(v=bf(9, 3, 128)), dict(k=bf(9, 3, 128)),
-           dict(k=bf(9, 4, 192)), dict(v=bf(9, 4, 64)), dict(k_rope=bf(8, 64)), dict(k_rope=bf(9, 32)), dict(cu_q=i32(2)),
+           dict(k=bf(9, 4, 120)), dict(v=bf(9, 4, 64)), dict(k_rope=bf(8, 64)), dict(k_rope=bf(9, 32)), dict(cu_q=i32(2)),
            dict(cu_k=i32(2)), dict(cu_k_host=cu[:2].contiguous()), dict(k=bf(9, 1, 128), v=bf(9, 1, 128))]
     _refused(kda.latent_prefill, good, bad)
     low = dict(good, num_seqs=2, total_q=9, total_k=9, H=4, causal=1, out=bf(9, 4, 128), lse=None)
@@ -113,8 +113,13 @@ def test_outputs(monkeypatch):
     assert seen
 
 
-def test_longer_tables_lengths_and_offsets_pass():
-    """Buffers that a server keeps may be longer than the call."""
+def test_larger_tensors_pass():
+    """Buffers that a server keeps may be longer than the call, rows wider than what is read of them."""
+    with pytest.raises(ValueError, match="on the GPU"):
+        kda.kda_verify_draft(torch.zeros(3, 5, 16), torch.zeros(3, 4, 16), i32(3, 4), None, torch.zeros(3, 4), torch.zeros(3), 3, 4, 13,
+                             i32(3, 5), i32(3), stream=0)
+    with pytest.raises(ValueError, match="on the GPU"):
+        kda.latent_append(bf(3, 576), bf(3, 72), _cache(), 1, i32(3), stream=0)
     with pytest.raises(ValueError, match="on the GPU"):
         kda.latent_decode(bf(3, 2, 8, 576), _cache(), 1, i32(9, 4), i32(9), 0.07, stream=0)
     with pytest.raises(ValueError, match="on the GPU"):
