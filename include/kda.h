@@ -23,9 +23,9 @@
  *     prefill entry points kda_chunk_prefill and kda_chunk_prefill_ex take
  *     their hand-off rings stream-ordered from a memory pool the library owns
  *     (see kda_chunk_prefill); kda_chunk_prefill_noalloc uses a fixed device
- *     array instead and allocates nothing; kda_latent_decode and, for few
- *     queries over many keys, kda_latent_prefill take their partial results
- *     from the same pool; every other entry point needs no scratch.
+ *     array instead and allocates nothing; kda_latent_decode, kda_latent_decode_tree
+ *     and, for few queries over many keys, kda_latent_prefill take their partial
+ *     results from the same pool; every other entry point needs no scratch.
  *   - Tensors are dense, row-major, with the last dimension contiguous.
  *     bf16 tensors are passed as uint16_t bit patterns (IEEE bfloat16).
  *     Every device pointer must be 16-byte aligned.
@@ -353,6 +353,41 @@ int kda_decode_multi(const uint16_t* q, const uint16_t* k, const uint16_t* v,
                      int N, int K, int H, int Dk, int Dv, int decay, void* stream);
 
 /*
+ * Trees of drafted tokens.  A sequence's K <= KDA_TREE_MAX_NODES places hold the nodes of a tree
+ * that hangs on its last cached token (usually place 0 holds the newest token and the drafts hang
+ * on it):
+ *   parents     (device) int32 [N, K]: the place of each node's parent, before its own; -1: the
+ *               node follows the last cached token; below -1: the place holds no node (trees of
+ *               fewer than K nodes), and what it holds in the other inputs is never used.
+ * A parent that is not before its child, or holds no node, makes the child no node; the next
+ * kda_device_status then returns KDA_ERR_INVALID_ARG.  Nothing of a node reaches a node that it is
+ * not an ancestor of, whatever it holds.  A chain of drafts is the tree with parents
+ * -1, 0, 1, ..., K - 2.
+ */
+#define KDA_TREE_MAX_NODES 64
+
+/*
+ * kda_decode_tree -- kda_decode_multi's verify pass for a tree: each node's output from the state
+ * that its path from the root leads to.  The pool is only read (the accepted path is committed by
+ * a kda_decode_multi over its tokens).
+ *
+ *   q, k, v, log_alpha, beta, state_pool, state_slots, decay: as in kda_decode_multi, a node in a
+ *               token's place; with S the sequence's state, node i has
+ *                   S_i = (I - beta_i k_i k_i^T) Diag(alpha_i) S_parent(i) + beta_i k_i v_i^T
+ *                   o_i = S_i^T q_i                          (S_parent = S for parents[i] = -1)
+ *   parents     as above
+ *   out         (device) [N, K, H, Dv], bf16 or fp32 per out_dtype; zeros for a place without a node
+ * State slots need not be distinct.  An out-of-range slot skips its sequence (out is left as it
+ * was) and is reported.  Dk == Dv in {64, 128}.  Deterministic.  fp32 throughout: the result
+ * differs from that of kda_decode_multi on the same path in the order of its sums.
+ */
+int kda_decode_tree(const uint16_t* q, const uint16_t* k, const uint16_t* v,
+                    const float* log_alpha, const uint16_t* beta,
+                    const float* state_pool, int num_slots, const int32_t* state_slots,
+                    const int32_t* parents, void* out, int out_dtype,
+                    int N, int K, int H, int Dk, int Dv, int decay, void* stream);
+
+/*
  * kda_prepare_inputs -- the KDA module's input preparation in one pass (the module of
  * the Kimi K3 primer, wiki summary, section 3: a short causal convolution of the
  * projections, an L2 norm on q and k, the alpha and beta gates).  Writes exactly the
@@ -438,6 +473,32 @@ int kda_latent_append(const uint16_t* c, int64_t ldc, const uint16_t* k_rope, in
                       const int32_t* slots, int total_tokens, void* stream);
 
 /*
+ * kda_latent_append_rope -- kda_latent_append with the position parts rotated on the way, of the
+ * new tokens' queries too.
+ *
+ *   k_rope      unrotated; what enters the cache is its rotation by positions[t]
+ *   positions   (device) int32 [total_tokens]: the position of each token in its text, any value (a
+ *               node of a tree of drafts sits at its depth, not at its place in the cache)
+ *   inv_freq    (device) fp32 [KDA_LATENT_ROPE / 2]: pair i turns by positions[t] * inv_freq[i], in
+ *                   (x, y) -> (x cos - y sin, x sin + y cos);
+ *               magnitudes below 2^32 (anything else gives NaN in its pair).  The angle is formed
+ *               exactly to within positions[t] * 2^-64 turns, the rotation in fp32, rounded once.
+ *   interleaved 1: pair i is values (2 i, 2 i + 1); 0: values (i, i + KDA_LATENT_ROPE / 2)
+ *   q           (device) bf16 or NULL: the position parts of H heads' queries, KDA_LATENT_ROPE values each,
+ *               token / head strides ldq, hdq in elements (multiples of 8, hdq at least
+ *               KDA_LATENT_ROPE: slices of [T, H, 192] rows, say)
+ *   q_out       (device) bf16, strides ldo, hdo: the rotated parts (where kda_latent_decode or
+ *               kda_latent_prefill reads them); may be q itself with the same strides.  NULL with q.
+ * A token whose slot is negative (padding) or out of range (reported) is skipped, its rows of q_out
+ * are left as they were.  H is ignored when q is NULL.
+ */
+int kda_latent_append_rope(const uint16_t* c, int64_t ldc, const uint16_t* k_rope, int64_t ldr,
+                           void* cache, int cache_dtype, int num_pages, int page_size,
+                           const int32_t* slots, const int32_t* positions, const float* inv_freq, int interleaved,
+                           const uint16_t* q, int64_t ldq, int64_t hdq, uint16_t* q_out, int64_t ldo, int64_t hdo,
+                           int total_tokens, int H, void* stream);
+
+/*
  * kda_latent_gather -- read cached tokens back as dense bf16 rows (to expand a cached prefix
  * into per-head keys and values, or to move it).
  *
@@ -490,6 +551,19 @@ int kda_latent_gather(const void* cache, int cache_dtype, int num_pages, int pag
 int kda_latent_decode(const uint16_t* q, const void* cache, int cache_dtype, int num_pages, int page_size,
                       const int32_t* block_table, int max_pages, const int32_t* seq_lens,
                       int N, int K, int H, float sm_scale, uint16_t* out, float* lse, void* stream);
+
+/*
+ * kda_latent_decode_tree -- kda_latent_decode for a tree of drafted tokens (see KDA_TREE_MAX_NODES):
+ * the last K cached tokens of a sequence are the tree's nodes, place j at token seq_lens[n] - K + j.
+ *
+ *   parents     (device) int32 [N, K] as for kda_decode_tree
+ * Node j sees the seq_lens[n] - K tokens before the tree, its ancestors and itself; a place without a
+ * node gives zeros and lse = -inf.  seq_lens[n] is 0 (a sequence that is not there: zeros and -inf) or
+ * at least K, else it counts as 0 and is reported.  Everything else as in kda_latent_decode.
+ */
+int kda_latent_decode_tree(const uint16_t* q, const void* cache, int cache_dtype, int num_pages, int page_size,
+                           const int32_t* block_table, int max_pages, const int32_t* seq_lens, const int32_t* parents,
+                           int N, int K, int H, float sm_scale, uint16_t* out, float* lse, void* stream);
 
 /*
  * kda_latent_prefill -- expanded latent attention over packed prompts: per-head keys and values
@@ -546,6 +620,31 @@ int kda_verify_draft(const float* target_probs, int64_t ldp, const float* draft_
                      const float* u_sample, int N, int K, int V, int32_t* tokens, int32_t* num_tokens,
                      void* stream);
 
+/*
+ * kda_token_logprobs -- what a server answers with beside its tokens: the log probabilities of given
+ * tokens under rows of logits, their ranks, the rows' entropies and most likely tokens.
+ *
+ *   logits      (device) [R, V], bf16 or fp32 per logits_dtype (kda_out_dtype), rows ld elements apart
+ *               (any ld >= V, rows aligned to their elements)
+ *   tokens      (device) int32 [R] or NULL (alternatives and entropies alone)
+ *   scale       finite, > 0 (1 / temperature): z = scale * logits
+ *   logprob     (device) fp32 [R], NULL with tokens: z_t - log sum exp z
+ *   rank        (device) int32 [R] or NULL: the place of the token, from 1, in the order of the logits,
+ *               largest first, equal ones by lowest index
+ *   entropy     (device) fp32 [R] or NULL: -sum p log p, natural
+ *   top_logprob, top_token  (device) fp32, int32 [R, top]: the first `top` tokens of that order;
+ *               past the vocabulary's end -inf and -1
+ * A row whose token is negative is padding: zeros, rank 0, alternatives -inf and -1; so is one whose
+ * token is V or more, which is reported.  Logits of -inf have probability 0 (log probability -inf; a row
+ * of nothing else: all of them, and entropy 0); a row that holds a NaN or +inf gives NaN, rank 0 and
+ * tokens of -1.  Sums are fp32, one partial sum a thread.  Deterministic.
+ * top <= KDA_LOGPROBS_MAX_TOP, V <= 2^30, else KDA_ERR_UNSUPPORTED.
+ */
+#define KDA_LOGPROBS_MAX_TOP 32
+int kda_token_logprobs(const void* logits, int logits_dtype, int64_t ld, const int32_t* tokens, int R, int V, int top,
+                       float scale, float* logprob, int32_t* rank, float* entropy, float* top_logprob, int32_t* top_token,
+                       void* stream);
+
 /* Number of checkpoint slots kda_chunk_prefill writes: sum over sequences of
  * ceil(len / ckpt_stride) (0 when ckpt_stride == 0).  cu_seqlens_host is a host
  * array of num_seqs + 1 offsets.  Returns -1 on invalid arguments. */
@@ -563,7 +662,8 @@ int64_t kda_ckpt_count_ex(const int32_t* cu_seqlens_host, const int32_t* start_p
  * kernel returned early; its outputs are undefined), KDA_ERR_RANGE (a prefill
  * met decays or magnitudes outside its numeric domain, see the conventions at
  * the top; its outputs are undefined), KDA_ERR_INVALID_ARG (a device-side index
- * of kda_decode_multi, kda_latent_* or kda_verify_draft was out of range), or KDA_ERR_CUDA if the
+ * of kda_decode_multi, kda_decode_tree, kda_latent_*, kda_verify_draft or
+ * kda_token_logprobs was out of range), or KDA_ERR_CUDA if the
  * synchronisation itself failed.  The first failure recorded since the last
  * call is the one returned. */
 int kda_device_status(void* stream);

@@ -50,8 +50,18 @@ int launch_latent_gather(const void* cache, int e4m3, int num_pages, int page_si
                          const int32_t* start, const int32_t* cu, int num_seqs, int T, uint16_t* c, long long ldc,
                          uint16_t* r, long long ldr, int* status, cudaStream_t stream);
 int launch_latent_decode(const uint16_t* q, const void* cache, int e4m3, int num_pages, int page_size,
-                         const int32_t* table, int max_pages, const int32_t* seq_lens, int N, int K, int H,
-                         float sm_scale, uint16_t* out, float* lse, void* scratch, int* status, cudaStream_t stream);
+                         const int32_t* table, int max_pages, const int32_t* seq_lens, const int32_t* parents, int N, int K,
+                         int H, float sm_scale, uint16_t* out, float* lse, void* scratch, int* status, cudaStream_t stream);
+int launch_latent_append_rope(const uint16_t* c, long long ldc, const uint16_t* r, long long ldr, void* cache, int e4m3,
+                              long long num_rows, const int32_t* slots, const int32_t* pos, const float* freq, int inter,
+                              const uint16_t* q, long long ldq, long long hdq, uint16_t* q_out, long long ldo, long long hdo,
+                              int T, int H, int* status, cudaStream_t stream);
+int launch_decode_tree(const uint16_t* q, const uint16_t* k, const uint16_t* v, const float* la, const uint16_t* beta,
+                       const float* pool, int num_slots, const int32_t* slots, const int32_t* parents, void* out, int out_f32,
+                       int N, int K, int H, int D, int decay, int* status, cudaStream_t stream);
+int launch_token_logprobs(const void* x, int f32, long long ld, const int32_t* tok, int R, int V, int top, float scale,
+                          float* logprob, int32_t* rank, float* entropy, float* top_lp, int32_t* top_tok, int* status,
+                          cudaStream_t stream);
 size_t latent_decode_scratch(int rows);
 int launch_latent_prefill(const uint16_t* q, const uint16_t* k, long long ldk, long long hdk, const uint16_t* v,
                           long long ldv, long long hdv, const uint16_t* r, long long ldr, const int32_t* cu_q,
@@ -731,6 +741,36 @@ int kda_decode_multi(const uint16_t* q, const uint16_t* k, const uint16_t* v,
     return rc == 0 ? KDA_OK : KDA_ERR_CUDA;
 }
 
+int kda_decode_tree(const uint16_t* q, const uint16_t* k, const uint16_t* v,
+                    const float* log_alpha, const uint16_t* beta,
+                    const float* state_pool, int num_slots, const int32_t* state_slots,
+                    const int32_t* parents, void* out, int out_dtype,
+                    int N, int K, int H, int Dk, int Dv, int decay, void* stream) {
+    if (N < 0 || K < 0 || H <= 0 || num_slots < 0) return KDA_ERR_INVALID_ARG;
+    if (decay != KDA_DECAY_CHANNEL && decay != KDA_DECAY_HEAD && decay != KDA_DECAY_NONE) return KDA_ERR_INVALID_ARG;
+    if (out_dtype != KDA_OUT_BF16 && out_dtype != KDA_OUT_F32) return KDA_ERR_INVALID_ARG;
+    if (!head_dims_ok(Dk, Dv)) return KDA_ERR_UNSUPPORTED;
+    if (Dk != Dv) return KDA_ERR_UNSUPPORTED;
+    if (K > KDA_TREE_MAX_NODES) return KDA_ERR_UNSUPPORTED;
+    if (N == 0 || K == 0) return KDA_OK;
+    if (!q || !k || !v || !beta || !state_pool || !parents || !out) return KDA_ERR_INVALID_ARG;
+    if ((decay == KDA_DECAY_NONE) != (log_alpha == nullptr)) return KDA_ERR_INVALID_ARG;
+    if (!state_slots && num_slots < N) return KDA_ERR_INVALID_ARG;
+    if (num_slots == 0) return KDA_ERR_INVALID_ARG;
+    const void* ptrs[] = {q, k, v, log_alpha, beta, state_pool, out};
+    for (const void* p : ptrs)
+        if (p && !aligned16(p)) return KDA_ERR_INVALID_ARG;
+    if ((reinterpret_cast<uintptr_t>(state_slots) & 3u) || (reinterpret_cast<uintptr_t>(parents) & 3u))
+        return KDA_ERR_INVALID_ARG;
+    if (static_cast<int64_t>(N) * K * H >= (int64_t(1) << 31)) return KDA_ERR_INVALID_ARG;
+    int* status = nullptr;
+    int rc = device_setup(&status);
+    if (rc != KDA_OK) return rc;
+    rc = kda::launch_decode_tree(q, k, v, log_alpha, beta, state_pool, num_slots, state_slots, parents, out,
+                                 out_dtype == KDA_OUT_F32, N, K, H, Dk, decay, status, static_cast<cudaStream_t>(stream));
+    return rc == 0 ? KDA_OK : KDA_ERR_CUDA;
+}
+
 int kda_prepare_inputs(const uint16_t* xq, const uint16_t* xk, const uint16_t* xv,
                        const float* conv_w, const uint16_t* conv_state,
                        const float* a_raw, const uint16_t* b_raw,
@@ -809,6 +849,37 @@ int kda_latent_append(const uint16_t* c, int64_t ldc, const uint16_t* k_rope, in
     return rc == 0 ? KDA_OK : KDA_ERR_CUDA;
 }
 
+int kda_latent_append_rope(const uint16_t* c, int64_t ldc, const uint16_t* k_rope, int64_t ldr,
+                           void* cache, int cache_dtype, int num_pages, int page_size,
+                           const int32_t* slots, const int32_t* positions, const float* inv_freq, int interleaved,
+                           const uint16_t* q, int64_t ldq, int64_t hdq, uint16_t* q_out, int64_t ldo, int64_t hdo,
+                           int total_tokens, int H, void* stream) {
+    int rc = check_latent_cache(cache, cache_dtype, num_pages, page_size);
+    if (rc != KDA_OK) return rc;
+    if (total_tokens < 0 || (interleaved != 0 && interleaved != 1)) return KDA_ERR_INVALID_ARG;
+    if ((q == nullptr) != (q_out == nullptr) || (q && H <= 0)) return KDA_ERR_INVALID_ARG;
+    if (total_tokens == 0) return KDA_OK;
+    if (!stride_ok(ldc, KDA_LATENT_DIM) || !stride_ok(ldr, KDA_LATENT_ROPE)) return KDA_ERR_INVALID_ARG;
+    if (!c || !k_rope || !slots || !positions || !inv_freq || !aligned16(c) || !aligned16(k_rope)) return KDA_ERR_INVALID_ARG;
+    const void* p4[] = {slots, positions, inv_freq};
+    for (const void* p : p4)
+        if (reinterpret_cast<uintptr_t>(p) & 3u) return KDA_ERR_INVALID_ARG;
+    if (q) {
+        if (!aligned16(q) || !aligned16(q_out)) return KDA_ERR_INVALID_ARG;
+        if (!stride_ok(ldq, KDA_LATENT_ROPE) || !stride_ok(hdq, KDA_LATENT_ROPE) || !stride_ok(ldo, KDA_LATENT_ROPE) ||
+            !stride_ok(hdo, KDA_LATENT_ROPE))
+            return KDA_ERR_INVALID_ARG;
+        if (static_cast<int64_t>(total_tokens) * H >= (int64_t(1) << 31)) return KDA_ERR_INVALID_ARG;
+    }
+    int* status = nullptr;
+    rc = device_setup(&status);
+    if (rc != KDA_OK) return rc;
+    rc = kda::launch_latent_append_rope(c, ldc, k_rope, ldr, cache, cache_dtype == KDA_CACHE_E4M3,
+                                        static_cast<int64_t>(num_pages) * page_size, slots, positions, inv_freq, interleaved,
+                                        q, ldq, hdq, q_out, ldo, hdo, total_tokens, H, status, static_cast<cudaStream_t>(stream));
+    return rc == 0 ? KDA_OK : KDA_ERR_CUDA;
+}
+
 int kda_latent_gather(const void* cache, int cache_dtype, int num_pages, int page_size,
                       const int32_t* block_table, int max_pages, const int32_t* start_pos,
                       const int32_t* cu_seqlens, const int32_t* cu_seqlens_host,
@@ -832,9 +903,10 @@ int kda_latent_gather(const void* cache, int cache_dtype, int num_pages, int pag
     return rc == 0 ? KDA_OK : KDA_ERR_CUDA;
 }
 
-int kda_latent_decode(const uint16_t* q, const void* cache, int cache_dtype, int num_pages, int page_size,
-                      const int32_t* block_table, int max_pages, const int32_t* seq_lens,
-                      int N, int K, int H, float sm_scale, uint16_t* out, float* lse, void* stream) {
+// Shared by kda_latent_decode (parents NULL) and kda_latent_decode_tree.
+static int latent_decode_call(const uint16_t* q, const void* cache, int cache_dtype, int num_pages, int page_size,
+                              const int32_t* block_table, int max_pages, const int32_t* seq_lens, const int32_t* parents,
+                              int N, int K, int H, float sm_scale, uint16_t* out, float* lse, void* stream) {
     int rc = check_latent_cache(cache, cache_dtype, num_pages, page_size);
     if (rc != KDA_OK) return rc;
     if (N < 0 || K < 0 || H <= 0 || max_pages < 0 || !scale_ok(sm_scale)) return KDA_ERR_INVALID_ARG;
@@ -845,7 +917,7 @@ int kda_latent_decode(const uint16_t* q, const void* cache, int cache_dtype, int
     if (N == 0 || K == 0) return KDA_OK;
     if (!q || !seq_lens || !out || (max_pages > 0 && !block_table)) return KDA_ERR_INVALID_ARG;
     if (!aligned16(q) || !aligned16(out)) return KDA_ERR_INVALID_ARG;
-    const void* p4[] = {block_table, seq_lens, lse};
+    const void* p4[] = {block_table, seq_lens, lse, parents};
     for (const void* p : p4)
         if (reinterpret_cast<uintptr_t>(p) & 3u) return KDA_ERR_INVALID_ARG;
     int* status = nullptr;
@@ -858,9 +930,25 @@ int kda_latent_decode(const uint16_t* q, const void* cache, int cache_dtype, int
     void* ws = nullptr;
     if (cudaMallocFromPoolAsync(&ws, kda::latent_decode_scratch(K * H), pool, st) != cudaSuccess) return KDA_ERR_CUDA;
     rc = kda::launch_latent_decode(q, cache, cache_dtype == KDA_CACHE_E4M3, num_pages, page_size, block_table, max_pages,
-                                   seq_lens, N, K, H, sm_scale, out, lse, ws, status, st);
+                                   seq_lens, parents, N, K, H, sm_scale, out, lse, ws, status, st);
     const bool freed = cudaFreeAsync(ws, st) == cudaSuccess;
     return (rc == 0 && freed) ? KDA_OK : KDA_ERR_CUDA;
+}
+
+int kda_latent_decode(const uint16_t* q, const void* cache, int cache_dtype, int num_pages, int page_size,
+                      const int32_t* block_table, int max_pages, const int32_t* seq_lens,
+                      int N, int K, int H, float sm_scale, uint16_t* out, float* lse, void* stream) {
+    return latent_decode_call(q, cache, cache_dtype, num_pages, page_size, block_table, max_pages, seq_lens, nullptr, N, K, H,
+                              sm_scale, out, lse, stream);
+}
+
+int kda_latent_decode_tree(const uint16_t* q, const void* cache, int cache_dtype, int num_pages, int page_size,
+                           const int32_t* block_table, int max_pages, const int32_t* seq_lens, const int32_t* parents,
+                           int N, int K, int H, float sm_scale, uint16_t* out, float* lse, void* stream) {
+    if (K > KDA_TREE_MAX_NODES) return KDA_ERR_UNSUPPORTED;
+    if (N > 0 && K > 0 && !parents) return KDA_ERR_INVALID_ARG;
+    return latent_decode_call(q, cache, cache_dtype, num_pages, page_size, block_table, max_pages, seq_lens, parents, N, K, H,
+                              sm_scale, out, lse, stream);
 }
 
 int kda_latent_prefill(const uint16_t* q, const uint16_t* k, int64_t ldk, int64_t hdk,
@@ -921,6 +1009,29 @@ int kda_verify_draft(const float* target_probs, int64_t ldp, const float* draft_
     if (rc != KDA_OK) return rc;
     rc = kda::launch_verify(target_probs, ldp, draft_probs, ldq, draft_tokens, num_draft, u_accept, u_sample, N, K, V,
                             tokens, num_tokens, status, static_cast<cudaStream_t>(stream));
+    return rc == 0 ? KDA_OK : KDA_ERR_CUDA;
+}
+
+int kda_token_logprobs(const void* logits, int logits_dtype, int64_t ld, const int32_t* tokens, int R, int V, int top,
+                       float scale, float* logprob, int32_t* rank, float* entropy, float* top_logprob, int32_t* top_token,
+                       void* stream) {
+    if (R < 0 || V <= 0 || top < 0 || !(scale > 0.f) || !scale_ok(scale)) return KDA_ERR_INVALID_ARG;
+    if (logits_dtype != KDA_OUT_BF16 && logits_dtype != KDA_OUT_F32) return KDA_ERR_INVALID_ARG;
+    if (top > KDA_LOGPROBS_MAX_TOP || V > (1 << 30)) return KDA_ERR_UNSUPPORTED;
+    if (R == 0) return KDA_OK;
+    if (ld < V || ld >= (int64_t(1) << 40) || !logits) return KDA_ERR_INVALID_ARG;
+    if (static_cast<int64_t>(R) * 16 >= (int64_t(1) << 31)) return KDA_ERR_INVALID_ARG;
+    if ((tokens == nullptr) != (logprob == nullptr) || (!tokens && rank)) return KDA_ERR_INVALID_ARG;
+    if (top > 0 && (!top_logprob || !top_token)) return KDA_ERR_INVALID_ARG;
+    if (reinterpret_cast<uintptr_t>(logits) & (logits_dtype == KDA_OUT_F32 ? 3u : 1u)) return KDA_ERR_INVALID_ARG;
+    const void* p4[] = {tokens, logprob, rank, entropy, top_logprob, top_token};
+    for (const void* p : p4)
+        if (reinterpret_cast<uintptr_t>(p) & 3u) return KDA_ERR_INVALID_ARG;
+    int* status = nullptr;
+    int rc = device_setup(&status);
+    if (rc != KDA_OK) return rc;
+    rc = kda::launch_token_logprobs(logits, logits_dtype == KDA_OUT_F32, ld, tokens, R, V, top, scale, logprob, rank, entropy,
+                                    top_logprob, top_token, status, static_cast<cudaStream_t>(stream));
     return rc == 0 ? KDA_OK : KDA_ERR_CUDA;
 }
 

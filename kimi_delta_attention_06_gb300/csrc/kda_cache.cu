@@ -9,31 +9,14 @@ namespace kda {
 
 constexpr int kCacheThreads = 256;
 
-// 16 consecutive latents per lane (32 bytes), 2 position values per lane.
+// A token's latents at src (32 lanes x 32 bytes) into its cache row, with the scale of an e4m3 row.  Lane: 16 latents.
 template <bool E4M3>
-__global__ void __launch_bounds__(kCacheThreads)
-kda_latent_append_kernel(const uint16_t* __restrict__ c, long long ldc, const uint16_t* __restrict__ r, long long ldr,
-                         uint8_t* __restrict__ cache, long long num_rows, const int32_t* __restrict__ slots, int T,
-                         int* status)
-{
-    const int lane = threadIdx.x & 31;
-    const long long t = static_cast<long long>(blockIdx.x) * (kCacheThreads / 32) + (threadIdx.x >> 5);
-    if (t >= T) return;
-    const int slot = slots[t];
-    const uint4* src = reinterpret_cast<const uint4*>(c + t * ldc);
-    const uint32_t rope = reinterpret_cast<const uint32_t*>(r + t * ldr)[lane];
-    if (slot < 0) return;
-    if (slot >= num_rows) {
-        if (lane == 0) set_status(status, kStatusIndex);
-        return;
-    }
-    uint8_t* row = cache + static_cast<size_t>(slot) * lat_row_bytes(E4M3);
+__device__ __forceinline__ void put_latents(uint8_t* row, const uint4* src, int lane) {
     if constexpr (!E4M3) {
         uint4* dst = reinterpret_cast<uint4*>(row);
         const uint4 a = src[lane], b = src[lane + 32];
         dst[lane] = a;
         dst[lane + 32] = b;
-        reinterpret_cast<uint32_t*>(row + 2 * kLatDim)[lane] = rope;
     } else {
         // 16 latents of this lane: one 16-byte store of codes
         const uint4 a = src[2 * lane], b = src[2 * lane + 1];
@@ -61,10 +44,162 @@ kda_latent_append_kernel(const uint16_t* __restrict__ c, long long ldc, const ui
             o[i] = f32x2_to_e4m3x2(x[4 * i] * inv, x[4 * i + 1] * inv) |
                    (f32x2_to_e4m3x2(x[4 * i + 2] * inv, x[4 * i + 3] * inv) << 16);
         reinterpret_cast<uint4*>(row)[lane] = make_uint4(o[0], o[1], o[2], o[3]);
-        reinterpret_cast<uint32_t*>(row + kLatDim)[lane] = rope;
         if (lane < 4)
             reinterpret_cast<uint32_t*>(row + kLatScaleAt)[lane] =
                 lane == 0 ? static_cast<uint32_t>(127 + e) << 23 : 0u;
+    }
+}
+
+// 16 consecutive latents per lane (32 bytes), 2 position values per lane.
+template <bool E4M3>
+__global__ void __launch_bounds__(kCacheThreads)
+kda_latent_append_kernel(const uint16_t* __restrict__ c, long long ldc, const uint16_t* __restrict__ r, long long ldr,
+                         uint8_t* __restrict__ cache, long long num_rows, const int32_t* __restrict__ slots, int T,
+                         int* status)
+{
+    const int lane = threadIdx.x & 31;
+    const long long t = static_cast<long long>(blockIdx.x) * (kCacheThreads / 32) + (threadIdx.x >> 5);
+    if (t >= T) return;
+    const int slot = slots[t];
+    const uint4* src = reinterpret_cast<const uint4*>(c + t * ldc);
+    const uint32_t rope = reinterpret_cast<const uint32_t*>(r + t * ldr)[lane];
+    if (slot < 0) return;
+    if (slot >= num_rows) {
+        if (lane == 0) set_status(status, kStatusIndex);
+        return;
+    }
+    uint8_t* row = cache + static_cast<size_t>(slot) * lat_row_bytes(E4M3);
+    put_latents<E4M3>(row, src, lane);
+    reinterpret_cast<uint32_t*>(row + (E4M3 ? kLatDim : 2 * kLatDim))[lane] = rope;
+}
+
+// The same with the position parts rotated on the way: pair i of a key or query turns by pos * f_i,
+//     (x, y) -> (x cos - y sin, x sin + y cos),
+// with pairs of neighbours (2 i, 2 i + 1) or of the two halves (i, i + 32).  The angle matters modulo a turn, and
+// pos * f rounded to 32 bits is off by 0.03 rad at pos = 10^6, so it is taken in fixed point: f / 2 pi as a 64-bit
+// fraction of a turn (its whole turns vanish at whole positions), times pos modulo 2^64, is exact but for the
+// fraction's own rounding, pos * 2^-64.
+//
+// A warp takes a token (or some of its heads, where tokens are few): lane i the angle of pair i, once; then 8 lanes a
+// head, 4 pairs a lane, with 4 heads at once.
+constexpr int kRopeThreads = 128;
+
+// f / 2 pi modulo a turn, in units of 2^-64: 24 bits of f times 96 bits of 1 / 2 pi, moved to its place.  (|f| < 2^32.)
+__device__ __forceinline__ uint64_t rope_turns(float f) {
+    constexpr uint64_t hi = 0x28be60dbull, lo = 0x9391054a7f09d5f4ull;      // floor(2^96 / 2 pi)
+    const uint32_t b = __float_as_uint(f), e = b >> 23 & 0xffu;
+    const uint64_t m = (b & 0x7fffffu) | (e ? 0x800000u : 0u);
+    const uint64_t p0 = m * lo, p1 = __umul64hi(m, lo) + m * hi;
+    const int s = max(182 - static_cast<int>(e ? e : 1), 1);               // f = m 2^(e - 150); 96 - 64 + 150 - e
+    const uint64_t t = s >= 128 ? 0 : s >= 64 ? p1 >> (s - 64) : (p1 << (64 - s)) | (p0 >> s);
+    return b >> 31 ? ~t + 1 : t;
+}
+
+struct RopeArgs {
+    const uint16_t* c; long long ldc;
+    const uint16_t* r; long long ldr;
+    uint8_t* cache; long long num_rows;
+    const int32_t* slots;
+    const int32_t* pos;
+    const float* freq;
+    const uint16_t* q; long long ldq, hdq;
+    uint16_t* q_out; long long ldo, hdo;
+    int T, H, split;                             // split: warps a token (each takes every split-th group of 4 heads)
+    int* status;
+};
+
+// 4 pairs of a lane: loaded, turned, stored.  INTER: 8 neighbours (16 bytes); else 4 of each half (8 bytes each).
+template <bool INTER>
+struct RopePairs {
+    uint32_t w[4];
+    __device__ __forceinline__ void load(const uint16_t* p, int g) {
+        if constexpr (INTER) {
+            const uint4 v = *reinterpret_cast<const uint4*>(p + 8 * g);
+            w[0] = v.x; w[1] = v.y; w[2] = v.z; w[3] = v.w;
+        } else {
+            const uint2 a = *reinterpret_cast<const uint2*>(p + 4 * g), b = *reinterpret_cast<const uint2*>(p + 32 + 4 * g);
+            w[0] = a.x; w[1] = a.y; w[2] = b.x; w[3] = b.y;
+        }
+    }
+    __device__ __forceinline__ void turn(const float (&cs)[4], const float (&sn)[4]) {
+        if constexpr (INTER) {
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                const float2 x = bf16x2_bits_to_f32(w[i]);
+                w[i] = f32x2_to_bf16x2_bits(x.x * cs[i] - x.y * sn[i], x.x * sn[i] + x.y * cs[i]);
+            }
+        } else {
+#pragma unroll
+            for (int i = 0; i < 2; ++i) {
+                const float2 x = bf16x2_bits_to_f32(w[i]), y = bf16x2_bits_to_f32(w[i + 2]);
+                w[i] = f32x2_to_bf16x2_bits(x.x * cs[2 * i] - y.x * sn[2 * i], x.y * cs[2 * i + 1] - y.y * sn[2 * i + 1]);
+                w[i + 2] = f32x2_to_bf16x2_bits(x.x * sn[2 * i] + y.x * cs[2 * i], x.y * sn[2 * i + 1] + y.y * cs[2 * i + 1]);
+            }
+        }
+    }
+    __device__ __forceinline__ void store(uint16_t* p, int g) const {
+        if constexpr (INTER) {
+            *reinterpret_cast<uint4*>(p + 8 * g) = make_uint4(w[0], w[1], w[2], w[3]);
+        } else {
+            *reinterpret_cast<uint2*>(p + 4 * g) = make_uint2(w[0], w[1]);
+            *reinterpret_cast<uint2*>(p + 32 + 4 * g) = make_uint2(w[2], w[3]);
+        }
+    }
+};
+
+template <bool E4M3, bool INTER>
+__global__ void __launch_bounds__(kRopeThreads)
+kda_latent_append_rope_kernel(const RopeArgs a)
+{
+    const int lane = threadIdx.x & 31, g = lane & 7, sub = lane >> 3;
+    const long long unit = static_cast<long long>(blockIdx.x) * (kRopeThreads / 32) + (threadIdx.x >> 5);
+    const long long t = unit / a.split;
+    const int part = static_cast<int>(unit - t * a.split);
+    if (t >= a.T) return;
+    const int slot = a.slots[t], pos = a.pos[t];
+    const float f = a.freq[lane];
+    if (slot < 0) return;
+    if (slot >= a.num_rows) {
+        if (lane == 0 && part == 0) set_status(a.status, kStatusIndex);
+        return;
+    }
+    const uint64_t turns = rope_turns(f) * static_cast<uint64_t>(static_cast<long long>(pos));
+    float s, c;
+    sincospif(static_cast<float>(static_cast<int32_t>(turns >> 32)) * 0x1p-31f, &s, &c);
+    if (!(fabsf(f) < 0x1p32f)) s = c = __int_as_float(0x7fffffff);
+    float cs[4], sn[4];                          // of pairs 4 g .. 4 g + 3
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        cs[i] = __shfl_sync(0xffffffffu, c, 4 * g + i);
+        sn[i] = __shfl_sync(0xffffffffu, s, 4 * g + i);
+    }
+    if (part == 0) {
+        uint8_t* row = a.cache + static_cast<size_t>(slot) * lat_row_bytes(E4M3);
+        put_latents<E4M3>(row, reinterpret_cast<const uint4*>(a.c + t * a.ldc), lane);
+        if (sub == 0) {
+            RopePairs<INTER> x;
+            x.load(a.r + t * a.ldr, g);
+            x.turn(cs, sn);
+            x.store(reinterpret_cast<uint16_t*>(row + (E4M3 ? kLatDim : 2 * kLatDim)), g);
+        }
+    }
+    if (!a.q) return;
+    constexpr int U = 4;                         // heads in flight, a lane
+    for (int h0 = 4 * part + sub; h0 < a.H; h0 += 4 * a.split * U) {
+        RopePairs<INTER> x[U];
+#pragma unroll
+        for (int i = 0; i < U; ++i) {
+            const int h = h0 + 4 * a.split * i;
+            if (h < a.H) x[i].load(a.q + t * a.ldq + h * a.hdq, g);
+        }
+#pragma unroll
+        for (int i = 0; i < U; ++i) {
+            const int h = h0 + 4 * a.split * i;
+            if (h < a.H) {
+                x[i].turn(cs, sn);
+                x[i].store(a.q_out + t * a.ldo + h * a.hdo, g);
+            }
+        }
     }
 }
 
@@ -177,6 +312,27 @@ int launch_latent_gather(const void* cache, int e4m3, int num_pages, int page_si
     else
         kda_latent_gather_kernel<false><<<blocks, kCacheThreads, 0, stream>>>(p, num_pages, page_size, table, max_pages, start,
                                                                            cu, num_seqs, T, c, ldc, r, ldr, status);
+    return cudaGetLastError() == cudaSuccess ? 0 : -3;
+}
+
+int launch_latent_append_rope(const uint16_t* c, long long ldc, const uint16_t* r, long long ldr, void* cache, int e4m3,
+                              long long num_rows, const int32_t* slots, const int32_t* pos, const float* freq, int inter,
+                              const uint16_t* q, long long ldq, long long hdq, uint16_t* q_out, long long ldo, long long hdo,
+                              int T, int H, int* status, cudaStream_t stream)
+{
+    if (T == 0) return 0;
+    const int split = 1;
+    const RopeArgs a{c, ldc, r, ldr, static_cast<uint8_t*>(cache), num_rows, slots, pos, freq, q, ldq, hdq, q_out, ldo, hdo,
+                     T, q ? H : 0, split, status};
+    constexpr unsigned per = kRopeThreads / 32;
+    const unsigned blocks = static_cast<unsigned>((static_cast<long long>(T) * split + per - 1) / per);
+    if (e4m3) {
+        if (inter) kda_latent_append_rope_kernel<true, true><<<blocks, kRopeThreads, 0, stream>>>(a);
+        else kda_latent_append_rope_kernel<true, false><<<blocks, kRopeThreads, 0, stream>>>(a);
+    } else {
+        if (inter) kda_latent_append_rope_kernel<false, true><<<blocks, kRopeThreads, 0, stream>>>(a);
+        else kda_latent_append_rope_kernel<false, false><<<blocks, kRopeThreads, 0, stream>>>(a);
+    }
     return cudaGetLastError() == cudaSuccess ? 0 : -3;
 }
 

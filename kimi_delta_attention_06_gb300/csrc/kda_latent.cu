@@ -30,6 +30,7 @@
 #include <cuda.h>
 #include "latent.cuh"
 #include "tc.cuh"
+#include "tree.cuh"
 
 namespace kda {
 
@@ -54,12 +55,13 @@ struct LatWork {
     const int32_t* seq_lens;
     int N, G;                                   // G: most runs
     int lead;
+    int least;                                  // shortest length of a sequence that is not empty (a tree's K nodes)
     long long max_len;
 };
 
 __device__ __forceinline__ int lat_len(const LatWork& w, int n) {
     const int len = w.seq_lens[n];
-    return len < 0 || len > w.max_len ? 0 : len;
+    return len < w.least || len > w.max_len ? 0 : len;
 }
 __device__ __forceinline__ int lat_tiles(int len) { return (len + kTile - 1) / kTile; }
 __device__ __forceinline__ int lat_count(const LatWork& w, int len) { return len > 0 ? lat_tiles(len) + w.lead : 0; }   // with the lead
@@ -153,6 +155,7 @@ struct LatArgs {
     LatWork w;
     LatentCache ch;
     const uint16_t* q;
+    const int32_t* parents;                      // of a tree's nodes [N, K], else nullptr
     int K, H, rows, RT;                          // rows = K * H, RT row tiles
     int box;                                     // cache rows per TMA box (divides the page and the tile)
     float scale_log2;
@@ -189,7 +192,8 @@ struct LatShape {
     static constexpr uint32_t kTmemCols = kUsed <= 128u ? 128u : kUsed <= 256u ? 256u : 512u;
     static_assert(kUsed <= 512u, "TMEM");
 };
-static_assert(LatShape<64, false>::kBytes <= 232448 && LatShape<64, true>::kBytes <= 232448, "227 KB of shared memory");
+static_assert(LatShape<64, false>::kBytes + 64 * 8 <= 232448 && LatShape<64, true>::kBytes + 64 * 8 <= 232448,
+              "227 KB of shared memory");
 
 // A row's weights are exp2(x - m).  m follows the row's maximum M lazily: bf16, m <= M <= m + 8 (the
 // sums have the range for it); e4m3, m + 10 <= M <= m + 15, so that the weights times s fill e5m2's
@@ -263,19 +267,24 @@ __device__ __forceinline__ bool drop_nonfinite(uint8_t* c, int lo, int hi, int t
 
 // In O, the results of rows that see a NaN or infinite bf16 latent among the segment's tokens from `clear` on: NaN in
 // that channel (weight 0: 0 * inf; any other weight has made the sum NaN already).
-template <int R>
+// (Of a tree's nodes, the rows that see one of them: `seen`, else the rows that see past the first.)
+template <int R, bool TREE>
 __device__ __noinline__ void mark_nonfinite(const LatentCache& ch, int n, int clear, int from, int to, const int* s_j,
-                                            uint32_t ta, int channel) {
+                                            const uint64_t* seen, uint32_t ta, int channel) {
 #pragma unroll 1
     for (int b = 0; b < 4; ++b) {
         int first = 0x7fffffff;                                  // the first such token: rows that see past it
+        uint64_t nodes = 0;                                      // or all of them, as a tree's nodes
         for (int t = max(from, max(clear, 0)); t < to && first == 0x7fffffff; ++t) {
             int page = ch.table[static_cast<size_t>(n) * ch.max_pages + t / ch.page_size];
             if (page < 0 || page >= ch.num_pages) page = 0;     // (as it was copied)
             const uint8_t* row = ch.rows + (static_cast<size_t>(page) * ch.page_size + t % ch.page_size) * kLatRowBf16;
-            if ((reinterpret_cast<const uint16_t*>(row)[128 * b + channel] & 0x7f80u) == 0x7f80u) first = t;
+            if ((reinterpret_cast<const uint16_t*>(row)[128 * b + channel] & 0x7f80u) == 0x7f80u) {
+                if constexpr (TREE) nodes |= 1ull << (t - clear);
+                else first = t;
+            }
         }
-        if (!__any_sync(0xffffffffu, first != 0x7fffffff)) continue;
+        if (!__any_sync(0xffffffffu, TREE ? nodes != 0 : first != 0x7fffffff)) continue;
 #pragma unroll 1
         for (int c0 = 0; c0 < R; c0 += 16) {
             float o[16];
@@ -283,14 +292,14 @@ __device__ __noinline__ void mark_nonfinite(const LatentCache& ch, int n, int cl
             tc::tmem_wait_ld();
 #pragma unroll
             for (int i = 0; i < 16; ++i)
-                if (clear + s_j[c0 + i] > first) o[i] = __int_as_float(0x7fffffff);
+                if (TREE ? (seen[c0 + i] & nodes) != 0 : clear + s_j[c0 + i] > first) o[i] = __int_as_float(0x7fffffff);
             tc::tmem_st16(ta + b * R + c0, o);
         }
         tc::tmem_wait_st();
     }
 }
 
-template <int R, bool E4M3>
+template <int R, bool E4M3, bool TREE>
 __global__ void __launch_bounds__(LatShape<R, E4M3>::kThreads, 1)
 kda_latent_decode_kernel(const __grid_constant__ LatMaps maps, const LatArgs a)
 {
@@ -306,6 +315,7 @@ kda_latent_decode_kernel(const __grid_constant__ LatMaps maps, const LatArgs a)
     float* s_f = s_red + 4 * R;                                 // [R]
     int* s_j = reinterpret_cast<int*>(s_f + R);                 // [R]: query token of each row
     float* s_a = s_f + 2 * R;                                   // [R]: e4m3: 2^k * scale of each row
+    uint64_t* s_set = reinterpret_cast<uint64_t*>(s_a + R);     // [R]: TREE: the nodes that each row sees (none: no node itself)
     constexpr int NS = Sh::kStages;
 
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
@@ -353,8 +363,21 @@ kda_latent_decode_kernel(const __grid_constant__ LatMaps maps, const LatArgs a)
         while (ok && sw.next(a.w)) {
 #pragma unroll
             for (int i = 0; i < R / 4; ++i) { m[i] = -INFINITY; l[i] = 0.f; }
-            const int clear = sw.len - (a.K - 1);               // tokens that every row sees
+            const int clear = sw.len - (TREE ? a.K : a.K - 1);  // tokens that every row sees
             bool spoilt = false;                                // a later one held a NaN or infinity
+            if constexpr (TREE) {                               // (the last readers of the sets before are past a barrier)
+                if (warp == 0) {
+                    uint64_t set[2];
+                    if (tree_sets(a.parents + static_cast<long long>(sw.n) * a.K, a.K, lane, set) && lane == 0)
+                        set_status(a.status, kStatusIndex);
+#pragma unroll
+                    for (int r = lane; r < (R < 32 ? 32 : R); r += 32) {
+                        const uint64_t mine = tree_set_of(set, s_j[min(r, R - 1)]);
+                        if (r < R) s_set[r] = mine;
+                    }
+                }
+                tc::named_sync(kBarSoft, Sh::kSoft);
+            }
             if constexpr (E4M3) {
                 // Q of the segment (the last S product of the segment before has run): a warp a row, the
                 // loads of 4 rows in flight
@@ -444,8 +467,14 @@ kda_latent_decode_kernel(const __grid_constant__ LatMaps maps, const LatArgs a)
                 if (edge) {
 #pragma unroll
                     for (int i = 0; i < R / 2; ++i) {
-                        const int see = clear + s_j[8 * (i >> 2) + rq + (i & 1)];
-                        x[i] = tok + 4 * (i & 2) < see ? x[i] : -INFINITY;
+                        const int r = 8 * (i >> 2) + rq + (i & 1);
+                        if constexpr (TREE) {
+                            const int node = tok + 4 * (i & 2) - clear;
+                            x[i] = node < 0 || (node < a.K && s_set[r] >> node & 1) ? x[i] : -INFINITY;
+                        } else {
+                            const int see = clear + s_j[r];
+                            x[i] = tok + 4 * (i & 2) < see ? x[i] : -INFINITY;
+                        }
                     }
                     // rows past the end of the sequence hold anything: they enter the second product as zeros
                     const int valid = sw.len - t * kTile;
@@ -461,7 +490,7 @@ kda_latent_decode_kernel(const __grid_constant__ LatMaps maps, const LatArgs a)
                             if (16 * warp + tq + 8 >= valid) { s1 = 1.f; e1 = 0.f; }
                         }
                     }
-                    if (ok && a.K > 1)
+                    if (ok && (TREE || a.K > 1))
                         spoilt |= drop_nonfinite<R, E4M3>(sC + g % NS * Sh::kStage, max(0, clear - t * kTile), min(kTile, valid), tid);
                 }
                 bool grow = !ok;
@@ -585,12 +614,17 @@ kda_latent_decode_kernel(const __grid_constant__ LatMaps maps, const LatArgs a)
                 if (tid < 4) s_f[r] = m[i];
             }
             if (!tc::named_sync_and(kBarSoft, Sh::kSoft, !spoilt) && !E4M3)
-                mark_nonfinite<R>(a.ch, sw.n, clear, sw.t0 * kTile, min(sw.len, sw.t1 * kTile), s_j, tmO + lane_tm, 32 * warp + lane);
+                mark_nonfinite<R, TREE>(a.ch, sw.n, clear, sw.t0 * kTile, min(sw.len, sw.t1 * kTile), s_j, s_set, tmO + lane_tm,
+                                        32 * warp + lane);
             const bool whole = sw.whole();
             const long long row_at = static_cast<long long>(sw.n) * a.rows + row0;
             const size_t part = (static_cast<size_t>(run) * a.RT + rt) * 2 + (sw.first ? 0 : 1);
             if (tid < R) {                                       // a thread a row
-                const float mr = s_f[tid], sum = (s_red[tid] + s_red[R + tid]) + (s_red[2 * R + tid] + s_red[3 * R + tid]);
+                float mr = s_f[tid], sum = (s_red[tid] + s_red[R + tid]) + (s_red[2 * R + tid] + s_red[3 * R + tid]);
+                if (TREE && s_set[tid] == 0) {                   // no node: it has seen nothing
+                    mr = -INFINITY;
+                    sum = 0.f;
+                }
                 if (!whole) *reinterpret_cast<float2*>(a.part_ml + (part * R + tid) * 2) = make_float2(mr, sum);
                 else if (a.lse && tid < nrows) a.lse[row_at + tid] = (mr + log2f(sum)) * 0.69314718055994531f;
                 s_f[tid] = sum == 0.f ? 0.f : 1.f / sum;
@@ -623,7 +657,12 @@ kda_latent_decode_kernel(const __grid_constant__ LatMaps maps, const LatArgs a)
 #pragma unroll
                     for (int i = 0; i < 16; i += 2) {
                         const float2 f = *reinterpret_cast<const float2*>(s_f + c0 + i);
-                        const uint32_t w = f32x2_to_bf16x2_bits(o[i] * f.x, o[i + 1] * f.y);
+                        float y0 = o[i] * f.x, y1 = o[i + 1] * f.y;
+                        if constexpr (TREE) {                    // (a place without a node may hold anything)
+                            y0 = f.x == 0.f ? 0.f : y0;
+                            y1 = f.y == 0.f ? 0.f : y1;
+                        }
+                        const uint32_t w = f32x2_to_bf16x2_bits(y0, y1);
                         const uint32_t got = __shfl_xor_sync(0xffffffffu, w, 1);
                         if (c0 + i + odd < nrows) *reinterpret_cast<uint32_t*>(d + i * kLatDim) = __byte_perm(w, got, sel);
                     }
@@ -816,7 +855,7 @@ kda_latent_combine_kernel(const LatArgs a, int Q, int NG)
     for (int i = tid; i < a.w.N; i += threads) {
         const int raw = a.w.seq_lens[i];
         const int tiles = lat_tiles(lat_len(a.w, i));
-        if (i == n && row == 0 && (raw < 0 || raw > a.w.max_len)) set_status(a.status, kStatusIndex);
+        if (i == n && row == 0 && raw != lat_len(a.w, i)) set_status(a.status, kStatusIndex);   // out of range: counted as 0
         T += tiles > 0 ? tiles + a.w.lead : 0;
         if (i < n) before += tiles > 0 ? tiles + a.w.lead : 0;
     }
@@ -1036,13 +1075,14 @@ int sm_count() {
     return count[dev];
 }
 
-template <int R, bool E4M3>
+template <int R, bool E4M3, bool TREE>
 int launch_decode_shape(const LatMaps& maps, const LatArgs& a, cudaStream_t stream) {
     using Sh = LatShape<R, E4M3>;
+    constexpr uint32_t bytes = Sh::kBytes + (TREE ? R * 8u : 0u);
     static bool attr_done[kMaxDevicesAttr] = {};
-    if (!raise_smem_limit(reinterpret_cast<const void*>(kda_latent_decode_kernel<R, E4M3>), static_cast<int>(Sh::kBytes), attr_done))
+    if (!raise_smem_limit(reinterpret_cast<const void*>(kda_latent_decode_kernel<R, E4M3, TREE>), static_cast<int>(bytes), attr_done))
         return -3;
-    kda_latent_decode_kernel<R, E4M3><<<static_cast<unsigned>(a.w.G) * a.RT, Sh::kThreads, Sh::kBytes, stream>>>(maps, a);
+    kda_latent_decode_kernel<R, E4M3, TREE><<<static_cast<unsigned>(a.w.G) * a.RT, Sh::kThreads, bytes, stream>>>(maps, a);
     if (cudaGetLastError() != cudaSuccess) return -3;
     cudaLaunchConfig_t cfg = {};
     // a row's partials number about G / N + 1: few of them (many sequences), a warp a row; else
@@ -1066,6 +1106,14 @@ int launch_decode_shape(const LatMaps& maps, const LatArgs& a, cudaStream_t stre
     return cudaLaunchKernelEx(&cfg, kda_latent_combine_kernel<R>, a, Q, NG) == cudaSuccess ? 0 : -3;
 }
 
+template <bool TREE>
+int launch_decode_rows(int R, int e4m3, const LatMaps& maps, const LatArgs& a, cudaStream_t stream) {
+    if (e4m3) return R == 16 ? launch_decode_shape<16, true, TREE>(maps, a, stream)
+                   : R == 32 ? launch_decode_shape<32, true, TREE>(maps, a, stream) : launch_decode_shape<64, true, TREE>(maps, a, stream);
+    return R == 16 ? launch_decode_shape<16, false, TREE>(maps, a, stream)
+         : R == 32 ? launch_decode_shape<32, false, TREE>(maps, a, stream) : launch_decode_shape<64, false, TREE>(maps, a, stream);
+}
+
 // Rows a CTA takes: 16, 32 or 64.
 int rows_per_cta(int rows) { return rows <= 16 ? 16 : rows <= 32 ? 32 : 64; }
 }  // namespace
@@ -1082,16 +1130,18 @@ size_t latent_decode_scratch(int rows) {
 }
 
 int launch_latent_decode(const uint16_t* q, const void* cache, int e4m3, int num_pages, int page_size,
-                         const int32_t* table, int max_pages, const int32_t* seq_lens, int N, int K, int H,
-                         float sm_scale, uint16_t* out, float* lse, void* scratch, int* status, cudaStream_t stream)
+                         const int32_t* table, int max_pages, const int32_t* seq_lens, const int32_t* parents, int N, int K,
+                         int H, float sm_scale, uint16_t* out, float* lse, void* scratch, int* status, cudaStream_t stream)
 {
     LatArgs a = {};
     const int rows = K * H, R = rows_per_cta(rows);
     // (a segment's start and end in tiles: the best of 1, 2, 3, 4, 6 and of 4, 6, 8, 10, where Q is split too)
-    a.w = LatWork{seq_lens, N, latent_decode_runs(rows), N == 1 ? 0 : e4m3 && R == 64 ? 8 : 2, static_cast<long long>(max_pages) * page_size};
+    a.w = LatWork{seq_lens, N, latent_decode_runs(rows), N == 1 ? 0 : e4m3 && R == 64 ? 8 : 2, parents ? K : 0,
+                  static_cast<long long>(max_pages) * page_size};
     if (a.w.G <= 0) return -3;
     a.ch = LatentCache{static_cast<const uint8_t*>(cache), table, num_pages, page_size, max_pages};
     a.q = q;
+    a.parents = parents;
     a.K = K;
     a.H = H;
     a.rows = rows;
@@ -1119,10 +1169,7 @@ int launch_latent_decode(const uint16_t* q, const void* cache, int e4m3, int num
          !map_2d(&maps.s, CU_TENSOR_MAP_DATA_TYPE_UINT8, cache, slots, kLatRowE4m3, kLatRowE4m3, 16, a.box,
                  CU_TENSOR_MAP_SWIZZLE_NONE)))
         return -3;
-    if (e4m3) return R == 16 ? launch_decode_shape<16, true>(maps, a, stream)
-                   : R == 32 ? launch_decode_shape<32, true>(maps, a, stream) : launch_decode_shape<64, true>(maps, a, stream);
-    return R == 16 ? launch_decode_shape<16, false>(maps, a, stream)
-         : R == 32 ? launch_decode_shape<32, false>(maps, a, stream) : launch_decode_shape<64, false>(maps, a, stream);
+    return parents ? launch_decode_rows<true>(R, e4m3, maps, a, stream) : launch_decode_rows<false>(R, e4m3, maps, a, stream);
 }
 
 }  // namespace kda

@@ -4,12 +4,13 @@ The functions named like the C entry points (``kda_chunk_prefill``,
 ``kda_chunk_prefill_ex``, ``kda_chunk_prefill_noalloc``, ``kda_decode_step``,
 ``kda_prepare_inputs``, ``kda_output_norm``, ``kda_decode_multi``, ``kda_ckpt_count``,
 ``kda_latent_append``, ``kda_latent_gather``, ``kda_latent_decode``, ``kda_latent_prefill``, ``kda_verify_draft``,
+``kda_latent_append_rope``, ``kda_latent_decode_tree``, ``kda_decode_tree``, ``kda_token_logprobs``,
 ``kda_device_status``, ``kda_status_string``, ``kda_chunk_size``) only marshal
 arguments: torch
 tensors become raw device pointers, the current torch stream becomes the
 ``stream`` argument, and a negative status raises ``KdaError``.  ``prefill``,
-``decode_step``, ``latent_gather``, ``latent_decode``, ``latent_prefill`` and ``verify_draft``
-additionally allocate the output tensors with torch (a call with ``stream=`` from that stream's memory).
+``decode_step``, ``latent_gather``, ``latent_decode``, ``latent_prefill``, ``verify_draft``, ``latent_append_rope``,
+``latent_decode_tree``, ``decode_tree`` and ``token_logprobs`` additionally allocate the output tensors with torch (a call with ``stream=`` from that stream's memory).
 
 There is no fallback: if ``libkda.so`` is missing or cannot be loaded the
 first call raises.
@@ -49,6 +50,8 @@ KDA_LATENT_MAX_PAGE = 1024
 KDA_LATENT_MAX_ROWS = 512
 KDA_LATENT_MAX_TOKENS = 2**31 - 4096
 KDA_VERIFY_MAX_DRAFT = 64
+KDA_TREE_MAX_NODES = 64
+KDA_LOGPROBS_MAX_TOP = 32
 
 _vp = ctypes.c_void_p
 _i = ctypes.c_int
@@ -118,6 +121,15 @@ def load():
                                                _i, _i, _i, _i, _i, _f, _vp, _vp, _vp]
             lib.kda_verify_draft.restype = _i
             lib.kda_verify_draft.argtypes = [_vp, _i64, _vp, _i64, _vp, _vp, _vp, _vp, _i, _i, _i, _vp, _vp, _vp]
+            lib.kda_latent_append_rope.restype = _i
+            lib.kda_latent_append_rope.argtypes = [_vp, _i64, _vp, _i64, _vp, _i, _i, _i, _vp, _vp, _vp, _i,
+                                                   _vp, _i64, _i64, _vp, _i64, _i64, _i, _i, _vp]
+            lib.kda_latent_decode_tree.restype = _i
+            lib.kda_latent_decode_tree.argtypes = [_vp, _vp, _i, _i, _i, _vp, _i, _vp, _vp, _i, _i, _i, _f, _vp, _vp, _vp]
+            lib.kda_decode_tree.restype = _i
+            lib.kda_decode_tree.argtypes = [_vp, _vp, _vp, _vp, _vp, _vp, _i, _vp, _vp, _vp, _i, _i, _i, _i, _i, _i, _i, _vp]
+            lib.kda_token_logprobs.restype = _i
+            lib.kda_token_logprobs.argtypes = [_vp, _i, _i64, _vp, _i, _i, _i, _f, _vp, _vp, _vp, _vp, _vp, _vp]
             lib.kda_ckpt_count.restype = ctypes.c_int64
             lib.kda_ckpt_count.argtypes = [_vp, _i, _i]
             lib.kda_ckpt_count_ex.restype = ctypes.c_int64
@@ -520,7 +532,8 @@ def _latent_gather(cache, cache_dtype, block_table, start_pos, cu_seqlens, cu_ho
     return c, k_rope
 
 
-def _latent_decode(q, cache, cache_dtype, block_table, seq_lens, N, K, H, sm_scale, out, lse, stream, make=False, want_lse=False):
+def _latent_decode(q, cache, cache_dtype, block_table, seq_lens, N, K, H, sm_scale, out, lse, stream, make=False, want_lse=False,
+                   parents=None, tree=False):
     qp = _dense(q, _BF16, N * K * H * 576, "q")
     if q.size(-1) != 576:
         _short("q", q, "[N, K, H, 576] (the absorbed query, then its position part)")
@@ -529,6 +542,9 @@ def _latent_decode(q, cache, cache_dtype, block_table, seq_lens, N, K, H, sm_sca
     if len(table) != 2 or table[0] < N:
         _short("block_table", block_table, f"[{N}, max_pages]")
     sp = _dense(seq_lens, _I32, N, "seq_lens")
+    if tree:
+        np_ = _dense(parents, _I32, N * K, "parents")
+        _on_gpu(parents)
     _on_gpu(q, cache, block_table, seq_lens)
     if make:
         dev, side = q.device, _side(stream)
@@ -537,11 +553,83 @@ def _latent_decode(q, cache, cache_dtype, block_table, seq_lens, N, K, H, sm_sca
         op, lp = out.data_ptr(), lse.data_ptr() if want_lse else None
     else:
         op, lp = _out(out, _BF16, N * K * H * KDA_LATENT_DIM, "out"), _out(lse, _F32, N * K * H, "lse")
-    rc = load().kda_latent_decode(qp, p, cache_dtype, num_pages, page_size, tp, table[1], sp, N, K, H, sm_scale, op, lp,
-                                  _stream(stream))
+    if tree:
+        rc = load().kda_latent_decode_tree(qp, p, cache_dtype, num_pages, page_size, tp, table[1], sp, np_, N, K, H, sm_scale, op,
+                                           lp, _stream(stream))
+    else:
+        rc = load().kda_latent_decode(qp, p, cache_dtype, num_pages, page_size, tp, table[1], sp, N, K, H, sm_scale, op, lp,
+                                      _stream(stream))
     if rc:
-        _check(rc, "kda_latent_decode")
+        _check(rc, "kda_latent_decode_tree" if tree else "kda_latent_decode")
     return out, lse
+
+
+def _rope_heads(t, T: int, H: int, what: str):
+    """(address, token and head stride) of the position parts [T, H, 64] of heads."""
+    return _rows3(t, _BF16, T, H, KDA_LATENT_ROPE, KDA_LATENT_ROPE, what)
+
+
+def _latent_append_rope(c, k_rope, cache, cache_dtype, slots, positions, inv_freq, interleaved, q, q_out, total_tokens, H,
+                        stream, make=False):
+    cp, ldc = _rows2(c, _BF16, total_tokens, KDA_LATENT_DIM, "c")
+    rp, ldr = _rows2(k_rope, _BF16, total_tokens, KDA_LATENT_ROPE, "k_rope")
+    p, num_pages, page_size = _pages(cache, cache_dtype)
+    sp, pp = _dense(slots, _I32, total_tokens, "slots"), _dense(positions, _I32, total_tokens, "positions")
+    fp = _dense(inv_freq, _F32, KDA_LATENT_ROPE // 2, "inv_freq")
+    qp, ldq, hdq = (None, 0, 0) if q is None else _rope_heads(q, total_tokens, H, "q")
+    op, ldo, hdo = (None, 0, 0) if q_out is None else _rope_heads(q_out, total_tokens, H, "q_out")
+    _on_gpu(c, k_rope, cache, slots, positions, inv_freq, q, q_out)
+    if make and q is not None and q_out is None:
+        q_out = _empty((total_tokens, H, KDA_LATENT_ROPE), q.device, _BF16, _side(stream))
+        op, ldo, hdo = q_out.data_ptr(), H * KDA_LATENT_ROPE, KDA_LATENT_ROPE
+    rc = load().kda_latent_append_rope(cp, ldc, rp, ldr, p, cache_dtype, num_pages, page_size, sp, pp, fp, interleaved, qp, ldq,
+                                       hdq, op, ldo, hdo, total_tokens, H, _stream(stream))
+    if rc:
+        _check(rc, "kda_latent_append_rope")
+    return q_out
+
+
+def _decode_tree(q, k, v, log_alpha, beta, state_pool, num_slots, state_slots, parents, out, out_dtype, N, K, H, Dk, Dv, decay,
+                 stream, make=False):
+    tok = N * K * H
+    qp, kp = _dense(q, _BF16, tok * Dk, "q"), _dense(k, _BF16, tok * Dk, "k")
+    vp, bp = _dense(v, _BF16, tok * Dv, "v"), _dense(beta, _BF16, tok, "beta")
+    lp = _dense(log_alpha, _F32, tok * Dk if decay == KDA_DECAY_CHANNEL else tok if decay == KDA_DECAY_HEAD else 0, "log_alpha")
+    sp, ip = _dense(state_pool, _F32, num_slots * H * Dk * Dv, "state_pool"), _dense(state_slots, _I32, N, "state_slots")
+    np_ = _dense(parents, _I32, N * K, "parents")
+    _on_gpu(q, k, v, log_alpha, beta, state_pool, state_slots, parents)
+    if make:
+        out = _empty((N, K, H, Dv), q.device, _F32 if out_dtype == KDA_OUT_F32 else _BF16, _side(stream))
+        op = out.data_ptr()
+    else:
+        op = _out(out, _F32 if out_dtype == KDA_OUT_F32 else _BF16, tok * Dv, "out")
+    rc = load().kda_decode_tree(qp, kp, vp, lp, bp, sp, num_slots, ip, np_, op, out_dtype, N, K, H, Dk, Dv, decay, _stream(stream))
+    if rc:
+        _check(rc, "kda_decode_tree")
+    return out
+
+
+def _token_logprobs(logits, tokens, R, V, top, scale, logprob, rank, entropy, top_logprob, top_token, stream, make=False):
+    dtype = logits.dtype
+    if dtype is not _BF16 and dtype is not _F32:
+        raise TypeError(f"logits: expected a bfloat16 or float32 tensor, got {dtype}")
+    xp, ld = _rows2(logits, dtype, R, V, "logits")
+    tp = _dense(tokens, _I32, R, "tokens")
+    _on_gpu(logits, tokens)
+    if make:
+        dev, side = logits.device, _side(stream)
+        if tokens is not None:
+            logprob, rank = _empty((R,), dev, _F32, side), _empty((R,), dev, _I32, side)
+        entropy = _empty((R,), dev, _F32, side)
+        if top > 0:
+            top_logprob, top_token = _empty((R, top), dev, _F32, side), _empty((R, top), dev, _I32, side)
+    lp, kp, ep = _out(logprob, _F32, R, "logprob"), _out(rank, _I32, R, "rank"), _out(entropy, _F32, R, "entropy")
+    vp, ip = _out(top_logprob, _F32, R * top, "top_logprob"), _out(top_token, _I32, R * top, "top_token")
+    rc = load().kda_token_logprobs(xp, KDA_OUT_F32 if dtype is _F32 else KDA_OUT_BF16, ld, tp, R, V, top, scale, lp, kp, ep, vp,
+                                   ip, _stream(stream))
+    if rc:
+        _check(rc, "kda_token_logprobs")
+    return logprob, rank, entropy, top_logprob, top_token
 
 
 def _latent_prefill(q, k, v, k_rope, cu_q, cq, cu_k, ck, num_seqs, total_q, total_k, H, causal, sm_scale, out, lse, stream,
@@ -625,6 +713,27 @@ def kda_verify_draft(target_probs, draft_probs, draft_tokens, num_draft, u_accep
                      tokens, num_tokens, stream=None):
     _verify_draft(target_probs, draft_probs, draft_tokens, num_draft, u_accept, u_sample, N, K, V, tokens, num_tokens,
                   stream)
+
+
+def kda_latent_append_rope(c, k_rope, cache, cache_dtype: int, slots, positions, inv_freq, interleaved: int, q, q_out,
+                           total_tokens: int, H: int, stream=None):
+    _latent_append_rope(c, k_rope, cache, cache_dtype, slots, positions, inv_freq, interleaved, q, q_out, total_tokens, H, stream)
+
+
+def kda_latent_decode_tree(q, cache, cache_dtype: int, block_table, seq_lens, parents, N: int, K: int, H: int, sm_scale: float,
+                           out, lse, stream=None):
+    _latent_decode(q, cache, cache_dtype, block_table, seq_lens, N, K, H, sm_scale, out, lse, stream, parents=parents, tree=True)
+
+
+def kda_decode_tree(q, k, v, log_alpha, beta, state_pool, num_slots: int, state_slots, parents, out, out_dtype: int, N: int,
+                    K: int, H: int, Dk: int, Dv: int, decay: int = KDA_DECAY_CHANNEL, stream=None):
+    _decode_tree(q, k, v, log_alpha, beta, state_pool, num_slots, state_slots, parents, out, out_dtype, N, K, H, Dk, Dv, decay,
+                 stream)
+
+
+def kda_token_logprobs(logits, tokens, R: int, V: int, top: int, scale: float, logprob, rank, entropy, top_logprob, top_token,
+                       stream=None):
+    _token_logprobs(logits, tokens, R, V, top, scale, logprob, rank, entropy, top_logprob, top_token, stream)
 
 
 def kda_debug_expire_wait(limit_ns: int, stream=None):
@@ -735,3 +844,40 @@ def verify_draft(target_probs, draft_probs, draft_tokens, u_accept, u_sample, nu
         _short("draft_tokens, u_accept", draft_tokens, f"[{N}, {K1 - 1}]")
     return _verify_draft(target_probs, draft_probs, draft_tokens, num_draft, u_accept, u_sample, N, K1 - 1, V, None, None, stream,
                          make=True)
+
+
+def latent_append_rope(c, k_rope, cache, cache_dtype: int, slots, positions, inv_freq, q=None, q_out=None,
+                       interleaved: bool = False, stream=None):
+    """latent_append with k_rope [T, 64], and the position parts q [T, H, 64] of the queries where given, rotated by
+    ``positions`` [T] times ``inv_freq`` [32].  Returns the rotated parts: ``q_out`` where given (it may be ``q``), else a
+    new tensor [T, H, 64] (rows of skipped tokens unset), or None without q."""
+    if q is None and q_out is not None:
+        raise ValueError("q_out: there is no q")
+    return _latent_append_rope(c, k_rope, cache, cache_dtype, slots, positions, inv_freq, int(interleaved), q, q_out, c.shape[0],
+                               0 if q is None else q.shape[1], stream, make=True)
+
+
+def latent_decode_tree(q, cache, cache_dtype: int, block_table, seq_lens, parents, sm_scale: float, want_lse: bool = False,
+                       stream=None):
+    """Absorbed latent attention of the nodes q [N, K, H, 576] of a tree a sequence, parents [N, K], whose rows are the last K
+    of the cache; returns (out [N, K, H, 512] bf16, lse [N, K, H] fp32 or None)."""
+    N, K, H, _ = q.shape
+    return _latent_decode(q, cache, cache_dtype, block_table, seq_lens, N, K, H, sm_scale, None, None, stream, True, want_lse,
+                          parents, True)
+
+
+def decode_tree(q, k, v, log_alpha, beta, state_pool, parents, state_slots=None, out_dtype=torch.bfloat16,
+                decay: int = KDA_DECAY_CHANNEL, stream=None):
+    """KDA outputs [N, K, H, D] of the nodes of a tree a sequence, parents [N, K], from the states state_pool
+    [slots, H, D, D], which stay as they are."""
+    N, K, H, Dk = q.shape
+    return _decode_tree(q, k, v, log_alpha, beta, state_pool, state_pool.shape[0], state_slots, parents, None,
+                        KDA_OUT_F32 if out_dtype == torch.float32 else KDA_OUT_BF16, N, K, H, Dk, v.shape[3], decay, stream,
+                        make=True)
+
+
+def token_logprobs(logits, tokens=None, top: int = 0, scale: float = 1.0, stream=None):
+    """Of each row of logits [R, V] (bf16 or fp32) times ``scale``: returns (logprob [R], rank [R] int32 of tokens [R], or None
+    without tokens; entropy [R]; top_logprob [R, top], top_token [R, top] int32 of the most likely tokens, or None)."""
+    R, V = logits.shape
+    return _token_logprobs(logits, tokens, R, V, top, scale, None, None, None, None, None, stream, make=True)
