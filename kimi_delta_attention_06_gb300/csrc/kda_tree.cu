@@ -73,6 +73,7 @@ __device__ __forceinline__ void tree_mma(uint32_t d, uint32_t a, uint64_t b, uin
         "tcgen05.mma.cta_group::1.kind::tf32 [%0], [%1], %2, %3, p;\n\t}\n"
         :: "r"(d), "r"(a), "l"(b), "r"(id), "r"(acc));
 }
+template <int V> struct TreeInt { static constexpr int value = V; };
 // The leading 11 bits of x; x less these is exact.
 __device__ __forceinline__ float tree_lead(float x) { return __uint_as_float(__float_as_uint(x) & 0xffffe000u); }
 
@@ -215,26 +216,43 @@ kda_tree_kernel(const TreeArgs a)
                 query[c] = on ? bf16_bits_to_f32(s_query[e * D + lane * C + c]) : 0.f;
                 p[c] = 1.f;
             }
-            while (left) {
-                const int b = 63 - __clzll(left), eb = it * KP + b;
-                left &= ~(1ull << b);
-                float m = 0.f, w = 0.f;
+            while (left) {                                      // 4 nodes of the path at a time
+                float v[8];                                     // their products with the key, then with the query
+                int b4[4];
 #pragma unroll
-                for (int c = 0; c < C; ++c) {
-                    const float kb = p[c] * bf16_bits_to_f32(s_key[eb * D + lane * C + c]);
-                    m = fmaf(key[c], kb, m);
-                    w = fmaf(query[c], kb, w);
-                    p[c] *= s_alpha[eb * D + lane * C + c];
-                }
+                for (int z = 0; z < 4; ++z) {
+                    const bool on = left != 0;
+                    const int b = on ? 63 - __clzll(left) : 0, eb = it * KP + b;
+                    left &= ~(1ull << b);
+                    b4[z] = on ? b : -1;
+                    v[z] = v[z + 4] = 0.f;
 #pragma unroll
-                for (int off = 16; off > 0; off >>= 1) {
-                    m += __shfl_xor_sync(0xffffffffu, m, off);
-                    w += __shfl_xor_sync(0xffffffffu, w, off);
+                    for (int c = 0; c < C; ++c) {
+                        const float kb = p[c] * bf16_bits_to_f32(s_key[eb * D + lane * C + c]);
+                        v[z] = fmaf(key[c], kb, v[z]);
+                        v[z + 4] = fmaf(query[c], kb, v[z + 4]);
+                        const float al = s_alpha[eb * D + lane * C + c];
+                        p[c] = on ? p[c] * al : p[c];
+                    }
                 }
-                if (lane == 0) {
-                    s_m[(it * KP + i) * KP + b] = m;
-                    s_n[(it * KP + i) * KP + b] = w;
-                }
+                // 8 sums over the lanes, halved from step to step: lane l has sum l / 4 in the end
+                auto halve = [&](int off, int count) {
+                    const bool up = (lane & off) != 0;
+#pragma unroll
+                    for (int z = 0; z < 4; ++z)
+                        if (z < count) {
+                            const float give = up ? v[z] : v[z + count];
+                            v[z] = (up ? v[z + count] : v[z]) + __shfl_xor_sync(0xffffffffu, give, off);
+                        }
+                };
+                halve(16, 4);
+                halve(8, 2);
+                halve(4, 1);
+                v[0] += __shfl_xor_sync(0xffffffffu, v[0], 2);
+                v[0] += __shfl_xor_sync(0xffffffffu, v[0], 1);
+                const int z = lane >> 2 & 3;
+                const int b = z == 0 ? b4[0] : z == 1 ? b4[1] : z == 2 ? b4[2] : b4[3];
+                if ((lane & 3) == 0 && b >= 0) (lane < 16 ? s_m : s_n)[(it * KP + i) * KP + b] = v[0];
             }
             const uint32_t rk = it * 2 * KC + r, rq = rk + KC;
             float kl[C], kr[C], ql[C], qr[C];
@@ -321,53 +339,106 @@ kda_tree_kernel(const TreeArgs a)
     auto rows_at = [&](int i, int query) {                              // TMEM columns of nodes i .. i + 7
         return lane_tm + Sh::kD + (i / KC) * Sh::kRows + item * 2 * KC + query * KC + i % KC;
     };
-    if (group == 0) {
+    // x - sum of row[b] u[b] over the nodes of `on`: up to 16 places from registers, whose u do not wait for shared memory
+    // (a place that is not on the path is left out, not multiplied by zero: it may hold anything); else 4 of the path at
+    // a time, their loads together
+    constexpr bool kRegs = KP <= 16;
+    float ur[kRegs ? KP : 1];
+    auto along = [&](float x, const float* row, uint64_t on, auto upto, float sign) {
+        if constexpr (kRegs) {
+            constexpr int n4 = (decltype(upto)::value + 3) / 4;
+            const uint32_t bits = static_cast<uint32_t>(on);
+            float4 m[n4 > 0 ? n4 : 1];
 #pragma unroll
-        for (int i0 = 0; i0 < KP; i0 += 8) {
-            if (i0 >= a.K) break;
-            float P[8];
-            tree_tmem_ld8(rows_at(i0, 0), P);
+            for (int q = 0; q < n4; ++q) m[q] = reinterpret_cast<const float4*>(row)[q];
+            float y = 0.f;
 #pragma unroll
-            for (int r = 0; r < 8; ++r) {
-                const int i = i0 + r;
-                const uint64_t on = set[i];
-                if (on == 0) continue;
-                float x = bf16_bits_to_f32(s_value[(item * KP + i) * D + col]) - P[r];
-                for (uint64_t left = on & ~(1ull << i); left;) {
-                    const int b = 63 - __clzll(left);
-                    left &= ~(1ull << b);
-                    x = fmaf(-M[i * KP + b], u[b * D], x);
-                }
-                u[i * D] = beta[i] * x;
+            for (int q = 0; q < n4; ++q) {
+                if (bits >> (4 * q) & 1) x = fmaf(sign * m[q].x, ur[4 * q], x);
+                if (bits >> (4 * q + 1) & 1) y = fmaf(sign * m[q].y, ur[4 * q + 1], y);
+                if (bits >> (4 * q + 2) & 1) x = fmaf(sign * m[q].z, ur[4 * q + 2], x);
+                if (bits >> (4 * q + 3) & 1) y = fmaf(sign * m[q].w, ur[4 * q + 3], y);
             }
-        }
-    }
-    __syncthreads();
-    // 6. the outputs, 8 nodes a group in turn
+            return x + y;
+        } else {
+            while (on) {
+                int b4[4];
+                float m[4], w[4];
 #pragma unroll
-    for (int i0 = 0; i0 < KP; i0 += 8) {
-        if (i0 >= a.K) break;
-        if (KP > 8 && (i0 / 8 & 1) != group) continue;
-        if (KP == 8 && group == 1) break;
+                for (int z = 0; z < 4; ++z) {
+                    b4[z] = on ? 63 - __clzll(on) : -1;
+                    if (on) on &= ~(1ull << b4[z]);
+                }
+#pragma unroll
+                for (int z = 0; z < 4; ++z) {
+                    m[z] = row[max(b4[z], 0)];
+                    w[z] = u[max(b4[z], 0) * D];
+                }
+#pragma unroll
+                for (int z = 0; z < 4; ++z)
+                    if (b4[z] >= 0) x = fmaf(sign * m[z], w[z], x);
+            }
+            return x;
+        }
+    };
+    // a step for every place 0 .. KP - 1, unrolled where u is in registers
+    auto nodes8 = [&](auto i0, auto&& use) {
+        constexpr int z = decltype(i0)::value;
+        use(TreeInt<z>{}, 0); use(TreeInt<z + 1>{}, 1); use(TreeInt<z + 2>{}, 2); use(TreeInt<z + 3>{}, 3);
+        use(TreeInt<z + 4>{}, 4); use(TreeInt<z + 5>{}, 5); use(TreeInt<z + 6>{}, 6); use(TreeInt<z + 7>{}, 7);
+    };
+    auto solve = [&](auto z0, int i0) {                                 // u of places i0 .. i0 + 7 (z0: the same, if unrolled)
+        float P[8];
+        tree_tmem_ld8(rows_at(i0, 0), P);
+        nodes8(z0, [&](auto z, int r) {
+            const int i = i0 + r;
+            const uint64_t on = set[i];
+            float x = 0.f;
+            if (on) {
+                x = bf16_bits_to_f32(s_value[(item * KP + i) * D + col]) - P[r];
+                x = beta[i] * along(x, M + i * KP, on & ~(1ull << i), z, -1.f);
+                u[i * D] = x;
+            }
+            if constexpr (kRegs) ur[decltype(z)::value] = x;
+        });
+    };
+    auto answer = [&](auto z0, int i0) {                                // outputs of places i0 .. i0 + 7
         float P[8];
         tree_tmem_ld8(rows_at(i0, 1), P);
-#pragma unroll
-        for (int r = 0; r < 8; ++r) {
+        nodes8(z0, [&](auto z, int r) {
             const int i = i0 + r;
-            if (i >= a.K) break;
             const uint64_t on = set[i];
-            float o = on ? P[r] : 0.f;
-            for (uint64_t left = on; left;) {
-                const int b = 63 - __clzll(left);
-                left &= ~(1ull << b);
-                o = fmaf(Nn[i * KP + b], u[b * D], o);
-            }
-            if (good && ok) {
+            float o = 0.f;
+            if (on) o = along(P[r], Nn + i * KP, on, TreeInt<decltype(z)::value + 1>{}, 1.f);
+            if (good && ok && i < a.K) {
                 const size_t to = ((static_cast<size_t>(n) * a.K + i) * a.H + h) * D + col;
                 if (a.out_f32) reinterpret_cast<float*>(a.out)[to] = o;
                 else reinterpret_cast<uint16_t*>(a.out)[to] = f32_to_bf16_bits(o);
             }
+        });
+    };
+    if (group == 0) {
+        if constexpr (kRegs) {
+            solve(TreeInt<0>{}, 0);
+            if constexpr (KP > 8) solve(TreeInt<8>{}, 8);
+        } else {
+#pragma unroll 1
+            for (int i0 = 0; i0 < a.K; i0 += 8) solve(TreeInt<0>{}, i0);
         }
+    }
+    __syncthreads();
+    // 6. the outputs: the first places (whose paths are short) by the group that has u at hand
+    if constexpr (kRegs) {
+        if (group == 0) {
+            answer(TreeInt<0>{}, 0);
+        } else if constexpr (KP > 8) {
+#pragma unroll
+            for (int i = 0; i < KP; ++i) ur[i] = u[i * D];              // (unset where there is no node: not used)
+            answer(TreeInt<8>{}, 8);
+        }
+    } else {
+#pragma unroll 1
+        for (int i0 = 8 * group; i0 < a.K; i0 += 16) answer(TreeInt<0>{}, i0);
     }
     if (!ok) set_status(a.status, kStatusTimeout);
     tc::fence_before_sync();

@@ -14,6 +14,11 @@
       (absorbed latent attention of K tokens of N sequences of T cached tokens each, pages of 64)
   python -m kimi_delta_attention_06_gb300.run_case --what latent_prefill --T 8192 [--H 32]
   python -m kimi_delta_attention_06_gb300.run_case --what verify --N 256 --K 4 [--vocab 131072]
+  python -m kimi_delta_attention_06_gb300.run_case --what latent_append_rope --T 32768 [--H 32] [--cache e4m3]
+  python -m kimi_delta_attention_06_gb300.run_case --what latent_decode_tree --N 16 --T 16384 --K 8 [--H 32] [--cache bf16]
+  python -m kimi_delta_attention_06_gb300.run_case --what decode_tree --N 256 --K 16 [--H 32] [--D 128] [--decay head]
+      (trees of K nodes, each node's parent one of the 4 before it)
+  python -m kimi_delta_attention_06_gb300.run_case --what logprobs --N 256 [--vocab 131072] [--top 20] [--logits bf16]
 
 Inputs are the seeded synthetic tensors of workloads.py, generated on the GPU
 (varlen: 16 packed sequences of log-uniform length, about 280k tokens).
@@ -45,8 +50,26 @@ def latent_case(a, dev, stream):
         cud = cu.to(dev)
         return (lambda: kda.latent_prefill(q, kv[..., :128], kv[..., 128:], r, cu, cu, 192 ** -0.5, cu_q=cud, cu_k=cud,
                                            stream=stream)), f"{a.T} tokens x {a.H} heads, causal", a.T
+    if a.what == "logprobs":
+        x = torch.randn(a.N, a.vocab, generator=g, device=dev).mul_(2.0).to(torch.bfloat16 if a.logits == "bf16" else torch.float32)
+        t = torch.randint(0, a.vocab, (a.N,), generator=g, device=dev).to(torch.int32)
+        return (lambda: kda.token_logprobs(x, t, top=a.top, stream=stream)), \
+            f"{a.N} rows of {a.vocab} {a.logits} logits ({x.numel() * x.element_size() / 1e9:.3f} GB), {a.top} alternatives", a.N
+    # a tree a sequence: each node hangs on one of the 4 before it
+    j = torch.arange(a.K, device=dev)
+    back = 1 + torch.randint(0, 4, (a.N, a.K), generator=g, device=dev)
+    parents = torch.where(j == 0, -1, (j - back).clamp_min(0)).to(torch.int32)
+    if a.what == "decode_tree":
+        d = workloads.decode_case(N=a.N, H=a.H, D=a.D, steps=a.K, seed=4, device=dev)
+        x = [torch.stack([s[k] for s in d.steps], dim=1).contiguous() for k in ("q", "k", "v", "log_alpha", "beta")]
+        pool = d.state
+        decay = {"channel": kda.KDA_DECAY_CHANNEL, "head": kda.KDA_DECAY_HEAD, "none": kda.KDA_DECAY_NONE}[a.decay]
+        if a.decay != "channel":
+            x[3] = x[3][..., 0].contiguous() if a.decay == "head" else None
+        return (lambda: kda.decode_tree(*x, pool, parents, decay=decay, stream=stream)), \
+            f"{a.N} sequences x {a.K} nodes x {a.H} heads of {a.D} ({pool.numel() * 4 / 1e9:.3f} GB of states)", a.N * a.K
     dt = kda.KDA_CACHE_E4M3 if a.cache == "e4m3" else kda.KDA_CACHE_BF16
-    n = a.N if a.what == "latent_decode" else 1
+    n = a.N if a.what in ("latent_decode", "latent_decode_tree") else 1
     per = -(-a.T // 64)
     table = torch.randperm(n * per, generator=g, device=dev).to(torch.int32).view(n, per)
     cache = kda.latent_cache(n * per, 64, dt, device=dev)
@@ -55,6 +78,12 @@ def latent_case(a, dev, stream):
     c, r = rn(a.T, 512), rn(a.T, 64)
     for i in range(n):
         kda.latent_append(c, r, cache, dt, slots[i], stream=stream)
+    if a.what == "latent_append_rope":
+        q = rn(a.T, a.H, 192)[..., 128:]
+        pos, freq = t.to(torch.int32) + 100000, (1e4 ** (-torch.arange(32, device=dev) / 32.0)).float()
+        out = torch.empty(a.T, a.H, 64, dtype=torch.bfloat16, device=dev)
+        return (lambda: kda.latent_append_rope(c, r, cache, dt, slots[0], pos, freq, q=q, q_out=out, stream=stream)), \
+            f"{a.T} tokens, {a.H} heads, {a.cache}", a.T
     if a.what == "latent_append":
         return (lambda: kda.latent_append(c, r, cache, dt, slots[0], stream=stream)), f"{a.T} tokens, {a.cache}", a.T
     if a.what == "latent_gather":
@@ -63,6 +92,9 @@ def latent_case(a, dev, stream):
         return (lambda: kda.latent_gather(cache, dt, table, cu, cu_seqlens=cud, stream=stream)), f"{a.T} tokens, {a.cache}", a.T
     q = rn(n, a.K, a.H, 576)
     lens = torch.full((n,), a.T, dtype=torch.int32, device=dev)
+    if a.what == "latent_decode_tree":
+        return (lambda: kda.latent_decode_tree(q, cache, dt, table, lens, parents, 192 ** -0.5, stream=stream)), \
+            f"{n} sequences of {a.T} cached tokens ({n * a.T * cache.shape[2] / 1e9:.3f} GB), trees of {a.K} x {a.H} rows, {a.cache}", n * a.K
     return (lambda: kda.latent_decode(q, cache, dt, table, lens, 192 ** -0.5, stream=stream)), \
         f"{n} sequences of {a.T} cached tokens ({n * a.T * cache.shape[2] / 1e9:.3f} GB), {a.K} x {a.H} rows, {a.cache}", n * a.K
 
@@ -70,10 +102,13 @@ def latent_case(a, dev, stream):
 def main(argv=None):
     ap = argparse.ArgumentParser()
     ap.add_argument("--what", choices=["prefill", "varlen", "decode", "decode_multi", "prep", "outnorm", "latent_append",
-                                       "latent_gather", "latent_decode", "latent_prefill", "verify"],
+                                       "latent_gather", "latent_decode", "latent_prefill", "verify", "latent_append_rope",
+                                       "latent_decode_tree", "decode_tree", "logprobs"],
                     default="prefill")
     ap.add_argument("--cache", choices=["bf16", "e4m3"], default="e4m3", help="latent cache rows")
-    ap.add_argument("--vocab", type=int, default=131072, help="verify: vocabulary size")
+    ap.add_argument("--vocab", type=int, default=131072, help="verify, logprobs: vocabulary size")
+    ap.add_argument("--top", type=int, default=20, help="logprobs: alternatives a row")
+    ap.add_argument("--logits", choices=["bf16", "f32"], default="bf16", help="logprobs: type of the logits")
     ap.add_argument("--K", type=int, default=4, help="tokens per sequence (decode_multi, latent_decode), drafts (verify)")
     ap.add_argument("--commit", type=int, default=0, help="decode_multi: 1 writes the states back")
     ap.add_argument("--decay", choices=["channel", "head", "none"], default="channel",
@@ -145,7 +180,7 @@ def main(argv=None):
                 kda.kda_output_norm(o, kda.KDA_OUT_BF16, gam, 1e-6, y, T, H, D, stream)
             nbytes = T * H * D * 2 * 2
         units, count = f"{T} tokens x {H} heads ({nbytes / 1e9:.3f} GB moved)", T
-    elif a.what.startswith("latent") or a.what == "verify":
+    elif a.what.startswith("latent") or a.what in ("verify", "decode_tree", "logprobs"):
         run, units, count = latent_case(a, dev, stream)
     elif a.what == "decode_multi":
         d = workloads.decode_case(N=a.N, H=a.H, D=a.D, steps=a.K, seed=4, device=dev)
