@@ -13,8 +13,7 @@
 // where W is K x K numbers a head, a row of which a warp finds by substitution along the node's path.
 //
 // The product P^T [128 columns x 2 K] = S_0^T [128 x D] rows^T [D x 2 K] runs on the tensor cores with S_0^T in TMEM (its
-// lanes are the state's columns, so a warp's loads of a state's row are 128 contiguous bytes and nothing passes through
-// shared memory), as three tf32 products of the operands' leading 11 bits and what is left of them: 22 bits, an fp32
+// lanes are the state's columns, a thread's a column), as three tf32 products of the operands' leading 11 bits and what is left of them: 22 bits, an fp32
 // product but for 2^-21.  So do L and N, as products of the decayed rows with the keys over their decays (CTAs in which a
 // decay leaves 2^-100 .. 2^100 walk their paths instead), and W (V - P), with V - P in TMEM in S_0^T's place (a NaN
 // or an infinity in it enters as 0, and is put back for the nodes whose paths hold it: 0 * NaN is none).
@@ -33,48 +32,56 @@ struct TreeArgs {
     const float* pool;
     const int32_t *slots, *parents;
     void* out;
-    int num_slots, out_f32, N, K, H, decay;
+    int num_slots, out_f32, N, K, H, decay, sms;
     int* status;
 };
 
-// A CTA takes 128 columns: one head's state of 128 x 128, or two of 64 x 64 (items).  Nodes go through the product
+// A turn of a CTA is 128 columns: one head's state of 128 x 128, or two of 64 x 64 (items).  Nodes go through the product
 // in chunks of at most 32, so that their rows fit beside the rest.
 template <int D, int KP>
 struct TreeShape {
-    static constexpr int kThreads = 256, kItems = 128 / D;
-    static constexpr int KC = KP < 32 ? KP : 32, kChunks = KP / KC;
-    static constexpr int kRows = kItems * 2 * KC;                       // N of a product: per item the keys, then the queries
-    static constexpr int kSlabs = D / 32;                               // 32 channels: 128 bytes of a row of fp32
-    static constexpr uint32_t kTile = kRows * 128u * kSlabs;            // one term of the rows
-    static constexpr bool kWhole = kChunks > 1 || D == 64;              // S_0 stays in TMEM (else a quarter at a time, in turns)
-    static constexpr int kBufs = kWhole ? kSlabs : 2;                   // buffers of 32 channels (leading bits, the rest)
+    static constexpr int kItems = 128 / D, kNodes = kItems * KP;
+    static constexpr int KC = KP < 32 ? KP : KP == 64 && D == 64 ? 16 : 32, kChunks = KP / KC;
+    static constexpr int kSlabs = D / 32;                               // 32 channels: 128 bytes of a row of fp32, a quarter or half of S_0
+    // The rows' two terms lie one after the other per item, so that one product serves both, up to 32 places; beyond,
+    // a tile a term.  kRows: rows of a slab; kItem: rows (and accumulators) of an item; kRest: from a row to its second term
+    static constexpr bool kStack = KP <= 32;
+    static constexpr int kItem = (kStack ? 4 : 2) * KC, kRows = kItems * kItem;
+    static constexpr uint32_t kTile = kRows * 128u * kSlabs, kRest = kStack ? 2 * KC * 128u : kTile, kTiles = kStack ? kTile : 2 * kTile;
+    // the keys over their decays: 8 rows and their second terms in turn, or a tile a term
+    static constexpr int kSideItem = (kStack ? 2 : 1) * KP, kSideRows = kItems * kSideItem;
+    static constexpr uint32_t kSide = kSideRows * 128u * kSlabs, kSides = kStack ? kSide : 2 * kSide;
+    // CTAs an SM, slabs of S_0 that are on their way in shared memory (each group its own), and in TMEM (all of them
+    // where it is used twice)
+    static constexpr int kCtas = KP <= 16 ? 2 : 1, kRing = KP == 32 ? 4 : 2;
+    static constexpr bool kWhole = kChunks > 1;
+    static constexpr int kBufs = kWhole ? kSlabs : 2;
     static constexpr uint32_t kD = kBufs * 64u;                         // TMEM column of the accumulators
     // L and N have accumulators of their own where there is room, else those of the product, before it
-    static constexpr uint32_t kProduct = kD + kChunks * kRows;
-    static constexpr bool kApart = kProduct + kChunks * kRows <= (kProduct <= 256u ? 256u : 512u);
-    static constexpr uint32_t kL = kApart ? kProduct : kD;
-    static constexpr uint32_t kUsed = kL + kChunks * kRows;
-    static constexpr uint32_t kCols = kUsed <= 256u ? 256u : 512u;
-    static_assert(kUsed <= 512u && 2 * KP <= kD, "TMEM");
-    static constexpr int kNodes = kItems * KP;
-    static constexpr uint32_t kSide = kNodes * 128u * kSlabs;           // one term of the keys over their decays
+    static constexpr uint32_t kProduct = kD + kChunks * kRows, kMost = 512u / kCtas;
+    static constexpr bool kApart = kProduct + kChunks * kRows <= kMost;
+    static constexpr uint32_t kL = kApart ? kProduct : kD, kUsed = kL + kChunks * kRows;
+    static constexpr uint32_t kCols = kUsed <= 128u ? 128u : kUsed <= 256u ? 256u : 512u;
+    static_assert(kCols <= kMost && 2 * KP <= kD, "TMEM");
+    static_assert(kApart || kBufs == kSlabs, "the first products do not wait for what follows the last slab");
     // bytes of shared memory.  (The side's products read 64 rows from each item's first: what follows it, beyond KP)
-    static constexpr uint32_t oSide = 0, oRows = oSide + 2 * kSide, oDecay = oRows + 2 * kTile;
-    static constexpr uint32_t oM = kChunks > 1 ? oDecay + kNodes * D * 4u : oDecay;        // (one chunk: the decays are done with)
-    static constexpr uint32_t kMN = kItems * KP * KP * 4u, oN = oM + kMN;
-    static constexpr uint32_t oLog = oRows;                             // log alphas as they arrive
-    // W [place][32 places a slab] in two terms, in the side's place; V in the decays'
+    static constexpr uint32_t oSide = 0, oRows = oSide + kSides, oState = oRows + kTiles;
+    static constexpr uint32_t oM = oState + kRing * 16384u, kMN = kItems * KP * KP * 4u, oN = oM + kMN, oV = oN + kMN;
+    // W [place][32 places a slab] in two terms, in the side's place
     static constexpr int kWRows = KP < 16 ? 16 : KP, kWSlabs = KP > 32 ? 2 : 1;
     static constexpr uint32_t kW = kItems * kWRows * 128u * kWSlabs, oW = oSide;
-    static constexpr bool kVSide = oM == oDecay && 2 * kMN + kNodes * D * 2u > kNodes * D * 4u;
-    static constexpr uint32_t oV = kVSide ? oW + 2 * kW : oM == oDecay ? oDecay + 2 * kMN : oDecay;
-    static_assert(2 * kW + (kVSide ? kNodes * D * 2u : 0u) <= 2 * kSide, "W in the side's place");
-    static_assert(kNodes * D * 4u <= 2 * kTile, "log alphas in the rows' place");
-    static constexpr uint32_t kPast = oN + kMN > oDecay + kNodes * D * 4u ? oN + kMN : oDecay + kNodes * D * 4u;
-    static constexpr uint32_t oSet = kPast, oBeta = oSet + kNodes * 8u, oBar = oBeta + kNodes * 4u;
-    static constexpr uint32_t kBytes = oBar + 64u;
-    static_assert(kBytes <= 232448u && (kCols > 256u || kBytes <= 115712u), "227 KB of shared memory, or 113");
-    static_assert(oRows + 2 * kTile >= oSide + 2 * kSide + 8192u, "the side's last products stay within");
+    static_assert(2 * kW <= kSides, "W in the side's place");
+    // a thread's share of the rows: CH channels of one place, or of two; lanes of a warp go over places
+    static constexpr int kLanes = KP < 32 ? KP : 32, kPlaces = KP / kLanes, kG = 32 / kLanes, CH = 16 / kG;
+    static constexpr uint32_t kBit = KP > 32 ? 8u : 4u;                 // bytes of a set
+    static constexpr uint32_t oNone = oRows;                            // of 256 threads: places that are no number
+    static constexpr int kRounds = KP == 8 ? 3 : KP == 16 ? 4 : KP == 32 ? 5 : 6;      // of the decays' products, doubling their reach
+    static constexpr uint32_t oSet = oV + kNodes * D * 2u, oBeta = oSet + 2 * kNodes * kBit, oUp = oBeta + 2 * kNodes * 2u;
+    static constexpr uint32_t oFar = oUp + 2 * kNodes, oBar = oFar + 2 * kRounds * kNodes;
+    static constexpr uint32_t kBytes = oBar + 224u;
+    static_assert(kBytes <= (kCtas == 1 ? 232448u : kCtas == 2 ? 115712u : 76800u), "shared memory");
+    static_assert(oState >= oSide + kSides + 8192u, "the side's last products stay within");
+    static_assert(256u * kBit <= kTiles && D % CH == 0, "none; channels");
 };
 
 __device__ __forceinline__ void tree_tmem_ld8(uint32_t ta, float (&r)[8]) {
@@ -111,7 +118,6 @@ __device__ __forceinline__ void tree_copy4(uint32_t dst, const void* src) {
     asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" :: "r"(dst), "l"(src) : "memory");
 }
 __device__ __forceinline__ void tree_copies_done() { asm volatile("cp.async.wait_all;" ::: "memory"); }
-template <int V> struct TreeInt { static constexpr int value = V; };
 // The leading 11 bits of x; x less these is exact.
 __device__ __forceinline__ float tree_lead(float x) { return __uint_as_float(__float_as_uint(x) & 0xffffe000u); }
 
@@ -119,496 +125,686 @@ template <bool WIDE> struct TreeBits { using type = uint32_t; };
 template <> struct TreeBits<true> { using type = uint64_t; };
 __device__ __forceinline__ int tree_top(uint32_t x) { return 31 - __clz(x); }
 __device__ __forceinline__ int tree_top(uint64_t x) { return 63 - __clzll(x); }
+__device__ __forceinline__ float tree_rcp(float x) {                    // to within a step, of a normal number
+    float y;
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
 
+constexpr int kTreeThreads = 320;                // 8 warps that work, one that issues products, one that brings the state
+constexpr uint32_t kTreeAll = 1;                 // named barrier of the 8 warps
+
+// 8 warps in two groups of 4, each a whole set of TMEM's lanes (a thread a column of the state).
+//   1  the state's first slabs into TMEM      2  decays along the paths, rows into shared memory      3  the other slabs, as they come
+//   4  L and N out of TMEM                    5  W                                  6  V - P into TMEM            7  outputs
+// The inputs of the next turn are on their way from 3 on; the state's next slabs, and the rest of it into L2, always.
 template <int D, int KP>
-__global__ void __launch_bounds__(256, TreeShape<D, KP>::kCols <= 256u ? 2 : 1)
+__global__ void __launch_bounds__(kTreeThreads, TreeShape<D, KP>::kCtas)
 kda_tree_kernel(const TreeArgs a)
 {
     using Sh = TreeShape<D, KP>;
     using Set = typename TreeBits<(KP > 32)>::type;                     // a path: bit b is place b
-    constexpr int KC = Sh::KC, kItems = Sh::kItems, G = D / 64;
+    constexpr int KC = Sh::KC, kItems = Sh::kItems, G = D / 64, kSlabs = Sh::kSlabs, kRing = Sh::kRing, kBufs = Sh::kBufs;
+    constexpr int kChunks = Sh::kChunks;
     constexpr Set kOne = 1;
     extern __shared__ __align__(1024) uint8_t sm[];
-    float* s_decay = reinterpret_cast<float*>(sm + Sh::oDecay);         // [place][channel]: products of alphas from the root
     float* s_m = reinterpret_cast<float*>(sm + Sh::oM);
-    float* s_n = reinterpret_cast<float*>(sm + Sh::oN);                 // N, then W
-    uint64_t* s_set = reinterpret_cast<uint64_t*>(sm + Sh::oSet);
-    float* s_beta = reinterpret_cast<float*>(sm + Sh::oBeta);
-    uint64_t* bars = reinterpret_cast<uint64_t*>(sm + Sh::oBar);        // [0..1] a buffer's products are done, [2] all are, [3..4] a buffer is written, [5] L's and N's, [6] W's
-    uint32_t* s_tmem = reinterpret_cast<uint32_t*>(bars + 7);
+    float* s_n = reinterpret_cast<float*>(sm + Sh::oN);
+    Set* s_sets = reinterpret_cast<Set*>(sm + Sh::oSet);                // [2][place]: of this turn and the next
+    uint16_t* s_betas = reinterpret_cast<uint16_t*>(sm + Sh::oBeta);    // [2][place]
+    int8_t* s_ups = reinterpret_cast<int8_t*>(sm + Sh::oUp);            // [2][place]: of the parent, -1 without one, -2 without a node
+    int8_t* s_fars = reinterpret_cast<int8_t*>(sm + Sh::oFar);          // [2][round][place]: the ancestor 2^round up, -1 without one
+    uint64_t* bars = reinterpret_cast<uint64_t*>(sm + Sh::oBar);
+    uint64_t *b_full = bars, *b_empty = bars + 4;                       // a slab is in shared memory; has been read
+    uint64_t *b_put = bars + 8, *b_free = bars + 12;                    // is in TMEM; its products are done
+    uint64_t *b_rows = bars + 16, *b_side = bars + 17, *b_read = bars + 18;    // the rows are written; L and N are done; have been read
+    uint64_t *b_prod = bars + 19, *b_e = bars + 20, *b_w = bars + 21;   // the product is done; V - P is in TMEM; W (V - P) is done
+    // everything is; the trees of even and odd turns are there; such a turn is done.  (Of each barrier, the side that completes
+    // a phase waits for the side that waits on it before it can complete the next)
+    uint64_t *b_last = bars + 22, *b_tree = bars + 14, *b_done = bars + 24;
+    uint32_t* s_tmem = reinterpret_cast<uint32_t*>(bars + 23);
+    int* s_walk = reinterpret_cast<int*>(bars + 26);                    // [2]: of even and odd turns
 
-    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, group = warp >> 2;
-    const uint32_t heads = static_cast<uint32_t>(a.N) * a.H, first = blockIdx.x * static_cast<uint32_t>(kItems);
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     if (tid == 0) {
-        tc::mbar_init(&bars[0], 1);
-        tc::mbar_init(&bars[1], 1);
-        tc::mbar_init(&bars[2], 1);
-        tc::mbar_init(&bars[3], 128);
-        tc::mbar_init(&bars[4], 128);
-        tc::mbar_init(&bars[5], 1);
-        tc::mbar_init(&bars[6], 1);
-        tc::mbar_fence_init();
-    }
-    if (warp == 7) tc::tmem_alloc(s_tmem, Sh::kCols);
-    // the items' sequence and head (past the last: the last again)
-    int seq[kItems], head[kItems];
-#pragma unroll
-    for (int i = 0; i < kItems; ++i) {
-        const uint32_t x = min(first + i, heads - 1);
-        seq[i] = static_cast<int>(x / static_cast<uint32_t>(a.H));
-        head[i] = static_cast<int>(x - static_cast<uint32_t>(seq[i]) * a.H);
-    }
-
-    const int column = 32 * (warp & 3) + lane, item = kItems == 1 ? 0 : column / D, col = column % D;
-    const bool there = first + item < heads;
-    const int n = kItems == 1 || item == 0 ? seq[0] : seq[kItems - 1], h = kItems == 1 || item == 0 ? head[0] : head[kItems - 1];
-    const int slot = a.slots ? a.slots[n] : n;
-    const bool good = there && slot >= 0 && slot < a.num_slots;
-    if (there && !good && col == 0 && group == 0) set_status(a.status, kStatusTree);
-    constexpr int kUnits = KC / 8, kPer = D / 4;                        // units a thread, units a node
-    uint2 kx[kUnits], qx[kUnits];
-    auto token = [&](int it, int j) {                                   // row of place j of an item in the inputs
-        return (static_cast<size_t>(it == 0 ? seq[0] : seq[kItems - 1]) * a.K + j) * a.H + (it == 0 ? head[0] : head[kItems - 1]);
-    };
-    auto fetch = [&](int chunk) {
-#pragma unroll
-        for (int z = 0; z < kUnits; ++z) {
-            const int f = (tid + 256 * z) / kPer, c = (tid + 256 * z) % kPer * 4, it = f / KC, j = chunk * KC + f % KC;
-            kx[z] = qx[z] = make_uint2(0u, 0u);
-            if (j < a.K) {
-                const size_t at = token(it, j) * D + c;
-                kx[z] = *reinterpret_cast<const uint2*>(a.k + at);
-                qx[z] = *reinterpret_cast<const uint2*>(a.q + at);
-            }
+        for (int i = 0; i < kRing; ++i) {
+            tc::mbar_init(&b_full[i], 1);
+            tc::mbar_init(&b_empty[i], 128);
         }
-    };
-    // 1. on their way, in this order, as what comes later waits for what came before: log alphas, keys and queries of the
-    // first chunk (units of 4 channels), the state (a column a thread, half of the channels a group)
-    for (int f = tid; f < (a.decay == 0 ? Sh::kNodes * kPer : a.decay == 1 ? Sh::kNodes : 0); f += 256) {
-        const int e = a.decay == 0 ? f / kPer : f, j = e % KP;
-        if (j >= a.K) continue;
-        if (a.decay == 0) tree_copy16(tc::smem_u32(sm) + Sh::oLog + f * 16, a.la + token(e / KP, j) * D + f % kPer * 4);
-        else tree_copy4(tc::smem_u32(sm) + Sh::oLog + f * 4, a.la + token(e / KP, j));
+        for (int i = 0; i < kBufs; ++i) {
+            tc::mbar_init(&b_put[i], 128);
+            if (!Sh::kWhole) tc::mbar_init(&b_free[i], 1);
+        }
+        for (int i = 0; i < 2; ++i) {
+            tc::mbar_init(&b_tree[i], 32);
+            tc::mbar_init(&b_done[i], 1);
+        }
+        tc::mbar_init(b_rows, 256);
+        tc::mbar_init(b_side, 1);
+        tc::mbar_init(b_read, 128);
+        tc::mbar_init(b_prod, 1);
+        tc::mbar_init(b_e, 256);
+        tc::mbar_init(b_w, 1);
+        tc::mbar_init(b_last, 1);
+        tc::mbar_fence_init();
+        s_walk[0] = s_walk[1] = 0;
     }
-    fetch(0);
-    const size_t tok0 = static_cast<size_t>(n) * a.K * a.H + h;         // this item's place 0 in the inputs
-    constexpr int kHalf = D / 2;
-    float s[kHalf];
-    {
-        const float* S = a.pool + ((good ? static_cast<size_t>(slot) : 0) * a.H + h) * D * D + group * kHalf * D + col;
-#pragma unroll
-        for (int k = 0; k < kHalf; ++k) s[k] = __ldcs(S + k * D);
-    }
-
-    // 2. the trees
-    if (warp < kItems) {
-        uint64_t set[2] = {0, 0};
-        if (first + warp < heads &&
-            tree_sets(a.parents + static_cast<long long>(warp == 0 ? seq[0] : seq[kItems - 1]) * a.K, a.K, lane, set) && lane == 0)
-            set_status(a.status, kStatusTree);
-        if (lane < KP) s_set[warp * KP + lane] = set[0];
-        if (lane + 32 < KP) s_set[warp * KP + lane + 32] = set[1];
-    } else if (warp >= 4 && tid - 128 < Sh::kNodes) {
-        const int e = tid - 128, j = e % KP;
-        s_beta[e] = j < a.K ? bf16_bits_to_f32(a.beta[token(e / KP, j)]) : 0.f;
-    }
-    tree_copies_done();
+    if (warp == 8) tc::tmem_alloc(s_tmem, Sh::kCols);
     tc::fence_before_sync();
     __syncthreads();
     tc::fence_after_sync();
-    const uint32_t tm = *s_tmem, lane_tm = tm + (static_cast<uint32_t>(32 * (warp & 3)) << 16);
+    const uint32_t tm = *s_tmem, sm0 = tc::smem_u32(sm);
+    const uint32_t heads = static_cast<uint32_t>(a.N) * a.H, stride = gridDim.x * static_cast<uint32_t>(kItems);
+    // what a turn works on: the items' sequence and head (past the last: the last again)
+    struct Turn {
+        uint32_t first;
+        int seq[kItems], head[kItems];
+        __device__ __forceinline__ Turn(uint32_t f, uint32_t heads, int H) : first(f) {
+#pragma unroll
+            for (int i = 0; i < kItems; ++i) {
+                const uint32_t x = min(first + i, heads - 1);
+                seq[i] = static_cast<int>(x / static_cast<uint32_t>(H));
+                head[i] = static_cast<int>(x - static_cast<uint32_t>(seq[i]) * H);
+            }
+        }
+        __device__ __forceinline__ int n(int it) const { return kItems == 1 || it == 0 ? seq[0] : seq[kItems - 1]; }
+        __device__ __forceinline__ int h(int it) const { return kItems == 1 || it == 0 ? head[0] : head[kItems - 1]; }
+        // row of place j of an item in the inputs
+        __device__ __forceinline__ size_t token(int it, int j, int K, int H) const { return (static_cast<size_t>(n(it)) * K + j) * H + h(it); }
+    };
+    auto slot_of = [&](const Turn& w, int it) {                         // -1: none to read
+        const int slot = a.slots ? a.slots[w.n(it)] : w.n(it);
+        return w.first + it < heads && slot >= 0 && slot < a.num_slots ? slot : -1;
+    };
     bool ok = true;
-    // decays along the paths: a channel a thread, a node's its parent's times its alpha
-    bool far = false;                                                   // one has left the range whose inverse is at hand
-    if (group == 0) {
-        float* dec = s_decay + item * KP * D + col;
-        const float* la = reinterpret_cast<const float*>(sm + Sh::oLog);
+    const uint32_t begin = blockIdx.x * static_cast<uint32_t>(kItems);
+
+    if (warp == 9) {
+        // ---- the trees; the state: slabs of 32 channels through the ring; all inputs a turn ahead into L2 ----
+        uint32_t c = 0, turn = 0;                                       // slabs and turns so far
+        for (uint32_t first = begin; first < heads && ok; first += stride, ++turn) {
+            const Turn w(first, heads, a.H);
+            const float* S[kItems];
+#pragma unroll
+            for (int it = 0; it < kItems; ++it) {
+                const int slot = slot_of(w, it);
+                S[it] = a.pool + ((slot >= 0 ? static_cast<size_t>(slot) : 0) * a.H + w.h(it)) * D * D;
+            }
+            if (first + stride < heads) {
+                const Turn z(first + stride, heads, a.H);
+#pragma unroll
+                for (int it = 0; it < kItems; ++it) {
+                    if (const int slot = slot_of(z, it); slot >= 0 && lane == 0)
+                        asm volatile("cp.async.bulk.prefetch.L2.global [%0], %1;"
+                                     :: "l"(a.pool + (static_cast<size_t>(slot) * a.H + z.h(it)) * D * D), "r"(D * D * 4) : "memory");
+                    for (int j = lane; j < a.K; j += 32) {
+                        const size_t at = z.token(it, j, a.K, a.H) * D;
+#pragma unroll
+                        for (int x = 0; x < D * 2; x += 128) {
+                            asm volatile("prefetch.global.L2 [%0];" :: "l"(reinterpret_cast<const uint8_t*>(a.k + at) + x));
+                            asm volatile("prefetch.global.L2 [%0];" :: "l"(reinterpret_cast<const uint8_t*>(a.q + at) + x));
+                            asm volatile("prefetch.global.L2 [%0];" :: "l"(reinterpret_cast<const uint8_t*>(a.v + at) + x));
+                        }
+                        if (a.decay == 0)
+#pragma unroll
+                            for (int x = 0; x < D * 4; x += 128)
+                                asm volatile("prefetch.global.L2 [%0];" :: "l"(reinterpret_cast<const uint8_t*>(a.la + at) + x));
+                    }
+                }
+            }
+            // the trees, where the last turn's but one have been read
+            const uint32_t odd = turn & 1;
+            if (turn >= 2) ok = tc::mbar_wait_bounded(&b_done[odd], (turn / 2 - 1) & 1, kWaitLimitNs);
+            ok = __all_sync(0xffffffffu, ok);
+            if (!ok) break;
+            for (int i = lane; i < Sh::kNodes; i += 32) {
+                const int j = i % KP;
+                s_betas[odd * Sh::kNodes + i] = j < a.K ? a.beta[w.token(i / KP, j, a.K, a.H)] : 0;
+            }
 #pragma unroll 1
-        for (int j0 = 0; j0 < a.K; j0 += 8) {                           // (what does not depend on other nodes first)
-            float al[8];
-            int up[8];
-            bool on[8];
+            for (int it = 0; it < kItems; ++it) {
+                uint64_t set[2] = {0, 0};
+                if (first + it < heads && tree_sets(a.parents + static_cast<long long>(w.n(it)) * a.K, a.K, lane, set) && lane == 0)
+                    set_status(a.status, kStatusTree);
+                int up[2];
 #pragma unroll
-            for (int r = 0; r < 8; ++r) {
-                const int e = item * KP + j0 + r;
-                const Set set = static_cast<Set>(s_set[e]);
-                const Set above = set & ~(kOne << (j0 + r));
-                up[r] = above ? tree_top(above) : -1;
-                on[r] = set != 0;
-                al[r] = a.decay == 2 ? 1.f : expf(a.decay == 0 ? la[e * D + col] : la[e]);
-            }
-#pragma unroll
-            for (int r = 0; r < 8; ++r) {
-                const float x = up[r] >= 0 ? al[r] * dec[up[r] * D] : al[r];
-                dec[(j0 + r) * D] = x;
-                far |= on[r] && (x < 0x1p-100f || (x > 0x1p100f && x < INFINITY));
-            }
-        }
-    }
-    // (a key over such a decay would overflow: those CTAs walk their paths)
-    const bool walk = __syncthreads_or(far) != 0;
-
-    // S_0^T into TMEM: buffer b, 32 channels of this thread's half
-    auto put = [&](int b, auto from) {
-        uint32_t lead[32], rest[32];
-#pragma unroll
-        for (int i = 0; i < 32; ++i) {
-            const float x = s[decltype(from)::value + i], y = tree_lead(x);
-            lead[i] = __float_as_uint(y);
-            rest[i] = __float_as_uint(x - y);
-        }
-        tc::tmem_st32x(lane_tm + b * 64, lead);
-        tc::tmem_st32x(lane_tm + b * 64 + 32, rest);
-        tc::tmem_wait_st();
-        tc::fence_before_sync();
-    };
-    using Low = TreeInt<0>;
-    using High = TreeInt<(kHalf > 32 ? 32 : 0)>;
-    constexpr uint32_t id = tc::idesc(128, Sh::kRows, tc::kFmtTF32, false, false);
-    auto product = [&](int b, int slab, int chunk, bool start) {        // buffer b times the slab of its channels (one thread)
-        const uint32_t d = tm + Sh::kD + chunk * Sh::kRows, ta = tm + b * 64;
-        const uint32_t rows = tree_desc(tc::smem_u32(sm) + Sh::oRows + slab * (Sh::kRows * 128u));
-#pragma unroll
-        for (uint32_t k = 0; k < 4; ++k) {
-            tree_mma(d, ta + k * 8u, rows + k * 2u, id, start && k == 0 ? 0u : 1u);
-            tree_mma(d, ta + k * 8u, rows + Sh::kTile / 16u + k * 2u, id, 1u);
-            tree_mma(d, ta + 32u + k * 8u, rows + k * 2u, id, 1u);
-        }
-    };
-
-    // the keys over their decays (64 rows from an item's first) times the item's rows: L and N, transposed
-    constexpr uint32_t id_side = tc::idesc(64, 2 * KC, tc::kFmtTF32, false, false);
-    auto side = [&](int it, int chunk) {                                // (one thread; into the columns of the chunk's rows)
-        const uint32_t d = tm + Sh::kL + chunk * Sh::kRows + it * 2 * KC;
-        const uint32_t sa = tree_desc(tc::smem_u32(sm) + Sh::oSide + it * KP * 128u);
-        const uint32_t sb = tree_desc(tc::smem_u32(sm) + Sh::oRows + it * 2 * KC * 128u);
-#pragma unroll
-        for (uint32_t k = 0; k < Sh::kSlabs * 4u; ++k) {
-            const uint32_t pa = sa + (k >> 2) * (Sh::kNodes * 8u) + (k & 3) * 2u, pb = sb + (k >> 2) * (Sh::kRows * 8u) + (k & 3) * 2u;
-            tree_mma_ss(d, pa, pb, id_side, k > 0 ? 1u : 0u);
-            tree_mma_ss(d, pa, pb + Sh::kTile / 16u, id_side, 1u);
-            tree_mma_ss(d, pa + Sh::kSide / 16u, pb, id_side, 1u);
-        }
-    };
-    auto split = [&](uint32_t off, uint32_t term, float4 x) {           // four channels of a row in their two terms
-        const float4 lead = make_float4(tree_lead(x.x), tree_lead(x.y), tree_lead(x.z), tree_lead(x.w));
-        *reinterpret_cast<float4*>(sm + off) = lead;
-        *reinterpret_cast<float4*>(sm + off + term) = make_float4(x.x - lead.x, x.y - lead.y, x.z - lead.z, x.w - lead.w);
-    };
-
-    auto fetch_v = [&] {                                                // V, as the first operand's columns go: [place][column of the item]
-        for (int f = tid; f < Sh::kNodes * D / 8; f += 256) {
-            const int e = f / (D / 8), j = e % KP;
-            if (j < a.K) tree_copy16(tc::smem_u32(sm) + Sh::oV + f * 16, a.v + token(e / KP, j) * D + f % (D / 8) * 8);
-        }
-    };
-
+                for (int z = 0; z < 2; ++z) {
+                    const int j = lane + 32 * z;
+                    const uint64_t above = set[z] & ~(1ull << j);
+                    up[z] = above ? tree_top(above) : set[z] ? -1 : -2;
+                    if (j >= KP) continue;
+                    s_sets[(odd * kItems + it) * KP + j] = static_cast<Set>(set[z]);
+                    s_ups[(odd * kItems + it) * KP + j] = static_cast<int8_t>(up[z]);
+                }
+                int far[2] = {max(up[0], -1), max(up[1], -1)};
 #pragma unroll 1
-    for (int chunk = 0; chunk < Sh::kChunks; ++chunk) {
-        // 3. the rows: keys and queries times their decays, keys over them
-        if (chunk > 0) fetch(chunk);
+                for (int r = 0; r < Sh::kRounds; ++r) {
+                    int8_t* to = s_fars + ((odd * Sh::kRounds + r) * kItems + it) * KP;
+                    if (lane < KP) to[lane] = static_cast<int8_t>(far[0]);
+                    if (lane + 32 < KP) to[lane + 32] = static_cast<int8_t>(far[1]);
+                    int next[2];
 #pragma unroll
-        for (int z = 0; z < kUnits; ++z) {
-            const int f = (tid + 256 * z) / kPer, c = (tid + 256 * z) % kPer * 4, it = f / KC, r = f % KC, e = it * KP + chunk * KC + r;
-            const bool node = s_set[e] != 0;
-            const float2 k0 = bf16x2_bits_to_f32(kx[z].x), k1 = bf16x2_bits_to_f32(kx[z].y);
-            const float2 q0 = bf16x2_bits_to_f32(qx[z].x), q1 = bf16x2_bits_to_f32(qx[z].y);
-            const float4 p = *reinterpret_cast<const float4*>(s_decay + e * D + c);
-            const float4 none = make_float4(0.f, 0.f, 0.f, 0.f);
-            const uint32_t row = it * 2 * KC + r;
-            split(Sh::oRows + tc::sw128_off32(row, c, Sh::kRows), Sh::kTile,
-                  node ? make_float4(p.x * k0.x, p.y * k0.y, p.z * k1.x, p.w * k1.y) : none);
-            split(Sh::oRows + tc::sw128_off32(row + KC, c, Sh::kRows), Sh::kTile,
-                  node ? make_float4(p.x * q0.x, p.y * q0.y, p.z * q1.x, p.w * q1.y) : none);
-            split(Sh::oSide + tc::sw128_off32(e, c, Sh::kNodes), Sh::kSide,
-                  node ? make_float4(k0.x * __frcp_rn(p.x), k0.y * __frcp_rn(p.y), k1.x * __frcp_rn(p.z), k1.y * __frcp_rn(p.w)) : none);
-        }
-        tc::fence_smem_to_async();
-        if (chunk == 0) {
-            if constexpr (Sh::kWhole) {
-                put(group * (Sh::kSlabs / 2), Low{});
-                if constexpr (kHalf > 32) put(group * (Sh::kSlabs / 2) + 1, High{});
-            } else {
-                put(group, Low{});
+                    for (int z = 0; z < 2; ++z) {
+                        const int n0 = __shfl_sync(0xffffffffu, far[0], far[z] & 31), n1 = __shfl_sync(0xffffffffu, far[1], far[z] & 31);
+                        next[z] = far[z] >= 32 ? n1 : n0;
+                    }
+#pragma unroll
+                    for (int z = 0; z < 2; ++z) far[z] = far[z] >= 0 ? next[z] : -1;
+                }
             }
-        }
-        __syncthreads();
-        if (chunk + 1 == Sh::kChunks && !Sh::kVSide) fetch_v();         // (the decays are done with)
-        // 4. the products, L's and N's first where they share accumulators
-        auto sides = [&] {
-            if (!walk && warp == 4) {                                   // (beside warp 0, which issues the others)
-                tc::fence_after_sync();
-                if (tc::elect_one()) {
-                    for (int it = 0; it < kItems; ++it) side(it, chunk);
-                    tc::mma_commit(&bars[5]);
+            tc::mbar_arrive(&b_tree[odd]);
+            for (int q = 0; q < kSlabs && ok; ++q, ++c) {
+                const uint32_t at = c % kRing;
+                if (c >= kRing) ok = tc::mbar_wait_bounded(&b_empty[at], (c / kRing - 1) & 1, kWaitLimitNs);
+                ok = __all_sync(0xffffffffu, ok);
+                if (!ok) break;
+                if (lane == 0) {
+                    tc::mbar_arrive_expect_tx(&b_full[at], 16384u);
+#pragma unroll
+                    for (int it = 0; it < kItems; ++it)
+                        tc::bulk_load_g2s(sm0 + Sh::oState + at * 16384u + it * (16384u / kItems), S[it] + q * 32 * D, 16384u / kItems, &b_full[at]);
                 }
                 __syncwarp();
             }
-        };
-        auto paths = [&] {                                              // L and N into shared memory
-        if (!walk) {
-            if (group == 0) {
-                // row a of the product is lane a % 16 of warp a / 16
-                if (16 * warp < KP) {
-                    ok = tc::mbar_wait_bounded(&bars[5], chunk & 1, kWaitLimitNs) && ok;
-                    ok = __all_sync(0xffffffffu, ok);
-                    tc::fence_after_sync();
-                    const int b = 16 * warp + lane;
-#pragma unroll
-                    for (int it = 0; it < kItems; ++it)
-#pragma unroll
-                        for (int c0 = 0; c0 < 2 * KC; c0 += 8) {
-                            float x[8];
-                            tree_tmem_ld8(lane_tm + Sh::kL + chunk * Sh::kRows + it * 2 * KC + c0, x);
-                            float* to = (c0 < KC ? s_m : s_n) + (it * KP + chunk * KC + c0 % KC) * KP + b;
-                            if (lane < 16 && b < KP) {
-#pragma unroll
-                                for (int r = 0; r < 8; ++r) to[r * KP] = x[r];
-                            }
-                        }
-                    tc::fence_before_sync();
-                }
-                tc::named_sync(1, 128);
-            }
-        } else {
-            // half a warp a node, up its path; lane l of the 16: channels 4 l .. + 3 of each 64
-            const int hl = lane & 15;
-#pragma unroll 1
-            for (int f = 2 * warp + (lane >> 4); f < kItems * KC; f += 16) {
-                const int it = f / KC, i = chunk * KC + f % KC, e = it * KP + i;
-                Set left = static_cast<Set>(s_set[e]);
-                float key[4 * G], query[4 * G], p[4 * G];
-#pragma unroll
-                for (int c = 0; c < 4 * G; ++c) {
-                    const size_t at = token(it, left ? i : 0) * D + c / 4 * 64 + 4 * hl + c % 4;
-                    key[c] = bf16_bits_to_f32(a.k[at]);
-                    query[c] = bf16_bits_to_f32(a.q[at]);
-                    p[c] = 1.f;
-                }
-                while (__any_sync(0xffffffffu, left != 0)) {
-                    const bool on = left != 0;
-                    const int b = on ? tree_top(left) : 0;
-                    left &= ~(kOne << b);
-                    const size_t tok = token(it, b);
-                    float m = 0.f, w = 0.f;
-#pragma unroll
-                    for (int c = 0; c < 4 * G; ++c) {
-                        const size_t at = tok * D + c / 4 * 64 + 4 * hl + c % 4;
-                        const float kb = p[c] * bf16_bits_to_f32(a.k[at]);
-                        m = fmaf(key[c], kb, m);
-                        w = fmaf(query[c], kb, w);
-                        p[c] *= a.decay == 2 ? 1.f : expf(a.la[a.decay == 0 ? at : tok]);
-                    }
-#pragma unroll
-                    for (int off = 8; off > 0; off >>= 1) {
-                        m += __shfl_xor_sync(0xffffffffu, m, off);
-                        w += __shfl_xor_sync(0xffffffffu, w, off);
-                    }
-                    if (hl == 0 && on) {
-                        s_m[(it * KP + i) * KP + b] = m;
-                        s_n[(it * KP + i) * KP + b] = w;
-                    }
-                }
-            }
         }
-        };
-        if (warp == 0) tc::fence_after_sync();
-        sides();
-        if constexpr (!Sh::kApart) {
-            paths();
-            if (warp == 0) tc::fence_after_sync();
-        }
-        if (warp == 0) {
-            if (tc::elect_one()) {
-                if constexpr (Sh::kWhole) {
-                    for (int b = 0; b < Sh::kBufs; ++b) product(b, b, chunk, b == 0);
-                    tc::mma_commit(&bars[2]);
-                } else {
-                    product(0, 0, 0, true);
-                    tc::mma_commit(&bars[0]);
-                    product(1, 2, 0, false);
-                    tc::mma_commit(&bars[1]);
-                }
-            }
-            __syncwarp();
-        }
-        if constexpr (!Sh::kWhole) {
-            // the second quarters follow where the first have been read
-            ok = tc::mbar_wait_bounded(&bars[group], 0, kWaitLimitNs);
-            ok = __all_sync(0xffffffffu, ok);
-            if (ok) {
-                tc::fence_after_sync();
-                put(group, High{});
-            }
-            tc::mbar_arrive(&bars[3 + group]);
-            if (warp == 0) {
-                for (int b = 0; b < 2; ++b) {
-                    ok = tc::mbar_wait_bounded(&bars[3 + b], 0, kWaitLimitNs) && ok;
-                    ok = __all_sync(0xffffffffu, ok);
-                    tc::fence_after_sync();
-                    if (tc::elect_one()) {
-                        product(b, 1 + 2 * b, 0, false);
-                        if (b == 1) tc::mma_commit(&bars[2]);
-                    }
-                    __syncwarp();
-                }
-            }
-        }
-        if constexpr (Sh::kApart) paths();
-        if (chunk + 1 < Sh::kChunks) {                                  // the rows are written again
-            ok = tc::mbar_wait_bounded(&bars[2], chunk & 1, kWaitLimitNs) && ok;
-            ok = __all_sync(0xffffffffu, ok);
-            __syncthreads();
-        }
-    }
-
-    if constexpr (Sh::kVSide) {                                         // (the side is done with)
-        if (!walk) {
-            ok = tc::mbar_wait_bounded(&bars[5], (Sh::kChunks - 1) & 1, kWaitLimitNs) && ok;
-            ok = __all_sync(0xffffffffu, ok);
-        }
-        fetch_v();
-    }
-    __syncthreads();
-    // 5. W while the products run: a warp a row, lane b place b (and b + 32): w_c is final once the places above c are done.
-    // Zeros where the path does not lead
-    constexpr int kLanes = KP < 32 ? KP : 32, kP = KP > 32 ? 2 : 1;     // lanes a row, places a lane
-#pragma unroll 1
-    for (int e = warp * (32 / kLanes) + lane / kLanes; e < Sh::kNodes; e += 8 * (32 / kLanes)) {
-        const int it = e / KP, i = e % KP, mine = lane % kLanes;
-        const Set on = static_cast<Set>(s_set[e]);
-        float w[kP];
-        float* row = s_n + (it * KP + i) * KP;
-        const float* L = s_m + it * KP * KP + mine;
-        const float* beta = s_beta + it * KP;
-#pragma unroll
-        for (int z = 0; z < kP; ++z) w[z] = on >> (mine + 32 * z) & 1 ? row[mine + 32 * z] : 0.f;
-        // (nothing is below a path's first node)
-        for (Set left = on; __any_sync(0xffffffffu, (left & (left - 1)) != 0);) {
-            int c4[4];
-            Set below[4];
-            float b4[4], m4[4][kP];
-#pragma unroll
-            for (int y = 0; y < 4; ++y) {                               // 4 places of the path, their loads together
-                c4[y] = left ? tree_top(left) : 0;
-                left &= ~(kOne << c4[y]);
-                below[y] = left;
-                b4[y] = beta[c4[y]];
-#pragma unroll
-                for (int z = 0; z < kP; ++z) m4[y][z] = L[c4[y] * KP + 32 * z];
-            }
-#pragma unroll
-            for (int y = 0; y < 4; ++y) {
-                float wc = __shfl_sync(0xffffffffu, w[0], c4[y] & 31, kLanes);
-                if constexpr (kP == 2) {
-                    const float hi = __shfl_sync(0xffffffffu, w[1], c4[y] & 31);
-                    wc = c4[y] >= 32 ? hi : wc;
-                }
-                wc *= b4[y];
-#pragma unroll
-                for (int z = 0; z < kP; ++z)
-                    if (below[y] >> (mine + 32 * z) & 1) w[z] = fmaf(-wc, m4[y][z], w[z]);
-            }
-        }
-#pragma unroll
-        for (int z = 0; z < kP; ++z) {
-            const int b = mine + 32 * z;
-            const float x = on >> b & 1 ? w[z] * beta[b] : 0.f, y = tree_lead(x);
-            float* to = reinterpret_cast<float*>(sm + Sh::oW + z * (kItems * Sh::kWRows * 128) +
-                                                 tc::sw128_off32(it * Sh::kWRows + i, mine, kItems * Sh::kWRows));
-            to[0] = y;
-            to[Sh::kW / 4] = x - y;
-        }
-    }
-    tc::fence_smem_to_async();
-    tree_copies_done();
-    ok = tc::mbar_wait_bounded(&bars[2], (Sh::kChunks - 1) & 1, kWaitLimitNs) && ok;
-    ok = __all_sync(0xffffffffu, ok);
-    __syncthreads();
-    tc::fence_after_sync();
-
-    // 6. V - P, a column a thread and every other 8 places a group, into S_0^T's place
-    const uint64_t* set = s_set + item * KP;
-    const uint16_t* v = reinterpret_cast<const uint16_t*>(sm + Sh::oV) + item * KP * D + col;
-    auto rows_at = [&](int i, int query) {                              // TMEM columns of places i .. i + 7
-        return lane_tm + Sh::kD + (i / KC) * Sh::kRows + item * 2 * KC + query * KC + i % KC;
-    };
-    Set none = 0;                                                       // places where it is no number (0 goes in: 0 * NaN is none)
-#pragma unroll 2
-    for (int i0 = 8 * group; i0 < KP; i0 += 16) {
-        float x[8], y[8];
-        tree_tmem_ld8(rows_at(i0, 0), x);
-#pragma unroll
-        for (int r = 0; r < 8; ++r) {
-            float d = set[i0 + r] != 0 ? bf16_bits_to_f32(v[(i0 + r) * D]) - x[r] : 0.f;
-            if (!(fabsf(d) < INFINITY)) {
-                none |= kOne << (i0 + r);
-                d = 0.f;
-            }
-            x[r] = tree_lead(d);
-            y[r] = d - x[r];
-        }
-        tree_tmem_st8(lane_tm + i0, x);
-        tree_tmem_st8(lane_tm + KP + i0, y);
-    }
-    tc::tmem_wait_st();
-    tc::fence_before_sync();
-    const bool some = __syncthreads_or(none != 0) != 0;
-    if (warp == 0) {
-        tc::fence_after_sync();
+        // (copies in flight land before the shared memory is given back)
+        if (!ok)
+            for (uint32_t i = c > kRing ? c - kRing : 0; i < c; ++i) tc::mbar_wait_bounded(&b_full[i % kRing], i / kRing & 1, kWaitLimitNs);
+        __syncwarp();
+    } else if (warp == 8) {
+        // ---- the products ----
         if (tc::elect_one()) {
-            // Q += W (V - P), per item and chunk (N at least 16: what follows 8 places' columns is not read again)
+            constexpr uint32_t id = tc::idesc(128, Sh::kRows, tc::kFmtTF32, false, false);
+            constexpr uint32_t id_rest = tc::idesc(128, 2 * KC, tc::kFmtTF32, false, false);
+            constexpr uint32_t id_side = tc::idesc(64, Sh::kItem, tc::kFmtTF32, false, false);
+            // (N at least 16: what follows 8 places' columns is not read again)
             constexpr int kN = KC < 16 ? 16 : KC;
             constexpr uint32_t id_w = tc::idesc(128, kN, tc::kFmtTF32, false, false);
-            for (int chunk = 0; chunk < Sh::kChunks; ++chunk)
-                for (int it = 0; it < kItems; ++it) {
-                    const uint32_t d = tm + Sh::kD + chunk * Sh::kRows + it * 2 * KC + KC;
-                    const uint32_t sw = tree_desc(tc::smem_u32(sm) + Sh::oW + (it * Sh::kWRows + chunk * KC) * 128u);
+            uint32_t turn = 0, run = 0, puts = 0;
+            for (uint32_t first = begin; first < heads && ok; first += stride, ++turn) {
+                for (int chunk = 0; chunk < kChunks && ok; ++chunk, ++run) {
+                    ok = tc::mbar_wait_bounded(b_rows, run & 1, kWaitLimitNs);
+                    if (!ok) break;
+                    tc::fence_after_sync();
+                    const bool walk = *reinterpret_cast<volatile int*>(s_walk + (turn & 1)) != 0;
+                    auto side = [&] {
+                        // the keys over their decays (64 rows from an item's first) times the item's rows: L and N, transposed
+                        if (!walk)
+#pragma unroll 1
+                            for (int it = 0; it < kItems; ++it) {
+                                const uint32_t d = tm + Sh::kL + chunk * Sh::kRows + it * Sh::kItem;
+                                const uint32_t sa = tree_desc(sm0 + Sh::oSide + it * Sh::kSideItem * 128u);
+                                const uint32_t sb = tree_desc(sm0 + Sh::oRows + it * Sh::kItem * 128u);
 #pragma unroll
-                    for (uint32_t k = 0; k < KP / 8; ++k) {
-                        const uint32_t at = sw + (k >> 2) * (kItems * Sh::kWRows * 8u) + (k & 3) * 2u;
-                        tree_mma(d, tm + k * 8u, at, id_w, 1u);
-                        tree_mma(d, tm + k * 8u, at + Sh::kW / 16u, id_w, 1u);
-                        tree_mma(d, tm + KP + k * 8u, at, id_w, 1u);
+                                for (uint32_t k = 0; k < kSlabs * 4u; ++k) {
+                                    const uint32_t pa = sa + (k >> 2) * (Sh::kSideRows * 8u) + (k & 3) * 2u, pb = sb + (k >> 2) * (Sh::kRows * 8u) + (k & 3) * 2u;
+                                    tree_mma_ss(d, pa, pb, id_side, k > 0 ? 1u : 0u);
+                                    if constexpr (!Sh::kStack) {
+                                        tree_mma_ss(d, pa, pb + Sh::kRest / 16u, id_side, 1u);
+                                        tree_mma_ss(d, pa + Sh::kSide / 16u, pb, id_side, 1u);
+                                    }
+                                }
+                            }
+                        tc::mma_commit(b_side);
+                    };
+                    if (!Sh::kApart) {
+                        side();
+                        ok = tc::mbar_wait_bounded(b_read, run & 1, kWaitLimitNs);
+                        if (!ok) break;
+                        tc::fence_after_sync();
                     }
+                    const uint32_t d = tm + Sh::kD + chunk * Sh::kRows;
+                    for (int q = 0; q < kSlabs; ++q) {
+                        // (beside the slabs that wait for the first ones' place)
+                        if (Sh::kApart && q == kBufs % kSlabs) side();
+                        const int b = q % kBufs;
+                        if (chunk == 0) {
+                            ok = tc::mbar_wait_bounded(&b_put[b], puts / kBufs & 1, kWaitLimitNs);
+                            if (!ok) break;
+                            tc::fence_after_sync();
+                            ++puts;
+                        }
+                        const uint32_t ta = tm + b * 64, rows = tree_desc(sm0 + Sh::oRows + q * (Sh::kRows * 128u));
+#pragma unroll
+                        for (uint32_t k = 0; k < 4; ++k) {
+                            // (stacked: both terms of the rows, their accumulators side by side)
+                            tree_mma(d, ta + k * 8u, rows + k * 2u, id, q == 0 && k == 0 ? 0u : 1u);
+                            if constexpr (Sh::kStack) {
+#pragma unroll
+                                for (uint32_t it = 0; it < kItems; ++it)
+                                    tree_mma(d + it * Sh::kItem, ta + 32u + k * 8u, rows + it * Sh::kItem * 8u + k * 2u, id_rest, 1u);
+                            } else {
+                                tree_mma(d, ta + k * 8u, rows + Sh::kRest / 16u + k * 2u, id, 1u);
+                                tree_mma(d, ta + 32u + k * 8u, rows + k * 2u, id, 1u);
+                            }
+                        }
+                        if (!Sh::kWhole) tc::mma_commit(&b_free[b]);
+                    }
+                    if (ok) tc::mma_commit(b_prod);
                 }
-            tc::mma_commit(&bars[6]);
+                if (!ok) break;
+                ok = tc::mbar_wait_bounded(b_e, turn & 1, kWaitLimitNs);
+                if (!ok) break;
+                tc::fence_after_sync();
+                // Q += W (V - P), per item and chunk
+                for (int chunk = 0; chunk < kChunks; ++chunk)
+#pragma unroll 1
+                    for (int it = 0; it < kItems; ++it) {
+                        const uint32_t d = tm + Sh::kD + chunk * Sh::kRows + it * Sh::kItem + KC;
+                        const uint32_t sw = tree_desc(sm0 + Sh::oW + (it * Sh::kWRows + chunk * KC) * 128u);
+#pragma unroll
+                        for (uint32_t k = 0; k < KP / 8; ++k) {
+                            const uint32_t at = sw + (k >> 2) * (kItems * Sh::kWRows * 8u) + (k & 3) * 2u;
+                            tree_mma(d, tm + k * 8u, at, id_w, 1u);
+                            tree_mma(d, tm + k * 8u, at + Sh::kW / 16u, id_w, 1u);
+                            tree_mma(d, tm + KP + k * 8u, at, id_w, 1u);
+                        }
+                    }
+                tc::mma_commit(b_w);
+            }
+            // nothing of this CTA's is left running when it returns its TMEM
+            tc::mma_commit(b_last);
+            if (!tc::mbar_wait_bounded(b_last, 0, kWaitLimitNs)) ok = false;
         }
         __syncwarp();
-    }
-    if (some) {                                                         // the other group's places of this column too
-        Set* s_none = reinterpret_cast<Set*>(sm + Sh::oRows);           // (the rows are done with)
-        s_none[group * 128 + column] = none;
-        __syncthreads();
-        none |= s_none[(1 - group) * 128 + column];
-    }
-    ok = tc::mbar_wait_bounded(&bars[6], 0, kWaitLimitNs) && ok;
-    ok = __all_sync(0xffffffffu, ok);
-    tc::fence_after_sync();
-
-    // 7. the outputs, every other 8 places a group
-    const size_t step = static_cast<size_t>(a.H) * D;
-    const size_t to = tok0 * D + col;
-#pragma unroll 1
-    for (int i0 = 8 * group; i0 < a.K; i0 += 16) {
-        float o[8];
-        tree_tmem_ld8(rows_at(i0, 1), o);
-        if (!good || !ok) continue;
+    } else {
+        const int group = warp >> 2, column = 32 * (warp & 3) + lane, item = kItems == 1 ? 0 : column / D, col = column % D;
+        const uint32_t lane_tm = tm + (static_cast<uint32_t>(32 * (warp & 3)) << 16);
+        // this thread's share of the rows
+        constexpr int CH = Sh::CH, kPlaces = Sh::kPlaces, kWords = CH / 2;
+        const int place = lane % Sh::kLanes, block = (warp * Sh::kG + lane / Sh::kLanes) * CH, part = block / D, chan = block % D;
+        // the inputs on their way: log alphas, keys and queries
+        float la[kPlaces][CH];
+        uint32_t kx[kPlaces][kWords], qx[kPlaces][kWords];
+        auto fetch = [&](const Turn& w) {
 #pragma unroll
-        for (int r = 0; r < 8; ++r) {
-            if (i0 + r >= a.K) break;
-            const Set on = static_cast<Set>(set[i0 + r]);
-            float x = on ? o[r] : 0.f;
-            if (on & none) x = __int_as_float(0x7fffffff);
-            if (a.out_f32) reinterpret_cast<float*>(a.out)[to + (i0 + r) * step] = x;
-            else reinterpret_cast<uint16_t*>(a.out)[to + (i0 + r) * step] = f32_to_bf16_bits(x);
+            for (int z = 0; z < kPlaces; ++z) {
+                const int j = min(place + 32 * z, a.K - 1);
+                const size_t tok = w.token(part, j, a.K, a.H), at = tok * D + chan;
+                if (a.decay == 0) {
+#pragma unroll
+                    for (int c = 0; c < CH; c += 4) {
+                        const float4 x = *reinterpret_cast<const float4*>(a.la + at + c);
+                        la[z][c] = x.x; la[z][c + 1] = x.y; la[z][c + 2] = x.z; la[z][c + 3] = x.w;
+                    }
+                } else {
+                    const float x = a.decay == 1 ? a.la[tok] : 0.f;
+#pragma unroll
+                    for (int c = 0; c < CH; ++c) la[z][c] = x;
+                }
+                auto words = [&](const uint16_t* from, uint32_t (&to)[kWords]) {
+                    if constexpr (kWords == 2) {
+                        const uint2 x = *reinterpret_cast<const uint2*>(from);
+                        to[0] = x.x; to[1] = x.y;
+                    } else {
+#pragma unroll
+                        for (int c = 0; c < kWords; c += 4) {
+                            const uint4 x = *reinterpret_cast<const uint4*>(from + 2 * c);
+                            to[c] = x.x; to[c + 1] = x.y; to[c + 2] = x.z; to[c + 3] = x.w;
+                        }
+                    }
+                };
+                words(a.k + at, kx[z]);
+                words(a.q + at, qx[z]);
+            }
+        };
+        auto fetch_v = [&](const Turn& w) {                             // [place][column of the item]
+            for (int f = tid; f < Sh::kNodes * D / 8; f += 256) {
+                const int e = f / (D / 8), j = e % KP;
+                if (j < a.K) tree_copy16(sm0 + Sh::oV + f * 16, a.v + w.token(e / KP, j, a.K, a.H) * D + f % (D / 8) * 8);
+            }
+        };
+        auto split = [&](uint32_t off, uint32_t term, float4 x) {       // four channels of a row in their two terms
+            const float4 lead = make_float4(tree_lead(x.x), tree_lead(x.y), tree_lead(x.z), tree_lead(x.w));
+            *reinterpret_cast<float4*>(sm + off) = lead;
+            *reinterpret_cast<float4*>(sm + off + term) = make_float4(x.x - lead.x, x.y - lead.y, x.z - lead.z, x.w - lead.w);
+        };
+        Turn next(begin, heads, a.H);
+        fetch(next);
+        uint32_t turn = 0, run = 0, slab = 0;
+#pragma unroll 1
+        for (; next.first < heads; ++turn) {
+            const Turn now = next;
+            const uint32_t odd = turn & 1;                              // of what completes once a turn
+            const Set* s_set = s_sets + odd * Sh::kNodes;
+            const uint16_t* s_beta = s_betas + odd * Sh::kNodes;
+            const int slot = slot_of(now, item);
+            if (slot < 0 && now.first + item < heads && col == 0 && group == 0) set_status(a.status, kStatusTree);
+            fetch_v(now);
+            // 1, 3. slab q of the state into TMEM (a group each in turn)
+            auto put = [&](int q) {
+                const uint32_t c = slab + q, b = q % kBufs;
+                ok = tc::mbar_wait_bounded(&b_full[c % kRing], c / kRing & 1, kWaitLimitNs) && ok;
+                ok = __all_sync(0xffffffffu, ok);
+                if (!ok) return;
+                const float* S = reinterpret_cast<const float*>(sm + Sh::oState + c % kRing * 16384u) + item * 32 * D + col;
+                uint32_t lead[32], rest[32];
+#pragma unroll
+                for (int i = 0; i < 32; ++i) {
+                    const float x = S[i * D], y = tree_lead(x);
+                    lead[i] = __float_as_uint(y);
+                    // (in order with the arrival: the copy that follows it must not overtake a load that is still in flight)
+                    asm volatile("sub.rn.f32 %0, %1, %2;" : "=r"(rest[i]) : "f"(x), "f"(y) : "memory");
+                }
+                tc::mbar_arrive(&b_empty[c % kRing]);
+                // (the first of a turn follow on its last turn's end)
+                if (q >= kBufs) {
+                    ok = tc::mbar_wait_bounded(&b_free[b], (turn * (kSlabs / kBufs) + q / kBufs - 1) & 1, kWaitLimitNs);
+                    ok = __all_sync(0xffffffffu, ok);
+                    if (!ok) return;
+                    tc::fence_after_sync();
+                }
+                tc::tmem_st32x(lane_tm + b * 64, lead);
+                tc::tmem_st32x(lane_tm + b * 64 + 32, rest);
+                tc::tmem_wait_st();
+                tc::fence_before_sync();
+                tc::mbar_arrive(&b_put[b]);
+            };
+#pragma unroll 1
+            for (int q = group; q < kBufs && ok; q += 2) put(q);
+            // 2. decays along the paths: a node's product reaches 1, 2, 4 .. nodes up, a lane a node
+            ok = tc::mbar_wait_bounded(&b_tree[odd], turn / 2 & 1, kWaitLimitNs) && ok;
+            ok = __all_sync(0xffffffffu, ok);
+            float p[kPlaces][CH];
+#pragma unroll
+            for (int z = 0; z < kPlaces; ++z)
+#pragma unroll
+                for (int c = 0; c < CH; ++c) p[z][c] = expf(la[z][c]);
+            const int8_t* fars = s_fars + (odd * Sh::kRounds * kItems + part) * KP + place;
+#pragma unroll 1
+            for (int r = 0; r < Sh::kRounds; ++r) {
+                int up[kPlaces];
+                bool more = false;
+#pragma unroll
+                for (int z = 0; z < kPlaces; ++z) {
+                    up[z] = fars[r * kItems * KP + 32 * z];
+                    more |= up[z] >= 0;
+                }
+                if (!__any_sync(0xffffffffu, more)) break;
+#pragma unroll
+                for (int c = 0; c < CH; ++c) {
+                    float y[kPlaces];
+#pragma unroll
+                    for (int z = 0; z < kPlaces; ++z) {
+                        y[z] = __shfl_sync(0xffffffffu, p[0][c], up[z], Sh::kLanes);
+                        if constexpr (kPlaces == 2) {
+                            const float hi = __shfl_sync(0xffffffffu, p[1][c], up[z]);
+                            y[z] = up[z] >= 32 ? hi : y[z];
+                        }
+                    }
+#pragma unroll
+                    for (int z = 0; z < kPlaces; ++z) p[z][c] *= up[z] >= 0 ? y[z] : 1.f;
+                }
+            }
+            // (a key over a decay outside this range would overflow: such turns walk their paths)
+            bool far = false;
+            Set mine[kPlaces];
+#pragma unroll
+            for (int z = 0; z < kPlaces; ++z) {
+                mine[z] = s_set[part * KP + place + 32 * z];
+                if (mine[z] != 0)
+#pragma unroll
+                    for (int c = 0; c < CH; ++c) far |= p[z][c] < 0x1p-100f || (p[z][c] > 0x1p100f && p[z][c] < INFINITY);
+            }
+            if (far) s_walk[odd] = 1;
+            bool walk = false;
+
+#pragma unroll 1
+            for (int chunk = 0; chunk < kChunks; ++chunk, ++run) {
+                // the rows: keys and queries times their decays, keys over them
+#pragma unroll
+                for (int z = 0; z < kPlaces; ++z) {
+                    const int i = place + 32 * z;
+                    if (kChunks > 1 && i / KC != chunk) continue;
+                    const uint32_t row = part * Sh::kItem + i % KC;
+                    const uint32_t beside = part * Sh::kSideItem + (Sh::kStack ? i / 8 * 16 + i % 8 : i);
+#pragma unroll
+                    for (int c = 0; c < CH; c += 4) {
+                        float k[4], q[4], d[4];
+#pragma unroll
+                        for (int w = 0; w < 2; ++w) {
+                            const float2 x = bf16x2_bits_to_f32(mine[z] ? kx[z][c / 2 + w] : 0u), y = bf16x2_bits_to_f32(mine[z] ? qx[z][c / 2 + w] : 0u);
+                            k[2 * w] = x.x; k[2 * w + 1] = x.y;
+                            q[2 * w] = y.x; q[2 * w + 1] = y.y;
+                        }
+#pragma unroll
+                        for (int w = 0; w < 4; ++w) d[w] = mine[z] ? p[z][c + w] : 1.f;
+                        split(Sh::oRows + tc::sw128_off32(row, chan + c, Sh::kRows), Sh::kRest,
+                              make_float4(d[0] * k[0], d[1] * k[1], d[2] * k[2], d[3] * k[3]));
+                        split(Sh::oRows + tc::sw128_off32(row + KC, chan + c, Sh::kRows), Sh::kRest,
+                              make_float4(d[0] * q[0], d[1] * q[1], d[2] * q[2], d[3] * q[3]));
+                        split(Sh::oSide + tc::sw128_off32(beside, chan + c, Sh::kSideRows), Sh::kStack ? 1024u : Sh::kSide,
+                              make_float4(k[0] * tree_rcp(d[0]), k[1] * tree_rcp(d[1]), k[2] * tree_rcp(d[2]), k[3] * tree_rcp(d[3])));
+                    }
+                }
+                tc::fence_smem_to_async();
+                tc::mbar_arrive(b_rows);
+                if (chunk + 1 == kChunks) {                             // the next turn's inputs, into what is done with
+                    next = Turn(now.first + stride, heads, a.H);
+                    if (next.first < heads) fetch(next);
+                }
+                // 3. the other slabs
+                if (chunk == 0) {
+#pragma unroll 1
+                    for (int q = kBufs + group; q < kSlabs && ok; q += 2) put(q);
+                    slab += kSlabs;
+                }
+                tc::named_sync(kTreeAll, 256);                          // (of all threads: whether to walk)
+                walk = *reinterpret_cast<volatile int*>(s_walk + odd) != 0;
+                if (tid == 0) s_walk[1 - odd] = 0;
+                // 4. L and N of the chunk's nodes
+                if (!walk) {
+                    // row x of the product is lane x % 16 of warp x / 16
+                    constexpr int kOwn = Sh::kStack ? 8 : 16;           // places a warp (stacked: lanes 8 .. 15 their second terms)
+                    if (kOwn * warp < KP) {
+                        ok = tc::mbar_wait_bounded(b_side, run & 1, kWaitLimitNs) && ok;
+                        ok = __all_sync(0xffffffffu, ok);
+                        tc::fence_after_sync();
+                    }
+                    if (kOwn * warp < KP) {
+                        const int b = kOwn * warp + lane;
+#pragma unroll 1
+                        for (int it = 0; it < kItems; ++it)
+#pragma unroll
+                            for (int c0 = 0; c0 < 2 * KC; c0 += 8) {
+                                float x[8];
+                                const uint32_t from = lane_tm + Sh::kL + chunk * Sh::kRows + it * Sh::kItem + c0;
+                                tree_tmem_ld8(from, x);
+                                if constexpr (Sh::kStack) {
+                                    float y[8];
+                                    tree_tmem_ld8(from + 2 * KC, y);
+#pragma unroll
+                                    for (int r = 0; r < 8; ++r) x[r] += __shfl_xor_sync(0xffffffffu, x[r], 8) + y[r];
+                                }
+                                float* to = (c0 < KC ? s_m : s_n) + (it * KP + chunk * KC + c0 % KC) * KP + b;
+                                if (lane < kOwn && b < KP) {
+#pragma unroll
+                                    for (int r = 0; r < 8; ++r) to[r * KP] = x[r];
+                                }
+                            }
+                        tc::fence_before_sync();
+                    }
+                } else {
+                    // half a warp a node, up its path; lane l of the 16: channels 4 l .. + 3 of each 64
+                    const int hl = lane & 15;
+#pragma unroll 1
+                    for (int f = 2 * warp + (lane >> 4); f < kItems * KC; f += 16) {
+                        const int it = f / KC, i = chunk * KC + f % KC, e = it * KP + i;
+                        Set left = s_set[e];
+                        float key[4 * G], query[4 * G], p[4 * G];
+#pragma unroll
+                        for (int c = 0; c < 4 * G; ++c) {
+                            const size_t at = now.token(it, left ? i : 0, a.K, a.H) * D + c / 4 * 64 + 4 * hl + c % 4;
+                            key[c] = bf16_bits_to_f32(a.k[at]);
+                            query[c] = bf16_bits_to_f32(a.q[at]);
+                            p[c] = 1.f;
+                        }
+                        while (__any_sync(0xffffffffu, left != 0)) {
+                            const bool on = left != 0;
+                            const int b = on ? tree_top(left) : 0;
+                            left &= ~(kOne << b);
+                            const size_t tok = now.token(it, b, a.K, a.H);
+                            float m = 0.f, w = 0.f;
+#pragma unroll
+                            for (int c = 0; c < 4 * G; ++c) {
+                                const size_t at = tok * D + c / 4 * 64 + 4 * hl + c % 4;
+                                const float kb = p[c] * bf16_bits_to_f32(a.k[at]);
+                                m = fmaf(key[c], kb, m);
+                                w = fmaf(query[c], kb, w);
+                                p[c] *= a.decay == 2 ? 1.f : expf(a.la[a.decay == 0 ? at : tok]);
+                            }
+#pragma unroll
+                            for (int off = 8; off > 0; off >>= 1) {
+                                m += __shfl_xor_sync(0xffffffffu, m, off);
+                                w += __shfl_xor_sync(0xffffffffu, w, off);
+                            }
+                            if (hl == 0 && on) {
+                                s_m[(it * KP + i) * KP + b] = m;
+                                s_n[(it * KP + i) * KP + b] = w;
+                            }
+                        }
+                    }
+                }
+                if (!Sh::kApart && group == 0) tc::mbar_arrive(b_read);
+                if (chunk + 1 < kChunks) {                              // the rows are written again
+                    ok = tc::mbar_wait_bounded(b_prod, run & 1, kWaitLimitNs) && ok;
+                    ok = __all_sync(0xffffffffu, ok);
+                }
+            }
+            tc::named_sync(kTreeAll, 256);
+            // 5. W while the products run: a warp a row (or two), lane b place b (and b + 32): w_c is final once the places above c
+            // are done.  Zeros where the path does not lead
+            constexpr int kLanes = Sh::kLanes, kP = kPlaces;            // lanes a row, places a lane
+#pragma unroll 1
+            for (int e = warp * (32 / kLanes) + lane / kLanes; e < Sh::kNodes; e += 8 * (32 / kLanes)) {
+                const int it = e / KP, i = e % KP, mine = lane % kLanes;
+                const Set on = s_set[e];
+                float w[kP];
+                const float* row = s_n + (it * KP + i) * KP;
+                const float* L = s_m + it * KP * KP + mine;
+                const uint16_t* beta = s_beta + it * KP;
+#pragma unroll
+                for (int z = 0; z < kP; ++z) w[z] = on >> (mine + 32 * z) & 1 ? row[mine + 32 * z] : 0.f;
+                // (nothing is below a path's first node)
+                for (Set left = on; __any_sync(0xffffffffu, (left & (left - 1)) != 0);) {
+                    int c4[4];
+                    Set below[4];
+                    float b4[4], m4[4][kP];
+#pragma unroll
+                    for (int y = 0; y < 4; ++y) {                       // 4 places of the path, their loads together
+                        c4[y] = left ? tree_top(left) : 0;
+                        left &= ~(kOne << c4[y]);
+                        below[y] = left;
+                        b4[y] = bf16_bits_to_f32(beta[c4[y]]);
+#pragma unroll
+                        for (int z = 0; z < kP; ++z) m4[y][z] = L[c4[y] * KP + 32 * z];
+                    }
+#pragma unroll
+                    for (int y = 0; y < 4; ++y) {
+                        float wc = __shfl_sync(0xffffffffu, w[0], c4[y] & 31, kLanes);
+                        if constexpr (kP == 2) {
+                            const float hi = __shfl_sync(0xffffffffu, w[1], c4[y] & 31);
+                            wc = c4[y] >= 32 ? hi : wc;
+                        }
+                        wc *= b4[y];
+#pragma unroll
+                        for (int z = 0; z < kP; ++z)
+                            if (below[y] >> (mine + 32 * z) & 1) w[z] = fmaf(-wc, m4[y][z], w[z]);
+                    }
+                }
+#pragma unroll
+                for (int z = 0; z < kP; ++z) {
+                    const int b = mine + 32 * z;
+                    const float x = on >> b & 1 ? w[z] * bf16_bits_to_f32(beta[b]) : 0.f, y = tree_lead(x);
+                    float* to = reinterpret_cast<float*>(sm + Sh::oW + z * (kItems * Sh::kWRows * 128) +
+                                                         tc::sw128_off32(it * Sh::kWRows + i, mine, kItems * Sh::kWRows));
+                    to[0] = y;
+                    to[Sh::kW / 4] = x - y;
+                }
+            }
+            tc::fence_smem_to_async();
+            tree_copies_done();
+            ok = tc::mbar_wait_bounded(b_prod, (run - 1) & 1, kWaitLimitNs) && ok;
+            ok = __all_sync(0xffffffffu, ok);
+            tc::named_sync(kTreeAll, 256);
+            tc::fence_after_sync();
+            // 6. V - P, a column a thread and every other 8 places a group, into S_0^T's place
+            const Set* set = s_set + item * KP;
+            const uint16_t* v = reinterpret_cast<const uint16_t*>(sm + Sh::oV) + item * KP * D + col;
+            auto rows_at = [&](int i, int query, float (&x)[8]) {       // places i .. i + 7 of P, or of Q
+                const uint32_t from = lane_tm + Sh::kD + (i / KC) * Sh::kRows + item * Sh::kItem + query * KC + i % KC;
+                tree_tmem_ld8(from, x);
+                if constexpr (Sh::kStack) {
+                    float y[8];
+                    tree_tmem_ld8(from + 2 * KC, y);
+#pragma unroll
+                    for (int r = 0; r < 8; ++r) x[r] += y[r];
+                }
+            };
+            Set none = 0;                                               // places where it is no number (0 goes in: 0 * NaN is none)
+#pragma unroll 2
+            for (int i0 = 8 * group; i0 < KP; i0 += 16) {
+                float x[8], y[8];
+                rows_at(i0, 0, x);
+#pragma unroll
+                for (int r = 0; r < 8; ++r) {
+                    float d = set[i0 + r] != 0 ? bf16_bits_to_f32(v[(i0 + r) * D]) - x[r] : 0.f;
+                    if (!(fabsf(d) < INFINITY)) {
+                        none |= kOne << (i0 + r);
+                        d = 0.f;
+                    }
+                    x[r] = tree_lead(d);
+                    y[r] = d - x[r];
+                }
+                tree_tmem_st8(lane_tm + i0, x);
+                tree_tmem_st8(lane_tm + KP + i0, y);
+            }
+            tc::tmem_wait_st();
+            tc::fence_before_sync();
+            tc::mbar_arrive(b_e);
+            if (!tc::named_sync_and(kTreeAll, 256, none == 0)) {        // the other group's places of this column too
+                Set* s_none = reinterpret_cast<Set*>(sm + Sh::oNone);   // (the rows are done with)
+                s_none[group * 128 + column] = none;
+                tc::named_sync(kTreeAll, 256);
+                none |= s_none[(1 - group) * 128 + column];
+                tc::named_sync(kTreeAll, 256);
+            }
+            ok = tc::mbar_wait_bounded(b_w, odd, kWaitLimitNs) && ok;
+            ok = __all_sync(0xffffffffu, ok);
+            tc::fence_after_sync();
+
+            // 7. the outputs, every other 8 places a group
+            const size_t step = static_cast<size_t>(a.H) * D;
+            const size_t to = now.token(item, 0, a.K, a.H) * D + col;
+#pragma unroll 1
+            for (int i0 = 8 * group; i0 < a.K; i0 += 16) {
+                float o[8];
+                rows_at(i0, 1, o);
+                if (slot < 0 || !ok) continue;
+#pragma unroll
+                for (int r = 0; r < 8; ++r) {
+                    if (i0 + r >= a.K) break;
+                    const Set on = set[i0 + r];
+                    float x = on ? o[r] : 0.f;
+                    if (on & none) x = __int_as_float(0x7fffffff);
+                    if (a.out_f32) reinterpret_cast<float*>(a.out)[to + (i0 + r) * step] = x;
+                    else reinterpret_cast<uint16_t*>(a.out)[to + (i0 + r) * step] = f32_to_bf16_bits(x);
+                }
+            }
+            tc::fence_before_sync();
+            // (a wait that ran out: nothing more is begun)
+            if (!tc::named_sync_and(kTreeAll, 256, ok)) { ok = false; break; }
+            tc::fence_after_sync();
+            if (tid == 0) tc::mbar_arrive(&b_done[odd]);
         }
+        tree_copies_done();
     }
     if (!ok) set_status(a.status, kStatusTimeout);
+    __syncwarp();
     tc::fence_before_sync();
     __syncthreads();
     tc::fence_after_sync();
-    if (warp == 7) tc::tmem_dealloc(tm, Sh::kCols);
+    if (warp == 8) tc::tmem_dealloc(tm, Sh::kCols);
 }
 
 namespace {
@@ -618,7 +814,8 @@ int launch_tree_shape(const TreeArgs& a, cudaStream_t stream) {
     static bool attr_done[kMaxDevicesAttr] = {};
     if (!raise_smem_limit(reinterpret_cast<const void*>(kda_tree_kernel<D, KP>), Sh::kBytes, attr_done)) return -3;
     const long long heads = static_cast<long long>(a.N) * a.H;
-    kda_tree_kernel<D, KP><<<static_cast<unsigned>((heads + Sh::kItems - 1) / Sh::kItems), Sh::kThreads, Sh::kBytes, stream>>>(a);
+    const long long turns = (heads + Sh::kItems - 1) / Sh::kItems, at_once = static_cast<long long>(a.sms) * Sh::kCtas;
+    kda_tree_kernel<D, KP><<<static_cast<unsigned>(turns < at_once ? turns : at_once), kTreeThreads, Sh::kBytes, stream>>>(a);
     return cudaGetLastError() == cudaSuccess ? 0 : -3;
 }
 template <int D>
@@ -632,7 +829,11 @@ int launch_decode_tree(const uint16_t* q, const uint16_t* k, const uint16_t* v, 
                        const float* pool, int num_slots, const int32_t* slots, const int32_t* parents, void* out, int out_f32,
                        int N, int K, int H, int D, int decay, int* status, cudaStream_t stream)
 {
-    const TreeArgs a{q, k, v, la, beta, pool, slots, parents, out, num_slots, out_f32, N, K, H, decay, status};
+    static int sms[kMaxDevicesAttr] = {};
+    int dev = 0;
+    if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= kMaxDevicesAttr) return -3;
+    if (!sms[dev] && cudaDeviceGetAttribute(&sms[dev], cudaDevAttrMultiProcessorCount, dev) != cudaSuccess) return -3;
+    const TreeArgs a{q, k, v, la, beta, pool, slots, parents, out, num_slots, out_f32, N, K, H, decay, sms[dev], status};
     return D == 128 ? launch_tree_dim<128>(a, stream) : launch_tree_dim<64>(a, stream);
 }
 

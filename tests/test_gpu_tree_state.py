@@ -163,3 +163,22 @@ def test_state_offsets_past_32_bits():
     got = kda.decode_tree(*d, pool, par, state_slots=at, out_dtype=torch.float32)
     _ok()
     assert torch.equal(got, kda.decode_tree(*d, pool[-1:].clone(), par, out_dtype=torch.float32))
+
+
+@pytest.mark.parametrize("decay", [CH, HD], ids=["channel", "head"])
+@pytest.mark.parametrize("D", [64, 128])
+@pytest.mark.parametrize("K", [3, 8, 13, 16, 29, 32, 50, 64])
+def test_many_heads_one_after_another(K, D, decay):
+    """More heads than the device works on at once, an odd number of them: each as in a call of its own sequence."""
+    N, H = 91, 11
+    x, pool = inputs(N, K, H, D, decay, seed=K + D)
+    rows = [T.tree(K, n, 1 + n % 7, nodes=max(1, K - n % 5)) for n in range(N)]
+    got = run(x, pool, rows, decay=decay)
+    _ok()
+    for n in (0, 1, 40, 77, 89, 90):
+        one = [None if t is None else t[n:n + 1] for t in x]
+        alone = run(one, pool, rows[n:n + 1], [n], decay=decay)
+        _ok()
+        assert torch.equal(got[n], alone[0]), n
+    n = 90
+    check(got[n:], [None if t is None else t[n:] for t in x], pool[n:], rows[n:], [0])
