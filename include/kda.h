@@ -627,7 +627,7 @@ int kda_verify_draft(const float* target_probs, int64_t ldp, const float* draft_
  *   logits      (device) [R, V], bf16 or fp32 per logits_dtype (kda_out_dtype), rows ld elements apart
  *               (any ld >= V, rows aligned to their elements)
  *   tokens      (device) int32 [R] or NULL (alternatives and entropies alone)
- *   scale       finite, > 0 (1 / temperature): z = scale * logits
+ *   scale       1e-6 .. 1e6 (1 / temperature): z = scale * logits
  *   logprob     (device) fp32 [R], NULL with tokens: z_t - log sum exp z
  *   rank        (device) int32 [R] or NULL: the place of the token, from 1, in the order of the logits,
  *               largest first, equal ones by lowest index

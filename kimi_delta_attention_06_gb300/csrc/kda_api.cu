@@ -1015,7 +1015,7 @@ int kda_verify_draft(const float* target_probs, int64_t ldp, const float* draft_
 int kda_token_logprobs(const void* logits, int logits_dtype, int64_t ld, const int32_t* tokens, int R, int V, int top,
                        float scale, float* logprob, int32_t* rank, float* entropy, float* top_logprob, int32_t* top_token,
                        void* stream) {
-    if (R < 0 || V <= 0 || top < 0 || !(scale > 0.f) || !scale_ok(scale)) return KDA_ERR_INVALID_ARG;
+    if (R < 0 || V <= 0 || top < 0 || !(scale >= 1e-6f && scale <= 1e6f)) return KDA_ERR_INVALID_ARG;
     if (logits_dtype != KDA_OUT_BF16 && logits_dtype != KDA_OUT_F32) return KDA_ERR_INVALID_ARG;
     if (top > KDA_LOGPROBS_MAX_TOP || V > (1 << 30)) return KDA_ERR_UNSUPPORTED;
     if (R == 0) return KDA_OK;

@@ -45,6 +45,7 @@ def expected(row, t, scale, top):
     dent = ds + 3 * H24 * eyy + ey * (2.0 ** -22 + (2 * n + 8) * H24) + (float(ls) + ey) * 4 * H24
     lp = torch.where(x > -math.inf, x - m - ls, torch.full_like(x, -math.inf))
     ent = float(ls) + ey if m > -math.inf else 0.0
+    lp = torch.where(lp < -torch.finfo(F32).max, torch.full_like(lp, -math.inf), lp)   # beyond fp32: -inf
     o = order(row)
     rank = None if t is None else int((o == t).nonzero()[0]) + 1
     near = lambda v: ds + 4 * H24 * ((v + ls).abs() + abs(float(ls)))    # the difference, the product, the sum
@@ -209,3 +210,39 @@ def test_row_offsets_past_32_bits_and_repeats():
     assert all(torch.equal(p, q) for p, q in zip(a, b))
     some = [0, R // 2, R - 2, R - 1]
     check(x[some].cpu(), [int(tok[i]) for i in some], 3, 1.0, [g[some] for g in a])
+
+
+@pytest.mark.parametrize("dtype", [BF, F32], ids=["bf16", "f32"])
+@pytest.mark.parametrize("scale", [1e-6, 0.02, 1.0, 1e6])
+def test_large_logits_and_scales(dtype, scale):
+    """Logits far from 0, where neighbours of the type are far apart; lowest values and -inf side by side; scales that
+    leave a row flat, or one token alone."""
+    V = 30011
+    x = rows(6, V, F32, 11)
+    x[1] = x[1] * 100 + 1e6
+    x[2] = x[2] * 1e28 + 9e29
+    x[3] = torch.finfo(dtype).min
+    x[3, ::2] = -math.inf
+    x[4] = torch.finfo(dtype).min / 3
+    x[4, 5:9000:3] = torch.finfo(dtype).min
+    x[5, :] = -math.inf
+    x[5, 17], x[5, 29000] = -3.0e38, -1.0e38
+    x = x.to(dtype)
+    tok = [7, 9, 11, 1, 6, 17]
+    for R in (6, 1):
+        got = run(x[:R] if R > 1 else x[3:4], tok if R > 1 else tok[3:4], 7, scale, pad=2)
+        _ok()
+        check(x[:R] if R > 1 else x[3:4], tok if R > 1 else tok[3:4], 7, scale, got)
+
+
+def test_rows_alone_and_together():
+    """Few rows are spread over several CTAs each, many are not: the same tokens and ranks, and sums to within rounding."""
+    x = rows(700, 65000, BF, 12)
+    tok = torch.randint(0, 65000, (700,), generator=torch.Generator().manual_seed(1)).tolist()
+    many = run(x, tok, 32)
+    for r0, r1 in ((0, 1), (5, 8), (100, 140), (0, 300)):
+        few = run(x[r0:r1], tok[r0:r1], 32)
+        _ok()
+        assert torch.equal(few[1], many[1][r0:r1]) and torch.equal(few[4], many[4][r0:r1])
+        for i in (0, 2, 3):
+            assert torch.allclose(few[i], many[i][r0:r1], rtol=2e-6, atol=2e-6)

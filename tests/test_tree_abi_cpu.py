@@ -73,7 +73,7 @@ def test_token_logprobs_refusals(lib):
                 tt=0x7000, st=None)
     f = lambda **o: _call(lib, "kda_token_logprobs", order, base, **o)
     for o in (dict(R=-1), dict(V=0), dict(top=-1), dict(scale=0.0), dict(scale=-1.0), dict(scale=float("nan")),
-              dict(scale=float("inf")), dict(dt=2), dict(ld=99), dict(x=None), dict(x=0x1001), dict(dt=1, x=0x1002),
+              dict(scale=float("inf")), dict(scale=9e-7), dict(scale=1.1e6), dict(dt=2), dict(ld=99), dict(x=None), dict(x=0x1001), dict(dt=1, x=0x1002),
               dict(tok=None), dict(lp=None), dict(tok=None, lp=None), dict(tl=None), dict(tt=None), dict(tok=0x2002),
               dict(rank=0x4001), dict(ent=0x5002), dict(tl=0x6002), dict(tt=0x7001), dict(R=1 << 27)):
         assert f(**o) == BAD, o
