@@ -48,6 +48,13 @@ struct LatentCache {
 // most two per CTA (its first and its last), which the combine kernel joins.  A segment costs
 // its start (Q, the first copies) and its end (O) besides its tiles, so each sequence counts
 // `lead` tiles more before its first one; a run's share of them is no work.
+//
+// Trees have places without a node, mostly their last ones, and with them whole row tiles to leave out.  So a tree's row
+// tiles are sequences of their own (all sequences' first row tiles, all their second ones, .. `each` times), of length 0
+// where no row of theirs is a node, and a run is a CTA's alone.  In this order the readers of a sequence's tokens still
+// run side by side where most trees are full (16 sequences of 341k tokens in all, trees of 4 to 8 nodes x 32 heads, e4m3:
+// 233 -> 204 us; a sequence's row tiles one after another: 203, and 64 x 8000 tokens, 4 nodes x 64 heads, bf16: 395 us
+// for 352).
 constexpr int kTile = 64;                       // tokens per tile
 constexpr int kMinTiles = 2;                    // shortest run of tiles worth a CTA of its own
 
@@ -57,11 +64,30 @@ struct LatWork {
     int lead;
     int least;                                  // shortest length of a sequence that is not empty (a tree's K nodes)
     long long max_len;
+    int each;                                   // row tiles that are sequences of their own (1: none are), ..
+    const uint8_t* need;                        // .. and how many of them a sequence needs (nullptr: all)
 };
+constexpr int kMaxNeed = 512;                   // up to so many sequences are looked at for it
 
-__device__ __forceinline__ int lat_len(const LatWork& w, int n) {
+__device__ __forceinline__ int lat_seq(const LatWork& w, int n) {
     const int len = w.seq_lens[n];
     return len < w.least || len > w.max_len ? 0 : len;
+}
+__device__ __forceinline__ int lat_len(const LatWork& w, int n) {
+    if (w.each <= 1) return lat_seq(w, n);
+    const int seqs = w.N / w.each, tile = n / seqs, s = n - tile * seqs;
+    return w.need && tile >= w.need[s] ? 0 : lat_seq(w, s);
+}
+// Row tiles of sequence n that are sequences of their own and not left out (as the attention kernel has found them).
+__device__ __forceinline__ int lat_needed(const LatWork& w, const int32_t* need, int n) {
+    return w.each <= 1 ? 1 : w.N / w.each <= kMaxNeed ? need[n] : w.each;
+}
+// Row tiles that a tree needs: R rows each, H of a node, up to its last place with a node.
+__device__ __forceinline__ int lat_need(const int32_t* parents, int K, int H, int R) {
+    int last = 0;
+    for (int j = 0; j < K; ++j)
+        if (__ldg(parents + j) >= -1) last = j + 1;
+    return (last * H + R - 1) / R;
 }
 __device__ __forceinline__ int lat_tiles(int len) { return (len + kTile - 1) / kTile; }
 __device__ __forceinline__ int lat_count(const LatWork& w, int len) { return len > 0 ? lat_tiles(len) + w.lead : 0; }   // with the lead
@@ -162,6 +188,7 @@ struct LatArgs {
     uint16_t* out;
     float* lse;
     float *part_o, *part_ml;                     // partials: [run][row tile][2][R][512], [..][R][2]
+    int32_t* need;                               // [N]: row tiles that a tree needs, where a.w.each > 1
     int* status;
 };
 
@@ -192,7 +219,7 @@ struct LatShape {
     static constexpr uint32_t kTmemCols = kUsed <= 128u ? 128u : kUsed <= 256u ? 256u : 512u;
     static_assert(kUsed <= 512u, "TMEM");
 };
-static_assert(LatShape<64, false>::kBytes + 64 * 8 <= 232448 && LatShape<64, true>::kBytes + 64 * 8 <= 232448,
+static_assert(LatShape<64, false>::kBytes + 64 * 8 + kMaxNeed <= 232448 && LatShape<64, true>::kBytes + 64 * 8 + kMaxNeed <= 232448,
               "227 KB of shared memory");
 
 // A row's weights are exp2(x - m).  m follows the row's maximum M lazily: bf16, m <= M <= m + 8 (the
@@ -316,11 +343,16 @@ kda_latent_decode_kernel(const __grid_constant__ LatMaps maps, const LatArgs a)
     int* s_j = reinterpret_cast<int*>(s_f + R);                 // [R]: query token of each row
     float* s_a = s_f + 2 * R;                                   // [R]: e4m3: 2^k * scale of each row
     uint64_t* s_set = reinterpret_cast<uint64_t*>(s_a + R);     // [R]: TREE: the nodes that each row sees (none: no node itself)
+    uint8_t* s_need = reinterpret_cast<uint8_t*>(s_set + R);    // [kMaxNeed]: TREE: row tiles of each sequence
     constexpr int NS = Sh::kStages;
 
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const int rt = blockIdx.x % a.RT, run = blockIdx.x / a.RT;
-    const int row0 = rt * R, nrows = min(R, a.rows - row0);
+    LatWork work = a.w;
+    // of a segment: its sequence, its first row there and how many follow
+    auto seq_of = [&](int n) { return TREE && a.w.each > 1 ? n % (a.w.N / a.w.each) : n; };
+    auto row_of = [&](int n) { return TREE && a.w.each > 1 ? n / (a.w.N / a.w.each) * R : rt * R; };
+    auto rows_of = [&](int n) { return min(R, a.rows - row_of(n)); };
 
     if (tid == 0) {
         for (int i = 0; i < NS; ++i) {
@@ -334,7 +366,7 @@ kda_latent_decode_kernel(const __grid_constant__ LatMaps maps, const LatArgs a)
         tc::mbar_fence_init();
     }
     {   // the page table goes to L2 while the lengths that say where to read it are on their way: a line a thread
-        const size_t lines = (static_cast<size_t>(a.w.N) * a.ch.max_pages * 4 + 127) / 128;
+        const size_t lines = (static_cast<size_t>(a.w.N / a.w.each) * a.ch.max_pages * 4 + 127) / 128;
         const size_t mine = static_cast<size_t>(blockIdx.x) * Sh::kThreads + tid;
         if (mine < lines) asm volatile("prefetch.global.L2 [%0];" :: "l"(reinterpret_cast<const uint8_t*>(a.ch.table) + mine * 128));
     }
@@ -343,7 +375,15 @@ kda_latent_decode_kernel(const __grid_constant__ LatMaps maps, const LatArgs a)
         if (E4M3) tc::tma_prefetch_map(&maps.s);
         else tc::tma_prefetch_map(&maps.q);
     }
-    if (tid < R) s_j[tid] = min((row0 + tid) / a.H, a.K - 1);
+    if (tid < R) s_j[tid] = min((rt * R + tid) / a.H, a.K - 1);
+    if (TREE && work.each > 1 && work.N / work.each <= kMaxNeed) {
+        for (int i = tid; i < work.N / work.each; i += Sh::kThreads) {
+            const int need = lat_need(a.parents + static_cast<long long>(i) * a.K, a.K, a.H, R);
+            s_need[i] = static_cast<uint8_t>(need);
+            if (blockIdx.x == 0) a.need[i] = need;              // for the kernel that joins
+        }
+        work.need = s_need;
+    }
     if (warp == Sh::kMmaWarp) tc::tmem_alloc(s_tmem, Sh::kTmemCols);
     tc::fence_before_sync();
     __syncthreads();
@@ -351,7 +391,7 @@ kda_latent_decode_kernel(const __grid_constant__ LatMaps maps, const LatArgs a)
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");   // the combine kernel waits for this grid's end
     const uint32_t tm = *s_tmem, tmO = tm, tmS = tm + 4 * Sh::kO;
     SegWalk sw;
-    sw.init(a.w, run);
+    sw.init(work, run);
     bool ok = true;
 
     if (warp < 4) {
@@ -360,19 +400,20 @@ kda_latent_decode_kernel(const __grid_constant__ LatMaps maps, const LatArgs a)
         const uint32_t lane_tm = static_cast<uint32_t>(warp * 32) << 16;
         float m[R / 4], l[R / 4];
         int g = 0;                                              // tiles done by this CTA
-        while (ok && sw.next(a.w)) {
+        while (ok && sw.next(work)) {
 #pragma unroll
             for (int i = 0; i < R / 4; ++i) { m[i] = -INFINITY; l[i] = 0.f; }
             const int clear = sw.len - (TREE ? a.K : a.K - 1);  // tokens that every row sees
+            const int seq = seq_of(sw.n), row0 = row_of(sw.n), nrows = rows_of(sw.n);
             bool spoilt = false;                                // a later one held a NaN or infinity
             if constexpr (TREE) {                               // (the last readers of the sets before are past a barrier)
                 if (warp == 0) {
                     uint64_t set[2];
-                    if (tree_sets(a.parents + static_cast<long long>(sw.n) * a.K, a.K, lane, set) && lane == 0)
+                    if (tree_sets(a.parents + static_cast<long long>(seq) * a.K, a.K, lane, set) && lane == 0)
                         set_status(a.status, kStatusIndex);
 #pragma unroll
                     for (int r = lane; r < (R < 32 ? 32 : R); r += 32) {
-                        const uint64_t mine = tree_set_of(set, s_j[min(r, R - 1)]);
+                        const uint64_t mine = tree_set_of(set, min((row0 + min(r, R - 1)) / a.H, a.K - 1));
                         if (r < R) s_set[r] = mine;
                     }
                 }
@@ -387,7 +428,7 @@ kda_latent_decode_kernel(const __grid_constant__ LatMaps maps, const LatArgs a)
                     uint32_t rope[4];
 #pragma unroll
                     for (int k = 0; k < 4; ++k) {
-                        const uint16_t* src = a.q + (static_cast<long long>(sw.n) * a.rows + row0 + min(rb + 4 * k, nrows - 1)) * kLatQ;
+                        const uint16_t* src = a.q + (static_cast<long long>(seq) * a.rows + row0 + min(rb + 4 * k, nrows - 1)) * kLatQ;
                         w0[k] = reinterpret_cast<const uint4*>(src)[2 * lane];
                         w1[k] = reinterpret_cast<const uint4*>(src)[2 * lane + 1];
                         rope[k] = reinterpret_cast<const uint32_t*>(src + kLatDim)[lane];
@@ -614,10 +655,10 @@ kda_latent_decode_kernel(const __grid_constant__ LatMaps maps, const LatArgs a)
                 if (tid < 4) s_f[r] = m[i];
             }
             if (!tc::named_sync_and(kBarSoft, Sh::kSoft, !spoilt) && !E4M3)
-                mark_nonfinite<R, TREE>(a.ch, sw.n, clear, sw.t0 * kTile, min(sw.len, sw.t1 * kTile), s_j, s_set, tmO + lane_tm,
+                mark_nonfinite<R, TREE>(a.ch, seq, clear, sw.t0 * kTile, min(sw.len, sw.t1 * kTile), s_j, s_set, tmO + lane_tm,
                                         32 * warp + lane);
             const bool whole = sw.whole();
-            const long long row_at = static_cast<long long>(sw.n) * a.rows + row0;
+            const long long row_at = static_cast<long long>(seq) * a.rows + row0;
             const size_t part = (static_cast<size_t>(run) * a.RT + rt) * 2 + (sw.first ? 0 : 1);
             if (tid < R) {                                       // a thread a row
                 float mr = s_f[tid], sum = (s_red[tid] + s_red[R + tid]) + (s_red[2 * R + tid] + s_red[3 * R + tid]);
@@ -687,7 +728,7 @@ kda_latent_decode_kernel(const __grid_constant__ LatMaps maps, const LatArgs a)
         const uint32_t c_lo = static_cast<uint32_t>(dC) | (tc::smem_u32(sC) >> 4);
         const uint32_t p_lo = static_cast<uint32_t>(d0) | (tc::smem_u32(sP) >> 4);
         SegWalk sv = sw;                                        // the O product's walk follows the S product's
-        bool more_s = sw.next(a.w), more_o = sv.next(a.w);
+        bool more_s = sw.next(work), more_o = sv.next(work);
         int gs = 0, go = 0, qs = 0;                             // S and O tiles issued, segments whose Q is in
         int ts = sw.t0, to = sv.t0;
         uint64_t since = 0;
@@ -723,7 +764,7 @@ kda_latent_decode_kernel(const __grid_constant__ LatMaps maps, const LatArgs a)
                 tc::mma_commit(&empty[go % NS]);
                 ++go;
                 if (++to == sv.t1) {
-                    more_o = sv.next(a.w);
+                    more_o = sv.next(work);
                     to = sv.t0;
                 }
                 moved = true;
@@ -752,7 +793,7 @@ kda_latent_decode_kernel(const __grid_constant__ LatMaps maps, const LatArgs a)
                 ++gs;
                 if (++ts == sw.t1) {
                     ++qs;
-                    more_s = sw.next(a.w);
+                    more_s = sw.next(work);
                     ts = sw.t0;
                 }
                 moved = true;
@@ -773,11 +814,11 @@ kda_latent_decode_kernel(const __grid_constant__ LatMaps maps, const LatArgs a)
         // ---- TMA: C tiles in boxes of `box` whole rows (one page or a part of one); bf16: Q of each segment ----
         const int nbox = kTile / a.box;
         int g = 0, seg = 0;
-        while (ok && sw.next(a.w)) {
+        while (ok && sw.next(work)) {
             auto pages = [&](int t) {                           // lane i: first cache row of box i of tile t, -1 = past the end
                 const int tok = t * kTile + lane * a.box;
                 if (t >= sw.t1 || lane >= nbox || tok >= sw.len) return -1;
-                int page = a.ch.table[static_cast<size_t>(sw.n) * a.ch.max_pages + tok / a.ch.page_size];
+                int page = a.ch.table[static_cast<size_t>(seq_of(sw.n)) * a.ch.max_pages + tok / a.ch.page_size];
                 if (page < 0 || page >= a.ch.num_pages) { set_status(a.status, kStatusIndex); page = 0; }
                 return page * a.ch.page_size + tok % a.ch.page_size;
             };
@@ -791,7 +832,7 @@ kda_latent_decode_kernel(const __grid_constant__ LatMaps maps, const LatArgs a)
                 __syncwarp();
                 if (lane < 9)
                     tc::tma_load_2d(tc::smem_u32(sQ) + lane * Sh::kSlabQ, &maps.q, 64 * lane,
-                                    static_cast<int>(static_cast<long long>(sw.n) * a.rows + row0), q_full);
+                                    static_cast<int>(static_cast<long long>(seq_of(sw.n)) * a.rows + row_of(sw.n)), q_full);
                 ++seg;
             }
             for (int t = sw.t0; t < sw.t1; ++t, ++g) {
@@ -815,7 +856,7 @@ kda_latent_decode_kernel(const __grid_constant__ LatMaps maps, const LatArgs a)
                     // sequences x 64 heads 209 -> 194 us, 16 x K = 4 x 32 heads 105 -> 97, one of 145408 x 64
                     // heads 55.6 -> 53.3.  (With 32 rows HBM is the bound: 189 -> 205.  Three stages of an e4m3
                     // cache cover it: no change.  Two tiles ahead: 196, 99, 53.7.)
-                    if (rt == 0 && next >= 0) tc::tma_prefetch_4d(&maps.c, 0, 0, 0, next >> 3);
+                    if ((TREE && a.w.each > 1 || rt == 0) && next >= 0) tc::tma_prefetch_4d(&maps.c, 0, 0, 0, next >> 3);
                 }
                 at = next;
             }
@@ -852,12 +893,14 @@ kda_latent_combine_kernel(const LatArgs a, int Q, int NG)
     const int tid = threadIdx.x, grp = tid / lanes, ch = (blockIdx.x % Q * lanes + tid % lanes) * 4;
     const int warps = threads >> 5;
     long long before = 0, T = 0;
-    for (int i = tid; i < a.w.N; i += threads) {
-        const int raw = a.w.seq_lens[i];
-        const int tiles = lat_tiles(lat_len(a.w, i));
-        if (i == n && row == 0 && raw != lat_len(a.w, i)) set_status(a.status, kStatusIndex);   // out of range: counted as 0
-        T += tiles > 0 ? tiles + a.w.lead : 0;
-        if (i < n) before += tiles > 0 ? tiles + a.w.lead : 0;
+    const int seqs = a.w.N / a.w.each, tile = a.w.each > 1 ? row / R : 0;     // (of those that are sequences of their own)
+    if (a.w.each > 1) asm volatile("griddepcontrol.wait;" ::: "memory");    // (for what the trees need)
+    for (int i = tid; i < seqs; i += threads) {
+        const int raw = a.w.seq_lens[i], tiles = lat_tiles(lat_seq(a.w, i)), count = tiles > 0 ? tiles + a.w.lead : 0;
+        if (i == n && row == 0 && raw != lat_seq(a.w, i)) set_status(a.status, kStatusIndex);   // out of range: counted as 0
+        const int need = lat_needed(a.w, a.need, i);
+        T += static_cast<long long>(need) * count;
+        before += static_cast<long long>(min(need, tile) + (i < n && need > tile ? 1 : 0)) * count;
     }
 #pragma unroll
     for (int off = 16; off > 0; off >>= 1) {
@@ -868,7 +911,7 @@ kda_latent_combine_kernel(const LatArgs a, int Q, int NG)
     __syncthreads();
     T = before = 0;
     for (int i = 0; i < warps; ++i) { T += s_sum[0][i]; before += s_sum[1][i]; }
-    const int len = lat_len(a.w, n), tiles = lat_tiles(len);
+    const int tiles = tile < lat_needed(a.w, a.need, n) ? lat_tiles(lat_seq(a.w, n)) : 0;
     const long long at = static_cast<long long>(n) * a.rows + row;
     int c0 = 0, parts = 1, late = 0;
     if (tiles > 0) {
@@ -888,7 +931,7 @@ kda_latent_combine_kernel(const LatArgs a, int Q, int NG)
     if (parts == 1) return;                                      // its CTA finished it
     const int r = row % R;
     const size_t stride = static_cast<size_t>(a.RT) * 2 * R;     // rows of partials between runs
-    const size_t base = (static_cast<size_t>(c0) * a.RT + row / R) * 2 * R + r;
+    const size_t base = (static_cast<size_t>(c0) * a.RT + (a.w.each > 1 ? 0 : row / R)) * 2 * R + r;
     auto slot = [&](int i) { return base + i * stride + (i == 0 && late ? R : 0); };
     float M = -INFINITY, L = 0.f;
     float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
@@ -947,15 +990,20 @@ kda_latent_combine_rows_kernel(const LatArgs a)
 {
     const int lane = threadIdx.x & 31;
     const long long at = static_cast<long long>(blockIdx.x) * 4 + (threadIdx.x >> 5);     // row n * rows + row
-    const int n = static_cast<int>(min(at, static_cast<long long>(a.w.N) * a.rows - 1) / a.rows);
+    const int seqs = a.w.N / a.w.each;
+    const int n = static_cast<int>(min(at, static_cast<long long>(seqs) * a.rows - 1) / a.rows);
     const int row = static_cast<int>(at - static_cast<long long>(n) * a.rows);
+    const int tile = a.w.each > 1 ? min(row, a.rows - 1) / R : 0;            // (of those that are sequences of their own)
     long long T = 0, before = 0;
     int len = 0;
-    for (int i0 = 0; i0 < a.w.N; i0 += 32) {
-        const int i = i0 + lane, v = i < a.w.N ? lat_len(a.w, i) : 0;
+    if (a.w.each > 1) asm volatile("griddepcontrol.wait;" ::: "memory");    // (for what the trees need)
+    for (int i0 = 0; i0 < seqs; i0 += 32) {
+        const int i = i0 + lane, v = i < seqs ? lat_seq(a.w, i) : 0;
         if (i == n && row == 0 && a.w.seq_lens[i] != v) set_status(a.status, kStatusIndex);   // out of range: counted as 0
-        T += lat_count(a.w, v);
-        if (i < n) before += lat_count(a.w, v);
+        const long long count = lat_count(a.w, v);
+        const int need = i < seqs ? lat_needed(a.w, a.need, i) : 0;
+        T += need * count;
+        before += (min(need, tile) + (i < n && need > tile ? 1 : 0)) * count;
         if (n >= i0 && n < i0 + 32) len = __shfl_sync(0xffffffffu, v, n - i0);
     }
 #pragma unroll
@@ -963,7 +1011,7 @@ kda_latent_combine_rows_kernel(const LatArgs a)
         T += __shfl_xor_sync(0xffffffffu, T, off);
         before += __shfl_xor_sync(0xffffffffu, before, off);
     }
-    const int tiles = lat_tiles(len);
+    const int tiles = tile < lat_needed(a.w, a.need, n) ? lat_tiles(len) : 0;
     int c0 = 0, parts = 1, late = 0;
     if (tiles > 0) {
         const long long runs = lat_runs(T, a.w.G);
@@ -982,7 +1030,7 @@ kda_latent_combine_rows_kernel(const LatArgs a)
     }
     if (parts == 1) return;                                      // its CTA finished it
     const size_t stride = static_cast<size_t>(a.RT) * 2 * R;
-    const size_t base = (static_cast<size_t>(c0) * a.RT + row / R) * 2 * R + row % R;
+    const size_t base = (static_cast<size_t>(c0) * a.RT + (a.w.each > 1 ? 0 : row / R)) * 2 * R + row % R;
     float M = -INFINITY, L = 0.f;
     float4 acc[4];
 #pragma unroll
@@ -1078,7 +1126,7 @@ int sm_count() {
 template <int R, bool E4M3, bool TREE>
 int launch_decode_shape(const LatMaps& maps, const LatArgs& a, cudaStream_t stream) {
     using Sh = LatShape<R, E4M3>;
-    constexpr uint32_t bytes = Sh::kBytes + (TREE ? R * 8u : 0u);
+    constexpr uint32_t bytes = Sh::kBytes + (TREE ? R * 8u + kMaxNeed : 0u);
     static bool attr_done[kMaxDevicesAttr] = {};
     if (!raise_smem_limit(reinterpret_cast<const void*>(kda_latent_decode_kernel<R, E4M3, TREE>), static_cast<int>(bytes), attr_done))
         return -3;
@@ -1089,12 +1137,12 @@ int launch_decode_shape(const LatMaps& maps, const LatArgs& a, cudaStream_t stre
     // groups of threads with 8 of them each (4: 1 to 10 us more), a row's channels over 4 blocks where
     // rows are too few for a block on each SM (20 tokens of 48 rows each, 192 rows: 16.5 us with 4, 15.3
     // with 1; 24 rows over 33851 tokens: 19.8 with 4, 27.4 with 1 and a pass each for maxima, sums and O)
-    const int about = a.w.G / a.w.N + 1;
+    const int seqs = a.w.N / a.w.each, about = a.w.G / a.w.N + 1;
     const bool by_warp = about <= 16;
-    const int Q = static_cast<long long>(a.w.N) * a.rows < sm_count() ? 4 : 1;
+    const int Q = static_cast<long long>(seqs) * a.rows < sm_count() ? 4 : 1;
     int NG = 1;
     while (NG < 4 * Q && NG * 8 < about) NG *= 2;
-    cfg.gridDim = dim3(by_warp ? (static_cast<unsigned>(a.w.N) * a.rows + 3) / 4 : static_cast<unsigned>(a.w.N) * a.rows * Q);
+    cfg.gridDim = dim3(by_warp ? (static_cast<unsigned>(seqs) * a.rows + 3) / 4 : static_cast<unsigned>(seqs) * a.rows * Q);
     cfg.blockDim = dim3(by_warp ? 128 : 128 / Q * NG);
     cfg.stream = stream;
     cudaLaunchAttribute at[1];
@@ -1124,9 +1172,12 @@ int latent_decode_runs(int rows) {
     const int G = sms / RT > 0 ? sms / RT : (sms > 0 ? 1 : 0);
     return G < kMaxRuns ? G : kMaxRuns;
 }
-size_t latent_decode_scratch(int rows) {
+// A tree's row tiles as sequences of their own: one run a CTA (see the work split).
+static bool tree_split(int rows, bool tree) { return tree && rows > 64; }
+size_t latent_decode_scratch(int rows, int N, bool tree) {
     const size_t R = rows_per_cta(rows), RT = (rows + R - 1) / R;
-    return static_cast<size_t>(latent_decode_runs(rows)) * RT * 2 * R * (kLatDim + 2) * sizeof(float);
+    const size_t runs = tree_split(rows, tree) ? latent_decode_runs(64) : latent_decode_runs(rows) * RT;
+    return runs * 2 * R * (kLatDim + 2) * sizeof(float) + (tree_split(rows, tree) ? static_cast<size_t>(N) * sizeof(int32_t) : 0);
 }
 
 int launch_latent_decode(const uint16_t* q, const void* cache, int e4m3, int num_pages, int page_size,
@@ -1136,8 +1187,10 @@ int launch_latent_decode(const uint16_t* q, const void* cache, int e4m3, int num
     LatArgs a = {};
     const int rows = K * H, R = rows_per_cta(rows);
     // (a segment's start and end in tiles: the best of 1, 2, 3, 4, 6 and of 4, 6, 8, 10, where Q is split too)
-    a.w = LatWork{seq_lens, N, latent_decode_runs(rows), N == 1 ? 0 : e4m3 && R == 64 ? 8 : 2, parents ? K : 0,
-                  static_cast<long long>(max_pages) * page_size};
+    const bool apart = tree_split(rows, parents != nullptr);
+    const int each = apart ? (rows + R - 1) / R : 1;
+    a.w = LatWork{seq_lens, N * each, latent_decode_runs(apart ? 64 : rows), N * each == 1 ? 0 : e4m3 && R == 64 ? 8 : 2, parents ? K : 0,
+                  static_cast<long long>(max_pages) * page_size, each, nullptr};
     if (a.w.G <= 0) return -3;
     a.ch = LatentCache{static_cast<const uint8_t*>(cache), table, num_pages, page_size, max_pages};
     a.q = q;
@@ -1145,13 +1198,14 @@ int launch_latent_decode(const uint16_t* q, const void* cache, int e4m3, int num
     a.K = K;
     a.H = H;
     a.rows = rows;
-    a.RT = (rows + R - 1) / R;
+    a.RT = apart ? 1 : (rows + R - 1) / R;
     a.box = page_size % 64 == 0 ? 64 : page_size % 32 == 0 ? 32 : 16;
     a.scale_log2 = sm_scale * 1.4426950408889634f;
     a.out = out;
     a.lse = lse;
     a.part_o = static_cast<float*>(scratch);
     a.part_ml = a.part_o + static_cast<size_t>(a.w.G) * a.RT * 2 * R * kLatDim;
+    a.need = reinterpret_cast<int32_t*>(a.part_ml + static_cast<size_t>(a.w.G) * a.RT * 2 * R * 2);
     a.status = status;
     LatMaps maps;
     const CUtensorMapSwizzle swz = CU_TENSOR_MAP_SWIZZLE_128B;
