@@ -378,8 +378,10 @@ int kda_decode_multi(const uint16_t* q, const uint16_t* k, const uint16_t* v,
  *   parents     as above
  *   out         (device) [N, K, H, Dv], bf16 or fp32 per out_dtype; zeros for a place without a node
  * State slots need not be distinct.  An out-of-range slot skips its sequence (out is left as it
- * was) and is reported.  Dk == Dv in {64, 128}.  Deterministic.  fp32 throughout: the result
- * differs from that of kda_decode_multi on the same path in the order of its sums.
+ * was) and is reported.  Dk == Dv in {64, 128}.  Deterministic.  Products keep 22 bits of each
+ * factor and sums are fp32, in another order than kda_decode_multi's on the same path (a few 1e-7 of
+ * the outputs' magnitudes off).  A state that holds NaN or infinities, or a magnitude above 3.4e38 / 2,
+ * may make its outputs NaN; one that only a node's inputs bring reaches its descendants alone.
  */
 int kda_decode_tree(const uint16_t* q, const uint16_t* k, const uint16_t* v,
                     const float* log_alpha, const uint16_t* beta,

@@ -14,7 +14,9 @@
 //
 // The product P^T [128 columns x 2 K] = S_0^T [128 x D] rows^T [D x 2 K] runs on the tensor cores with S_0^T in TMEM (its
 // lanes are the state's columns, a thread's a column), as three tf32 products of the operands' leading 11 bits and what is left of them: 22 bits, an fp32
-// product but for 2^-21.  So do L and N, as products of the decayed rows with the keys over their decays (CTAs in which a
+// product but for 2^-21.  The tensor cores round sums towards zero: the two small products have an accumulator of their own, or
+// go first, and W (V - P) is not added to Q there (errors of 64 x 8 heads of 64 x 64, 48 nodes, against 64 bits:
+// 1.4e-6 -> 2.5e-7).  So do L and N, as products of the decayed rows with the keys over their decays (CTAs in which a
 // decay leaves 2^-100 .. 2^100 walk their paths instead), and W (V - P), with V - P in TMEM in S_0^T's place (a NaN
 // or an infinity in it enters as 0, and is put back for the nodes whose paths hold it: 0 * NaN is none).
 #include "common.cuh"
@@ -63,6 +65,8 @@ struct TreeShape {
     static constexpr uint32_t kL = kApart ? kProduct : kD, kUsed = kL + kChunks * kRows;
     static constexpr uint32_t kCols = kUsed <= 128u ? 128u : kUsed <= 256u ? 256u : 512u;
     static_assert(kCols <= kMost && 2 * KP <= kD, "TMEM");
+    static_assert(KC >= 16 || kApart, "16 columns of W (V - P) in L's place");
+    static_assert(kStack || kWhole, "the small products first: the state is there twice");
     static_assert(kApart || kBufs == kSlabs, "the first products do not wait for what follows the last slab");
     // bytes of shared memory.  (The side's products read 64 rows from each item's first: what follows it, beyond KP)
     static constexpr uint32_t oSide = 0, oRows = oSide + kSides, oState = oRows + kTiles;
@@ -118,8 +122,10 @@ __device__ __forceinline__ void tree_copy4(uint32_t dst, const void* src) {
     asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" :: "r"(dst), "l"(src) : "memory");
 }
 __device__ __forceinline__ void tree_copies_done() { asm volatile("cp.async.wait_all;" ::: "memory"); }
-// The leading 11 bits of x; x less these is exact.
-__device__ __forceinline__ float tree_lead(float x) { return __uint_as_float(__float_as_uint(x) & 0xffffe000u); }
+// x rounded to its leading 11 bits (to the nearest: what is left is then as often negative, and so are the products that are
+// left out); x less these is exact.  (A NaN that turns into a number here is still one in x less it.)
+__device__ __forceinline__ float tree_lead(float x) { return __uint_as_float((__float_as_uint(x) + 0x1000u) & 0xffffe000u); }
+constexpr float kTreeMost = 0x1.ffep127f;        // from here on it would be infinite
 
 template <bool WIDE> struct TreeBits { using type = uint32_t; };
 template <> struct TreeBits<true> { using type = uint64_t; };
@@ -336,11 +342,13 @@ kda_tree_kernel(const TreeArgs a)
                                 const uint32_t sa = tree_desc(sm0 + Sh::oSide + it * Sh::kSideItem * 128u);
                                 const uint32_t sb = tree_desc(sm0 + Sh::oRows + it * Sh::kItem * 128u);
 #pragma unroll
-                                for (uint32_t k = 0; k < kSlabs * 4u; ++k) {
+                                for (uint32_t x = 0; x < (Sh::kStack ? 1u : 2u) * kSlabs * 4u; ++x) {
+                                    const uint32_t k = x % (kSlabs * 4u);
                                     const uint32_t pa = sa + (k >> 2) * (Sh::kSideRows * 8u) + (k & 3) * 2u, pb = sb + (k >> 2) * (Sh::kRows * 8u) + (k & 3) * 2u;
-                                    tree_mma_ss(d, pa, pb, id_side, k > 0 ? 1u : 0u);
-                                    if constexpr (!Sh::kStack) {
-                                        tree_mma_ss(d, pa, pb + Sh::kRest / 16u, id_side, 1u);
+                                    if (Sh::kStack || x >= kSlabs * 4u) {
+                                        tree_mma_ss(d, pa, pb, id_side, x > 0 ? 1u : 0u);
+                                    } else {
+                                        tree_mma_ss(d, pa, pb + Sh::kRest / 16u, id_side, x > 0 ? 1u : 0u);
                                         tree_mma_ss(d, pa + Sh::kSide / 16u, pb, id_side, 1u);
                                     }
                                 }
@@ -367,37 +375,45 @@ kda_tree_kernel(const TreeArgs a)
                         const uint32_t ta = tm + b * 64, rows = tree_desc(sm0 + Sh::oRows + q * (Sh::kRows * 128u));
 #pragma unroll
                         for (uint32_t k = 0; k < 4; ++k) {
-                            // (stacked: both terms of the rows, their accumulators side by side)
-                            tree_mma(d, ta + k * 8u, rows + k * 2u, id, q == 0 && k == 0 ? 0u : 1u);
+                            // (stacked: both terms of the rows, their accumulators side by side, the small ones' second)
                             if constexpr (Sh::kStack) {
+                                tree_mma(d, ta + k * 8u, rows + k * 2u, id, q == 0 && k == 0 ? 0u : 1u);
 #pragma unroll
                                 for (uint32_t it = 0; it < kItems; ++it)
-                                    tree_mma(d + it * Sh::kItem, ta + 32u + k * 8u, rows + it * Sh::kItem * 8u + k * 2u, id_rest, 1u);
+                                    tree_mma(d + it * Sh::kItem + 2 * KC, ta + 32u + k * 8u, rows + it * Sh::kItem * 8u + k * 2u, id_rest, 1u);
                             } else {
-                                tree_mma(d, ta + k * 8u, rows + Sh::kRest / 16u + k * 2u, id, 1u);
+                                tree_mma(d, ta + k * 8u, rows + Sh::kRest / 16u + k * 2u, id, q == 0 && k == 0 ? 0u : 1u);
                                 tree_mma(d, ta + 32u + k * 8u, rows + k * 2u, id, 1u);
                             }
                         }
                         if (!Sh::kWhole) tc::mma_commit(&b_free[b]);
                     }
+                    if (!Sh::kStack && ok)
+#pragma unroll
+                        for (uint32_t x = 0; x < kSlabs * 4u; ++x)
+                            tree_mma(d, tm + (x >> 2) * 64 + (x & 3) * 8u,
+                                     tree_desc(sm0 + Sh::oRows + (x >> 2) * (Sh::kRows * 128u)) + (x & 3) * 2u, id, 1u);
                     if (ok) tc::mma_commit(b_prod);
                 }
                 if (!ok) break;
                 ok = tc::mbar_wait_bounded(b_e, turn & 1, kWaitLimitNs);
                 if (!ok) break;
                 tc::fence_after_sync();
-                // Q += W (V - P), per item and chunk
+                // W (V - P), per item and chunk, where L was
                 for (int chunk = 0; chunk < kChunks; ++chunk)
 #pragma unroll 1
                     for (int it = 0; it < kItems; ++it) {
-                        const uint32_t d = tm + Sh::kD + chunk * Sh::kRows + it * Sh::kItem + KC;
+                        const uint32_t d = tm + Sh::kL + chunk * Sh::kRows + it * Sh::kItem;
                         const uint32_t sw = tree_desc(sm0 + Sh::oW + (it * Sh::kWRows + chunk * KC) * 128u);
 #pragma unroll
-                        for (uint32_t k = 0; k < KP / 8; ++k) {
-                            const uint32_t at = sw + (k >> 2) * (kItems * Sh::kWRows * 8u) + (k & 3) * 2u;
-                            tree_mma(d, tm + k * 8u, at, id_w, 1u);
-                            tree_mma(d, tm + k * 8u, at + Sh::kW / 16u, id_w, 1u);
-                            tree_mma(d, tm + KP + k * 8u, at, id_w, 1u);
+                        for (uint32_t x = 0; x < KP / 4; ++x) {
+                            const uint32_t k = x % (KP / 8), at = sw + (k >> 2) * (kItems * Sh::kWRows * 8u) + (k & 3) * 2u;
+                            if (x >= KP / 8) {
+                                tree_mma(d, tm + k * 8u, at, id_w, 1u);
+                            } else {
+                                tree_mma(d, tm + k * 8u, at + Sh::kW / 16u, id_w, x > 0 ? 1u : 0u);
+                                tree_mma(d, tm + KP + k * 8u, at, id_w, 1u);
+                            }
                         }
                     }
                 tc::mma_commit(b_w);
@@ -749,7 +765,7 @@ kda_tree_kernel(const TreeArgs a)
 #pragma unroll
                 for (int r = 0; r < 8; ++r) {
                     float d = set[i0 + r] != 0 ? bf16_bits_to_f32(v[(i0 + r) * D]) - x[r] : 0.f;
-                    if (!(fabsf(d) < INFINITY)) {
+                    if (!(fabsf(d) < kTreeMost)) {
                         none |= kOne << (i0 + r);
                         d = 0.f;
                     }
@@ -778,14 +794,15 @@ kda_tree_kernel(const TreeArgs a)
             const size_t to = now.token(item, 0, a.K, a.H) * D + col;
 #pragma unroll 1
             for (int i0 = 8 * group; i0 < a.K; i0 += 16) {
-                float o[8];
+                float o[8], x8[8];
                 rows_at(i0, 1, o);
+                tree_tmem_ld8(lane_tm + Sh::kL + (i0 / KC) * Sh::kRows + item * Sh::kItem + i0 % KC, x8);
                 if (slot < 0 || !ok) continue;
 #pragma unroll
                 for (int r = 0; r < 8; ++r) {
                     if (i0 + r >= a.K) break;
                     const Set on = set[i0 + r];
-                    float x = on ? o[r] : 0.f;
+                    float x = on ? o[r] + x8[r] : 0.f;
                     if (on & none) x = __int_as_float(0x7fffffff);
                     if (a.out_f32) reinterpret_cast<float*>(a.out)[to + (i0 + r) * step] = x;
                     else reinterpret_cast<uint16_t*>(a.out)[to + (i0 + r) * step] = f32_to_bf16_bits(x);

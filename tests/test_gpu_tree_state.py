@@ -182,3 +182,18 @@ def test_many_heads_one_after_another(K, D, decay):
         assert torch.equal(got[n], alone[0]), n
     n = 90
     check(got[n:], [None if t is None else t[n:] for t in x], pool[n:], rows[n:], [0])
+
+
+@pytest.mark.parametrize("D,K,decay", [(64, 6, CH), (64, 48, HD), (128, 16, CH), (128, 30, NO), (128, 64, CH)])
+def test_sums_do_not_lean(D, K, decay):
+    """The tensor cores take 8 terms a step and round the sum towards zero, by up to 2^-23 of it: D / 8 steps of the state's
+    product, K / 8 of the path's, half of that on average and on one side.  With 4 half steps for the rest, that bounds the
+    errors' root mean square by (D / 8 + K / 8 + 4) 2^-24 of the outputs'."""
+    x, pool = inputs(4, K, 4, D, decay, seed=K + D)
+    rows = [T.tree(K, n, 6) for n in range(4)]
+    got = run(x, pool, rows, decay=decay).double().cpu()
+    _ok()
+    q, k, v, la, beta = x
+    ref = torch.stack([T.state_outputs(q[n], k[n], v[n], None if la is None else la[n], beta[n], pool[n], rows[n])[0] for n in range(4)])
+    rel = float((got - ref).norm() / ref.norm())
+    assert rel <= (D / 8 + K / 8 + 4) * 2.0 ** -24, f"{rel:.2g}"
