@@ -194,9 +194,13 @@ struct LatArgs {
 
 template <int R, bool E4M3>
 struct LatShape {
-    static constexpr int kSoft = 128;            // warps 0..3: softmax, rescale, epilogue
-    static constexpr int kMmaWarp = 4, kTmaWarp = 5;
-    static constexpr int kThreads = 192;
+    // softmax, rescale, epilogue: groups of 4 warps, each RW rows of a tile (64 rows, one group of 4 warps to two: 16 trees of
+    // 4 to 8 nodes x 32 heads over 341k tokens, e4m3, 204 -> 184 us; one of 12 nodes x 4 heads over 1500 tokens, bf16, 17.6 -> 14.4;
+    // 16 chains of 8 x 32 over the same, e4m3, 229 -> 223)
+    static constexpr int kGroups = R == 64 ? 2 : 1, RW = R / kGroups;
+    static constexpr int kSoft = 128 * kGroups;
+    static constexpr int kMmaWarp = 4 * kGroups, kTmaWarp = kMmaWarp + 1;
+    static constexpr int kThreads = kSoft + 64;
     // as many as fit: a stage is taken for a copy's latency (about 3000 clocks) and both products
     static constexpr int kStages = E4M3 ? (R <= 32 ? 4 : 3) : 2;
     static constexpr uint32_t kSlabQ = R * 128u;
@@ -297,7 +301,7 @@ __device__ __forceinline__ bool drop_nonfinite(uint8_t* c, int lo, int hi, int t
 // (Of a tree's nodes, the rows that see one of them: `seen`, else the rows that see past the first.)
 template <int R, bool TREE>
 __device__ __noinline__ void mark_nonfinite(const LatentCache& ch, int n, int clear, int from, int to, const int* s_j,
-                                            const uint64_t* seen, uint32_t ta, int channel) {
+                                            const uint64_t* seen, uint32_t ta, int channel, int row_g) {
 #pragma unroll 1
     for (int b = 0; b < 4; ++b) {
         int first = 0x7fffffff;                                  // the first such token: rows that see past it
@@ -313,7 +317,7 @@ __device__ __noinline__ void mark_nonfinite(const LatentCache& ch, int n, int cl
         }
         if (!__any_sync(0xffffffffu, TREE ? nodes != 0 : first != 0x7fffffff)) continue;
 #pragma unroll 1
-        for (int c0 = 0; c0 < R; c0 += 16) {
+        for (int c0 = row_g; c0 < row_g + LatShape<R, false>::RW; c0 += 16) {
             float o[16];
             tc::tmem_ld16(ta + b * R + c0, o);
             tc::tmem_wait_ld();
@@ -394,15 +398,17 @@ kda_latent_decode_kernel(const __grid_constant__ LatMaps maps, const LatArgs a)
     sw.init(work, run);
     bool ok = true;
 
-    if (warp < 4) {
-        // ---- softmax ----
-        const int tq = lane >> 2, rq = 2 * (lane & 3);
-        const uint32_t lane_tm = static_cast<uint32_t>(warp * 32) << 16;
-        float m[R / 4], l[R / 4];
+    if (warp < Sh::kMmaWarp) {
+        // ---- softmax: rows row_g .. + RW, a thread's tokens and rows of them as tmem_ld_s gives them ----
+        constexpr int RW = Sh::RW;
+        const int wq = warp & 3, row_g = (warp >> 2) * RW;
+        const int tq = lane >> 2, rq = row_g + 2 * (lane & 3);
+        const uint32_t lane_tm = static_cast<uint32_t>(wq * 32) << 16;
+        float m[RW / 4], l[RW / 4];
         int g = 0;                                              // tiles done by this CTA
         while (ok && sw.next(work)) {
 #pragma unroll
-            for (int i = 0; i < R / 4; ++i) { m[i] = -INFINITY; l[i] = 0.f; }
+            for (int i = 0; i < RW / 4; ++i) { m[i] = -INFINITY; l[i] = 0.f; }
             const int clear = sw.len - (TREE ? a.K : a.K - 1);  // tokens that every row sees
             const int seq = seq_of(sw.n), row0 = row_of(sw.n), nrows = rows_of(sw.n);
             bool spoilt = false;                                // a later one held a NaN or infinity
@@ -423,19 +429,19 @@ kda_latent_decode_kernel(const __grid_constant__ LatMaps maps, const LatArgs a)
                 // Q of the segment (the last S product of the segment before has run): a warp a row, the
                 // loads of 4 rows in flight
 #pragma unroll 1
-                for (int rb = warp; rb < R; rb += 16) {
+                for (int rb = warp; rb < R; rb += 4 * Sh::kMmaWarp) {
                     uint4 w0[4], w1[4];
                     uint32_t rope[4];
 #pragma unroll
                     for (int k = 0; k < 4; ++k) {
-                        const uint16_t* src = a.q + (static_cast<long long>(seq) * a.rows + row0 + min(rb + 4 * k, nrows - 1)) * kLatQ;
+                        const uint16_t* src = a.q + (static_cast<long long>(seq) * a.rows + row0 + min(rb + Sh::kMmaWarp * k, nrows - 1)) * kLatQ;
                         w0[k] = reinterpret_cast<const uint4*>(src)[2 * lane];
                         w1[k] = reinterpret_cast<const uint4*>(src)[2 * lane + 1];
                         rope[k] = reinterpret_cast<const uint32_t*>(src + kLatDim)[lane];
                     }
 #pragma unroll
                     for (int k = 0; k < 4; ++k) {
-                        const int r = rb + 4 * k;
+                        const int r = rb + Sh::kMmaWarp * k;
                         const uint32_t wv[8] = {w0[k].x, w0[k].y, w0[k].z, w0[k].w, w1[k].x, w1[k].y, w1[k].z, w1[k].w};
                         uint32_t top2 = 0u;                     // largest magnitudes by their bits, two at a time
 #pragma unroll
@@ -473,15 +479,15 @@ kda_latent_decode_kernel(const __grid_constant__ LatMaps maps, const LatArgs a)
             }
             for (int t = sw.t0; t < sw.t1; ++t, ++g) {
                 ok = __all_sync(0xffffffffu, ok && tc::mbar_wait_bounded(&s_full[g & 1], (g >> 1) & 1, kWaitLimitNs));
-                float x[R / 2];
+                float x[RW / 2];
                 float s0 = 1.f, s1 = 1.f, e0 = 0.f, e1 = 0.f;   // e4m3: scales of the thread's two tokens, their exponents
                 if (ok) {
                     tc::fence_after_sync();
-                    tmem_ld_s<R>(tmS + (g & 1) * Sh::kS + lane_tm, x);
+                    tmem_ld_s<RW>(tmS + (g & 1) * Sh::kS + row_g + lane_tm, x);
                     if constexpr (E4M3) {
                         const float* sc = reinterpret_cast<const float*>(sC + g % NS * Sh::kStage + Sh::kRows);
-                        s0 = sc[(16 * warp + tq) * 4];
-                        s1 = sc[(16 * warp + tq + 8) * 4];
+                        s0 = sc[(16 * wq + tq) * 4];
+                        s1 = sc[(16 * wq + tq + 8) * 4];
                         // (held above -90, so that the sums of 2^(x - m) stay within fp32; see f0, f1)
                         e0 = static_cast<float>(max(static_cast<int>(__float_as_uint(s0) >> 23) - 127, -90));
                         e1 = static_cast<float>(max(static_cast<int>(__float_as_uint(s1) >> 23) - 127, -90));
@@ -490,24 +496,24 @@ kda_latent_decode_kernel(const __grid_constant__ LatMaps maps, const LatArgs a)
                         float a0 = e0, a1 = e1;
                         if (!(fabsf(s0) < INFINITY)) { a0 = __int_as_float(0x7fffffff); s0 = 1.f; e0 = 0.f; }
                         if (!(fabsf(s1) < INFINITY)) { a1 = __int_as_float(0x7fffffff); s1 = 1.f; e1 = 0.f; }
-                        float xr[R / 2];
-                        tmem_ld_s<R>(tmS + (g & 1) * Sh::kS + R + lane_tm, xr);
+                        float xr[RW / 2];
+                        tmem_ld_s<RW>(tmS + (g & 1) * Sh::kS + R + row_g + lane_tm, xr);
                         // x: scores in powers of two, plus the scale's exponent (the weights carry s)
 #pragma unroll
-                        for (int i = 0; i < R / 2; ++i) {
+                        for (int i = 0; i < RW / 2; ++i) {
                             const float sa = s_a[8 * (i >> 2) + rq + (i & 1)] * (i & 2 ? s1 : s0);
                             x[i] = fmaf(x[i], sa, fmaf(xr[i], a.scale_log2, i & 2 ? a1 : a0));
                         }
                     } else {
 #pragma unroll
-                        for (int i = 0; i < R / 2; ++i) x[i] *= a.scale_log2;
+                        for (int i = 0; i < RW / 2; ++i) x[i] *= a.scale_log2;
                     }
                 }
-                const int tok = t * kTile + 16 * warp + tq;     // and tok + 8
+                const int tok = t * kTile + 16 * wq + tq;     // and tok + 8
                 const bool edge = (t + 1) * kTile > clear;
                 if (edge) {
 #pragma unroll
-                    for (int i = 0; i < R / 2; ++i) {
+                    for (int i = 0; i < RW / 2; ++i) {
                         const int r = 8 * (i >> 2) + rq + (i & 1);
                         if constexpr (TREE) {
                             const int node = tok + 4 * (i & 2) - clear;
@@ -527,8 +533,8 @@ kda_latent_decode_kernel(const __grid_constant__ LatMaps maps, const LatArgs a)
                             *reinterpret_cast<uint4*>(c + (r >> 3) * Sh::kGroup + slab * Sh::kSlabC + (r & 7) * 128 + ch * 16) = make_uint4(0, 0, 0, 0);
                         }
                         if (E4M3) {                             // and their scales are not to be used
-                            if (16 * warp + tq >= valid) { s0 = 1.f; e0 = 0.f; }
-                            if (16 * warp + tq + 8 >= valid) { s1 = 1.f; e1 = 0.f; }
+                            if (16 * wq + tq >= valid) { s0 = 1.f; e0 = 0.f; }
+                            if (16 * wq + tq + 8 >= valid) { s1 = 1.f; e1 = 0.f; }
                         }
                     }
                     if (ok && (TREE || a.K > 1))
@@ -536,7 +542,7 @@ kda_latent_decode_kernel(const __grid_constant__ LatMaps maps, const LatArgs a)
                 }
                 bool grow = !ok;
 #pragma unroll
-                for (int i = 0; i < R / 2; ++i) grow |= x[i] > m[2 * (i >> 2) + (i & 1)] + kMost<E4M3>;
+                for (int i = 0; i < RW / 2; ++i) grow |= x[i] > m[2 * (i >> 2) + (i & 1)] + kMost<E4M3>;
                 bool waited = g == 0;                           // for the previous tile's product: it has read P and is in O
                 if (!tc::named_sync_and(kBarSoft, Sh::kSoft, !grow)) {
                     if (ok && !waited) ok = tc::mbar_wait_bounded(&empty[(g - 1) % NS], (g - 1) / NS & 1, kWaitLimitNs);
@@ -545,28 +551,28 @@ kda_latent_decode_kernel(const __grid_constant__ LatMaps maps, const LatArgs a)
                     if (!ok) break;
                     tc::fence_after_sync();
 #pragma unroll
-                    for (int i = 0; i < R / 4; ++i) {           // maxima of the tile, per row
+                    for (int i = 0; i < RW / 4; ++i) {           // maxima of the tile, per row
                         float v = fmaxf(x[4 * (i >> 1) + (i & 1)], x[4 * (i >> 1) + 2 + (i & 1)]);
                         v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, 4));
                         v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, 8));
                         v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, 16));
-                        if (lane < 4) s_red[warp * R + 8 * (i >> 1) + rq + (i & 1)] = v;
+                        if (lane < 4) s_red[wq * R + 8 * (i >> 1) + rq + (i & 1)] = v;
                     }
                     tc::named_sync(kBarSoft, Sh::kSoft);
 #pragma unroll
-                    for (int i = 0; i < R / 4; ++i) {
+                    for (int i = 0; i < RW / 4; ++i) {
                         const int r = 8 * (i >> 1) + rq + (i & 1);
                         const float mx = fmaxf(fmaxf(s_red[r], s_red[R + r]), fmaxf(s_red[2 * R + r], s_red[3 * R + r]));
                         const float mn = fmaxf(m[i], mx - kAbove<E4M3>);
                         const float f = mn == m[i] ? 1.f : lat_ex2(m[i] - mn);
                         m[i] = mn;
                         l[i] *= f;
-                        if (tid < 4) s_f[r] = f;
+                        if (wq == 0 && lane < 4) s_f[r] = f;
                     }
                     tc::named_sync(kBarSoft, Sh::kSoft);
                     if (t > sw.t0) {                            // O *= f, 16 columns (rows) at a time
 #pragma unroll 1
-                        for (int c0 = 0; c0 < static_cast<int>(Sh::kO); c0 += 16) {
+                        for (int c0 = row_g; c0 < (Sh::kGroups > 1 ? row_g + RW : static_cast<int>(Sh::kO)); c0 += 16) {
                             const float* f = s_f + c0 % R;
                             bool one = true;
 #pragma unroll
@@ -587,13 +593,13 @@ kda_latent_decode_kernel(const __grid_constant__ LatMaps maps, const LatArgs a)
                 }
                 // P = exp2(x - m), rounded for the product (see above); the sums keep fp32.  It is made in
                 // registers while the previous tile's product still reads P
-                const int tr = 16 * warp + tq;
+                const int tr = 16 * wq + tq;
                 // e4m3: exp2(x - m) carries 2^e; the sums take it out (r0, r1), and a scale below 2^-90 puts the
                 // rest of it in (f0, f1, else 1).  A NaN score leaves no NaN in P, but one in the sums
                 const float r0 = lat_ex2(-e0), r1 = lat_ex2(-e1), f0 = s0 * r0, f1 = s1 * r1;
-                uint32_t pk[E4M3 ? 3 * (R / 8) : R / 4];
+                uint32_t pk[E4M3 ? 3 * (RW / 8) : RW / 4];
 #pragma unroll
-                for (int b = 0; b < R / 8; ++b) {
+                for (int b = 0; b < RW / 8; ++b) {
                     const float m0 = m[2 * b] == -INFINITY ? 0.f : m[2 * b], m1 = m[2 * b + 1] == -INFINITY ? 0.f : m[2 * b + 1];
                     const float p0 = lat_ex2(x[4 * b] - m0), p1 = lat_ex2(x[4 * b + 1] - m1);
                     const float p2 = lat_ex2(x[4 * b + 2] - m0), p3 = lat_ex2(x[4 * b + 3] - m1);
@@ -620,7 +626,7 @@ kda_latent_decode_kernel(const __grid_constant__ LatMaps maps, const LatArgs a)
                 ok = __all_sync(0xffffffffu, ok);
                 if (!ok) continue;
 #pragma unroll
-                for (int b = 0; b < R / 8; ++b) {
+                for (int b = 0; b < RW / 8; ++b) {
                     if constexpr (!E4M3) {
                         const uint32_t off = tc::sw128_off16(tr, 8 * b + rq, kTile);
                         *reinterpret_cast<uint32_t*>(sP + off) = pk[2 * b];
@@ -645,18 +651,18 @@ kda_latent_decode_kernel(const __grid_constant__ LatMaps maps, const LatArgs a)
             if (!ok) break;
             tc::fence_after_sync();
 #pragma unroll
-            for (int i = 0; i < R / 4; ++i) {
+            for (int i = 0; i < RW / 4; ++i) {
                 float v = l[i];
                 v += __shfl_xor_sync(0xffffffffu, v, 4);
                 v += __shfl_xor_sync(0xffffffffu, v, 8);
                 v += __shfl_xor_sync(0xffffffffu, v, 16);
                 const int r = 8 * (i >> 1) + rq + (i & 1);
-                if (lane < 4) s_red[warp * R + r] = v;
-                if (tid < 4) s_f[r] = m[i];
+                if (lane < 4) s_red[wq * R + r] = v;
+                if (wq == 0 && lane < 4) s_f[r] = m[i];
             }
             if (!tc::named_sync_and(kBarSoft, Sh::kSoft, !spoilt) && !E4M3)
                 mark_nonfinite<R, TREE>(a.ch, seq, clear, sw.t0 * kTile, min(sw.len, sw.t1 * kTile), s_j, s_set, tmO + lane_tm,
-                                        32 * warp + lane);
+                                        32 * wq + lane, row_g);
             const bool whole = sw.whole();
             const long long row_at = static_cast<long long>(seq) * a.rows + row0;
             const size_t part = (static_cast<size_t>(run) * a.RT + rt) * 2 + (sw.first ? 0 : 1);
@@ -671,11 +677,11 @@ kda_latent_decode_kernel(const __grid_constant__ LatMaps maps, const LatArgs a)
                 s_f[tid] = sum == 0.f ? 0.f : 1.f / sum;
             }
             tc::named_sync(kBarSoft, Sh::kSoft);
-            const int ch = 32 * warp + lane;
+            const int ch = 32 * wq + lane;
             if (!whole) {
                 float* d32 = a.part_o + part * R * kLatDim + ch;
 #pragma unroll 1
-                for (int c = 0; c < R / 4; ++c) {                // 16 rows x 128 channels a step
+                for (int c = row_g / 4; c < (row_g + RW) / 4; ++c) {     // 16 rows x 128 channels a step
                     float o[16];
                     load_o<R, Sh::kSide>(tmO + (c & 3) * Sh::kO + (c >> 2) * 16 + lane_tm, o);
                     float* d = d32 + (c >> 2) * 16 * kLatDim + (c & 3) * 128;
@@ -689,7 +695,7 @@ kda_latent_decode_kernel(const __grid_constant__ LatMaps maps, const LatArgs a)
                 const uint32_t sel = odd ? 0x3276u : 0x5410u;
                 uint16_t* d16 = a.out + (row_at + odd) * kLatDim + (ch - odd);
 #pragma unroll 1
-                for (int c = 0; c < R / 4; ++c) {
+                for (int c = row_g / 4; c < (row_g + RW) / 4; ++c) {
                     const int c0 = (c >> 2) * 16;
                     if (c0 >= nrows) break;
                     float o[16];
