@@ -10,7 +10,7 @@
 // a path are products of alphas, which neither overflow nor cancel.  With L_ab = beta_a [k_a . A(a, b) k_b] and N the
 // second bracket, both on paths alone, and V, P, Q the rows v, S_0^T (A k), S_0^T (A q), that is
 //     O = Q + W (V - P),      W = N (I + L)^-1 Diag(beta),
-// where W is K x K numbers a head, a row of which a warp finds by substitution along the node's path.
+// where W is K x K numbers a head, found by substitution: by lanes of a warp a row, along the node's path or over all places.
 //
 // The product P^T [128 columns x 2 K] = S_0^T [128 x D] rows^T [D x 2 K] runs on the tensor cores with S_0^T in TMEM (its
 // lanes are the state's columns, a thread's a column), as three tf32 products of the operands' leading 11 bits and what is left of them: 22 bits, an fp32
@@ -81,8 +81,11 @@ struct TreeShape {
     static constexpr uint32_t oNone = oRows;                            // of 256 threads: places that are no number
     static constexpr int kRounds = KP == 8 ? 3 : KP == 16 ? 4 : KP == 32 ? 5 : 6;      // of the decays' products, doubling their reach
     static constexpr uint32_t oSet = oV + kNodes * D * 2u, oBeta = oSet + 2 * kNodes * kBit, oUp = oBeta + 2 * kNodes * 2u;
-    static constexpr uint32_t oFar = oUp + 2 * kNodes, oBar = oFar + 2 * kRounds * kNodes;
-    static constexpr uint32_t kBytes = oBar + 224u;
+    static constexpr uint32_t oFar = oUp + 2 * kNodes, oDesc = oFar + 2 * kRounds * kNodes, oBar = oDesc + 2 * kNodes * kBit;
+    static constexpr uint32_t kBytes = oBar + 256u;
+    // W by whole rows of L (else along the paths), where a row has so many lanes, and a lane so many quads of places
+    static constexpr bool kDense = KP > 16;
+    static constexpr int kWLanes = KP / 4 < 256 / kNodes ? KP / 4 : 256 / kNodes, kQuads = KP / 4 / kWLanes;
     static_assert(kBytes <= (kCtas == 1 ? 232448u : kCtas == 2 ? 115712u : 76800u), "shared memory");
     static_assert(oState >= oSide + kSides + 8192u, "the side's last products stay within");
     static_assert(256u * kBit <= kTiles && D % CH == 0, "none; channels");
@@ -160,6 +163,7 @@ kda_tree_kernel(const TreeArgs a)
     uint16_t* s_betas = reinterpret_cast<uint16_t*>(sm + Sh::oBeta);    // [2][place]
     int8_t* s_ups = reinterpret_cast<int8_t*>(sm + Sh::oUp);            // [2][place]: of the parent, -1 without one, -2 without a node
     int8_t* s_fars = reinterpret_cast<int8_t*>(sm + Sh::oFar);          // [2][round][place]: the ancestor 2^round up, -1 without one
+    Set* s_descs = reinterpret_cast<Set*>(sm + Sh::oDesc);              // [2][place]: the places whose paths it is on
     uint64_t* bars = reinterpret_cast<uint64_t*>(sm + Sh::oBar);
     uint64_t *b_full = bars, *b_empty = bars + 4;                       // a slab is in shared memory; has been read
     uint64_t *b_put = bars + 8, *b_free = bars + 12;                    // is in TMEM; its products are done
@@ -170,6 +174,7 @@ kda_tree_kernel(const TreeArgs a)
     uint64_t *b_last = bars + 22, *b_tree = bars + 14, *b_done = bars + 24;
     uint32_t* s_tmem = reinterpret_cast<uint32_t*>(bars + 23);
     int* s_walk = reinterpret_cast<int*>(bars + 26);                    // [2]: of even and odd turns
+    Set* s_bad = reinterpret_cast<Set*>(bars + 27);                     // [2][item]: places whose row of L holds no number
 
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     if (tid == 0) {
@@ -187,13 +192,14 @@ kda_tree_kernel(const TreeArgs a)
         }
         tc::mbar_init(b_rows, 256);
         tc::mbar_init(b_side, 1);
-        tc::mbar_init(b_read, 128);
+        tc::mbar_init(b_read, 256);
         tc::mbar_init(b_prod, 1);
         tc::mbar_init(b_e, 256);
         tc::mbar_init(b_w, 1);
         tc::mbar_init(b_last, 1);
         tc::mbar_fence_init();
         s_walk[0] = s_walk[1] = 0;
+        for (int i = 0; i < 2 * kItems; ++i) s_bad[i] = 0;
     }
     if (warp == 8) tc::tmem_alloc(s_tmem, Sh::kCols);
     tc::fence_before_sync();
@@ -224,6 +230,7 @@ kda_tree_kernel(const TreeArgs a)
     };
     bool ok = true;
     const uint32_t begin = blockIdx.x * static_cast<uint32_t>(kItems);
+    const int chunks = kChunks == 1 ? 1 : (a.K + KC - 1) / KC;          // (of the places that there are)
 
     if (warp == 9) {
         // ---- the trees; the state: slabs of 32 channels through the ring; all inputs a turn ahead into L2 ----
@@ -272,6 +279,13 @@ kda_tree_kernel(const TreeArgs a)
                 uint64_t set[2] = {0, 0};
                 if (first + it < heads && tree_sets(a.parents + static_cast<long long>(w.n(it)) * a.K, a.K, lane, set) && lane == 0)
                     set_status(a.status, kStatusTree);
+                Set desc[2] = {0, 0};
+#pragma unroll 4
+                for (int c = 0; c < (Sh::kDense ? KP : 0); ++c) {
+                    const Set path = static_cast<Set>(__shfl_sync(0xffffffffu, KP > 32 && c >= 32 ? set[1] : set[0], c & 31));
+                    desc[0] |= (path >> lane & 1) << c;
+                    if constexpr (KP > 32) desc[1] |= (path >> (lane + 32) & 1) << c;
+                }
                 int up[2];
 #pragma unroll
                 for (int z = 0; z < 2; ++z) {
@@ -281,6 +295,7 @@ kda_tree_kernel(const TreeArgs a)
                     if (j >= KP) continue;
                     s_sets[(odd * kItems + it) * KP + j] = static_cast<Set>(set[z]);
                     s_ups[(odd * kItems + it) * KP + j] = static_cast<int8_t>(up[z]);
+                    if (Sh::kDense) s_descs[(odd * kItems + it) * KP + j] = desc[z];
                 }
                 int far[2] = {max(up[0], -1), max(up[1], -1)};
 #pragma unroll 1
@@ -328,7 +343,7 @@ kda_tree_kernel(const TreeArgs a)
             constexpr uint32_t id_w = tc::idesc(128, kN, tc::kFmtTF32, false, false);
             uint32_t turn = 0, run = 0, puts = 0;
             for (uint32_t first = begin; first < heads && ok; first += stride, ++turn) {
-                for (int chunk = 0; chunk < kChunks && ok; ++chunk, ++run) {
+                for (int chunk = 0; chunk < chunks && ok; ++chunk, ++run) {
                     ok = tc::mbar_wait_bounded(b_rows, run & 1, kWaitLimitNs);
                     if (!ok) break;
                     tc::fence_after_sync();
@@ -400,7 +415,7 @@ kda_tree_kernel(const TreeArgs a)
                 if (!ok) break;
                 tc::fence_after_sync();
                 // W (V - P), per item and chunk, where L was
-                for (int chunk = 0; chunk < kChunks; ++chunk)
+                for (int chunk = 0; chunk < chunks; ++chunk)
 #pragma unroll 1
                     for (int it = 0; it < kItems; ++it) {
                         const uint32_t d = tm + Sh::kL + chunk * Sh::kRows + it * Sh::kItem;
@@ -566,7 +581,7 @@ kda_tree_kernel(const TreeArgs a)
             bool walk = false;
 
 #pragma unroll 1
-            for (int chunk = 0; chunk < kChunks; ++chunk, ++run) {
+            for (int chunk = 0; chunk < chunks; ++chunk, ++run) {
                 // the rows: keys and queries times their decays, keys over them
 #pragma unroll
                 for (int z = 0; z < kPlaces; ++z) {
@@ -595,7 +610,7 @@ kda_tree_kernel(const TreeArgs a)
                 }
                 tc::fence_smem_to_async();
                 tc::mbar_arrive(b_rows);
-                if (chunk + 1 == kChunks) {                             // the next turn's inputs, into what is done with
+                if (chunk + 1 == chunks) {                              // the next turn's inputs, into what is done with
                     next = Turn(now.first + stride, heads, a.H);
                     if (next.first < heads) fetch(next);
                 }
@@ -607,24 +622,33 @@ kda_tree_kernel(const TreeArgs a)
                 }
                 tc::named_sync(kTreeAll, 256);                          // (of all threads: whether to walk)
                 walk = *reinterpret_cast<volatile int*>(s_walk + odd) != 0;
-                if (tid == 0) s_walk[1 - odd] = 0;
-                // 4. L and N of the chunk's nodes
+                if (tid == 0) {
+                    s_walk[1 - odd] = 0;
+                    for (int it = 0; it < kItems; ++it) s_bad[(1 - odd) * kItems + it] = 0;
+                }
+                // 4. L and N of the chunk's nodes.  Dense: beta L, and zeros where the path does not lead (L: nor to the node itself);
+                // what is no number in L enters as 0, and the node is marked: its own and its descendants' outputs are none
+                auto mark = [&](int it, Set places) {
+                    if constexpr (KP > 32) atomicOr(reinterpret_cast<unsigned long long*>(s_bad + odd * kItems + it), static_cast<unsigned long long>(places));
+                    else atomicOr(s_bad + odd * kItems + it, places);
+                };
                 if (!walk) {
                     // row x of the product is lane x % 16 of warp x / 16
                     constexpr int kOwn = Sh::kStack ? 8 : 16;           // places a warp (stacked: lanes 8 .. 15 their second terms)
-                    if (kOwn * warp < KP) {
+                    if (const int b = kOwn * (warp & 3) + lane; b - lane < KP && (Sh::kDense || group == 0)) {     // dense: one group L, the other N
                         ok = tc::mbar_wait_bounded(b_side, run & 1, kWaitLimitNs) && ok;
                         ok = __all_sync(0xffffffffu, ok);
                         tc::fence_after_sync();
-                    }
-                    if (kOwn * warp < KP) {
-                        const int b = kOwn * warp + lane;
 #pragma unroll 1
-                        for (int it = 0; it < kItems; ++it)
+                        for (int it = 0; it < kItems; ++it) {
+                            const Set below = Sh::kDense && b < KP ? s_descs[(odd * kItems + it) * KP + b] : 0;
+                            float* to = (group == 0 ? s_m : s_n) + (it * KP + chunk * KC) * KP + b;
+                            static_assert(Sh::kDense || kChunks == 1);
+                            float any = 0.f;                            // NaN where one is none
 #pragma unroll
-                            for (int c0 = 0; c0 < 2 * KC; c0 += 8) {
+                            for (int c0 = 0; c0 < (Sh::kDense ? 1 : 2) * KC; c0 += 8) {
                                 float x[8];
-                                const uint32_t from = lane_tm + Sh::kL + chunk * Sh::kRows + it * Sh::kItem + c0;
+                                const uint32_t from = lane_tm + Sh::kL + chunk * Sh::kRows + it * Sh::kItem + group * KC + c0;
                                 tree_tmem_ld8(from, x);
                                 if constexpr (Sh::kStack) {
                                     float y[8];
@@ -632,12 +656,37 @@ kda_tree_kernel(const TreeArgs a)
 #pragma unroll
                                     for (int r = 0; r < 8; ++r) x[r] += __shfl_xor_sync(0xffffffffu, x[r], 8) + y[r];
                                 }
-                                float* to = (c0 < KC ? s_m : s_n) + (it * KP + chunk * KC + c0 % KC) * KP + b;
+                                const int first = chunk * KC + c0;
+                                if (!Sh::kDense) {
+                                    if (c0 == KC) to = s_n + (it * KP - KC) * KP + b;
+                                } else if (group == 0) {
+                                    const uint4 beta = *reinterpret_cast<const uint4*>(s_beta + it * KP + first);
+                                    const uint32_t beta2[4] = {beta.x, beta.y, beta.z, beta.w};
+#pragma unroll
+                                    for (int r = 0; r < 8; r += 2) {
+                                        const float2 f = bf16x2_bits_to_f32(beta2[r / 2]);
+                                        x[r] = (below >> (first + r) & 1) && b != first + r ? x[r] * f.x : 0.f;
+                                        x[r + 1] = (below >> (first + r + 1) & 1) && b != first + r + 1 ? x[r + 1] * f.y : 0.f;
+                                        any = fmaf(x[r + 1], 0.f, fmaf(x[r], 0.f, any));
+                                    }
+                                } else {
+#pragma unroll
+                                    for (int r = 0; r < 8; ++r) x[r] = below >> (first + r) & 1 ? x[r] : 0.f;
+                                }
                                 if (lane < kOwn && b < KP) {
 #pragma unroll
-                                    for (int r = 0; r < 8; ++r) to[r * KP] = x[r];
+                                    for (int r = 0; r < 8; ++r) to[(c0 + r) * KP] = x[r];
                                 }
                             }
+                            if (any != 0.f && lane < kOwn && b < KP) {
+#pragma unroll 1
+                                for (int r = 0; r < KC; ++r)
+                                    if (!(fabsf(to[r * KP]) < INFINITY)) {
+                                        to[r * KP] = 0.f;
+                                        mark(it, kOne << (chunk * KC + r));
+                                    }
+                            }
+                        }
                         tc::fence_before_sync();
                     }
                 } else {
@@ -647,6 +696,11 @@ kda_tree_kernel(const TreeArgs a)
                     for (int f = 2 * warp + (lane >> 4); f < kItems * KC; f += 16) {
                         const int it = f / KC, i = chunk * KC + f % KC, e = it * KP + i;
                         Set left = s_set[e];
+                        if (Sh::kDense) {
+#pragma unroll
+                            for (int b = hl; b < KP; b += 16) s_m[e * KP + b] = s_n[e * KP + b] = 0.f;
+                            __syncwarp();
+                        }
                         float key[4 * G], query[4 * G], p[4 * G];
 #pragma unroll
                         for (int c = 0; c < 4 * G; ++c) {
@@ -675,65 +729,105 @@ kda_tree_kernel(const TreeArgs a)
                                 w += __shfl_xor_sync(0xffffffffu, w, off);
                             }
                             if (hl == 0 && on) {
-                                s_m[(it * KP + i) * KP + b] = m;
-                                s_n[(it * KP + i) * KP + b] = w;
+                                if (Sh::kDense) {
+                                    m *= b < i ? bf16_bits_to_f32(s_beta[e]) : 0.f;
+                                    if (!(fabsf(m) < INFINITY) && b < i) mark(it, kOne << i);
+                                    m = fabsf(m) < INFINITY ? m : 0.f;
+                                }
+                                s_m[e * KP + b] = m;
+                                s_n[e * KP + b] = w;
                             }
                         }
                     }
                 }
-                if (!Sh::kApart && group == 0) tc::mbar_arrive(b_read);
-                if (chunk + 1 < kChunks) {                              // the rows are written again
+                if (!Sh::kApart) tc::mbar_arrive(b_read);
+                if (chunk + 1 < chunks) {                               // the rows are written again
                     ok = tc::mbar_wait_bounded(b_prod, run & 1, kWaitLimitNs) && ok;
                     ok = __all_sync(0xffffffffu, ok);
                 }
             }
             tc::named_sync(kTreeAll, 256);
-            // 5. W while the products run: a warp a row (or two), lane b place b (and b + 32): w_c is final once the places above c
-            // are done.  Zeros where the path does not lead
-            constexpr int kLanes = Sh::kLanes, kP = kPlaces;            // lanes a row, places a lane
-#pragma unroll 1
-            for (int e = warp * (32 / kLanes) + lane / kLanes; e < Sh::kNodes; e += 8 * (32 / kLanes)) {
-                const int it = e / KP, i = e % KP, mine = lane % kLanes;
-                const Set on = s_set[e];
-                float w[kP];
-                const float* row = s_n + (it * KP + i) * KP;
-                const float* L = s_m + it * KP * KP + mine;
-                const uint16_t* beta = s_beta + it * KP;
+            // 5. W while the products run.  Dense: kWLanes lanes a row, each every kWLanes-th quad of its places: from the last quad of
+            // places up, whose four numbers are solved for by every lane, then taken out of the places above them (zeros where a
+            // path does not lead).  Else 32 / kLanes rows a warp along their paths, lane b place b: w_c is final once the places
+            // above c are done.  (256 x 32 heads, dense to paths: 8 nodes 177 to 162 us, 16: 231 to 214, 32: 445 to 487, 64: 1240
+            // to 1530; the dense one is given what two CTAs an SM have no registers for.)
+            if constexpr (Sh::kDense) {
+                constexpr int kL = Sh::kWLanes, kQ = Sh::kQuads;
+                const int e = min(tid / kL, Sh::kNodes - 1), it = e / KP, i = e % KP, s = tid % kL;
+                if (32 * warp < Sh::kNodes * kL) {
+                    const float* L = s_m + it * KP * KP;
+                    float w[kQ][4];
 #pragma unroll
-                for (int z = 0; z < kP; ++z) w[z] = on >> (mine + 32 * z) & 1 ? row[mine + 32 * z] : 0.f;
-                // (nothing is below a path's first node)
-                for (Set left = on; __any_sync(0xffffffffu, (left & (left - 1)) != 0);) {
-                    int c4[4];
-                    Set below[4];
-                    float b4[4], m4[4][kP];
-#pragma unroll
-                    for (int y = 0; y < 4; ++y) {                       // 4 places of the path, their loads together
-                        c4[y] = left ? tree_top(left) : 0;
-                        left &= ~(kOne << c4[y]);
-                        below[y] = left;
-                        b4[y] = bf16_bits_to_f32(beta[c4[y]]);
-#pragma unroll
-                        for (int z = 0; z < kP; ++z) m4[y][z] = L[c4[y] * KP + 32 * z];
+                    for (int j = 0; j < kQ; ++j) {
+                        const float4 n = *reinterpret_cast<const float4*>(s_n + e * KP + (j * kL + s) * 4);
+                        w[j][0] = n.x; w[j][1] = n.y; w[j][2] = n.z; w[j][3] = n.w;
                     }
 #pragma unroll
-                    for (int y = 0; y < 4; ++y) {
-                        float wc = __shfl_sync(0xffffffffu, w[0], c4[y] & 31, kLanes);
-                        if constexpr (kP == 2) {
-                            const float hi = __shfl_sync(0xffffffffu, w[1], c4[y] & 31);
-                            wc = c4[y] >= 32 ? hi : wc;
+                    for (int b = KP / 4 - 1; b >= 0; --b) {
+                        if (4 * b >= a.K) continue;                     // (no rows of L there)
+                        float x[4];
+#pragma unroll
+                        for (int r = 0; r < 4; ++r) x[r] = __shfl_sync(0xffffffffu, w[b / kL][r], b % kL, kL);
+                        const float* at = L + 4 * b * KP;
+                        const float4 l1 = *reinterpret_cast<const float4*>(at + KP + 4 * b), l2 = *reinterpret_cast<const float4*>(at + 2 * KP + 4 * b),
+                                     l3 = *reinterpret_cast<const float4*>(at + 3 * KP + 4 * b);
+                        x[2] = fmaf(-x[3], l3.z, x[2]);
+                        x[1] = fmaf(-x[2], l2.y, fmaf(-x[3], l3.y, x[1]));
+                        x[0] = fmaf(-x[1], l1.x, fmaf(-x[2], l2.x, fmaf(-x[3], l3.x, x[0])));
+#pragma unroll
+                        for (int j = 0; j <= b / kL; ++j)
+#pragma unroll
+                            for (int r = 3; r >= 0; --r) {
+                                const float4 l = *reinterpret_cast<const float4*>(at + r * KP + (j * kL + s) * 4);
+                                w[j][0] = fmaf(-x[r], l.x, w[j][0]);
+                                w[j][1] = fmaf(-x[r], l.y, w[j][1]);
+                                w[j][2] = fmaf(-x[r], l.z, w[j][2]);
+                                w[j][3] = fmaf(-x[r], l.w, w[j][3]);
+                            }
+                    }
+                    const Set on = s_set[e];
+                    if (tid / kL < Sh::kNodes)
+#pragma unroll
+                        for (int j = 0; j < kQ; ++j) {
+                            const int b = (j * kL + s) * 4;
+                            const uint2 beta = *reinterpret_cast<const uint2*>(s_beta + it * KP + b);
+                            const float2 lo = bf16x2_bits_to_f32(beta.x), hi = bf16x2_bits_to_f32(beta.y);
+                            split(Sh::oW + tc::sw128_off32(it * Sh::kWRows + i, b, kItems * Sh::kWRows), Sh::kW,
+                                  make_float4(on >> b & 1 ? w[j][0] * lo.x : 0.f, on >> (b + 1) & 1 ? w[j][1] * lo.y : 0.f,
+                                              on >> (b + 2) & 1 ? w[j][2] * hi.x : 0.f, on >> (b + 3) & 1 ? w[j][3] * hi.y : 0.f));
                         }
-                        wc *= b4[y];
-#pragma unroll
-                        for (int z = 0; z < kP; ++z)
-                            if (below[y] >> (mine + 32 * z) & 1) w[z] = fmaf(-wc, m4[y][z], w[z]);
-                    }
                 }
+            } else {
+                constexpr int kLanes = Sh::kLanes;
+#pragma unroll 1
+                for (int e = warp * (32 / kLanes) + lane / kLanes; e < Sh::kNodes; e += 8 * (32 / kLanes)) {
+                    const int it = e / KP, i = e % KP, mine = lane % kLanes;
+                    const Set on = s_set[e];
+                    const float* L = s_m + it * KP * KP + mine;
+                    const uint16_t* beta = s_beta + it * KP;
+                    float w = on >> mine & 1 ? s_n[(it * KP + i) * KP + mine] : 0.f;
+                    // (nothing is below a path's first node)
+                    for (Set left = on; __any_sync(0xffffffffu, (left & (left - 1)) != 0);) {
+                        int c4[4];
+                        Set below[4];
+                        float b4[4], m4[4];
 #pragma unroll
-                for (int z = 0; z < kP; ++z) {
-                    const int b = mine + 32 * z;
-                    const float x = on >> b & 1 ? w[z] * bf16_bits_to_f32(beta[b]) : 0.f, y = tree_lead(x);
-                    float* to = reinterpret_cast<float*>(sm + Sh::oW + z * (kItems * Sh::kWRows * 128) +
-                                                         tc::sw128_off32(it * Sh::kWRows + i, mine, kItems * Sh::kWRows));
+                        for (int y = 0; y < 4; ++y) {                   // 4 places of the path, their loads together
+                            c4[y] = left ? tree_top(left) : 0;
+                            left &= ~(kOne << c4[y]);
+                            below[y] = left;
+                            b4[y] = bf16_bits_to_f32(beta[c4[y]]);
+                            m4[y] = L[c4[y] * KP];
+                        }
+#pragma unroll
+                        for (int y = 0; y < 4; ++y) {
+                            const float wc = __shfl_sync(0xffffffffu, w, c4[y] & 31, kLanes) * b4[y];
+                            if (below[y] >> mine & 1) w = fmaf(-wc, m4[y], w);
+                        }
+                    }
+                    const float x = on >> mine & 1 ? w * bf16_bits_to_f32(beta[mine]) : 0.f, y = tree_lead(x);
+                    float* to = reinterpret_cast<float*>(sm + Sh::oW + tc::sw128_off32(it * Sh::kWRows + i, mine, kItems * Sh::kWRows));
                     to[0] = y;
                     to[Sh::kW / 4] = x - y;
                 }
@@ -757,7 +851,7 @@ kda_tree_kernel(const TreeArgs a)
                     for (int r = 0; r < 8; ++r) x[r] += y[r];
                 }
             };
-            Set none = 0;                                               // places where it is no number (0 goes in: 0 * NaN is none)
+            Set none = Sh::kDense ? s_bad[odd * kItems + item] : 0;     // places where it is no number (0 goes in: 0 * NaN is none)
 #pragma unroll 2
             for (int i0 = 8 * group; i0 < KP; i0 += 16) {
                 float x[8], y[8];
