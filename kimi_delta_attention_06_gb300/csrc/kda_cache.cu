@@ -158,6 +158,17 @@ kda_latent_append_rope_kernel(const RopeArgs a)
     if (t >= a.T) return;
     const int slot = a.slots[t], pos = a.pos[t];
     const float f = a.freq[lane];
+    // (the first heads' loads, and the key's, beside those)
+    constexpr int U = 4;                         // heads in flight, a lane
+    RopePairs<INTER> x[U], key;
+    const uint16_t* q = a.q + t * a.ldq;
+    auto load = [&](int h0) {
+#pragma unroll
+        for (int i = 0; i < U; ++i)
+            if (const int h = h0 + 4 * a.split * i; h < a.H) x[i].load(q + h * a.hdq, g);
+    };
+    load(4 * part + sub);                        // (none without queries: H is 0 then)
+    if (part == 0 && sub == 0) key.load(a.r + t * a.ldr, g);
     if (slot < 0) return;
     if (slot >= a.num_rows) {
         if (lane == 0 && part == 0) set_status(a.status, kStatusIndex);
@@ -177,29 +188,20 @@ kda_latent_append_rope_kernel(const RopeArgs a)
         uint8_t* row = a.cache + static_cast<size_t>(slot) * lat_row_bytes(E4M3);
         put_latents<E4M3>(row, reinterpret_cast<const uint4*>(a.c + t * a.ldc), lane);
         if (sub == 0) {
-            RopePairs<INTER> x;
-            x.load(a.r + t * a.ldr, g);
-            x.turn(cs, sn);
-            x.store(reinterpret_cast<uint16_t*>(row + (E4M3 ? kLatDim : 2 * kLatDim)), g);
+            key.turn(cs, sn);
+            key.store(reinterpret_cast<uint16_t*>(row + (E4M3 ? kLatDim : 2 * kLatDim)), g);
         }
     }
-    if (!a.q) return;
-    constexpr int U = 4;                         // heads in flight, a lane
-    for (int h0 = 4 * part + sub; h0 < a.H; h0 += 4 * a.split * U) {
-        RopePairs<INTER> x[U];
+    uint16_t* out = a.q_out + t * a.ldo;
+    for (int h0 = 4 * part + sub; h0 < a.H;) {
 #pragma unroll
-        for (int i = 0; i < U; ++i) {
-            const int h = h0 + 4 * a.split * i;
-            if (h < a.H) x[i].load(a.q + t * a.ldq + h * a.hdq, g);
-        }
-#pragma unroll
-        for (int i = 0; i < U; ++i) {
-            const int h = h0 + 4 * a.split * i;
-            if (h < a.H) {
+        for (int i = 0; i < U; ++i)
+            if (const int h = h0 + 4 * a.split * i; h < a.H) {
                 x[i].turn(cs, sn);
-                x[i].store(a.q_out + t * a.ldo + h * a.hdo, g);
+                x[i].store(out + h * a.hdo, g);
             }
-        }
+        h0 += 4 * a.split * U;
+        load(h0);
     }
 }
 
@@ -321,7 +323,7 @@ int launch_latent_append_rope(const uint16_t* c, long long ldc, const uint16_t* 
                               int T, int H, int* status, cudaStream_t stream)
 {
     if (T == 0) return 0;
-    const int split = 1;
+    const char* ev = getenv("RS"); const int split = ev ? atoi(ev) : 1;
     const RopeArgs a{c, ldc, r, ldr, static_cast<uint8_t*>(cache), num_rows, slots, pos, freq, q, ldq, hdq, q_out, ldo, hdo,
                      T, q ? H : 0, split, status};
     constexpr unsigned per = kRopeThreads / 32;

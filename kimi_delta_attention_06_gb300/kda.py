@@ -618,13 +618,18 @@ def _token_logprobs(logits, tokens, R, V, top, scale, logprob, rank, entropy, to
     _on_gpu(logits, tokens)
     if make:
         dev, side = logits.device, _side(stream)
+        lp = kp = vp = ip = None
         if tokens is not None:
             logprob, rank = _empty((R,), dev, _F32, side), _empty((R,), dev, _I32, side)
+            lp, kp = logprob.data_ptr(), rank.data_ptr()
         entropy = _empty((R,), dev, _F32, side)
+        ep = entropy.data_ptr()
         if top > 0:
             top_logprob, top_token = _empty((R, top), dev, _F32, side), _empty((R, top), dev, _I32, side)
-    lp, kp, ep = _out(logprob, _F32, R, "logprob"), _out(rank, _I32, R, "rank"), _out(entropy, _F32, R, "entropy")
-    vp, ip = _out(top_logprob, _F32, R * top, "top_logprob"), _out(top_token, _I32, R * top, "top_token")
+            vp, ip = top_logprob.data_ptr(), top_token.data_ptr()
+    else:
+        lp, kp, ep = _out(logprob, _F32, R, "logprob"), _out(rank, _I32, R, "rank"), _out(entropy, _F32, R, "entropy")
+        vp, ip = _out(top_logprob, _F32, R * top, "top_logprob"), _out(top_token, _I32, R * top, "top_token")
     rc = load().kda_token_logprobs(xp, KDA_OUT_F32 if dtype is _F32 else KDA_OUT_BF16, ld, tp, R, V, top, scale, lp, kp, ep, vp,
                                    ip, _stream(stream))
     if rc:
