@@ -80,8 +80,10 @@ kda_latent_append_kernel(const uint16_t* __restrict__ c, long long ldc, const ui
 // fraction of a turn (its whole turns vanish at whole positions), times pos modulo 2^64, is exact but for the
 // fraction's own rounding, pos * 2^-64.
 //
-// A warp takes a token (or some of its heads, where tokens are few): lane i the angle of pair i, once; then 8 lanes a
-// head, 4 pairs a lane, with 4 heads at once.
+// A warp takes a token: lane i the angle of pair i, once; then 8 lanes a head, 4 pairs a lane, 16 heads in flight, the first
+// of them on their way before the slot is known.  Bound by HBM: 32768 tokens of 32 heads, bf16, 55 us (6.2 TB/s); 768 of
+// them, e4m3, 3.4 us, most of it the launch and two loads one after the other.  (Heads of a token over 2 warps: 56 and
+// 3.2 us, over 4: 74 and 3.3.  The loads after the angle: 59 and 4.1.)
 constexpr int kRopeThreads = 128;
 
 // f / 2 pi modulo a turn, in units of 2^-64: 24 bits of f times 96 bits of 1 / 2 pi, moved to its place.  (|f| < 2^32.)
@@ -104,7 +106,7 @@ struct RopeArgs {
     const float* freq;
     const uint16_t* q; long long ldq, hdq;
     uint16_t* q_out; long long ldo, hdo;
-    int T, H, split;                             // split: warps a token (each takes every split-th group of 4 heads)
+    int T, H;
     int* status;
 };
 
@@ -152,9 +154,7 @@ __global__ void __launch_bounds__(kRopeThreads)
 kda_latent_append_rope_kernel(const RopeArgs a)
 {
     const int lane = threadIdx.x & 31, g = lane & 7, sub = lane >> 3;
-    const long long unit = static_cast<long long>(blockIdx.x) * (kRopeThreads / 32) + (threadIdx.x >> 5);
-    const long long t = unit / a.split;
-    const int part = static_cast<int>(unit - t * a.split);
+    const long long t = static_cast<long long>(blockIdx.x) * (kRopeThreads / 32) + (threadIdx.x >> 5);
     if (t >= a.T) return;
     const int slot = a.slots[t], pos = a.pos[t];
     const float f = a.freq[lane];
@@ -165,13 +165,13 @@ kda_latent_append_rope_kernel(const RopeArgs a)
     auto load = [&](int h0) {
 #pragma unroll
         for (int i = 0; i < U; ++i)
-            if (const int h = h0 + 4 * a.split * i; h < a.H) x[i].load(q + h * a.hdq, g);
+            if (const int h = h0 + 4 * i; h < a.H) x[i].load(q + h * a.hdq, g);
     };
-    load(4 * part + sub);                        // (none without queries: H is 0 then)
-    if (part == 0 && sub == 0) key.load(a.r + t * a.ldr, g);
+    load(sub);                                   // (none without queries: H is 0 then)
+    if (sub == 0) key.load(a.r + t * a.ldr, g);
     if (slot < 0) return;
     if (slot >= a.num_rows) {
-        if (lane == 0 && part == 0) set_status(a.status, kStatusIndex);
+        if (lane == 0) set_status(a.status, kStatusIndex);
         return;
     }
     const uint64_t turns = rope_turns(f) * static_cast<uint64_t>(static_cast<long long>(pos));
@@ -184,23 +184,21 @@ kda_latent_append_rope_kernel(const RopeArgs a)
         cs[i] = __shfl_sync(0xffffffffu, c, 4 * g + i);
         sn[i] = __shfl_sync(0xffffffffu, s, 4 * g + i);
     }
-    if (part == 0) {
-        uint8_t* row = a.cache + static_cast<size_t>(slot) * lat_row_bytes(E4M3);
-        put_latents<E4M3>(row, reinterpret_cast<const uint4*>(a.c + t * a.ldc), lane);
-        if (sub == 0) {
-            key.turn(cs, sn);
-            key.store(reinterpret_cast<uint16_t*>(row + (E4M3 ? kLatDim : 2 * kLatDim)), g);
-        }
+    uint8_t* row = a.cache + static_cast<size_t>(slot) * lat_row_bytes(E4M3);
+    put_latents<E4M3>(row, reinterpret_cast<const uint4*>(a.c + t * a.ldc), lane);
+    if (sub == 0) {
+        key.turn(cs, sn);
+        key.store(reinterpret_cast<uint16_t*>(row + (E4M3 ? kLatDim : 2 * kLatDim)), g);
     }
     uint16_t* out = a.q_out + t * a.ldo;
-    for (int h0 = 4 * part + sub; h0 < a.H;) {
+    for (int h0 = sub; h0 < a.H;) {
 #pragma unroll
         for (int i = 0; i < U; ++i)
-            if (const int h = h0 + 4 * a.split * i; h < a.H) {
+            if (const int h = h0 + 4 * i; h < a.H) {
                 x[i].turn(cs, sn);
                 x[i].store(out + h * a.hdo, g);
             }
-        h0 += 4 * a.split * U;
+        h0 += 4 * U;
         load(h0);
     }
 }
@@ -323,11 +321,10 @@ int launch_latent_append_rope(const uint16_t* c, long long ldc, const uint16_t* 
                               int T, int H, int* status, cudaStream_t stream)
 {
     if (T == 0) return 0;
-    const char* ev = getenv("RS"); const int split = ev ? atoi(ev) : 1;
     const RopeArgs a{c, ldc, r, ldr, static_cast<uint8_t*>(cache), num_rows, slots, pos, freq, q, ldq, hdq, q_out, ldo, hdo,
-                     T, q ? H : 0, split, status};
+                     T, q ? H : 0, status};
     constexpr unsigned per = kRopeThreads / 32;
-    const unsigned blocks = static_cast<unsigned>((static_cast<long long>(T) * split + per - 1) / per);
+    const unsigned blocks = static_cast<unsigned>((static_cast<long long>(T) + per - 1) / per);
     if (e4m3) {
         if (inter) kda_latent_append_rope_kernel<true, true><<<blocks, kRopeThreads, 0, stream>>>(a);
         else kda_latent_append_rope_kernel<true, false><<<blocks, kRopeThreads, 0, stream>>>(a);
