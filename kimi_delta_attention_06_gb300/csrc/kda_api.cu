@@ -928,7 +928,8 @@ static int latent_decode_call(const uint16_t* q, const void* cache, int cache_dt
     if (rc != KDA_OK) return rc;
     const cudaStream_t st = static_cast<cudaStream_t>(stream);
     void* ws = nullptr;
-    if (cudaMallocFromPoolAsync(&ws, kda::latent_decode_scratch(K * H, N, parents != nullptr), pool, st) != cudaSuccess) return KDA_ERR_CUDA;
+    if (cudaMallocFromPoolAsync(&ws, kda::latent_decode_scratch(K * H, N, parents != nullptr), pool, st) != cudaSuccess)
+        return KDA_ERR_CUDA;
     rc = kda::launch_latent_decode(q, cache, cache_dtype == KDA_CACHE_E4M3, num_pages, page_size, block_table, max_pages,
                                    seq_lens, parents, N, K, H, sm_scale, out, lse, ws, status, st);
     const bool freed = cudaFreeAsync(ws, st) == cudaSuccess;

@@ -195,7 +195,7 @@ struct LatArgs {
 template <int R, bool E4M3>
 struct LatShape {
     // softmax, rescale, epilogue: groups of 4 warps, each RW rows of a tile (64 rows, one group of 4 warps to two: 16 trees of
-    // 4 to 8 nodes x 32 heads over 341k tokens, e4m3, 204 -> 184 us; one of 12 nodes x 4 heads over 1500 tokens, bf16, 17.6 -> 14.4;
+    // 4 to 8 nodes x 32 heads over 341k tokens, e4m3, 204 -> 184 us; 3 of 12 nodes x 4 heads over 200 tokens at most, bf16, 17.6 -> 14.4;
     // 16 chains of 8 x 32 over the same, e4m3, 229 -> 223)
     static constexpr int kGroups = R == 64 ? 2 : 1, RW = R / kGroups;
     static constexpr int kSoft = 128 * kGroups;

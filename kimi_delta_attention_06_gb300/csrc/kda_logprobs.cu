@@ -20,6 +20,10 @@
 //
 // A cluster of C CTAs serves a row, each a contiguous slice of it: its sums and its sorted list go into the shared memory
 // of the first, which joins them.
+//
+// Measured in a graph: 2048 rows of 131072 bf16, 1 alternative: 113 us, 4.7 TB/s; 256 rows of 100003, 8: 24.3 us; 4 rows of
+// 131072 fp32, 20: 10.8 us.  The pass alone runs at 6.2 TB/s; the rest is what follows it in each CTA, a chain of steps of a
+// few thousand clocks (sums, order of the maxima, the steps read again, order of what they hold).
 #include <cfloat>
 #include <cuda_bf16.h>
 #include "common.cuh"
@@ -27,8 +31,8 @@
 
 namespace kda {
 
-constexpr int kLogThreads = 256, kLogWarps = kLogThreads / 32, kLogGroups = kLogThreads / 2, kLogMaxTop = 32, kLogSteps = 24, kLogFew = 64, kLogKeep = 1024;
-constexpr int kLogMaxCluster = 16;
+constexpr int kLogThreads = 256, kLogWarps = kLogThreads / 32, kLogGroups = kLogThreads / 2, kLogMaxTop = 32, kLogSteps = 24;
+constexpr int kLogFew = 64, kLogKeep = 1024, kLogMaxCluster = 8;
 constexpr int kStatusToken = -1;                 // KDA_ERR_INVALID_ARG, recorded on the device
 using LogKey = unsigned long long;               // a value's order bits, then its index negated; 0: none
 
@@ -564,10 +568,11 @@ kda_logprobs_kernel(const LogArgs a)
     }
 }
 
-// CTAs a row
+// CTAs a row: as many as run at once, of slices that a step or more of every thread takes.  (2048 rows of 131072 bf16, 1, 2, 4
+// CTAs a row: 113, 136, 180 us; 256 of 100003: 26.1, 24.3, 32.3; 4 of 131072 fp32, 1, 2, 4, 8: 27.7, 20.3, 14.2, 10.8)
 int logprobs_cluster(int R, int V, int sms, int bytes) {
     int C = 1;
-    while (C < 8 && static_cast<long long>(R) * 2 * C <= 4 * sms && V / (2 * C) * bytes >= 16384) C *= 2;
+    while (C < kLogMaxCluster && static_cast<long long>(R) * 2 * C <= 4 * sms && V / (2 * C) * bytes >= 16384) C *= 2;
     return C;
 }
 
