@@ -78,16 +78,16 @@ __device__ __forceinline__ int lat_len(const LatWork& w, int n) {
     const int seqs = w.N / w.each, tile = n / seqs, s = n - tile * seqs;
     return w.need && tile >= w.need[s] ? 0 : lat_seq(w, s);
 }
-// Row tiles of sequence n that are sequences of their own and not left out (as the attention kernel has found them).
-__device__ __forceinline__ int lat_needed(const LatWork& w, const int32_t* need, int n) {
-    return w.each <= 1 ? 1 : w.N / w.each <= kMaxNeed ? need[n] : w.each;
-}
 // Row tiles that a tree needs: R rows each, H of a node, up to its last place with a node.
 __device__ __forceinline__ int lat_need(const int32_t* parents, int K, int H, int R) {
     int last = 0;
     for (int j = 0; j < K; ++j)
         if (__ldg(parents + j) >= -1) last = j + 1;
     return (last * H + R - 1) / R;
+}
+// Row tiles of sequence n that are sequences of their own and not left out.
+__device__ __forceinline__ int lat_needed(const LatWork& w, const int32_t* parents, int K, int H, int R, int n) {
+    return w.each <= 1 ? 1 : w.N / w.each <= kMaxNeed ? lat_need(parents + static_cast<long long>(n) * K, K, H, R) : w.each;
 }
 __device__ __forceinline__ int lat_tiles(int len) { return (len + kTile - 1) / kTile; }
 __device__ __forceinline__ int lat_count(const LatWork& w, int len) { return len > 0 ? lat_tiles(len) + w.lead : 0; }   // with the lead
@@ -188,7 +188,6 @@ struct LatArgs {
     uint16_t* out;
     float* lse;
     float *part_o, *part_ml;                     // partials: [run][row tile][2][R][512], [..][R][2]
-    int32_t* need;                               // [N]: row tiles that a tree needs, where a.w.each > 1
     int* status;
 };
 
@@ -382,9 +381,7 @@ kda_latent_decode_kernel(const __grid_constant__ LatMaps maps, const LatArgs a)
     if (tid < R) s_j[tid] = min((rt * R + tid) / a.H, a.K - 1);
     if (TREE && work.each > 1 && work.N / work.each <= kMaxNeed) {
         for (int i = tid; i < work.N / work.each; i += Sh::kThreads) {
-            const int need = lat_need(a.parents + static_cast<long long>(i) * a.K, a.K, a.H, R);
-            s_need[i] = static_cast<uint8_t>(need);
-            if (blockIdx.x == 0) a.need[i] = need;              // for the kernel that joins
+            s_need[i] = static_cast<uint8_t>(lat_need(a.parents + static_cast<long long>(i) * a.K, a.K, a.H, R));
         }
         work.need = s_need;
     }
@@ -900,11 +897,10 @@ kda_latent_combine_kernel(const LatArgs a, int Q, int NG)
     const int warps = threads >> 5;
     long long before = 0, T = 0;
     const int seqs = a.w.N / a.w.each, tile = a.w.each > 1 ? row / R : 0;     // (of those that are sequences of their own)
-    if (a.w.each > 1) asm volatile("griddepcontrol.wait;" ::: "memory");    // (for what the trees need)
     for (int i = tid; i < seqs; i += threads) {
         const int raw = a.w.seq_lens[i], tiles = lat_tiles(lat_seq(a.w, i)), count = tiles > 0 ? tiles + a.w.lead : 0;
         if (i == n && row == 0 && raw != lat_seq(a.w, i)) set_status(a.status, kStatusIndex);   // out of range: counted as 0
-        const int need = lat_needed(a.w, a.need, i);
+        const int need = lat_needed(a.w, a.parents, a.K, a.H, R, i);
         T += static_cast<long long>(need) * count;
         before += static_cast<long long>(min(need, tile) + (i < n && need > tile ? 1 : 0)) * count;
     }
@@ -917,7 +913,7 @@ kda_latent_combine_kernel(const LatArgs a, int Q, int NG)
     __syncthreads();
     T = before = 0;
     for (int i = 0; i < warps; ++i) { T += s_sum[0][i]; before += s_sum[1][i]; }
-    const int tiles = tile < lat_needed(a.w, a.need, n) ? lat_tiles(lat_seq(a.w, n)) : 0;
+    const int tiles = tile < lat_needed(a.w, a.parents, a.K, a.H, R, n) ? lat_tiles(lat_seq(a.w, n)) : 0;
     const long long at = static_cast<long long>(n) * a.rows + row;
     int c0 = 0, parts = 1, late = 0;
     if (tiles > 0) {
@@ -1002,12 +998,11 @@ kda_latent_combine_rows_kernel(const LatArgs a)
     const int tile = a.w.each > 1 ? min(row, a.rows - 1) / R : 0;            // (of those that are sequences of their own)
     long long T = 0, before = 0;
     int len = 0;
-    if (a.w.each > 1) asm volatile("griddepcontrol.wait;" ::: "memory");    // (for what the trees need)
     for (int i0 = 0; i0 < seqs; i0 += 32) {
         const int i = i0 + lane, v = i < seqs ? lat_seq(a.w, i) : 0;
         if (i == n && row == 0 && a.w.seq_lens[i] != v) set_status(a.status, kStatusIndex);   // out of range: counted as 0
         const long long count = lat_count(a.w, v);
-        const int need = i < seqs ? lat_needed(a.w, a.need, i) : 0;
+        const int need = i < seqs ? lat_needed(a.w, a.parents, a.K, a.H, R, i) : 0;
         T += need * count;
         before += (min(need, tile) + (i < n && need > tile ? 1 : 0)) * count;
         if (n >= i0 && n < i0 + 32) len = __shfl_sync(0xffffffffu, v, n - i0);
@@ -1017,7 +1012,7 @@ kda_latent_combine_rows_kernel(const LatArgs a)
         T += __shfl_xor_sync(0xffffffffu, T, off);
         before += __shfl_xor_sync(0xffffffffu, before, off);
     }
-    const int tiles = tile < lat_needed(a.w, a.need, n) ? lat_tiles(len) : 0;
+    const int tiles = tile < lat_needed(a.w, a.parents, a.K, a.H, R, n) ? lat_tiles(len) : 0;
     int c0 = 0, parts = 1, late = 0;
     if (tiles > 0) {
         const long long runs = lat_runs(T, a.w.G);
@@ -1178,12 +1173,14 @@ int latent_decode_runs(int rows) {
     const int G = sms / RT > 0 ? sms / RT : (sms > 0 ? 1 : 0);
     return G < kMaxRuns ? G : kMaxRuns;
 }
-// A tree's row tiles as sequences of their own: one run a CTA (see the work split).
-static bool tree_split(int rows, bool tree) { return tree && rows > 64; }
-size_t latent_decode_scratch(int rows, int N, bool tree) {
+// A tree's row tiles as sequences of their own: one run a CTA (see the work split).  Two of a bf16 cache stay together: where
+// some of the second are left out, what the first have read has left L2 (16 trees of 2 to 4 nodes x 32 heads over 341k
+// tokens: apart 141 us, together 128; e4m3, apart: 122, chains of 4, all of whose rows are there: 127).
+static bool tree_split(int rows, bool tree, int e4m3) { return tree && rows > (e4m3 ? 64 : 128); }
+size_t latent_decode_scratch(int rows, bool tree, int e4m3) {
     const size_t R = rows_per_cta(rows), RT = (rows + R - 1) / R;
-    const size_t runs = tree_split(rows, tree) ? latent_decode_runs(64) : latent_decode_runs(rows) * RT;
-    return runs * 2 * R * (kLatDim + 2) * sizeof(float) + (tree_split(rows, tree) ? static_cast<size_t>(N) * sizeof(int32_t) : 0);
+    const size_t runs = tree_split(rows, tree, e4m3) ? latent_decode_runs(64) : latent_decode_runs(rows) * RT;
+    return runs * 2 * R * (kLatDim + 2) * sizeof(float);
 }
 
 int launch_latent_decode(const uint16_t* q, const void* cache, int e4m3, int num_pages, int page_size,
@@ -1193,7 +1190,7 @@ int launch_latent_decode(const uint16_t* q, const void* cache, int e4m3, int num
     LatArgs a = {};
     const int rows = K * H, R = rows_per_cta(rows);
     // (a segment's start and end in tiles: the best of 1, 2, 3, 4, 6 and of 4, 6, 8, 10, where Q is split too)
-    const bool apart = tree_split(rows, parents != nullptr);
+    const bool apart = tree_split(rows, parents != nullptr, e4m3);
     const int each = apart ? (rows + R - 1) / R : 1;
     a.w = LatWork{seq_lens, N * each, latent_decode_runs(apart ? 64 : rows), N * each == 1 ? 0 : e4m3 && R == 64 ? 8 : 2, parents ? K : 0,
                   static_cast<long long>(max_pages) * page_size, each, nullptr};
@@ -1211,7 +1208,6 @@ int launch_latent_decode(const uint16_t* q, const void* cache, int e4m3, int num
     a.lse = lse;
     a.part_o = static_cast<float*>(scratch);
     a.part_ml = a.part_o + static_cast<size_t>(a.w.G) * a.RT * 2 * R * kLatDim;
-    a.need = reinterpret_cast<int32_t*>(a.part_ml + static_cast<size_t>(a.w.G) * a.RT * 2 * R * 2);
     a.status = status;
     LatMaps maps;
     const CUtensorMapSwizzle swz = CU_TENSOR_MAP_SWIZZLE_128B;
