@@ -519,9 +519,9 @@ kda_tree_kernel(const TreeArgs a)
                 for (int i = 0; i < 32; ++i) {
                     const float x = S[i * D], y = tree_lead(x);
                     lead[i] = __float_as_uint(y);
-                    // (in order with the arrival: the copy that follows it must not overtake a load that is still in flight)
-                    asm volatile("sub.rn.f32 %0, %1, %2;" : "=r"(rest[i]) : "f"(x), "f"(y) : "memory");
+                    rest[i] = __float_as_uint(x - y);
                 }
+                tc::fence_smem_to_async();                              // (the copy that follows the arrival must not overtake a load)
                 tc::mbar_arrive(&b_empty[c % kRing]);
                 // (the first of a turn follow on its last turn's end)
                 if (q >= kBufs) {

@@ -197,3 +197,23 @@ def test_sums_do_not_lean(D, K, decay):
     ref = torch.stack([T.state_outputs(q[n], k[n], v[n], None if la is None else la[n], beta[n], pool[n], rows[n])[0] for n in range(4)])
     rel = float((got - ref).norm() / ref.norm())
     assert rel <= (D / 8 + K / 8 + 4) * 2.0 ** -24, f"{rel:.2g}"
+
+
+@pytest.mark.parametrize("N,H,D,K", [(256, 32, 128, 16), (300, 32, 128, 7), (512, 32, 64, 13), (100, 32, 128, 25), (256, 16, 64, 40)])
+def test_every_channel_of_many_states(N, H, D, K):
+    """Queries that pick a channel of the state each, where nothing is written: outputs are its rows, to the 22 bits that the
+    products keep.  (CTAs that serve dozens of states one after another: a piece of the next one in a piece's place shows.)"""
+    g = torch.Generator(device=DEV).manual_seed(K)
+    pool = torch.randn(N, H, D, D, device=DEV, generator=g)
+    par = torch.tensor([T.tree(K, n, 6) for n in range(N)], dtype=torch.int32, device=DEV)
+    zero = torch.zeros(N, K, H, D, dtype=torch.bfloat16, device=DEV)
+    beta = torch.zeros(N, K, H, dtype=torch.bfloat16, device=DEV)
+    for it in range(-(-D // K)):
+        at = (torch.arange(K, device=DEV) * -(-D // K) + it).clamp_max(D - 1)
+        q = zero.clone()
+        q.scatter_(3, at.view(1, K, 1, 1).expand(N, K, H, 1), 1.0)
+        for _ in range(3):
+            o = kda.decode_tree(q, zero, zero, None, beta, pool, par, out_dtype=torch.float32, decay=NO)
+            want = pool[:, :, at].permute(0, 2, 1, 3)
+            assert ((o - want).abs() <= 2.0 ** -21 * want.abs()).all()
+    _ok()
