@@ -20,8 +20,8 @@
 // decay leaves 2^-100 .. 2^100 walk their paths instead), and W (V - P), with V - P in TMEM in S_0^T's place (a NaN
 // or an infinity in it enters as 0, and is put back for the nodes whose paths hold it: 0 * NaN is none).
 //
-// Measured in a graph: 256 sequences x 32 heads of 128 x 128, trees of 16 nodes: 191 us for 0.70 GB that cannot be done without
-// (103 us of HBM); 64 x 8 of 64 x 64, 48 nodes: 48 us; one sequence, 32 heads, 8 nodes: 6.4 us.  Bound by a turn's chain (decays,
+// Measured in a graph: 256 sequences x 32 heads of 128 x 128, trees of 16 nodes: 189 us for 0.70 GB that cannot be done without
+// (103 us of HBM); 64 x 8 of 64 x 64, 48 nodes: 48 us; one sequence, 32 heads, 8 nodes: 6.5 us.  Bound by a turn's chain (decays,
 // rows, product, V - P, product, outputs; 11 to 12 thousand clocks at 16 nodes) with two CTAs an SM to fill it, one from 17
 // nodes on, where TMEM and shared memory hold no more.  Decays outside the range: 283 for 196 us at 16 nodes, 111 for 49 at 48.
 #include "common.cuh"
@@ -584,6 +584,13 @@ kda_tree_kernel(const TreeArgs a)
             }
             if (far) s_walk[odd] = 1;
             bool walk = false;
+            // the next turn's inputs, into what is done with: before the other slabs, or behind them where registers are short
+            // (16 nodes: 196 us before them, 189 behind; 32: 445, 475)
+            auto ahead = [&](int chunk) {
+                if (chunk + 1 < chunks) return;
+                next = Turn(now.first + stride, heads, a.H);
+                if (next.first < heads) fetch(next);
+            };
 
 #pragma unroll 1
             for (int chunk = 0; chunk < chunks; ++chunk, ++run) {
@@ -615,16 +622,14 @@ kda_tree_kernel(const TreeArgs a)
                 }
                 tc::fence_smem_to_async();
                 tc::mbar_arrive(b_rows);
-                if (chunk + 1 == chunks) {                              // the next turn's inputs, into what is done with
-                    next = Turn(now.first + stride, heads, a.H);
-                    if (next.first < heads) fetch(next);
-                }
+                if (Sh::kCtas == 1) ahead(chunk);
                 // 3. the other slabs
                 if (chunk == 0) {
 #pragma unroll 1
                     for (int q = kBufs + group; q < kSlabs && ok; q += 2) put(q);
                     slab += kSlabs;
                 }
+                if (Sh::kCtas > 1) ahead(chunk);
                 tc::named_sync(kTreeAll, 256);                          // (of all threads: whether to walk)
                 walk = *reinterpret_cast<volatile int*>(s_walk + odd) != 0;
                 if (tid == 0) {
