@@ -125,3 +125,28 @@ def test_rotation_leaves_a_model_without_positions_alone():
 def test_command(capsys):
     main(["--seqs", "3", "--prompt", "50", "--draft", "2", "--branches", "3", "--steps", "3", "--rotary", "10000"])
     assert "3 steps of 6 drafted tokens" in capsys.readouterr().out
+
+
+def test_without_drafts_and_with_parents_that_are_none():
+    """A tree of the last token alone is a step without drafts; a place whose parent is not before it holds no node, is never
+    part of a path, and is reported."""
+    m = HybridModel(seed=6, vocab=32, rotary=10000.0)
+    tok = _prompts(m, [30, 7], 3)
+    last = torch.tensor([3, 4], dtype=torch.int32, device=DEV)
+    a, b = HybridServer(m, 2, 100), HybridServer(m, 2, 100)
+    a.prompt(tok), b.prompt(tok)
+    u = torch.rand(2, 1, device=DEV, generator=torch.Generator(device=DEV).manual_seed(2))
+    empty = torch.empty(2, 0, dtype=torch.int32, device=DEV)
+    tokens, num, scores = a.step_tree(last, empty, empty.long(), u)
+    b.step(last, empty, torch.empty(2, 0, m.V, device=DEV), torch.empty(2, 0, device=DEV), u[:, 0].contiguous())
+    assert num.tolist() == [1, 1] and tokens.shape == (2, 1) and scores[3] is None
+    assert kda.kda_device_status() == kda.KDA_OK
+    _same(a, b, [t.tolist() + [int(l)] for t, l in zip(tok, last)])
+    # every token is drafted below place 1, which is below itself
+    c = HybridServer(m, 2, 200)
+    c.prompt(tok)
+    drafts = torch.arange(33, device=DEV).clamp_max(31).to(torch.int32).expand(2, -1).contiguous()
+    parents = torch.ones(2, 33, dtype=torch.long, device=DEV)
+    _, num, _ = c.step_tree(last, drafts, parents, torch.rand(2, 34, device=DEV))
+    assert num.tolist() == [1, 1]
+    assert kda.kda_device_status() == kda.KDA_ERR_INVALID_ARG
