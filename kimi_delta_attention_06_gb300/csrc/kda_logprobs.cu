@@ -21,8 +21,8 @@
 // A cluster of C CTAs serves a row, each a contiguous slice of it: its sums and its sorted list go into the shared memory
 // of the first, which joins them.
 //
-// Measured in a graph: 2048 rows of 131072 bf16, 1 alternative: 113 us, 4.7 TB/s; 256 rows of 100003, 8: 24.3 us; 4 rows of
-// 131072 fp32, 20: 10.8 us.  The pass alone runs at 6.2 TB/s; the rest is what follows it in each CTA, a chain of steps of a
+// Measured in a graph: 2048 rows of 131072 bf16, 1 alternative: 112 us, 4.8 TB/s; 256 rows of 100003, 8: 22.4 us; 4 rows of
+// 131072 fp32, 20: 9.3 us.  The pass alone runs at 6.2 TB/s; the rest is what follows it in each CTA, a chain of steps of a
 // few thousand clocks (sums, order of the maxima, the steps read again, order of what they hold).
 #include <cfloat>
 #include <cuda_bf16.h>
@@ -32,7 +32,7 @@
 namespace kda {
 
 constexpr int kLogThreads = 256, kLogWarps = kLogThreads / 32, kLogGroups = kLogThreads / 2, kLogMaxTop = 32, kLogSteps = 24;
-constexpr int kLogFew = 64, kLogKeep = 1024, kLogMaxCluster = 8;
+constexpr int kLogFew = 64, kLogKeep = 1024, kLogHits = 1024, kLogMaxCluster = 8;
 constexpr int kStatusToken = -1;                 // KDA_ERR_INVALID_ARG, recorded on the device
 using LogKey = unsigned long long;               // a value's order bits, then its index negated; 0: none
 
@@ -202,11 +202,12 @@ kda_logprobs_kernel(const LogArgs a)
     __shared__ int s_rank[kLogGroups];
     __shared__ float s_step[kLogSteps][kLogThreads];                    // maxima of each thread's steps, or of several
     __shared__ LogKey s_keep[kLogKeep];
+    __shared__ int s_hit[kLogHits];                                     // steps to read again: a thread's first chunk of each
     __shared__ LogKey s_list[kLogMaxTop];
     __shared__ __align__(8) uint64_t s_bar;
     __shared__ LogKey s_least, s_next;
     __shared__ LogSums s_all;
-    __shared__ int s_count, s_ok;
+    __shared__ int s_count, s_hits, s_ok;
 
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const int C = a.C, rank = C > 1 ? static_cast<int>(tc::cluster_ctarank()) : 0;
@@ -358,7 +359,7 @@ kda_logprobs_kernel(const LogArgs a)
     }
     const uint32_t gv = max(mv, __shfl_xor_sync(0xffffffffu, mv, 1));
     if ((tid & 1) == 0) { s_val[tid >> 1] = gv; s_rank[tid >> 1] = 0; }
-    if (tid == 0) s_count = 0;
+    if (tid == 0) s_count = s_hits = 0;
     if (tid < kLogMaxTop) s_list[tid] = 0;
     __syncthreads();
     if (warp == 0) {
@@ -459,16 +460,50 @@ kda_logprobs_kernel(const LogArgs a)
                 if (y >= bound) use(y);
             }
         };
-        scan([&](LogKey e) {
+        auto keep = [&](LogKey e) {
             const int i = atomicAdd(&s_count, 1);
             if (i < kLogKeep) s_keep[i] = e;
-        });
+        };
+        // the steps that reach it, first, then their chunks a thread each: one latency for all of them (each thread its own, one
+        // after another, 2048 rows of 131072, 20 alternatives: 163 us to 137, caches flushed)
+#pragma unroll 4
+        for (int z = 0; z * fold * kStep + tid < chunks; ++z) {
+            if (s_step[z][tid] < reach) continue;
+            for (int k0 = z * fold * kStep + tid; k0 < min((z + 1) * fold * kStep, chunks); k0 += kStep) {
+                const int i = atomicAdd(&s_hits, 1);
+                if (i < kLogHits) s_hit[i] = k0;
+            }
+        }
+        __syncthreads();
+        const int hits = s_hits;
+        if (hits <= kLogHits) {
+            for (int i = tid; i < hits * U; i += kLogThreads) {
+                const int k = s_hit[i / U] + i % U * kLogThreads;
+                if (k >= chunks) continue;
+                const uint4 one[1] = {__ldg(body + k)};
+                if (Vec::template top<1>(one) < reach) continue;
+                float e[N];
+                Vec::unpack(one[0], e);
+#pragma unroll
+                for (int j = 0; j < N; ++j) {
+                    const LogKey y = log_key(order_bits(e[j]), first + k * N + j);
+                    if (y >= bound) keep(y);
+                }
+            }
+            if (tid < singles) {
+                const LogKey y = log_key(order_bits(Vec::one(row + single(tid))), single(tid));
+                if (y >= bound) keep(y);
+            }
+        } else {
+            scan(keep);
+        }
         __syncthreads();
         const int n = s_count;
         if (n <= kLogKeep) {
             for (int i = tid; i < n; i += kLogThreads) {
                 const LogKey e = s_keep[i];
                 int above = 0;
+#pragma unroll 4
                 for (int j = 0; j < n; ++j) above += s_keep[j] > e;
                 if (above < top) s_list[above] = e;
             }
@@ -538,6 +573,7 @@ kda_logprobs_kernel(const LogArgs a)
             for (int i = tid; i < n; i += kLogThreads) {
                 const LogKey e = s_keep[i];
                 int above = 0;
+#pragma unroll 4
                 for (int j = 0; j < n; ++j) above += s_keep[j] > e;
                 if (above < top) s_list[above] = e;
             }
@@ -569,7 +605,7 @@ kda_logprobs_kernel(const LogArgs a)
 }
 
 // CTAs a row: as many as run at once, of slices that a step or more of every thread takes.  (2048 rows of 131072 bf16, 1, 2, 4
-// CTAs a row: 113, 136, 180 us; 256 of 100003: 26.1, 24.3, 32.3; 4 of 131072 fp32, 1, 2, 4, 8: 27.7, 20.3, 14.2, 10.8)
+// CTAs a row: 112, 134, 176 us; 256 of 100003: 23.1, 22.4, 30.1; 4 of 131072 fp32, 1, 2, 4, 8: 21.0, 15.2, 11.3, 9.3)
 int logprobs_cluster(int R, int V, int sms, int bytes) {
     int C = 1;
     while (C < kLogMaxCluster && static_cast<long long>(R) * 2 * C <= 4 * sms && V / (2 * C) * bytes >= 16384) C *= 2;
