@@ -62,7 +62,7 @@ int launch_decode_tree(const uint16_t* q, const uint16_t* k, const uint16_t* v, 
 int launch_token_logprobs(const void* x, int f32, long long ld, const int32_t* tok, int R, int V, int top, float scale,
                           float* logprob, int32_t* rank, float* entropy, float* top_lp, int32_t* top_tok, int* status,
                           cudaStream_t stream);
-size_t latent_decode_scratch(int rows, bool tree, int e4m3);
+size_t latent_decode_scratch(int rows, int N, bool tree, int e4m3);
 int launch_latent_prefill(const uint16_t* q, const uint16_t* k, long long ldk, long long hdk, const uint16_t* v,
                           long long ldv, long long hdv, const uint16_t* r, long long ldr, const int32_t* cu_q,
                           const int32_t* cu_k, int num_seqs, int total_q, int total_k, int units, int H, int causal,
@@ -928,7 +928,7 @@ static int latent_decode_call(const uint16_t* q, const void* cache, int cache_dt
     if (rc != KDA_OK) return rc;
     const cudaStream_t st = static_cast<cudaStream_t>(stream);
     void* ws = nullptr;
-    if (cudaMallocFromPoolAsync(&ws, kda::latent_decode_scratch(K * H, parents != nullptr, cache_dtype == KDA_CACHE_E4M3), pool, st) != cudaSuccess)
+    if (cudaMallocFromPoolAsync(&ws, kda::latent_decode_scratch(K * H, N, parents != nullptr, cache_dtype == KDA_CACHE_E4M3), pool, st) != cudaSuccess)
         return KDA_ERR_CUDA;
     rc = kda::launch_latent_decode(q, cache, cache_dtype == KDA_CACHE_E4M3, num_pages, page_size, block_table, max_pages,
                                    seq_lens, parents, N, K, H, sm_scale, out, lse, ws, status, st);

@@ -78,17 +78,14 @@ __device__ __forceinline__ int lat_len(const LatWork& w, int n) {
     const int seqs = w.N / w.each, tile = n / seqs, s = n - tile * seqs;
     return w.need && tile >= w.need[s] ? 0 : lat_seq(w, s);
 }
-// Row tiles that a tree needs: R rows each, H of a node, up to its last place with a node.
-__device__ __forceinline__ int lat_need(const int32_t* parents, int K, int H, int R) {
-    int last = 0;
-    for (int j = 0; j < K; ++j)
-        if (__ldg(parents + j) >= -1) last = j + 1;
+// Row tiles that a tree needs, as one warp finds it: R rows each, H of a node, up to its last place with a node.
+__device__ __forceinline__ int lat_need(const int32_t* parents, int K, int H, int R, int lane) {
+    const unsigned lo = __ballot_sync(0xffffffffu, lane < K && __ldg(parents + lane) >= -1);
+    const unsigned hi = K > 32 ? __ballot_sync(0xffffffffu, lane + 32 < K && __ldg(parents + lane + 32) >= -1) : 0u;
+    const int last = hi ? 64 - __clz(hi) : 32 - __clz(lo);
     return (last * H + R - 1) / R;
 }
-// Row tiles of sequence n that are sequences of their own and not left out.
-__device__ __forceinline__ int lat_needed(const LatWork& w, const int32_t* parents, int K, int H, int R, int n) {
-    return w.each <= 1 ? 1 : w.N / w.each <= kMaxNeed ? lat_need(parents + static_cast<long long>(n) * K, K, H, R) : w.each;
-}
+constexpr int kFewTrees = 32;                   // up to so many are looked at by every warp of the kernel that joins
 __device__ __forceinline__ int lat_tiles(int len) { return (len + kTile - 1) / kTile; }
 __device__ __forceinline__ int lat_count(const LatWork& w, int len) { return len > 0 ? lat_tiles(len) + w.lead : 0; }   // with the lead
 // Runs in use for T tiles, and the bounds of run c.
@@ -188,8 +185,30 @@ struct LatArgs {
     uint16_t* out;
     float* lse;
     float *part_o, *part_ml;                     // partials: [run][row tile][2][R][512], [..][R][2]
+    int32_t* need;                               // [N]: row tiles that a tree needs, where many trees' are sequences of their own
     int* status;
 };
+
+// Row tiles of each sequence that are sequences of their own and not left out: lane i of sequence i0 + i.  Few trees every warp
+// of the joining kernel looks at itself, while the attention runs; of many it waits for what the attention has found (looked
+// at by every warp, 512 trees of 64 nodes took 28 ms, of which the attention was 0.7).
+template <int R>
+__device__ __forceinline__ int lat_needed(const LatArgs& a, int i0, int lane) {
+    const int seqs = a.w.N / a.w.each;
+    if (a.w.each <= 1 || seqs > kMaxNeed) return a.w.each;
+    if (seqs > kFewTrees) return i0 + lane < seqs ? a.need[i0 + lane] : 0;
+    int mine = 0;
+#pragma unroll 4
+    for (int i = 0; i < seqs; ++i) {
+        const int need = lat_need(a.parents + static_cast<long long>(i) * a.K, a.K, a.H, R, lane);
+        mine = lane == i ? need : mine;
+    }
+    return mine;
+}
+__device__ __forceinline__ void lat_wait_needed(const LatArgs& a) {
+    const int seqs = a.w.N / a.w.each;
+    if (a.w.each > 1 && seqs > kFewTrees && seqs <= kMaxNeed) asm volatile("griddepcontrol.wait;" ::: "memory");
+}
 
 template <int R, bool E4M3>
 struct LatShape {
@@ -380,8 +399,12 @@ kda_latent_decode_kernel(const __grid_constant__ LatMaps maps, const LatArgs a)
     }
     if (tid < R) s_j[tid] = min((rt * R + tid) / a.H, a.K - 1);
     if (TREE && work.each > 1 && work.N / work.each <= kMaxNeed) {
-        for (int i = tid; i < work.N / work.each; i += Sh::kThreads) {
-            s_need[i] = static_cast<uint8_t>(lat_need(a.parents + static_cast<long long>(i) * a.K, a.K, a.H, R));
+        const int seqs = work.N / work.each;
+#pragma unroll 4
+        for (int i = warp; i < seqs; i += Sh::kThreads / 32) {
+            const int need = lat_need(a.parents + static_cast<long long>(i) * a.K, a.K, a.H, R, lane);
+            if (lane == 0) s_need[i] = static_cast<uint8_t>(need);
+            if (lane == 0 && blockIdx.x == 0 && seqs > kFewTrees) a.need[i] = need;     // for the kernel that joins
         }
         work.need = s_need;
     }
@@ -891,16 +914,20 @@ kda_latent_combine_kernel(const LatArgs a, int Q, int NG)
     __shared__ long long s_sum[2][16];
     __shared__ float4 s_acc[512];
     __shared__ float2 s_ml[16];                                 // (m, l) of each group
+    __shared__ int s_need;                                      // row tiles of sequence n
     const int lanes = 128 / Q, threads = lanes * NG;
     const int unit = blockIdx.x / Q, n = unit / a.rows, row = unit % a.rows;
     const int tid = threadIdx.x, grp = tid / lanes, ch = (blockIdx.x % Q * lanes + tid % lanes) * 4;
     const int warps = threads >> 5;
     long long before = 0, T = 0;
     const int seqs = a.w.N / a.w.each, tile = a.w.each > 1 ? row / R : 0;     // (of those that are sequences of their own)
-    for (int i = tid; i < seqs; i += threads) {
+    lat_wait_needed(a);
+    for (int i0 = tid & ~31; i0 < seqs; i0 += threads) {
+        const int i = i0 + (tid & 31), need = lat_needed<R>(a, i0, tid & 31);
+        if (i >= seqs) continue;
         const int raw = a.w.seq_lens[i], tiles = lat_tiles(lat_seq(a.w, i)), count = tiles > 0 ? tiles + a.w.lead : 0;
         if (i == n && row == 0 && raw != lat_seq(a.w, i)) set_status(a.status, kStatusIndex);   // out of range: counted as 0
-        const int need = lat_needed(a.w, a.parents, a.K, a.H, R, i);
+        if (i == n) s_need = need;
         T += static_cast<long long>(need) * count;
         before += static_cast<long long>(min(need, tile) + (i < n && need > tile ? 1 : 0)) * count;
     }
@@ -913,7 +940,7 @@ kda_latent_combine_kernel(const LatArgs a, int Q, int NG)
     __syncthreads();
     T = before = 0;
     for (int i = 0; i < warps; ++i) { T += s_sum[0][i]; before += s_sum[1][i]; }
-    const int tiles = tile < lat_needed(a.w, a.parents, a.K, a.H, R, n) ? lat_tiles(lat_seq(a.w, n)) : 0;
+    const int tiles = tile < s_need ? lat_tiles(lat_seq(a.w, n)) : 0;
     const long long at = static_cast<long long>(n) * a.rows + row;
     int c0 = 0, parts = 1, late = 0;
     if (tiles > 0) {
@@ -997,22 +1024,26 @@ kda_latent_combine_rows_kernel(const LatArgs a)
     const int row = static_cast<int>(at - static_cast<long long>(n) * a.rows);
     const int tile = a.w.each > 1 ? min(row, a.rows - 1) / R : 0;            // (of those that are sequences of their own)
     long long T = 0, before = 0;
-    int len = 0;
+    int len = 0, needed = 0;
+    lat_wait_needed(a);
     for (int i0 = 0; i0 < seqs; i0 += 32) {
         const int i = i0 + lane, v = i < seqs ? lat_seq(a.w, i) : 0;
         if (i == n && row == 0 && a.w.seq_lens[i] != v) set_status(a.status, kStatusIndex);   // out of range: counted as 0
         const long long count = lat_count(a.w, v);
-        const int need = i < seqs ? lat_needed(a.w, a.parents, a.K, a.H, R, i) : 0;
+        const int need = lat_needed<R>(a, i0, lane);                         // (past the last: no tiles)
         T += need * count;
         before += (min(need, tile) + (i < n && need > tile ? 1 : 0)) * count;
-        if (n >= i0 && n < i0 + 32) len = __shfl_sync(0xffffffffu, v, n - i0);
+        if (n >= i0 && n < i0 + 32) {
+            len = __shfl_sync(0xffffffffu, v, n - i0);
+            needed = __shfl_sync(0xffffffffu, need, n - i0);
+        }
     }
 #pragma unroll
     for (int off = 16; off > 0; off >>= 1) {
         T += __shfl_xor_sync(0xffffffffu, T, off);
         before += __shfl_xor_sync(0xffffffffu, before, off);
     }
-    const int tiles = tile < lat_needed(a.w, a.parents, a.K, a.H, R, n) ? lat_tiles(len) : 0;
+    const int tiles = tile < needed ? lat_tiles(len) : 0;
     int c0 = 0, parts = 1, late = 0;
     if (tiles > 0) {
         const long long runs = lat_runs(T, a.w.G);
@@ -1177,10 +1208,10 @@ int latent_decode_runs(int rows) {
 // some of the second are left out, what the first have read has left L2 (16 trees of 2 to 4 nodes x 32 heads over 341k
 // tokens: apart 141 us, together 128; e4m3, apart: 122, chains of 4, all of whose rows are there: 127).
 static bool tree_split(int rows, bool tree, int e4m3) { return tree && rows > (e4m3 ? 64 : 128); }
-size_t latent_decode_scratch(int rows, bool tree, int e4m3) {
+size_t latent_decode_scratch(int rows, int N, bool tree, int e4m3) {
     const size_t R = rows_per_cta(rows), RT = (rows + R - 1) / R;
     const size_t runs = tree_split(rows, tree, e4m3) ? latent_decode_runs(64) : latent_decode_runs(rows) * RT;
-    return runs * 2 * R * (kLatDim + 2) * sizeof(float);
+    return runs * 2 * R * (kLatDim + 2) * sizeof(float) + (tree_split(rows, tree, e4m3) ? static_cast<size_t>(N) * sizeof(int32_t) : 0);
 }
 
 int launch_latent_decode(const uint16_t* q, const void* cache, int e4m3, int num_pages, int page_size,
@@ -1208,6 +1239,7 @@ int launch_latent_decode(const uint16_t* q, const void* cache, int e4m3, int num
     a.lse = lse;
     a.part_o = static_cast<float*>(scratch);
     a.part_ml = a.part_o + static_cast<size_t>(a.w.G) * a.RT * 2 * R * kLatDim;
+    a.need = reinterpret_cast<int32_t*>(a.part_ml + static_cast<size_t>(a.w.G) * a.RT * 2 * R * 2);
     a.status = status;
     LatMaps maps;
     const CUtensorMapSwizzle swz = CU_TENSOR_MAP_SWIZZLE_128B;
