@@ -65,9 +65,12 @@ struct LatWork {
     int least;                                  // shortest length of a sequence that is not empty (a tree's K nodes)
     long long max_len;
     int each;                                   // row tiles that are sequences of their own (1: none are), ..
-    const uint8_t* need;                        // .. and how many of them a sequence needs (nullptr: all)
+    int most;                                   // (kMaxNeed)
+    const uint8_t* need;                        // .. and how many of them a sequence needs (nullptr: all), ..
+    const int32_t* lens;                        // .. beside its length (0: of an empty one)
 };
-constexpr int kMaxNeed = 512;                   // up to so many sequences are looked at for it
+// Up to so many sequences are looked at for it (shared memory; of more, all row tiles are worked through).
+template <bool E4M3> constexpr int kMaxNeed = E4M3 ? 512 : 128;
 
 __device__ __forceinline__ int lat_seq(const LatWork& w, int n) {
     const int len = w.seq_lens[n];
@@ -76,7 +79,7 @@ __device__ __forceinline__ int lat_seq(const LatWork& w, int n) {
 __device__ __forceinline__ int lat_len(const LatWork& w, int n) {
     if (w.each <= 1) return lat_seq(w, n);
     const int seqs = w.N / w.each, tile = n / seqs, s = n - tile * seqs;
-    return w.need && tile >= w.need[s] ? 0 : lat_seq(w, s);
+    return !w.need ? lat_seq(w, s) : tile < w.need[s] ? w.lens[s] : 0;
 }
 // Row tiles that a tree needs, as one warp finds it: R rows each, H of a node, up to its last place with a node.
 __device__ __forceinline__ int lat_need(const int32_t* parents, int K, int H, int R, int lane) {
@@ -85,7 +88,9 @@ __device__ __forceinline__ int lat_need(const int32_t* parents, int K, int H, in
     const int last = hi ? 64 - __clz(hi) : 32 - __clz(lo);
     return (last * H + R - 1) / R;
 }
-constexpr int kFewTrees = 32;                   // up to so many are looked at by every warp of the kernel that joins
+// Up to so many sequences every warp of the joining kernel counts itself, while the attention runs; of more it takes what the
+// attention has counted (512 chains of 8 x 32 rows over 200 tokens, e4m3: 345 -> 247 us; 64 x 1 x 32 rows: 187 -> 190).
+constexpr int few_sequences(bool apart) { return apart ? 32 : 128; }
 __device__ __forceinline__ int lat_tiles(int len) { return (len + kTile - 1) / kTile; }
 __device__ __forceinline__ int lat_count(const LatWork& w, int len) { return len > 0 ? lat_tiles(len) + w.lead : 0; }   // with the lead
 // Runs in use for T tiles, and the bounds of run c.
@@ -105,6 +110,7 @@ struct SegWalk {
     long long pos, end, base;                   // next tile, end of the run, first (counted) tile of sequence n
     int n, len, count;                          // count: its tiles and its lead
     int t0, t1;                                 // current segment: tiles [t0, t1) of sequence n
+    long long total;                            // tiles of all sequences, counted with their leads
     bool first;
 
     __device__ __forceinline__ void init(const LatWork& w, int c) {
@@ -119,6 +125,7 @@ struct SegWalk {
             for (int off = 16; off > 0; off >>= 1) T += __shfl_xor_sync(0xffffffffu, T, off);
         }
         pos = end = base = 0;
+        total = T;
         n = len = count = t0 = t1 = 0;
         first = true;
         if (T == 0) return;
@@ -185,29 +192,45 @@ struct LatArgs {
     uint16_t* out;
     float* lse;
     float *part_o, *part_ml;                     // partials: [run][row tile][2][R][512], [..][R][2]
-    int32_t* need;                               // [N]: row tiles that a tree needs, where many trees' are sequences of their own
+    long long* first;                            // [N + 1]: counted tiles before each sequence, of all; nullptr where they are few
     int* status;
 };
 
-// Row tiles of each sequence that are sequences of their own and not left out: lane i of sequence i0 + i.  Few trees every warp
-// of the joining kernel looks at itself, while the attention runs; of many it waits for what the attention has found (looked
-// at by every warp, 512 trees of 64 nodes took 28 ms, of which the attention was 0.7).
+// Row tiles of sequence n that are sequences of their own and not left out (a warp together).
 template <int R>
-__device__ __forceinline__ int lat_needed(const LatArgs& a, int i0, int lane) {
-    const int seqs = a.w.N / a.w.each;
-    if (a.w.each <= 1 || seqs > kMaxNeed) return a.w.each;
-    if (seqs > kFewTrees) return i0 + lane < seqs ? a.need[i0 + lane] : 0;
-    int mine = 0;
-#pragma unroll 4
-    for (int i = 0; i < seqs; ++i) {
-        const int need = lat_need(a.parents + static_cast<long long>(i) * a.K, a.K, a.H, R, lane);
-        mine = lane == i ? need : mine;
-    }
-    return mine;
+__device__ __forceinline__ int lat_needed(const LatArgs& a, int n, int lane) {
+    return a.w.each <= 1 || a.w.N / a.w.each > a.w.most ? a.w.each
+                                                        : lat_need(a.parents + static_cast<long long>(n) * a.K, a.K, a.H, R, lane);
 }
-__device__ __forceinline__ void lat_wait_needed(const LatArgs& a) {
+// Of few sequences: the counted tiles of all, and of those before row tile `tile` of sequence n; its own length and row tiles.
+struct LatCount { long long T, before; int len, need; };
+template <int R>
+__device__ __forceinline__ LatCount lat_counted(const LatArgs& a, int n, int tile, int lane) {
     const int seqs = a.w.N / a.w.each;
-    if (a.w.each > 1 && seqs > kFewTrees && seqs <= kMaxNeed) asm volatile("griddepcontrol.wait;" ::: "memory");
+    LatCount c{0, 0, 0, 0};
+    for (int i0 = 0; i0 < seqs; i0 += 32) {
+        const int i = i0 + lane, v = i < seqs ? lat_seq(a.w, i) : 0;
+        int mine = a.w.each;
+        if (a.w.each > 1)
+#pragma unroll 4
+            for (int k = i0; k < min(i0 + 32, seqs); ++k) {
+                const int need = lat_needed<R>(a, k, lane);
+                mine = i == k ? need : mine;
+            }
+        const long long count = lat_count(a.w, v);
+        c.T += mine * count;
+        c.before += (min(mine, tile) + (i < n && mine > tile ? 1 : 0)) * count;
+        if (n >= i0 && n < i0 + 32) {
+            c.len = __shfl_sync(0xffffffffu, v, n - i0);
+            c.need = __shfl_sync(0xffffffffu, mine, n - i0);
+        }
+    }
+#pragma unroll
+    for (int off = 16; off > 0; off >>= 1) {
+        c.T += __shfl_xor_sync(0xffffffffu, c.T, off);
+        c.before += __shfl_xor_sync(0xffffffffu, c.before, off);
+    }
+    return c;
 }
 
 template <int R, bool E4M3>
@@ -241,7 +264,7 @@ struct LatShape {
     static constexpr uint32_t kTmemCols = kUsed <= 128u ? 128u : kUsed <= 256u ? 256u : 512u;
     static_assert(kUsed <= 512u, "TMEM");
 };
-static_assert(LatShape<64, false>::kBytes + 64 * 8 + kMaxNeed <= 232448 && LatShape<64, true>::kBytes + 64 * 8 + kMaxNeed <= 232448,
+static_assert(LatShape<64, false>::kBytes + 64 * 8 + 5 * kMaxNeed<false> <= 232448 && LatShape<64, true>::kBytes + 64 * 8 + 5 * kMaxNeed<true> <= 232448,
               "227 KB of shared memory");
 
 // A row's weights are exp2(x - m).  m follows the row's maximum M lazily: bf16, m <= M <= m + 8 (the
@@ -365,7 +388,8 @@ kda_latent_decode_kernel(const __grid_constant__ LatMaps maps, const LatArgs a)
     int* s_j = reinterpret_cast<int*>(s_f + R);                 // [R]: query token of each row
     float* s_a = s_f + 2 * R;                                   // [R]: e4m3: 2^k * scale of each row
     uint64_t* s_set = reinterpret_cast<uint64_t*>(s_a + R);     // [R]: TREE: the nodes that each row sees (none: no node itself)
-    uint8_t* s_need = reinterpret_cast<uint8_t*>(s_set + R);    // [kMaxNeed]: TREE: row tiles of each sequence
+    int32_t* s_lens = reinterpret_cast<int32_t*>(s_set + R);    // [kMaxNeed]: TREE: each sequence's length, ..
+    uint8_t* s_need = reinterpret_cast<uint8_t*>(s_lens + kMaxNeed<E4M3>);    // .. and its row tiles
     constexpr int NS = Sh::kStages;
 
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
@@ -398,15 +422,16 @@ kda_latent_decode_kernel(const __grid_constant__ LatMaps maps, const LatArgs a)
         else tc::tma_prefetch_map(&maps.q);
     }
     if (tid < R) s_j[tid] = min((rt * R + tid) / a.H, a.K - 1);
-    if (TREE && work.each > 1 && work.N / work.each <= kMaxNeed) {
+    if (TREE && work.each > 1 && work.N / work.each <= kMaxNeed<E4M3>) {
         const int seqs = work.N / work.each;
 #pragma unroll 4
         for (int i = warp; i < seqs; i += Sh::kThreads / 32) {
             const int need = lat_need(a.parents + static_cast<long long>(i) * a.K, a.K, a.H, R, lane);
             if (lane == 0) s_need[i] = static_cast<uint8_t>(need);
-            if (lane == 0 && blockIdx.x == 0 && seqs > kFewTrees) a.need[i] = need;     // for the kernel that joins
         }
+        for (int i = tid; i < seqs; i += Sh::kThreads) s_lens[i] = lat_seq(a.w, i);
         work.need = s_need;
+        work.lens = s_lens;
     }
     if (warp == Sh::kMmaWarp) tc::tmem_alloc(s_tmem, Sh::kTmemCols);
     tc::fence_before_sync();
@@ -886,7 +911,9 @@ kda_latent_decode_kernel(const __grid_constant__ LatMaps maps, const LatArgs a)
                 }
                 at = next;
             }
+            if (a.first && lane == 0) a.first[sw.n] = sw.base;   // (for the kernel that joins; every part of a sequence says the same)
         }
+        if (a.first && blockIdx.x == 0 && lane == 0) a.first[a.w.N] = sw.total;
         // copies in flight land before the CTA's shared memory is given back
         if (!ok) {
             if (seg > 0) tc::mbar_wait_bounded(q_full, (seg - 1) & 1, kWaitLimitNs);
@@ -911,36 +938,16 @@ template <int R>
 __global__ void __launch_bounds__(512)
 kda_latent_combine_kernel(const LatArgs a, int Q, int NG)
 {
-    __shared__ long long s_sum[2][16];
     __shared__ float4 s_acc[512];
     __shared__ float2 s_ml[16];                                 // (m, l) of each group
-    __shared__ int s_need;                                      // row tiles of sequence n
-    const int lanes = 128 / Q, threads = lanes * NG;
+    const int lanes = 128 / Q;
     const int unit = blockIdx.x / Q, n = unit / a.rows, row = unit % a.rows;
     const int tid = threadIdx.x, grp = tid / lanes, ch = (blockIdx.x % Q * lanes + tid % lanes) * 4;
-    const int warps = threads >> 5;
-    long long before = 0, T = 0;
-    const int seqs = a.w.N / a.w.each, tile = a.w.each > 1 ? row / R : 0;     // (of those that are sequences of their own)
-    lat_wait_needed(a);
-    for (int i0 = tid & ~31; i0 < seqs; i0 += threads) {
-        const int i = i0 + (tid & 31), need = lat_needed<R>(a, i0, tid & 31);
-        if (i >= seqs) continue;
-        const int raw = a.w.seq_lens[i], tiles = lat_tiles(lat_seq(a.w, i)), count = tiles > 0 ? tiles + a.w.lead : 0;
-        if (i == n && row == 0 && raw != lat_seq(a.w, i)) set_status(a.status, kStatusIndex);   // out of range: counted as 0
-        if (i == n) s_need = need;
-        T += static_cast<long long>(need) * count;
-        before += static_cast<long long>(min(need, tile) + (i < n && need > tile ? 1 : 0)) * count;
-    }
-#pragma unroll
-    for (int off = 16; off > 0; off >>= 1) {
-        T += __shfl_xor_sync(0xffffffffu, T, off);
-        before += __shfl_xor_sync(0xffffffffu, before, off);
-    }
-    if ((tid & 31) == 0) { s_sum[0][tid >> 5] = T; s_sum[1][tid >> 5] = before; }
-    __syncthreads();
-    T = before = 0;
-    for (int i = 0; i < warps; ++i) { T += s_sum[0][i]; before += s_sum[1][i]; }
-    const int tiles = tile < s_need ? lat_tiles(lat_seq(a.w, n)) : 0;
+    const int tile = a.w.each > 1 ? row / R : 0;                 // (of those that are sequences of their own)
+    const LatCount c = lat_counted<R>(a, n, tile, tid & 31);
+    if (tid == 0 && row == 0 && a.w.seq_lens[n] != c.len) set_status(a.status, kStatusIndex);    // out of range: counted as 0
+    const long long T = c.T, before = c.before;
+    const int tiles = tile < c.need ? lat_tiles(c.len) : 0;
     const long long at = static_cast<long long>(n) * a.rows + row;
     int c0 = 0, parts = 1, late = 0;
     if (tiles > 0) {
@@ -1023,27 +1030,25 @@ kda_latent_combine_rows_kernel(const LatArgs a)
     const int n = static_cast<int>(min(at, static_cast<long long>(seqs) * a.rows - 1) / a.rows);
     const int row = static_cast<int>(at - static_cast<long long>(n) * a.rows);
     const int tile = a.w.each > 1 ? min(row, a.rows - 1) / R : 0;            // (of those that are sequences of their own)
-    long long T = 0, before = 0;
-    int len = 0, needed = 0;
-    lat_wait_needed(a);
-    for (int i0 = 0; i0 < seqs; i0 += 32) {
-        const int i = i0 + lane, v = i < seqs ? lat_seq(a.w, i) : 0;
-        if (i == n && row == 0 && a.w.seq_lens[i] != v) set_status(a.status, kStatusIndex);   // out of range: counted as 0
-        const long long count = lat_count(a.w, v);
-        const int need = lat_needed<R>(a, i0, lane);                         // (past the last: no tiles)
-        T += need * count;
-        before += (min(need, tile) + (i < n && need > tile ? 1 : 0)) * count;
-        if (n >= i0 && n < i0 + 32) {
-            len = __shfl_sync(0xffffffffu, v, n - i0);
-            needed = __shfl_sync(0xffffffffu, need, n - i0);
+    LatCount c{0, 0, 0, 0};
+    if (!a.first) {
+        c = lat_counted<R>(a, n, tile, lane);
+    } else {
+        c.len = lat_seq(a.w, n);
+        c.need = lat_needed<R>(a, n, lane);
+    }
+    if (lane == 0 && row == 0 && a.w.seq_lens[n] != c.len) set_status(a.status, kStatusIndex);   // out of range: counted as 0
+    const int tiles = tile < c.need ? lat_tiles(c.len) : 0;
+    if (a.first) {                                               // (of many: as the attention has counted them)
+        asm volatile("griddepcontrol.wait;" ::: "memory");
+        if (tiles > 0) {
+            c.T = a.first[a.w.N];
+            c.before = a.first[tile * seqs + n];
+            // (a wait that ran out there has left them anything: nothing is joined then)
+            if (c.before < 0 || c.before + a.w.lead + tiles > c.T || c.T >> 44) return;
         }
     }
-#pragma unroll
-    for (int off = 16; off > 0; off >>= 1) {
-        T += __shfl_xor_sync(0xffffffffu, T, off);
-        before += __shfl_xor_sync(0xffffffffu, before, off);
-    }
-    const int tiles = tile < needed ? lat_tiles(len) : 0;
+    const long long T = c.T, before = c.before;
     int c0 = 0, parts = 1, late = 0;
     if (tiles > 0) {
         const long long runs = lat_runs(T, a.w.G);
@@ -1158,7 +1163,7 @@ int sm_count() {
 template <int R, bool E4M3, bool TREE>
 int launch_decode_shape(const LatMaps& maps, const LatArgs& a, cudaStream_t stream) {
     using Sh = LatShape<R, E4M3>;
-    constexpr uint32_t bytes = Sh::kBytes + (TREE ? R * 8u + kMaxNeed : 0u);
+    constexpr uint32_t bytes = Sh::kBytes + (TREE ? R * 8u + 5u * kMaxNeed<E4M3> : 0u);
     static bool attr_done[kMaxDevicesAttr] = {};
     if (!raise_smem_limit(reinterpret_cast<const void*>(kda_latent_decode_kernel<R, E4M3, TREE>), static_cast<int>(bytes), attr_done))
         return -3;
@@ -1170,7 +1175,7 @@ int launch_decode_shape(const LatMaps& maps, const LatArgs& a, cudaStream_t stre
     // rows are too few for a block on each SM (20 tokens of 48 rows each, 192 rows: 16.5 us with 4, 15.3
     // with 1; 24 rows over 33851 tokens: 19.8 with 4, 27.4 with 1 and a pass each for maxima, sums and O)
     const int seqs = a.w.N / a.w.each, about = a.w.G / a.w.N + 1;
-    const bool by_warp = about <= 16;
+    const bool by_warp = about <= 16 || a.first;
     const int Q = static_cast<long long>(seqs) * a.rows < sm_count() ? 4 : 1;
     int NG = 1;
     while (NG < 4 * Q && NG * 8 < about) NG *= 2;
@@ -1210,8 +1215,9 @@ int latent_decode_runs(int rows) {
 static bool tree_split(int rows, bool tree, int e4m3) { return tree && rows > (e4m3 ? 64 : 128); }
 size_t latent_decode_scratch(int rows, int N, bool tree, int e4m3) {
     const size_t R = rows_per_cta(rows), RT = (rows + R - 1) / R;
-    const size_t runs = tree_split(rows, tree, e4m3) ? latent_decode_runs(64) : latent_decode_runs(rows) * RT;
-    return runs * 2 * R * (kLatDim + 2) * sizeof(float) + (tree_split(rows, tree, e4m3) ? static_cast<size_t>(N) * sizeof(int32_t) : 0);
+    const bool apart = tree_split(rows, tree, e4m3);
+    const size_t runs = apart ? latent_decode_runs(64) : latent_decode_runs(rows) * RT;
+    return runs * 2 * R * (kLatDim + 2) * sizeof(float) + (N > few_sequences(apart) ? (static_cast<size_t>(N) * (apart ? RT : 1) + 1) * sizeof(long long) : 0);
 }
 
 int launch_latent_decode(const uint16_t* q, const void* cache, int e4m3, int num_pages, int page_size,
@@ -1224,7 +1230,7 @@ int launch_latent_decode(const uint16_t* q, const void* cache, int e4m3, int num
     const bool apart = tree_split(rows, parents != nullptr, e4m3);
     const int each = apart ? (rows + R - 1) / R : 1;
     a.w = LatWork{seq_lens, N * each, latent_decode_runs(apart ? 64 : rows), N * each == 1 ? 0 : e4m3 && R == 64 ? 8 : 2, parents ? K : 0,
-                  static_cast<long long>(max_pages) * page_size, each, nullptr};
+                  static_cast<long long>(max_pages) * page_size, each, e4m3 ? kMaxNeed<true> : kMaxNeed<false>, nullptr, nullptr};
     if (a.w.G <= 0) return -3;
     a.ch = LatentCache{static_cast<const uint8_t*>(cache), table, num_pages, page_size, max_pages};
     a.q = q;
@@ -1239,7 +1245,7 @@ int launch_latent_decode(const uint16_t* q, const void* cache, int e4m3, int num
     a.lse = lse;
     a.part_o = static_cast<float*>(scratch);
     a.part_ml = a.part_o + static_cast<size_t>(a.w.G) * a.RT * 2 * R * kLatDim;
-    a.need = reinterpret_cast<int32_t*>(a.part_ml + static_cast<size_t>(a.w.G) * a.RT * 2 * R * 2);
+    if (N > few_sequences(apart)) a.first = reinterpret_cast<long long*>(a.part_ml + static_cast<size_t>(a.w.G) * a.RT * 2 * R * 2);
     a.status = status;
     LatMaps maps;
     const CUtensorMapSwizzle swz = CU_TENSOR_MAP_SWIZZLE_128B;

@@ -208,3 +208,29 @@ def test_many_trees_of_several_row_tiles(N, dtype):
             else:
                 assert torch.isfinite(lse[n, j]).all()
     assert kda.kda_device_status() == kda.KDA_OK
+
+
+@pytest.mark.parametrize("dtype", [BF, E4], ids=["bf16", "e4m3"])
+@pytest.mark.parametrize("N,K,H", [(128, 2, 8), (129, 2, 8), (129, 4, 64), (300, 1, 16), (33, 8, 32), (32, 8, 32)])
+def test_many_sequences_are_joined_alike(N, K, H, dtype):
+    """Sequences enough to be counted by the attention itself, cut anywhere: what calls on a part of them give, chains and trees,
+    empty ones and long ones among them."""
+    lens = [0 if n % 11 == 5 else K + (n * 37) % 400 + (3000 if n % 50 == 7 else 0) for n in range(N)]
+    cache, table, _ = L.paged(lens, 32, dtype, seed=N)
+    cache, table, ld = cache.to(DEV), table.to(DEV), _i32(lens)
+    q = _rn(L.gen(N + 1), N, K, H, 576)
+    par = _i32([T.tree(K, n, 3, nodes=1 + n % K) for n in range(N)])
+    calls = [lambda s: kda.latent_decode(q[s].contiguous(), cache, dtype, table[s].contiguous(), ld[s].contiguous(), 0.07, want_lse=True),
+             lambda s: kda.latent_decode_tree(q[s].contiguous(), cache, dtype, table[s].contiguous(), ld[s].contiguous(),
+                                              par[s].contiguous(), 0.07, want_lse=True)]
+    for call in calls:
+        out, lse = call(slice(0, N))
+        for at in range(0, N, 25):
+            part = slice(at, at + 25)
+            o, l = call(part)
+            # (cut into other parts: the sums' order differs; outputs are rounded to bf16, half a step of 2^-8 a side)
+            assert float((out[part].float() - o.float()).abs().max()) <= 2.0 ** -7 * float(o.float().abs().max())
+            fin = torch.isfinite(l)
+            assert torch.equal(fin, torch.isfinite(lse[part]))
+            assert not fin.any() or float((lse[part] - l)[fin].abs().max()) < 1e-4
+    assert kda.kda_device_status() == kda.KDA_OK
