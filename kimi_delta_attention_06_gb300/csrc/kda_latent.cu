@@ -468,7 +468,7 @@ kda_latent_decode_kernel(const __grid_constant__ LatMaps maps, const LatArgs a)
                         if (r < R) s_set[r] = mine;
                     }
                 }
-                tc::named_sync(kBarSoft, Sh::kSoft);
+                if (!E4M3) tc::named_sync(kBarSoft, Sh::kSoft);  // (e4m3: the one after Q)
             }
             if constexpr (E4M3) {
                 // Q of the segment (the last S product of the segment before has run): a warp a row, the
