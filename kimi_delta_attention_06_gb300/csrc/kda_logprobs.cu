@@ -4,9 +4,10 @@
 //     entropy = lse - sum p z,   rank = place of t in the order (x descending, lowest index first),
 // and the first `top` tokens of that order.
 //
-// One pass over the row.  Each thread takes its exponents relative to a reference, its first step's maximum m (a later
-// one where an exponent would pass 2^60, which fp32 has the room for: a rescaling whenever one lane of a warp meets a
-// larger maximum took nearly half of the instructions), and keeps the sum of e^(z - z_m), the same sum weighted by the
+// One pass over the row.  Each thread takes its exponents relative to a reference, its warp's first step's maximum m (a
+// later one where a term would pass 2^6: a rescaling whenever one lane of a warp meets a larger maximum took nearly half of
+// the instructions, and terms up to 2^60, which fp32 has the room for, left the entropy of a sharp row up to 2^-18 off: it is
+// the difference of two numbers as large as the exponent), and keeps the sum of e^(z - z_m), the same sum weighted by the
 // exponents, and the count of elements ahead of the given token; they are joined by the usual rescaling.
 // Exponents are in powers of two, y = x c - r with c = scale * log2 e and the reference r = m c rounded: r is a number
 // like any other, so its rounding is no error.  Where that rounding is no longer small, from 2^20 on (rows of a type's
@@ -33,6 +34,7 @@ namespace kda {
 
 constexpr int kLogThreads = 256, kLogWarps = kLogThreads / 32, kLogGroups = kLogThreads / 2, kLogMaxTop = 32, kLogSteps = 24;
 constexpr int kLogFew = 64, kLogKeep = 1024, kLogHits = 1024, kLogMaxCluster = 8;
+constexpr float kLogAbove = 6.f;                 // powers of two that a term may be above its reference
 constexpr int kStatusToken = -1;                 // KDA_ERR_INVALID_ARG, recorded on the device
 using LogKey = unsigned long long;               // a value's order bits, then its index negated; 0: none
 
@@ -264,7 +266,7 @@ kda_logprobs_kernel(const LogArgs a)
         wide = log_wide(m, c);
         r = fabsf(m) < INFINITY && !wide ? __fmul_rn(m, c) : 0.f;
         low = fabsf(m) < INFINITY ? __fsub_rd(m, 160.f * inv) : -1e30f;
-        lim = fmaf(60.f, inv, m);
+        lim = fmaf(kLogAbove, inv, m);
     };
     constexpr int kStep = U * kLogThreads;       // chunks a step
     const int fold = ((chunks + kStep - 1) / kStep + kLogSteps - 1) / kLogSteps;         // steps that share a place of s_step
@@ -293,7 +295,8 @@ kda_logprobs_kernel(const LogArgs a)
             largest = b;
             at = k0;
         }
-        if (!(b <= lim)) raise(b);               // (a NaN is above everything, and stays)
+        const float top = k0 > 0 ? b : from_order(__reduce_max_sync(0xffffffffu, order_bits(b)));
+        if (!(top <= lim)) raise(top);           // (a NaN is above everything, and stays)
         if (!wide) {
             const float2 c2 = make_float2(c, c), r2 = make_float2(-r, -r);
 #pragma unroll

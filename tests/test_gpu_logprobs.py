@@ -246,3 +246,19 @@ def test_rows_alone_and_together():
         assert torch.equal(few[1], many[1][r0:r1]) and torch.equal(few[4], many[4][r0:r1])
         for i in (0, 2, 3):
             assert torch.allclose(few[i], many[i][r0:r1], rtol=2e-6, atol=2e-6)
+
+
+@pytest.mark.parametrize("dtype", [BF, F32])
+@pytest.mark.parametrize("V", [30000, 105187])
+def test_entropy_of_sharp_rows(dtype, V):
+    """The entropy is the difference of the log of a sum and a mean exponent.  Terms are at most 2^6 of their
+    reference, so both are below 8 where a few tokens hold the row, a rounding of either is at most 8 half steps, and a
+    dozen of those at random (the sums' last additions, the quotient, the logarithm) are 28: in nats, 28 ln 2 2^-24."""
+    g = torch.Generator().manual_seed(V)
+    x = (torch.randn(150, V, generator=g) * 3.2).to(dtype)
+    _, _, ent, _, _ = kda.token_logprobs(x.to(DEV), None, scale=1.9)
+    _ok()
+    lp = torch.log_softmax(x.double() * 1.9, -1)
+    ref = -(lp.exp() * lp).sum(-1)
+    err = float((ent.double().cpu() - ref).pow(2).mean().sqrt())
+    assert err <= 28 * math.log(2) * H24, f"{err:.2g}"
