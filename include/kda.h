@@ -382,6 +382,8 @@ int kda_decode_multi(const uint16_t* q, const uint16_t* k, const uint16_t* v,
  * factor and sums are fp32, in another order than kda_decode_multi's on the same path (a few 1e-7 of
  * the outputs' magnitudes off).  A state that holds NaN or infinities, or a magnitude above 3.4e38 / 2,
  * may make its outputs NaN; one that only a node's inputs bring reaches its descendants alone.
+ * Keys are taken over the product of the decays on their node's path where that is at least 2^-100
+ * in every channel: one above 2^27 there may make its descendants' outputs NaN.
  */
 int kda_decode_tree(const uint16_t* q, const uint16_t* k, const uint16_t* v,
                     const float* log_alpha, const uint16_t* beta,

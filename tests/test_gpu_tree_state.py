@@ -217,3 +217,39 @@ def test_every_channel_of_many_states(N, H, D, K):
             want = pool[:, :, at].permute(0, 2, 1, 3)
             assert ((o - want).abs() <= 2.0 ** -21 * want.abs()).all()
     _ok()
+
+
+@pytest.mark.parametrize("D,K", [(128, 8), (64, 15), (128, 16), (128, 25), (64, 32), (64, 40), (128, 64)])
+@pytest.mark.parametrize("what", ["q", "k", "v", "log_alpha", "beta"])
+@pytest.mark.parametrize("shift", [-2.0, 25.0], ids=["near", "far"])
+def test_one_bad_input_of_one_node(D, K, what, shift):
+    """One input of one node and head holds NaN or an infinity: its descendants in that head (of a query: itself) have no
+    finite row, everything else has the bits that it has without."""
+    x, pool = inputs(1, K, 3, D, CH, seed=K, shift=shift)          # (far: decays of a path below 2^-100)
+    row = T.tree(K, 2, 4)
+    node = 3
+    clean = run(x, pool, [row])
+    at = ["q", "k", "v", "log_alpha", "beta"].index(what)
+    for bad in (float("nan"), float("inf")) if what != "log_alpha" else (float("nan"),):
+        y = [t.clone() for t in x]
+        y[at][0, node, 1] = bad
+        got = run(y, pool, [row])
+        _ok()
+        for j in range(K):
+            hit = j == node if what == "q" else node in T.path(row, j)
+            for h in range(3):
+                if h == 1 and hit:
+                    assert not torch.isfinite(got[0, j, h]).any(), (j, h)
+                else:
+                    assert torch.equal(got[0, j, h], clean[0, j, h]), (j, h)
+
+
+def test_places_without_any_node():
+    """Trees of no node at all beside others: zeros."""
+    for K, D in ((3, 128), (20, 64), (50, 128)):
+        x, pool = inputs(3, K, 2, D, HD, seed=D)
+        rows = [[-2] * K, T.tree(K, 1, 3), [-7] * K]
+        got = run(x, pool, rows, decay=HD)
+        _ok()
+        assert not got[0].any() and not got[2].any()
+        check(got, x, pool, rows, [0, 1, 2])
