@@ -547,8 +547,7 @@ int kda_latent_gather(const void* cache, int cache_dtype, int num_pages, int pag
  * KDA_LATENT_MAX_TOKENS, else KDA_ERR_INVALID_ARG.  seq_lens[n] outside
  * [0, max_pages * page_size] counts as 0 and is reported; a page outside [0, num_pages) is
  * reported and leaves the sequence's outputs unspecified.  Scratch: partial results of at most
- * two work items per SM and, for many sequences, 8 bytes a sequence (a tree: and 64 rows),
- * stream-ordered from the library's pool as for kda_chunk_prefill.
+ * two work items per SM, stream-ordered from the library's pool as for kda_chunk_prefill.
  * Deterministic.
  */
 #define KDA_LATENT_MAX_ROWS 512

@@ -88,9 +88,6 @@ __device__ __forceinline__ int lat_need(const int32_t* parents, int K, int H, in
     const int last = hi ? 64 - __clz(hi) : 32 - __clz(lo);
     return (last * H + R - 1) / R;
 }
-// Up to so many sequences every warp of the joining kernel counts itself, while the attention runs; of more it takes what the
-// attention has counted (512 chains of 8 x 32 rows over 200 tokens, e4m3: 345 -> 247 us; 64 x 1 x 32 rows: 187 -> 190).
-constexpr int few_sequences(bool apart) { return apart ? 32 : 128; }
 __device__ __forceinline__ int lat_tiles(int len) { return (len + kTile - 1) / kTile; }
 __device__ __forceinline__ int lat_count(const LatWork& w, int len) { return len > 0 ? lat_tiles(len) + w.lead : 0; }   // with the lead
 // Runs in use for T tiles, and the bounds of run c.
@@ -181,6 +178,9 @@ struct SegWalk {
 // K = 4 94 -> 145.)
 struct LatMaps { CUtensorMap q, c, s; };
 
+// The sequence that a run begins and leaves to the next one (n; -1: none), the counted tiles before it and of all.
+struct LatCut { long long before, T; int n; };
+
 struct LatArgs {
     LatWork w;
     LatentCache ch;
@@ -192,7 +192,7 @@ struct LatArgs {
     uint16_t* out;
     float* lse;
     float *part_o, *part_ml;                     // partials: [run][row tile][2][R][512], [..][R][2]
-    long long* first;                            // [N + 1]: counted tiles before each sequence, of all; nullptr where they are few
+    LatCut* cuts;                                // [G]: of each run; nullptr where sequences are few
     int* status;
 };
 
@@ -763,6 +763,16 @@ kda_latent_decode_kernel(const __grid_constant__ LatMaps maps, const LatArgs a)
             tc::fence_before_sync();                             // the next segment's product overwrites O
             sw.first = false;
         }
+        // sequences that hold nothing, where the kernel that joins sees those alone that are cut
+        if (a.cuts && ok)
+            for (int n = run; n < a.w.N; n += a.w.G) {
+                if (lat_len(work, n) != 0) continue;
+                const int seq = seq_of(n), row0 = row_of(n), nrows = rows_of(n);
+                const long long at = static_cast<long long>(seq) * a.rows + row0;
+                for (int i = tid; i < nrows * (kLatDim / 8); i += Sh::kSoft) reinterpret_cast<uint4*>(a.out + at * kLatDim)[i] = make_uint4(0, 0, 0, 0);
+                if (a.lse && tid < nrows) a.lse[at + tid] = -INFINITY;
+                if (tid == 0 && row0 == 0 && lat_seq(a.w, seq) != a.w.seq_lens[seq]) set_status(a.status, kStatusIndex);
+            }
     } else if (warp == Sh::kMmaWarp) {
         // ---- both products; whichever has its inputs goes first ----
         // One thread runs it all: the tensor cores queue only about two products, so what stands between
@@ -865,6 +875,7 @@ kda_latent_decode_kernel(const __grid_constant__ LatMaps maps, const LatArgs a)
         // ---- TMA: C tiles in boxes of `box` whole rows (one page or a part of one); bf16: Q of each segment ----
         const int nbox = kTile / a.box;
         int g = 0, seg = 0;
+        LatCut cut{0, 0, -1};
         while (ok && sw.next(work)) {
             auto pages = [&](int t) {                           // lane i: first cache row of box i of tile t, -1 = past the end
                 const int tok = t * kTile + lane * a.box;
@@ -911,9 +922,9 @@ kda_latent_decode_kernel(const __grid_constant__ LatMaps maps, const LatArgs a)
                 }
                 at = next;
             }
-            if (a.first && lane == 0) a.first[sw.n] = sw.base;   // (for the kernel that joins; every part of a sequence says the same)
+            if (sw.t0 == 0 && !sw.whole()) cut = LatCut{sw.base, sw.total, sw.n};
         }
-        if (a.first && blockIdx.x == 0 && lane == 0) a.first[a.w.N] = sw.total;
+        if (a.cuts && rt == 0 && lane == 0) a.cuts[run] = ok ? cut : LatCut{0, 0, -1};      // for the kernel that joins
         // copies in flight land before the CTA's shared memory is given back
         if (!ok) {
             if (seg > 0) tc::mbar_wait_bounded(q_full, (seg - 1) & 1, kWaitLimitNs);
@@ -1020,35 +1031,37 @@ kda_latent_combine_kernel(const LatArgs a, int Q, int NG)
 
 // The same for many rows of few partials: a warp a row, 16 channels a lane, no block-wide step.
 // (Four blocks an SM are enough: for more, the compiler spills into 48 registers.)
-template <int R>
+// MANY: of the runs' cut sequences alone.
+template <int R, bool MANY>
 __global__ void __launch_bounds__(128, 4)
 kda_latent_combine_rows_kernel(const LatArgs a)
 {
     const int lane = threadIdx.x & 31;
-    const long long at = static_cast<long long>(blockIdx.x) * 4 + (threadIdx.x >> 5);     // row n * rows + row
+    const long long unit = static_cast<long long>(blockIdx.x) * 4 + (threadIdx.x >> 5);
     const int seqs = a.w.N / a.w.each;
-    const int n = static_cast<int>(min(at, static_cast<long long>(seqs) * a.rows - 1) / a.rows);
-    const int row = static_cast<int>(at - static_cast<long long>(n) * a.rows);
-    const int tile = a.w.each > 1 ? min(row, a.rows - 1) / R : 0;            // (of those that are sequences of their own)
-    LatCount c{0, 0, 0, 0};
-    if (!a.first) {
-        c = lat_counted<R>(a, n, tile, lane);
-    } else {
-        c.len = lat_seq(a.w, n);
-        c.need = lat_needed<R>(a, n, lane);
-    }
-    if (lane == 0 && row == 0 && a.w.seq_lens[n] != c.len) set_status(a.status, kStatusIndex);   // out of range: counted as 0
-    const int tiles = tile < c.need ? lat_tiles(c.len) : 0;
-    if (a.first) {                                               // (of many: as the attention has counted them)
+    int n, row, tiles;
+    long long T, before;
+    if constexpr (MANY) {                                        // unit: row of a run's cut sequence
+        const int per = a.w.each > 1 ? R : a.rows, run = static_cast<int>(unit / per);
         asm volatile("griddepcontrol.wait;" ::: "memory");
-        if (tiles > 0) {
-            c.T = a.first[a.w.N];
-            c.before = a.first[tile * seqs + n];
-            // (a wait that ran out there has left them anything: nothing is joined then)
-            if (c.before < 0 || c.before + a.w.lead + tiles > c.T || c.T >> 44) return;
-        }
+        const LatCut cut = run < a.w.G ? a.cuts[run] : LatCut{0, 0, -1};
+        if (cut.n < 0) return;
+        n = a.w.each > 1 ? cut.n % seqs : cut.n;
+        row = static_cast<int>(unit - static_cast<long long>(run) * per) + (a.w.each > 1 ? cut.n / seqs * R : 0);
+        tiles = lat_tiles(lat_seq(a.w, n));
+        T = cut.T;
+        before = cut.before;
+    } else {                                                     // unit: n * rows + row
+        n = static_cast<int>(min(unit, static_cast<long long>(seqs) * a.rows - 1) / a.rows);
+        row = static_cast<int>(unit - static_cast<long long>(n) * a.rows);
+        const int tile = a.w.each > 1 ? min(row, a.rows - 1) / R : 0;        // (of those that are sequences of their own)
+        const LatCount c = lat_counted<R>(a, n, tile, lane);
+        if (lane == 0 && row == 0 && a.w.seq_lens[n] != c.len) set_status(a.status, kStatusIndex);   // out of range: counted as 0
+        tiles = tile < c.need ? lat_tiles(c.len) : 0;
+        T = c.T;
+        before = c.before;
     }
-    const long long T = c.T, before = c.before;
+    const long long at = static_cast<long long>(n) * a.rows + row;
     int c0 = 0, parts = 1, late = 0;
     if (tiles > 0) {
         const long long runs = lat_runs(T, a.w.G);
@@ -1056,7 +1069,7 @@ kda_latent_combine_rows_kernel(const LatArgs a)
         parts = static_cast<int>(run_of(T, runs, before + a.w.lead + tiles - 1)) - c0 + 1;
         late = run_begin(T, runs, c0) < before ? 1 : 0;
     }
-    asm volatile("griddepcontrol.wait;" ::: "memory");          // every block: this grid ends after the one before it
+    if (!MANY) asm volatile("griddepcontrol.wait;" ::: "memory");            // every block: this grid ends after the one before it
     if (row >= a.rows) return;                                   // (past the last row)
     uint2* out = reinterpret_cast<uint2*>(a.out + at * kLatDim) + lane;
     if (tiles == 0) {
@@ -1175,11 +1188,13 @@ int launch_decode_shape(const LatMaps& maps, const LatArgs& a, cudaStream_t stre
     // rows are too few for a block on each SM (20 tokens of 48 rows each, 192 rows: 16.5 us with 4, 15.3
     // with 1; 24 rows over 33851 tokens: 19.8 with 4, 27.4 with 1 and a pass each for maxima, sums and O)
     const int seqs = a.w.N / a.w.each, about = a.w.G / a.w.N + 1;
-    const bool by_warp = about <= 16 || a.first;
+    const bool by_warp = about <= 16 || a.cuts;
+    // (of the cut sequences, where those are what is joined: G at most)
+    const long long warps = a.cuts ? static_cast<long long>(a.w.G) * (a.w.each > 1 ? R : a.rows) : static_cast<long long>(seqs) * a.rows;
     const int Q = static_cast<long long>(seqs) * a.rows < sm_count() ? 4 : 1;
     int NG = 1;
     while (NG < 4 * Q && NG * 8 < about) NG *= 2;
-    cfg.gridDim = dim3(by_warp ? (static_cast<unsigned>(seqs) * a.rows + 3) / 4 : static_cast<unsigned>(seqs) * a.rows * Q);
+    cfg.gridDim = dim3(by_warp ? static_cast<unsigned>((warps + 3) / 4) : static_cast<unsigned>(seqs) * a.rows * Q);
     cfg.blockDim = dim3(by_warp ? 128 : 128 / Q * NG);
     cfg.stream = stream;
     cudaLaunchAttribute at[1];
@@ -1187,7 +1202,8 @@ int launch_decode_shape(const LatMaps& maps, const LatArgs& a, cudaStream_t stre
     at[0].val.programmaticStreamSerializationAllowed = 1;
     cfg.attrs = at;
     cfg.numAttrs = 1;
-    if (by_warp) return cudaLaunchKernelEx(&cfg, kda_latent_combine_rows_kernel<R>, a) == cudaSuccess ? 0 : -3;
+    if (a.cuts) return cudaLaunchKernelEx(&cfg, kda_latent_combine_rows_kernel<R, true>, a) == cudaSuccess ? 0 : -3;
+    if (by_warp) return cudaLaunchKernelEx(&cfg, kda_latent_combine_rows_kernel<R, false>, a) == cudaSuccess ? 0 : -3;
     return cudaLaunchKernelEx(&cfg, kda_latent_combine_kernel<R>, a, Q, NG) == cudaSuccess ? 0 : -3;
 }
 
@@ -1213,11 +1229,17 @@ int latent_decode_runs(int rows) {
 // some of the second are left out, what the first have read has left L2 (16 trees of 2 to 4 nodes x 32 heads over 341k
 // tokens: apart 141 us, together 128; e4m3, apart: 122, chains of 4, all of whose rows are there: 127).
 static bool tree_split(int rows, bool tree, int e4m3) { return tree && rows > (e4m3 ? 64 : 128); }
+// Few sequences every warp of the joining kernel counts itself, while the attention runs; of many sequences and rows it is told
+// which are cut, and looks at those alone (512 chains of 8 x 32 rows over 200 tokens, e4m3: 345 -> 216 us; 64 of 16 x 32 over
+// 2000: 211 -> 204; but 64 of 1 x 32 over 1k to 64k, bf16: 188.3 -> 189.0).
+static bool join_cuts(int N, int rows, bool apart) {
+    return N > 32 && (apart || N > 128 || static_cast<long long>(N) * rows > 8192);
+}
 size_t latent_decode_scratch(int rows, int N, bool tree, int e4m3) {
     const size_t R = rows_per_cta(rows), RT = (rows + R - 1) / R;
     const bool apart = tree_split(rows, tree, e4m3);
     const size_t runs = apart ? latent_decode_runs(64) : latent_decode_runs(rows) * RT;
-    return runs * 2 * R * (kLatDim + 2) * sizeof(float) + (N > few_sequences(apart) ? (static_cast<size_t>(N) * (apart ? RT : 1) + 1) * sizeof(long long) : 0);
+    return runs * 2 * R * (kLatDim + 2) * sizeof(float) + (join_cuts(N, rows, apart) ? latent_decode_runs(apart ? 64 : rows) * sizeof(LatCut) : 0);
 }
 
 int launch_latent_decode(const uint16_t* q, const void* cache, int e4m3, int num_pages, int page_size,
@@ -1245,7 +1267,7 @@ int launch_latent_decode(const uint16_t* q, const void* cache, int e4m3, int num
     a.lse = lse;
     a.part_o = static_cast<float*>(scratch);
     a.part_ml = a.part_o + static_cast<size_t>(a.w.G) * a.RT * 2 * R * kLatDim;
-    if (N > few_sequences(apart)) a.first = reinterpret_cast<long long*>(a.part_ml + static_cast<size_t>(a.w.G) * a.RT * 2 * R * 2);
+    if (join_cuts(N, rows, apart)) a.cuts = reinterpret_cast<LatCut*>(a.part_ml + static_cast<size_t>(a.w.G) * a.RT * 2 * R * 2);
     a.status = status;
     LatMaps maps;
     const CUtensorMapSwizzle swz = CU_TENSOR_MAP_SWIZZLE_128B;

@@ -234,3 +234,27 @@ def test_many_sequences_are_joined_alike(N, K, H, dtype):
             assert torch.equal(fin, torch.isfinite(lse[part]))
             assert not fin.any() or float((lse[part] - l)[fin].abs().max()) < 1e-4
     assert kda.kda_device_status() == kda.KDA_OK
+
+
+@pytest.mark.parametrize("tree", [False, True], ids=["chain", "tree"])
+def test_bad_lengths_among_many_sequences(tree):
+    """Lengths that are none count as 0 and are reported, where the attention itself writes what is empty."""
+    N, K, H = 200, 3, 32
+    lens = [K + n % 90 for n in range(N)]
+    cache, table, _ = L.paged(lens, 16, BF, seed=3)
+    cache, table = cache.to(DEV), table.to(DEV)
+    q, par = _rn(L.gen(4), N, K, H, 576), _i32([T.tree(K, n, 2) for n in range(N)])
+    call = lambda ld: (kda.latent_decode_tree(q, cache, BF, table, ld, par, 0.07, want_lse=True) if tree else
+                       kda.latent_decode(q, cache, BF, table, ld, 0.07, want_lse=True))
+    zero = list(lens)
+    for n in (0, 7, 131, N - 1):
+        zero[n] = 0
+    want = call(_i32(zero))
+    assert kda.kda_device_status() == kda.KDA_OK
+    bad = list(zero)
+    bad[0], bad[7], bad[N - 1] = -5, table.shape[1] * 16 + 1, 2 ** 31 - 1
+    got = call(_i32(bad))
+    assert kda.kda_device_status() == kda.KDA_ERR_INVALID_ARG
+    assert all(torch.equal(a, b) for a, b in zip(got, want))
+    for n in (0, 7, 131, N - 1):
+        assert not want[0][n].any() and (want[1][n] == float("-inf")).all()
