@@ -565,7 +565,10 @@ def _latent_decode(q, cache, cache_dtype, block_table, seq_lens, N, K, H, sm_sca
 
 
 def _rope_heads(t, T: int, H: int, what: str):
-    """(address, token and head stride) of the position parts [T, H, 64] of heads."""
+    """(address, token and head stride) of the position parts [T, H, 64] of heads.  Whole heads [T, H, 192] or [T, H, 576]
+    are refused: their first 64 values, which would be turned, are not their position parts."""
+    if t.dim() == 3 and t.shape[2] > KDA_LATENT_ROPE:
+        _short(what, t, f"[{T}, {H}, {KDA_LATENT_ROPE}] (the position parts alone, a slice of whole heads)")
     return _rows3(t, _BF16, T, H, KDA_LATENT_ROPE, KDA_LATENT_ROPE, what)
 
 
