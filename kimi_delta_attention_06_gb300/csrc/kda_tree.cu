@@ -16,14 +16,16 @@
 // lanes are the state's columns, a thread's a column), as three tf32 products of the operands' leading 11 bits and what is left of them: 22 bits, an fp32
 // product but for 2^-21.  The tensor cores round sums towards zero: the two small products have an accumulator of their own, or
 // go first, and W (V - P) is not added to Q there (errors of 64 x 8 heads of 64 x 64, 48 nodes, against 64 bits:
-// 1.4e-6 -> 2.5e-7).  So do L and N, as products of the decayed rows with the keys over their decays (CTAs in which a
-// decay leaves 2^-100 .. 2^100 walk their paths instead), and W (V - P), with V - P in TMEM in S_0^T's place (a NaN
-// or an infinity in it enters as 0, and is put back for the nodes whose paths hold it: 0 * NaN is none).
+// 1.4e-6 -> 2.5e-7).  So do L and N, as products of the decayed rows with the keys over their decays (nodes on whose paths
+// a decay leaves 2^-100 .. 2^100 walk them instead: a node's arithmetic follows from its own path alone), and W (V - P), with
+// V - P in TMEM in S_0^T's place (a NaN or an infinity in it enters as 0, and is put back for the nodes whose paths hold it:
+// 0 * NaN is none).
 //
-// Measured in a graph: 256 sequences x 32 heads of 128 x 128, trees of 16 nodes: 189 us for 0.70 GB that cannot be done without
-// (103 us of HBM); 64 x 8 of 64 x 64, 48 nodes: 48 us; one sequence, 32 heads, 8 nodes: 6.5 us.  Bound by a turn's chain (decays,
+// Measured in a graph: 256 sequences x 32 heads of 128 x 128, trees of 16 nodes: 186 us for 0.70 GB that cannot be done without
+// (103 us of HBM); 64 x 8 of 64 x 64, 48 nodes: 46 us; one sequence, 32 heads, 8 nodes: 6.5 us.  Bound by a turn's chain (decays,
 // rows, product, V - P, product, outputs; 11 to 12 thousand clocks at 16 nodes) with two CTAs an SM to fill it, one from 17
-// nodes on, where TMEM and shared memory hold no more.  Decays outside the range: 283 for 196 us at 16 nodes, 111 for 49 at 48.
+// nodes on, where TMEM and shared memory hold no more.  Decays outside the range from
+// the fourth node on, or everywhere: 262 and 292 us at 16 nodes, 125 and 116 at 48.
 #include "common.cuh"
 #include "tc.cuh"
 #include "tree.cuh"
@@ -87,7 +89,7 @@ struct TreeShape {
     static constexpr int kRounds = KP == 8 ? 3 : KP == 16 ? 4 : KP == 32 ? 5 : 6;      // of the decays' products, doubling their reach
     static constexpr uint32_t oSet = oV + kNodes * D * 2u, oBeta = oSet + 2 * kNodes * kBit, oUp = oBeta + 2 * kNodes * 2u;
     static constexpr uint32_t oFar = oUp + 2 * kNodes, oDesc = oFar + 2 * kRounds * kNodes, oBar = oDesc + 2 * kNodes * kBit;
-    static constexpr uint32_t kBytes = oBar + 256u;
+    static constexpr uint32_t kBytes = oBar + 288u;
     // W by whole rows of L (else along the paths), where a row has so many lanes, and a lane so many quads of places
     static constexpr bool kDense = KP > 16;
     static constexpr int kWLanes = KP / 4 < 256 / kNodes ? KP / 4 : 256 / kNodes, kQuads = KP / 4 / kWLanes;
@@ -178,8 +180,8 @@ kda_tree_kernel(const TreeArgs a)
     // a phase waits for the side that waits on it before it can complete the next)
     uint64_t *b_last = bars + 22, *b_tree = bars + 14, *b_done = bars + 24;
     uint32_t* s_tmem = reinterpret_cast<uint32_t*>(bars + 23);
-    int* s_walk = reinterpret_cast<int*>(bars + 26);                    // [2]: of even and odd turns
-    Set* s_bad = reinterpret_cast<Set*>(bars + 27);                     // [2][item]: places whose row of L holds no number
+    Set* s_bad = reinterpret_cast<Set*>(bars + 26);                     // [2][item]: places whose row of L holds no number, ..
+    Set* s_far = s_bad + 2 * kItems;                                    // .. whose decays leave the products' range
 
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     if (tid == 0) {
@@ -203,8 +205,7 @@ kda_tree_kernel(const TreeArgs a)
         tc::mbar_init(b_w, 1);
         tc::mbar_init(b_last, 1);
         tc::mbar_fence_init();
-        s_walk[0] = s_walk[1] = 0;
-        for (int i = 0; i < 2 * kItems; ++i) s_bad[i] = 0;
+        for (int i = 0; i < 2 * kItems; ++i) s_bad[i] = s_far[i] = 0;
     }
     if (warp == 8) tc::tmem_alloc(s_tmem, Sh::kCols);
     tc::fence_before_sync();
@@ -352,27 +353,25 @@ kda_tree_kernel(const TreeArgs a)
                     ok = tc::mbar_wait_bounded(b_rows, run & 1, kWaitLimitNs);
                     if (!ok) break;
                     tc::fence_after_sync();
-                    const bool walk = *reinterpret_cast<volatile int*>(s_walk + (turn & 1)) != 0;
                     auto side = [&] {
                         // the keys over their decays (64 rows from an item's first) times the item's rows: L and N, transposed
-                        if (!walk)
 #pragma unroll 1
-                            for (int it = 0; it < kItems; ++it) {
-                                const uint32_t d = tm + Sh::kL + chunk * Sh::kRows + it * Sh::kItem;
-                                const uint32_t sa = tree_desc(sm0 + Sh::oSide + it * Sh::kSideItem * 128u);
-                                const uint32_t sb = tree_desc(sm0 + Sh::oRows + it * Sh::kItem * 128u);
+                        for (int it = 0; it < kItems; ++it) {
+                            const uint32_t d = tm + Sh::kL + chunk * Sh::kRows + it * Sh::kItem;
+                            const uint32_t sa = tree_desc(sm0 + Sh::oSide + it * Sh::kSideItem * 128u);
+                            const uint32_t sb = tree_desc(sm0 + Sh::oRows + it * Sh::kItem * 128u);
 #pragma unroll
-                                for (uint32_t x = 0; x < (Sh::kStack ? 1u : 2u) * kSlabs * 4u; ++x) {
-                                    const uint32_t k = x % (kSlabs * 4u);
-                                    const uint32_t pa = sa + (k >> 2) * (Sh::kSideRows * 8u) + (k & 3) * 2u, pb = sb + (k >> 2) * (Sh::kRows * 8u) + (k & 3) * 2u;
-                                    if (Sh::kStack || x >= kSlabs * 4u) {
-                                        tree_mma_ss(d, pa, pb, id_side, x > 0 ? 1u : 0u);
-                                    } else {
-                                        tree_mma_ss(d, pa, pb + Sh::kRest / 16u, id_side, x > 0 ? 1u : 0u);
-                                        tree_mma_ss(d, pa + Sh::kSide / 16u, pb, id_side, 1u);
-                                    }
+                            for (uint32_t x = 0; x < (Sh::kStack ? 1u : 2u) * kSlabs * 4u; ++x) {
+                                const uint32_t k = x % (kSlabs * 4u);
+                                const uint32_t pa = sa + (k >> 2) * (Sh::kSideRows * 8u) + (k & 3) * 2u, pb = sb + (k >> 2) * (Sh::kRows * 8u) + (k & 3) * 2u;
+                                if (Sh::kStack || x >= kSlabs * 4u) {
+                                    tree_mma_ss(d, pa, pb, id_side, x > 0 ? 1u : 0u);
+                                } else {
+                                    tree_mma_ss(d, pa, pb + Sh::kRest / 16u, id_side, x > 0 ? 1u : 0u);
+                                    tree_mma_ss(d, pa + Sh::kSide / 16u, pb, id_side, 1u);
                                 }
                             }
+                        }
                         tc::mma_commit(b_side);
                     };
                     if (!Sh::kApart) {
@@ -572,18 +571,24 @@ kda_tree_kernel(const TreeArgs a)
                     for (int z = 0; z < kPlaces; ++z) p[z][c] *= up[z] >= 0 ? y[z] : 1.f;
                 }
             }
-            // (a key over a decay outside this range would overflow: such turns walk their paths)
-            bool far = false;
+            auto add = [&](Set* to, Set places) {
+                if constexpr (KP > 32) atomicOr(reinterpret_cast<unsigned long long*>(to), static_cast<unsigned long long>(places));
+                else atomicOr(to, places);
+            };
+            // (a key over a decay outside this range would overflow: nodes with such a one on their paths walk them, and they alone.
+            // NaN and infinities do not count)
             Set mine[kPlaces];
 #pragma unroll
             for (int z = 0; z < kPlaces; ++z) {
                 mine[z] = s_set[part * KP + place + 32 * z];
-                if (mine[z] != 0)
+                float least = INFINITY, most = 0.f;
 #pragma unroll
-                    for (int c = 0; c < CH; ++c) far |= p[z][c] < 0x1p-100f || (p[z][c] > 0x1p100f && p[z][c] < INFINITY);
+                for (int c = 0; c < CH; ++c) {
+                    least = fminf(least, p[z][c]);
+                    most = fmaxf(most, p[z][c] < INFINITY ? p[z][c] : 0.f);
+                }
+                if ((least < 0x1p-100f || most > 0x1p100f) && mine[z] != 0) add(s_far + odd * kItems + part, kOne << (place + 32 * z));
             }
-            if (far) s_walk[odd] = 1;
-            bool walk = false;
             // the next turn's inputs, into what is done with: before the other slabs, or behind them where registers are short
             // (16 nodes: 196 us before them, 189 behind; 32: 445, 475)
             auto ahead = [&](int chunk) {
@@ -630,87 +635,89 @@ kda_tree_kernel(const TreeArgs a)
                     slab += kSlabs;
                 }
                 if (Sh::kCtas > 1) ahead(chunk);
-                tc::named_sync(kTreeAll, 256);                          // (of all threads: whether to walk)
-                walk = *reinterpret_cast<volatile int*>(s_walk + odd) != 0;
-                if (tid == 0) {
-                    s_walk[1 - odd] = 0;
-                    for (int it = 0; it < kItems; ++it) s_bad[(1 - odd) * kItems + it] = 0;
-                }
+                tc::named_sync(kTreeAll, 256);                          // (of all threads: what is far)
+                if (tid == 0)
+                    for (int it = 0; it < kItems; ++it) s_bad[(1 - odd) * kItems + it] = s_far[(1 - odd) * kItems + it] = 0;
+                bool walk = false;
+#pragma unroll
+                for (int it = 0; it < kItems; ++it) walk |= s_far[odd * kItems + it] != 0;
                 // 4. L and N of the chunk's nodes.  Dense: beta L, and zeros where the path does not lead (L: nor to the node itself);
                 // what is no number in L enters as 0, and the node is marked: its own and its descendants' outputs are none
-                auto mark = [&](int it, Set places) {
-                    if constexpr (KP > 32) atomicOr(reinterpret_cast<unsigned long long*>(s_bad + odd * kItems + it), static_cast<unsigned long long>(places));
-                    else atomicOr(s_bad + odd * kItems + it, places);
-                };
-                if (!walk) {
-                    // row x of the product is lane x % 16 of warp x / 16
-                    constexpr int kOwn = Sh::kStack ? 8 : 16;           // places a warp (stacked: lanes 8 .. 15 their second terms)
-                    if (const int b = kOwn * (warp & 3) + lane; b - lane < KP && (Sh::kDense || group == 0)) {     // dense: one group L, the other N
-                        ok = tc::mbar_wait_bounded(b_side, run & 1, kWaitLimitNs) && ok;
-                        ok = __all_sync(0xffffffffu, ok);
-                        tc::fence_after_sync();
+                auto walks = [&](int it, int i) { return (s_set[it * KP + i] & s_far[odd * kItems + it]) != 0; };
+                // row x of the product is lane x % 16 of warp x / 16
+                constexpr int kOwn = Sh::kStack ? 8 : 16;           // places a warp (stacked: lanes 8 .. 15 their second terms)
+                if (const int b = kOwn * (warp & 3) + lane; b - lane < KP && (Sh::kDense || group == 0)) {     // dense: one group L, the other N
+                    ok = tc::mbar_wait_bounded(b_side, run & 1, kWaitLimitNs) && ok;
+                    ok = __all_sync(0xffffffffu, ok);
+                    tc::fence_after_sync();
 #pragma unroll 1
-                        for (int it = 0; it < kItems; ++it) {
-                            const Set below = Sh::kDense && b < KP ? s_descs[(odd * kItems + it) * KP + b] : 0;
-                            float* to = (group == 0 ? s_m : s_n) + (it * KP + chunk * KC) * KP + b;
-                            static_assert(Sh::kDense || kChunks == 1);
-                            float any = 0.f;                            // NaN where one is none
+                    for (int it = 0; it < kItems; ++it) {
+                        // (nothing of it is wanted where all nodes walk)
+                        if (Sh::kDense && walk && !__any_sync(0xffffffffu, lane < KC && s_set[it * KP + chunk * KC + lane] != 0 && !walks(it, chunk * KC + lane))) continue;
+                        const Set below = Sh::kDense && b < KP ? s_descs[(odd * kItems + it) * KP + b] : 0;
+                        float* to = (group == 0 ? s_m : s_n) + (it * KP + chunk * KC) * KP + b;
+                        static_assert(Sh::kDense || kChunks == 1);
+                        float any = 0.f;                            // NaN where one is none
 #pragma unroll
-                            for (int c0 = 0; c0 < (Sh::kDense ? 1 : 2) * KC; c0 += 8) {
-                                float x[8];
-                                const uint32_t from = lane_tm + Sh::kL + chunk * Sh::kRows + it * Sh::kItem + group * KC + c0;
-                                tree_tmem_ld8(from, x);
-                                if constexpr (Sh::kStack) {
-                                    float y[8];
-                                    tree_tmem_ld8(from + 2 * KC, y);
+                        for (int c0 = 0; c0 < (Sh::kDense ? 1 : 2) * KC; c0 += 8) {
+                            float x[8];
+                            const uint32_t from = lane_tm + Sh::kL + chunk * Sh::kRows + it * Sh::kItem + group * KC + c0;
+                            tree_tmem_ld8(from, x);
+                            if constexpr (Sh::kStack) {
+                                float y[8];
+                                tree_tmem_ld8(from + 2 * KC, y);
 #pragma unroll
-                                    for (int r = 0; r < 8; ++r) x[r] += __shfl_xor_sync(0xffffffffu, x[r], 8) + y[r];
-                                }
-                                const int first = chunk * KC + c0;
-                                if (!Sh::kDense) {
-                                    if (c0 == KC) to = s_n + (it * KP - KC) * KP + b;
-                                } else if (group == 0) {
-                                    const uint4 beta = *reinterpret_cast<const uint4*>(s_beta + it * KP + first);
-                                    const uint32_t beta2[4] = {beta.x, beta.y, beta.z, beta.w};
-#pragma unroll
-                                    for (int r = 0; r < 8; r += 2) {
-                                        const float2 f = bf16x2_bits_to_f32(beta2[r / 2]);
-                                        x[r] = (below >> (first + r) & 1) && b != first + r ? x[r] * f.x : 0.f;
-                                        x[r + 1] = (below >> (first + r + 1) & 1) && b != first + r + 1 ? x[r + 1] * f.y : 0.f;
-                                        any = fmaf(x[r + 1], 0.f, fmaf(x[r], 0.f, any));
-                                    }
-                                } else {
-#pragma unroll
-                                    for (int r = 0; r < 8; ++r) x[r] = below >> (first + r) & 1 ? x[r] : 0.f;
-                                }
-                                if (lane < kOwn && b < KP) {
-#pragma unroll
-                                    for (int r = 0; r < 8; ++r) to[(c0 + r) * KP] = x[r];
-                                }
+                                for (int r = 0; r < 8; ++r) x[r] += __shfl_xor_sync(0xffffffffu, x[r], 8) + y[r];
                             }
-                            if (any != 0.f && lane < kOwn && b < KP) {
-#pragma unroll 1
-                                for (int r = 0; r < KC; ++r)
-                                    if (!(fabsf(to[r * KP]) < INFINITY)) {
-                                        to[r * KP] = 0.f;
-                                        mark(it, kOne << (chunk * KC + r));
-                                    }
+                            const int first = chunk * KC + c0;
+                            if (!Sh::kDense) {
+                                if (c0 == KC) to = s_n + (it * KP - KC) * KP + b;
+                            } else if (group == 0) {
+                                const uint4 beta = *reinterpret_cast<const uint4*>(s_beta + it * KP + first);
+                                const uint32_t beta2[4] = {beta.x, beta.y, beta.z, beta.w};
+#pragma unroll
+                                for (int r = 0; r < 8; r += 2) {
+                                    const float2 f = bf16x2_bits_to_f32(beta2[r / 2]);
+                                    x[r] = (below >> (first + r) & 1) && b != first + r ? x[r] * f.x : 0.f;
+                                    x[r + 1] = (below >> (first + r + 1) & 1) && b != first + r + 1 ? x[r + 1] * f.y : 0.f;
+                                    any = fmaf(x[r + 1], 0.f, fmaf(x[r], 0.f, any));
+                                }
+                            } else {
+#pragma unroll
+                                for (int r = 0; r < 8; ++r) x[r] = below >> (first + r) & 1 ? x[r] : 0.f;
+                            }
+                            if (lane < kOwn && b < KP) {
+#pragma unroll
+                                for (int r = 0; r < 8; ++r) to[(c0 + r) * KP] = x[r];
                             }
                         }
-                        tc::fence_before_sync();
+                        if (any != 0.f && lane < kOwn && b < KP) {
+#pragma unroll 1
+                            for (int r = 0; r < KC; ++r)
+                                if (!walks(it, chunk * KC + r) && !(fabsf(to[r * KP]) < INFINITY)) {
+                                    to[r * KP] = 0.f;
+                                    add(s_bad + odd * kItems + it, kOne << (chunk * KC + r));
+                                }
+                        }
                     }
-                } else {
-                    // half a warp a node, up its path; lane l of the 16: channels 4 l .. + 3 of each 64
+                    tc::fence_before_sync();
+                }
+                if (walk) {
+                    // those of the nodes below a far decay again: half a warp a node, up its path; lane l of the 16: channels
+                    // 4 l .. + 3 of each 64
                     const int hl = lane & 15;
+                    tc::named_sync(kTreeAll, 256);
 #pragma unroll 1
                     for (int f = 2 * warp + (lane >> 4); f < kItems * KC; f += 16) {
                         const int it = f / KC, i = chunk * KC + f % KC, e = it * KP + i;
-                        Set left = s_set[e];
+                        Set left = walks(it, i) ? s_set[e] : 0;
                         if (Sh::kDense) {
+                            if (left || s_set[e] == 0)
 #pragma unroll
-                            for (int b = hl; b < KP; b += 16) s_m[e * KP + b] = s_n[e * KP + b] = 0.f;
+                                for (int b = hl; b < KP; b += 16) s_m[e * KP + b] = s_n[e * KP + b] = 0.f;
                             __syncwarp();
                         }
+                        if (Sh::kDense && !__any_sync(0xffffffffu, left != 0)) continue;
                         float key[4 * G], query[4 * G], p[4 * G];
 #pragma unroll
                         for (int c = 0; c < 4 * G; ++c) {
@@ -741,7 +748,7 @@ kda_tree_kernel(const TreeArgs a)
                             if (hl == 0 && on) {
                                 if (Sh::kDense) {
                                     m *= b < i ? bf16_bits_to_f32(s_beta[e]) : 0.f;
-                                    if (!(fabsf(m) < INFINITY) && b < i) mark(it, kOne << i);
+                                    if (!(fabsf(m) < INFINITY) && b < i) add(s_bad + odd * kItems + it, kOne << i);
                                     m = fabsf(m) < INFINITY ? m : 0.f;
                                 }
                                 s_m[e * KP + b] = m;
