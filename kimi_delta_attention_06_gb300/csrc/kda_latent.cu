@@ -72,14 +72,19 @@ struct LatWork {
 // Up to so many sequences are looked at for it (shared memory; of more, all row tiles are worked through).
 template <bool E4M3> constexpr int kMaxNeed = E4M3 ? 512 : 128;
 
+// (What only trees have is a constant for chains: with it looked up, one sequence of 145408 x 32 heads took 43.4 us for 42.2,
+// 64 of 1k to 64k 189.2 for 187.2, 3 of up to 200 x 4 heads 8.5 for 8.1.)
+template <bool TREE> __device__ __forceinline__ int lat_each(const LatWork& w) { return TREE ? w.each : 1; }
+template <bool TREE>
 __device__ __forceinline__ int lat_seq(const LatWork& w, int n) {
     const int len = w.seq_lens[n];
-    return len < w.least || len > w.max_len ? 0 : len;
+    return len < (TREE ? w.least : 0) || len > w.max_len ? 0 : len;
 }
+template <bool TREE>
 __device__ __forceinline__ int lat_len(const LatWork& w, int n) {
-    if (w.each <= 1) return lat_seq(w, n);
+    if (lat_each<TREE>(w) <= 1) return lat_seq<TREE>(w, n);
     const int seqs = w.N / w.each, tile = n / seqs, s = n - tile * seqs;
-    return !w.need ? lat_seq(w, s) : tile < w.need[s] ? w.lens[s] : 0;
+    return !w.need ? lat_seq<TREE>(w, s) : tile < w.need[s] ? w.lens[s] : 0;
 }
 // Row tiles that a tree needs, as one warp finds it: R rows each, H of a node, up to its last place with a node.
 __device__ __forceinline__ int lat_need(const int32_t* parents, int K, int H, int R, int lane) {
@@ -103,6 +108,7 @@ __device__ __forceinline__ long long run_begin(long long T, long long runs, long
 __device__ __forceinline__ long long run_of(long long T, long long runs, long long t) { return run_div((t + 1) * runs - 1, T); }
 
 // Walks the segments of one run; every warp keeps its own copy (init is warp-collective).
+template <bool TREE>
 struct SegWalk {
     long long pos, end, base;                   // next tile, end of the run, first (counted) tile of sequence n
     int n, len, count;                          // count: its tiles and its lead
@@ -112,9 +118,9 @@ struct SegWalk {
 
     __device__ __forceinline__ void init(const LatWork& w, int c) {
         const int lane = threadIdx.x & 31;
-        const int len0 = lane < w.N ? lat_len(w, lane) : 0;     // the first 32 stay in registers
+        const int len0 = lane < w.N ? lat_len<TREE>(w, lane) : 0;     // the first 32 stay in registers
         long long T = lat_count(w, len0);
-        for (int i = lane + 32; i < w.N; i += 32) T += lat_count(w, lat_len(w, i));
+        for (int i = lane + 32; i < w.N; i += 32) T += lat_count(w, lat_len<TREE>(w, i));
         if (w.N <= 32 && __reduce_max_sync(0xffffffffu, static_cast<unsigned>(T)) < (1u << 26)) {
             T = __reduce_add_sync(0xffffffffu, static_cast<unsigned>(T));
         } else {
@@ -131,7 +137,7 @@ struct SegWalk {
         pos = run_begin(T, runs, c);
         end = run_begin(T, runs, c + 1);
         for (int i0 = 0; i0 < w.N; i0 += 32) {
-            const int lane_len = i0 == 0 ? len0 : i0 + lane < w.N ? lat_len(w, i0 + lane) : 0;
+            const int lane_len = i0 == 0 ? len0 : i0 + lane < w.N ? lat_len<TREE>(w, i0 + lane) : 0;
             const int mine = lat_count(w, lane_len);
             int incl = mine;
 #pragma unroll
@@ -157,7 +163,7 @@ struct SegWalk {
             while (pos >= base + count) {
                 base += count;
                 ++n;
-                len = lat_len(w, n);
+                len = lat_len<TREE>(w, n);
                 count = lat_count(w, len);
             }
             const long long stop = end - base < count ? end - base : count;
@@ -197,24 +203,24 @@ struct LatArgs {
 };
 
 // Row tiles of sequence n that are sequences of their own and not left out (a warp together).
-template <int R>
+template <int R, bool TREE>
 __device__ __forceinline__ int lat_needed(const LatArgs& a, int n, int lane) {
-    return a.w.each <= 1 || a.w.N / a.w.each > a.w.most ? a.w.each
+    return lat_each<TREE>(a.w) <= 1 || a.w.N / a.w.each > a.w.most ? a.w.each
                                                         : lat_need(a.parents + static_cast<long long>(n) * a.K, a.K, a.H, R, lane);
 }
 // Of few sequences: the counted tiles of all, and of those before row tile `tile` of sequence n; its own length and row tiles.
 struct LatCount { long long T, before; int len, need; };
-template <int R>
+template <int R, bool TREE>
 __device__ __forceinline__ LatCount lat_counted(const LatArgs& a, int n, int tile, int lane) {
-    const int seqs = a.w.N / a.w.each;
+    const int each = lat_each<TREE>(a.w), seqs = a.w.N / each;
     LatCount c{0, 0, 0, 0};
     for (int i0 = 0; i0 < seqs; i0 += 32) {
-        const int i = i0 + lane, v = i < seqs ? lat_seq(a.w, i) : 0;
-        int mine = a.w.each;
-        if (a.w.each > 1)
+        const int i = i0 + lane, v = i < seqs ? lat_seq<TREE>(a.w, i) : 0;
+        int mine = each;
+        if (each > 1)
 #pragma unroll 4
             for (int k = i0; k < min(i0 + 32, seqs); ++k) {
-                const int need = lat_needed<R>(a, k, lane);
+                const int need = lat_needed<R, TREE>(a, k, lane);
                 mine = i == k ? need : mine;
             }
         const long long count = lat_count(a.w, v);
@@ -396,8 +402,9 @@ kda_latent_decode_kernel(const __grid_constant__ LatMaps maps, const LatArgs a)
     const int rt = blockIdx.x % a.RT, run = blockIdx.x / a.RT;
     LatWork work = a.w;
     // of a segment: its sequence, its first row there and how many follow
-    auto seq_of = [&](int n) { return TREE && a.w.each > 1 ? n % (a.w.N / a.w.each) : n; };
-    auto row_of = [&](int n) { return TREE && a.w.each > 1 ? n / (a.w.N / a.w.each) * R : rt * R; };
+    const int each = lat_each<TREE>(a.w);
+    auto seq_of = [&](int n) { return each > 1 ? n % (a.w.N / each) : n; };
+    auto row_of = [&](int n) { return each > 1 ? n / (a.w.N / each) * R : rt * R; };
     auto rows_of = [&](int n) { return min(R, a.rows - row_of(n)); };
 
     if (tid == 0) {
@@ -412,7 +419,7 @@ kda_latent_decode_kernel(const __grid_constant__ LatMaps maps, const LatArgs a)
         tc::mbar_fence_init();
     }
     {   // the page table goes to L2 while the lengths that say where to read it are on their way: a line a thread
-        const size_t lines = (static_cast<size_t>(a.w.N / a.w.each) * a.ch.max_pages * 4 + 127) / 128;
+        const size_t lines = (static_cast<size_t>(a.w.N / each) * a.ch.max_pages * 4 + 127) / 128;
         const size_t mine = static_cast<size_t>(blockIdx.x) * Sh::kThreads + tid;
         if (mine < lines) asm volatile("prefetch.global.L2 [%0];" :: "l"(reinterpret_cast<const uint8_t*>(a.ch.table) + mine * 128));
     }
@@ -422,14 +429,14 @@ kda_latent_decode_kernel(const __grid_constant__ LatMaps maps, const LatArgs a)
         else tc::tma_prefetch_map(&maps.q);
     }
     if (tid < R) s_j[tid] = min((rt * R + tid) / a.H, a.K - 1);
-    if (TREE && work.each > 1 && work.N / work.each <= kMaxNeed<E4M3>) {
-        const int seqs = work.N / work.each;
+    if (each > 1 && work.N / each <= kMaxNeed<E4M3>) {
+        const int seqs = work.N / each;
 #pragma unroll 4
         for (int i = warp; i < seqs; i += Sh::kThreads / 32) {
             const int need = lat_need(a.parents + static_cast<long long>(i) * a.K, a.K, a.H, R, lane);
             if (lane == 0) s_need[i] = static_cast<uint8_t>(need);
         }
-        for (int i = tid; i < seqs; i += Sh::kThreads) s_lens[i] = lat_seq(a.w, i);
+        for (int i = tid; i < seqs; i += Sh::kThreads) s_lens[i] = lat_seq<TREE>(a.w, i);
         work.need = s_need;
         work.lens = s_lens;
     }
@@ -439,14 +446,14 @@ kda_latent_decode_kernel(const __grid_constant__ LatMaps maps, const LatArgs a)
     tc::fence_after_sync();
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");   // the combine kernel waits for this grid's end
     const uint32_t tm = *s_tmem, tmO = tm, tmS = tm + 4 * Sh::kO;
-    SegWalk sw;
+    SegWalk<TREE> sw;
     sw.init(work, run);
     bool ok = true;
 
     if (warp < Sh::kMmaWarp) {
         // ---- softmax: rows row_g .. + RW, a thread's tokens and rows of them as tmem_ld_s gives them ----
         constexpr int RW = Sh::RW;
-        const int wq = warp & 3, row_g = (warp >> 2) * RW;
+        const int wq = Sh::kGroups > 1 ? warp & 3 : warp, row_g = Sh::kGroups > 1 ? (warp >> 2) * RW : 0;
         const int tq = lane >> 2, rq = row_g + 2 * (lane & 3);
         const uint32_t lane_tm = static_cast<uint32_t>(wq * 32) << 16;
         float m[RW / 4], l[RW / 4];
@@ -766,12 +773,12 @@ kda_latent_decode_kernel(const __grid_constant__ LatMaps maps, const LatArgs a)
         // sequences that hold nothing, where the kernel that joins sees those alone that are cut
         if (a.cuts && ok)
             for (int n = run; n < a.w.N; n += a.w.G) {
-                if (lat_len(work, n) != 0) continue;
+                if (lat_len<TREE>(work, n) != 0) continue;
                 const int seq = seq_of(n), row0 = row_of(n), nrows = rows_of(n);
                 const long long at = static_cast<long long>(seq) * a.rows + row0;
                 for (int i = tid; i < nrows * (kLatDim / 8); i += Sh::kSoft) reinterpret_cast<uint4*>(a.out + at * kLatDim)[i] = make_uint4(0, 0, 0, 0);
                 if (a.lse && tid < nrows) a.lse[at + tid] = -INFINITY;
-                if (tid == 0 && row0 == 0 && lat_seq(a.w, seq) != a.w.seq_lens[seq]) set_status(a.status, kStatusIndex);
+                if (tid == 0 && row0 == 0 && lat_seq<TREE>(a.w, seq) != a.w.seq_lens[seq]) set_status(a.status, kStatusIndex);
             }
     } else if (warp == Sh::kMmaWarp) {
         // ---- both products; whichever has its inputs goes first ----
@@ -788,7 +795,7 @@ kda_latent_decode_kernel(const __grid_constant__ LatMaps maps, const LatArgs a)
         const uint32_t hi_c = static_cast<uint32_t>(dC >> 32);
         const uint32_t c_lo = static_cast<uint32_t>(dC) | (tc::smem_u32(sC) >> 4);
         const uint32_t p_lo = static_cast<uint32_t>(d0) | (tc::smem_u32(sP) >> 4);
-        SegWalk sv = sw;                                        // the O product's walk follows the S product's
+        SegWalk<TREE> sv = sw;                                  // the O product's walk follows the S product's
         bool more_s = sw.next(work), more_o = sv.next(work);
         int gs = 0, go = 0, qs = 0;                             // S and O tiles issued, segments whose Q is in
         int ts = sw.t0, to = sv.t0;
@@ -918,7 +925,7 @@ kda_latent_decode_kernel(const __grid_constant__ LatMaps maps, const LatArgs a)
                     // sequences x 64 heads 209 -> 194 us, 16 x K = 4 x 32 heads 105 -> 97, one of 145408 x 64
                     // heads 55.6 -> 53.3.  (With 32 rows HBM is the bound: 189 -> 205.  Three stages of an e4m3
                     // cache cover it: no change.  Two tiles ahead: 196, 99, 53.7.)
-                    if ((TREE && a.w.each > 1 || rt == 0) && next >= 0) tc::tma_prefetch_4d(&maps.c, 0, 0, 0, next >> 3);
+                    if ((each > 1 || rt == 0) && next >= 0) tc::tma_prefetch_4d(&maps.c, 0, 0, 0, next >> 3);
                 }
                 at = next;
             }
@@ -945,7 +952,7 @@ kda_latent_decode_kernel(const __grid_constant__ LatMaps maps, const LatArgs a)
 // loads in flight; then the groups are joined.
 constexpr int kMaxRuns = 1024;                  // partials of a row (at most one a run)
 
-template <int R>
+template <int R, bool TREE>
 __global__ void __launch_bounds__(512)
 kda_latent_combine_kernel(const LatArgs a, int Q, int NG)
 {
@@ -954,8 +961,8 @@ kda_latent_combine_kernel(const LatArgs a, int Q, int NG)
     const int lanes = 128 / Q;
     const int unit = blockIdx.x / Q, n = unit / a.rows, row = unit % a.rows;
     const int tid = threadIdx.x, grp = tid / lanes, ch = (blockIdx.x % Q * lanes + tid % lanes) * 4;
-    const int tile = a.w.each > 1 ? row / R : 0;                 // (of those that are sequences of their own)
-    const LatCount c = lat_counted<R>(a, n, tile, tid & 31);
+    const int each = lat_each<TREE>(a.w), tile = each > 1 ? row / R : 0;     // (of those that are sequences of their own)
+    const LatCount c = lat_counted<R, TREE>(a, n, tile, tid & 31);
     if (tid == 0 && row == 0 && a.w.seq_lens[n] != c.len) set_status(a.status, kStatusIndex);    // out of range: counted as 0
     const long long T = c.T, before = c.before;
     const int tiles = tile < c.need ? lat_tiles(c.len) : 0;
@@ -978,7 +985,7 @@ kda_latent_combine_kernel(const LatArgs a, int Q, int NG)
     if (parts == 1) return;                                      // its CTA finished it
     const int r = row % R;
     const size_t stride = static_cast<size_t>(a.RT) * 2 * R;     // rows of partials between runs
-    const size_t base = (static_cast<size_t>(c0) * a.RT + (a.w.each > 1 ? 0 : row / R)) * 2 * R + r;
+    const size_t base = (static_cast<size_t>(c0) * a.RT + (each > 1 ? 0 : row / R)) * 2 * R + r;
     auto slot = [&](int i) { return base + i * stride + (i == 0 && late ? R : 0); };
     float M = -INFINITY, L = 0.f;
     float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
@@ -1032,30 +1039,30 @@ kda_latent_combine_kernel(const LatArgs a, int Q, int NG)
 // The same for many rows of few partials: a warp a row, 16 channels a lane, no block-wide step.
 // (Four blocks an SM are enough: for more, the compiler spills into 48 registers.)
 // MANY: of the runs' cut sequences alone.
-template <int R, bool MANY>
+template <int R, bool MANY, bool TREE>
 __global__ void __launch_bounds__(128, 4)
 kda_latent_combine_rows_kernel(const LatArgs a)
 {
     const int lane = threadIdx.x & 31;
     const long long unit = static_cast<long long>(blockIdx.x) * 4 + (threadIdx.x >> 5);
-    const int seqs = a.w.N / a.w.each;
+    const int each = lat_each<TREE>(a.w), seqs = a.w.N / each;
     int n, row, tiles;
     long long T, before;
     if constexpr (MANY) {                                        // unit: row of a run's cut sequence
-        const int per = a.w.each > 1 ? R : a.rows, run = static_cast<int>(unit / per);
+        const int per = each > 1 ? R : a.rows, run = static_cast<int>(unit / per);
         asm volatile("griddepcontrol.wait;" ::: "memory");
         const LatCut cut = run < a.w.G ? a.cuts[run] : LatCut{0, 0, -1};
         if (cut.n < 0) return;
-        n = a.w.each > 1 ? cut.n % seqs : cut.n;
-        row = static_cast<int>(unit - static_cast<long long>(run) * per) + (a.w.each > 1 ? cut.n / seqs * R : 0);
-        tiles = lat_tiles(lat_seq(a.w, n));
+        n = each > 1 ? cut.n % seqs : cut.n;
+        row = static_cast<int>(unit - static_cast<long long>(run) * per) + (each > 1 ? cut.n / seqs * R : 0);
+        tiles = lat_tiles(lat_seq<TREE>(a.w, n));
         T = cut.T;
         before = cut.before;
     } else {                                                     // unit: n * rows + row
         n = static_cast<int>(min(unit, static_cast<long long>(seqs) * a.rows - 1) / a.rows);
         row = static_cast<int>(unit - static_cast<long long>(n) * a.rows);
-        const int tile = a.w.each > 1 ? min(row, a.rows - 1) / R : 0;        // (of those that are sequences of their own)
-        const LatCount c = lat_counted<R>(a, n, tile, lane);
+        const int tile = each > 1 ? min(row, a.rows - 1) / R : 0;        // (of those that are sequences of their own)
+        const LatCount c = lat_counted<R, TREE>(a, n, tile, lane);
         if (lane == 0 && row == 0 && a.w.seq_lens[n] != c.len) set_status(a.status, kStatusIndex);   // out of range: counted as 0
         tiles = tile < c.need ? lat_tiles(c.len) : 0;
         T = c.T;
@@ -1080,7 +1087,7 @@ kda_latent_combine_rows_kernel(const LatArgs a)
     }
     if (parts == 1) return;                                      // its CTA finished it
     const size_t stride = static_cast<size_t>(a.RT) * 2 * R;
-    const size_t base = (static_cast<size_t>(c0) * a.RT + (a.w.each > 1 ? 0 : row / R)) * 2 * R + row % R;
+    const size_t base = (static_cast<size_t>(c0) * a.RT + (each > 1 ? 0 : row / R)) * 2 * R + row % R;
     float M = -INFINITY, L = 0.f;
     float4 acc[4];
 #pragma unroll
@@ -1202,9 +1209,9 @@ int launch_decode_shape(const LatMaps& maps, const LatArgs& a, cudaStream_t stre
     at[0].val.programmaticStreamSerializationAllowed = 1;
     cfg.attrs = at;
     cfg.numAttrs = 1;
-    if (a.cuts) return cudaLaunchKernelEx(&cfg, kda_latent_combine_rows_kernel<R, true>, a) == cudaSuccess ? 0 : -3;
-    if (by_warp) return cudaLaunchKernelEx(&cfg, kda_latent_combine_rows_kernel<R, false>, a) == cudaSuccess ? 0 : -3;
-    return cudaLaunchKernelEx(&cfg, kda_latent_combine_kernel<R>, a, Q, NG) == cudaSuccess ? 0 : -3;
+    if (a.cuts) return cudaLaunchKernelEx(&cfg, kda_latent_combine_rows_kernel<R, true, TREE>, a) == cudaSuccess ? 0 : -3;
+    if (by_warp) return cudaLaunchKernelEx(&cfg, kda_latent_combine_rows_kernel<R, false, TREE>, a) == cudaSuccess ? 0 : -3;
+    return cudaLaunchKernelEx(&cfg, kda_latent_combine_kernel<R, TREE>, a, Q, NG) == cudaSuccess ? 0 : -3;
 }
 
 template <bool TREE>
