@@ -9,14 +9,17 @@ namespace kda {
 
 constexpr int kCacheThreads = 256;
 
-// A token's latents at src (32 lanes x 32 bytes) into its cache row, with the scale of an e4m3 row.  Lane: 16 latents.
+// A token's latents at src (32 lanes x 32 bytes) into its cache row.  Lane: 16 latents.  Returns the exponent of an e4m3 row's
+// scale, which put_scale writes after the position part, so that a row is written from its first byte to its last (the scale
+// before the position part: 145408 tokens with their read-back 85.8 us for 84.3).
 template <bool E4M3>
-__device__ __forceinline__ void put_latents(uint8_t* row, const uint4* src, int lane) {
+__device__ __forceinline__ int put_latents(uint8_t* row, const uint4* src, int lane) {
     if constexpr (!E4M3) {
         uint4* dst = reinterpret_cast<uint4*>(row);
         const uint4 a = src[lane], b = src[lane + 32];
         dst[lane] = a;
         dst[lane + 32] = b;
+        return 0;
     } else {
         // 16 latents of this lane: one 16-byte store of codes
         const uint4 a = src[2 * lane], b = src[2 * lane + 1];
@@ -44,10 +47,13 @@ __device__ __forceinline__ void put_latents(uint8_t* row, const uint4* src, int 
             o[i] = f32x2_to_e4m3x2(x[4 * i] * inv, x[4 * i + 1] * inv) |
                    (f32x2_to_e4m3x2(x[4 * i + 2] * inv, x[4 * i + 3] * inv) << 16);
         reinterpret_cast<uint4*>(row)[lane] = make_uint4(o[0], o[1], o[2], o[3]);
-        if (lane < 4)
-            reinterpret_cast<uint32_t*>(row + kLatScaleAt)[lane] =
-                lane == 0 ? static_cast<uint32_t>(127 + e) << 23 : 0u;
+        return e;
     }
+}
+template <bool E4M3>
+__device__ __forceinline__ void put_scale(uint8_t* row, int e, int lane) {
+    if (E4M3 && lane < 4)
+        reinterpret_cast<uint32_t*>(row + kLatScaleAt)[lane] = lane == 0 ? static_cast<uint32_t>(127 + e) << 23 : 0u;
 }
 
 // 16 consecutive latents per lane (32 bytes), 2 position values per lane.
@@ -69,8 +75,9 @@ kda_latent_append_kernel(const uint16_t* __restrict__ c, long long ldc, const ui
         return;
     }
     uint8_t* row = cache + static_cast<size_t>(slot) * lat_row_bytes(E4M3);
-    put_latents<E4M3>(row, src, lane);
+    const int e = put_latents<E4M3>(row, src, lane);
     reinterpret_cast<uint32_t*>(row + (E4M3 ? kLatDim : 2 * kLatDim))[lane] = rope;
+    put_scale<E4M3>(row, e, lane);
 }
 
 // The same with the position parts rotated on the way: pair i of a key or query turns by pos * f_i,
@@ -185,11 +192,12 @@ kda_latent_append_rope_kernel(const RopeArgs a)
         sn[i] = __shfl_sync(0xffffffffu, s, 4 * g + i);
     }
     uint8_t* row = a.cache + static_cast<size_t>(slot) * lat_row_bytes(E4M3);
-    put_latents<E4M3>(row, reinterpret_cast<const uint4*>(a.c + t * a.ldc), lane);
+    const int e = put_latents<E4M3>(row, reinterpret_cast<const uint4*>(a.c + t * a.ldc), lane);
     if (sub == 0) {
         key.turn(cs, sn);
         key.store(reinterpret_cast<uint16_t*>(row + (E4M3 ? kLatDim : 2 * kLatDim)), g);
     }
+    put_scale<E4M3>(row, e, lane);
     uint16_t* out = a.q_out + t * a.ldo;
     for (int h0 = sub; h0 < a.H;) {
 #pragma unroll
