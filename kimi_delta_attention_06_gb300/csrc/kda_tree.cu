@@ -87,13 +87,13 @@ struct TreeShape {
     static constexpr uint32_t kBit = KP > 32 ? 8u : 4u;                 // bytes of a set
     static constexpr uint32_t oNone = oRows;                            // of 256 threads: places that are no number
     static constexpr int kRounds = KP == 8 ? 3 : KP == 16 ? 4 : KP == 32 ? 5 : 6;      // of the decays' products, doubling their reach
-    static constexpr uint32_t oSet = oV + kNodes * D * 2u, oBeta = oSet + 2 * kNodes * kBit, oUp = oBeta + 2 * kNodes * 2u;
-    static constexpr uint32_t oFar = oUp + 2 * kNodes, oDesc = oFar + 2 * kRounds * kNodes, oBar = oDesc + 2 * kNodes * kBit;
+    static constexpr uint32_t oSet = oV + kNodes * D * 2u, oBeta = oSet + 2 * kNodes * kBit;
+    static constexpr uint32_t oFar = oBeta + 2 * kNodes * 2u, oDesc = oFar + 2 * kRounds * kNodes, oBar = oDesc + 2 * kNodes * kBit;
     static constexpr uint32_t kBytes = oBar + 288u;
     // W by whole rows of L (else along the paths), where a row has so many lanes, and a lane so many quads of places
     static constexpr bool kDense = KP > 16;
     static constexpr int kWLanes = KP / 4 < 256 / kNodes ? KP / 4 : 256 / kNodes, kQuads = KP / 4 / kWLanes;
-    static_assert(kBytes <= (kCtas == 1 ? 232448u : kCtas == 2 ? 115712u : 76800u), "shared memory");
+    static_assert(kBytes <= (kCtas == 1 ? 232448u : 115712u), "shared memory");
     static_assert(oState >= oSide + kSides + 8192u, "the side's last products stay within");
     static_assert(256u * kBit <= kTiles && D % CH == 0, "none; channels");
 };
@@ -127,9 +127,6 @@ __device__ __forceinline__ void tree_mma_ss(uint32_t d, uint32_t a, uint32_t b, 
 }
 __device__ __forceinline__ void tree_copy16(uint32_t dst, const void* src) {
     asm volatile("cp.async.ca.shared.global [%0], [%1], 16;" :: "r"(dst), "l"(src) : "memory");
-}
-__device__ __forceinline__ void tree_copy4(uint32_t dst, const void* src) {
-    asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" :: "r"(dst), "l"(src) : "memory");
 }
 __device__ __forceinline__ void tree_copies_done() { asm volatile("cp.async.wait_all;" ::: "memory"); }
 // x rounded to its leading 11 bits (to the nearest: what is left is then as often negative, and so are the products that are
@@ -168,7 +165,6 @@ kda_tree_kernel(const TreeArgs a)
     float* s_n = reinterpret_cast<float*>(sm + Sh::oN);
     Set* s_sets = reinterpret_cast<Set*>(sm + Sh::oSet);                // [2][place]: of this turn and the next
     uint16_t* s_betas = reinterpret_cast<uint16_t*>(sm + Sh::oBeta);    // [2][place]
-    int8_t* s_ups = reinterpret_cast<int8_t*>(sm + Sh::oUp);            // [2][place]: of the parent, -1 without one, -2 without a node
     int8_t* s_fars = reinterpret_cast<int8_t*>(sm + Sh::oFar);          // [2][round][place]: the ancestor 2^round up, -1 without one
     Set* s_descs = reinterpret_cast<Set*>(sm + Sh::oDesc);              // [2][place]: the places whose paths it is on
     uint64_t* bars = reinterpret_cast<uint64_t*>(sm + Sh::oBar);
@@ -292,18 +288,16 @@ kda_tree_kernel(const TreeArgs a)
                     desc[0] |= (path >> lane & 1) << c;
                     if constexpr (KP > 32) desc[1] |= (path >> (lane + 32) & 1) << c;
                 }
-                int up[2];
+                int far[2];                                             // the parent at first
 #pragma unroll
                 for (int z = 0; z < 2; ++z) {
                     const int j = lane + 32 * z;
                     const uint64_t above = set[z] & ~(1ull << j);
-                    up[z] = above ? tree_top(above) : set[z] ? -1 : -2;
+                    far[z] = above ? tree_top(above) : -1;
                     if (j >= KP) continue;
                     s_sets[(odd * kItems + it) * KP + j] = static_cast<Set>(set[z]);
-                    s_ups[(odd * kItems + it) * KP + j] = static_cast<int8_t>(up[z]);
                     if (Sh::kDense) s_descs[(odd * kItems + it) * KP + j] = desc[z];
                 }
-                int far[2] = {max(up[0], -1), max(up[1], -1)};
 #pragma unroll 1
                 for (int r = 0; r < Sh::kRounds; ++r) {
                     int8_t* to = s_fars + ((odd * Sh::kRounds + r) * kItems + it) * KP;
