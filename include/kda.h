@@ -485,8 +485,10 @@ int kda_latent_append(const uint16_t* c, int64_t ldc, const uint16_t* k_rope, in
  *               node of a tree of drafts sits at its depth, not at its place in the cache)
  *   inv_freq    (device) fp32 [KDA_LATENT_ROPE / 2]: pair i turns by positions[t] * inv_freq[i], in
  *                   (x, y) -> (x cos - y sin, x sin + y cos);
- *               magnitudes below 2^32 (anything else gives NaN in its pair).  The angle is formed
- *               exactly to within positions[t] * 2^-64 turns, the rotation in fp32, rounded once.
+ *               magnitudes below 2^32 (anything else gives NaN in its pair).  The product modulo a turn
+ *               is exact to within positions[t] * 2^-63 turns; its leading 32 bits, rounded to fp32, are the
+ *               angle (to within 2^-26 + 2^-32 of a turn).  Sine, cosine and the rotation are fp32, the result
+ *               is rounded once.
  *   interleaved 1: pair i is values (2 i, 2 i + 1); 0: values (i, i + KDA_LATENT_ROPE / 2)
  *   q           (device) bf16 or NULL: the position parts of H heads' queries, KDA_LATENT_ROPE values each,
  *               token / head strides ldq, hdq in elements (multiples of 8, hdq at least

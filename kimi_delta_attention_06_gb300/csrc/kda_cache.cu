@@ -85,7 +85,7 @@ kda_latent_append_kernel(const uint16_t* __restrict__ c, long long ldc, const ui
 // with pairs of neighbours (2 i, 2 i + 1) or of the two halves (i, i + 32).  The angle matters modulo a turn, and
 // pos * f rounded to 32 bits is off by 0.03 rad at pos = 10^6, so it is taken in fixed point: f / 2 pi as a 64-bit
 // fraction of a turn (its whole turns vanish at whole positions), times pos modulo 2^64, is exact but for the
-// fraction's own rounding, pos * 2^-64.
+// fraction's own rounding, at most pos * 2^-63.
 //
 // A warp takes a token: lane i the angle of pair i, once; then 8 lanes a head, 4 pairs a lane, 16 heads in flight, the first
 // of them on their way before the slot is known.  Bound by HBM: 32768 tokens of 32 heads, bf16, 55 us (6.2 TB/s); 768 of
