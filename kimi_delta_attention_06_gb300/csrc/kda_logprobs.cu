@@ -562,7 +562,10 @@ kda_logprobs_kernel(const LogArgs a)
             }
         }
         __syncthreads();
-        if (!s_ok) return;
+        if (!s_ok) {                             // (the others may still write here: not before they have left)
+            tc::cluster_sync();
+            return;
+        }
         if (top > 0) {
             const LogKey bound = s_least;
             for (int i = tid; i < C * kLogMaxTop; i += kLogThreads) {

@@ -236,6 +236,7 @@ kda_verify_kernel(const float* __restrict__ tp, long long ldp, const float* __re
     }
     if (s_owner < 0) {
         if (s_owner == -1 && rank == 0 && tid == 0) out[n * (K + 1) + a] = -1;
+        if (s_owner == -2) tc::cluster_sync();              // (the others may still write here: not before they have left)
         return;
     }
     if (rank != s_owner) return;
