@@ -593,8 +593,9 @@ kda_logprobs_kernel(const LogArgs a)
     const float nan = __int_as_float(0x7fffffff), ln2 = 0.69314718055994531f;
     const bool far = log_wide(all.m, c);
     const float l2 = log2f(all.s), ref = far || !(fabsf(all.m) < INFINITY) ? 0.f : __fmul_rn(all.m, c);
-    auto log_prob = [&](float x) {               // (a row of -inf alone: no token has a probability)
-        return x == -INFINITY ? -INFINITY : far || log_wide(x, c) ? fmaf(a.scale, x - all.m, -l2 * ln2) : (fmaf(x, c, -ref) - l2) * ln2;
+    auto log_prob = [&](float x) {               // (a row of -inf alone: no token has a probability; a difference may pass 2^128)
+        return x == -INFINITY ? -INFINITY : far || log_wide(x, c) ? fmaf(2.f * a.scale, 0.5f * x - 0.5f * all.m, -l2 * ln2)
+                                          : (fmaf(x, c, -ref) - l2) * ln2;
     };
     if (tid == 0) {
         if (a.tok) {
