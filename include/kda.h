@@ -379,8 +379,9 @@ int kda_decode_multi(const uint16_t* q, const uint16_t* k, const uint16_t* v,
  *   out         (device) [N, K, H, Dv], bf16 or fp32 per out_dtype; zeros for a place without a node
  * State slots need not be distinct.  An out-of-range slot skips its sequence (out is left as it
  * was) and is reported.  Dk == Dv in {64, 128}.  Deterministic.  Products keep 22 bits of each
- * factor and sums are fp32, in another order than kda_decode_multi's on the same path (a few 1e-7 of
- * the outputs' magnitudes off).  A state that holds NaN or infinities, or a magnitude above 3.4e38 / 2,
+ * factor (of one below 2^-104 those above 2^-126) and sums are fp32, in another order than
+ * kda_decode_multi's on the same path (a few 1e-7 of the outputs' magnitudes off).
+ * A state that holds NaN or infinities, or a magnitude above 3.4e38 / 2,
  * may make its outputs NaN; one that only a node's inputs bring reaches its descendants alone.
  * Keys are taken over the product of the decays on their node's path where that is at least 2^-100
  * in every channel: one above 2^27 there may make its descendants' outputs NaN.
@@ -565,7 +566,10 @@ int kda_latent_decode(const uint16_t* q, const void* cache, int cache_dtype, int
  *   parents     (device) int32 [N, K] as for kda_decode_tree
  * Node j sees the seq_lens[n] - K tokens before the tree, its ancestors and itself; a place without a
  * node gives zeros and lse = -inf.  seq_lens[n] is 0 (a sequence that is not there: zeros and -inf) or
- * at least K, else it counts as 0 and is reported.  Everything else as in kda_latent_decode.
+ * at least K, else it counts as 0 and is reported.  The block table covers all K places, those without
+ * a node too.  Everything else as in kda_latent_decode.
+ * Where K * H is above 64 (KDA_CACHE_BF16: 128), blocks of 64 of those rows behind a tree's last node are
+ * left out, for N up to 512 (KDA_CACHE_BF16: 128); of more sequences all rows take their time.
  */
 int kda_latent_decode_tree(const uint16_t* q, const void* cache, int cache_dtype, int num_pages, int page_size,
                            const int32_t* block_table, int max_pages, const int32_t* seq_lens, const int32_t* parents,

@@ -88,8 +88,8 @@ kda_latent_append_kernel(const uint16_t* __restrict__ c, long long ldc, const ui
 // fraction's own rounding, at most pos * 2^-63.
 //
 // A warp takes a token: lane i the angle of pair i, once; then 8 lanes a head, 4 pairs a lane, 16 heads in flight, the first
-// of them on their way before the slot is known.  Bound by HBM: 32768 tokens of 32 heads, bf16, 55 us (6.2 TB/s); 768 of
-// them, e4m3, 3.4 us, most of it the launch and two loads one after the other.  (Heads of a token over 2 warps: 56 and
+// of them on their way before the slot is known.  Bound by HBM: 32768 tokens of 32 heads, bf16, 55 us (6.2 TB/s; in another
+// session 52, over e4m3 50); 768 of them, e4m3, 3.4 us, most of it the launch and two loads one after the other.  (Heads of a token over 2 warps: 56 and
 // 3.2 us, over 4: 74 and 3.3.  The loads after the angle: 59 and 4.1.)
 constexpr int kRopeThreads = 128;
 

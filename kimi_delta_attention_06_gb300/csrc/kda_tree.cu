@@ -21,9 +21,9 @@
 // V - P in TMEM in S_0^T's place (a NaN or an infinity in it enters as 0, and is put back for the nodes whose paths hold it:
 // 0 * NaN is none).
 //
-// Measured in a graph: 256 sequences x 32 heads of 128 x 128, trees of 16 nodes: 186 us for 0.70 GB that cannot be done without
-// (103 us of HBM); 64 x 8 of 64 x 64, 48 nodes: 46 us; one sequence, 32 heads, 8 nodes: 6.5 us.  Bound by a turn's chain (decays,
-// rows, product, V - P, product, outputs; 11 to 12 thousand clocks at 16 nodes) with two CTAs an SM to fill it, one from 17
+// Measured in a graph: 256 sequences x 32 heads of 128 x 128, trees of 16 nodes: 185 us for 0.70 GB that cannot be done without
+// (103 us of HBM); 64 x 8 of 64 x 64, 48 nodes: 46 us; one sequence, 32 heads, 8 nodes: 6.4 us.  Bound by a turn's chain (decays,
+// rows, product, V - P, product, outputs; 13 thousand clocks at 16 nodes) with two CTAs an SM to fill it, one from 17
 // nodes on, where TMEM and shared memory hold no more.  Decays outside the range from
 // the fourth node on, or everywhere: 262 and 292 us at 16 nodes, 125 and 116 at 48.
 #include "common.cuh"
