@@ -870,6 +870,8 @@ def latent_decode_tree(q, cache, cache_dtype: int, block_table, seq_lens, parent
     """Absorbed latent attention of the nodes q [N, K, H, 576] of a tree a sequence, parents [N, K], whose rows are the last K
     of the cache; returns (out [N, K, H, 512] bf16, lse [N, K, H] fp32 or None)."""
     N, K, H, _ = q.shape
+    if parents.size(-1) != K:
+        _short("parents", parents, f"[{N}, {K}]")
     return _latent_decode(q, cache, cache_dtype, block_table, seq_lens, N, K, H, sm_scale, None, None, stream, True, want_lse,
                           parents, True)
 
@@ -879,6 +881,10 @@ def decode_tree(q, k, v, log_alpha, beta, state_pool, parents, state_slots=None,
     """KDA outputs [N, K, H, D] of the nodes of a tree a sequence, parents [N, K], from the states state_pool
     [slots, H, D, D], which stay as they are."""
     N, K, H, Dk = q.shape
+    if parents.size(-1) != K:
+        _short("parents", parents, f"[{N}, {K}]")
+    if state_pool.shape[1:] != (H, Dk, v.shape[3]):
+        _short("state_pool", state_pool, f"[slots, {H}, {Dk}, {v.shape[3]}]")
     return _decode_tree(q, k, v, log_alpha, beta, state_pool, state_pool.shape[0], state_slots, parents, None,
                         KDA_OUT_F32 if out_dtype == torch.float32 else KDA_OUT_BF16, N, K, H, Dk, v.shape[3], decay, stream,
                         make=True)
