@@ -885,6 +885,8 @@ def decode_tree(q, k, v, log_alpha, beta, state_pool, parents, state_slots=None,
         _short("parents", parents, f"[{N}, {K}]")
     if state_pool.shape[1:] != (H, Dk, v.shape[3]):
         _short("state_pool", state_pool, f"[slots, {H}, {Dk}, {v.shape[3]}]")
+    if out_dtype is not torch.bfloat16 and out_dtype is not torch.float32:
+        raise TypeError(f"out_dtype: torch.bfloat16 or torch.float32, got {out_dtype}")
     return _decode_tree(q, k, v, log_alpha, beta, state_pool, state_pool.shape[0], state_slots, parents, None,
                         KDA_OUT_F32 if out_dtype == torch.float32 else KDA_OUT_BF16, N, K, H, Dk, v.shape[3], decay, stream,
                         make=True)

@@ -48,3 +48,11 @@ def test_pools_of_other_heads():
             kda.decode_tree(**_state(state_pool=pool))
     with pytest.raises(ValueError, match="on the GPU"):
         kda.decode_tree(**_state(state_pool=torch.zeros(7, 4, 64, 64)))
+
+def test_outputs_of_other_types():
+    for t in (torch.float16, torch.float64, torch.int32):
+        with pytest.raises(TypeError, match="out_dtype"):
+            kda.decode_tree(**_state(out_dtype=t))
+    for t in (torch.bfloat16, torch.float32):
+        with pytest.raises(ValueError, match="on the GPU"):
+            kda.decode_tree(**_state(out_dtype=t))
