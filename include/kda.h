@@ -648,9 +648,10 @@ int kda_verify_draft(const float* target_probs, int64_t ldp, const float* draft_
  * token is V or more, which is reported.  Logits of -inf have probability 0 (log probability -inf; a row
  * of nothing else: all of them, and entropy 0); a row that holds a NaN or +inf gives NaN, rank 0 and
  * tokens of -1.  Sums are fp32, one partial sum a thread.  Deterministic.
- * top <= KDA_LOGPROBS_MAX_TOP, V <= 2^30, else KDA_ERR_UNSUPPORTED.
+ * top <= KDA_LOGPROBS_MAX_TOP, V <= KDA_LOGPROBS_MAX_VOCAB, else KDA_ERR_UNSUPPORTED.
  */
 #define KDA_LOGPROBS_MAX_TOP 32
+#define KDA_LOGPROBS_MAX_VOCAB 16777216
 int kda_token_logprobs(const void* logits, int logits_dtype, int64_t ld, const int32_t* tokens, int R, int V, int top,
                        float scale, float* logprob, int32_t* rank, float* entropy, float* top_logprob, int32_t* top_token,
                        void* stream);

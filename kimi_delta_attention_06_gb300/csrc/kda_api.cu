@@ -1018,7 +1018,9 @@ int kda_token_logprobs(const void* logits, int logits_dtype, int64_t ld, const i
                        void* stream) {
     if (R < 0 || V <= 0 || top < 0 || !(scale >= 1e-6f && scale <= 1e6f)) return KDA_ERR_INVALID_ARG;
     if (logits_dtype != KDA_OUT_BF16 && logits_dtype != KDA_OUT_F32) return KDA_ERR_INVALID_ARG;
-    if (top > KDA_LOGPROBS_MAX_TOP || V > (1 << 30)) return KDA_ERR_UNSUPPORTED;
+    // (longer rows would outgrow a thread's fp32 sums, at 2^30 by 3e-3 of the log probabilities, and the time that a CTA waits for
+    // the others of its row: 32 alternatives among many equal columns of one slice are looked for one after another, 10 s there)
+    if (top > KDA_LOGPROBS_MAX_TOP || V > KDA_LOGPROBS_MAX_VOCAB) return KDA_ERR_UNSUPPORTED;
     if (R == 0) return KDA_OK;
     if (ld < V || ld >= (int64_t(1) << 40) || !logits) return KDA_ERR_INVALID_ARG;
     if (static_cast<int64_t>(R) * 16 >= (int64_t(1) << 31)) return KDA_ERR_INVALID_ARG;

@@ -52,6 +52,7 @@ KDA_LATENT_MAX_TOKENS = 2**31 - 4096
 KDA_VERIFY_MAX_DRAFT = 64
 KDA_TREE_MAX_NODES = 64
 KDA_LOGPROBS_MAX_TOP = 32
+KDA_LOGPROBS_MAX_VOCAB = 2**24
 
 _vp = ctypes.c_void_p
 _i = ctypes.c_int
